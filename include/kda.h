@@ -54,7 +54,9 @@ typedef enum {
     KDA_ERR_TIMEOUT = 5,       /* device: a bounded wait gave up (status word)     */
     KDA_ERR_DEVICE_ARG = 6,    /* device: offsets outside [0, T] (status word)     */
     KDA_ERR_TOO_LARGE = 7,     /* kda_chunk_fwd_static: over its static scratch    */
-    KDA_ERR_RANGE = 8          /* device: a non-finite output value (status word)  */
+    KDA_ERR_RANGE = 8,         /* device: a non-finite output value (status word)  */
+    KDA_ERR_NO_PAGES = 9       /* device: kda_page_plan: a request's table row or
+                                  the free list has too few pages (status word)    */
 } kda_status;
 
 typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
@@ -408,6 +410,197 @@ kda_status kda_chunk_bwd(const void* q, const void* k, const void* v, int32_t qk
                          float* dinitial_state, void* workspace, int64_t workspace_bytes,
                          int32_t* status_dev, kda_stream_t stream);
 
+/* ==================================================================== paged attention
+ *
+ * Full attention beside the KDA layers of a hybrid stack, for serving: keys
+ * and values live in pages of a fixed number of tokens, and a request's pages
+ * are listed in its row of a block table.
+ *
+ *   k_cache, v_cache [num_pages, Hk, page_size, D]   F32 or BF16
+ *   block_table      [N, max_pages] int32            entry j of row n: the page
+ *                      holding tokens j * page_size .. of request n
+ *   slot of a token  = page * page_size + (position % page_size)
+ *
+ * One page's tokens of one head are contiguous, so that a tile of keys is a
+ * single two-dimensional copy.  The KDA layers of the same stack need no pages:
+ * their state has a fixed size (kda_recurrent_step).
+ */
+
+/*
+ * kda_page_plan -- block tables and slot maps from request lengths, on the
+ * device (no host copy of any length is needed, so a step that uses it can be
+ * captured in a CUDA graph).
+ *
+ * Request n has cached_lens[n] = c tokens in its pages and gets the new tokens
+ * cu_seqlens[n] .. cu_seqlens[n+1]-1 of the packed batch, m of them.  With
+ * P = page_size, have = ceil(c / P), want = ceil((c + m) / P) and base = the
+ * pages wanted by the requests before n,
+ *   block_table[n, have + j] = free_pages[start + base + j],  0 <= j < want - have
+ *   positions[t] = c + t - cu_seqlens[n]
+ *   slots[t]     = block_table[n, positions[t] / P] * P + positions[t] % P
+ *   seq_lens[n]  = c + m
+ *   free_end     = start + all pages taken
+ * A request whose row is too short (want > max_pages) takes no pages; one that
+ * the free list cannot serve whole takes none, nor does any later one that
+ * wants some.  Such a request keeps seq_lens[n] = c and gets slots -1, and
+ * *status_dev is set to KDA_ERR_NO_PAGES.  Offsets that are decreasing or
+ * outside [0, T], negative lengths and lengths of 2^31 or more in all set
+ * KDA_ERR_DEVICE_ARG: then no page is taken by any request, every slot is -1,
+ * every position 0 and seq_lens = cached_lens.  A page id below zero on the way to a slot gives -1 and
+ * KDA_ERR_DEVICE_ARG.
+ *
+ *   cached_lens [N] int32, cu_seqlens [N+1] int32
+ *   block_table [N, max_pages] int32  in/out: only the new entries are written
+ *   free_pages  [num_free] int32; free_start: device int32, the first index not
+ *               yet taken, or NULL for 0
+ *   seq_lens [N] int32, positions [T] int32, slots [T] int64, free_end [1] int32
+ *               (written); seq_lens must not be cached_lens, nor free_end
+ *               free_start (the kernel's CTAs read those while others write)
+ * N >= 0, 0 <= T < 2^31, page_size >= 1, max_pages >= 1, num_free >= 0.
+ */
+kda_status kda_page_plan(const int32_t* cached_lens, const int32_t* cu_seqlens, int32_t N,
+                         int64_t T, int32_t page_size, int32_t* block_table, int32_t max_pages,
+                         const int32_t* free_pages, int32_t num_free, const int32_t* free_start,
+                         int32_t* seq_lens, int32_t* positions, int64_t* slots,
+                         int32_t* free_end, int32_t* status_dev, kda_stream_t stream);
+
+/* Scalings of a rotation's frequencies for contexts longer than the trained one. */
+typedef enum {
+    KDA_ROPE_PLAIN = 0,    /* f_i = theta^(-2i / rot_dim)                               */
+    KDA_ROPE_LINEAR = 1,   /* positions interpolated: f_i / factor                      */
+    KDA_ROPE_NTK = 2,      /* theta * factor^(rot_dim / (rot_dim - 2)) as the base      */
+    KDA_ROPE_YARN = 3      /* by parts: channels that turn more than beta_fast times in
+                              original_len tokens keep f_i, fewer than beta_slow take
+                              f_i / factor, a linear ramp between (in channel index);
+                              rotated values are scaled by 0.1 ln(factor) + 1           */
+} kda_rope_scaling;
+
+/*
+ * kda_rope_inv_freq -- host function: fills inv_freq_host[rot_dim / 2] (FP64
+ * arithmetic, rounded once to F32) and *rope_scale_host (1 except for YaRN).
+ * The published methods: rotary embedding (Su et al. 2021), position
+ * interpolation (Chen et al. 2023), NTK-aware base change, YaRN (Peng et al.
+ * 2023).  theta > 1 and factor >= 1; original_len, beta_fast > beta_slow > 0 are
+ * read for KDA_ROPE_YARN only, and factor is not read for KDA_ROPE_PLAIN.
+ */
+kda_status kda_rope_inv_freq(int32_t rot_dim, double theta, int32_t scaling, double factor,
+                             double original_len, double beta_fast, double beta_slow,
+                             float* inv_freq_host, float* rope_scale_host);
+
+/*
+ * kda_qk_norm_rope -- per-head RMS norm of queries and keys and their rotation
+ * by position, in one pass: per row x of D channels (one token, one head),
+ *   n = x / sqrt(mean(x^2) + eps) * weight         (qk_norm = 1; else n = x)
+ *   a' = a cos - b sin,  b' = a sin + b cos        for each rotated pair (a, b)
+ * with the angle position * inv_freq[i] for pair i, cos and sin multiplied by
+ * rope_scale, and channels rot_dim .. D-1 left as normed.
+ *   interleaved = 0: pair i is channels (i, i + rot_dim / 2); 1: (2 i, 2 i + 1)
+ * FP32 arithmetic, rounded once to out_dtype.  The angle's turns are exact to
+ * 2^-53 times the position (64-bit fixed point), so far positions lose nothing.
+ *
+ *   q [T, Hq, D], k [T, Hk, D]  x_dtype; token t's heads start at t * q_stride
+ *               (k_stride) elements, so both can lie in one fused projection:
+ *               stride >= heads * D, and a multiple of 16 bytes
+ *   positions [T] int32;  inv_freq [rot_dim / 2] F32 (NULL when rot_dim = 0)
+ *   q_weight, k_weight [D] F32, or NULL for ones (unread when qk_norm = 0)
+ *   q_out [T, Hq, D], k_out [T, Hk, D]  out_dtype, dense; may be q (k) where
+ *               that is dense and of the same type
+ * D = 64 or 128, rot_dim a multiple of 16 and at most D (else
+ * KDA_ERR_UNSUPPORTED); Hq, Hk >= 1; 0 <= T < 2^31.
+ */
+kda_status kda_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            int32_t x_dtype, const int32_t* positions, const float* inv_freq,
+                            int32_t rot_dim, int32_t interleaved, float rope_scale,
+                            const float* q_weight, const float* k_weight, float eps,
+                            int32_t qk_norm, int64_t T, int32_t Hq, int32_t Hk, int32_t D,
+                            void* q_out, void* k_out, int32_t out_dtype, kda_stream_t stream);
+
+/*
+ * kda_qk_norm_rope_append -- kda_qk_norm_rope whose keys go to their pages, with
+ * the values: k_cache[slot] = normed and rotated k, v_cache[slot] = v, for the
+ * slot slots[t] of each token (a negative slot writes no key or value; one past
+ * the cache sets KDA_ERR_DEVICE_ARG in status_dev and writes none).
+ *   v [T, Hk, D] x_dtype with v_stride as k;  slots [T] int64 (kda_page_plan)
+ *   q_out [T, Hq, D] cache_dtype;  k_cache, v_cache [num_pages, Hk, page_size, D]
+ *               cache_dtype; page_size >= 1
+ */
+kda_status kda_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k,
+                                   int64_t k_stride, const void* v, int64_t v_stride,
+                                   int32_t x_dtype, const int32_t* positions,
+                                   const int64_t* slots, const float* inv_freq, int32_t rot_dim,
+                                   int32_t interleaved, float rope_scale, const float* q_weight,
+                                   const float* k_weight, float eps, int32_t qk_norm, int64_t T,
+                                   int32_t Hq, int32_t Hk, int32_t D, void* q_out, void* k_cache,
+                                   void* v_cache, int32_t cache_dtype, int32_t num_pages,
+                                   int32_t page_size, int32_t* status_dev, kda_stream_t stream);
+
+/* Bytes of workspace kda_qk_norm_rope_bwd needs (partial weight gradients). */
+kda_status kda_qk_norm_rope_bwd_workspace_size(int64_t T, int32_t Hq, int32_t Hk, int32_t D,
+                                               int64_t* bytes_host);
+
+/*
+ * kda_qk_norm_rope_bwd -- the vector-Jacobian product of kda_qk_norm_rope: from
+ * dq_out, dk_out (dense, dy_dtype) the gradients q_grad [T, Hq, D], k_grad
+ * [T, Hk, D] (dense, grad_dtype) and q_weight_grad, k_weight_grad [D] F32 (each
+ * may be NULL: not computed; not written when qk_norm = 0).  Per row, with
+ * d = the transposed rotation of dy, n = x rstd, h = d * weight:
+ *   dx = rstd (h - n mean(h n)),   dweight = sum over tokens and heads of d n
+ * FP32 arithmetic; the sums are taken in an order that only the sizes set, so
+ * the same call gives the same bits.  workspace: 16-byte aligned, at least
+ * kda_qk_norm_rope_bwd_workspace_size bytes, contents on entry irrelevant.  No
+ * output may be an input or another output, except that q_grad (k_grad) may be
+ * dq_out (dk_out) where the types match.
+ */
+kda_status kda_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                int32_t x_dtype, const void* dq_out, const void* dk_out,
+                                int32_t dy_dtype, const int32_t* positions,
+                                const float* inv_freq, int32_t rot_dim, int32_t interleaved,
+                                float rope_scale, const float* q_weight, const float* k_weight,
+                                float eps, int32_t qk_norm, int64_t T, int32_t Hq, int32_t Hk,
+                                int32_t D, void* q_grad, void* k_grad, int32_t grad_dtype,
+                                float* q_weight_grad, float* k_weight_grad, void* workspace,
+                                int64_t workspace_bytes, kda_stream_t stream);
+
+/* Bytes of workspace kda_paged_decode needs (states of the pieces of a split row);
+ * the same for every length. */
+kda_status kda_paged_decode_workspace_size(int32_t N, int32_t Hq, int32_t Hk, int32_t D,
+                                           int64_t* bytes_host);
+
+/*
+ * kda_paged_decode -- attention of one new token per request over its pages:
+ * for request n of L = seq_lens[n] tokens (the new one's key and value already
+ * appended) and query head h, reading key-value head h / (Hq / Hk),
+ *   s_t = scale * q . k_t,  out = sum_t e^(s_t) v_t / sum_t e^(s_t),  t < L
+ *   lse = log sum_t e^(s_t)
+ * in one pass over the keys and values with a running maximum and sum, the
+ * lengths of all requests together split evenly over the GPU and the pieces of
+ * a row joined from their (maximum, sum, output) in a second kernel.
+ * L = 0 gives a row of zeros and lse -infinity.  What a page holds past the
+ * request's last token is never used, whatever it is (NaN included).
+ *
+ *   q [N, Hq, D] dtype;  k_cache, v_cache [num_pages, Hk, page_size, D] dtype
+ *   block_table [N, max_pages] int32, seq_lens [N] int32
+ *   out [N, Hq, D] out_dtype;  lse [N, Hq] F32 or NULL (natural logarithm)
+ * Scores, statistics and output sums are FP32.  F32: products are IEEE FP32.
+ * BF16: products of BF16 values are exact; each weight e^(s_t) is used as two
+ * BF16 parts (16 significant bits, relative error 2^-17).
+ * A length outside [0, max_pages * page_size] counts as 0 and sets
+ * KDA_ERR_DEVICE_ARG in status_dev; a page outside [0, num_pages) that a
+ * request's length reaches sets it too: nothing outside the cache is read, and
+ * that request's rows are undefined.
+ * D = 64 or 128; page_size a power of two in 8 .. 1024; Hq a multiple of Hk; at
+ * most 2^31 - 1 rows in the cache (num_pages * Hk * page_size) (else
+ * KDA_ERR_UNSUPPORTED).  workspace: 16-byte aligned, at least
+ * kda_paged_decode_workspace_size bytes, contents on entry irrelevant; calls
+ * that share one must be ordered on one stream.
+ */
+kda_status kda_paged_decode(const void* q, const void* k_cache, const void* v_cache,
+                            int32_t dtype, const int32_t* block_table, const int32_t* seq_lens,
+                            int32_t N, int32_t Hq, int32_t Hk, int32_t D, int32_t num_pages,
+                            int32_t page_size, int32_t max_pages, float scale, void* out,
+                            int32_t out_dtype, float* lse, void* workspace,
+                            int64_t workspace_bytes, int32_t* status_dev, kda_stream_t stream);
+
 /*
  * kda_test_set_fault -- TEST HOOK, not for production use (no page
  * counterpart).  Lets a test make a bounded device wait run out without
@@ -440,7 +633,8 @@ const char* kda_status_string(int32_t status);
  * 3: workspace arguments; kda_chunk_workspace_size.  Later additions that
  * change no existing signature keep the number: kda_chunk_fwd_static,
  * kda_gated_rmsnorm, kda_chunk_bwd_workspace_size, kda_chunk_bwd,
- * KDA_ERR_RANGE, kda_test_set_fault, kda_chunk_fwd_gated_norm). */
+ * KDA_ERR_RANGE, kda_test_set_fault, kda_chunk_fwd_gated_norm, the paged
+ * attention entry points and KDA_ERR_NO_PAGES). */
 int32_t kda_abi_version(void);
 
 #ifdef __cplusplus

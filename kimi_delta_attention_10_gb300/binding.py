@@ -24,6 +24,7 @@ KDA_ERR_TIMEOUT = 5
 KDA_ERR_DEVICE_ARG = 6
 KDA_ERR_TOO_LARGE = 7
 KDA_ERR_RANGE = 8
+KDA_ERR_NO_PAGES = 9
 
 # kda_test_set_fault values (test hook)
 KDA_TEST_FAULT_NONE = 0
@@ -43,7 +44,10 @@ MODES = {"bf16_tc": KDA_MODE_BF16_TC, "fp32_exact": KDA_MODE_FP32_EXACT}
 EXPORTS = ("kda_gate", "kda_chunk_workspace_size", "kda_chunk_fwd", "kda_chunk_fwd_gated",
            "kda_chunk_fwd_gated_norm",
            "kda_chunk_fwd_static", "kda_recurrent_step", "kda_gated_rmsnorm",
-           "kda_chunk_bwd_workspace_size", "kda_chunk_bwd", "kda_test_set_fault",
+           "kda_chunk_bwd_workspace_size", "kda_chunk_bwd", "kda_page_plan",
+           "kda_rope_inv_freq", "kda_qk_norm_rope", "kda_qk_norm_rope_append",
+           "kda_qk_norm_rope_bwd_workspace_size", "kda_qk_norm_rope_bwd",
+           "kda_paged_decode_workspace_size", "kda_paged_decode", "kda_test_set_fault",
            "kda_status_string", "kda_abi_version")
 
 _lock = threading.Lock()
@@ -106,6 +110,29 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
                                       ctypes.c_float, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp,
                                       vp, vp, i64, vp, vp]
         lib.kda_chunk_bwd.restype = i32
+        f32, f64 = ctypes.c_float, ctypes.c_double
+        lib.kda_page_plan.argtypes = [vp, vp, i32, i64, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp,
+                                      vp, vp]
+        lib.kda_page_plan.restype = i32
+        lib.kda_rope_inv_freq.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp, vp]
+        lib.kda_rope_inv_freq.restype = i32
+        rope = [vp, vp, i32, i32, f32, vp, vp, f32, i32, i64, i32, i32, i32]
+        lib.kda_qk_norm_rope.argtypes = [vp, i64, vp, i64, i32, *rope, vp, vp, i32, vp]
+        lib.kda_qk_norm_rope.restype = i32
+        lib.kda_qk_norm_rope_append.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, *rope, vp, vp,
+                                                vp, i32, i32, i32, vp, vp]
+        lib.kda_qk_norm_rope_append.restype = i32
+        lib.kda_qk_norm_rope_bwd_workspace_size.argtypes = [i64, i32, i32, i32,
+                                                            ctypes.POINTER(i64)]
+        lib.kda_qk_norm_rope_bwd_workspace_size.restype = i32
+        lib.kda_qk_norm_rope_bwd.argtypes = [vp, i64, vp, i64, i32, vp, vp, i32, *rope, vp, vp,
+                                             i32, vp, vp, vp, i64, vp]
+        lib.kda_qk_norm_rope_bwd.restype = i32
+        lib.kda_paged_decode_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.POINTER(i64)]
+        lib.kda_paged_decode_workspace_size.restype = i32
+        lib.kda_paged_decode.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
+                                         i32, f32, vp, i32, vp, vp, i64, vp, vp]
+        lib.kda_paged_decode.restype = i32
         lib.kda_test_set_fault.argtypes = [i32]
         lib.kda_test_set_fault.restype = i32
         lib.kda_status_string.argtypes = [i32]
@@ -441,3 +468,292 @@ def kda_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     if st != KDA_OK:
         raise KDAError(st, "kda_chunk_bwd")
     return dq, dk, dv, dg, dbeta, dinit
+
+
+# ---------------------------------------------------------------- paged attention
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def _int_ptr(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, n: int = -1) -> Optional[int]:
+    """Device pointer of a contiguous integer tensor of `n` elements (any if negative)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if n >= 0 and t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, not {t.numel()}")
+    return _dev_ptr(t, name)
+
+
+def _f32_ptr(t: Optional[torch.Tensor], name: str, n: int) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32, not {t.dtype}")
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, not {t.numel()}")
+    return _dev_ptr(t, name)
+
+
+def _rows_ptr(t: torch.Tensor, name: str, T: int, H: int, D: int):
+    """(pointer, token stride) of [T, H, D] whose heads are dense within a token."""
+    if t.shape != (T, H, D):
+        raise ValueError(f"{name} must have shape {(T, H, D)}, not {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise RuntimeError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    st, sh, sc = t.stride()
+    if (sc != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be dense (strides {t.stride()})")
+    return t.data_ptr(), st if T > 1 else H * D
+
+
+def _dense_ptr(t: torch.Tensor, name: str, shape, dtype: torch.dtype) -> int:
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    return _dev_ptr(t, name)
+
+
+def kda_page_plan(cached_lens: torch.Tensor, cu_seqlens: torch.Tensor, block_table: torch.Tensor,
+                  free_pages: torch.Tensor, page_size: int, num_tokens: int,
+                  free_start: Optional[torch.Tensor] = None,
+                  seq_lens: Optional[torch.Tensor] = None,
+                  positions: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                  free_end: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None):
+    """Pages, slots and positions of the new tokens of N requests, from lengths on the
+    device: cached_lens [N], cu_seqlens [N+1] packing num_tokens new tokens, block_table
+    [N, max_pages] (new entries written in place), free_pages (taken in order from
+    free_start).  Returns (seq_lens [N], positions [T], slots [T] int64, free_end [1])."""
+    lib = load_library()
+    N, T = cached_lens.numel(), int(num_tokens)
+    if block_table.dim() != 2 or block_table.shape[0] != N:
+        raise ValueError(f"block_table must have shape [{N}, max_pages]")
+    dev, i32 = cached_lens.device, torch.int32
+    if seq_lens is None:
+        seq_lens = torch.empty(N, dtype=i32, device=dev)
+    if positions is None:
+        positions = torch.empty(T, dtype=i32, device=dev)
+    if slots is None:
+        slots = torch.empty(T, dtype=torch.int64, device=dev)
+    if free_end is None:
+        free_end = torch.empty(1, dtype=i32, device=dev)
+    st = lib.kda_page_plan(
+        _int_ptr(cached_lens, "cached_lens", i32), _int_ptr(cu_seqlens, "cu_seqlens", i32, N + 1),
+        N, T, int(page_size), _int_ptr(block_table, "block_table", i32), block_table.shape[1],
+        _int_ptr(free_pages, "free_pages", i32), free_pages.numel(),
+        _int_ptr(free_start, "free_start", i32, 1), _int_ptr(seq_lens, "seq_lens", i32, N),
+        _int_ptr(positions, "positions", i32, T), _int_ptr(slots, "slots", torch.int64, T),
+        _int_ptr(free_end, "free_end", i32, 1), _dev_ptr(status, "status"),
+        _stream_handle(stream, dev))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_page_plan")
+    return seq_lens, positions, slots, free_end
+
+
+def rope_inv_freq(rot_dim: int, theta: float = 10000.0, scaling: str = "plain",
+                  factor: float = 1.0, original_len: float = 0.0, beta_fast: float = 32.0,
+                  beta_slow: float = 1.0, device=None) -> Tuple[torch.Tensor, float]:
+    """(inv_freq [rot_dim / 2] FP32 on `device`, rope_scale) of a rotation, scaled for long
+    contexts by "linear", "ntk" or "yarn" (the last reads original_len and the betas)."""
+    f = torch.empty(max(rot_dim, 0) // 2, dtype=torch.float32)
+    m = ctypes.c_float(1.0)
+    st = load_library().kda_rope_inv_freq(rot_dim, theta, ROPE_SCALINGS[scaling], factor,
+                                          original_len, beta_fast, beta_slow, f.data_ptr(),
+                                          ctypes.addressof(m))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_rope_inv_freq")
+    return f.to(device) if device is not None else f, m.value
+
+
+def _rope_args(positions, inv_freq, T, Hq, Hk, D, q_weight, k_weight, eps, qk_norm, interleaved,
+               rope_scale):
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    return (_int_ptr(positions, "positions", torch.int32, T),
+            _f32_ptr(inv_freq, "inv_freq", rot // 2) if rot else None, rot,
+            1 if interleaved else 0, float(rope_scale), _f32_ptr(q_weight, "q_weight", D),
+            _f32_ptr(k_weight, "k_weight", D), float(eps), 1 if qk_norm else 0, T, Hq, Hk, D)
+
+
+def kda_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
+                     inv_freq: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     qk_norm: bool = True, interleaved: bool = False, rope_scale: float = 1.0,
+                     q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                     out_dtype: Optional[torch.dtype] = None,
+                     stream: Optional[torch.cuda.Stream] = None):
+    """Per-head RMS norm of q [T,Hq,D] and k [T,Hk,D] (weights [D] or None) and rotation of
+    the first 2 * len(inv_freq) channels by position, in one pass (None: no rotation).  q and
+    k may be slices of one projection.  Returns (q_out, k_out)."""
+    lib = load_library()
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    if k.dtype != q.dtype:
+        raise TypeError(f"k must be {q.dtype}, not {k.dtype}")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=out_dtype or q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((T, Hk, D), dtype=q_out.dtype, device=q.device)
+    st = lib.kda_qk_norm_rope(
+        *_rows_ptr(q, "q", T, Hq, D), *_rows_ptr(k, "k", T, Hk, D), _dtype_code(q),
+        *_rope_args(positions, inv_freq, T, Hq, Hk, D, q_weight, k_weight, eps, qk_norm,
+                    interleaved, rope_scale),
+        _dense_ptr(q_out, "q_out", (T, Hq, D), q_out.dtype),
+        _dense_ptr(k_out, "k_out", (T, Hk, D), q_out.dtype), _dtype_code(q_out),
+        _stream_handle(stream, q.device))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_qk_norm_rope")
+    return q_out, k_out
+
+
+def _cache_shape(k_cache, v_cache, Hk, D):
+    if k_cache.dim() != 4 or k_cache.shape[1] != Hk or k_cache.shape[3] != D:
+        raise ValueError(f"k_cache must have shape [num_pages, {Hk}, page_size, {D}], not "
+                         f"{tuple(k_cache.shape)}")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("v_cache must have the shape and dtype of k_cache")
+
+
+def kda_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                            positions: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+                            v_cache: torch.Tensor, inv_freq: Optional[torch.Tensor],
+                            q_weight: Optional[torch.Tensor] = None,
+                            k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                            qk_norm: bool = True, interleaved: bool = False,
+                            rope_scale: float = 1.0, q_out: Optional[torch.Tensor] = None,
+                            status: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """kda_qk_norm_rope with the keys, and the values v [T,Hk,D], written to the slots
+    (int64 [T], negative: skipped) of k_cache and v_cache [num_pages,Hk,page_size,D] in
+    place.  Returns q_out in the cache's dtype."""
+    lib = load_library()
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError(f"k and v must be {q.dtype}, not {k.dtype} and {v.dtype}")
+    _cache_shape(k_cache, v_cache, Hk, D)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=k_cache.dtype, device=q.device)
+    st = lib.kda_qk_norm_rope_append(
+        *_rows_ptr(q, "q", T, Hq, D), *_rows_ptr(k, "k", T, Hk, D), *_rows_ptr(v, "v", T, Hk, D),
+        _dtype_code(q), *_append_args(slots, positions, inv_freq, T, Hq, Hk, D, q_weight, k_weight,
+                                      eps, qk_norm, interleaved, rope_scale),
+        _dense_ptr(q_out, "q_out", (T, Hq, D), k_cache.dtype), _dev_ptr(k_cache, "k_cache"),
+        _dev_ptr(v_cache, "v_cache"), _dtype_code(k_cache), k_cache.shape[0], k_cache.shape[2],
+        _dev_ptr(status, "status"), _stream_handle(stream, q.device))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_qk_norm_rope_append")
+    return q_out
+
+
+def _append_args(slots, positions, inv_freq, T, *rest):
+    """_rope_args with the slots after the positions."""
+    pos, *more = _rope_args(positions, inv_freq, T, *rest)
+    return (pos, _int_ptr(slots, "slots", torch.int64, T), *more)
+
+
+def qk_norm_rope_bwd_workspace_size(T: int, Hq: int, Hk: int, D: int = 128) -> int:
+    """Bytes of workspace kda_qk_norm_rope_bwd needs."""
+    out = ctypes.c_int64(0)
+    st = load_library().kda_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D, ctypes.byref(out))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_qk_norm_rope_bwd_workspace_size")
+    return out.value
+
+
+def kda_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor,
+                         dk_out: torch.Tensor, positions: torch.Tensor,
+                         inv_freq: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                         k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                         qk_norm: bool = True, interleaved: bool = False, rope_scale: float = 1.0,
+                         q_grad: Optional[torch.Tensor] = None,
+                         k_grad: Optional[torch.Tensor] = None,
+                         grad_dtype: Optional[torch.dtype] = None,
+                         stream: Optional[torch.cuda.Stream] = None, workspace=None):
+    """Backward of kda_qk_norm_rope.  Returns (q_grad, k_grad, q_weight_grad, k_weight_grad):
+    the first two FP32 unless grad_dtype or given tensors say otherwise, the weights' FP32
+    (None where the weight is None or qk_norm is off).  workspace: None (a fresh buffer) or a
+    CUDA tensor of at least qk_norm_rope_bwd_workspace_size(...) bytes."""
+    lib = load_library()
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    dev = q.device
+    if k.dtype != q.dtype:
+        raise TypeError(f"k must be {q.dtype}, not {k.dtype}")
+    if q_grad is None:
+        q_grad = torch.empty((T, Hq, D), dtype=grad_dtype or torch.float32, device=dev)
+    if k_grad is None:
+        k_grad = torch.empty((T, Hk, D), dtype=q_grad.dtype, device=dev)
+    wgrad = [torch.empty(D, dtype=torch.float32, device=dev) if w is not None and qk_norm else None
+             for w in (q_weight, k_weight)]
+    if workspace is None and (wgrad[0] is not None or wgrad[1] is not None):
+        workspace = torch.empty(qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D), dtype=torch.uint8,
+                                device=dev)
+    st = lib.kda_qk_norm_rope_bwd(
+        *_rows_ptr(q, "q", T, Hq, D), *_rows_ptr(k, "k", T, Hk, D), _dtype_code(q),
+        _dense_ptr(dq_out, "dq_out", (T, Hq, D), dq_out.dtype),
+        _dense_ptr(dk_out, "dk_out", (T, Hk, D), dq_out.dtype), _dtype_code(dq_out),
+        *_rope_args(positions, inv_freq, T, Hq, Hk, D, q_weight, k_weight, eps, qk_norm,
+                    interleaved, rope_scale),
+        _dense_ptr(q_grad, "q_grad", (T, Hq, D), q_grad.dtype),
+        _dense_ptr(k_grad, "k_grad", (T, Hk, D), q_grad.dtype), _dtype_code(q_grad),
+        _dev_ptr(wgrad[0], "q_weight_grad"), _dev_ptr(wgrad[1], "k_weight_grad"),
+        _dev_ptr(workspace, "workspace"),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream_handle(stream, dev))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_qk_norm_rope_bwd")
+    return q_grad, k_grad, wgrad[0], wgrad[1]
+
+
+def paged_decode_workspace_size(N: int, Hq: int, Hk: int, D: int = 128) -> int:
+    """Bytes of workspace kda_paged_decode needs, whatever the lengths."""
+    out = ctypes.c_int64(0)
+    st = load_library().kda_paged_decode_workspace_size(N, Hq, Hk, D, ctypes.byref(out))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_paged_decode_workspace_size")
+    return out.value
+
+
+def kda_paged_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     block_table: torch.Tensor, seq_lens: torch.Tensor,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     out_dtype: Optional[torch.dtype] = None, lse: Optional[torch.Tensor] = None,
+                     want_lse: bool = False, status: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None, workspace=None):
+    """Attention of one new token per request, q [N,Hq,D], over the pages of k_cache and
+    v_cache [num_pages,Hk,page_size,D] named by block_table [N,max_pages], seq_lens [N] tokens
+    each.  Returns (out [N,Hq,D], lse [N,Hq] or None).  workspace: None (a fresh buffer) or a
+    CUDA tensor of at least paged_decode_workspace_size(...) bytes."""
+    lib = load_library()
+    N, Hq, D = q.shape
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must have shape [num_pages, Hk, page_size, D]")
+    num_pages, Hk, page_size = k_cache.shape[:3]
+    _cache_shape(k_cache, v_cache, Hk, D)
+    if block_table.dim() != 2 or block_table.shape[0] != N:
+        raise ValueError(f"block_table must have shape [{N}, max_pages]")
+    if scale is None:
+        scale = D ** -0.5
+    dev = q.device
+    if out is None:
+        out = torch.empty((N, Hq, D), dtype=out_dtype or q.dtype, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(paged_decode_workspace_size(N, Hq, Hk, D), dtype=torch.uint8,
+                                device=dev)
+    st = lib.kda_paged_decode(
+        _dense_ptr(q, "q", (N, Hq, D), k_cache.dtype), _dev_ptr(k_cache, "k_cache"),
+        _dev_ptr(v_cache, "v_cache"), _dtype_code(k_cache),
+        _int_ptr(block_table, "block_table", torch.int32),
+        _int_ptr(seq_lens, "seq_lens", torch.int32, N), N, Hq, Hk, D, num_pages, page_size,
+        block_table.shape[1], float(scale), _dense_ptr(out, "out", (N, Hq, D), out.dtype),
+        _dtype_code(out), _f32_ptr(lse, "lse", N * Hq), _dev_ptr(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _dev_ptr(status, "status"),
+        _stream_handle(stream, dev))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_paged_decode")
+    return out, lse

@@ -50,6 +50,7 @@ const char* kda_status_string(int32_t s)
             return "problem needs more than the 64 MiB static scratch of kda_chunk_fwd_static";
         case KDA_ERR_RANGE:
             return "device stored a non-finite value (an input or an FP16 operand out of range)";
+        case KDA_ERR_NO_PAGES: return "a request needs more pages than its table row or the free list holds";
         default: return "unknown status";
     }
 }

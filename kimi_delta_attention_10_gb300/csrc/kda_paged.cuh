@@ -1,0 +1,151 @@
+// Internal declarations of the paged-attention entry points (not public):
+// launch arguments, and the device code shared by their kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+// ---------------------------------------------------------------- launches
+struct PlanArgs {
+    const int32_t* cached;
+    const int32_t* cu;
+    int32_t N;
+    int32_t T;
+    int32_t page;
+    int32_t* table;
+    int32_t max_pages;
+    const int32_t* free_pages;
+    int32_t num_free;
+    const int32_t* free_start;
+    int32_t* seq_lens;
+    int32_t* positions;
+    int64_t* slots;
+    int32_t* free_end;
+    int32_t* status;
+};
+cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t stream);
+
+struct RopeArgs {
+    const void* q;
+    const void* k;
+    const void* v;           // append only
+    int64_t q_stride;        // elements between tokens
+    int64_t k_stride;
+    int64_t v_stride;
+    bool x_bf16;
+    const int32_t* positions;
+    const float* inv_freq;
+    int32_t rot;
+    int32_t interleaved;
+    float rope_scale;
+    const float* q_weight;
+    const float* k_weight;
+    float eps;
+    int32_t norm;
+    int32_t T;
+    int32_t Hq;
+    int32_t Hk;
+    int32_t D;
+    void* q_out;             // forward: outputs; backward: q_grad, k_grad
+    void* k_out;
+    bool out_bf16;
+    // append: k_out and v_out are the caches
+    void* v_out;
+    const int64_t* slots;
+    int64_t num_slots;
+    int32_t page;
+    int32_t* status;
+    // backward
+    const void* dq;
+    const void* dk;
+    bool dy_bf16;
+    float* q_wgrad;
+    float* k_wgrad;
+    float* partials;
+};
+cudaError_t launch_qk_rope(const RopeArgs& a, bool append, cudaStream_t stream);
+cudaError_t launch_qk_rope_bwd(const RopeArgs& a, cudaStream_t stream);
+int64_t qk_rope_bwd_workspace_bytes(int32_t D);
+
+struct DecodeArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    bool bf16;
+    const int32_t* table;
+    const int32_t* seq_lens;
+    int32_t N;
+    int32_t Hq;
+    int32_t Hk;
+    int32_t D;
+    int32_t num_pages;
+    int32_t page_shift;
+    int32_t max_pages;
+    float scale;
+    void* out;
+    bool out_bf16;
+    float* lse;
+    void* workspace;
+    int32_t* status;
+};
+int64_t paged_decode_workspace_bytes(int32_t N, int32_t Hq, int32_t Hk, int32_t D);
+cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------- vectors
+// 16 bytes of a row as FP32 values.
+template <typename T> struct Vec16;
+template <> struct Vec16<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void unpack(uint4 u, float (&f)[4])
+    {
+        f[0] = __uint_as_float(u.x);
+        f[1] = __uint_as_float(u.y);
+        f[2] = __uint_as_float(u.z);
+        f[3] = __uint_as_float(u.w);
+    }
+};
+template <> struct Vec16<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void unpack(uint4 u, float (&f)[8])
+    {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// Stores N consecutive values (N * sizeof(TOut) a multiple of 8 bytes, aligned).
+template <int N>
+__device__ __forceinline__ void store_vec(float* p, const float (&f)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        *reinterpret_cast<float4*>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+}
+template <int N>
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&f)[N])
+{
+    if constexpr (N == 8) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                                  pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    } else {
+        static_assert(N == 4, "four or eight values");
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+    }
+}
+
+}  // namespace kda

@@ -1,0 +1,199 @@
+// kda_page_plan: block tables, slots and positions from request lengths.
+//
+// With P tokens to a page, request n of c cached and m new tokens holds
+// have = ceil(c / P) pages and wants ceil((c + m) / P); its new pages are
+// free[base ..), base = the pages wanted by the requests before it.
+//
+// Latency-bound: the bytes of a decode step (a few KB) take nanoseconds, the
+// launch and one chain of dependent loads microseconds.  So there is one launch
+// and no scan across CTAs: each CTA owns a run of consecutive tokens, reads all
+// N lengths once (coalesced, independent loads) and sums the pages wanted before
+// its run, then walks the requests of its run, one per thread, with a scan in
+// shared memory.  Only requests with new tokens want pages, so a run's tokens
+// are all that is needed to place its pages.  N lengths per CTA cost N / 256
+// loads a thread: up to N in the ten thousands they hide behind the launch.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_paged.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int NT = 256;
+constexpr int NW = NT / 32;
+
+struct Need {
+    int32_t have;      // pages held
+    int32_t pages;     // new pages wanted (0 when the row is too short)
+    bool fits;
+};
+
+__device__ __forceinline__ Need need_of(int32_t c, int32_t m, const PlanArgs& a)
+{
+    Need r;
+    // unsigned: c + m and the round-up reach 2^31 + P - 1 at most
+    const uint32_t P = (uint32_t)a.page;
+    r.have = (int32_t)(((uint32_t)c + P - 1u) / P);
+    const int32_t want = (int32_t)(((uint32_t)c + (uint32_t)m + P - 1u) / P);
+    r.fits = want <= a.max_pages;
+    r.pages = r.fits ? want - r.have : 0;
+    return r;
+}
+
+// Inclusive scan of one value per thread over the CTA; *total gets the sum.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* warp_sums, int64_t* total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();                       // warp_sums may still be read
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        if (w < warp) before += warp_sums[w];
+        all += warp_sums[w];
+    }
+    *total = all;
+    return x + before;
+}
+
+__global__ void __launch_bounds__(NT) page_plan_kernel(PlanArgs a)
+{
+    __shared__ int64_t sums[NW];
+    __shared__ int32_t s_cu[NT + 1], s_c[NT], s_have[NT];
+    __shared__ int64_t s_base[NT];         // < 0: the request is not served
+    const int tid = threadIdx.x;
+    const int64_t t0 = (int64_t)blockIdx.x * a.T / gridDim.x;
+    const int64_t t1 = (int64_t)(blockIdx.x + 1) * a.T / gridDim.x;
+
+    // Pages wanted before the run, pages wanted at all, the run's first request.
+    int64_t before = 0, all = 0;
+    int32_t first = 0;
+    bool bad = false;
+    for (int32_t n = tid; n < a.N; n += NT) {
+        const int32_t c = a.cached[n], lo = a.cu[n], hi = a.cu[n + 1];
+        if (c < 0 || lo < 0 || hi < lo || hi > a.T || hi - lo > INT32_MAX - c ||
+            (n == 0 && lo != 0) || (n == a.N - 1 && hi != a.T)) {
+            bad = true;
+            continue;
+        }
+        const int32_t pages = need_of(c, hi - lo, a).pages;
+        all += pages;
+        if (hi <= t0) {
+            before += pages;
+            ++first;
+        }
+    }
+    if (a.N == 0 && a.T != 0) bad = true;
+    if (__syncthreads_or(bad)) {
+        for (int64_t t = t0 + tid; t < t1; t += NT) {
+            a.positions[t] = 0;
+            a.slots[t] = -1;
+        }
+        if (blockIdx.x == 0) {
+            for (int32_t n = tid; n < a.N; n += NT) a.seq_lens[n] = a.cached[n];
+            if (tid == 0) {
+                *a.free_end = a.free_start ? *a.free_start : 0;
+                report_status(a.status, KDA_ERR_DEVICE_ARG);
+            }
+        }
+        return;
+    }
+    int64_t base, total, firsts;
+    block_scan(before, sums, &base);
+    block_scan(first, sums, &firsts);
+    block_scan(all, sums, &total);
+    const int64_t start = a.free_start ? *a.free_start : 0;
+    const int64_t room = start < 0 || start > a.num_free ? 0 : a.num_free - start;
+    if (blockIdx.x == 0 && tid == 0) {
+        if (start < 0 || start > a.num_free) report_status(a.status, KDA_ERR_DEVICE_ARG);
+        if (total <= room) *a.free_end = (int32_t)(start + total);
+    }
+    // Requests without new tokens take nothing and belong to no run.
+    for (int64_t n = (int64_t)blockIdx.x * NT + tid; n < a.N; n += (int64_t)gridDim.x * NT)
+        if (a.cu[n + 1] == a.cu[n]) {
+            a.seq_lens[n] = a.cached[n];
+            if (!need_of(a.cached[n], 0, a).fits) report_status(a.status, KDA_ERR_NO_PAGES);
+        }
+
+    int64_t done = t0;
+    for (int64_t n0 = firsts; n0 < a.N && done < t1; n0 += NT) {
+        const int64_t n = n0 + tid;
+        int32_t c = 0, lo = a.T, hi = a.T;
+        Need w = {0, 0, true};
+        if (n < a.N) {
+            c = a.cached[n];
+            lo = a.cu[n];
+            hi = a.cu[n + 1];
+            w = need_of(c, hi - lo, a);
+        }
+        int64_t chunk;
+        const int64_t upto = base + block_scan(w.pages, sums, &chunk);   // pages taken up to n
+        const int64_t mine = upto - w.pages;
+        const bool ok = w.fits && (w.pages == 0 || upto <= room);
+        s_c[tid] = c;
+        s_have[tid] = w.have;
+        s_base[tid] = ok ? mine : -1;
+        s_cu[tid] = lo;
+        if (tid == NT - 1) s_cu[NT] = hi;
+        // the CTA of a request's first token writes what the request has one of
+        if (n < a.N && hi > lo && lo >= t0 && lo < t1) {
+            a.seq_lens[n] = ok ? c + (hi - lo) : c;
+            if (!ok) report_status(a.status, KDA_ERR_NO_PAGES);
+            if (!ok && w.fits && mine <= room) *a.free_end = (int32_t)(start + mine);
+        }
+        base += chunk;
+        __syncthreads();
+        const int64_t end = s_cu[NT] < t1 ? s_cu[NT] : t1;
+        for (int64_t t = done + tid; t < end; t += NT) {
+            int i = 0;                     // last request of the chunk with s_cu <= t
+#pragma unroll
+            for (int step = NT / 2; step > 0; step >>= 1)
+                if (s_cu[i + step] <= t) i += step;
+            const uint32_t P = (uint32_t)a.page;
+            const uint32_t pos = (uint32_t)s_c[i] + (uint32_t)(t - s_cu[i]);
+            const int32_t j = (int32_t)(pos / P), row = (int32_t)(pos - (uint32_t)j * P);
+            int64_t slot = -1;
+            if (s_base[i] >= 0) {
+                int32_t* entry = a.table + (n0 + i) * a.max_pages + j;
+                int32_t id;
+                if (j >= s_have[i]) {
+                    id = a.free_pages[start + s_base[i] + (j - s_have[i])];
+                    if (row == 0) *entry = id;
+                } else {
+                    id = *entry;           // held before: no CTA writes it
+                }
+                if (id >= 0)
+                    slot = (int64_t)id * a.page + row;
+                else
+                    report_status(a.status, KDA_ERR_DEVICE_ARG);
+            }
+            a.positions[t] = (int32_t)pos;
+            a.slots[t] = slot;
+        }
+        done = end > done ? end : done;
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t stream)
+{
+    // one token a thread; beyond four CTAs an SM the runs get longer instead
+    const int sms = device_sm_count();
+    int64_t blocks = ((int64_t)a.T + NT - 1) / NT;
+    const int64_t most = 4 * (int64_t)(sms > 0 ? sms : 152);
+    if (blocks > most) blocks = most;
+    if (blocks < 1) blocks = 1;
+    page_plan_kernel<<<(unsigned)blocks, NT, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

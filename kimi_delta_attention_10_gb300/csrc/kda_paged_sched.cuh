@@ -1,0 +1,134 @@
+// How the decode attention's work is dealt out, shared by its kernels and the
+// join: every (request, head unit) row of `tiles` tiles lies on one axis of
+// W = units * sum_n tiles_n tiles, ordered by request, unit, tile; CTA b of
+// B = min(CTAs, W) takes the tiles [b W / B, (b + 1) W / B), at least one.  A row that a CTA covers whole is
+// finished there; of a split row each CTA leaves a piece (maximum, sum, unscaled
+// output) in one of its two slots: slot 2 b where the row began before the CTA's
+// tiles, 2 b + 1 where it begins in them.  A CTA has at most one of each.
+#pragma once
+
+#include <stdint.h>
+
+#include "kda_paged.cuh"
+
+namespace kda {
+
+struct DecodeShape {
+    int32_t units;        // head units per request
+    int32_t heads;        // query heads per unit (the last of a group may have fewer)
+    int32_t ctas;         // CTAs launched
+    int32_t tile_shift;   // log2 of the tokens per tile
+};
+
+// Workspace: int64 prefix of tiles [N + 1], then the pieces' (m, l) pairs
+// [2 CTAs][heads], then their outputs [2 CTAs][heads][D].
+__host__ __device__ inline int64_t decode_ml_offset(int32_t N)
+{
+    return ((int64_t)(N + 1) * 8 + 255) / 256 * 256;
+}
+__host__ __device__ inline int64_t decode_o_offset(int32_t N, const DecodeShape& s)
+{
+    return decode_ml_offset(N) + ((int64_t)2 * s.ctas * s.heads * 8 + 255) / 256 * 256;
+}
+
+__device__ __forceinline__ int32_t decode_len(const DecodeArgs& a, int32_t n)
+{
+    const int32_t L = a.seq_lens[n];
+    const int64_t most = (int64_t)a.max_pages << a.page_shift;
+    return L < 0 || L > most ? 0 : L;
+}
+
+__device__ __forceinline__ int32_t tiles_of(int32_t L, int shift)
+{
+    return (int32_t)(((int64_t)L + (1 << shift) - 1) >> shift);
+}
+
+struct DecodeRange {
+    int64_t begin, end;   // the CTA's tiles
+    int64_t at;           // tiles of the requests before `n`, all units
+    int32_t n;            // request of tile `begin`
+};
+
+// Called by NT threads of a CTA (a multiple of 32): where the CTA's tiles lie.
+// CTA 0 also stores the prefix of tiles for the join.
+template <int NT>
+__device__ __forceinline__ DecodeRange decode_range(const DecodeArgs& a, const DecodeShape& s,
+                                                    int64_t* prefix_out)
+{
+    __shared__ int64_t sums[NT / 32];
+    __shared__ DecodeRange range;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t per = (a.N + NT - 1) / NT;         // consecutive requests per thread
+    const int32_t n0 = min(tid * per, a.N), n1 = min(n0 + per, a.N);
+    int64_t mine = 0;
+    for (int32_t n = n0; n < n1; ++n) mine += tiles_of(decode_len(a, n), s.tile_shift);
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    if (lane == 31) sums[warp] = upto;
+    if (tid == 0) range.n = a.N;
+    __syncthreads();
+    int64_t total = 0, before = upto - mine;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    const int64_t W = total * s.units;
+    const int64_t B = W < s.ctas ? W : s.ctas, b = blockIdx.x;
+    const int64_t begin = b < B ? b * W / B : 0, end = b < B ? (b + 1) * W / B : 0;
+    if (begin < end && before * s.units <= begin && begin < (before + mine) * s.units) {
+        int64_t at = before;
+        int32_t n = n0;
+        for (;; ++n) {
+            const int64_t next = at + tiles_of(decode_len(a, n), s.tile_shift);
+            if (begin < next * s.units) break;
+            at = next;
+        }
+        range.n = n;
+        range.at = at * s.units;
+    }
+    if (blockIdx.x == 0) {
+        int64_t at = before;
+        for (int32_t n = n0; n < n1; ++n) {
+            prefix_out[n] = at;
+            at += tiles_of(decode_len(a, n), s.tile_shift);
+        }
+        if (tid == 0) prefix_out[a.N] = total;
+        for (int32_t n = n0; n < n1; ++n)
+            if (a.seq_lens[n] != decode_len(a, n)) report_status(a.status, KDA_ERR_DEVICE_ARG);
+    }
+    __syncthreads();
+    DecodeRange r = range;
+    r.begin = begin;
+    r.end = end;
+    return r;
+}
+
+// Joins the split rows and writes the rows of empty requests.
+cudaError_t launch_decode_join(const DecodeArgs& a, const DecodeShape& s, cudaStream_t stream);
+
+// The tensor-core kernel (BF16).
+DecodeShape decode_tc_shape(const DecodeArgs& a);
+cudaError_t launch_paged_decode_tc(const DecodeArgs& a, const DecodeShape& s, cudaStream_t stream);
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <typename T>
+__device__ __forceinline__ void store_one(T* p, float x);
+template <>
+__device__ __forceinline__ void store_one<float>(float* p, float x)
+{
+    *p = x;
+}
+template <>
+__device__ __forceinline__ void store_one<__nv_bfloat16>(__nv_bfloat16* p, float x)
+{
+    *p = __float2bfloat16_rn(x);
+}
+
+}  // namespace kda
