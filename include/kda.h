@@ -22,7 +22,8 @@
  *     (calls of that entry point share it; see there) and the process-wide
  *     test switch of kda_test_set_fault; calls of every other entry point on
  *     different streams are independent.
- *   - Every device pointer must be 16-byte aligned (KDA_ERR_ALIGNMENT).
+ *   - Every device pointer must be 16-byte aligned (KDA_ERR_ALIGNMENT), except
+ *     kda_page_plan's.
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = the legacy
  *     default stream).  The library never synchronises.
  *   - Argument errors are detected on the host before anything is launched:
@@ -456,6 +457,8 @@ kda_status kda_chunk_bwd(const void* q, const void* k, const void* v, int32_t qk
  *   seq_lens [N] int32, positions [T] int32, slots [T] int64, free_end [1] int32
  *               (written); seq_lens must not be cached_lens, nor free_end
  *               free_start (the kernel's CTAs read those while others write)
+ * The arrays of this entry point are read and written one integer at a time, so
+ * that a slice of a pool will do: 4-byte alignment (slots: 8) instead of 16.
  * N >= 0, 0 <= T < 2^31, page_size >= 1, max_pages >= 1, num_free >= 0.
  */
 kda_status kda_page_plan(const int32_t* cached_lens, const int32_t* cu_seqlens, int32_t N,

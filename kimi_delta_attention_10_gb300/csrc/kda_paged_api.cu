@@ -75,11 +75,14 @@ kda_status kda_page_plan(const int32_t* cached_lens, const int32_t* cu_seqlens, 
         return KDA_ERR_INVALID_ARG;
     if (T > 0 && (!positions || !slots)) return KDA_ERR_INVALID_ARG;
     if (num_free > 0 && !free_pages) return KDA_ERR_INVALID_ARG;
-    if (!all_aligned({static_cast<const void*>(cached_lens), static_cast<const void*>(cu_seqlens),
-                      static_cast<const void*>(block_table), static_cast<const void*>(free_pages),
-                      static_cast<const void*>(free_start), static_cast<const void*>(seq_lens),
-                      static_cast<const void*>(positions), static_cast<const void*>(slots),
-                      static_cast<const void*>(free_end), static_cast<const void*>(status_dev)}))
+    // single integers are read and written: their natural alignment is enough
+    for (const void* p : {static_cast<const void*>(cached_lens), static_cast<const void*>(cu_seqlens),
+                          static_cast<const void*>(block_table), static_cast<const void*>(free_pages),
+                          static_cast<const void*>(free_start), static_cast<const void*>(seq_lens),
+                          static_cast<const void*>(positions), static_cast<const void*>(free_end),
+                          static_cast<const void*>(status_dev)})
+        if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return KDA_ERR_ALIGNMENT;
+    if (reinterpret_cast<uintptr_t>(slots) % 8 != 0)
         return KDA_ERR_ALIGNMENT;
     // no output may be an input or another output (checked on the base pointers)
     const void* outs[] = {block_table, seq_lens, positions, slots, free_end};

@@ -102,6 +102,17 @@ def test_plan_reports_bad_page_ids():
     assert out[2].tolist() == [-1, -1] + [32 + i for i in range(8)] + [-1, -1]
 
 
+def test_plan_takes_slices():
+    """Every array a slice that starts four (slots: eight) bytes into its buffer."""
+    at = lambda x, dtype=torch.int32: ints([0, *x], dtype)[1:]
+    out = [at([0, 0]), at([0] * 3), at([0] * 3, torch.int64), at([0])]
+    table = at([4, -1, 6, -1]).view(2, 2)
+    kda.kda_page_plan(at([3, 4]), at([0, 2, 3]), table, at([7, 8]), 4, 3, free_start=at([0]),
+                      seq_lens=out[0], positions=out[1], slots=out[2], free_end=out[3])
+    assert [o.tolist() for o in out] == [[5, 5], [3, 4, 4], [19, 28, 32], [2]]
+    assert table.tolist() == [[4, 7], [6, 8]]
+
+
 def test_plan_without_requests():
     out = run_plan([], [], 16, 2, [1, 2, 3], cu=[0], table=np.zeros((0, 2), int))
     assert out[0].numel() == 0 and out[1].numel() == 0

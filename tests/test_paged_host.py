@@ -47,7 +47,8 @@ PLAN = dict(cached=P(0), cu=P(1), N=2, T=10, page=16, table=P(2), max_pages=4, f
     (dict(N=0), INVALID), (dict(cached=None), INVALID), (dict(cu=None), INVALID),
     (dict(table=None), INVALID), (dict(free=None), INVALID), (dict(seq_lens=None), INVALID),
     (dict(positions=None), INVALID), (dict(slots=None), INVALID), (dict(free_end=None), INVALID),
-    (dict(cached=MIS), ALIGNMENT), (dict(free_start=MIS), ALIGNMENT), (dict(status=MIS), ALIGNMENT),
+    (dict(cached=P(0) + 2), ALIGNMENT), (dict(free_start=P(0) + 1), ALIGNMENT),
+    (dict(status=P(0) + 2), ALIGNMENT), (dict(slots=MIS), ALIGNMENT),
     (dict(seq_lens=P(0)), INVALID), (dict(free_start=P(7)), INVALID), (dict(slots=P(5)), INVALID),
 ])
 def test_plan_refuses(lib, kw, expect):
