@@ -1,10 +1,11 @@
-// kda_paged_decode on CUDA cores (IEEE FP32 products), and the join of split rows.
+// kda_paged_decode for FP32 caches, on CUDA cores (IEEE FP32 products), and the join
+// of split rows for either type.
 //
 //     s_t = scale q . k_t,   out = sum e^(s_t) v_t / sum e^(s_t)
 //
 // HBM-bound: every k and v is read once, 2 D values a token and key-value head.
 // Each warp works alone on batches of eight consecutive tokens (which lie in one
-// page): a row takes D * sizeof / 16 lanes, 16 bytes each, straight from memory to
+// page): a row takes D / 4 lanes, 16 bytes each, straight from memory to
 // registers, keys and values of the batch together in flight; the products with
 // the unit's query rows (in registers, scaled by scale * log2 e) are summed over
 // the row's lanes by shuffles, and one pass keeps the running maximum m, sum l and
@@ -25,10 +26,11 @@ constexpr int NW = NT / 32;
 constexpr int kBatch = 8;              // tokens per warp step
 constexpr int kTileShift = 6;          // 64 tokens: one batch per warp
 
-template <typename T, int D, int GT>
+template <int D, int GT>
 __global__ void __launch_bounds__(NT) paged_decode_kernel(DecodeArgs a, DecodeShape sh, int chunks)
 {
-    constexpr int VEC = 16 / (int)sizeof(T);
+    using T = float;
+    constexpr int VEC = 4;
     constexpr int LPR = D / VEC, RPW = 32 / LPR;
     constexpr int TB = kBatch / RPW;               // tokens per row group and step
     __shared__ float s_m[NW][GT], s_l[NW][GT];
@@ -261,17 +263,11 @@ __global__ void __launch_bounds__(NT) decode_join_kernel(DecodeArgs a, DecodeSha
 
 // Query heads per warp: the smallest of 1, 2, 4, 8 that covers the group, or 8
 // with several chunks of warps.
-int chunk_heads(int G, bool bf16)
-{
-    const int most = bf16 ? 4 : 8;                 // registers: q and o, VEC values a head
-    int gt = 1;
-    while (gt < G && gt < most) gt *= 2;
-    return gt;
-}
+int chunk_heads(int G) { return G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : 8; }
 
 DecodeShape simple_shape(const DecodeArgs& a, int* chunks)
 {
-    const int G = a.Hq / a.Hk, gt = chunk_heads(G, a.bf16);
+    const int G = a.Hq / a.Hk, gt = chunk_heads(G);
     int c = 1;
     while (c * gt < G && c < NW) c *= 2;
     *chunks = c;
@@ -284,16 +280,14 @@ DecodeShape simple_shape(const DecodeArgs& a, int* chunks)
     return s;
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_simple(const DecodeArgs& a, const DecodeShape& s, int chunks, cudaStream_t st)
 {
-    switch (chunk_heads(a.Hq / a.Hk, a.bf16)) {
-        case 1: paged_decode_kernel<T, D, 1><<<s.ctas, NT, 0, st>>>(a, s, chunks); break;
-        case 2: paged_decode_kernel<T, D, 2><<<s.ctas, NT, 0, st>>>(a, s, chunks); break;
-        case 4: paged_decode_kernel<T, D, 4><<<s.ctas, NT, 0, st>>>(a, s, chunks); break;
-        default:
-            if constexpr (sizeof(T) == 4)
-                paged_decode_kernel<T, D, 8><<<s.ctas, NT, 0, st>>>(a, s, chunks);
+    switch (chunk_heads(a.Hq / a.Hk)) {
+        case 1: paged_decode_kernel<D, 1><<<s.ctas, NT, 0, st>>>(a, s, chunks); break;
+        case 2: paged_decode_kernel<D, 2><<<s.ctas, NT, 0, st>>>(a, s, chunks); break;
+        case 4: paged_decode_kernel<D, 4><<<s.ctas, NT, 0, st>>>(a, s, chunks); break;
+        default: paged_decode_kernel<D, 8><<<s.ctas, NT, 0, st>>>(a, s, chunks);
     }
     return cudaGetLastError();
 }
@@ -312,12 +306,11 @@ cudaError_t launch_decode_join(const DecodeArgs& a, const DecodeShape& s, cudaSt
 
 int64_t paged_decode_workspace_bytes(int32_t N, int32_t Hq, int32_t Hk, int32_t D)
 {
+    DecodeArgs a = {};
+    a.N = N; a.Hq = Hq; a.Hk = Hk; a.D = D;
+    int chunks;
     int64_t most = 0;
-    for (int bf16 = 0; bf16 < 2; ++bf16) {
-        DecodeArgs a = {};
-        a.N = N; a.Hq = Hq; a.Hk = Hk; a.D = D; a.bf16 = bf16;
-        int chunks;
-        const DecodeShape s = simple_shape(a, &chunks);
+    for (const DecodeShape& s : {simple_shape(a, &chunks), decode_tc_shape(a)}) {
         const int64_t b = decode_o_offset(N, s) + (int64_t)2 * s.ctas * s.heads * D * 4;
         if (b > most) most = b;
     }
@@ -326,15 +319,17 @@ int64_t paged_decode_workspace_bytes(int32_t N, int32_t Hq, int32_t Hk, int32_t 
 
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t stream)
 {
-    int chunks;
-    const DecodeShape s = simple_shape(a, &chunks);
     cudaError_t e;
-    if (a.bf16)
-        e = a.D == 64 ? launch_simple<__nv_bfloat16, 64>(a, s, chunks, stream)
-                      : launch_simple<__nv_bfloat16, 128>(a, s, chunks, stream);
-    else
-        e = a.D == 64 ? launch_simple<float, 64>(a, s, chunks, stream)
-                      : launch_simple<float, 128>(a, s, chunks, stream);
+    DecodeShape s;
+    if (a.bf16) {
+        s = decode_tc_shape(a);
+        e = launch_paged_decode_tc(a, s, stream);
+    } else {
+        int chunks;
+        s = simple_shape(a, &chunks);
+        e = a.D == 64 ? launch_simple<64>(a, s, chunks, stream)
+                      : launch_simple<128>(a, s, chunks, stream);
+    }
     return e == cudaSuccess ? launch_decode_join(a, s, stream) : e;
 }
 

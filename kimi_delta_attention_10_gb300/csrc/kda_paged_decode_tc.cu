@@ -1,0 +1,596 @@
+// kda_paged_decode for BF16 caches on the tensor cores (tcgen05).
+//
+// Per tile of 128 tokens, with the roles of the usual product turned round so that
+// the long axis is the MMA's M and the few query heads its N:
+//     S[128 tokens, heads]  = K[128, D] Q[heads, D]^T          (M = 128, N = heads)
+//     O^T[D, heads]        += V^T[D, 128] P^T[heads, 128]^T    (M = D,   N = 2 heads)
+// K and V tiles are read from shared memory exactly as their pages lie in memory
+// (K-major keys, MN-major values), so nothing is transposed and nothing padded but
+// N.  The weights p = e^(s - m) go back to shared memory as two BF16 rows, the
+// rounded value and the rounded rest: N is nearly free here (the MMA's time is the
+// 128-row operand's read), and the weights then carry 16 bits instead of 8.
+//
+// HBM-bound: 2 D values a token and key-value head, once.  Warp roles:
+//   producer  one TMA box per page and 64 channels into a ring of K and V slots
+//             (swizzled as the MMA reads them), the block table read by its lanes;
+//   MMA       one thread: S of tile i + 1 is issued before the product with V of
+//             tile i, so that it runs while the softmax of tile i does;
+//   softmax   four warps (eight for more than 32 heads): one token a lane.  The
+//             tile's maximum per head is a warp reduction and four values through
+//             shared memory; m is moved only when it would grow by more than 2^8
+//             (p stays within FP32 and BF16 range, the ratios are exact either way),
+//             so the running output is rarely rescaled.  The sum of O over tiles is
+//             kept in registers: thread d adds up the D-row d of each tile's product.
+// The CTA's tiles run through all its rows without draining the ring.
+//
+// Tokens past the request's end: their scores are replaced by -infinity, their
+// value rows by zeros in shared memory (0 * NaN would not be 0), and pages past the
+// end are not loaded.
+#include <cuda_runtime.h>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math_constants.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "kda_paged_sched.cuh"
+#include "kda_tc.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr int kTile = 128;             // tokens per tile
+constexpr int kTileShift = 7;
+constexpr float kGrowth = 8.f;         // log2 of the growth that moves the reference maximum
+
+template <int D_, int HP_> struct Cfg {
+    static constexpr int D = D_, HP = HP_;             // HP: query heads per unit, padded
+    static constexpr int NWG = HP > 32 ? 2 : 1;        // softmax warpgroups
+    static constexpr int HW = HP / NWG;                // heads of each
+    static constexpr int QR = HP < 16 ? 16 : HP;       // N of the first product
+    static constexpr int NPV = 2 * HP;                 // N of the second
+    static constexpr int NT = NWG * 128 + 64;
+    static constexpr int CTAS = D == 64 && HP <= 32 ? 2 : 1;   // per SM
+    static constexpr uint32_t SLOT = kTile * D * 2;
+    static constexpr uint32_t PBUF = NPV * 256, QBUF = QR * D * 2;
+    static constexpr int NQ = HP > 32 ? 1 : 2;         // query buffers
+    static constexpr uint32_t MISC = HP <= 8 ? 1024 : HP <= 32 ? 2048 : 4096;   // barriers, maxima, sums
+    // shared memory of an SM 228 KB, 1 KB of it kept per CTA; 1 KB for alignment
+    // and 1 KB for the static part
+    static constexpr uint32_t ROOM = (CTAS == 2 ? 113 * 1024 : 227 * 1024) - 2048;
+    static constexpr int NS_ = (ROOM - 2 * PBUF - NQ * QBUF - MISC) / SLOT;
+    static constexpr int NS = NS_ > 8 ? 8 : NS_;       // ring slots
+    static_assert(NS >= 4, "K and V of two tiles");
+    static constexpr uint32_t OFF_P = NS * SLOT, OFF_Q = OFF_P + 2 * PBUF,
+                              OFF_MISC = OFF_Q + NQ * QBUF, SMEM = OFF_MISC + MISC + 1024;
+    static constexpr uint32_t TM_O = 2 * QR;           // after two S buffers
+    static constexpr uint32_t TM_USED = TM_O + 2 * NPV;
+    static constexpr uint32_t TM_COLS = TM_USED <= 64 ? 64 : TM_USED <= 128 ? 128
+                                        : TM_USED <= 256 ? 256 : 512;
+    static_assert(TM_COLS * CTAS <= 512, "tensor memory of an SM");
+};
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+struct Bars {
+    uint64_t full[8], empty[8];        // ring slots
+    uint64_t sfull[2], sempty[2];      // S in tensor memory
+    uint64_t pfull[2];                 // P in shared memory (and the O buffer read)
+    uint64_t ofull[2];                 // O in tensor memory (and the P buffer read)
+    uint64_t qfull[2], qempty[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int32_t abort;
+};
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y,
+                                            uint64_t* m)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(m))
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8])
+{
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t a, float (&r)[8]) { tmem_ld8(a, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t a, float (&r)[16]) { tmem_ld16(a, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t a, float (&r)[32]) { tmem_ld32(a, r); }
+
+__device__ __forceinline__ float warp_max(float x)
+{
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The rows (request, head unit) of a CTA's tiles, in order; every role walks its own.
+struct Walk {
+    int64_t pos, end, at;
+    int32_t n, u, tile0, tile1, tiles, L;
+    __device__ __forceinline__ explicit Walk(const DecodeRange& r)
+        : pos(r.begin), end(r.end), at(r.at), n(r.n), tile0(0), tile1(0) {}
+    __device__ __forceinline__ bool next(const DecodeArgs& a, const DecodeShape& sh)
+    {
+        pos += tile1 - tile0;
+        if (pos >= end) return false;
+        for (;; ++n) {
+            L = decode_len(a, n);
+            tiles = tiles_of(L, kTileShift);
+            const int64_t all = (int64_t)tiles * sh.units;
+            if (pos < at + all) break;
+            at += all;
+        }
+        u = (int32_t)((pos - at) / tiles);
+        tile0 = (int32_t)(pos - at - (int64_t)u * tiles);
+        tile1 = (int32_t)min((int64_t)tiles, tile0 + (end - pos));
+        return true;
+    }
+};
+
+template <int D, int HP>
+__global__ void __launch_bounds__(Cfg<D, HP>::NT, Cfg<D, HP>::CTAS)
+paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps maps)
+{
+    using C = Cfg<D, HP>;
+    constexpr int HALVES = D / 64, HW = C::HW, NS = C::NS;
+    extern __shared__ unsigned char raw[];
+    unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    Bars& bar = *reinterpret_cast<Bars*>(sm + C::OFF_MISC);
+    float* s_max = reinterpret_cast<float*>(sm + C::OFF_MISC + 512);     // [2][NWG][4][HW]
+    float* s_sum = s_max + 2 * 4 * HP;                                   // [4][HP]
+    static_assert(sizeof(Bars) <= 512 && 512 + 12 * HP * 4 <= C::MISC, "misc region");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int G = a.Hq / a.Hk, groups = sh.units / a.Hk;
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.sfull[i], 1);
+            mbar_init(&bar.sempty[i], C::NWG * 4);
+            mbar_init(&bar.pfull[i], C::NWG * 4);
+            mbar_init(&bar.ofull[i], 1);
+            mbar_init(&bar.qfull[i], 1);
+            mbar_init(&bar.qempty[i], 1);
+        }
+        mbar_init(&bar.drain, 1);
+        bar.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::NWG * 4 + 1) {
+        tmem_alloc(&bar.tmem, C::TM_COLS);
+        tmem_relinquish();
+    }
+    char* ws = static_cast<char*>(a.workspace);
+    const DecodeRange rg = decode_range<C::NT>(a, sh, reinterpret_cast<int64_t*>(ws));
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = bar.tmem;
+
+    // A wait that gives up marks the CTA: the producer stops, the others run their
+    // loops to the end without waiting or multiplying, so that all barriers meet.
+    volatile int32_t* abort_flag = &bar.abort;
+    bool dead = false;
+    auto wait = [&](uint64_t* m, uint32_t parity) {
+        if (dead) return;
+        for (uint32_t j = 0; j < kPollsPerCheck; ++j)
+            if (mbar_try_wait(m, parity)) return;
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t i = 0; i < kMaxTimerChecks; ++i) {
+            for (uint32_t j = 0; j < kPollsPerCheck; ++j)
+                if (mbar_try_wait(m, parity)) return;
+            if (*abort_flag) break;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+        }
+        dead = true;
+        *abort_flag = 1;
+        report_status(a.status, KDA_ERR_TIMEOUT);
+    };
+
+    Walk w(rg);
+    if (warp == C::NWG * 4) {
+        // ------------------------------------------------------------ producer
+        const int rows = min(1 << a.page_shift, kTile);           // tokens per box
+        const int row_shift = a.page_shift < kTileShift ? a.page_shift : kTileShift;
+        uint32_t c = 0;                                            // copies into the ring
+        uint32_t item = 0;
+        const int j = lane / HALVES, half = lane % HALVES;
+        while (!dead && w.next(a, sh)) {
+            const int hk = w.u / groups, g0 = (w.u - hk * groups) * HP;
+            {
+                const uint32_t qb = item % C::NQ;
+                wait(&bar.qempty[qb], ((item / C::NQ) & 1) ^ 1);
+                dead = __any_sync(0xffffffffu, dead);
+                if (dead) break;
+                if (lane == 0) mbar_arrive_expect_tx(&bar.qfull[qb], C::QBUF);
+                __syncwarp();
+                if (lane < HALVES)
+                    tma_load_2d(smem_u32(sm + C::OFF_Q + qb * C::QBUF + lane * C::QR * 128),
+                                &maps.q, 64 * lane, w.n * a.Hq + hk * G + g0, &bar.qfull[qb]);
+                ++item;
+            }
+            const int32_t* table = a.table + (int64_t)w.n * a.max_pages;
+            for (int t = w.tile0; t < w.tile1 && !dead; ++t) {
+                const int tok = t << kTileShift, valid = min(kTile, w.L - tok);
+                const int boxes = ((valid + rows - 1) >> row_shift) * HALVES;
+                int y = 0;
+                if (lane < boxes) {
+                    const int at = tok + (j << row_shift);
+                    int32_t page = table[at >> a.page_shift];
+                    if ((uint32_t)page >= (uint32_t)a.num_pages) {
+                        report_status(a.status, KDA_ERR_DEVICE_ARG);
+                        page = 0;
+                    }
+                    y = ((page * a.Hk + hk) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
+                }
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t slot = c % NS;
+                    wait(&bar.empty[slot], ((c / NS) & 1) ^ 1);
+                    dead = __any_sync(0xffffffffu, dead);
+                    if (dead) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], boxes * rows * 128);
+                    __syncwarp();
+                    if (lane < boxes)
+                        tma_load_2d(smem_u32(sm + slot * C::SLOT + half * (kTile * 128) +
+                                             ((j << row_shift) * 128)),
+                                    kv ? &maps.v : &maps.k, 64 * half, y, &bar.full[slot]);
+                    ++c;
+                }
+            }
+        }
+        // every copy has landed before the CTA ends (all were waited for, unless a wait gave up)
+        if (lane == 0) {
+            for (uint32_t i = c > (uint32_t)NS ? c - NS : 0; i < c; ++i)
+                mbar_wait(&bar.full[i % NS], (i / NS) & 1);
+            for (uint32_t i = item > (uint32_t)C::NQ ? item - C::NQ : 0; i < item; ++i)
+                mbar_wait(&bar.qfull[i % C::NQ], (i / C::NQ) & 1);
+        }
+    } else if (warp == C::NWG * 4 + 1) {
+        // ------------------------------------------------------------ MMA
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc(kFmtBF16, kTile, C::QR);
+            constexpr uint32_t id_o = idesc(kFmtBF16, D, C::NPV, true, false);
+            const uint64_t dK = desc_kmajor(smem_u32(sm), kTile, 0);
+            const uint64_t dV = D == 128 ? desc_mnmajor128(smem_u32(sm), kTile * 128, 0)
+                                         : desc_mnmajor64(smem_u32(sm), 0);
+            const uint64_t dQ = desc_kmajor(smem_u32(sm + C::OFF_Q), C::QR, 0);
+            const uint64_t dP = desc_kmajor(smem_u32(sm + C::OFF_P), C::NPV, 0);
+            uint32_t i = 0, item = 0;
+            auto product_with_v = [&](uint32_t t) {
+                const uint32_t slot = (2 * t + 1) % NS, b = t & 1;
+                wait(&bar.full[slot], ((2 * t + 1) / NS) & 1);
+                wait(&bar.pfull[b], (t >> 1) & 1);
+                if (dead) return;
+                fence_after_sync();
+#pragma unroll
+                for (int s = 0; s < kTile / 16; ++s)
+                    mma_bf16(tmem + C::TM_O + b * C::NPV,
+                             desc_advance(dV, slot * C::SLOT + mnmajor_off(s)),
+                             desc_advance(dP, b * C::PBUF + kmajor_off(C::NPV, s)), id_o, s > 0);
+                commit(&bar.empty[slot]);
+                commit(&bar.ofull[b]);
+            };
+            while (w.next(a, sh)) {
+                const uint32_t qb = item % C::NQ;
+                wait(&bar.qfull[qb], (item / C::NQ) & 1);
+                for (int t = w.tile0; t < w.tile1; ++t, ++i) {
+                    const uint32_t slot = (2 * i) % NS, b = i & 1;
+                    wait(&bar.full[slot], ((2 * i) / NS) & 1);
+                    wait(&bar.sempty[b], ((i >> 1) & 1) ^ 1);
+                    if (!dead) {
+                        fence_after_sync();
+#pragma unroll
+                        for (int s = 0; s < D / 16; ++s)
+                            mma_bf16(tmem + b * C::QR,
+                                     desc_advance(dK, slot * C::SLOT + kmajor_off(kTile, s)),
+                                     desc_advance(dQ, qb * C::QBUF + kmajor_off(C::QR, s)), id_s,
+                                     s > 0);
+                        commit(&bar.empty[slot]);
+                        if (t + 1 == w.tile1) commit(&bar.qempty[qb]);
+                        commit(&bar.sfull[b]);
+                    }
+                    if (i > 0) product_with_v(i - 1);
+                }
+                ++item;
+            }
+            if (i > 0) product_with_v(i - 1);
+            commit(&bar.drain);                            // no MMA outlives the loop
+            mbar_wait(&bar.drain, 0);
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int wg = warp >> 2, quad = warp & 3, row = tid & 127;     // row: token, then channel
+        const uint32_t tlane = tmem_addr(tmem, 32 * quad, 0);
+        const float c = a.scale * kLog2e;
+        const int bar_id = 1 + wg;
+        // the row's place in a P row: 128-byte rows of 64 tokens
+        const uint32_t p_base = smem_u32(sm + C::OFF_P) + (row >> 6) * (C::NPV * 128) +
+                                (row & 7) * 2 + wg * HW * 128;
+        const uint32_t p_chunk = (row >> 3) & 7;
+        float2* ws_ml = reinterpret_cast<float2*>(ws + decode_ml_offset(a.N));
+        float* ws_o = reinterpret_cast<float*>(ws + decode_o_offset(a.N, sh));
+        uint32_t i = 0;
+        while (w.next(a, sh)) {
+            float ref[HW], l[HW], acc[HW];
+#pragma unroll
+            for (int g = 0; g < HW; ++g) {
+                ref[g] = -CUDART_INF_F;
+                l[g] = acc[g] = 0.f;
+            }
+            bool pending = false;
+            auto add_o = [&](uint32_t t) {
+                wait(&bar.ofull[t & 1], (t >> 1) & 1);
+                __syncwarp();
+                fence_after_sync();
+                const uint32_t o = tlane + C::TM_O + (t & 1) * C::NPV + wg * HW;
+                float x[HW];
+                tmem_ld(o, x);
+#pragma unroll
+                for (int g = 0; g < HW; ++g) acc[g] += x[g];
+                tmem_ld(o + HP, x);
+#pragma unroll
+                for (int g = 0; g < HW; ++g) acc[g] += x[g];
+            };
+            for (int t = w.tile0; t < w.tile1; ++t, ++i) {
+                const uint32_t b = i & 1;
+                const int valid = w.L - (t << kTileShift);
+                float s[HW];
+                wait(&bar.sfull[b], (i >> 1) & 1);
+                __syncwarp();
+                fence_after_sync();
+                tmem_ld(tlane + b * C::QR + wg * HW, s);
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.sempty[b]);
+                float* maxima = s_max + (b * C::NWG + wg) * 4 * HW;
+                float mine = 0.f;
+#pragma unroll
+                for (int g = 0; g < HW; ++g) {
+                    s[g] = row < valid ? s[g] * c : -CUDART_INF_F;
+                    const float m = warp_max(s[g]);
+                    if (lane == g) mine = m;
+                }
+                if (lane < HW) maxima[quad * HW + lane] = mine;
+                named_sync(bar_id, 128);
+                bool grown = false;
+                float top[HW];
+#pragma unroll
+                for (int g = 0; g < HW; g += 4) {
+                    float4 m = *reinterpret_cast<const float4*>(maxima + g);
+#pragma unroll
+                    for (int k = 1; k < 4; ++k) {
+                        const float4 x = *reinterpret_cast<const float4*>(maxima + k * HW + g);
+                        m.x = fmaxf(m.x, x.x);
+                        m.y = fmaxf(m.y, x.y);
+                        m.z = fmaxf(m.z, x.z);
+                        m.w = fmaxf(m.w, x.w);
+                    }
+                    top[g] = m.x;
+                    top[g + 1] = m.y;
+                    top[g + 2] = m.z;
+                    top[g + 3] = m.w;
+                }
+#pragma unroll
+                for (int g = 0; g < HW; ++g) grown |= top[g] > ref[g] + kGrowth;
+                if (grown) {                               // uniform over the warpgroup
+                    if (pending) add_o(i - 1);
+                    pending = false;
+#pragma unroll
+                    for (int g = 0; g < HW; ++g) {
+                        if (top[g] > ref[g] + kGrowth) {
+                            // ref -infinity: sums and output are zero
+                            const float keep = exp2f(ref[g] - top[g]);
+                            l[g] *= keep;
+                            acc[g] *= keep;
+                            ref[g] = top[g];
+                        }
+                    }
+                }
+                const uint32_t p = p_base + b * C::PBUF;
+#pragma unroll
+                for (int g = 0; g < HW; g += 2) {
+                    float e[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        // all scores so far -infinity: nothing to subtract
+                        const float m = ref[g + k] == -CUDART_INF_F ? 0.f : ref[g + k];
+                        e[k] = ex2_approx(s[g + k] - m);
+                        l[g + k] += e[k];
+                    }
+                    const uint32_t hi = pack_bf16(e[0], e[1]);
+                    const uint32_t lo = pack_bf16(e[0] - __uint_as_float(hi << 16),
+                                                  e[1] - __uint_as_float(hi & 0xffff0000u));
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        // row g + k of the warpgroup's (HW and HP are multiples of 8)
+                        const uint32_t at = p + ((g + k) >> 3) * 1024 + ((g + k) & 7) * 128 +
+                                            ((p_chunk ^ ((g + k) & 7)) << 4);
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at),
+                                     "h"((uint16_t)(k ? hi >> 16 : hi & 0xffffu)) : "memory");
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + HP * 128),
+                                     "h"((uint16_t)(k ? lo >> 16 : lo & 0xffffu)) : "memory");
+                    }
+                }
+                if (valid < kTile && wg == 0) {
+                    // value rows past the end, once they have landed
+                    const uint32_t slot = (2 * i + 1) % NS;
+                    wait(&bar.full[slot], ((2 * i + 1) / NS) & 1);
+                    if (row >= valid) {
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                *reinterpret_cast<uint4*>(sm + slot * C::SLOT +
+                                                          h * (kTile * 128) + row * 128 + k * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_async_smem();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.pfull[b]);
+                if (pending) add_o(i - 1);
+                pending = true;
+            }
+            add_o(i - 1);
+            // the sums of all tokens' weights
+#pragma unroll
+            for (int g = 0; g < HW; ++g) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], o);
+                if (lane == 0) s_sum[quad * HP + wg * HW + g] = l[g];
+            }
+            named_sync(bar_id, 128);
+            const int hk = w.u / groups, g0 = (w.u - hk * groups) * HP + wg * HW;
+            const bool whole = w.tile0 == 0 && w.tile1 == w.tiles;
+            const int64_t r0 = whole ? (int64_t)w.n * a.Hq + hk * G + g0
+                                     : (2 * (int64_t)blockIdx.x + (w.tile0 == 0)) * HP + wg * HW;
+            // D = 64: a warp's tensor-memory lanes 0 .. 15 hold channels 16 quad ..
+            const int ch = D == 128 ? row : 16 * quad + lane;
+            const bool mine = D == 128 || lane < 16;
+#pragma unroll
+            for (int g = 0; g < HW; ++g) {
+                if (g0 + g >= G) break;
+                const float* sp = s_sum + wg * HW + g;
+                const float sum = sp[0] + sp[HP] + sp[2 * HP] + sp[3 * HP];
+                const int64_t r = r0 + g;
+                if (whole) {
+                    if (mine) {
+                        const float y = acc[g] / sum;
+                        if (a.out_bf16)
+                            store_one(static_cast<__nv_bfloat16*>(a.out) + r * D + ch, y);
+                        else
+                            store_one(static_cast<float*>(a.out) + r * D + ch, y);
+                    }
+                    if (row == 0 && a.lse != nullptr) a.lse[r] = ref[g] * kLn2 + logf(sum);
+                } else {
+                    if (mine) ws_o[r * D + ch] = acc[g];
+                    if (row == 0) ws_ml[r] = make_float2(ref[g], sum);
+                }
+            }
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == C::NWG * 4 + 1) {
+        fence_after_sync();
+        tmem_dealloc(tmem, C::TM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------- launch
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled()
+{
+    static const EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return static_cast<EncodeTiledFn>(nullptr);
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+// rows x D BF16 values, read as boxes of box_rows x 64, 128-byte swizzled; rows
+// past the end read as zeros.
+cudaError_t encode_rows(CUtensorMap* m, const void* base, int64_t rows, int D, int box_rows)
+{
+    const EncodeTiledFn fn = encode_tiled();
+    if (fn == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+int padded_heads(int G)
+{
+    return G <= 8 ? 8 : G <= 16 ? 16 : G <= 32 ? 32 : 64;
+}
+
+template <int D, int HP>
+cudaError_t launch_typed(const DecodeArgs& a, const DecodeShape& s, cudaStream_t stream)
+{
+    using C = Cfg<D, HP>;
+    Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    const int page = 1 << a.page_shift;
+    const int64_t rows = (int64_t)a.num_pages * a.Hk * page;
+    const int64_t qrows = (int64_t)a.N * a.Hq;
+    const int box = page < kTile ? page : kTile;
+    cudaError_t e = encode_rows(&maps.q, a.q, qrows, D, C::QR);
+    // an empty cache has no page to read: the maps only have to be valid
+    if (e == cudaSuccess) e = encode_rows(&maps.k, rows ? a.k : a.q, rows ? rows : qrows, D, box);
+    if (e == cudaSuccess) e = encode_rows(&maps.v, rows ? a.v : a.q, rows ? rows : qrows, D, box);
+    if (e != cudaSuccess) return e;
+    auto kern = paged_decode_tc_kernel<D, HP>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    kern<<<s.ctas, C::NT, C::SMEM, stream>>>(a, s, maps);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+DecodeShape decode_tc_shape(const DecodeArgs& a)
+{
+    const int G = a.Hq / a.Hk, hp = padded_heads(G);
+    const int sms = device_sm_count();
+    DecodeShape s;
+    s.heads = hp;
+    s.units = a.Hk * ((G + hp - 1) / hp);
+    s.ctas = (sms > 0 ? sms : 152) * (a.D == 64 && hp <= 32 ? 2 : 1);
+    s.tile_shift = kTileShift;
+    return s;
+}
+
+cudaError_t launch_paged_decode_tc(const DecodeArgs& a, const DecodeShape& s, cudaStream_t stream)
+{
+    if (a.D == 64) {
+        switch (s.heads) {
+            case 8: return launch_typed<64, 8>(a, s, stream);
+            case 16: return launch_typed<64, 16>(a, s, stream);
+            case 32: return launch_typed<64, 32>(a, s, stream);
+            default: return launch_typed<64, 64>(a, s, stream);
+        }
+    }
+    switch (s.heads) {
+        case 8: return launch_typed<128, 8>(a, s, stream);
+        case 16: return launch_typed<128, 16>(a, s, stream);
+        case 32: return launch_typed<128, 32>(a, s, stream);
+        default: return launch_typed<128, 64>(a, s, stream);
+    }
+}
+
+}  // namespace kda
