@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from functools import lru_cache
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -173,9 +174,16 @@ def _dev_ptr(t: Optional[torch.Tensor], name: str) -> Optional[int]:
     return t.data_ptr()
 
 
+# The current stream's handle without building a Stream object (2 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream: Optional[torch.cuda.Stream], device) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def kda_gate(f: torch.Tensor, A_log: torch.Tensor, dt_bias: torch.Tensor, b: torch.Tensor,
@@ -471,32 +479,43 @@ def kda_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
 
 
 # ---------------------------------------------------------------- paged attention
+# These calls are short on the GPU, so their marshalling is kept to one look at each
+# tensor: a launch every few microseconds is bound by this file, not by the kernels.
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+_CODE = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
+_I32, _I64, _FP32 = torch.int32, torch.int64, torch.float32
 
 
-def _int_ptr(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, n: int = -1) -> Optional[int]:
-    """Device pointer of a contiguous integer tensor of `n` elements (any if negative)."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
+def _refuse(t, name: str, dtype: torch.dtype, n: int = -1):
+    """Raises for the first thing that is wrong with `t`."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if n >= 0 and t.numel() != n:
         raise ValueError(f"{name} must have {n} elements, not {t.numel()}")
-    return _dev_ptr(t, name)
+    _dev_ptr(t, name)
+    raise ValueError(f"{name}: unsupported tensor")
 
 
-def _f32_ptr(t: Optional[torch.Tensor], name: str, n: int) -> Optional[int]:
+def _ptr(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
+    """Device pointer of a contiguous tensor of `dtype`."""
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _refuse(t, name, dtype)
+    return t.data_ptr()
+
+
+def _ptr_n(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, n: int) -> Optional[int]:
+    """_ptr of `n` elements; None passes."""
     if t is None:
         return None
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} must be torch.float32, not {t.dtype}")
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements, not {t.numel()}")
-    return _dev_ptr(t, name)
+    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+        _refuse(t, name, dtype, n)
+    return t.data_ptr()
 
 
-def _rows_ptr(t: torch.Tensor, name: str, T: int, H: int, D: int):
+def _rows_ptr(t: torch.Tensor, name: str, dtype: torch.dtype, T: int, H: int, D: int):
     """(pointer, token stride) of [T, H, D] whose heads are dense within a token."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != (T, H, D):
         raise ValueError(f"{name} must have shape {(T, H, D)}, not {tuple(t.shape)}")
     if not t.is_cuda:
@@ -510,9 +529,28 @@ def _rows_ptr(t: torch.Tensor, name: str, T: int, H: int, D: int):
 def _dense_ptr(t: torch.Tensor, name: str, shape, dtype: torch.dtype) -> int:
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    return _dev_ptr(t, name)
+    return _ptr(t, name, dtype)
+
+
+_scratch = {}
+
+
+def _own_scratch(nbytes: int, dev, stream: Optional[torch.cuda.Stream], handle: int) -> int:
+    """Pointer to the workspace of a call that was given none: one buffer per stream, kept
+    and grown, since calls on one stream are ordered.  (An allocation between two launches
+    costs as much host time as a launch.)  A captured call gets a buffer of its graph's own."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev).data_ptr()
+    key = (dev.index, handle)
+    buf = _scratch.get(key)
+    if buf is None or buf.nbytes < nbytes:
+        if stream is None:
+            buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        else:
+            with torch.cuda.stream(stream):
+                buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _scratch[key] = buf
+    return buf.data_ptr()
 
 
 def kda_page_plan(cached_lens: torch.Tensor, cu_seqlens: torch.Tensor, block_table: torch.Tensor,
@@ -527,26 +565,26 @@ def kda_page_plan(cached_lens: torch.Tensor, cu_seqlens: torch.Tensor, block_tab
     device: cached_lens [N], cu_seqlens [N+1] packing num_tokens new tokens, block_table
     [N, max_pages] (new entries written in place), free_pages (taken in order from
     free_start).  Returns (seq_lens [N], positions [T], slots [T] int64, free_end [1])."""
-    lib = load_library()
+    lib = _lib or load_library()
     N, T = cached_lens.numel(), int(num_tokens)
     if block_table.dim() != 2 or block_table.shape[0] != N:
         raise ValueError(f"block_table must have shape [{N}, max_pages]")
-    dev, i32 = cached_lens.device, torch.int32
+    dev = cached_lens.device
     if seq_lens is None:
-        seq_lens = torch.empty(N, dtype=i32, device=dev)
+        seq_lens = torch.empty(N, dtype=_I32, device=dev)
     if positions is None:
-        positions = torch.empty(T, dtype=i32, device=dev)
+        positions = torch.empty(T, dtype=_I32, device=dev)
     if slots is None:
-        slots = torch.empty(T, dtype=torch.int64, device=dev)
+        slots = torch.empty(T, dtype=_I64, device=dev)
     if free_end is None:
-        free_end = torch.empty(1, dtype=i32, device=dev)
+        free_end = torch.empty(1, dtype=_I32, device=dev)
     st = lib.kda_page_plan(
-        _int_ptr(cached_lens, "cached_lens", i32), _int_ptr(cu_seqlens, "cu_seqlens", i32, N + 1),
-        N, T, int(page_size), _int_ptr(block_table, "block_table", i32), block_table.shape[1],
-        _int_ptr(free_pages, "free_pages", i32), free_pages.numel(),
-        _int_ptr(free_start, "free_start", i32, 1), _int_ptr(seq_lens, "seq_lens", i32, N),
-        _int_ptr(positions, "positions", i32, T), _int_ptr(slots, "slots", torch.int64, T),
-        _int_ptr(free_end, "free_end", i32, 1), _dev_ptr(status, "status"),
+        _ptr(cached_lens, "cached_lens", _I32), _ptr_n(cu_seqlens, "cu_seqlens", _I32, N + 1), N, T,
+        int(page_size), _ptr(block_table, "block_table", _I32), block_table.shape[1],
+        _ptr(free_pages, "free_pages", _I32), free_pages.numel(),
+        _ptr_n(free_start, "free_start", _I32, 1), _ptr_n(seq_lens, "seq_lens", _I32, N),
+        _ptr_n(positions, "positions", _I32, T), _ptr_n(slots, "slots", _I64, T),
+        _ptr_n(free_end, "free_end", _I32, 1), _dev_ptr(status, "status"),
         _stream_handle(stream, dev))
     if st != KDA_OK:
         raise KDAError(st, "kda_page_plan")
@@ -568,13 +606,11 @@ def rope_inv_freq(rot_dim: int, theta: float = 10000.0, scaling: str = "plain",
     return f.to(device) if device is not None else f, m.value
 
 
-def _rope_args(positions, inv_freq, T, Hq, Hk, D, q_weight, k_weight, eps, qk_norm, interleaved,
-               rope_scale):
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    return (_int_ptr(positions, "positions", torch.int32, T),
-            _f32_ptr(inv_freq, "inv_freq", rot // 2) if rot else None, rot,
-            1 if interleaved else 0, float(rope_scale), _f32_ptr(q_weight, "q_weight", D),
-            _f32_ptr(k_weight, "k_weight", D), float(eps), 1 if qk_norm else 0, T, Hq, Hk, D)
+def _code(dtype: torch.dtype) -> int:
+    code = _CODE.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
 
 
 def kda_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
@@ -587,33 +623,38 @@ def kda_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
     """Per-head RMS norm of q [T,Hq,D] and k [T,Hk,D] (weights [D] or None) and rotation of
     the first 2 * len(inv_freq) channels by position, in one pass (None: no rotation).  q and
     k may be slices of one projection.  Returns (q_out, k_out)."""
-    lib = load_library()
+    lib = _lib or load_library()
     T, Hq, D = q.shape
-    Hk = k.shape[1]
-    if k.dtype != q.dtype:
-        raise TypeError(f"k must be {q.dtype}, not {k.dtype}")
+    Hk, dev, dt = k.shape[1], q.device, q.dtype
+    if k.dtype is not dt:
+        raise TypeError(f"k must be {dt}, not {k.dtype}")
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=out_dtype or q.dtype, device=q.device)
+        q_out = torch.empty((T, Hq, D), dtype=out_dtype or dt, device=dev)
+    odt = q_out.dtype
     if k_out is None:
-        k_out = torch.empty((T, Hk, D), dtype=q_out.dtype, device=q.device)
+        k_out = torch.empty((T, Hk, D), dtype=odt, device=dev)
+    pairs = 0 if inv_freq is None else inv_freq.numel()
+    qp, qs = _rows_ptr(q, "q", dt, T, Hq, D)
+    kp, ks = _rows_ptr(k, "k", dt, T, Hk, D)
     st = lib.kda_qk_norm_rope(
-        *_rows_ptr(q, "q", T, Hq, D), *_rows_ptr(k, "k", T, Hk, D), _dtype_code(q),
-        *_rope_args(positions, inv_freq, T, Hq, Hk, D, q_weight, k_weight, eps, qk_norm,
-                    interleaved, rope_scale),
-        _dense_ptr(q_out, "q_out", (T, Hq, D), q_out.dtype),
-        _dense_ptr(k_out, "k_out", (T, Hk, D), q_out.dtype), _dtype_code(q_out),
-        _stream_handle(stream, q.device))
+        qp, qs, kp, ks, _code(dt), _ptr_n(positions, "positions", _I32, T),
+        _ptr_n(inv_freq, "inv_freq", _FP32, pairs), 2 * pairs, 1 if interleaved else 0, rope_scale,
+        _ptr_n(q_weight, "q_weight", _FP32, D), _ptr_n(k_weight, "k_weight", _FP32, D), eps,
+        1 if qk_norm else 0, T, Hq, Hk, D, _dense_ptr(q_out, "q_out", (T, Hq, D), odt),
+        _dense_ptr(k_out, "k_out", (T, Hk, D), odt), _code(odt), _stream_handle(stream, dev))
     if st != KDA_OK:
         raise KDAError(st, "kda_qk_norm_rope")
     return q_out, k_out
 
 
 def _cache_shape(k_cache, v_cache, Hk, D):
-    if k_cache.dim() != 4 or k_cache.shape[1] != Hk or k_cache.shape[3] != D:
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[1] != Hk or shape[3] != D:
         raise ValueError(f"k_cache must have shape [num_pages, {Hk}, page_size, {D}], not "
-                         f"{tuple(k_cache.shape)}")
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+                         f"{tuple(shape)}")
+    if v_cache.shape != shape or v_cache.dtype is not k_cache.dtype:
         raise ValueError("v_cache must have the shape and dtype of k_cache")
+    return shape
 
 
 def kda_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -628,32 +669,32 @@ def kda_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """kda_qk_norm_rope with the keys, and the values v [T,Hk,D], written to the slots
     (int64 [T], negative: skipped) of k_cache and v_cache [num_pages,Hk,page_size,D] in
     place.  Returns q_out in the cache's dtype."""
-    lib = load_library()
+    lib = _lib or load_library()
     T, Hq, D = q.shape
-    Hk = k.shape[1]
-    if k.dtype != q.dtype or v.dtype != q.dtype:
-        raise TypeError(f"k and v must be {q.dtype}, not {k.dtype} and {v.dtype}")
-    _cache_shape(k_cache, v_cache, Hk, D)
+    Hk, dev, dt, cdt = k.shape[1], q.device, q.dtype, k_cache.dtype
+    if k.dtype is not dt or v.dtype is not dt:
+        raise TypeError(f"k must be {dt} and v as well, not {k.dtype} and {v.dtype}")
+    num_pages, _, page_size, _ = _cache_shape(k_cache, v_cache, Hk, D)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=k_cache.dtype, device=q.device)
+        q_out = torch.empty((T, Hq, D), dtype=cdt, device=dev)
+    pairs = 0 if inv_freq is None else inv_freq.numel()
+    qp, qs = _rows_ptr(q, "q", dt, T, Hq, D)
+    kp, ks = _rows_ptr(k, "k", dt, T, Hk, D)
+    vp, vs = _rows_ptr(v, "v", dt, T, Hk, D)
     st = lib.kda_qk_norm_rope_append(
-        *_rows_ptr(q, "q", T, Hq, D), *_rows_ptr(k, "k", T, Hk, D), *_rows_ptr(v, "v", T, Hk, D),
-        _dtype_code(q), *_append_args(slots, positions, inv_freq, T, Hq, Hk, D, q_weight, k_weight,
-                                      eps, qk_norm, interleaved, rope_scale),
-        _dense_ptr(q_out, "q_out", (T, Hq, D), k_cache.dtype), _dev_ptr(k_cache, "k_cache"),
-        _dev_ptr(v_cache, "v_cache"), _dtype_code(k_cache), k_cache.shape[0], k_cache.shape[2],
-        _dev_ptr(status, "status"), _stream_handle(stream, q.device))
+        qp, qs, kp, ks, vp, vs, _code(dt), _ptr_n(positions, "positions", _I32, T),
+        _ptr_n(slots, "slots", _I64, T), _ptr_n(inv_freq, "inv_freq", _FP32, pairs), 2 * pairs,
+        1 if interleaved else 0, rope_scale, _ptr_n(q_weight, "q_weight", _FP32, D),
+        _ptr_n(k_weight, "k_weight", _FP32, D), eps, 1 if qk_norm else 0, T, Hq, Hk, D,
+        _dense_ptr(q_out, "q_out", (T, Hq, D), cdt), _ptr(k_cache, "k_cache", cdt),
+        _ptr(v_cache, "v_cache", cdt), _code(cdt), num_pages, page_size,
+        _dev_ptr(status, "status"), _stream_handle(stream, dev))
     if st != KDA_OK:
         raise KDAError(st, "kda_qk_norm_rope_append")
     return q_out
 
 
-def _append_args(slots, positions, inv_freq, T, *rest):
-    """_rope_args with the slots after the positions."""
-    pos, *more = _rope_args(positions, inv_freq, T, *rest)
-    return (pos, _int_ptr(slots, "slots", torch.int64, T), *more)
-
-
+@lru_cache(maxsize=256)
 def qk_norm_rope_bwd_workspace_size(T: int, Hq: int, Hk: int, D: int = 128) -> int:
     """Bytes of workspace kda_qk_norm_rope_bwd needs."""
     out = ctypes.c_int64(0)
@@ -674,40 +715,48 @@ def kda_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor,
                          stream: Optional[torch.cuda.Stream] = None, workspace=None):
     """Backward of kda_qk_norm_rope.  Returns (q_grad, k_grad, q_weight_grad, k_weight_grad):
     the first two FP32 unless grad_dtype or given tensors say otherwise, the weights' FP32
-    (None where the weight is None or qk_norm is off).  workspace: None (a fresh buffer) or a
-    CUDA tensor of at least qk_norm_rope_bwd_workspace_size(...) bytes."""
-    lib = load_library()
+    (None where the weight is None or qk_norm is off).  workspace: None (one kept per
+    stream) or a CUDA tensor of at least qk_norm_rope_bwd_workspace_size(...) bytes."""
+    lib = _lib or load_library()
     T, Hq, D = q.shape
-    Hk = k.shape[1]
-    dev = q.device
-    if k.dtype != q.dtype:
-        raise TypeError(f"k must be {q.dtype}, not {k.dtype}")
+    Hk, dev, dt, ydt = k.shape[1], q.device, q.dtype, dq_out.dtype
+    if k.dtype is not dt:
+        raise TypeError(f"k must be {dt}, not {k.dtype}")
     if q_grad is None:
-        q_grad = torch.empty((T, Hq, D), dtype=grad_dtype or torch.float32, device=dev)
+        q_grad = torch.empty((T, Hq, D), dtype=grad_dtype or _FP32, device=dev)
+    gdt = q_grad.dtype
     if k_grad is None:
-        k_grad = torch.empty((T, Hk, D), dtype=q_grad.dtype, device=dev)
-    wgrad = [torch.empty(D, dtype=torch.float32, device=dev) if w is not None and qk_norm else None
-             for w in (q_weight, k_weight)]
-    if workspace is None and (wgrad[0] is not None or wgrad[1] is not None):
-        workspace = torch.empty(qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D), dtype=torch.uint8,
-                                device=dev)
+        k_grad = torch.empty((T, Hk, D), dtype=gdt, device=dev)
+    qp, qs = _rows_ptr(q, "q", dt, T, Hq, D)
+    kp, ks = _rows_ptr(k, "k", dt, T, Hk, D)
+    wq = wk = None
+    handle = _stream_handle(stream, dev)
+    ws, ws_bytes = None, 0
+    if qk_norm and (q_weight is not None or k_weight is not None):
+        wq, wk = torch.empty((2, D), dtype=_FP32, device=dev).unbind(0)
+        wq, wk = wq if q_weight is not None else None, wk if k_weight is not None else None
+        if workspace is None:
+            ws_bytes = qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D)
+            ws = _own_scratch(ws_bytes, dev, stream, handle)
+    if workspace is not None:
+        ws, ws_bytes = _dev_ptr(workspace, "workspace"), workspace.nbytes
+    pairs = 0 if inv_freq is None else inv_freq.numel()
     st = lib.kda_qk_norm_rope_bwd(
-        *_rows_ptr(q, "q", T, Hq, D), *_rows_ptr(k, "k", T, Hk, D), _dtype_code(q),
-        _dense_ptr(dq_out, "dq_out", (T, Hq, D), dq_out.dtype),
-        _dense_ptr(dk_out, "dk_out", (T, Hk, D), dq_out.dtype), _dtype_code(dq_out),
-        *_rope_args(positions, inv_freq, T, Hq, Hk, D, q_weight, k_weight, eps, qk_norm,
-                    interleaved, rope_scale),
-        _dense_ptr(q_grad, "q_grad", (T, Hq, D), q_grad.dtype),
-        _dense_ptr(k_grad, "k_grad", (T, Hk, D), q_grad.dtype), _dtype_code(q_grad),
-        _dev_ptr(wgrad[0], "q_weight_grad"), _dev_ptr(wgrad[1], "k_weight_grad"),
-        _dev_ptr(workspace, "workspace"),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _stream_handle(stream, dev))
+        qp, qs, kp, ks, _code(dt), _dense_ptr(dq_out, "dq_out", (T, Hq, D), ydt),
+        _dense_ptr(dk_out, "dk_out", (T, Hk, D), ydt), _code(ydt),
+        _ptr_n(positions, "positions", _I32, T), _ptr_n(inv_freq, "inv_freq", _FP32, pairs),
+        2 * pairs, 1 if interleaved else 0, rope_scale, _ptr_n(q_weight, "q_weight", _FP32, D),
+        _ptr_n(k_weight, "k_weight", _FP32, D), eps, 1 if qk_norm else 0, T, Hq, Hk, D,
+        _dense_ptr(q_grad, "q_grad", (T, Hq, D), gdt),
+        _dense_ptr(k_grad, "k_grad", (T, Hk, D), gdt), _code(gdt),
+        None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(), ws, ws_bytes,
+        handle)
     if st != KDA_OK:
         raise KDAError(st, "kda_qk_norm_rope_bwd")
-    return q_grad, k_grad, wgrad[0], wgrad[1]
+    return q_grad, k_grad, wq, wk
 
 
+@lru_cache(maxsize=256)
 def paged_decode_workspace_size(N: int, Hq: int, Hk: int, D: int = 128) -> int:
     """Bytes of workspace kda_paged_decode needs, whatever the lengths."""
     out = ctypes.c_int64(0)
@@ -725,35 +774,33 @@ def kda_paged_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
                      stream: Optional[torch.cuda.Stream] = None, workspace=None):
     """Attention of one new token per request, q [N,Hq,D], over the pages of k_cache and
     v_cache [num_pages,Hk,page_size,D] named by block_table [N,max_pages], seq_lens [N] tokens
-    each.  Returns (out [N,Hq,D], lse [N,Hq] or None).  workspace: None (a fresh buffer) or a
+    each.  Returns (out [N,Hq,D], lse [N,Hq] or None).  workspace: None (one kept per stream) or a
     CUDA tensor of at least paged_decode_workspace_size(...) bytes."""
-    lib = load_library()
+    lib = _lib or load_library()
     N, Hq, D = q.shape
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must have shape [num_pages, Hk, page_size, D]")
-    num_pages, Hk, page_size = k_cache.shape[:3]
-    _cache_shape(k_cache, v_cache, Hk, D)
-    if block_table.dim() != 2 or block_table.shape[0] != N:
+    dev, dt = q.device, k_cache.dtype
+    num_pages, Hk, page_size, _ = _cache_shape(k_cache, v_cache, k_cache.shape[1], D)
+    rows, max_pages = block_table.shape
+    if rows != N:
         raise ValueError(f"block_table must have shape [{N}, max_pages]")
-    if scale is None:
-        scale = D ** -0.5
-    dev = q.device
     if out is None:
         out = torch.empty((N, Hq, D), dtype=out_dtype or q.dtype, device=dev)
     if lse is None and want_lse:
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
+        lse = torch.empty((N, Hq), dtype=_FP32, device=dev)
+    qp = _ptr(q, "q", dt)
+    handle = _stream_handle(stream, dev)
     if workspace is None:
-        workspace = torch.empty(paged_decode_workspace_size(N, Hq, Hk, D), dtype=torch.uint8,
-                                device=dev)
+        ws_bytes = paged_decode_workspace_size(N, Hq, Hk, D)
+        ws = _own_scratch(ws_bytes, dev, stream, handle)
+    else:
+        ws, ws_bytes = _dev_ptr(workspace, "workspace"), workspace.nbytes
+    odt = out.dtype
     st = lib.kda_paged_decode(
-        _dense_ptr(q, "q", (N, Hq, D), k_cache.dtype), _dev_ptr(k_cache, "k_cache"),
-        _dev_ptr(v_cache, "v_cache"), _dtype_code(k_cache),
-        _int_ptr(block_table, "block_table", torch.int32),
-        _int_ptr(seq_lens, "seq_lens", torch.int32, N), N, Hq, Hk, D, num_pages, page_size,
-        block_table.shape[1], float(scale), _dense_ptr(out, "out", (N, Hq, D), out.dtype),
-        _dtype_code(out), _f32_ptr(lse, "lse", N * Hq), _dev_ptr(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _dev_ptr(status, "status"),
-        _stream_handle(stream, dev))
+        qp, _ptr(k_cache, "k_cache", dt), _ptr(v_cache, "v_cache", dt), _code(dt),
+        _ptr(block_table, "block_table", _I32), _ptr_n(seq_lens, "seq_lens", _I32, N), N, Hq, Hk, D,
+        num_pages, page_size, max_pages, D ** -0.5 if scale is None else scale,
+        _dense_ptr(out, "out", (N, Hq, D), odt), _code(odt), _ptr_n(lse, "lse", _FP32, N * Hq),
+        ws, ws_bytes, _dev_ptr(status, "status"), handle)
     if st != KDA_OK:
         raise KDAError(st, "kda_paged_decode")
     return out, lse

@@ -10,6 +10,36 @@
 
 namespace kda {
 
+// SMs of the current device (152 without one); asked once per device, since a call of
+// a few microseconds notices the query.
+int sm_count();
+
+// Launches `kern` so that it may start while the kernel before it on the stream ends
+// (programmatic dependent launch): it waits for that kernel's memory itself.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), unsigned blocks, unsigned threads, cudaStream_t stream,
+                         A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+__device__ __forceinline__ void let_next_start()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- launches
 struct PlanArgs {
     const int32_t* cached;

@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(NT) paged_decode_kernel(DecodeArgs a, DecodeSh
     char* ws = static_cast<char*>(a.workspace);
     float2* ws_ml = reinterpret_cast<float2*>(ws + decode_ml_offset(a.N));
     float* ws_o = reinterpret_cast<float*>(ws + decode_o_offset(a.N, sh));
+    let_next_start();
     const DecodeRange rg = decode_range<NT>(a, sh, reinterpret_cast<int64_t*>(ws));
     const T* kc = static_cast<const T*>(a.k);
     const T* vc = static_cast<const T*>(a.v);
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(NT) decode_join_kernel(DecodeArgs a, DecodeSha
     const int64_t* prefix = reinterpret_cast<const int64_t*>(ws);
     const float2* ws_ml = reinterpret_cast<const float2*>(ws + decode_ml_offset(a.N));
     const float* ws_o = reinterpret_cast<const float*>(ws + decode_o_offset(a.N, sh));
+    wait_for_previous();
     const int64_t p0 = prefix[n], tiles = prefix[n + 1] - p0, W = prefix[a.N] * sh.units;
     const int64_t r = blockIdx.x;
     float y = 0.f, lse = -CUDART_INF_F;
@@ -274,8 +276,7 @@ DecodeShape simple_shape(const DecodeArgs& a, int* chunks)
     DecodeShape s;
     s.heads = c * gt;
     s.units = a.Hk * ((G + s.heads - 1) / s.heads);
-    const int sms = device_sm_count();
-    s.ctas = (sms > 0 ? sms : 152) * 2;
+    s.ctas = sm_count() * 2;
     s.tile_shift = kTileShift;
     return s;
 }
@@ -297,11 +298,8 @@ cudaError_t launch_simple(const DecodeArgs& a, const DecodeShape& s, int chunks,
 cudaError_t launch_decode_join(const DecodeArgs& a, const DecodeShape& s, cudaStream_t stream)
 {
     const int64_t rows = (int64_t)a.N * a.Hq;
-    if (a.D == 64)
-        decode_join_kernel<64><<<(unsigned)rows, NT, 0, stream>>>(a, s);
-    else
-        decode_join_kernel<128><<<(unsigned)rows, NT, 0, stream>>>(a, s);
-    return cudaGetLastError();
+    return launch_after(a.D == 64 ? decode_join_kernel<64> : decode_join_kernel<128>,
+                        (unsigned)rows, NT, stream, a, s);
 }
 
 int64_t paged_decode_workspace_bytes(int32_t N, int32_t Hq, int32_t Hk, int32_t D)

@@ -33,6 +33,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "kda_paged_sched.cuh"
 #include "kda_tc.cuh"
 
@@ -179,6 +181,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
         tmem_alloc(&bar.tmem, C::TM_COLS);
         tmem_relinquish();
     }
+    let_next_start();
     char* ws = static_cast<char*>(a.workspace);
     const DecodeRange rg = decode_range<C::NT>(a, sh, reinterpret_cast<int64_t*>(ws));
     fence_before_sync();
@@ -555,8 +558,17 @@ cudaError_t launch_typed(const DecodeArgs& a, const DecodeShape& s, cudaStream_t
     if (e == cudaSuccess) e = encode_rows(&maps.v, rows ? a.v : a.q, rows ? rows : qrows, D, box);
     if (e != cudaSuccess) return e;
     auto kern = paged_decode_tc_kernel<D, HP>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    // once per device: the setting stays with the kernel
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(set.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+        if (e != cudaSuccess) return e;
+        set.fetch_or(bit, std::memory_order_relaxed);
+    }
     kern<<<s.ctas, C::NT, C::SMEM, stream>>>(a, s, maps);
     return cudaGetLastError();
 }
@@ -566,11 +578,10 @@ cudaError_t launch_typed(const DecodeArgs& a, const DecodeShape& s, cudaStream_t
 DecodeShape decode_tc_shape(const DecodeArgs& a)
 {
     const int G = a.Hq / a.Hk, hp = padded_heads(G);
-    const int sms = device_sm_count();
     DecodeShape s;
     s.heads = hp;
     s.units = a.Hk * ((G + hp - 1) / hp);
-    s.ctas = (sms > 0 ? sms : 152) * (a.D == 64 && hp <= 32 ? 2 : 1);
+    s.ctas = sm_count() * (a.D == 64 && hp <= 32 ? 2 : 1);
     s.tile_shift = kTileShift;
     return s;
 }

@@ -15,6 +15,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kda_paged.cuh"
 
 namespace kda {
@@ -184,12 +186,26 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(PlanArgs a)
 
 }  // namespace
 
+int sm_count()
+{
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 152;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        n = device_sm_count();
+        if (n <= 0) return 152;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t stream)
 {
     // one token a thread; beyond four CTAs an SM the runs get longer instead
-    const int sms = device_sm_count();
     int64_t blocks = ((int64_t)a.T + NT - 1) / NT;
-    const int64_t most = 4 * (int64_t)(sms > 0 ? sms : 152);
+    const int64_t most = 4 * (int64_t)sm_count();
     if (blocks > most) blocks = most;
     if (blocks < 1) blocks = 1;
     page_plan_kernel<<<(unsigned)blocks, NT, 0, stream>>>(a);
