@@ -4,211 +4,295 @@
 //     s_t = scale q . k_t,   out = sum e^(s_t) v_t / sum e^(s_t)
 //
 // HBM-bound: every k and v is read once, 2 D values a token and key-value head.
-// Each warp works alone on batches of eight consecutive tokens (which lie in one
-// page): a row takes D / 4 lanes, 16 bytes each, straight from memory to
-// registers, keys and values of the batch together in flight; the products with
-// the unit's query rows (in registers, scaled by scale * log2 e) are summed over
-// the row's lanes by shuffles, and one pass keeps the running maximum m, sum l and
-// output o in base 2.  The CTA's warps take different batches of the same row and
-// merge (m, l, o) through shared memory at the end of it.
+// One CTA per SM; a producer warp fills slots of 32 tokens' keys and values by TMA, one
+// box per page (the keys in 128-byte columns, swizzled, so that 32 lanes can read 32
+// rows without bank conflicts).  Each of the other warps (six for 128 channels, ten
+// for 64: 160 to 192 KB of slots) has one slot and takes its tile on its own:
+//   scores   one token a lane: its key row against the unit's query rows, which all
+//            lanes read at the same address (scaled by scale * log2 e beforehand);
+//   softmax  a warp reduction per head; the reference maximum moves only when it
+//            would grow by more than 2^8, which is exact and rarely rescales;
+//   values   four channels a lane, the weights back from shared memory four tokens
+//            at a time.  Rows past the end are not read.
+// No lane reduces anything else across the warp, so 16 heads still cost less than
+// the 1400 clocks that 32 tokens of 128 channels take to arrive.  At the end of a
+// row the warps merge (m, l, o) through shared memory, four heads at a time.
 #include <cuda_runtime.h>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>
 #include <stdint.h>
+#include <string.h>
+
+#include <atomic>
 
 #include "kda_paged_sched.cuh"
+#include "kda_paged_tma.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int NT = 256;
-constexpr int NW = NT / 32;
-constexpr int kBatch = 8;              // tokens per warp step
-constexpr int kTileShift = 6;          // 64 tokens: one batch per warp
+using namespace tc;
+
+constexpr int kJoin = 256;             // threads of the join
+constexpr int kTile = 32;
+constexpr int kTileShift = 5;
+constexpr float kGrowth = 8.f;         // log2 of the growth that moves the reference maximum
+constexpr int kMerge = 4;              // heads merged at a time
+
+template <int D, int GT> struct Cfg {
+    static constexpr int W = D == 128 ? 6 : 10;                // warps that compute, and slots
+    static constexpr int NT = 32 * (W + 1);
+    static constexpr uint32_t TILE = kTile * D * 4;            // keys or values of a slot
+    static constexpr uint32_t SLOT = 2 * TILE;
+    static constexpr uint32_t OFF_Q = W * SLOT, OFF_P = OFF_Q + GT * D * 4,
+                              OFF_O = OFF_P + W * GT * kTile * 4,
+                              OFF_ML = OFF_O + W * kMerge * D * 4, OFF_BAR = OFF_ML + W * GT * 8,
+                              SMEM = OFF_BAR + 512 + 1024;
+    static_assert(SMEM + 256 <= 227 * 1024, "shared memory of a CTA");
+};
+
+struct Maps {
+    CUtensorMap k, v;
+};
+
+struct Bars {
+    uint64_t full[10], empty[10];      // a warp's slot
+    int32_t abort;
+};
 
 template <int D, int GT>
-__global__ void __launch_bounds__(NT) paged_decode_kernel(DecodeArgs a, DecodeShape sh, int chunks)
+__global__ void __launch_bounds__(Cfg<D, GT>::NT, 1)
+paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps maps)
 {
-    using T = float;
-    constexpr int VEC = 4;
-    constexpr int LPR = D / VEC, RPW = 32 / LPR;
-    constexpr int TB = kBatch / RPW;               // tokens per row group and step
-    __shared__ float s_m[NW][GT], s_l[NW][GT];
-    __shared__ float s_o[NW][GT][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane / LPR, chan = (lane % LPR) * VEC;
-    const int G = a.Hq / a.Hk;
-    // The warps are dealt to head chunks of GT heads; those of one chunk share the row's tokens.
-    const int chunk = warp % chunks, stream = warp / chunks, streams = NW / chunks;
+    using C = Cfg<D, GT>;
+    constexpr int W = C::W;
+    constexpr int BLOCKS = D / 32;                 // 128-byte columns of a key row
+    constexpr int LPR = D / 4, RPW = 32 / LPR;     // lanes per value row, rows at a time
+    extern __shared__ unsigned char raw[];
+    unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    Bars& bar = *reinterpret_cast<Bars*>(sm + C::OFF_BAR);
+    float* s_q = reinterpret_cast<float*>(sm + C::OFF_Q);          // [GT][D]
+    float* s_p = reinterpret_cast<float*>(sm + C::OFF_P);          // [W][GT][kTile]
+    float* s_o = reinterpret_cast<float*>(sm + C::OFF_O);          // [W][kMerge][D]
+    float2* s_ml = reinterpret_cast<float2*>(sm + C::OFF_ML);      // [W][GT]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int G = a.Hq / a.Hk, groups = sh.units / a.Hk;
+
+    if (tid == 0) {
+        for (int i = 0; i < W; ++i) {
+            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.empty[i], 1);
+        }
+        bar.abort = 0;
+        fence_mbar_init();
+    }
+    let_next_start();
     char* ws = static_cast<char*>(a.workspace);
+    const DecodeRange rg = decode_range<C::NT>(a, sh, reinterpret_cast<int64_t*>(ws));   // syncs
+
+    BoundedWait wait(&bar.abort, a.status);
+    DecodeWalk w(rg);
+    if (warp == W) {
+        // ------------------------------------------------------------ producer
+        const int shift = a.page_shift < kTileShift ? a.page_shift : kTileShift;
+        const int rows = 1 << shift;                               // tokens per box
+        uint32_t c = 0;
+        while (!wait.dead && w.next(a, sh)) {
+            const int hk = w.u / groups;
+            const int32_t* table = a.table + (int64_t)w.n * a.max_pages;
+            for (int t = w.tile0; t < w.tile1 && !wait.dead; ++t, ++c) {
+                const int tok = t << kTileShift, valid = min(kTile, w.L - tok);
+                const int pages = (valid + rows - 1) >> shift;
+                // lanes: the keys' columns page by page, then the values' pages
+                const bool key = lane < pages * BLOCKS;
+                const int j = key ? lane / BLOCKS : lane - pages * BLOCKS;
+                const bool any = j < pages;
+                int y = 0;
+                if (any)
+                    y = page_row(a, table, hk, tok + (j << shift));
+                const uint32_t slot = c % W;
+                wait(&bar.empty[slot], ((c / W) & 1) ^ 1);
+                wait.dead = __any_sync(0xffffffffu, wait.dead);
+                if (wait.dead) break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&bar.full[slot], 2u * pages * rows * D * 4);
+                __syncwarp();
+                const uint32_t dst = smem_u32(sm + slot * C::SLOT);
+                if (any) {
+                    const int col = lane % BLOCKS;
+                    if (key)
+                        tma_load_2d(dst + col * (kTile * 128) + (j << shift) * 128, &maps.k,
+                                    32 * col, y, &bar.full[slot]);
+                    else
+                        tma_load_2d(dst + C::TILE + (j << shift) * (D * 4), &maps.v, 0, y,
+                                    &bar.full[slot]);
+                }
+            }
+        }
+        // every copy has landed before the CTA ends
+        if (lane == 0)
+            for (uint32_t i = c > (uint32_t)W ? c - W : 0; i < c; ++i)
+                mbar_wait(&bar.full[i % W], (i / W) & 1);
+        return;
+    }
+    // ---------------------------------------------------------------- compute
+    const float qscale = a.scale * kLog2e;
     float2* ws_ml = reinterpret_cast<float2*>(ws + decode_ml_offset(a.N));
     float* ws_o = reinterpret_cast<float*>(ws + decode_o_offset(a.N, sh));
-    let_next_start();
-    const DecodeRange rg = decode_range<NT>(a, sh, reinterpret_cast<int64_t*>(ws));
-    const T* kc = static_cast<const T*>(a.k);
-    const T* vc = static_cast<const T*>(a.v);
-    const int groups = sh.units / a.Hk;            // units per key-value head
-    const float qscale = a.scale * kLog2e;
-
-    int64_t pos = rg.begin, at = rg.at;
-    int32_t n = rg.n;
-    while (pos < rg.end) {
-        const int32_t L = decode_len(a, n), tiles = tiles_of(L, sh.tile_shift);
-        if (pos >= at + (int64_t)tiles * sh.units) {
-            at += (int64_t)tiles * sh.units;
-            ++n;
-            continue;
+    float* my_p = s_p + warp * GT * kTile;
+    const int sub = lane / LPR, chan = (lane % LPR) * 4;
+    uint32_t c0 = 0;                               // the CTA's tiles before this row
+    while (w.next(a, sh)) {
+        const int hk = w.u / groups, g0 = (w.u - hk * groups) * GT;    // in the group of G
+        for (int i = tid; i < GT * D; i += 32 * W) {
+            const int g = i / D;
+            s_q[i] = g0 + g < G ? static_cast<const float*>(a.q)[((int64_t)w.n * a.Hq + hk * G + g0) *
+                                                                     D + i] * qscale
+                                : 0.f;
         }
-        const int32_t u = (int32_t)((pos - at) / tiles);
-        const int32_t tile0 = (int32_t)(pos - at - (int64_t)u * tiles);
-        const int32_t tile1 = (int32_t)min((int64_t)tiles, tile0 + (rg.end - pos));
-        const int hk = u / groups;
-        const int head0 = (u - hk * groups) * sh.heads + chunk * GT;   // in the group of G
-        const int t0 = tile0 << sh.tile_shift, t1 = min(L, tile1 << sh.tile_shift);
-
-        float q[GT][VEC], o[GT][VEC], m[GT], l[GT];
+        float m[GT], l[GT], o[GT][4];
 #pragma unroll
         for (int g = 0; g < GT; ++g) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (head0 + g < G)
-                x = *reinterpret_cast<const uint4*>(
-                    static_cast<const T*>(a.q) +
-                    ((int64_t)n * a.Hq + hk * G + head0 + g) * D + chan);
-            Vec16<T>::unpack(x, q[g]);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                q[g][j] *= qscale;
-                o[g][j] = 0.f;
-            }
             m[g] = -CUDART_INF_F;
             l[g] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[g][i] = 0.f;
         }
-        const int32_t* row = a.table + (int64_t)n * a.max_pages;
-        for (int b = t0 + stream * kBatch; b < t1; b += streams * kBatch) {
-            const int32_t page = row[b >> a.page_shift];
-            if ((uint32_t)page >= (uint32_t)a.num_pages) {
-                if (lane == 0) report_status(a.status, KDA_ERR_DEVICE_ARG);
-                continue;
-            }
-            const int64_t base = ((((int64_t)page * a.Hk + hk) << a.page_shift) +
-                                  (b & ((1 << a.page_shift) - 1))) * D + chan;
-            uint4 ku[TB], vu[TB];
+        named_sync(1, 32 * W);
+        // tile c of the CTA is in slot c % W, which is the warp's own: a warp that shared
+        // slots could mistake an earlier filling's phase for its own
+        for (int t = w.tile0 + (int)((warp + W - c0 % W) % W); t < w.tile1; t += W) {
+            const uint32_t c = c0 + (t - w.tile0);
+            const int valid = min(kTile, w.L - (t << kTileShift));
+            wait(&bar.full[warp], (c / W) & 1);
+            const unsigned char* kt = sm + warp * C::SLOT + lane * 128;
+            const float* vt = reinterpret_cast<const float*>(sm + warp * C::SLOT + C::TILE);
+            float s[GT];
 #pragma unroll
-            for (int j = 0; j < TB; ++j) {
-                const int t = j * RPW + sub;
-                ku[j] = vu[j] = make_uint4(0, 0, 0, 0);     // rows past the end: never read
-                if (b + t < t1) {
-                    ku[j] = __ldg(reinterpret_cast<const uint4*>(kc + base + (int64_t)t * D));
-                    vu[j] = __ldg(reinterpret_cast<const uint4*>(vc + base + (int64_t)t * D));
-                }
-            }
-            float s[TB][GT];
-#pragma unroll
-            for (int j = 0; j < TB; ++j) {
-                float kf[VEC];
-                Vec16<T>::unpack(ku[j], kf);
-                const bool live = b + j * RPW + sub < t1;
+            for (int g = 0; g < GT; ++g) s[g] = 0.f;
+#pragma unroll 8
+            for (int j = 0; j < D / 4; ++j) {
+                const float4 k = *reinterpret_cast<const float4*>(
+                    kt + (j >> 3) * (kTile * 128) + (((j & 7) ^ (lane & 7)) << 4));
 #pragma unroll
                 for (int g = 0; g < GT; ++g) {
-                    float x = 0.f;
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) x = fmaf(q[g][i], kf[i], x);
-#pragma unroll
-                    for (int k = LPR / 2; k > 0; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-                    s[j][g] = live ? x : -CUDART_INF_F;
+                    const float4 q = *reinterpret_cast<const float4*>(s_q + g * D + 4 * j);
+                    s[g] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[g]))));
                 }
             }
+            __syncwarp();                          // the last tile's weights are read
 #pragma unroll
             for (int g = 0; g < GT; ++g) {
-                float top = m[g];
+                const float x = lane < valid ? s[g] : -CUDART_INF_F;
+                const float top = warp_max(x);
+                if (top > m[g] + kGrowth) {        // uniform
+                    const float keep = exp2f(m[g] - top);
+                    m[g] = top;
+                    l[g] *= keep;
 #pragma unroll
-                for (int j = 0; j < TB; ++j) top = fmaxf(top, s[j][g]);
-                // a row group that has seen no token yet: nothing to subtract
-                const float ref = top == -CUDART_INF_F ? 0.f : top;
-                const float keep = exp2f(m[g] - ref);
-                m[g] = top;
-                l[g] *= keep;
+                    for (int i = 0; i < 4; ++i) o[g][i] *= keep;
+                }
+                // all scores so far -infinity: nothing to subtract
+                const float e = exp2f(x - (m[g] == -CUDART_INF_F ? 0.f : m[g]));
+                l[g] += e;
+                my_p[g * kTile + lane] = e;
+            }
+            __syncwarp();
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) o[g][i] *= keep;
+            for (int r = 0; r < kTile; r += 4 * RPW) {
+                if (r >= valid) break;             // uniform
+                float4 v[4];
 #pragma unroll
-                for (int j = 0; j < TB; ++j) {
-                    s[j][g] = exp2f(s[j][g] - ref);
-                    l[g] += s[j][g];
+                for (int i = 0; i < 4; ++i) {
+                    const int row = r + 4 * sub + i;
+                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);    // 0 * NaN is not 0
+                    if (row < valid) v[i] = *reinterpret_cast<const float4*>(vt + row * D + chan);
+                }
+#pragma unroll
+                for (int g = 0; g < GT; ++g) {
+                    const float4 p = *reinterpret_cast<const float4*>(my_p + g * kTile + r + 4 * sub);
+                    const float pi[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        o[g][0] = fmaf(pi[i], v[i].x, o[g][0]);
+                        o[g][1] = fmaf(pi[i], v[i].y, o[g][1]);
+                        o[g][2] = fmaf(pi[i], v[i].z, o[g][2]);
+                        o[g][3] = fmaf(pi[i], v[i].w, o[g][3]);
+                    }
                 }
             }
-#pragma unroll
-            for (int j = 0; j < TB; ++j) {
-                float vf[VEC];
-                Vec16<T>::unpack(vu[j], vf);
-#pragma unroll
-                for (int g = 0; g < GT; ++g)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) o[g][i] = fmaf(s[j][g], vf[i], o[g][i]);
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.empty[warp]);
         }
-        // merge the warp's row groups, then the chunk's warps
+        c0 += w.tile1 - w.tile0;
+        // merge: the row's maximum of each head over the warps, then outputs to it
 #pragma unroll
         for (int g = 0; g < GT; ++g) {
-            float top = m[g];
 #pragma unroll
-            for (int k = LPR; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-            const float keep = top == -CUDART_INF_F ? 0.f : exp2f(m[g] - top);
-            float lg = l[g] * keep;
-#pragma unroll
-            for (int k = LPR; k < 32; k <<= 1) lg += __shfl_xor_sync(0xffffffffu, lg, k);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                float x = o[g][i] * keep;
-#pragma unroll
-                for (int k = LPR; k < 32; k <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-                if (sub == 0) s_o[warp][g][chan + i] = x;
-            }
-            if (lane == 0) {
-                s_m[warp][g] = top;
-                s_l[warp][g] = lg;
-            }
+            for (int k = 16; k > 0; k >>= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], k);
+            if (lane == 0) s_ml[warp * GT + g] = make_float2(m[g], l[g]);
         }
-        __syncthreads();
-        const bool whole = tile0 == 0 && tile1 == tiles;
-        const int64_t piece = 2 * (int64_t)blockIdx.x + (tile0 == 0 ? 1 : 0);
-        for (int i = threadIdx.x; i < chunks * GT * D; i += NT) {
-            const int ch = i % D, g = (i / D) % GT, c = i / (D * GT);
-            const int head = (u - hk * groups) * sh.heads + c * GT + g;
-            if (c * GT + g >= sh.heads || head >= G) continue;
-            float top = -CUDART_INF_F;
-            for (int w = c; w < NW; w += chunks) top = fmaxf(top, s_m[w][g]);
-            float lsum = 0.f, x = 0.f;
-            if (top != -CUDART_INF_F)
-                for (int w = c; w < NW; w += chunks) {
-                    const float keep = exp2f(s_m[w][g] - top);
-                    lsum += s_l[w][g] * keep;
-                    x += s_o[w][g][ch] * keep;
+        named_sync(1, 32 * W);
+        const bool whole = w.tile0 == 0 && w.tile1 == w.tiles;
+        const int64_t r0 = whole ? (int64_t)w.n * a.Hq + hk * G + g0
+                                 : (2 * (int64_t)blockIdx.x + (w.tile0 == 0)) * GT;
+#pragma unroll
+        for (int gb = 0; gb < GT; gb += kMerge) {
+#pragma unroll
+            for (int g = gb; g < gb + kMerge && g < GT; ++g) {
+                float top = -CUDART_INF_F;
+#pragma unroll
+                for (int k = 0; k < W; ++k) top = fmaxf(top, s_ml[k * GT + g].x);
+                const float keep = top == -CUDART_INF_F ? 0.f : exp2f(m[g] - top);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[g][i] *= keep;
+#pragma unroll
+                    for (int k = LPR; k < 32; k <<= 1)
+                        o[g][i] += __shfl_xor_sync(0xffffffffu, o[g][i], k);
                 }
-            if (whole) {
-                const int64_t r = (int64_t)n * a.Hq + hk * G + head;
-                const float y = x / lsum;
-                if (a.out_bf16)
-                    store_one(static_cast<__nv_bfloat16*>(a.out) + r * D + ch, y);
-                else
-                    store_one(static_cast<float*>(a.out) + r * D + ch, y);
-                if (ch == 0 && a.lse != nullptr) a.lse[r] = top * kLn2 + logf(lsum);
-            } else {
-                const int64_t r = piece * sh.heads + c * GT + g;
-                ws_o[r * D + ch] = x;
-                if (ch == 0) ws_ml[r] = make_float2(top, lsum);
+                if (sub == 0)
+                    *reinterpret_cast<float4*>(s_o + (warp * kMerge + g - gb) * D + chan) =
+                        make_float4(o[g][0], o[g][1], o[g][2], o[g][3]);
             }
+            named_sync(1, 32 * W);
+            for (int i = tid; i < kMerge * D; i += 32 * W) {
+                const int g = gb + i / D, ch = i % D;
+                if (g >= GT || g0 + g >= G) continue;
+                float top = -CUDART_INF_F, sum = 0.f, x = 0.f;
+#pragma unroll
+                for (int k = 0; k < W; ++k) top = fmaxf(top, s_ml[k * GT + g].x);
+#pragma unroll
+                for (int k = 0; k < W; ++k) {
+                    const float2 ml = s_ml[k * GT + g];
+                    if (top != -CUDART_INF_F) sum += ml.y * exp2f(ml.x - top);
+                    x += s_o[(k * kMerge + g - gb) * D + ch];
+                }
+                const int64_t r = r0 + g;
+                if (whole) {
+                    const float y = x / sum;
+                    if (a.out_bf16)
+                        store_one(static_cast<__nv_bfloat16*>(a.out) + r * D + ch, y);
+                    else
+                        store_one(static_cast<float*>(a.out) + r * D + ch, y);
+                    if (ch == 0 && a.lse != nullptr) a.lse[r] = top * kLn2 + logf(sum);
+                } else {
+                    ws_o[r * D + ch] = x;
+                    if (ch == 0) ws_ml[r] = make_float2(top, sum);
+                }
+            }
+            named_sync(1, 32 * W);
         }
-        __syncthreads();
-        pos += tile1 - tile0;
     }
 }
 
 // One query head of one request per block: nothing to do for a whole row, zeros
 // for an empty request, and for a split row the joined pieces in the CTAs' order.
 template <int D>
-__global__ void __launch_bounds__(NT) decode_join_kernel(DecodeArgs a, DecodeShape sh)
+__global__ void __launch_bounds__(kJoin) decode_join_kernel(DecodeArgs a, DecodeShape sh)
 {
-    constexpr int P = NT / D;                      // pieces taken side by side
+    constexpr int P = kJoin / D;                      // pieces taken side by side
     __shared__ float s_x[P][D], s_l[P];
     const int h = blockIdx.x % a.Hq;
     const int32_t n = blockIdx.x / a.Hq;
@@ -263,34 +347,51 @@ __global__ void __launch_bounds__(NT) decode_join_kernel(DecodeArgs a, DecodeSha
     if (ch == 0 && a.lse != nullptr) a.lse[r] = lse;
 }
 
-// Query heads per warp: the smallest of 1, 2, 4, 8 that covers the group, or 8
-// with several chunks of warps.
-int chunk_heads(int G) { return G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : 8; }
+// Query heads per unit: the smallest of 1, 2, 4, 8, 16 that covers the group (more
+// heads than that read the cache once per 16).
+int unit_heads(int G) { return G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : G <= 8 ? 8 : 16; }
 
-DecodeShape simple_shape(const DecodeArgs& a, int* chunks)
+DecodeShape fp32_shape(const DecodeArgs& a)
 {
-    const int G = a.Hq / a.Hk, gt = chunk_heads(G);
-    int c = 1;
-    while (c * gt < G && c < NW) c *= 2;
-    *chunks = c;
+    const int G = a.Hq / a.Hk;
     DecodeShape s;
-    s.heads = c * gt;
+    s.heads = unit_heads(G);
     s.units = a.Hk * ((G + s.heads - 1) / s.heads);
-    s.ctas = sm_count() * 2;
+    s.ctas = sm_count();
     s.tile_shift = kTileShift;
     return s;
 }
 
-template <int D>
-cudaError_t launch_simple(const DecodeArgs& a, const DecodeShape& s, int chunks, cudaStream_t st)
+template <int D, int GT>
+cudaError_t launch_typed(const DecodeArgs& a, const DecodeShape& s, cudaStream_t stream)
 {
-    switch (chunk_heads(a.Hq / a.Hk)) {
-        case 1: paged_decode_kernel<D, 1><<<s.ctas, NT, 0, st>>>(a, s, chunks); break;
-        case 2: paged_decode_kernel<D, 2><<<s.ctas, NT, 0, st>>>(a, s, chunks); break;
-        case 4: paged_decode_kernel<D, 4><<<s.ctas, NT, 0, st>>>(a, s, chunks); break;
-        default: paged_decode_kernel<D, 8><<<s.ctas, NT, 0, st>>>(a, s, chunks);
-    }
+    using C = Cfg<D, GT>;
+    Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    const int page = 1 << a.page_shift, box = page < kTile ? page : kTile;
+    const int64_t rows = (int64_t)a.num_pages * a.Hk * page, qrows = (int64_t)a.N * a.Hq;
+    // an empty cache has no page to read: the maps only have to be valid
+    cudaError_t e = encode_rows(&maps.k, rows ? a.k : a.q, false, rows ? rows : qrows, D, 32, box, true);
+    if (e == cudaSuccess)
+        e = encode_rows(&maps.v, rows ? a.v : a.q, false, rows ? rows : qrows, D, D, box, false);
+    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> set{0};
+    e = allow_smem(paged_decode_kernel<D, GT>, C::SMEM, &set);
+    if (e != cudaSuccess) return e;
+    paged_decode_kernel<D, GT><<<s.ctas, C::NT, C::SMEM, stream>>>(a, s, maps);
     return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_fp32(const DecodeArgs& a, const DecodeShape& s, cudaStream_t st)
+{
+    switch (s.heads) {
+        case 1: return launch_typed<D, 1>(a, s, st);
+        case 2: return launch_typed<D, 2>(a, s, st);
+        case 4: return launch_typed<D, 4>(a, s, st);
+        case 8: return launch_typed<D, 8>(a, s, st);
+        default: return launch_typed<D, 16>(a, s, st);
+    }
 }
 
 }  // namespace
@@ -299,16 +400,15 @@ cudaError_t launch_decode_join(const DecodeArgs& a, const DecodeShape& s, cudaSt
 {
     const int64_t rows = (int64_t)a.N * a.Hq;
     return launch_after(a.D == 64 ? decode_join_kernel<64> : decode_join_kernel<128>,
-                        (unsigned)rows, NT, stream, a, s);
+                        (unsigned)rows, kJoin, stream, a, s);
 }
 
 int64_t paged_decode_workspace_bytes(int32_t N, int32_t Hq, int32_t Hk, int32_t D)
 {
     DecodeArgs a = {};
     a.N = N; a.Hq = Hq; a.Hk = Hk; a.D = D;
-    int chunks;
     int64_t most = 0;
-    for (const DecodeShape& s : {simple_shape(a, &chunks), decode_tc_shape(a)}) {
+    for (const DecodeShape& s : {fp32_shape(a), decode_tc_shape(a)}) {
         const int64_t b = decode_o_offset(N, s) + (int64_t)2 * s.ctas * s.heads * D * 4;
         if (b > most) most = b;
     }
@@ -317,17 +417,10 @@ int64_t paged_decode_workspace_bytes(int32_t N, int32_t Hq, int32_t Hk, int32_t 
 
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t stream)
 {
-    cudaError_t e;
-    DecodeShape s;
-    if (a.bf16) {
-        s = decode_tc_shape(a);
-        e = launch_paged_decode_tc(a, s, stream);
-    } else {
-        int chunks;
-        s = simple_shape(a, &chunks);
-        e = a.D == 64 ? launch_simple<64>(a, s, chunks, stream)
-                      : launch_simple<128>(a, s, chunks, stream);
-    }
+    const DecodeShape s = a.bf16 ? decode_tc_shape(a) : fp32_shape(a);
+    const cudaError_t e = a.bf16 ? launch_paged_decode_tc(a, s, stream)
+                          : a.D == 64 ? launch_fp32<64>(a, s, stream)
+                                      : launch_fp32<128>(a, s, stream);
     return e == cudaSuccess ? launch_decode_join(a, s, stream) : e;
 }
 

@@ -36,7 +36,7 @@
 #include <atomic>
 
 #include "kda_paged_sched.cuh"
-#include "kda_tc.cuh"
+#include "kda_paged_tma.cuh"
 
 namespace kda {
 namespace {
@@ -89,16 +89,6 @@ struct Bars {
     int32_t abort;
 };
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y,
-                                            uint64_t* m)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(m))
-        : "memory");
-}
-
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8])
 {
     uint32_t* u = reinterpret_cast<uint32_t*>(r);
@@ -113,37 +103,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8])
 __device__ __forceinline__ void tmem_ld(uint32_t a, float (&r)[8]) { tmem_ld8(a, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t a, float (&r)[16]) { tmem_ld16(a, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t a, float (&r)[32]) { tmem_ld32(a, r); }
-
-__device__ __forceinline__ float warp_max(float x)
-{
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// The rows (request, head unit) of a CTA's tiles, in order; every role walks its own.
-struct Walk {
-    int64_t pos, end, at;
-    int32_t n, u, tile0, tile1, tiles, L;
-    __device__ __forceinline__ explicit Walk(const DecodeRange& r)
-        : pos(r.begin), end(r.end), at(r.at), n(r.n), tile0(0), tile1(0) {}
-    __device__ __forceinline__ bool next(const DecodeArgs& a, const DecodeShape& sh)
-    {
-        pos += tile1 - tile0;
-        if (pos >= end) return false;
-        for (;; ++n) {
-            L = decode_len(a, n);
-            tiles = tiles_of(L, kTileShift);
-            const int64_t all = (int64_t)tiles * sh.units;
-            if (pos < at + all) break;
-            at += all;
-        }
-        u = (int32_t)((pos - at) / tiles);
-        tile0 = (int32_t)(pos - at - (int64_t)u * tiles);
-        tile1 = (int32_t)min((int64_t)tiles, tile0 + (end - pos));
-        return true;
-    }
-};
 
 template <int D, int HP>
 __global__ void __launch_bounds__(Cfg<D, HP>::NT, Cfg<D, HP>::CTAS)
@@ -189,27 +148,8 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
     fence_after_sync();
     const uint32_t tmem = bar.tmem;
 
-    // A wait that gives up marks the CTA: the producer stops, the others run their
-    // loops to the end without waiting or multiplying, so that all barriers meet.
-    volatile int32_t* abort_flag = &bar.abort;
-    bool dead = false;
-    auto wait = [&](uint64_t* m, uint32_t parity) {
-        if (dead) return;
-        for (uint32_t j = 0; j < kPollsPerCheck; ++j)
-            if (mbar_try_wait(m, parity)) return;
-        const uint64_t t0 = globaltimer_ns();
-        for (uint32_t i = 0; i < kMaxTimerChecks; ++i) {
-            for (uint32_t j = 0; j < kPollsPerCheck; ++j)
-                if (mbar_try_wait(m, parity)) return;
-            if (*abort_flag) break;
-            if (globaltimer_ns() - t0 > kWaitLimitNs) break;
-        }
-        dead = true;
-        *abort_flag = 1;
-        report_status(a.status, KDA_ERR_TIMEOUT);
-    };
-
-    Walk w(rg);
+    BoundedWait wait(&bar.abort, a.status);
+    DecodeWalk w(rg);
     if (warp == C::NWG * 4) {
         // ------------------------------------------------------------ producer
         const int rows = min(1 << a.page_shift, kTile);           // tokens per box
@@ -217,13 +157,13 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
         uint32_t c = 0;                                            // copies into the ring
         uint32_t item = 0;
         const int j = lane / HALVES, half = lane % HALVES;
-        while (!dead && w.next(a, sh)) {
+        while (!wait.dead && w.next(a, sh)) {
             const int hk = w.u / groups, g0 = (w.u - hk * groups) * HP;
             {
                 const uint32_t qb = item % C::NQ;
                 wait(&bar.qempty[qb], ((item / C::NQ) & 1) ^ 1);
-                dead = __any_sync(0xffffffffu, dead);
-                if (dead) break;
+                wait.dead = __any_sync(0xffffffffu, wait.dead);
+                if (wait.dead) break;
                 if (lane == 0) mbar_arrive_expect_tx(&bar.qfull[qb], C::QBUF);
                 __syncwarp();
                 if (lane < HALVES)
@@ -232,25 +172,17 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                 ++item;
             }
             const int32_t* table = a.table + (int64_t)w.n * a.max_pages;
-            for (int t = w.tile0; t < w.tile1 && !dead; ++t) {
+            for (int t = w.tile0; t < w.tile1 && !wait.dead; ++t) {
                 const int tok = t << kTileShift, valid = min(kTile, w.L - tok);
                 const int boxes = ((valid + rows - 1) >> row_shift) * HALVES;
                 int y = 0;
-                if (lane < boxes) {
-                    const int at = tok + (j << row_shift);
-                    int32_t page = table[at >> a.page_shift];
-                    if ((uint32_t)page >= (uint32_t)a.num_pages) {
-                        report_status(a.status, KDA_ERR_DEVICE_ARG);
-                        page = 0;
-                    }
-                    y = ((page * a.Hk + hk) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
-                }
+                if (lane < boxes) y = page_row(a, table, hk, tok + (j << row_shift));
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t slot = c % NS;
                     wait(&bar.empty[slot], ((c / NS) & 1) ^ 1);
-                    dead = __any_sync(0xffffffffu, dead);
-                    if (dead) break;
+                    wait.dead = __any_sync(0xffffffffu, wait.dead);
+                    if (wait.dead) break;
                     if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], boxes * rows * 128);
                     __syncwarp();
                     if (lane < boxes)
@@ -283,7 +215,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                 const uint32_t slot = (2 * t + 1) % NS, b = t & 1;
                 wait(&bar.full[slot], ((2 * t + 1) / NS) & 1);
                 wait(&bar.pfull[b], (t >> 1) & 1);
-                if (dead) return;
+                if (wait.dead) return;
                 fence_after_sync();
 #pragma unroll
                 for (int s = 0; s < kTile / 16; ++s)
@@ -300,7 +232,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                     const uint32_t slot = (2 * i) % NS, b = i & 1;
                     wait(&bar.full[slot], ((2 * i) / NS) & 1);
                     wait(&bar.sempty[b], ((i >> 1) & 1) ^ 1);
-                    if (!dead) {
+                    if (!wait.dead) {
                         fence_after_sync();
 #pragma unroll
                         for (int s = 0; s < D / 16; ++s)
@@ -502,41 +434,6 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
 }
 
 // ---------------------------------------------------------------- launch
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled()
-{
-    static const EncodeTiledFn fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return static_cast<EncodeTiledFn>(nullptr);
-        return reinterpret_cast<EncodeTiledFn>(p);
-    }();
-    return fn;
-}
-
-// rows x D BF16 values, read as boxes of box_rows x 64, 128-byte swizzled; rows
-// past the end read as zeros.
-cudaError_t encode_rows(CUtensorMap* m, const void* base, int64_t rows, int D, int box_rows)
-{
-    const EncodeTiledFn fn = encode_tiled();
-    if (fn == nullptr) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
-                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 int padded_heads(int G)
 {
     return G <= 8 ? 8 : G <= 16 ? 16 : G <= 32 ? 32 : 64;
@@ -552,23 +449,15 @@ cudaError_t launch_typed(const DecodeArgs& a, const DecodeShape& s, cudaStream_t
     const int64_t rows = (int64_t)a.num_pages * a.Hk * page;
     const int64_t qrows = (int64_t)a.N * a.Hq;
     const int box = page < kTile ? page : kTile;
-    cudaError_t e = encode_rows(&maps.q, a.q, qrows, D, C::QR);
+    cudaError_t e = encode_rows(&maps.q, a.q, true, qrows, D, 64, C::QR, true);
     // an empty cache has no page to read: the maps only have to be valid
-    if (e == cudaSuccess) e = encode_rows(&maps.k, rows ? a.k : a.q, rows ? rows : qrows, D, box);
-    if (e == cudaSuccess) e = encode_rows(&maps.v, rows ? a.v : a.q, rows ? rows : qrows, D, box);
+    if (e == cudaSuccess) e = encode_rows(&maps.k, rows ? a.k : a.q, true, rows ? rows : qrows, D, 64, box, true);
+    if (e == cudaSuccess) e = encode_rows(&maps.v, rows ? a.v : a.q, true, rows ? rows : qrows, D, 64, box, true);
     if (e != cudaSuccess) return e;
     auto kern = paged_decode_tc_kernel<D, HP>;
-    // once per device: the setting stays with the kernel
     static std::atomic<uint64_t> set{0};
-    int dev = 0;
-    e = cudaGetDevice(&dev);
+    e = allow_smem(kern, C::SMEM, &set);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (!(set.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
-        if (e != cudaSuccess) return e;
-        set.fetch_or(bit, std::memory_order_relaxed);
-    }
     kern<<<s.ctas, C::NT, C::SMEM, stream>>>(a, s, maps);
     return cudaGetLastError();
 }
