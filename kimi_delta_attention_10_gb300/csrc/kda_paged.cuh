@@ -17,16 +17,12 @@ int sm_count();
 // Launches `kern` so that it may start while the kernel before it on the stream ends
 // (programmatic dependent launch): it waits for that kernel's memory itself.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kern)(P...), unsigned blocks, unsigned threads, cudaStream_t stream,
-                         A... args)
+cudaError_t launch_after(void (*kern)(P...), cudaLaunchConfig_t cfg, cudaStream_t stream, A... args)
 {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(threads);
-    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);

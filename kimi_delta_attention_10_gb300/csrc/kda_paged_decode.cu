@@ -4,18 +4,17 @@
 //     s_t = scale q . k_t,   out = sum e^(s_t) v_t / sum e^(s_t)
 //
 // HBM-bound: every k and v is read once, 2 D values a token and key-value head.
-// One CTA per SM; a producer warp fills slots of 32 tokens' keys and values by TMA, one
-// box per page (the keys in 128-byte columns, swizzled, so that 32 lanes can read 32
-// rows without bank conflicts).  Each of the other warps (six for 128 channels, ten
-// for 64: 160 to 192 KB of slots) has one slot and takes its tile on its own:
-//   scores   one token a lane: its key row against the unit's query rows, which all
+// One CTA per SM; two producer warps (keys, values) fill slots of 32 tokens (64 of 64
+// channels) by TMA, one box per page (the keys in 128-byte columns, swizzled, so that
+// 32 lanes can read 32 rows without bank conflicts).  Each of six other warps has one
+// slot of 32 KB and takes its tile on its own:
+//   scores   one or two tokens a lane: key rows against the unit's query rows, which all
 //            lanes read at the same address (scaled by scale * log2 e beforehand);
 //   softmax  a warp reduction per head; the reference maximum moves only when it
 //            would grow by more than 2^8, which is exact and rarely rescales;
 //   values   four channels a lane, the weights back from shared memory four tokens
 //            at a time.  Rows past the end are not read.
-// No lane reduces anything else across the warp, so 16 heads still cost less than
-// the 1400 clocks that 32 tokens of 128 channels take to arrive.  At the end of a
+// No lane reduces anything else across the warp.  At the end of a
 // row the warps merge (m, l, o) through shared memory, four heads at a time.
 #include <cuda_runtime.h>
 #include <cuda.h>
@@ -35,21 +34,21 @@ namespace {
 using namespace tc;
 
 constexpr int kJoin = 256;             // threads of the join
-constexpr int kTile = 32;
-constexpr int kTileShift = 5;
 constexpr float kGrowth = 8.f;         // log2 of the growth that moves the reference maximum
 constexpr int kMerge = 4;              // heads merged at a time
 
 template <int D, int GT> struct Cfg {
-    static constexpr int W = D == 128 ? 6 : 10;                // warps that compute, and slots
-    static constexpr int NT = 32 * (W + 1);
+    static constexpr int W = D == 64 && GT == 16 ? 5 : 6;     // warps that compute, and slots
+    static constexpr int NT = 32 * (W + 2);
+    static constexpr int TPL = 128 / D, kTile = 32 * TPL;      // tokens per lane and tile
+    static constexpr int kTileShift = D == 128 ? 5 : 6;
     static constexpr uint32_t TILE = kTile * D * 4;            // keys or values of a slot
     static constexpr uint32_t SLOT = 2 * TILE;
     static constexpr uint32_t OFF_Q = W * SLOT, OFF_P = OFF_Q + GT * D * 4,
                               OFF_O = OFF_P + W * GT * kTile * 4,
                               OFF_ML = OFF_O + W * kMerge * D * 4, OFF_BAR = OFF_ML + W * GT * 8,
                               SMEM = OFF_BAR + 512 + 1024;
-    static_assert(SMEM + 256 <= 227 * 1024, "shared memory of a CTA");
+    static_assert(SMEM + 256 <= 227 * 1024 && 2 * W * 8 + 4 <= 512, "shared memory of a CTA");
 };
 
 struct Maps {
@@ -57,7 +56,7 @@ struct Maps {
 };
 
 struct Bars {
-    uint64_t full[10], empty[10];      // a warp's slot
+    uint64_t full[6], empty[6];        // a warp's slot
     int32_t abort;
 };
 
@@ -66,7 +65,7 @@ __global__ void __launch_bounds__(Cfg<D, GT>::NT, 1)
 paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps maps)
 {
     using C = Cfg<D, GT>;
-    constexpr int W = C::W;
+    constexpr int W = C::W, TPL = C::TPL, kTile = C::kTile, kTileShift = C::kTileShift;
     constexpr int BLOCKS = D / 32;                 // 128-byte columns of a key row
     constexpr int LPR = D / 4, RPW = 32 / LPR;     // lanes per value row, rows at a time
     extern __shared__ unsigned char raw[];
@@ -81,7 +80,7 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
 
     if (tid == 0) {
         for (int i = 0; i < W; ++i) {
-            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.full[i], 2);
             mbar_init(&bar.empty[i], 1);
         }
         bar.abort = 0;
@@ -89,45 +88,37 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
     }
     let_next_start();
     char* ws = static_cast<char*>(a.workspace);
-    const DecodeRange rg = decode_range<C::NT>(a, sh, reinterpret_cast<int64_t*>(ws));   // syncs
+    const DecodeRange rg = decode_range<C::NT>(a, sh, ws);   // syncs
 
     BoundedWait wait(&bar.abort, a.status);
     DecodeWalk w(rg);
-    if (warp == W) {
-        // ------------------------------------------------------------ producer
+    if (warp >= W) {
+        // ------------------------------------------------------------ producers
+        const bool keys = warp == W;
+        const void* map = keys ? &maps.k : &maps.v;
         const int shift = a.page_shift < kTileShift ? a.page_shift : kTileShift;
         const int rows = 1 << shift;                               // tokens per box
+        const int j = keys ? lane / BLOCKS : lane, col = keys ? lane % BLOCKS : 0;
+        const uint32_t box = keys ? col * (kTile * 128) + (j << shift) * 128
+                                  : C::TILE + (j << shift) * (D * 4);
         uint32_t c = 0;
         while (!wait.dead && w.next(a, sh)) {
             const int hk = w.u / groups;
             const int32_t* table = a.table + (int64_t)w.n * a.max_pages;
-            for (int t = w.tile0; t < w.tile1 && !wait.dead; ++t, ++c) {
+            for (int t = w.tile0; t < w.tile1; ++t, ++c) {
                 const int tok = t << kTileShift, valid = min(kTile, w.L - tok);
                 const int pages = (valid + rows - 1) >> shift;
-                // lanes: the keys' columns page by page, then the values' pages
-                const bool key = lane < pages * BLOCKS;
-                const int j = key ? lane / BLOCKS : lane - pages * BLOCKS;
-                const bool any = j < pages;
                 int y = 0;
-                if (any)
-                    y = page_row(a, table, hk, tok + (j << shift));
+                if (j < pages) y = page_row(a, table, hk, tok + (j << shift));
                 const uint32_t slot = c % W;
                 wait(&bar.empty[slot], ((c / W) & 1) ^ 1);
                 wait.dead = __any_sync(0xffffffffu, wait.dead);
                 if (wait.dead) break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&bar.full[slot], 2u * pages * rows * D * 4);
+                if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], pages * rows * D * 4);
                 __syncwarp();
-                const uint32_t dst = smem_u32(sm + slot * C::SLOT);
-                if (any) {
-                    const int col = lane % BLOCKS;
-                    if (key)
-                        tma_load_2d(dst + col * (kTile * 128) + (j << shift) * 128, &maps.k,
-                                    32 * col, y, &bar.full[slot]);
-                    else
-                        tma_load_2d(dst + C::TILE + (j << shift) * (D * 4), &maps.v, 0, y,
-                                    &bar.full[slot]);
-                }
+                if (j < pages)
+                    tma_load_2d(smem_u32(sm + slot * C::SLOT) + box, map, 32 * col, y,
+                                &bar.full[slot]);
             }
         }
         // every copy has landed before the CTA ends
@@ -138,8 +129,8 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
     }
     // ---------------------------------------------------------------- compute
     const float qscale = a.scale * kLog2e;
-    float2* ws_ml = reinterpret_cast<float2*>(ws + decode_ml_offset(a.N));
-    float* ws_o = reinterpret_cast<float*>(ws + decode_o_offset(a.N, sh));
+    float2* ws_ml = reinterpret_cast<float2*>(ws + decode_ml_offset(sh));
+    float* ws_o = reinterpret_cast<float*>(ws + decode_o_offset(sh));
     float* my_p = s_p + warp * GT * kTile;
     const int sub = lane / LPR, chan = (lane % LPR) * 4;
     uint32_t c0 = 0;                               // the CTA's tiles before this row
@@ -168,24 +159,38 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
             wait(&bar.full[warp], (c / W) & 1);
             const unsigned char* kt = sm + warp * C::SLOT + lane * 128;
             const float* vt = reinterpret_cast<const float*>(sm + warp * C::SLOT + C::TILE);
-            float s[GT];
+            float s[TPL][GT];
 #pragma unroll
-            for (int g = 0; g < GT; ++g) s[g] = 0.f;
+            for (int i = 0; i < TPL; ++i)
+#pragma unroll
+                for (int g = 0; g < GT; ++g) s[i][g] = 0.f;
 #pragma unroll 8
             for (int j = 0; j < D / 4; ++j) {
-                const float4 k = *reinterpret_cast<const float4*>(
-                    kt + (j >> 3) * (kTile * 128) + (((j & 7) ^ (lane & 7)) << 4));
+                float4 k[TPL];
+#pragma unroll
+                for (int i = 0; i < TPL; ++i)
+                    k[i] = *reinterpret_cast<const float4*>(kt + (j >> 3) * (kTile * 128) +
+                                                            i * 32 * 128 +
+                                                            (((j & 7) ^ (lane & 7)) << 4));
 #pragma unroll
                 for (int g = 0; g < GT; ++g) {
                     const float4 q = *reinterpret_cast<const float4*>(s_q + g * D + 4 * j);
-                    s[g] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[g]))));
+#pragma unroll
+                    for (int i = 0; i < TPL; ++i)
+                        s[i][g] = fmaf(q.x, k[i].x, fmaf(q.y, k[i].y, fmaf(q.z, k[i].z,
+                                                                          fmaf(q.w, k[i].w, s[i][g]))));
                 }
             }
             __syncwarp();                          // the last tile's weights are read
 #pragma unroll
             for (int g = 0; g < GT; ++g) {
-                const float x = lane < valid ? s[g] : -CUDART_INF_F;
-                const float top = warp_max(x);
+                float x[TPL], top = -CUDART_INF_F;
+#pragma unroll
+                for (int i = 0; i < TPL; ++i) {
+                    x[i] = lane + 32 * i < valid ? s[i][g] : -CUDART_INF_F;
+                    top = fmaxf(top, x[i]);
+                }
+                top = warp_max(top);
                 if (top > m[g] + kGrowth) {        // uniform
                     const float keep = exp2f(m[g] - top);
                     m[g] = top;
@@ -194,9 +199,13 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
                     for (int i = 0; i < 4; ++i) o[g][i] *= keep;
                 }
                 // all scores so far -infinity: nothing to subtract
-                const float e = exp2f(x - (m[g] == -CUDART_INF_F ? 0.f : m[g]));
-                l[g] += e;
-                my_p[g * kTile + lane] = e;
+                const float ref = m[g] == -CUDART_INF_F ? 0.f : m[g];
+#pragma unroll
+                for (int i = 0; i < TPL; ++i) {
+                    const float e = exp2f(x[i] - ref);
+                    l[g] += e;
+                    my_p[g * kTile + lane + 32 * i] = e;
+                }
             }
             __syncwarp();
 #pragma unroll
@@ -287,64 +296,85 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
     }
 }
 
-// One query head of one request per block: nothing to do for a whole row, zeros
-// for an empty request, and for a split row the joined pieces in the CTAs' order.
+// Joins the split rows.  Block (b, y) looks at the row that CTA b's tiles begin inside
+// of: where that is the row's first split, it joins the pieces of every gridDim.y-th
+// head from y, in the CTAs' order; most blocks find nothing to do.  A block's threads
+// take four channels of a piece each, several pieces side by side, so that even a row
+// split over all CTAs is some twenty loads deep.  Empty requests' rows are dealt to
+// all blocks.
 template <int D>
 __global__ void __launch_bounds__(kJoin) decode_join_kernel(DecodeArgs a, DecodeShape sh)
 {
-    constexpr int P = kJoin / D;                      // pieces taken side by side
-    __shared__ float s_x[P][D], s_l[P];
-    const int h = blockIdx.x % a.Hq;
-    const int32_t n = blockIdx.x / a.Hq;
-    const int G = a.Hq / a.Hk, hk = h / G, groups = sh.units / a.Hk;
-    const int g = (h - hk * G) % sh.heads;
-    const int u = hk * groups + (h - hk * G) / sh.heads;
-    const int ch = threadIdx.x % D, part = threadIdx.x / D;
-    const char* ws = static_cast<const char*>(a.workspace);
-    const int64_t* prefix = reinterpret_cast<const int64_t*>(ws);
-    const float2* ws_ml = reinterpret_cast<const float2*>(ws + decode_ml_offset(a.N));
-    const float* ws_o = reinterpret_cast<const float*>(ws + decode_o_offset(a.N, sh));
+    constexpr int LANES = D / 4, P = kJoin / LANES;        // threads per piece, pieces side by side
+    __shared__ float4 s_x[P][LANES];
+    __shared__ float s_l[P];
+    const int ch = (threadIdx.x % LANES) * 4, part = threadIdx.x / LANES;
+    auto store = [&](int64_t r, float4 y) {
+        if (a.out_bf16)
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + r * D + ch) =
+                make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+        else
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + r * D + ch) = y;
+    };
+    for (int64_t n = blockIdx.x + (int64_t)gridDim.x * blockIdx.y; n < a.N;
+         n += (int64_t)gridDim.x * gridDim.y) {
+        if (decode_len(a, n) != 0) continue;
+        for (int h = part; h < a.Hq; h += P) {
+            store(n * a.Hq + h, make_float4(0.f, 0.f, 0.f, 0.f));
+            if (ch == 0 && a.lse != nullptr) a.lse[n * a.Hq + h] = -CUDART_INF_F;
+        }
+    }
     wait_for_previous();
-    const int64_t p0 = prefix[n], tiles = prefix[n + 1] - p0, W = prefix[a.N] * sh.units;
-    const int64_t r = blockIdx.x;
-    float y = 0.f, lse = -CUDART_INF_F;
-    if (tiles > 0) {
-        const int64_t first = p0 * sh.units + u * tiles, last = first + tiles - 1;
-        // the CTA of tile x: the last b with b W / B <= x
-        const int64_t B = W < sh.ctas ? W : sh.ctas;
-        const int64_t b0 = ((first + 1) * B - 1) / W, b1 = ((last + 1) * B - 1) / W;
-        if (b0 == b1) return;                      // whole: written by its CTA
-        // the row begins in the first CTA's tiles, and before the others'
+    const char* ws = static_cast<const char*>(a.workspace);
+    const DecodeStart st = reinterpret_cast<const DecodeStart*>(ws)[blockIdx.x];
+    if (st.tile0 == 0) return;                             // nothing, or a row's own beginning
+    const float2* ws_ml = reinterpret_cast<const float2*>(ws + decode_ml_offset(sh));
+    const float* ws_o = reinterpret_cast<const float*>(ws + decode_o_offset(sh));
+    const int64_t B = st.W < sh.ctas ? st.W : sh.ctas;
+    const int64_t first = blockIdx.x * st.W / B - st.tile0, last = first + st.tiles - 1;
+    // the CTA of tile x: the last b with b W / B <= x
+    const int64_t b0 = ((first + 1) * B - 1) / st.W, b1 = ((last + 1) * B - 1) / st.W;
+    if (b0 + 1 != blockIdx.x) return;                      // an earlier split joins the row
+    const int G = a.Hq / a.Hk, groups = sh.units / a.Hk;
+    const int hk = st.u / groups, g0 = (st.u - hk * groups) * sh.heads;
+    const int heads = min(sh.heads, G - g0);
+    for (int g = blockIdx.y; g < heads; g += gridDim.y) {
         float top = -CUDART_INF_F;
+#pragma unroll 4
         for (int64_t b = b0; b <= b1; ++b)
             top = fmaxf(top, ws_ml[(2 * b + (b == b0)) * sh.heads + g].x);
-        float x = 0.f, l = 0.f;
-        if (top != -CUDART_INF_F)
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+        if (top != -CUDART_INF_F) {
+#pragma unroll 4
             for (int64_t b = b0 + part; b <= b1; b += P) {
-                const int64_t i = (2 * b + (b == b0)) * sh.heads + g;
+                const int64_t i = (2 * b + (b == b0)) * sh.heads + g;   // the row begins in b0's tiles
                 const float2 ml = ws_ml[i];
+                const float4 o = *reinterpret_cast<const float4*>(ws_o + i * D + ch);
                 const float keep = exp2f(ml.x - top);
                 l = fmaf(ml.y, keep, l);
-                x = fmaf(ws_o[i * D + ch], keep, x);
+                x.x = fmaf(o.x, keep, x.x);
+                x.y = fmaf(o.y, keep, x.y);
+                x.z = fmaf(o.z, keep, x.z);
+                x.w = fmaf(o.w, keep, x.w);
             }
-        s_x[part][ch] = x;
+        }
+        __syncthreads();                                   // the last head's sums are read
+        s_x[part][ch / 4] = x;
         if (ch == 0) s_l[part] = l;
         __syncthreads();
-        x = l = 0.f;
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            x += s_x[i][ch];
+        if (part != 0) continue;
+        const int pieces = (int)min((int64_t)P, b1 - b0 + 1);
+        for (int i = 1; i < pieces; ++i) {
+            const float4 o = s_x[i][ch / 4];
+            x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
             l += s_l[i];
         }
-        y = x / l;
-        lse = top * kLn2 + logf(l);
+        const float inv = 1.f / l;
+        const int64_t r = (int64_t)st.n * a.Hq + hk * G + g0 + g;
+        store(r, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+        if (ch == 0 && a.lse != nullptr) a.lse[r] = top * kLn2 + logf(l);
     }
-    if (part != 0) return;
-    if (a.out_bf16)
-        store_one(static_cast<__nv_bfloat16*>(a.out) + r * D + ch, y);
-    else
-        store_one(static_cast<float*>(a.out) + r * D + ch, y);
-    if (ch == 0 && a.lse != nullptr) a.lse[r] = lse;
 }
 
 // Query heads per unit: the smallest of 1, 2, 4, 8, 16 that covers the group (more
@@ -358,7 +388,7 @@ DecodeShape fp32_shape(const DecodeArgs& a)
     s.heads = unit_heads(G);
     s.units = a.Hk * ((G + s.heads - 1) / s.heads);
     s.ctas = sm_count();
-    s.tile_shift = kTileShift;
+    s.tile_shift = a.D == 128 ? 5 : 6;
     return s;
 }
 
@@ -368,7 +398,7 @@ cudaError_t launch_typed(const DecodeArgs& a, const DecodeShape& s, cudaStream_t
     using C = Cfg<D, GT>;
     Maps maps;
     memset(&maps, 0, sizeof(maps));
-    const int page = 1 << a.page_shift, box = page < kTile ? page : kTile;
+    const int page = 1 << a.page_shift, box = page < C::kTile ? page : C::kTile;
     const int64_t rows = (int64_t)a.num_pages * a.Hk * page, qrows = (int64_t)a.N * a.Hq;
     // an empty cache has no page to read: the maps only have to be valid
     cudaError_t e = encode_rows(&maps.k, rows ? a.k : a.q, false, rows ? rows : qrows, D, 32, box, true);
@@ -398,9 +428,11 @@ cudaError_t launch_fp32(const DecodeArgs& a, const DecodeShape& s, cudaStream_t 
 
 cudaError_t launch_decode_join(const DecodeArgs& a, const DecodeShape& s, cudaStream_t stream)
 {
-    const int64_t rows = (int64_t)a.N * a.Hq;
-    return launch_after(a.D == 64 ? decode_join_kernel<64> : decode_join_kernel<128>,
-                        (unsigned)rows, kJoin, stream, a, s);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)s.ctas, (unsigned)(s.heads < 8 ? s.heads : 8));
+    cfg.blockDim = dim3(kJoin);
+    return launch_after(a.D == 64 ? decode_join_kernel<64> : decode_join_kernel<128>, cfg, stream, a,
+                        s);
 }
 
 int64_t paged_decode_workspace_bytes(int32_t N, int32_t Hq, int32_t Hk, int32_t D)
@@ -409,7 +441,7 @@ int64_t paged_decode_workspace_bytes(int32_t N, int32_t Hq, int32_t Hk, int32_t 
     a.N = N; a.Hq = Hq; a.Hk = Hk; a.D = D;
     int64_t most = 0;
     for (const DecodeShape& s : {fp32_shape(a), decode_tc_shape(a)}) {
-        const int64_t b = decode_o_offset(N, s) + (int64_t)2 * s.ctas * s.heads * D * 4;
+        const int64_t b = decode_workspace(s, D);
         if (b > most) most = b;
     }
     return most;

@@ -11,16 +11,18 @@
 // 128-row operand's read), and the weights then carry 16 bits instead of 8.
 //
 // HBM-bound: 2 D values a token and key-value head, once.  Warp roles:
-//   producer  one TMA box per page and 64 channels into a ring of K and V slots
-//             (swizzled as the MMA reads them), the block table read by its lanes;
+//   producers one warp for K, one for V: a TMA box per page and 64 channels into a
+//             ring of slots (swizzled as the MMA reads them), the block table read by
+//             the lanes;
 //   MMA       one thread: S of tile i + 1 is issued before the product with V of
-//             tile i, so that it runs while the softmax of tile i does;
+//             tile i, so that it runs while the softmax of tile i does; O adds up in
+//             tensor memory over a row's tiles;
 //   softmax   four warps (eight for more than 32 heads): one token a lane.  The
-//             tile's maximum per head is a warp reduction and four values through
-//             shared memory; m is moved only when it would grow by more than 2^8
-//             (p stays within FP32 and BF16 range, the ratios are exact either way),
-//             so the running output is rarely rescaled.  The sum of O over tiles is
-//             kept in registers: thread d adds up the D-row d of each tile's product.
+//             reference maximum m moves only when some score of the tile exceeds it
+//             by more than 2^8 (p stays within FP32 and BF16 range, the ratios are
+//             exact either way): one barrier with a vote per tile, and only after a
+//             yes the tile's maxima (a warp reduction, four values through shared
+//             memory) and a rescaling of O.
 // The CTA's tiles run through all its rows without draining the ring.
 //
 // Tokens past the request's end: their scores are replaced by -infinity, their
@@ -53,7 +55,8 @@ template <int D_, int HP_> struct Cfg {
     static constexpr int HW = HP / NWG;                // heads of each
     static constexpr int QR = HP < 16 ? 16 : HP;       // N of the first product
     static constexpr int NPV = 2 * HP;                 // N of the second
-    static constexpr int NT = NWG * 128 + 64;
+    static constexpr int NT = NWG * 128 + 96;
+    static constexpr int WARP_K = NWG * 4, WARP_V = WARP_K + 1, WARP_MMA = WARP_K + 2;
     static constexpr int CTAS = D == 64 && HP <= 32 ? 2 : 1;   // per SM
     static constexpr uint32_t SLOT = kTile * D * 2;
     static constexpr uint32_t PBUF = NPV * 256, QBUF = QR * D * 2;
@@ -68,7 +71,7 @@ template <int D_, int HP_> struct Cfg {
     static constexpr uint32_t OFF_P = NS * SLOT, OFF_Q = OFF_P + 2 * PBUF,
                               OFF_MISC = OFF_Q + NQ * QBUF, SMEM = OFF_MISC + MISC + 1024;
     static constexpr uint32_t TM_O = 2 * QR;           // after two S buffers
-    static constexpr uint32_t TM_USED = TM_O + 2 * NPV;
+    static constexpr uint32_t TM_USED = TM_O + NPV;
     static constexpr uint32_t TM_COLS = TM_USED <= 64 ? 64 : TM_USED <= 128 ? 128
                                         : TM_USED <= 256 ? 256 : 512;
     static_assert(TM_COLS * CTAS <= 512, "tensor memory of an SM");
@@ -81,8 +84,8 @@ struct Maps {
 struct Bars {
     uint64_t full[8], empty[8];        // ring slots
     uint64_t sfull[2], sempty[2];      // S in tensor memory
-    uint64_t pfull[2];                 // P in shared memory (and the O buffer read)
-    uint64_t ofull[2];                 // O in tensor memory (and the P buffer read)
+    uint64_t pfull[2];                 // P in shared memory
+    uint64_t ofull[2];                 // product with V done: O is whole, the P buffer read
     uint64_t qfull[2], qempty[2];
     uint64_t drain;
     uint32_t tmem;
@@ -103,6 +106,15 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8])
 __device__ __forceinline__ void tmem_ld(uint32_t a, float (&r)[8]) { tmem_ld8(a, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t a, float (&r)[16]) { tmem_ld16(a, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t a, float (&r)[32]) { tmem_ld32(a, r); }
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&r)[8])
+{
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(u[0]),
+                 "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
+                 "r"(taddr)
+                 : "memory");
+}
 
 template <int D, int HP>
 __global__ void __launch_bounds__(Cfg<D, HP>::NT, Cfg<D, HP>::CTAS)
@@ -136,13 +148,13 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
         bar.abort = 0;
         fence_mbar_init();
     }
-    if (warp == C::NWG * 4 + 1) {
+    if (warp == C::WARP_MMA) {
         tmem_alloc(&bar.tmem, C::TM_COLS);
         tmem_relinquish();
     }
     let_next_start();
     char* ws = static_cast<char*>(a.workspace);
-    const DecodeRange rg = decode_range<C::NT>(a, sh, reinterpret_cast<int64_t*>(ws));
+    const DecodeRange rg = decode_range<C::NT>(a, sh, ws);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -150,16 +162,17 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
 
     BoundedWait wait(&bar.abort, a.status);
     DecodeWalk w(rg);
-    if (warp == C::NWG * 4) {
-        // ------------------------------------------------------------ producer
-        const int rows = min(1 << a.page_shift, kTile);           // tokens per box
+    if (warp == C::WARP_K || warp == C::WARP_V) {
+        // ------------------------------------------------------------ producers
+        const bool keys = warp == C::WARP_K;
+        const void* map = keys ? &maps.k : &maps.v;
         const int row_shift = a.page_shift < kTileShift ? a.page_shift : kTileShift;
-        uint32_t c = 0;                                            // copies into the ring
-        uint32_t item = 0;
+        const int rows = 1 << row_shift;                           // tokens per box
+        uint32_t i = 0, item = 0;                                  // tiles and rows so far
         const int j = lane / HALVES, half = lane % HALVES;
         while (!wait.dead && w.next(a, sh)) {
             const int hk = w.u / groups, g0 = (w.u - hk * groups) * HP;
-            {
+            if (keys) {
                 const uint32_t qb = item % C::NQ;
                 wait(&bar.qempty[qb], ((item / C::NQ) & 1) ^ 1);
                 wait.dead = __any_sync(0xffffffffu, wait.dead);
@@ -172,35 +185,33 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                 ++item;
             }
             const int32_t* table = a.table + (int64_t)w.n * a.max_pages;
-            for (int t = w.tile0; t < w.tile1 && !wait.dead; ++t) {
+            for (int t = w.tile0; t < w.tile1; ++t, ++i) {
                 const int tok = t << kTileShift, valid = min(kTile, w.L - tok);
                 const int boxes = ((valid + rows - 1) >> row_shift) * HALVES;
                 int y = 0;
                 if (lane < boxes) y = page_row(a, table, hk, tok + (j << row_shift));
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const uint32_t slot = c % NS;
-                    wait(&bar.empty[slot], ((c / NS) & 1) ^ 1);
-                    wait.dead = __any_sync(0xffffffffu, wait.dead);
-                    if (wait.dead) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], boxes * rows * 128);
-                    __syncwarp();
-                    if (lane < boxes)
-                        tma_load_2d(smem_u32(sm + slot * C::SLOT + half * (kTile * 128) +
-                                             ((j << row_shift) * 128)),
-                                    kv ? &maps.v : &maps.k, 64 * half, y, &bar.full[slot]);
-                    ++c;
-                }
+                const uint32_t c = 2 * i + (keys ? 0 : 1), slot = c % NS;
+                wait(&bar.empty[slot], ((c / NS) & 1) ^ 1);
+                wait.dead = __any_sync(0xffffffffu, wait.dead);
+                if (wait.dead) break;
+                if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], boxes * rows * 128);
+                __syncwarp();
+                if (lane < boxes)
+                    tma_load_2d(smem_u32(sm + slot * C::SLOT + half * (kTile * 128) +
+                                         ((j << row_shift) * 128)),
+                                map, 64 * half, y, &bar.full[slot]);
             }
         }
         // every copy has landed before the CTA ends (all were waited for, unless a wait gave up)
         if (lane == 0) {
-            for (uint32_t i = c > (uint32_t)NS ? c - NS : 0; i < c; ++i)
-                mbar_wait(&bar.full[i % NS], (i / NS) & 1);
-            for (uint32_t i = item > (uint32_t)C::NQ ? item - C::NQ : 0; i < item; ++i)
-                mbar_wait(&bar.qfull[i % C::NQ], (i / C::NQ) & 1);
+            for (uint32_t k = i > (uint32_t)NS ? i - NS : 0; k < i; ++k) {
+                const uint32_t c = 2 * k + (keys ? 0 : 1);
+                if (c + NS >= 2 * i) mbar_wait(&bar.full[c % NS], (c / NS) & 1);
+            }
+            for (uint32_t k = item > (uint32_t)C::NQ ? item - C::NQ : 0; k < item; ++k)
+                mbar_wait(&bar.qfull[k % C::NQ], (k / C::NQ) & 1);
         }
-    } else if (warp == C::NWG * 4 + 1) {
+    } else if (warp == C::WARP_MMA) {
         // ------------------------------------------------------------ MMA
         if (lane == 0) {
             constexpr uint32_t id_s = idesc(kFmtBF16, kTile, C::QR);
@@ -211,6 +222,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
             const uint64_t dQ = desc_kmajor(smem_u32(sm + C::OFF_Q), C::QR, 0);
             const uint64_t dP = desc_kmajor(smem_u32(sm + C::OFF_P), C::NPV, 0);
             uint32_t i = 0, item = 0;
+            bool begins = false;                           // tile i - 1 is its row's first here
             auto product_with_v = [&](uint32_t t) {
                 const uint32_t slot = (2 * t + 1) % NS, b = t & 1;
                 wait(&bar.full[slot], ((2 * t + 1) / NS) & 1);
@@ -219,9 +231,9 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                 fence_after_sync();
 #pragma unroll
                 for (int s = 0; s < kTile / 16; ++s)
-                    mma_bf16(tmem + C::TM_O + b * C::NPV,
-                             desc_advance(dV, slot * C::SLOT + mnmajor_off(s)),
-                             desc_advance(dP, b * C::PBUF + kmajor_off(C::NPV, s)), id_o, s > 0);
+                    mma_bf16(tmem + C::TM_O, desc_advance(dV, slot * C::SLOT + mnmajor_off(s)),
+                             desc_advance(dP, b * C::PBUF + kmajor_off(C::NPV, s)), id_o,
+                             s > 0 || !begins);
                 commit(&bar.empty[slot]);
                 commit(&bar.ofull[b]);
             };
@@ -245,6 +257,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                         commit(&bar.sfull[b]);
                     }
                     if (i > 0) product_with_v(i - 1);
+                    begins = t == w.tile0;
                 }
                 ++item;
             }
@@ -262,30 +275,17 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
         const uint32_t p_base = smem_u32(sm + C::OFF_P) + (row >> 6) * (C::NPV * 128) +
                                 (row & 7) * 2 + wg * HW * 128;
         const uint32_t p_chunk = (row >> 3) & 7;
-        float2* ws_ml = reinterpret_cast<float2*>(ws + decode_ml_offset(a.N));
-        float* ws_o = reinterpret_cast<float*>(ws + decode_o_offset(a.N, sh));
+        float2* ws_ml = reinterpret_cast<float2*>(ws + decode_ml_offset(sh));
+        float* ws_o = reinterpret_cast<float*>(ws + decode_o_offset(sh));
         uint32_t i = 0;
         while (w.next(a, sh)) {
-            float ref[HW], l[HW], acc[HW];
+            float ref[HW], l[HW];
 #pragma unroll
             for (int g = 0; g < HW; ++g) {
                 ref[g] = -CUDART_INF_F;
-                l[g] = acc[g] = 0.f;
+                l[g] = 0.f;
             }
-            bool pending = false;
-            auto add_o = [&](uint32_t t) {
-                wait(&bar.ofull[t & 1], (t >> 1) & 1);
-                __syncwarp();
-                fence_after_sync();
-                const uint32_t o = tlane + C::TM_O + (t & 1) * C::NPV + wg * HW;
-                float x[HW];
-                tmem_ld(o, x);
-#pragma unroll
-                for (int g = 0; g < HW; ++g) acc[g] += x[g];
-                tmem_ld(o + HP, x);
-#pragma unroll
-                for (int g = 0; g < HW; ++g) acc[g] += x[g];
-            };
+            bool open = true;                              // some reference is still -infinity
             for (int t = w.tile0; t < w.tile1; ++t, ++i) {
                 const uint32_t b = i & 1;
                 const int valid = w.L - (t << kTileShift);
@@ -297,50 +297,66 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.sempty[b]);
-                float* maxima = s_max + (b * C::NWG + wg) * 4 * HW;
-                float mine = 0.f;
+                if (valid < kTile) {
 #pragma unroll
-                for (int g = 0; g < HW; ++g) {
-                    s[g] = row < valid ? s[g] * c : -CUDART_INF_F;
-                    const float m = warp_max(s[g]);
-                    if (lane == g) mine = m;
+                    for (int g = 0; g < HW; ++g) s[g] = row < valid ? s[g] * c : -CUDART_INF_F;
+                } else {
+#pragma unroll
+                    for (int g = 0; g < HW; ++g) s[g] *= c;
                 }
-                if (lane < HW) maxima[quad * HW + lane] = mine;
-                named_sync(bar_id, 128);
-                bool grown = false;
-                float top[HW];
+                bool grown = open;                         // uniform over the warpgroup
+                if (!grown) {
+                    float over = -CUDART_INF_F;
 #pragma unroll
-                for (int g = 0; g < HW; g += 4) {
-                    float4 m = *reinterpret_cast<const float4*>(maxima + g);
-#pragma unroll
-                    for (int k = 1; k < 4; ++k) {
-                        const float4 x = *reinterpret_cast<const float4*>(maxima + k * HW + g);
-                        m.x = fmaxf(m.x, x.x);
-                        m.y = fmaxf(m.y, x.y);
-                        m.z = fmaxf(m.z, x.z);
-                        m.w = fmaxf(m.w, x.w);
-                    }
-                    top[g] = m.x;
-                    top[g + 1] = m.y;
-                    top[g + 2] = m.z;
-                    top[g + 3] = m.w;
+                    for (int g = 0; g < HW; ++g) over = fmaxf(over, s[g] - ref[g]);
+                    grown = named_sync_or(bar_id, 128, over > kGrowth);
                 }
-#pragma unroll
-                for (int g = 0; g < HW; ++g) grown |= top[g] > ref[g] + kGrowth;
-                if (grown) {                               // uniform over the warpgroup
-                    if (pending) add_o(i - 1);
-                    pending = false;
+                if (grown) {
+                    float* maxima = s_max + (b * C::NWG + wg) * 4 * HW;
+                    float mine = 0.f;
 #pragma unroll
                     for (int g = 0; g < HW; ++g) {
-                        if (top[g] > ref[g] + kGrowth) {
-                            // ref -infinity: sums and output are zero
-                            const float keep = exp2f(ref[g] - top[g]);
-                            l[g] *= keep;
-                            acc[g] *= keep;
-                            ref[g] = top[g];
+                        const float m = warp_max(s[g]);
+                        if (lane == g) mine = m;
+                    }
+                    if (lane < HW) maxima[quad * HW + lane] = mine;
+                    if (t > w.tile0) wait(&bar.ofull[b ^ 1], ((i - 1) >> 1) & 1);
+                    named_sync(bar_id, 128);
+                    open = false;
+#pragma unroll
+                    for (int g0 = 0; g0 < HW; g0 += 8) {
+                        float keep[8];
+                        bool moved = false;
+#pragma unroll
+                        for (int g = 0; g < 8; ++g) {
+                            const float* x = maxima + g0 + g;
+                            const float top = fmaxf(fmaxf(x[0], x[HW]), fmaxf(x[2 * HW], x[3 * HW]));
+                            keep[g] = 1.f;
+                            if (top > ref[g0 + g] + kGrowth) {
+                                keep[g] = exp2f(ref[g0 + g] - top);
+                                ref[g0 + g] = top;
+                                l[g0 + g] *= keep[g];
+                                moved = true;
+                            }
+                            open |= ref[g0 + g] == -CUDART_INF_F;
+                        }
+                        if (t > w.tile0 && moved) {
+                            fence_after_sync();
+#pragma unroll
+                            for (int part = 0; part < 2; ++part) {
+                                const uint32_t o = tlane + C::TM_O + part * HP + wg * HW + g0;
+                                float x[8];
+                                tmem_ld8(o, x);
+#pragma unroll
+                                for (int g = 0; g < 8; ++g) x[g] *= keep[g];
+                                tmem_st8(o, x);
+                            }
+                            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                         }
                     }
                 }
+                // the P buffer's last reader
+                if (i >= 2) wait(&bar.ofull[b], ((i - 2) >> 1) & 1);
                 const uint32_t p = p_base + b * C::PBUF;
 #pragma unroll
                 for (int g = 0; g < HW; g += 2) {
@@ -384,10 +400,19 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.pfull[b]);
-                if (pending) add_o(i - 1);
-                pending = true;
             }
-            add_o(i - 1);
+            // the row's last product; the next one overwrites O after the next pfull
+            wait(&bar.ofull[(i - 1) & 1], ((i - 1) >> 1) & 1);
+            __syncwarp();
+            fence_after_sync();
+            float acc[HW];
+            tmem_ld(tlane + C::TM_O + wg * HW, acc);
+            {
+                float x[HW];
+                tmem_ld(tlane + C::TM_O + HP + wg * HW, x);
+#pragma unroll
+                for (int g = 0; g < HW; ++g) acc[g] += x[g];
+            }
             // the sums of all tokens' weights
 #pragma unroll
             for (int g = 0; g < HW; ++g) {
@@ -427,7 +452,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
     }
     fence_before_sync();
     __syncthreads();
-    if (warp == C::NWG * 4 + 1) {
+    if (warp == C::WARP_MMA) {
         fence_after_sync();
         tmem_dealloc(tmem, C::TM_COLS);
     }

@@ -20,15 +20,26 @@ struct DecodeShape {
     int32_t tile_shift;   // log2 of the tokens per tile
 };
 
-// Workspace: int64 prefix of tiles [N + 1], then the pieces' (m, l) pairs
-// [2 CTAs][heads], then their outputs [2 CTAs][heads][D].
-__host__ __device__ inline int64_t decode_ml_offset(int32_t N)
+// Where a CTA's tiles begin; the join starts from these.
+struct alignas(16) DecodeStart {
+    int32_t n, u, tile0, tiles;        // request, unit, the first tile's index in its row, the row's tiles
+    int64_t W;
+    int64_t pad;
+};
+
+// Workspace: the CTAs' starts, then the pieces' (m, l) pairs [2 CTAs][heads], then
+// their outputs [2 CTAs][heads][D].
+__host__ __device__ inline int64_t decode_ml_offset(const DecodeShape& s)
 {
-    return ((int64_t)(N + 1) * 8 + 255) / 256 * 256;
+    return ((int64_t)s.ctas * sizeof(DecodeStart) + 255) / 256 * 256;
 }
-__host__ __device__ inline int64_t decode_o_offset(int32_t N, const DecodeShape& s)
+__host__ __device__ inline int64_t decode_o_offset(const DecodeShape& s)
 {
-    return decode_ml_offset(N) + ((int64_t)2 * s.ctas * s.heads * 8 + 255) / 256 * 256;
+    return decode_ml_offset(s) + ((int64_t)2 * s.ctas * s.heads * 8 + 255) / 256 * 256;
+}
+inline int64_t decode_workspace(const DecodeShape& s, int32_t D)
+{
+    return decode_o_offset(s) + (int64_t)2 * s.ctas * s.heads * D * 4;
 }
 
 __device__ __forceinline__ int32_t decode_len(const DecodeArgs& a, int32_t n)
@@ -49,11 +60,11 @@ struct DecodeRange {
     int32_t n;            // request of tile `begin`
 };
 
-// Called by NT threads of a CTA (a multiple of 32): where the CTA's tiles lie.
-// CTA 0 also stores the prefix of tiles for the join.
+// Called by NT threads of a CTA (a multiple of 32): where the CTA's tiles lie.  It also
+// leaves the CTA's start for the join; CTA 0 reports bad lengths.
 template <int NT>
 __device__ __forceinline__ DecodeRange decode_range(const DecodeArgs& a, const DecodeShape& s,
-                                                    int64_t* prefix_out)
+                                                    void* workspace)
 {
     __shared__ int64_t sums[NT / 32];
     __shared__ DecodeRange range;
@@ -69,7 +80,6 @@ __device__ __forceinline__ DecodeRange decode_range(const DecodeArgs& a, const D
         if (lane >= o) upto += y;
     }
     if (lane == 31) sums[warp] = upto;
-    if (tid == 0) range.n = a.N;
     __syncthreads();
     int64_t total = 0, before = upto - mine;
 #pragma unroll
@@ -90,17 +100,15 @@ __device__ __forceinline__ DecodeRange decode_range(const DecodeArgs& a, const D
         }
         range.n = n;
         range.at = at * s.units;
+        const int32_t tiles = tiles_of(decode_len(a, n), s.tile_shift);
+        const int64_t in = begin - range.at;
+        static_cast<DecodeStart*>(workspace)[b] = {n, (int32_t)(in / tiles), (int32_t)(in % tiles),
+                                                   tiles, W, 0};
     }
-    if (blockIdx.x == 0) {
-        int64_t at = before;
-        for (int32_t n = n0; n < n1; ++n) {
-            prefix_out[n] = at;
-            at += tiles_of(decode_len(a, n), s.tile_shift);
-        }
-        if (tid == 0) prefix_out[a.N] = total;
+    if (tid == 0 && begin >= end) static_cast<DecodeStart*>(workspace)[b] = {0, 0, 0, 0, W, 0};
+    if (blockIdx.x == 0)
         for (int32_t n = n0; n < n1; ++n)
             if (a.seq_lens[n] != decode_len(a, n)) report_status(a.status, KDA_ERR_DEVICE_ARG);
-    }
     __syncthreads();
     DecodeRange r = range;
     r.begin = begin;

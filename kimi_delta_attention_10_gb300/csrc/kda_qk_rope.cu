@@ -601,8 +601,10 @@ cudaError_t launch_bwd(const RopeArgs& a, cudaStream_t stream)
         qk_rope_bwd_kernel<TIn, TDy, TOut, D, false><<<(unsigned)blocks, NT, 0, stream>>>(a, slices);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && a.norm && (a.q_wgrad != nullptr || a.k_wgrad != nullptr)) {
-        e = launch_after(dw_sum_kernel, 2 * D / 32, 1024, stream, a.partials, (int)blocks, D,
-                         a.q_wgrad, a.k_wgrad);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * D / 32);
+        cfg.blockDim = dim3(1024);
+        e = launch_after(dw_sum_kernel, cfg, stream, a.partials, (int)blocks, D, a.q_wgrad, a.k_wgrad);
     }
     return e;
 }
