@@ -296,16 +296,17 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
     }
 }
 
-// Joins the split rows.  Block (b, y) looks at the row that CTA b's tiles begin inside
-// of: where that is the row's first split, it joins the pieces of every gridDim.y-th
-// head from y, in the CTAs' order; most blocks find nothing to do.  A block's threads
-// take four channels of a piece each, several pieces side by side, so that even a row
-// split over all CTAs is some twenty loads deep.  Empty requests' rows are dealt to
-// all blocks.
+// Joins the split rows.  Block (b, y) joins the row whose first split is where CTA b's
+// tiles begin, every gridDim.y-th head from y; most blocks find nothing to do.  Four
+// channels a lane; the block's groups of D / 4 lanes take a head each, or, where the
+// row has many pieces, share the pieces of one head, so that even a row split over all
+// CTAs is some twenty loads deep.  Pieces are added in the CTAs' order.  Empty
+// requests' rows are dealt to all blocks.
 template <int D>
 __global__ void __launch_bounds__(kJoin) decode_join_kernel(DecodeArgs a, DecodeShape sh)
 {
-    constexpr int LANES = D / 4, P = kJoin / LANES;        // threads per piece, pieces side by side
+    constexpr int LANES = D / 4, P = kJoin / LANES;        // lanes of a group, groups
+    constexpr int kMany = 4;                               // pieces from which groups share a head
     __shared__ float4 s_x[P][LANES];
     __shared__ float s_l[P];
     const int ch = (threadIdx.x % LANES) * 4, part = threadIdx.x / LANES;
@@ -326,50 +327,53 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(DecodeArgs a, Decode
     }
     wait_for_previous();
     const char* ws = static_cast<const char*>(a.workspace);
-    const DecodeStart st = reinterpret_cast<const DecodeStart*>(ws)[blockIdx.x];
-    if (st.tile0 == 0) return;                             // nothing, or a row's own beginning
+    const DecodeSplit st = reinterpret_cast<const DecodeSplit*>(ws)[blockIdx.x];
+    const int pieces = st.last - st.first + 1;
+    if (pieces <= 0) return;
     const float2* ws_ml = reinterpret_cast<const float2*>(ws + decode_ml_offset(sh));
     const float* ws_o = reinterpret_cast<const float*>(ws + decode_o_offset(sh));
-    const int64_t B = st.W < sh.ctas ? st.W : sh.ctas;
-    const int64_t first = blockIdx.x * st.W / B - st.tile0, last = first + st.tiles - 1;
-    // the CTA of tile x: the last b with b W / B <= x
-    const int64_t b0 = ((first + 1) * B - 1) / st.W, b1 = ((last + 1) * B - 1) / st.W;
-    if (b0 + 1 != blockIdx.x) return;                      // an earlier split joins the row
     const int G = a.Hq / a.Hk, groups = sh.units / a.Hk;
     const int hk = st.u / groups, g0 = (st.u - hk * groups) * sh.heads;
     const int heads = min(sh.heads, G - g0);
-    for (int g = blockIdx.y; g < heads; g += gridDim.y) {
-        float top = -CUDART_INF_F;
-#pragma unroll 4
-        for (int64_t b = b0; b <= b1; ++b)
-            top = fmaxf(top, ws_ml[(2 * b + (b == b0)) * sh.heads + g].x);
+    const bool share = pieces >= kMany;
+    const int stride = share ? P : 1, first = share ? part : 0;
+    for (int gb = share ? blockIdx.y : blockIdx.y * P; gb < heads;
+         gb += share ? gridDim.y : gridDim.y * P) {
+        const int g = share ? gb : gb + part;
+        // piece i: the row begins in the first CTA's tiles
+        auto piece = [&](int i) { return (2 * (int64_t)(st.first + i) + (i == 0)) * sh.heads + g; };
+        float top = -CUDART_INF_F, l = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-        if (top != -CUDART_INF_F) {
+        if (g < heads) {
+#pragma unroll 8
+            for (int i = 0; i < pieces; ++i) top = fmaxf(top, ws_ml[piece(i)].x);
+            if (top != -CUDART_INF_F) {
 #pragma unroll 4
-            for (int64_t b = b0 + part; b <= b1; b += P) {
-                const int64_t i = (2 * b + (b == b0)) * sh.heads + g;   // the row begins in b0's tiles
-                const float2 ml = ws_ml[i];
-                const float4 o = *reinterpret_cast<const float4*>(ws_o + i * D + ch);
-                const float keep = exp2f(ml.x - top);
-                l = fmaf(ml.y, keep, l);
-                x.x = fmaf(o.x, keep, x.x);
-                x.y = fmaf(o.y, keep, x.y);
-                x.z = fmaf(o.z, keep, x.z);
-                x.w = fmaf(o.w, keep, x.w);
+                for (int i = first; i < pieces; i += stride) {
+                    const float2 ml = ws_ml[piece(i)];
+                    const float4 o = *reinterpret_cast<const float4*>(ws_o + piece(i) * D + ch);
+                    const float keep = exp2f(ml.x - top);
+                    l = fmaf(ml.y, keep, l);
+                    x.x = fmaf(o.x, keep, x.x);
+                    x.y = fmaf(o.y, keep, x.y);
+                    x.z = fmaf(o.z, keep, x.z);
+                    x.w = fmaf(o.w, keep, x.w);
+                }
             }
         }
-        __syncthreads();                                   // the last head's sums are read
-        s_x[part][ch / 4] = x;
-        if (ch == 0) s_l[part] = l;
-        __syncthreads();
-        if (part != 0) continue;
-        const int pieces = (int)min((int64_t)P, b1 - b0 + 1);
-        for (int i = 1; i < pieces; ++i) {
-            const float4 o = s_x[i][ch / 4];
-            x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
-            l += s_l[i];
+        if (share) {
+            __syncthreads();                               // the last head's sums are read
+            s_x[part][ch / 4] = x;
+            if (ch == 0) s_l[part] = l;
+            __syncthreads();
+            if (part != 0) continue;
+            for (int i = 1; i < min(P, pieces); ++i) {
+                const float4 o = s_x[i][ch / 4];
+                x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
+                l += s_l[i];
+            }
         }
+        if (g >= heads) continue;
         const float inv = 1.f / l;
         const int64_t r = (int64_t)st.n * a.Hq + hk * G + g0 + g;
         store(r, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
@@ -429,7 +433,10 @@ cudaError_t launch_fp32(const DecodeArgs& a, const DecodeShape& s, cudaStream_t 
 cudaError_t launch_decode_join(const DecodeArgs& a, const DecodeShape& s, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)s.ctas, (unsigned)(s.heads < 8 ? s.heads : 8));
+    // many blocks for a head's pieces each only where rows are few and the pieces many
+    const int64_t rows = (int64_t)a.N * s.units;
+    const int heads = s.heads < 8 ? s.heads : 8;
+    cfg.gridDim = dim3((unsigned)s.ctas, (unsigned)(rows * 2 < s.ctas ? heads : heads < 2 ? 1 : 2));
     cfg.blockDim = dim3(kJoin);
     return launch_after(a.D == 64 ? decode_join_kernel<64> : decode_join_kernel<128>, cfg, stream, a,
                         s);

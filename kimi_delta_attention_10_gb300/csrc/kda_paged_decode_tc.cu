@@ -125,9 +125,10 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
     extern __shared__ unsigned char raw[];
     unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     Bars& bar = *reinterpret_cast<Bars*>(sm + C::OFF_MISC);
-    float* s_max = reinterpret_cast<float*>(sm + C::OFF_MISC + 512);     // [2][NWG][4][HW]
+    float* s_max = reinterpret_cast<float*>(sm + C::OFF_MISC + 256);     // [2][NWG][4][HW]
     float* s_sum = s_max + 2 * 4 * HP;                                   // [4][HP]
-    static_assert(sizeof(Bars) <= 512 && 512 + 12 * HP * 4 <= C::MISC, "misc region");
+    float* s_inv = s_sum + 4 * HP;                                       // [HP]
+    static_assert(sizeof(Bars) <= 256 && 256 + 13 * HP * 4 <= C::MISC, "misc region");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.Hq / a.Hk, groups = sh.units / a.Hk;
 
@@ -256,12 +257,13 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                         if (t + 1 == w.tile1) commit(&bar.qempty[qb]);
                         commit(&bar.sfull[b]);
                     }
-                    if (i > 0) product_with_v(i - 1);
+                    if (t > w.tile0) product_with_v(i - 1);
                     begins = t == w.tile0;
                 }
+                // the row's last product before the next row's keys are waited for
+                product_with_v(i - 1);
                 ++item;
             }
-            if (i > 0) product_with_v(i - 1);
             commit(&bar.drain);                            // no MMA outlives the loop
             mbar_wait(&bar.drain, 0);
         }
@@ -413,40 +415,59 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
 #pragma unroll
                 for (int g = 0; g < HW; ++g) acc[g] += x[g];
             }
-            // the sums of all tokens' weights
+            // the sums of all tokens' weights: each step halves the heads a lane sums
 #pragma unroll
-            for (int g = 0; g < HW; ++g) {
+            for (int n = HW, o = 16; o > 0; o >>= 1) {
+                if (n > 1) {
+                    n >>= 1;
+                    const bool up = lane & o;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], o);
-                if (lane == 0) s_sum[quad * HP + wg * HW + g] = l[g];
+                    for (int g = 0; g < n; ++g) {
+                        const float give = up ? l[g] : l[g + n], take = up ? l[g + n] : l[g];
+                        l[g] = take + __shfl_xor_sync(0xffffffffu, give, o);
+                    }
+                } else {
+                    l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+                }
             }
+            // lane 32 / HW * g has head g's (bits from the top)
+            constexpr int EACH = 32 / HW;
+            if (lane % EACH == 0) s_sum[quad * HP + wg * HW + lane / EACH] = l[0];
             named_sync(bar_id, 128);
             const int hk = w.u / groups, g0 = (w.u - hk * groups) * HP + wg * HW;
             const bool whole = w.tile0 == 0 && w.tile1 == w.tiles;
             const int64_t r0 = whole ? (int64_t)w.n * a.Hq + hk * G + g0
                                      : (2 * (int64_t)blockIdx.x + (w.tile0 == 0)) * HP + wg * HW;
+            const int heads = min(HW, G - g0);
+            // thread g finishes head g's statistics
+            float inv = 0.f;
+            if (row < heads) {
+                const float* sp = s_sum + wg * HW + row;
+                const float sum = sp[0] + sp[HP] + sp[2 * HP] + sp[3 * HP];
+                float m = ref[0];
+#pragma unroll
+                for (int g = 1; g < HW; ++g) m = row == g ? ref[g] : m;
+                if (!whole)
+                    ws_ml[r0 + row] = make_float2(m, sum);
+                else if (a.lse != nullptr)
+                    a.lse[r0 + row] = m * kLn2 + logf(sum);
+                inv = whole ? 1.f / sum : 1.f;
+                s_inv[wg * HW + row] = inv;
+            }
+            named_sync(bar_id, 128);
             // D = 64: a warp's tensor-memory lanes 0 .. 15 hold channels 16 quad ..
             const int ch = D == 128 ? row : 16 * quad + lane;
             const bool mine = D == 128 || lane < 16;
+            if (whole && a.out_bf16) {
+                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.out) + r0 * D + ch;
 #pragma unroll
-            for (int g = 0; g < HW; ++g) {
-                if (g0 + g >= G) break;
-                const float* sp = s_sum + wg * HW + g;
-                const float sum = sp[0] + sp[HP] + sp[2 * HP] + sp[3 * HP];
-                const int64_t r = r0 + g;
-                if (whole) {
-                    if (mine) {
-                        const float y = acc[g] / sum;
-                        if (a.out_bf16)
-                            store_one(static_cast<__nv_bfloat16*>(a.out) + r * D + ch, y);
-                        else
-                            store_one(static_cast<float*>(a.out) + r * D + ch, y);
-                    }
-                    if (row == 0 && a.lse != nullptr) a.lse[r] = ref[g] * kLn2 + logf(sum);
-                } else {
-                    if (mine) ws_o[r * D + ch] = acc[g];
-                    if (row == 0) ws_ml[r] = make_float2(ref[g], sum);
-                }
+                for (int g = 0; g < HW; ++g)
+                    if (mine && g < heads) store_one(y + g * D, acc[g] * s_inv[wg * HW + g]);
+            } else {
+                float* y = (whole ? static_cast<float*>(a.out) : ws_o) + r0 * D + ch;
+#pragma unroll
+                for (int g = 0; g < HW; ++g)
+                    if (mine && g < heads) y[g * D] = acc[g] * s_inv[wg * HW + g];
             }
         }
     }

@@ -1,10 +1,12 @@
-// How the decode attention's work is dealt out, shared by its kernels and the
-// join: every (request, head unit) row of `tiles` tiles lies on one axis of
-// W = units * sum_n tiles_n tiles, ordered by request, unit, tile; CTA b of
-// B = min(CTAs, W) takes the tiles [b W / B, (b + 1) W / B), at least one.  A row that a CTA covers whole is
-// finished there; of a split row each CTA leaves a piece (maximum, sum, unscaled
-// output) in one of its two slots: slot 2 b where the row began before the CTA's
-// tiles, 2 b + 1 where it begins in them.  A CTA has at most one of each.
+// How the decode attention's work is dealt out, shared by its kernels and the join:
+// every (request, head unit) row of `tiles` tiles lies on one axis of
+// W = units * sum_n (tiles_n + kStart) places, ordered by request, unit, tile; each row
+// begins with kStart places without a tile, which stand for the time that starting and
+// ending a row costs.  CTA b of B = min(CTAs, W) takes W / B places, the first W % B
+// CTAs one more.  A row whose tiles a CTA covers whole is finished there; of a split row
+// each CTA leaves a piece (maximum, sum, unscaled output) in one of its two slots: slot
+// 2 b where the row's tiles began before the CTA's, 2 b + 1 where they begin in them.
+// A CTA has at most one of each.
 #pragma once
 
 #include <stdint.h>
@@ -20,18 +22,19 @@ struct DecodeShape {
     int32_t tile_shift;   // log2 of the tokens per tile
 };
 
-// Where a CTA's tiles begin; the join starts from these.
-struct alignas(16) DecodeStart {
-    int32_t n, u, tile0, tiles;        // request, unit, the first tile's index in its row, the row's tiles
-    int64_t W;
-    int64_t pad;
+constexpr int kStart = 1;             // a row's places without a tile
+
+// The split row that a CTA's tiles begin inside of, for the join: its request and unit,
+// and the CTAs of its first and last tile (last < first: none, or not its first split).
+struct alignas(16) DecodeSplit {
+    int32_t n, u, first, last;
 };
 
-// Workspace: the CTAs' starts, then the pieces' (m, l) pairs [2 CTAs][heads], then
+// Workspace: the CTAs' splits, then the pieces' (m, l) pairs [2 CTAs][heads], then
 // their outputs [2 CTAs][heads][D].
 __host__ __device__ inline int64_t decode_ml_offset(const DecodeShape& s)
 {
-    return ((int64_t)s.ctas * sizeof(DecodeStart) + 255) / 256 * 256;
+    return ((int64_t)s.ctas * sizeof(DecodeSplit) + 255) / 256 * 256;
 }
 __host__ __device__ inline int64_t decode_o_offset(const DecodeShape& s)
 {
@@ -54,14 +57,21 @@ __device__ __forceinline__ int32_t tiles_of(int32_t L, int shift)
     return (int32_t)(((int64_t)L + (1 << shift) - 1) >> shift);
 }
 
+// a / b for a >= 0, b > 0; the 64-bit division is a call of a hundred instructions.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
 struct DecodeRange {
-    int64_t begin, end;   // the CTA's tiles
-    int64_t at;           // tiles of the requests before `n`, all units
-    int32_t n;            // request of tile `begin`
+    int64_t begin, end;   // the CTA's places
+    int64_t at;           // places of the requests before `n`, all units
+    int32_t n;            // request of place `begin`
 };
 
-// Called by NT threads of a CTA (a multiple of 32): where the CTA's tiles lie.  It also
-// leaves the CTA's start for the join; CTA 0 reports bad lengths.
+// Called by NT threads of a CTA (a multiple of 32): where the CTA's places lie.  It also
+// leaves the CTA's split for the join; CTA 0 reports bad lengths.
 template <int NT>
 __device__ __forceinline__ DecodeRange decode_range(const DecodeArgs& a, const DecodeShape& s,
                                                     void* workspace)
@@ -71,8 +81,12 @@ __device__ __forceinline__ DecodeRange decode_range(const DecodeArgs& a, const D
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t per = (a.N + NT - 1) / NT;         // consecutive requests per thread
     const int32_t n0 = min(tid * per, a.N), n1 = min(n0 + per, a.N);
+    auto places = [&](int32_t n) {
+        const int32_t tiles = tiles_of(decode_len(a, n), s.tile_shift);
+        return tiles ? tiles + kStart : 0;           // an empty request has no row
+    };
     int64_t mine = 0;
-    for (int32_t n = n0; n < n1; ++n) mine += tiles_of(decode_len(a, n), s.tile_shift);
+    for (int32_t n = n0; n < n1; ++n) mine += places(n);
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -87,26 +101,42 @@ __device__ __forceinline__ DecodeRange decode_range(const DecodeArgs& a, const D
         if (w < warp) before += sums[w];
         total += sums[w];
     }
-    const int64_t W = total * s.units;
-    const int64_t B = W < s.ctas ? W : s.ctas, b = blockIdx.x;
-    const int64_t begin = b < B ? b * W / B : 0, end = b < B ? (b + 1) * W / B : 0;
-    if (begin < end && before * s.units <= begin && begin < (before + mine) * s.units) {
-        int64_t at = before;
-        int32_t n = n0;
-        for (;; ++n) {
-            const int64_t next = at + tiles_of(decode_len(a, n), s.tile_shift);
-            if (begin < next * s.units) break;
-            at = next;
+    const int64_t W = total * s.units, b = blockIdx.x;
+    const int64_t B = W < s.ctas ? W : s.ctas;
+    int64_t begin = 0, end = 0;
+    if (b < B) {
+        const int64_t share = quotient(W, B), more = W - share * B;
+        begin = b * share + min(b, more);
+        end = begin + share + (b < more);
+        if (before * s.units <= begin && begin < (before + mine) * s.units) {
+            int64_t at = before;
+            int32_t n = n0;
+            for (;; ++n) {
+                const int64_t next = at + places(n);
+                if (begin < next * s.units) break;
+                at = next;
+            }
+            range.n = n;
+            range.at = at * s.units;
+            // the row of place `begin`, and the CTAs of its first and last tile
+            const int32_t p = places(n);
+            const int32_t u = (int32_t)quotient(begin - range.at, p);
+            const int64_t tile = range.at + (int64_t)u * p + kStart, last = tile + p - kStart - 1;
+            auto cta_of = [&](int64_t x) {
+                const int64_t edge = more * (share + 1);
+                return (int32_t)(x < edge ? quotient(x, share + 1) : more + quotient(x - edge, share));
+            };
+            DecodeSplit split = {n, u, 0, -1};
+            if (tile < begin && cta_of(tile) + 1 == b) {
+                split.first = (int32_t)b - 1;
+                split.last = cta_of(last);
+            }
+            static_cast<DecodeSplit*>(workspace)[b] = split;
         }
-        range.n = n;
-        range.at = at * s.units;
-        const int32_t tiles = tiles_of(decode_len(a, n), s.tile_shift);
-        const int64_t in = begin - range.at;
-        static_cast<DecodeStart*>(workspace)[b] = {n, (int32_t)(in / tiles), (int32_t)(in % tiles),
-                                                   tiles, W, 0};
+    } else if (tid == 0) {
+        static_cast<DecodeSplit*>(workspace)[b] = {0, 0, 0, -1};
     }
-    if (tid == 0 && begin >= end) static_cast<DecodeStart*>(workspace)[b] = {0, 0, 0, 0, W, 0};
-    if (blockIdx.x == 0)
+    if (b == 0)
         for (int32_t n = n0; n < n1; ++n)
             if (a.seq_lens[n] != decode_len(a, n)) report_status(a.status, KDA_ERR_DEVICE_ARG);
     __syncthreads();

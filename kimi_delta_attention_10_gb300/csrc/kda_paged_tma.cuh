@@ -34,22 +34,27 @@ struct DecodeWalk {
     int64_t pos, end, at;
     int32_t n, u, tile0, tile1, tiles, L;
     __device__ __forceinline__ explicit DecodeWalk(const DecodeRange& r)
-        : pos(r.begin), end(r.end), at(r.at), n(r.n), tile0(0), tile1(0) {}
+        : pos(r.begin), end(r.end), at(r.at), n(r.n), u(0), tile0(0), tile1(0), tiles(0), L(0) {}
+    // The next row with tiles tile0 .. tile1 - 1 (at least one) of this CTA.
     __device__ __forceinline__ bool next(const DecodeArgs& a, const DecodeShape& sh)
     {
-        pos += tile1 - tile0;
-        if (pos >= end) return false;
-        for (;; ++n) {
-            L = decode_len(a, n);
-            tiles = tiles_of(L, sh.tile_shift);
-            const int64_t all = (int64_t)tiles * sh.units;
-            if (pos < at + all) break;
-            at += all;
+        while (pos < end) {
+            for (;; ++n) {
+                L = decode_len(a, n);
+                tiles = tiles_of(L, sh.tile_shift);
+                const int64_t all = tiles ? (int64_t)(tiles + kStart) * sh.units : 0;
+                if (pos < at + all) break;
+                at += all;
+            }
+            const int32_t places = tiles + kStart;
+            u = (int32_t)quotient(pos - at, places);
+            const int64_t row = at + (int64_t)u * places;      // the row's first place
+            tile0 = max((int32_t)(pos - row) - kStart, 0);
+            pos = min(end, row + places);
+            tile1 = (int32_t)(pos - row) - kStart;
+            if (tile1 > tile0) return true;
         }
-        u = (int32_t)((pos - at) / tiles);
-        tile0 = (int32_t)(pos - at - (int64_t)u * tiles);
-        tile1 = (int32_t)min((int64_t)tiles, tile0 + (end - pos));
-        return true;
+        return false;
     }
 };
 
