@@ -733,8 +733,10 @@ def kda_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor,
     handle = _stream_handle(stream, dev)
     ws, ws_bytes = None, 0
     if qk_norm and (q_weight is not None or k_weight is not None):
-        wq, wk = torch.empty((2, D), dtype=_FP32, device=dev).unbind(0)
-        wq, wk = wq if q_weight is not None else None, wk if k_weight is not None else None
+        if q_weight is not None:
+            wq = torch.empty(D, dtype=_FP32, device=dev)
+        if k_weight is not None:
+            wk = torch.empty(D, dtype=_FP32, device=dev)
         if workspace is None:
             ws_bytes = qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D)
             ws = _own_scratch(ws_bytes, dev, stream, handle)

@@ -393,6 +393,7 @@ DecodeShape fp32_shape(const DecodeArgs& a)
     s.units = a.Hk * ((G + s.heads - 1) / s.heads);
     s.ctas = sm_count();
     s.tile_shift = a.D == 128 ? 5 : 6;
+    s.start = 3;
     return s;
 }
 

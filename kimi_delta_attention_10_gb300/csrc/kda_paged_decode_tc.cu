@@ -518,6 +518,7 @@ DecodeShape decode_tc_shape(const DecodeArgs& a)
     s.units = a.Hk * ((G + hp - 1) / hp);
     s.ctas = sm_count() * (a.D == 64 && hp <= 32 ? 2 : 1);
     s.tile_shift = kTileShift;
+    s.start = 1;
     return s;
 }
 

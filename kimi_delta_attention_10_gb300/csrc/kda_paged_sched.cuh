@@ -1,7 +1,7 @@
 // How the decode attention's work is dealt out, shared by its kernels and the join:
 // every (request, head unit) row of `tiles` tiles lies on one axis of
-// W = units * sum_n (tiles_n + kStart) places, ordered by request, unit, tile; each row
-// begins with kStart places without a tile, which stand for the time that starting and
+// W = units * sum_n (tiles_n + start) places, ordered by request, unit, tile; each row
+// begins with `start` places without a tile, which stand for the time that starting and
 // ending a row costs.  CTA b of B = min(CTAs, W) takes W / B places, the first W % B
 // CTAs one more.  A row whose tiles a CTA covers whole is finished there; of a split row
 // each CTA leaves a piece (maximum, sum, unscaled output) in one of its two slots: slot
@@ -20,9 +20,10 @@ struct DecodeShape {
     int32_t heads;        // query heads per unit (the last of a group may have fewer)
     int32_t ctas;         // CTAs launched
     int32_t tile_shift;   // log2 of the tokens per tile
+    int32_t start;        // places without a tile at the beginning of a row
 };
 
-constexpr int kStart = 1;             // a row's places without a tile
+
 
 // The split row that a CTA's tiles begin inside of, for the join: its request and unit,
 // and the CTAs of its first and last tile (last < first: none, or not its first split).
@@ -83,7 +84,7 @@ __device__ __forceinline__ DecodeRange decode_range(const DecodeArgs& a, const D
     const int32_t n0 = min(tid * per, a.N), n1 = min(n0 + per, a.N);
     auto places = [&](int32_t n) {
         const int32_t tiles = tiles_of(decode_len(a, n), s.tile_shift);
-        return tiles ? tiles + kStart : 0;           // an empty request has no row
+        return tiles ? tiles + s.start : 0;           // an empty request has no row
     };
     int64_t mine = 0;
     for (int32_t n = n0; n < n1; ++n) mine += places(n);
@@ -121,7 +122,7 @@ __device__ __forceinline__ DecodeRange decode_range(const DecodeArgs& a, const D
             // the row of place `begin`, and the CTAs of its first and last tile
             const int32_t p = places(n);
             const int32_t u = (int32_t)quotient(begin - range.at, p);
-            const int64_t tile = range.at + (int64_t)u * p + kStart, last = tile + p - kStart - 1;
+            const int64_t tile = range.at + (int64_t)u * p + s.start, last = tile + p - s.start - 1;
             auto cta_of = [&](int64_t x) {
                 const int64_t edge = more * (share + 1);
                 return (int32_t)(x < edge ? quotient(x, share + 1) : more + quotient(x - edge, share));

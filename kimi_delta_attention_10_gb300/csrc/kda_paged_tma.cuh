@@ -42,16 +42,16 @@ struct DecodeWalk {
             for (;; ++n) {
                 L = decode_len(a, n);
                 tiles = tiles_of(L, sh.tile_shift);
-                const int64_t all = tiles ? (int64_t)(tiles + kStart) * sh.units : 0;
+                const int64_t all = tiles ? (int64_t)(tiles + sh.start) * sh.units : 0;
                 if (pos < at + all) break;
                 at += all;
             }
-            const int32_t places = tiles + kStart;
+            const int32_t places = tiles + sh.start;
             u = (int32_t)quotient(pos - at, places);
             const int64_t row = at + (int64_t)u * places;      // the row's first place
-            tile0 = max((int32_t)(pos - row) - kStart, 0);
+            tile0 = max((int32_t)(pos - row) - sh.start, 0);
             pos = min(end, row + places);
-            tile1 = (int32_t)(pos - row) - kStart;
+            tile1 = (int32_t)(pos - row) - sh.start;
             if (tile1 > tile0) return true;
         }
         return false;
