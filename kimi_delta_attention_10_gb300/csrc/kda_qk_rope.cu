@@ -12,13 +12,14 @@
 // so a warp holds 1, 2 or 4 rows.  Each warp works alone: it takes one token,
 // computes that token's cosines and sines once (two angles a lane, exchanged
 // through 512 bytes of its own shared memory), keeps its lanes' C and S in
-// registers, and runs over the token's heads with kRows rows in flight and the
-// next kRows requested before these are worked on; the first are requested before
-// the angles.  With few tokens a token's heads are dealt to several warps
-// ("slices"), each of which recomputes the angles: that costs less than leaving
-// SMs idle.  At 23 bytes per clock and SM a warp has about 170 issue slots per
-// step of 512 bytes in and out, so the arithmetic is in pairs (f32x2) and the
-// partner channels are exchanged as loaded, before they are unpacked.
+// registers, and runs over the token's heads.  Rows come through a ring of four
+// asynchronous copies per warp (the first are under way before the angles are
+// computed): 32 warps keep 48 KB of an SM in flight without a register, and the
+// partner channels of the half layout are one more read of the ring instead of four
+// shuffles.  At 23 bytes per clock and SM a warp has about 170 issue slots per step
+// of 512 bytes in and out, so the arithmetic is in pairs (f32x2).  With few tokens a
+// token's heads are dealt to several warps ("slices"), each of which recomputes the
+// angles: that costs less than leaving SMs idle.
 //
 // Angles: position * inv_freq can be 10^6 radians, where FP32 has lost 0.06.
 // The frequency is turned into turns per position as a 64-bit binary fraction
@@ -30,6 +31,7 @@
 #include <stdint.h>
 
 #include "kda_paged.cuh"
+#include "kda_tc.cuh"
 
 namespace kda {
 namespace {
@@ -37,7 +39,6 @@ namespace {
 constexpr int NT = 256;
 constexpr int NW = NT / 32;
 constexpr int kMaxPairs = 64;          // rot_dim / 2
-constexpr int kRows = 2;               // rows per warp step and lane
 
 template <typename T, int D> struct Layout {
     static constexpr int VEC = 16 / (int)sizeof(T);
@@ -101,11 +102,6 @@ template <int N> __device__ __forceinline__ void store2(__nv_bfloat16* p, const 
         *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y));
 }
 
-template <typename T> __device__ __forceinline__ uint4 load16(const T* p)
-{
-    return *reinterpret_cast<const uint4*>(p);
-}
-
 template <int LPR> __device__ __forceinline__ float row_sum(float x)
 {
 #pragma unroll
@@ -113,21 +109,30 @@ template <int LPR> __device__ __forceinline__ float row_sum(float x)
     return x;
 }
 
-// The values of the other channels of this lane's pairs, from what its lanes loaded.
+__device__ __forceinline__ uint4 lds16(const unsigned char* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// The values of the other channels of this lane's pairs: its own, swapped, or the
+// partner lane's, at `other` in the ring.
 template <bool kInter, int N>
-__device__ __forceinline__ void partners(uint4 u, const float2 (&f)[N], int lane, float2 (&o)[N])
+__device__ __forceinline__ void partners(const float2 (&f)[N], const unsigned char* other, float2 (&o)[N])
 {
     if constexpr (kInter) {
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = make_float2(f[i].y, f[i].x);
     } else {
-        uint4 v;
-        v.x = __shfl_sync(0xffffffffu, u.x, lane);
-        v.y = __shfl_sync(0xffffffffu, u.y, lane);
-        v.z = __shfl_sync(0xffffffffu, u.z, lane);
-        v.w = __shfl_sync(0xffffffffu, u.w, lane);
-        unpack2<N>(v, o);
+        unpack2<N>(lds16(other), o);
     }
+}
+
+template <int N> __device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async8(void* dst, const void* src, bool valid)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(tc::smem_u32(dst)), "l"(src),
+                 "r"(valid ? 8 : 0)
+                 : "memory");
 }
 
 // ---------------------------------------------------------------- angles
@@ -219,61 +224,70 @@ template <int D> __device__ __forceinline__ void block_weights(const RopeArgs& a
 }
 
 // ---------------------------------------------------------------- forward
+constexpr int kRing = 4;
+
 // items = T * slices; warp-item i: token i / slices, rows of slice i % slices of
 // the q heads, then of the k heads, then (append) of the v heads.
 template <typename TIn, typename TOut, int D, bool kAppend, bool kInter>
-__global__ void __launch_bounds__(NT, 3) qk_rope_kernel(RopeArgs a, int slices)
+__global__ void __launch_bounds__(NT, 4) qk_rope_kernel(RopeArgs a, int slices)
 {
     using L = Layout<TIn, D>;
     constexpr int NP = L::VEC / 2;                         // pairs of values per lane
+    constexpr int kKinds = kAppend ? 3 : 2;
     __shared__ float2 table[NW][kMaxPairs];
     __shared__ float weights[2][D];
+    __shared__ __align__(16) unsigned char ring[NW][kRing][512];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane / L::LPR, chan = (lane % L::LPR) * L::VEC;
     const int partner = partner_lane(a, lane, chan, L::VEC);
     const int64_t items = (int64_t)a.T * slices, nwarps = (int64_t)gridDim.x * NW;
     const int step = slices * L::RPW;
-    constexpr int kKinds = kAppend ? 3 : 2;
     uint64_t f[2];
     bool ready = false;
     for (int64_t i = (int64_t)blockIdx.x * NW + warp;; i += nwarps) {
         // every warp of the block passes here once before its first item
         const bool any = i < items;
         const int64_t t = any ? (int64_t)((uint32_t)i / (uint32_t)slices) : 0;
-        const int top = any ? (int)(i - t * slices) * L::RPW : INT32_MAX;   // uniform in the warp
+        const int top = (int)(i - t * slices) * L::RPW;    // uniform in the warp
         const int32_t pos = any ? a.positions[t] : 0;
         int64_t slot = 0;
         if (kAppend && any) slot = a.slots[t];
-        const bool stored = !kAppend || (slot >= 0 && slot < a.num_slots);
-        const int kinds = stored ? kKinds : 1;
-        const TIn* src[kKinds];
-        src[0] = static_cast<const TIn*>(a.q) + t * a.q_stride;
-        src[1] = static_cast<const TIn*>(a.k) + t * a.k_stride;
-        if constexpr (kAppend) src[2] = static_cast<const TIn*>(a.v) + t * a.v_stride;
-        // the step's place: rows top + row, top + row + step, ... of kind `kind`
-        int kind = 0, row = 0;
+        const int64_t lane_off = (int64_t)(top + sub) * D + chan;
+        const TIn* src[3] = {static_cast<const TIn*>(a.q) + t * a.q_stride + lane_off,
+                             static_cast<const TIn*>(a.k) + t * a.k_stride + lane_off,
+                             kAppend ? static_cast<const TIn*>(a.v) + t * a.v_stride + lane_off : nullptr};
+        // the next copy: rows row .. of kind `want`
+        int want = 0, row = top;
+        const TIn* p = src[0];
         auto settle = [&] {
-            // the heads first: a slot is not waited for before q's rows are requested
-            while (top + row >= (kind == 0 ? a.Hq : a.Hk) && kind < kinds) {
-                ++kind;
-                row = 0;
+            if (want == 0 && row >= a.Hq) {
+                want = 1;
+                row = top;
+                p = src[1];
             }
-        };
-        auto request = [&](uint4 (&u)[kRows]) {
-            if (kind > 0 && kind >= kinds) return;
-            const TIn* x = kind == 0 ? src[0] : kind == 1 ? src[1] : src[kKinds - 1];
-            const int H = kind == 0 ? a.Hq : a.Hk;
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const int h = top + sub + row + r * step;
-                u[r] = make_uint4(0, 0, 0, 0);
-                if (h < H) u[r] = load16(x + (int64_t)h * D + chan);
+            if (want == 1 && row >= a.Hk) {
+                want = 2;
+                row = top;
+                p = src[2];
             }
+            if (want == 2 && (!kAppend || row >= a.Hk)) want = 3;
         };
-        uint4 next[kRows];
+        int put = 0;                                       // ring slot of the next copy
+        auto request = [&] {
+            if (want < 3) {
+                const bool valid = row + sub < (want == 0 ? a.Hq : a.Hk);
+                tc::cp_async16(&ring[warp][put][lane * 16], valid ? p : static_cast<const TIn*>(a.q), valid);
+                p += (int64_t)step * D;
+                row += step;
+                settle();
+            }
+            tc::cp_async_commit();
+            put = (put + 1) % kRing;
+        };
         if (any) {
             settle();
-            request(next);
+#pragma unroll
+            for (int k = 0; k < kRing - 1; ++k) request();
         }
         if (!ready) {
             lane_turns(a, lane, f);
@@ -281,55 +295,47 @@ __global__ void __launch_bounds__(NT, 3) qk_rope_kernel(RopeArgs a, int slices)
             ready = true;
         }
         if (!any) break;
-        if (kAppend && slot >= a.num_slots && lane == 0) report_status(a.status, KDA_ERR_DEVICE_ARG);
         warp_angles(a, f, table[warp], pos, lane);
+        const bool stored = !kAppend || (slot >= 0 && slot < a.num_slots);
+        if (kAppend && slot >= a.num_slots && lane == 0) report_status(a.status, KDA_ERR_DEVICE_ARG);
         int64_t paged = 0;                                 // the slot's row of head 0
         if (kAppend && stored) {
             const int64_t page = slot / a.page;
             paged = (page * a.Hk * a.page + (slot - page * a.page)) * D;
         }
-
-        float2 c[NP], s[NP];
-        int have = -1;                                     // the kind that c and s are for
-        while (kind < kinds) {
-            uint4 u[kRows];
+        int get = 0;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) u[r] = next[r];
-            const int now = kind, at = row;
-            row += kRows * step;
-            settle();
-            request(next);
-            if (now != have && now < 2) {
-                have = now;
+        for (int kind = 0; kind < kKinds; ++kind) {
+            const int H = kind == 0 ? a.Hq : a.Hk;
+            if (top >= H) continue;
+            const int64_t hstep = kAppend && kind > 0 ? (int64_t)a.page * D : D;
+            TOut* y = (kind == 0   ? static_cast<TOut*>(a.q_out) + t * a.Hq * D
+                       : !kAppend  ? static_cast<TOut*>(a.k_out) + t * a.Hk * D
+                       : kind == 1 ? static_cast<TOut*>(a.k_out) + paged
+                                   : static_cast<TOut*>(a.v_out) + paged) +
+                      (top + sub) * hstep + chan;
+            const int64_t jump = step * hstep;
+            float2 c[NP], s[NP];
+            if (kind < 2) {
 #pragma unroll
                 for (int j = 0; j < L::VEC; ++j) {
                     int o;
                     const float2 cs = channel_turn(a, table[warp], kInter, chan + j, &o);
-                    const float x = cs.x * weights[now][chan + j], y = cs.y * weights[now][o];
-                    if (j & 1) { c[j / 2].y = x; s[j / 2].y = y; }
-                    else { c[j / 2].x = x; s[j / 2].x = y; }
+                    const float x = cs.x * weights[kind][chan + j], z = cs.y * weights[kind][o];
+                    if (j & 1) { c[j / 2].y = x; s[j / 2].y = z; }
+                    else { c[j / 2].x = x; s[j / 2].x = z; }
                 }
             }
-            TOut* y;
-            int64_t hstep = D;
-            if (now == 0) {
-                y = static_cast<TOut*>(a.q_out) + t * a.Hq * D;
-            } else if (!kAppend) {
-                y = static_cast<TOut*>(a.k_out) + t * a.Hk * D;
-            } else {
-                y = static_cast<TOut*>(now == 1 ? a.k_out : a.v_out) + paged;
-                hstep = (int64_t)a.page * D;
-            }
-            const int H = now == 0 ? a.Hq : a.Hk;
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                if (top + at + r * step >= H) break;       // warp-uniform
-                const int h = top + sub + at + r * step;
+            for (int h = top; h < H; h += step, y += jump) {
+                copies_wait<kRing - 2>();
+                __syncwarp();                              // all lanes' parts; the last step's are read
+                const unsigned char* at = ring[warp][get];
                 float2 x[NP];
-                unpack2<NP>(u[r], x);
-                if (!kAppend || now < 2) {
+                unpack2<NP>(lds16(at + lane * 16), x);
+                if (kind < 2) {
                     float2 o[NP];
-                    partners<kInter, NP>(u[r], x, partner, o);
+                    partners<kInter, NP>(x, at + partner * 16, o);
+                    request();
                     float inv = 1.f;
                     if (a.norm) {
                         float2 ss = mul2(x[0], x[0]);
@@ -340,108 +346,19 @@ __global__ void __launch_bounds__(NT, 3) qk_rope_kernel(RopeArgs a, int slices)
 #pragma unroll
                     for (int j = 0; j < NP; ++j)
                         x[j] = mul2(fma2(o[j], s[j], mul2(x[j], c[j])), both(inv));
+                } else {
+                    request();
                 }
-                if (h < H) store2<NP>(y + h * hstep + chan, x);
+                get = (get + 1) % kRing;
+                if (h + sub < H && (kind == 0 || stored)) store2<NP>(y, x);
             }
         }
+        copies_wait<0>();
+        __syncwarp();
     }
 }
 
 // ---------------------------------------------------------------- backward
-// Rows of one kind of one token.
-template <typename TIn, typename TDy, typename TOut, int D, bool kInter>
-__device__ __forceinline__ void grad_rows(const RopeArgs& a, const TIn* x, const TDy* dy, TOut* dx,
-                                          int H, int top, int sub, int step, int chan, int partner,
-                                          const float* weights,
-                                          const float2 (&c)[Layout<TIn, D>::VEC / 2],
-                                          const float2 (&s)[Layout<TIn, D>::VEC / 2],
-                                          float2 (&dw)[Layout<TIn, D>::VEC / 2])
-{
-    using L = Layout<TIn, D>;
-    constexpr int VEC = L::VEC, NP = VEC / 2;
-    // 16-byte loads of dy per lane (8 bytes of one where dy is BF16 and x FP32)
-    constexpr int ND = VEC * (int)sizeof(TDy) >= 16 ? VEC * (int)sizeof(TDy) / 16 : 1;
-    constexpr int PV = 8 / (int)sizeof(TDy);               // pairs in 16 bytes of dy
-    float2 w[NP];
-#pragma unroll
-    for (int j = 0; j < NP; ++j) w[j] = make_float2(weights[chan + 2 * j], weights[chan + 2 * j + 1]);
-    auto request = [&](int at, uint4 (&u)[kRows], uint4 (&g)[kRows][ND]) {
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            const int h = top + sub + at + r * step;
-            u[r] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < ND; ++i) g[r][i] = make_uint4(0, 0, 0, 0);
-            if (h < H) {
-                u[r] = load16(x + (int64_t)h * D + chan);
-                const TDy* p = dy + (int64_t)h * D + chan;
-                if constexpr (VEC * sizeof(TDy) == 8) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(p);
-                    g[r][0].x = v.x;
-                    g[r][0].y = v.y;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < ND; ++i) g[r][i] = load16(p + i * (16 / (int)sizeof(TDy)));
-                }
-            }
-        }
-    };
-    uint4 un[kRows], gn[kRows][ND];
-    request(0, un, gn);
-    for (int at = 0; top + at < H; at += kRows * step) {
-        uint4 u[kRows], g[kRows][ND];
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            u[r] = un[r];
-#pragma unroll
-            for (int i = 0; i < ND; ++i) g[r][i] = gn[r][i];
-        }
-        request(at + kRows * step, un, gn);
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            if (top + at + r * step >= H) break;           // warp-uniform
-            const int h = top + sub + at + r * step;
-            float2 f[NP], d[NP], o[NP];
-            unpack2<NP>(u[r], f);
-#pragma unroll
-            for (int i = 0; i < ND; ++i) {
-                float2 part[PV], other[PV];
-                unpack2<PV>(g[r][i], part);
-                partners<kInter, PV>(g[r][i], part, partner, other);
-#pragma unroll
-                for (int j = 0; j < PV; ++j)
-                    if (i * PV + j < NP) {
-                        d[i * PV + j] = part[j];
-                        o[i * PV + j] = other[j];
-                    }
-            }
-            // the transposed rotation: s carries its signs
-#pragma unroll
-            for (int j = 0; j < NP; ++j) d[j] = fma2(o[j], s[j], mul2(d[j], c[j]));
-            if (a.norm) {
-                float2 ss = mul2(f[0], f[0]), hx = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int j = 1; j < NP; ++j) ss = fma2(f[j], f[j], ss);
-                float2 hw[NP];
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    hw[j] = mul2(d[j], w[j]);
-                    hx = fma2(hw[j], f[j], hx);
-                }
-                const float rstd = rsqrtf(row_sum<L::LPR>(ss.x + ss.y) * (1.f / D) + a.eps);
-                // n mean(h n) = x rstd^2 mean(h x)
-                const float m = row_sum<L::LPR>(hx.x + hx.y) * (1.f / D) * rstd * rstd;
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    dw[j] = fma2(mul2(f[j], both(rstd)), d[j], dw[j]);
-                    d[j] = mul2(fma2(f[j], both(-m), hw[j]), both(rstd));
-                }
-            }
-            if (h < H) store2<NP>(dx + (int64_t)h * D + chan, d);
-        }
-    }
-}
-
 // Sum of the CTA's dw over its warps and row groups, in a fixed order.
 template <int NP, int LPR, int D>
 __device__ __forceinline__ void block_dw(const float2 (&dw)[NP], float (*red)[D], float* out)
@@ -467,31 +384,92 @@ __device__ __forceinline__ void block_dw(const float2 (&dw)[NP], float (*red)[D]
     }
 }
 
+// A warp's ring of x and dy rows; DYB: bytes of dy a lane takes (8, 16 or 32).
+template <typename TIn, typename TDy, int D> struct BwdRing {
+    static constexpr int DYB = Layout<TIn, D>::VEC * (int)sizeof(TDy);
+    static constexpr int SLOTS = DYB == 32 ? 3 : 4;
+    static constexpr int BYTES = 512 + 32 * DYB;
+};
+
 template <typename TIn, typename TDy, typename TOut, int D, bool kInter>
 __global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int slices)
 {
     using L = Layout<TIn, D>;
-    constexpr int NP = L::VEC / 2;
+    using R = BwdRing<TIn, TDy, D>;
+    constexpr int NP = L::VEC / 2, DYB = R::DYB, S = R::SLOTS;
     __shared__ float2 table[NW][kMaxPairs];
     __shared__ float weights[2][D];
-    __shared__ float red[NW][D];
+    __shared__ __align__(16) unsigned char ring[NW][S][R::BYTES];
+    static_assert(sizeof(ring) >= NW * D * sizeof(float), "the sums of dw reuse the ring");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane / L::LPR, chan = (lane % L::LPR) * L::VEC;
     const int partner = partner_lane(a, lane, chan, L::VEC);
-    uint64_t f[2];
-    lane_turns(a, lane, f);
-    block_weights<D>(a, weights);
     const int64_t items = (int64_t)a.T * slices, nwarps = (int64_t)gridDim.x * NW;
     const int step = slices * L::RPW;
     let_next_start();
+    uint64_t f[2];
+    bool ready = false;
     float2 dwq[NP], dwk[NP];
 #pragma unroll
     for (int j = 0; j < NP; ++j) dwq[j] = dwk[j] = make_float2(0.f, 0.f);
-    for (int64_t i = (int64_t)blockIdx.x * NW + warp; i < items; i += nwarps) {
-        const int64_t t = (uint32_t)i / (uint32_t)slices;
+    for (int64_t i = (int64_t)blockIdx.x * NW + warp;; i += nwarps) {
+        const bool any = i < items;
+        const int64_t t = any ? (int64_t)((uint32_t)i / (uint32_t)slices) : 0;
         const int top = (int)(i - t * slices) * L::RPW;
-        warp_angles(a, f, table[warp], a.positions[t], lane);
-        float2 c[NP], s[NP];
+        const int32_t pos = any ? a.positions[t] : 0;
+        const int64_t lane_off = (int64_t)(top + sub) * D + chan;
+        const TIn* xq = static_cast<const TIn*>(a.q) + t * a.q_stride + lane_off;
+        const TIn* xk = static_cast<const TIn*>(a.k) + t * a.k_stride + lane_off;
+        const TDy* yq = static_cast<const TDy*>(a.dq) + t * a.Hq * D + lane_off;
+        const TDy* yk = static_cast<const TDy*>(a.dk) + t * a.Hk * D + lane_off;
+        int want = 0, row = top;
+        const TIn* px = xq;
+        const TDy* py = yq;
+        auto settle = [&] {
+            if (want == 0 && row >= a.Hq) {
+                want = 1;
+                row = top;
+                px = xk;
+                py = yk;
+            }
+            if (want == 1 && row >= a.Hk) want = 2;
+        };
+        int put = 0;
+        auto request = [&] {
+            if (want < 2) {
+                const bool valid = row + sub < (want == 0 ? a.Hq : a.Hk);
+                unsigned char* at = ring[warp][put];
+                tc::cp_async16(at + lane * 16, valid ? px : static_cast<const TIn*>(a.q), valid);
+                const TDy* from = valid ? py : static_cast<const TDy*>(a.dq);
+                if constexpr (DYB == 8) {
+                    cp_async8(at + 512 + lane * 8, from, valid);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < DYB / 16; ++k)
+                        tc::cp_async16(at + 512 + lane * DYB + 16 * k, from + k * (16 / (int)sizeof(TDy)),
+                                       valid);
+                }
+                px += (int64_t)step * D;
+                py += (int64_t)step * D;
+                row += step;
+                settle();
+            }
+            tc::cp_async_commit();
+            put = (put + 1) % S;
+        };
+        if (any) {
+            settle();
+#pragma unroll
+            for (int k = 0; k < S - 1; ++k) request();
+        }
+        if (!ready) {
+            lane_turns(a, lane, f);
+            block_weights<D>(a, weights);
+            ready = true;
+        }
+        if (!any) break;
+        warp_angles(a, f, table[warp], pos, lane);
+        float2 c[NP], s[NP];                               // of the transposed rotation
 #pragma unroll
         for (int j = 0; j < L::VEC; ++j) {
             int o;
@@ -499,17 +477,85 @@ __global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int slic
             if (j & 1) { c[j / 2].y = cs.x; s[j / 2].y = -cs.y; }
             else { c[j / 2].x = cs.x; s[j / 2].x = -cs.y; }
         }
-        grad_rows<TIn, TDy, TOut, D, kInter>(
-            a, static_cast<const TIn*>(a.q) + t * a.q_stride,
-            static_cast<const TDy*>(a.dq) + t * a.Hq * D, static_cast<TOut*>(a.q_out) + t * a.Hq * D,
-            a.Hq, top, sub, step, chan, partner, weights[0], c, s, dwq);
-        grad_rows<TIn, TDy, TOut, D, kInter>(
-            a, static_cast<const TIn*>(a.k) + t * a.k_stride,
-            static_cast<const TDy*>(a.dk) + t * a.Hk * D, static_cast<TOut*>(a.k_out) + t * a.Hk * D,
-            a.Hk, top, sub, step, chan, partner, weights[1], c, s, dwk);
+        int get = 0;
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+            const int H = kind == 0 ? a.Hq : a.Hk;
+            if (top >= H) continue;
+            TOut* dx = static_cast<TOut*>(kind == 0 ? a.q_out : a.k_out) + t * H * D + lane_off;
+            float2 w[NP];
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+                w[j] = make_float2(weights[kind][chan + 2 * j], weights[kind][chan + 2 * j + 1]);
+            for (int h = top; h < H; h += step, dx += (int64_t)step * D) {
+                copies_wait<S - 2>();
+                __syncwarp();
+                const unsigned char* at = ring[warp][get];
+                float2 x[NP], d[NP], o[NP];
+                unpack2<NP>(lds16(at + lane * 16), x);
+                if constexpr (DYB == 8) {
+                    // four BF16 values
+                    const uint2 u = *reinterpret_cast<const uint2*>(at + 512 + lane * 8);
+                    float2 v[4];
+                    unpack2<4>(make_uint4(u.x, u.y, 0, 0), v);
+                    d[0] = v[0];
+                    d[1] = v[1];
+                    if constexpr (kInter) {
+                        o[0] = make_float2(d[0].y, d[0].x);
+                        o[1] = make_float2(d[1].y, d[1].x);
+                    } else {
+                        const uint2 z = *reinterpret_cast<const uint2*>(at + 512 + partner * 8);
+                        unpack2<4>(make_uint4(z.x, z.y, 0, 0), v);
+                        o[0] = v[0];
+                        o[1] = v[1];
+                    }
+                } else {
+                    constexpr int PV = 8 / (int)sizeof(TDy);   // pairs in 16 bytes of dy
+#pragma unroll
+                    for (int k = 0; k < DYB / 16; ++k) {
+                        float2 v[PV], z[PV];
+                        unpack2<PV>(lds16(at + 512 + lane * DYB + 16 * k), v);
+                        partners<kInter, PV>(v, at + 512 + partner * DYB + 16 * k, z);
+#pragma unroll
+                        for (int j = 0; j < PV; ++j) {
+                            d[k * PV + j] = v[j];
+                            o[k * PV + j] = z[j];
+                        }
+                    }
+                }
+                request();
+                get = (get + 1) % S;
+#pragma unroll
+                for (int j = 0; j < NP; ++j) d[j] = fma2(o[j], s[j], mul2(d[j], c[j]));
+                if (a.norm) {
+                    float2 ss = mul2(x[0], x[0]), hx = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int j = 1; j < NP; ++j) ss = fma2(x[j], x[j], ss);
+                    float2 hw[NP];
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) {
+                        hw[j] = mul2(d[j], w[j]);
+                        hx = fma2(hw[j], x[j], hx);
+                    }
+                    const float rstd = rsqrtf(row_sum<L::LPR>(ss.x + ss.y) * (1.f / D) + a.eps);
+                    // n mean(h n) = x rstd^2 mean(h x)
+                    const float m = row_sum<L::LPR>(hx.x + hx.y) * (1.f / D) * rstd * rstd;
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) {
+                        float2& dw = kind == 0 ? dwq[j] : dwk[j];
+                        dw = fma2(mul2(x[j], both(rstd)), d[j], dw);
+                        d[j] = mul2(fma2(x[j], both(-m), hw[j]), both(rstd));
+                    }
+                }
+                if (h + sub < H) store2<NP>(dx, d);
+            }
+        }
+        copies_wait<0>();
+        __syncwarp();
     }
     if (a.norm && (a.q_wgrad != nullptr || a.k_wgrad != nullptr)) {
         float* out = a.partials + (int64_t)blockIdx.x * 2 * D;
+        float (*red)[D] = reinterpret_cast<float (*)[D]>(&ring[0][0][0]);
         block_dw<NP, L::LPR, D>(dwq, red, out);
         block_dw<NP, L::LPR, D>(dwk, red, out + D);
     }
@@ -536,7 +582,7 @@ __global__ void __launch_bounds__(1024) dw_sum_kernel(const float* partials, int
     }
 }
 
-constexpr int kFwdCtasPerSm = 3, kBwdCtasPerSm = 2;    // resident, by registers
+constexpr int kFwdCtasPerSm = 4, kBwdCtasPerSm = 2;    // resident, by registers
 int64_t bwd_ctas_bound() { return (int64_t)sm_count() * kBwdCtasPerSm; }
 
 // Warps per token.  `steps` warp steps of rows make a token; a warp-item costs its
