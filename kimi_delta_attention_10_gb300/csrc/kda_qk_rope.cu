@@ -585,20 +585,24 @@ __global__ void __launch_bounds__(1024) dw_sum_kernel(const float* partials, int
 constexpr int kFwdCtasPerSm = 4, kBwdCtasPerSm = 2;    // resident, by registers
 int64_t bwd_ctas_bound() { return (int64_t)sm_count() * kBwdCtasPerSm; }
 
-// Warps per token.  `steps` warp steps of rows make a token; a warp-item costs its
-// share of them and a start (the angles, C and S) of about kStart steps, and items
-// run in rounds of `warps`.  The count with the shortest schedule: one where the
-// tokens alone fill many rounds, as many as the rows allow for a few tokens.
-constexpr int kStart = 4;
-int slices_for(int64_t T, int steps, int64_t warps)
+// Warps per token.  A warp-item of s slices costs its share of the token's row steps
+// and a start (the angles, C and S), measured at about three steps where the arithmetic
+// is near the issue limit (BF16) and one where it hides behind memory (FP32).  Items run
+// `warps` at a time: the whole takes T s / warps items' time (but no less than 0.45 of
+// one, where too few warps are left to fill the memory's latency) and a quarter of an
+// item at the end.  Measured with 64 + 8 heads of 128 channels (us): 16384 BF16 tokens 100,
+// 108, 131 for 1, 2, 4 slices; 129 tokens 14.2, 5.8, 5.9 for 1, 8, 16; 16384 FP32 tokens
+// 191, 181, 178 for 1, 2, 4.
+int slices_for(int64_t T, int q_steps, int k_steps, int k_kinds, float start, int64_t warps)
 {
     int best = 1;
-    int64_t least = INT64_MAX;
-    for (int s = 1; s <= steps && s <= 64; ++s) {
-        if (T * s > INT32_MAX) break;
-        const int64_t rounds = (T * s + warps - 1) / warps;
-        const int64_t cost = rounds * ((steps + s - 1) / s + kStart);
-        if (cost < least) {
+    float least = 0.f;
+    const int most = q_steps > k_steps ? q_steps : k_steps;
+    for (int s = 1; s <= most && s <= 64 && T * s <= INT32_MAX; ++s) {
+        const int steps = (q_steps + s - 1) / s + k_kinds * ((k_steps + s - 1) / s);
+        const float fill = (float)(T * s) / (float)warps;
+        const float cost = ((fill > 0.45f ? fill : 0.45f) + 0.25f) * (steps + start);
+        if (s == 1 || cost < least) {
             least = cost;
             best = s;
         }
@@ -606,13 +610,15 @@ int slices_for(int64_t T, int steps, int64_t warps)
     return best;
 }
 int row_steps(int H, int rpw) { return (H + rpw - 1) / rpw; }
+template <typename T> constexpr float start_steps() { return sizeof(T) == 2 ? 3.f : 1.f; }
 
 template <typename TIn, typename TOut, int D, bool kInter>
 cudaError_t launch_fwd(const RopeArgs& a, bool append, cudaStream_t stream)
 {
     const int64_t resident = (int64_t)sm_count() * kFwdCtasPerSm;
     constexpr int rpw = Layout<TIn, D>::RPW;
-    const int slices = slices_for(a.T, row_steps(a.Hq, rpw), resident * NW);
+    const int slices = slices_for(a.T, row_steps(a.Hq, rpw), row_steps(a.Hk, rpw), append ? 2 : 1,
+                                  start_steps<TIn>(), resident * NW);
     int64_t blocks = ((int64_t)a.T * slices + NW - 1) / NW;
     // beyond eight rounds of CTAs each warp takes more tokens instead
     if (blocks > 8 * resident) blocks = 8 * resident;
@@ -638,7 +644,10 @@ cudaError_t launch_bwd(const RopeArgs& a, cudaStream_t stream)
 {
     // every CTA leaves a partial sum, so there are no more than are resident
     const int64_t resident = bwd_ctas_bound();
-    const int slices = slices_for(a.T, row_steps(a.Hq, Layout<TIn, D>::RPW), resident * NW);
+    constexpr int rpw = Layout<TIn, D>::RPW;
+    const int slices = slices_for(a.T, row_steps(a.Hq, rpw), row_steps(a.Hk, rpw), 1,
+                                  sizeof(TIn) == 2 ? 3.f : 2.5f,
+                                  resident * NW);
     int64_t blocks = ((int64_t)a.T * slices + NW - 1) / NW;
     if (blocks > resident) blocks = resident;
     if (a.interleaved)
