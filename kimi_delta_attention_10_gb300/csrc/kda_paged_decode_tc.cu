@@ -17,7 +17,7 @@
 //   MMA       one thread: S of tile i + 1 is issued before the product with V of
 //             tile i, so that it runs while the softmax of tile i does; O adds up in
 //             tensor memory over a row's tiles;
-//   softmax   four warps (eight for more than 32 heads): one token a lane.  The
+//   softmax   four warps per 16 heads: one token a lane.  The
 //             reference maximum m moves only when some score of the tile exceeds it
 //             by more than 2^8 (p stays within FP32 and BF16 range, the ratios are
 //             exact either way): one barrier with a vote per tile, and only after a
@@ -51,13 +51,13 @@ constexpr float kGrowth = 8.f;         // log2 of the growth that moves the refe
 
 template <int D_, int HP_> struct Cfg {
     static constexpr int D = D_, HP = HP_;             // HP: query heads per unit, padded
-    static constexpr int NWG = HP > 32 ? 2 : 1;        // softmax warpgroups
+    static constexpr int NWG = HP > 16 ? HP / 16 : 1;  // softmax warpgroups: 16 heads of a token a lane
     static constexpr int HW = HP / NWG;                // heads of each
     static constexpr int QR = HP < 16 ? 16 : HP;       // N of the first product
     static constexpr int NPV = 2 * HP;                 // N of the second
     static constexpr int NT = NWG * 128 + 96;
     static constexpr int WARP_K = NWG * 4, WARP_V = WARP_K + 1, WARP_MMA = WARP_K + 2;
-    static constexpr int CTAS = D == 64 && HP <= 32 ? 2 : 1;   // per SM
+    static constexpr int CTAS = D == 64 && HP <= 16 ? 2 : 1;   // per SM
     static constexpr uint32_t SLOT = kTile * D * 2;
     static constexpr uint32_t PBUF = NPV * 256, QBUF = QR * D * 2;
     static constexpr int NQ = HP > 32 ? 1 : 2;         // query buffers
@@ -66,8 +66,11 @@ template <int D_, int HP_> struct Cfg {
     // and 1 KB for the static part
     static constexpr uint32_t ROOM = (CTAS == 2 ? 113 * 1024 : 227 * 1024) - 2048;
     static constexpr int NS_ = (ROOM - 2 * PBUF - NQ * QBUF - MISC) / SLOT;
-    static constexpr int NS = NS_ > 8 ? 8 : NS_;       // ring slots
-    static_assert(NS >= 4, "K and V of two tiles");
+    // 128 KB an SM: with more in flight SMs share the bandwidth less evenly (64 ragged
+    // requests 304, 309, 317 us with 4, 5, 6 slots of 32 KB)
+    static constexpr int NSMAX = 128 * 1024 / (int)SLOT / CTAS;
+    static constexpr int NS = NS_ > NSMAX ? NSMAX : NS_;       // ring slots
+    static_assert(NS >= 4, "K and V of two tiles, and no slot in two producers' hands");
     static constexpr uint32_t OFF_P = NS * SLOT, OFF_Q = OFF_P + 2 * PBUF,
                               OFF_MISC = OFF_Q + NQ * QBUF, SMEM = OFF_MISC + MISC + 1024;
     static constexpr uint32_t TM_O = 2 * QR;           // after two S buffers
@@ -105,7 +108,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8])
 }
 __device__ __forceinline__ void tmem_ld(uint32_t a, float (&r)[8]) { tmem_ld8(a, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t a, float (&r)[16]) { tmem_ld16(a, r); }
-__device__ __forceinline__ void tmem_ld(uint32_t a, float (&r)[32]) { tmem_ld32(a, r); }
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&r)[8])
 {
@@ -516,7 +518,7 @@ DecodeShape decode_tc_shape(const DecodeArgs& a)
     DecodeShape s;
     s.heads = hp;
     s.units = a.Hk * ((G + hp - 1) / hp);
-    s.ctas = sm_count() * (a.D == 64 && hp <= 32 ? 2 : 1);
+    s.ctas = sm_count() * (a.D == 64 && hp <= 16 ? 2 : 1);
     s.tile_shift = kTileShift;
     s.start = 1;
     return s;

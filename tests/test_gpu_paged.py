@@ -384,6 +384,17 @@ def test_decode_few_rows_split_over_the_length(dtype, lens):
         check_decode(decode_case(lens, 4 * Hk, Hk, D, 64, dtype, len(lens) + D))
 
 
+@pytest.mark.parametrize("dtype,D", [(F32, 64), (BF16, 64), (BF16, 128)])
+def test_decode_many_tiles_a_block(dtype, D):
+    """Each block goes through many tiles and several rows of very different lengths, and two
+    rows are longer than a block's share; twice the same."""
+    rng = np.random.default_rng(11)
+    lens = rng.integers(1, 6000, 24).tolist() + [0, 30000, 1, 17000]
+    a = check_decode(decode_case(lens, 16, 16, D, 64, dtype, 12))
+    b = check_decode(decode_case(lens, 16, 16, D, 64, dtype, 12))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_decode_many_rows(dtype):
     """More requests than threads in a block, most of them short or empty."""
