@@ -1,10 +1,13 @@
-"""Builds libkda_gb300.so in-tree with nvcc for sm_103a (one -gencode)."""
+"""Builds libkda_gb300.so in-tree with nvcc for sm_103a (one -gencode), and the CPython
+module _marshal.so (g++, against the headers of the installed PyTorch)."""
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -14,6 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libkda_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
+MARSHAL_SRC = os.path.join(PKG, "marshal.cpp")
+MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -36,14 +41,27 @@ def sources():
 
 def _deps():
     return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) +
-            glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+            glob.glob(os.path.join(INCLUDE, "*.h")) + [MARSHAL_SRC, os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(MARSHAL_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(MARSHAL_PATH))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def marshal_command(out: str):
+    """g++ command of the _marshal module."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc = [os.path.join(torch_dir, "include"),
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+           sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
+            *[x for p in inc for x in ("-isystem", p)], MARSHAL_SRC, "-o", out,
+            "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -57,6 +75,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     cc = nvcc()
     inc = ["-I", INCLUDE, "-I", CSRC]
 
+    def compile_marshal(_):
+        tmp = MARSHAL_PATH + f".tmp{os.getpid()}"
+        r = subprocess.run(marshal_command(tmp), capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stdout}{r.stderr}")
+        os.replace(tmp, MARSHAL_PATH)
+
     def compile_one(src):
         obj = os.path.join(obj_dir, os.path.basename(src) + ".o")
         cmd = [cc, *ARCH, *NVCC_FLAGS, *extra_flags, *inc, "-c", src, "-o", obj]
@@ -68,8 +93,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     srcs = sources()
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        marshal = ex.submit(compile_marshal, None)
         objs = list(ex.map(compile_one, srcs))
+        marshal.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,4 +1,5 @@
-"""ctypes binding of libkda_gb300.so (include/kda.h): argument marshalling only.
+"""Binding of libkda_gb300.so (include/kda.h): argument marshalling only, by ctypes and,
+for the paged-attention calls, by the C++ module _marshal.
 
 Every computation runs in the library's CUDA kernels; PyTorch provides the
 device memory and the stream.  There is no fallback: if the library is
@@ -9,7 +10,6 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from functools import lru_cache
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -174,16 +174,9 @@ def _dev_ptr(t: Optional[torch.Tensor], name: str) -> Optional[int]:
     return t.data_ptr()
 
 
-# The current stream's handle without building a Stream object (2 us a call).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def _stream_handle(stream: Optional[torch.cuda.Stream], device) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is not None and device.index is not None:
-        return _raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    return s.cuda_stream
 
 
 def kda_gate(f: torch.Tensor, A_log: torch.Tensor, dt_bias: torch.Tensor, b: torch.Tensor,
@@ -479,78 +472,22 @@ def kda_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
 
 
 # ---------------------------------------------------------------- paged attention
-# These calls are short on the GPU, so their marshalling is kept to one look at each
-# tensor: a launch every few microseconds is bound by this file, not by the kernels.
+# These calls are short on the GPU, so their tensors are looked at in C++ (marshal.cpp):
+# a call costs the host the launch and little else.
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
-_CODE = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
-_I32, _I64, _FP32 = torch.int32, torch.int64, torch.float32
+_fast = None
 
 
-def _refuse(t, name: str, dtype: torch.dtype, n: int = -1):
-    """Raises for the first thing that is wrong with `t`."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if n >= 0 and t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements, not {t.numel()}")
-    _dev_ptr(t, name)
-    raise ValueError(f"{name}: unsupported tensor")
-
-
-def _ptr(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
-    """Device pointer of a contiguous tensor of `dtype`."""
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        _refuse(t, name, dtype)
-    return t.data_ptr()
-
-
-def _ptr_n(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, n: int) -> Optional[int]:
-    """_ptr of `n` elements; None passes."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
-        _refuse(t, name, dtype, n)
-    return t.data_ptr()
-
-
-def _rows_ptr(t: torch.Tensor, name: str, dtype: torch.dtype, T: int, H: int, D: int):
-    """(pointer, token stride) of [T, H, D] whose heads are dense within a token."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != (T, H, D):
-        raise ValueError(f"{name} must have shape {(T, H, D)}, not {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise RuntimeError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    st, sh, sc = t.stride()
-    if (sc != 1 and D > 1) or (sh != D and H > 1):
-        raise ValueError(f"{name}: the heads of a token must be dense (strides {t.stride()})")
-    return t.data_ptr(), st if T > 1 else H * D
-
-
-def _dense_ptr(t: torch.Tensor, name: str, shape, dtype: torch.dtype) -> int:
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    return _ptr(t, name, dtype)
-
-
-_scratch = {}
-
-
-def _own_scratch(nbytes: int, dev, stream: Optional[torch.cuda.Stream], handle: int) -> int:
-    """Pointer to the workspace of a call that was given none: one buffer per stream, kept
-    and grown, since calls on one stream are ordered.  (An allocation between two launches
-    costs as much host time as a launch.)  A captured call gets a buffer of its graph's own."""
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev).data_ptr()
-    key = (dev.index, handle)
-    buf = _scratch.get(key)
-    if buf is None or buf.nbytes < nbytes:
-        if stream is None:
-            buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        else:
-            with torch.cuda.stream(stream):
-                buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _scratch[key] = buf
-    return buf.data_ptr()
+def _load_marshal():
+    """The _marshal module, bound to the loaded library's functions."""
+    global _fast
+    lib = load_library()
+    if _fast is None:
+        from . import _marshal
+        _marshal.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                       for name in EXPORTS})
+        _fast = _marshal
+    return _fast
 
 
 def kda_page_plan(cached_lens: torch.Tensor, cu_seqlens: torch.Tensor, block_table: torch.Tensor,
@@ -565,30 +502,12 @@ def kda_page_plan(cached_lens: torch.Tensor, cu_seqlens: torch.Tensor, block_tab
     device: cached_lens [N], cu_seqlens [N+1] packing num_tokens new tokens, block_table
     [N, max_pages] (new entries written in place), free_pages (taken in order from
     free_start).  Returns (seq_lens [N], positions [T], slots [T] int64, free_end [1])."""
-    lib = _lib or load_library()
-    N, T = cached_lens.numel(), int(num_tokens)
-    if block_table.dim() != 2 or block_table.shape[0] != N:
-        raise ValueError(f"block_table must have shape [{N}, max_pages]")
-    dev = cached_lens.device
-    if seq_lens is None:
-        seq_lens = torch.empty(N, dtype=_I32, device=dev)
-    if positions is None:
-        positions = torch.empty(T, dtype=_I32, device=dev)
-    if slots is None:
-        slots = torch.empty(T, dtype=_I64, device=dev)
-    if free_end is None:
-        free_end = torch.empty(1, dtype=_I32, device=dev)
-    st = lib.kda_page_plan(
-        _ptr(cached_lens, "cached_lens", _I32), _ptr_n(cu_seqlens, "cu_seqlens", _I32, N + 1), N, T,
-        int(page_size), _ptr(block_table, "block_table", _I32), block_table.shape[1],
-        _ptr(free_pages, "free_pages", _I32), free_pages.numel(),
-        _ptr_n(free_start, "free_start", _I32, 1), _ptr_n(seq_lens, "seq_lens", _I32, N),
-        _ptr_n(positions, "positions", _I32, T), _ptr_n(slots, "slots", _I64, T),
-        _ptr_n(free_end, "free_end", _I32, 1), _dev_ptr(status, "status"),
-        _stream_handle(stream, dev))
-    if st != KDA_OK:
-        raise KDAError(st, "kda_page_plan")
-    return seq_lens, positions, slots, free_end
+    r = (_fast or _load_marshal()).page_plan(cached_lens, cu_seqlens, block_table, free_pages,
+                                             page_size, num_tokens, free_start, seq_lens,
+                                             positions, slots, free_end, status, stream)
+    if r.__class__ is int:
+        raise KDAError(r, "kda_page_plan")
+    return r
 
 
 def rope_inv_freq(rot_dim: int, theta: float = 10000.0, scaling: str = "plain",
@@ -606,13 +525,6 @@ def rope_inv_freq(rot_dim: int, theta: float = 10000.0, scaling: str = "plain",
     return f.to(device) if device is not None else f, m.value
 
 
-def _code(dtype: torch.dtype) -> int:
-    code = _CODE.get(dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {dtype}")
-    return code
-
-
 def kda_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
                      inv_freq: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
                      k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -623,38 +535,12 @@ def kda_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
     """Per-head RMS norm of q [T,Hq,D] and k [T,Hk,D] (weights [D] or None) and rotation of
     the first 2 * len(inv_freq) channels by position, in one pass (None: no rotation).  q and
     k may be slices of one projection.  Returns (q_out, k_out)."""
-    lib = _lib or load_library()
-    T, Hq, D = q.shape
-    Hk, dev, dt = k.shape[1], q.device, q.dtype
-    if k.dtype is not dt:
-        raise TypeError(f"k must be {dt}, not {k.dtype}")
-    if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=out_dtype or dt, device=dev)
-    odt = q_out.dtype
-    if k_out is None:
-        k_out = torch.empty((T, Hk, D), dtype=odt, device=dev)
-    pairs = 0 if inv_freq is None else inv_freq.numel()
-    qp, qs = _rows_ptr(q, "q", dt, T, Hq, D)
-    kp, ks = _rows_ptr(k, "k", dt, T, Hk, D)
-    st = lib.kda_qk_norm_rope(
-        qp, qs, kp, ks, _code(dt), _ptr_n(positions, "positions", _I32, T),
-        _ptr_n(inv_freq, "inv_freq", _FP32, pairs), 2 * pairs, 1 if interleaved else 0, rope_scale,
-        _ptr_n(q_weight, "q_weight", _FP32, D), _ptr_n(k_weight, "k_weight", _FP32, D), eps,
-        1 if qk_norm else 0, T, Hq, Hk, D, _dense_ptr(q_out, "q_out", (T, Hq, D), odt),
-        _dense_ptr(k_out, "k_out", (T, Hk, D), odt), _code(odt), _stream_handle(stream, dev))
-    if st != KDA_OK:
-        raise KDAError(st, "kda_qk_norm_rope")
-    return q_out, k_out
-
-
-def _cache_shape(k_cache, v_cache, Hk, D):
-    shape = k_cache.shape
-    if len(shape) != 4 or shape[1] != Hk or shape[3] != D:
-        raise ValueError(f"k_cache must have shape [num_pages, {Hk}, page_size, {D}], not "
-                         f"{tuple(shape)}")
-    if v_cache.shape != shape or v_cache.dtype is not k_cache.dtype:
-        raise ValueError("v_cache must have the shape and dtype of k_cache")
-    return shape
+    r = (_fast or _load_marshal()).norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps,
+                                             qk_norm, interleaved, rope_scale, q_out, k_out,
+                                             out_dtype, stream)
+    if r.__class__ is int:
+        raise KDAError(r, "kda_qk_norm_rope")
+    return r
 
 
 def kda_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -669,32 +555,14 @@ def kda_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """kda_qk_norm_rope with the keys, and the values v [T,Hk,D], written to the slots
     (int64 [T], negative: skipped) of k_cache and v_cache [num_pages,Hk,page_size,D] in
     place.  Returns q_out in the cache's dtype."""
-    lib = _lib or load_library()
-    T, Hq, D = q.shape
-    Hk, dev, dt, cdt = k.shape[1], q.device, q.dtype, k_cache.dtype
-    if k.dtype is not dt or v.dtype is not dt:
-        raise TypeError(f"k must be {dt} and v as well, not {k.dtype} and {v.dtype}")
-    num_pages, _, page_size, _ = _cache_shape(k_cache, v_cache, Hk, D)
-    if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=cdt, device=dev)
-    pairs = 0 if inv_freq is None else inv_freq.numel()
-    qp, qs = _rows_ptr(q, "q", dt, T, Hq, D)
-    kp, ks = _rows_ptr(k, "k", dt, T, Hk, D)
-    vp, vs = _rows_ptr(v, "v", dt, T, Hk, D)
-    st = lib.kda_qk_norm_rope_append(
-        qp, qs, kp, ks, vp, vs, _code(dt), _ptr_n(positions, "positions", _I32, T),
-        _ptr_n(slots, "slots", _I64, T), _ptr_n(inv_freq, "inv_freq", _FP32, pairs), 2 * pairs,
-        1 if interleaved else 0, rope_scale, _ptr_n(q_weight, "q_weight", _FP32, D),
-        _ptr_n(k_weight, "k_weight", _FP32, D), eps, 1 if qk_norm else 0, T, Hq, Hk, D,
-        _dense_ptr(q_out, "q_out", (T, Hq, D), cdt), _ptr(k_cache, "k_cache", cdt),
-        _ptr(v_cache, "v_cache", cdt), _code(cdt), num_pages, page_size,
-        _dev_ptr(status, "status"), _stream_handle(stream, dev))
-    if st != KDA_OK:
-        raise KDAError(st, "kda_qk_norm_rope_append")
-    return q_out
+    r = (_fast or _load_marshal()).append(q, k, v, slots, k_cache, v_cache, positions, inv_freq,
+                                          q_weight, k_weight, eps, qk_norm, interleaved,
+                                          rope_scale, q_out, status, stream)
+    if r.__class__ is int:
+        raise KDAError(r, "kda_qk_norm_rope_append")
+    return r
 
 
-@lru_cache(maxsize=256)
 def qk_norm_rope_bwd_workspace_size(T: int, Hq: int, Hk: int, D: int = 128) -> int:
     """Bytes of workspace kda_qk_norm_rope_bwd needs."""
     out = ctypes.c_int64(0)
@@ -717,48 +585,15 @@ def kda_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor,
     the first two FP32 unless grad_dtype or given tensors say otherwise, the weights' FP32
     (None where the weight is None or qk_norm is off).  workspace: None (one kept per
     stream) or a CUDA tensor of at least qk_norm_rope_bwd_workspace_size(...) bytes."""
-    lib = _lib or load_library()
-    T, Hq, D = q.shape
-    Hk, dev, dt, ydt = k.shape[1], q.device, q.dtype, dq_out.dtype
-    if k.dtype is not dt:
-        raise TypeError(f"k must be {dt}, not {k.dtype}")
-    if q_grad is None:
-        q_grad = torch.empty((T, Hq, D), dtype=grad_dtype or _FP32, device=dev)
-    gdt = q_grad.dtype
-    if k_grad is None:
-        k_grad = torch.empty((T, Hk, D), dtype=gdt, device=dev)
-    qp, qs = _rows_ptr(q, "q", dt, T, Hq, D)
-    kp, ks = _rows_ptr(k, "k", dt, T, Hk, D)
-    wq = wk = None
-    handle = _stream_handle(stream, dev)
-    ws, ws_bytes = None, 0
-    if qk_norm and (q_weight is not None or k_weight is not None):
-        if q_weight is not None:
-            wq = torch.empty(D, dtype=_FP32, device=dev)
-        if k_weight is not None:
-            wk = torch.empty(D, dtype=_FP32, device=dev)
-        if workspace is None:
-            ws_bytes = qk_norm_rope_bwd_workspace_size(T, Hq, Hk, D)
-            ws = _own_scratch(ws_bytes, dev, stream, handle)
-    if workspace is not None:
-        ws, ws_bytes = _dev_ptr(workspace, "workspace"), workspace.nbytes
-    pairs = 0 if inv_freq is None else inv_freq.numel()
-    st = lib.kda_qk_norm_rope_bwd(
-        qp, qs, kp, ks, _code(dt), _dense_ptr(dq_out, "dq_out", (T, Hq, D), ydt),
-        _dense_ptr(dk_out, "dk_out", (T, Hk, D), ydt), _code(ydt),
-        _ptr_n(positions, "positions", _I32, T), _ptr_n(inv_freq, "inv_freq", _FP32, pairs),
-        2 * pairs, 1 if interleaved else 0, rope_scale, _ptr_n(q_weight, "q_weight", _FP32, D),
-        _ptr_n(k_weight, "k_weight", _FP32, D), eps, 1 if qk_norm else 0, T, Hq, Hk, D,
-        _dense_ptr(q_grad, "q_grad", (T, Hq, D), gdt),
-        _dense_ptr(k_grad, "k_grad", (T, Hk, D), gdt), _code(gdt),
-        None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(), ws, ws_bytes,
-        handle)
-    if st != KDA_OK:
-        raise KDAError(st, "kda_qk_norm_rope_bwd")
-    return q_grad, k_grad, wq, wk
+    r = (_fast or _load_marshal()).norm_rope_bwd(q, k, dq_out, dk_out, positions, inv_freq,
+                                                 q_weight, k_weight, eps, qk_norm, interleaved,
+                                                 rope_scale, q_grad, k_grad, grad_dtype, workspace,
+                                                 stream)
+    if r.__class__ is int:
+        raise KDAError(r, "kda_qk_norm_rope_bwd")
+    return r
 
 
-@lru_cache(maxsize=256)
 def paged_decode_workspace_size(N: int, Hq: int, Hk: int, D: int = 128) -> int:
     """Bytes of workspace kda_paged_decode needs, whatever the lengths."""
     out = ctypes.c_int64(0)
@@ -776,33 +611,11 @@ def kda_paged_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
                      stream: Optional[torch.cuda.Stream] = None, workspace=None):
     """Attention of one new token per request, q [N,Hq,D], over the pages of k_cache and
     v_cache [num_pages,Hk,page_size,D] named by block_table [N,max_pages], seq_lens [N] tokens
-    each.  Returns (out [N,Hq,D], lse [N,Hq] or None).  workspace: None (one kept per stream) or a
-    CUDA tensor of at least paged_decode_workspace_size(...) bytes."""
-    lib = _lib or load_library()
-    N, Hq, D = q.shape
-    dev, dt = q.device, k_cache.dtype
-    num_pages, Hk, page_size, _ = _cache_shape(k_cache, v_cache, k_cache.shape[1], D)
-    rows, max_pages = block_table.shape
-    if rows != N:
-        raise ValueError(f"block_table must have shape [{N}, max_pages]")
-    if out is None:
-        out = torch.empty((N, Hq, D), dtype=out_dtype or q.dtype, device=dev)
-    if lse is None and want_lse:
-        lse = torch.empty((N, Hq), dtype=_FP32, device=dev)
-    qp = _ptr(q, "q", dt)
-    handle = _stream_handle(stream, dev)
-    if workspace is None:
-        ws_bytes = paged_decode_workspace_size(N, Hq, Hk, D)
-        ws = _own_scratch(ws_bytes, dev, stream, handle)
-    else:
-        ws, ws_bytes = _dev_ptr(workspace, "workspace"), workspace.nbytes
-    odt = out.dtype
-    st = lib.kda_paged_decode(
-        qp, _ptr(k_cache, "k_cache", dt), _ptr(v_cache, "v_cache", dt), _code(dt),
-        _ptr(block_table, "block_table", _I32), _ptr_n(seq_lens, "seq_lens", _I32, N), N, Hq, Hk, D,
-        num_pages, page_size, max_pages, D ** -0.5 if scale is None else scale,
-        _dense_ptr(out, "out", (N, Hq, D), odt), _code(odt), _ptr_n(lse, "lse", _FP32, N * Hq),
-        ws, ws_bytes, _dev_ptr(status, "status"), handle)
-    if st != KDA_OK:
-        raise KDAError(st, "kda_paged_decode")
-    return out, lse
+    each.  Returns (out [N,Hq,D], lse [N,Hq] or None).  workspace: None (one kept per stream)
+    or a CUDA tensor of at least paged_decode_workspace_size(...) bytes."""
+    r = (_fast or _load_marshal()).paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale,
+                                                out, out_dtype, lse, want_lse, status, workspace,
+                                                stream)
+    if r.__class__ is int:
+        raise KDAError(r, "kda_paged_decode")
+    return r
