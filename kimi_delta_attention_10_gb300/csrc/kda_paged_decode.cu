@@ -86,7 +86,7 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
         bar.abort = 0;
         fence_mbar_init();
     }
-    let_next_start();
+    wait_for_previous();
     char* ws = static_cast<char*>(a.workspace);
     const DecodeRange rg = decode_range<C::NT>(a, sh, ws);   // syncs
 
@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(DecodeArgs a, Decode
         else
             *reinterpret_cast<float4*>(static_cast<float*>(a.out) + r * D + ch) = y;
     };
+    wait_for_previous();
     for (int64_t n = blockIdx.x + (int64_t)gridDim.x * blockIdx.y; n < a.N;
          n += (int64_t)gridDim.x * gridDim.y) {
         if (decode_len(a, n) != 0) continue;
@@ -325,7 +326,6 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(DecodeArgs a, Decode
             if (ch == 0 && a.lse != nullptr) a.lse[n * a.Hq + h] = -CUDART_INF_F;
         }
     }
-    wait_for_previous();
     const char* ws = static_cast<const char*>(a.workspace);
     const DecodeSplit st = reinterpret_cast<const DecodeSplit*>(ws)[blockIdx.x];
     const int pieces = st.last - st.first + 1;
@@ -413,8 +413,8 @@ cudaError_t launch_typed(const DecodeArgs& a, const DecodeShape& s, cudaStream_t
     static std::atomic<uint64_t> set{0};
     e = allow_smem(paged_decode_kernel<D, GT>, C::SMEM, &set);
     if (e != cudaSuccess) return e;
-    paged_decode_kernel<D, GT><<<s.ctas, C::NT, C::SMEM, stream>>>(a, s, maps);
-    return cudaGetLastError();
+    return launch_after(paged_decode_kernel<D, GT>, launch_config(s.ctas, C::NT, C::SMEM), stream, a, s,
+                        maps);
 }
 
 template <int D>
@@ -433,12 +433,11 @@ cudaError_t launch_fp32(const DecodeArgs& a, const DecodeShape& s, cudaStream_t 
 
 cudaError_t launch_decode_join(const DecodeArgs& a, const DecodeShape& s, cudaStream_t stream)
 {
-    cudaLaunchConfig_t cfg = {};
+    cudaLaunchConfig_t cfg = launch_config(s.ctas, kJoin);
     // many blocks for a head's pieces each only where rows are few and the pieces many
     const int64_t rows = (int64_t)a.N * s.units;
     const int heads = s.heads < 8 ? s.heads : 8;
     cfg.gridDim = dim3((unsigned)s.ctas, (unsigned)(rows * 2 < s.ctas ? heads : heads < 2 ? 1 : 2));
-    cfg.blockDim = dim3(kJoin);
     return launch_after(a.D == 64 ? decode_join_kernel<64> : decode_join_kernel<128>, cfg, stream, a,
                         s);
 }

@@ -155,7 +155,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
         tmem_alloc(&bar.tmem, C::TM_COLS);
         tmem_relinquish();
     }
-    let_next_start();
+    wait_for_previous();
     char* ws = static_cast<char*>(a.workspace);
     const DecodeRange rg = decode_range<C::NT>(a, sh, ws);
     fence_before_sync();
@@ -506,8 +506,7 @@ cudaError_t launch_typed(const DecodeArgs& a, const DecodeShape& s, cudaStream_t
     static std::atomic<uint64_t> set{0};
     e = allow_smem(kern, C::SMEM, &set);
     if (e != cudaSuccess) return e;
-    kern<<<s.ctas, C::NT, C::SMEM, stream>>>(a, s, maps);
-    return cudaGetLastError();
+    return launch_after(kern, launch_config(s.ctas, C::NT, C::SMEM), stream, a, s, maps);
 }
 
 }  // namespace

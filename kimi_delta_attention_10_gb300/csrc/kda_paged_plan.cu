@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(PlanArgs a)
     __shared__ int32_t s_cu[NT + 1], s_c[NT], s_have[NT];
     __shared__ int64_t s_base[NT];         // < 0: the request is not served
     const int tid = threadIdx.x;
+    wait_for_previous();
     const int64_t t0 = (int64_t)blockIdx.x * a.T / gridDim.x;
     const int64_t t1 = (int64_t)(blockIdx.x + 1) * a.T / gridDim.x;
 
@@ -208,8 +209,7 @@ cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t stream)
     const int64_t most = 4 * (int64_t)sm_count();
     if (blocks > most) blocks = most;
     if (blocks < 1) blocks = 1;
-    page_plan_kernel<<<(unsigned)blocks, NT, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(page_plan_kernel, launch_config(blocks, NT), stream, a);
 }
 
 }  // namespace kda

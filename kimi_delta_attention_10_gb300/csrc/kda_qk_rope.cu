@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(NT, 4) qk_rope_kernel(RopeArgs a, int slices)
     const int partner = partner_lane(a, lane, chan, L::VEC);
     const int64_t items = (int64_t)a.T * slices, nwarps = (int64_t)gridDim.x * NW;
     const int step = slices * L::RPW;
+    wait_for_previous();
     uint64_t f[2];
     bool ready = false;
     for (int64_t i = (int64_t)blockIdx.x * NW + warp;; i += nwarps) {
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int slic
     const int partner = partner_lane(a, lane, chan, L::VEC);
     const int64_t items = (int64_t)a.T * slices, nwarps = (int64_t)gridDim.x * NW;
     const int step = slices * L::RPW;
-    let_next_start();
+    wait_for_previous();
     uint64_t f[2];
     bool ready = false;
     float2 dwq[NP], dwk[NP];
@@ -622,11 +623,9 @@ cudaError_t launch_fwd(const RopeArgs& a, bool append, cudaStream_t stream)
     int64_t blocks = ((int64_t)a.T * slices + NW - 1) / NW;
     // beyond eight rounds of CTAs each warp takes more tokens instead
     if (blocks > 8 * resident) blocks = 8 * resident;
-    if (append)
-        qk_rope_kernel<TIn, TOut, D, true, kInter><<<(unsigned)blocks, NT, 0, stream>>>(a, slices);
-    else
-        qk_rope_kernel<TIn, TOut, D, false, kInter><<<(unsigned)blocks, NT, 0, stream>>>(a, slices);
-    return cudaGetLastError();
+    return launch_after(append ? qk_rope_kernel<TIn, TOut, D, true, kInter>
+                               : qk_rope_kernel<TIn, TOut, D, false, kInter>,
+                        launch_config(blocks, NT), stream, a, slices);
 }
 
 template <typename TIn, typename TOut>
@@ -650,16 +649,12 @@ cudaError_t launch_bwd(const RopeArgs& a, cudaStream_t stream)
                                   resident * NW);
     int64_t blocks = ((int64_t)a.T * slices + NW - 1) / NW;
     if (blocks > resident) blocks = resident;
-    if (a.interleaved)
-        qk_rope_bwd_kernel<TIn, TDy, TOut, D, true><<<(unsigned)blocks, NT, 0, stream>>>(a, slices);
-    else
-        qk_rope_bwd_kernel<TIn, TDy, TOut, D, false><<<(unsigned)blocks, NT, 0, stream>>>(a, slices);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_after(a.interleaved ? qk_rope_bwd_kernel<TIn, TDy, TOut, D, true>
+                                               : qk_rope_bwd_kernel<TIn, TDy, TOut, D, false>,
+                                 launch_config(blocks, NT), stream, a, slices);
     if (e == cudaSuccess && a.norm && (a.q_wgrad != nullptr || a.k_wgrad != nullptr)) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * D / 32);
-        cfg.blockDim = dim3(1024);
-        e = launch_after(dw_sum_kernel, cfg, stream, a.partials, (int)blocks, D, a.q_wgrad, a.k_wgrad);
+        e = launch_after(dw_sum_kernel, launch_config(2 * D / 32, 1024), stream, a.partials, (int)blocks,
+                         D, a.q_wgrad, a.k_wgrad);
     }
     return e;
 }
