@@ -87,8 +87,11 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
         fence_mbar_init();
     }
     wait_for_previous();
+    DecodeLens lens;
+    lens.load(a);
+    __syncthreads();                               // the barriers
     char* ws = static_cast<char*>(a.workspace);
-    const DecodeRange rg = decode_range<C::NT>(a, sh, ws);   // syncs
+    const DecodeRange rg = decode_range<C::NT>(a, sh, lens, ws);
 
     BoundedWait wait(&bar.abort, a.status);
     DecodeWalk w(rg);
@@ -299,16 +302,16 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
 // Joins the split rows.  Block (b, y) joins the row whose first split is where CTA b's
 // tiles begin, every gridDim.y-th head from y; most blocks find nothing to do.  Four
 // channels a lane; the block's groups of D / 4 lanes take a head each, or, where the
-// row has many pieces, share the pieces of one head, so that even a row split over all
-// CTAs is some twenty loads deep.  Pieces are added in the CTAs' order.  Empty
+// row has many pieces, share the pieces of one head, four at a time each.  The order of
+// the sums is set by the number of pieces alone.  Empty
 // requests' rows are dealt to all blocks.
 template <int D>
 __global__ void __launch_bounds__(kJoin) decode_join_kernel(DecodeArgs a, DecodeShape sh)
 {
     constexpr int LANES = D / 4, P = kJoin / LANES;        // lanes of a group, groups
-    constexpr int kMany = 4;                               // pieces from which groups share a head
+    constexpr int kMany = 4;       // pieces requested together, and from which groups share a head
     __shared__ float4 s_x[P][LANES];
-    __shared__ float s_l[P];
+    __shared__ float2 s_ml[P];
     const int ch = (threadIdx.x % LANES) * 4, part = threadIdx.x / LANES;
     auto store = [&](int64_t r, float4 y) {
         if (a.out_bf16)
@@ -342,35 +345,59 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(DecodeArgs a, Decode
         const int g = share ? gb : gb + part;
         // piece i: the row begins in the first CTA's tiles
         auto piece = [&](int i) { return (2 * (int64_t)(st.first + i) + (i == 0)) * sh.heads + g; };
+        // the maxima, sums and outputs of up to kMany pieces are requested together
         float top = -CUDART_INF_F, l = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (g < heads) {
-#pragma unroll 8
-            for (int i = 0; i < pieces; ++i) top = fmaxf(top, ws_ml[piece(i)].x);
-            if (top != -CUDART_INF_F) {
-#pragma unroll 4
-                for (int i = first; i < pieces; i += stride) {
-                    const float2 ml = ws_ml[piece(i)];
-                    const float4 o = *reinterpret_cast<const float4*>(ws_o + piece(i) * D + ch);
-                    const float keep = exp2f(ml.x - top);
-                    l = fmaf(ml.y, keep, l);
-                    x.x = fmaf(o.x, keep, x.x);
-                    x.y = fmaf(o.y, keep, x.y);
-                    x.z = fmaf(o.z, keep, x.z);
-                    x.w = fmaf(o.w, keep, x.w);
+        auto add = [&](const float2 (&ml)[kMany], const float4 (&o)[kMany]) {
+            float m = top;
+#pragma unroll
+            for (int j = 0; j < kMany; ++j) m = fmaxf(m, ml[j].x);
+            if (m == -CUDART_INF_F) return;
+            const float old = exp2f(top - m);
+            top = m;
+            l *= old;
+            x = make_float4(x.x * old, x.y * old, x.z * old, x.w * old);
+#pragma unroll
+            for (int j = 0; j < kMany; ++j) {
+                const float keep = exp2f(ml[j].x - m);
+                l = fmaf(ml[j].y, keep, l);
+                x.x = fmaf(o[j].x, keep, x.x);
+                x.y = fmaf(o[j].y, keep, x.y);
+                x.z = fmaf(o[j].z, keep, x.z);
+                x.w = fmaf(o[j].w, keep, x.w);
+            }
+        };
+        for (int i0 = first; i0 < pieces && g < heads; i0 += kMany * stride) {
+            float2 ml[kMany];
+            float4 o[kMany];
+#pragma unroll
+            for (int j = 0; j < kMany; ++j) {
+                const int i = i0 + j * stride;
+                ml[j] = make_float2(-CUDART_INF_F, 0.f);
+                o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < pieces) {
+                    ml[j] = ws_ml[piece(i)];
+                    o[j] = *reinterpret_cast<const float4*>(ws_o + piece(i) * D + ch);
                 }
             }
+            add(ml, o);
         }
         if (share) {
             __syncthreads();                               // the last head's sums are read
             s_x[part][ch / 4] = x;
-            if (ch == 0) s_l[part] = l;
+            if (ch == 0) s_ml[part] = make_float2(top, l);
             __syncthreads();
             if (part != 0) continue;
-            for (int i = 1; i < min(P, pieces); ++i) {
-                const float4 o = s_x[i][ch / 4];
-                x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
-                l += s_l[i];
+            for (int i0 = 1; i0 < P; i0 += kMany) {
+                float2 ml[kMany];
+                float4 o[kMany];
+#pragma unroll
+                for (int j = 0; j < kMany; ++j) {
+                    const bool any = i0 + j < P;
+                    ml[j] = any ? s_ml[i0 + j] : make_float2(-CUDART_INF_F, 0.f);
+                    o[j] = any ? s_x[i0 + j][ch / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                add(ml, o);
             }
         }
         if (g >= heads) continue;
@@ -394,6 +421,7 @@ DecodeShape fp32_shape(const DecodeArgs& a)
     s.ctas = sm_count();
     s.tile_shift = a.D == 128 ? 5 : 6;
     s.start = 3;
+    s.least = 1;
     return s;
 }
 

@@ -118,6 +118,24 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&r)[8])
                  : "memory");
 }
 
+// Sums of N values over the warp's lanes: each step halves the values a lane sums, so that
+// l[0] of lane 32 / N * g is the sum of the lanes' l[g].
+template <int N, int O = 16, int M>
+__device__ __forceinline__ void warp_sums(float (&l)[M], int lane)
+{
+    if constexpr (N > 1) {
+        const bool up = lane & O;
+#pragma unroll
+        for (int g = 0; g < N / 2; ++g) {
+            const float give = up ? l[g] : l[g + N / 2], take = up ? l[g + N / 2] : l[g];
+            l[g] = take + __shfl_xor_sync(0xffffffffu, give, O);
+        }
+    } else {
+        l[0] += __shfl_xor_sync(0xffffffffu, l[0], O);
+    }
+    if constexpr (O > 1) warp_sums<(N > 1 ? N / 2 : 1), O / 2>(l, lane);
+}
+
 template <int D, int HP>
 __global__ void __launch_bounds__(Cfg<D, HP>::NT, Cfg<D, HP>::CTAS)
 paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps maps)
@@ -156,11 +174,13 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
         tmem_relinquish();
     }
     wait_for_previous();
-    char* ws = static_cast<char*>(a.workspace);
-    const DecodeRange rg = decode_range<C::NT>(a, sh, ws);
+    DecodeLens lens;
+    lens.load(a);
     fence_before_sync();
-    __syncthreads();
+    __syncthreads();                               // the barriers and the tensor memory
     fence_after_sync();
+    char* ws = static_cast<char*>(a.workspace);
+    const DecodeRange rg = decode_range<C::NT>(a, sh, lens, ws);
     const uint32_t tmem = bar.tmem;
 
     BoundedWait wait(&bar.abort, a.status);
@@ -226,7 +246,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
             const uint64_t dP = desc_kmajor(smem_u32(sm + C::OFF_P), C::NPV, 0);
             uint32_t i = 0, item = 0;
             bool begins = false;                           // tile i - 1 is its row's first here
-            auto product_with_v = [&](uint32_t t) {
+            auto product_with_v = [&](uint32_t t, int tokens) {
                 const uint32_t slot = (2 * t + 1) % NS, b = t & 1;
                 wait(&bar.full[slot], ((2 * t + 1) / NS) & 1);
                 wait(&bar.pfull[b], (t >> 1) & 1);
@@ -234,9 +254,10 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                 fence_after_sync();
 #pragma unroll
                 for (int s = 0; s < kTile / 16; ++s)
-                    mma_bf16(tmem + C::TM_O, desc_advance(dV, slot * C::SLOT + mnmajor_off(s)),
-                             desc_advance(dP, b * C::PBUF + kmajor_off(C::NPV, s)), id_o,
-                             s > 0 || !begins);
+                    if (16 * s < tokens)
+                        mma_bf16(tmem + C::TM_O, desc_advance(dV, slot * C::SLOT + mnmajor_off(s)),
+                                 desc_advance(dP, b * C::PBUF + kmajor_off(C::NPV, s)), id_o,
+                                 s > 0 || !begins);
                 commit(&bar.empty[slot]);
                 commit(&bar.ofull[b]);
             };
@@ -259,11 +280,11 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                         if (t + 1 == w.tile1) commit(&bar.qempty[qb]);
                         commit(&bar.sfull[b]);
                     }
-                    if (t > w.tile0) product_with_v(i - 1);
+                    if (t > w.tile0) product_with_v(i - 1, kTile);
                     begins = t == w.tile0;
                 }
                 // the row's last product before the next row's keys are waited for
-                product_with_v(i - 1);
+                product_with_v(i - 1, w.L - ((w.tile1 - 1) << kTileShift));
                 ++item;
             }
             commit(&bar.drain);                            // no MMA outlives the loop
@@ -390,15 +411,12 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                     // value rows past the end, once they have landed
                     const uint32_t slot = (2 * i + 1) % NS;
                     wait(&bar.full[slot], ((2 * i + 1) / NS) & 1);
-                    if (row >= valid) {
-#pragma unroll
-                        for (int h = 0; h < HALVES; ++h)
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                *reinterpret_cast<uint4*>(sm + slot * C::SLOT +
-                                                          h * (kTile * 128) + row * 128 + k * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                    }
+                    // as far as the product reads: its steps are 16 tokens
+                    const int rows = ((valid + 15) & ~15) - valid;
+                    for (int e = row; e < rows * 8 * HALVES; e += 128)
+                        *reinterpret_cast<uint4*>(sm + slot * C::SLOT + ((e >> 3) % HALVES) * (kTile * 128) +
+                                                  (valid + (e >> 3) / HALVES) * 128 + (e & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
                 }
                 fence_async_smem();
                 fence_before_sync();
@@ -417,22 +435,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
 #pragma unroll
                 for (int g = 0; g < HW; ++g) acc[g] += x[g];
             }
-            // the sums of all tokens' weights: each step halves the heads a lane sums
-#pragma unroll
-            for (int n = HW, o = 16; o > 0; o >>= 1) {
-                if (n > 1) {
-                    n >>= 1;
-                    const bool up = lane & o;
-#pragma unroll
-                    for (int g = 0; g < n; ++g) {
-                        const float give = up ? l[g] : l[g + n], take = up ? l[g + n] : l[g];
-                        l[g] = take + __shfl_xor_sync(0xffffffffu, give, o);
-                    }
-                } else {
-                    l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
-                }
-            }
-            // lane 32 / HW * g has head g's (bits from the top)
+            warp_sums<HW>(l, lane);
             constexpr int EACH = 32 / HW;
             if (lane % EACH == 0) s_sum[quad * HP + wg * HW + lane / EACH] = l[0];
             named_sync(bar_id, 128);
@@ -520,6 +523,7 @@ DecodeShape decode_tc_shape(const DecodeArgs& a)
     s.ctas = sm_count() * (a.D == 64 && hp <= 16 ? 2 : 1);
     s.tile_shift = kTileShift;
     s.start = 1;
+    s.least = 1;
     return s;
 }
 

@@ -33,14 +33,18 @@ __device__ __forceinline__ float warp_max(float x)
 struct DecodeWalk {
     int64_t pos, end, at;
     int32_t n, u, tile0, tile1, tiles, L;
+    int32_t known;        // the request that L is of
     __device__ __forceinline__ explicit DecodeWalk(const DecodeRange& r)
-        : pos(r.begin), end(r.end), at(r.at), n(r.n), u(0), tile0(0), tile1(0), tiles(0), L(0) {}
+        : pos(r.begin), end(r.end), at(r.at), n(r.n), u(0), tile0(0), tile1(0), tiles(0), L(r.L), known(r.n) {}
     // The next row with tiles tile0 .. tile1 - 1 (at least one) of this CTA.
     __device__ __forceinline__ bool next(const DecodeArgs& a, const DecodeShape& sh)
     {
         while (pos < end) {
             for (;; ++n) {
-                L = decode_len(a, n);
+                if (n != known) {
+                    L = decode_len(a, n);
+                    known = n;
+                }
                 tiles = tiles_of(L, sh.tile_shift);
                 const int64_t all = tiles ? (int64_t)(tiles + sh.start) * sh.units : 0;
                 if (pos < at + all) break;
