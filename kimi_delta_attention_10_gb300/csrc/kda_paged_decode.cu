@@ -8,9 +8,10 @@
 // channels) by TMA, one box per page (the keys in 128-byte columns, swizzled, so that
 // 32 lanes can read 32 rows without bank conflicts).  Each of six other warps has one
 // slot of 32 KB and takes its tile on its own:
-//   scores   one or two tokens a lane: key rows against the unit's query rows, which all
-//            lanes read at the same address (scaled by scale * log2 e beforehand);
-//   softmax  a warp reduction per head; the reference maximum moves only when it
+//   scores   a lane has 1 to 8 tokens and the unit's heads or a quarter of them (so that a
+//            value read from shared memory is used four times and more), queries scaled
+//            by scale * log2 e beforehand, products in pairs (f32x2);
+//   softmax  a reduction over the lanes per head; the reference maximum moves only when it
 //            would grow by more than 2^8, which is exact and rarely rescales;
 //   values   four channels a lane, the weights back from shared memory four tokens
 //            at a time.  Rows past the end are not read.
@@ -40,7 +41,9 @@ constexpr int kMerge = 4;              // heads merged at a time
 template <int D, int GT> struct Cfg {
     static constexpr int W = D == 64 && GT == 16 ? 5 : 6;     // warps that compute, and slots
     static constexpr int NT = 32 * (W + 2);
-    static constexpr int TPL = 128 / D, kTile = 32 * TPL;      // tokens per lane and tile
+    static constexpr int kTile = 4096 / D;                     // tokens per tile
+    // the warp's lanes for the scores: HS groups, each for HG heads, TT tokens a lane
+    static constexpr int HS = GT >= 8 ? 4 : GT == 4 ? 2 : 1, HG = GT / HS, TL = 32 / HS, TT = kTile / TL;
     static constexpr int kTileShift = D == 128 ? 5 : 6;
     static constexpr uint32_t TILE = kTile * D * 4;            // keys or values of a slot
     static constexpr uint32_t SLOT = 2 * TILE;
@@ -65,7 +68,8 @@ __global__ void __launch_bounds__(Cfg<D, GT>::NT, 1)
 paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps maps)
 {
     using C = Cfg<D, GT>;
-    constexpr int W = C::W, TPL = C::TPL, kTile = C::kTile, kTileShift = C::kTileShift;
+    constexpr int W = C::W, kTile = C::kTile, kTileShift = C::kTileShift;
+    constexpr int HG = C::HG, TL = C::TL, TT = C::TT;
     constexpr int BLOCKS = D / 32;                 // 128-byte columns of a key row
     constexpr int LPR = D / 4, RPW = 32 / LPR;     // lanes per value row, rows at a time
     extern __shared__ unsigned char raw[];
@@ -135,7 +139,8 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
     float2* ws_ml = reinterpret_cast<float2*>(ws + decode_ml_offset(sh));
     float* ws_o = reinterpret_cast<float*>(ws + decode_o_offset(sh));
     float* my_p = s_p + warp * GT * kTile;
-    const int sub = lane / LPR, chan = (lane % LPR) * 4;
+    const int sub = lane / LPR, chan = (lane % LPR) * 4;           // for the values
+    const int head = lane / TL * HG, tl = lane % TL;               // for the scores
     uint32_t c0 = 0;                               // the CTA's tiles before this row
     while (w.next(a, sh)) {
         const int hk = w.u / groups, g0 = (w.u - hk * groups) * GT;    // in the group of G
@@ -145,14 +150,16 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
                                                                      D + i] * qscale
                                 : 0.f;
         }
-        float m[GT], l[GT], o[GT][4];
+        float m[HG], l[HG], o[GT][4];
 #pragma unroll
-        for (int g = 0; g < GT; ++g) {
+        for (int g = 0; g < HG; ++g) {
             m[g] = -CUDART_INF_F;
             l[g] = 0.f;
+        }
+#pragma unroll
+        for (int g = 0; g < GT; ++g)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[g][i] = 0.f;
-        }
         named_sync(1, 32 * W);
         // tile c of the CTA is in slot c % W, which is the warp's own: a warp that shared
         // slots could mistake an earlier filling's phase for its own
@@ -160,54 +167,78 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
             const uint32_t c = c0 + (t - w.tile0);
             const int valid = min(kTile, w.L - (t << kTileShift));
             wait(&bar.full[warp], (c / W) & 1);
-            const unsigned char* kt = sm + warp * C::SLOT + lane * 128;
+            // tokens tl, tl + TL, ...: their rows have the same place in the swizzle
+            const unsigned char* kt = sm + warp * C::SLOT + tl * 128;
             const float* vt = reinterpret_cast<const float*>(sm + warp * C::SLOT + C::TILE);
-            float s[TPL][GT];
+            float2 s[TT][HG];
 #pragma unroll
-            for (int i = 0; i < TPL; ++i)
+            for (int i = 0; i < TT; ++i)
 #pragma unroll
-                for (int g = 0; g < GT; ++g) s[i][g] = 0.f;
-#pragma unroll 8
+                for (int g = 0; g < HG; ++g) s[i][g] = make_float2(0.f, 0.f);
+#pragma unroll(TT * HG > 16 ? 2 : 4)
             for (int j = 0; j < D / 4; ++j) {
-                float4 k[TPL];
+                float4 k[TT];
 #pragma unroll
-                for (int i = 0; i < TPL; ++i)
-                    k[i] = *reinterpret_cast<const float4*>(kt + (j >> 3) * (kTile * 128) +
-                                                            i * 32 * 128 +
-                                                            (((j & 7) ^ (lane & 7)) << 4));
+                for (int i = 0; i < TT; ++i)
+                    k[i] = *reinterpret_cast<const float4*>(kt + (j >> 3) * (kTile * 128) + i * TL * 128 +
+                                                            (((j & 7) ^ (tl & 7)) << 4));
 #pragma unroll
-                for (int g = 0; g < GT; ++g) {
-                    const float4 q = *reinterpret_cast<const float4*>(s_q + g * D + 4 * j);
+                for (int g = 0; g < HG; ++g) {
+                    const float4 q = *reinterpret_cast<const float4*>(s_q + (head + g) * D + 4 * j);
 #pragma unroll
-                    for (int i = 0; i < TPL; ++i)
-                        s[i][g] = fmaf(q.x, k[i].x, fmaf(q.y, k[i].y, fmaf(q.z, k[i].z,
-                                                                          fmaf(q.w, k[i].w, s[i][g]))));
+                    for (int i = 0; i < TT; ++i) {
+                        s[i][g] = fma2(make_float2(q.x, q.y), make_float2(k[i].x, k[i].y), s[i][g]);
+                        s[i][g] = fma2(make_float2(q.z, q.w), make_float2(k[i].z, k[i].w), s[i][g]);
+                    }
                 }
             }
             __syncwarp();                          // the last tile's weights are read
+            float x[TT][HG], top[HG];
+            bool grown = false;
 #pragma unroll
-            for (int g = 0; g < GT; ++g) {
-                float x[TPL], top = -CUDART_INF_F;
+            for (int g = 0; g < HG; ++g) {
+                top[g] = -CUDART_INF_F;
 #pragma unroll
-                for (int i = 0; i < TPL; ++i) {
-                    x[i] = lane + 32 * i < valid ? s[i][g] : -CUDART_INF_F;
-                    top = fmaxf(top, x[i]);
+                for (int i = 0; i < TT; ++i) {
+                    x[i][g] = tl + TL * i < valid ? s[i][g].x + s[i][g].y : -CUDART_INF_F;
+                    top[g] = fmaxf(top[g], x[i][g]);
                 }
-                top = warp_max(top);
-                if (top > m[g] + kGrowth) {        // uniform
-                    const float keep = exp2f(m[g] - top);
-                    m[g] = top;
-                    l[g] *= keep;
+                if constexpr (TL == 32) {
+                    top[g] = warp_max(top[g]);
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[g][i] *= keep;
+                    for (int k = TL / 2; k > 0; k >>= 1)
+                        top[g] = fmaxf(top[g], __shfl_xor_sync(0xffffffffu, top[g], k));
                 }
+                grown |= top[g] > m[g] + kGrowth;
+            }
+            if (__any_sync(0xffffffffu, grown)) {
+                float keep[HG];
+#pragma unroll
+                for (int g = 0; g < HG; ++g) {
+                    keep[g] = 1.f;
+                    if (top[g] > m[g] + kGrowth) {
+                        keep[g] = exp2f(m[g] - top[g]);
+                        m[g] = top[g];
+                    }
+                    l[g] *= keep[g];
+                }
+#pragma unroll
+                for (int g = 0; g < GT; ++g) {
+                    const float k = __shfl_sync(0xffffffffu, keep[g % HG], g / HG * TL);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[g][i] *= k;
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < HG; ++g) {
                 // all scores so far -infinity: nothing to subtract
                 const float ref = m[g] == -CUDART_INF_F ? 0.f : m[g];
 #pragma unroll
-                for (int i = 0; i < TPL; ++i) {
-                    const float e = exp2f(x[i] - ref);
+                for (int i = 0; i < TT; ++i) {
+                    const float e = exp2f(x[i][g] - ref);
                     l[g] += e;
-                    my_p[g * kTile + lane + 32 * i] = e;
+                    my_p[(head + g) * kTile + tl + TL * i] = e;
                 }
             }
             __syncwarp();
@@ -225,25 +256,30 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
                 for (int g = 0; g < GT; ++g) {
                     const float4 p = *reinterpret_cast<const float4*>(my_p + g * kTile + r + 4 * sub);
                     const float pi[4] = {p.x, p.y, p.z, p.w};
+                    float2 lo = make_float2(o[g][0], o[g][1]), hi = make_float2(o[g][2], o[g][3]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        o[g][0] = fmaf(pi[i], v[i].x, o[g][0]);
-                        o[g][1] = fmaf(pi[i], v[i].y, o[g][1]);
-                        o[g][2] = fmaf(pi[i], v[i].z, o[g][2]);
-                        o[g][3] = fmaf(pi[i], v[i].w, o[g][3]);
+                        lo = fma2(both(pi[i]), make_float2(v[i].x, v[i].y), lo);
+                        hi = fma2(both(pi[i]), make_float2(v[i].z, v[i].w), hi);
                     }
+                    o[g][0] = lo.x;
+                    o[g][1] = lo.y;
+                    o[g][2] = hi.x;
+                    o[g][3] = hi.y;
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.empty[warp]);
         }
+        // merge: the row's maximum of each head over the warps, then outputs to it; in the
+        // order of the row's tiles, whatever the CTA did before
+        const int turn = c0 % W;                       // the warp of the row's first tile
         c0 += w.tile1 - w.tile0;
-        // merge: the row's maximum of each head over the warps, then outputs to it
 #pragma unroll
-        for (int g = 0; g < GT; ++g) {
+        for (int g = 0; g < HG; ++g) {
 #pragma unroll
-            for (int k = 16; k > 0; k >>= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], k);
-            if (lane == 0) s_ml[warp * GT + g] = make_float2(m[g], l[g]);
+            for (int k = TL / 2; k > 0; k >>= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], k);
+            if (tl == 0) s_ml[warp * GT + head + g] = make_float2(m[g], l[g]);
         }
         named_sync(1, 32 * W);
         const bool whole = w.tile0 == 0 && w.tile1 == w.tiles;
@@ -256,7 +292,7 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
                 float top = -CUDART_INF_F;
 #pragma unroll
                 for (int k = 0; k < W; ++k) top = fmaxf(top, s_ml[k * GT + g].x);
-                const float keep = top == -CUDART_INF_F ? 0.f : exp2f(m[g] - top);
+                const float keep = top == -CUDART_INF_F ? 0.f : exp2f(s_ml[warp * GT + g].x - top);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     o[g][i] *= keep;
@@ -276,7 +312,8 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
 #pragma unroll
                 for (int k = 0; k < W; ++k) top = fmaxf(top, s_ml[k * GT + g].x);
 #pragma unroll
-                for (int k = 0; k < W; ++k) {
+                for (int j = 0; j < W; ++j) {
+                    const int k = turn + j < W ? turn + j : turn + j - W;
                     const float2 ml = s_ml[k * GT + g];
                     if (top != -CUDART_INF_F) sum += ml.y * exp2f(ml.x - top);
                     x += s_o[(k * kMerge + g - gb) * D + ch];

@@ -46,33 +46,6 @@ template <typename T, int D> struct Layout {
     static constexpr int RPW = 32 / LPR;       // rows per warp
 };
 
-// ---------------------------------------------------------------- pairs of FP32
-__device__ __forceinline__ uint64_t as_u64(float2 x)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x.x), "f"(x.y));
-    return r;
-}
-__device__ __forceinline__ float2 as_f2(uint64_t x)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
-    return as_f2(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
-    return as_f2(r);
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-
 // 16 bytes as pairs of FP32 values.
 template <int N> __device__ __forceinline__ void unpack2(uint4 u, float2 (&f)[N])
 {
