@@ -6,8 +6,8 @@
 // HBM-bound: every k and v is read once, 2 D values a token and key-value head.
 // One CTA per SM; two producer warps (keys, values) fill slots of 32 tokens (64 of 64
 // channels) by TMA, one box per page (the keys in 128-byte columns, swizzled, so that
-// 32 lanes can read 32 rows without bank conflicts).  Each of six other warps has one
-// slot of 32 KB and takes its tile on its own:
+// 32 lanes can read 32 rows without bank conflicts).  Six slots of 32 KB have a
+// warp each, or two that share the heads, which takes its tile on its own:
 //   scores   a lane has 1 to 8 tokens and the unit's heads or a quarter of them (so that a
 //            value read from shared memory is used four times and more), queries scaled
 //            by scale * log2 e beforehand, products in pairs (f32x2);
@@ -39,11 +39,13 @@ constexpr float kGrowth = 8.f;         // log2 of the growth that moves the refe
 constexpr int kMerge = 4;              // heads merged at a time
 
 template <int D, int GT> struct Cfg {
-    static constexpr int W = D == 64 && GT == 16 ? 5 : 6;     // warps that compute, and slots
-    static constexpr int NT = 32 * (W + 2);
+    static constexpr int W = D == 64 && GT == 16 ? 5 : 6;     // slots
+    static constexpr int PARTS = GT >= 8 ? 2 : 1, GH = GT / PARTS;   // warps per slot, heads of each
+    static constexpr int CW = W * PARTS;                       // warps that compute
+    static constexpr int NT = 32 * (CW + 2);
     static constexpr int kTile = 4096 / D;                     // tokens per tile
-    // the warp's lanes for the scores: HS groups, each for HG heads, TT tokens a lane
-    static constexpr int HS = GT >= 8 ? 4 : GT == 4 ? 2 : 1, HG = GT / HS, TL = 32 / HS, TT = kTile / TL;
+    // a warp's lanes for the scores: HS groups, each for HG heads, TT tokens a lane
+    static constexpr int HS = GH >= 8 ? 4 : GH == 4 ? 2 : 1, HG = GH / HS, TL = 32 / HS, TT = kTile / TL;
     static constexpr int kTileShift = D == 128 ? 5 : 6;
     static constexpr uint32_t TILE = kTile * D * 4;            // keys or values of a slot
     static constexpr uint32_t SLOT = 2 * TILE;
@@ -59,7 +61,7 @@ struct Maps {
 };
 
 struct Bars {
-    uint64_t full[6], empty[6];        // a warp's slot
+    uint64_t full[6], empty[6];        // slots
     int32_t abort;
 };
 
@@ -69,14 +71,14 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
 {
     using C = Cfg<D, GT>;
     constexpr int W = C::W, kTile = C::kTile, kTileShift = C::kTileShift;
-    constexpr int HG = C::HG, TL = C::TL, TT = C::TT;
+    constexpr int PARTS = C::PARTS, GH = C::GH, CW = C::CW, HG = C::HG, TL = C::TL, TT = C::TT;
     constexpr int BLOCKS = D / 32;                 // 128-byte columns of a key row
     constexpr int LPR = D / 4, RPW = 32 / LPR;     // lanes per value row, rows at a time
     extern __shared__ unsigned char raw[];
     unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     Bars& bar = *reinterpret_cast<Bars*>(sm + C::OFF_BAR);
     float* s_q = reinterpret_cast<float*>(sm + C::OFF_Q);          // [GT][D]
-    float* s_p = reinterpret_cast<float*>(sm + C::OFF_P);          // [W][GT][kTile]
+    float* s_p = reinterpret_cast<float*>(sm + C::OFF_P);          // [CW][GH][kTile]
     float* s_o = reinterpret_cast<float*>(sm + C::OFF_O);          // [W][kMerge][D]
     float2* s_ml = reinterpret_cast<float2*>(sm + C::OFF_ML);      // [W][GT]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -85,7 +87,7 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
     if (tid == 0) {
         for (int i = 0; i < W; ++i) {
             mbar_init(&bar.full[i], 2);
-            mbar_init(&bar.empty[i], 1);
+            mbar_init(&bar.empty[i], PARTS);
         }
         bar.abort = 0;
         fence_mbar_init();
@@ -99,9 +101,9 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
 
     BoundedWait wait(&bar.abort, a.status);
     DecodeWalk w(rg);
-    if (warp >= W) {
+    if (warp >= CW) {
         // ------------------------------------------------------------ producers
-        const bool keys = warp == W;
+        const bool keys = warp == CW;
         const void* map = keys ? &maps.k : &maps.v;
         const int shift = a.page_shift < kTileShift ? a.page_shift : kTileShift;
         const int rows = 1 << shift;                               // tokens per box
@@ -138,38 +140,39 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
     const float qscale = a.scale * kLog2e;
     float2* ws_ml = reinterpret_cast<float2*>(ws + decode_ml_offset(sh));
     float* ws_o = reinterpret_cast<float*>(ws + decode_o_offset(sh));
-    float* my_p = s_p + warp * GT * kTile;
+    float* my_p = s_p + warp * GH * kTile;
+    const int mine = warp % W, first = warp / W * GH;              // the warp's slot and heads
     const int sub = lane / LPR, chan = (lane % LPR) * 4;           // for the values
     const int head = lane / TL * HG, tl = lane % TL;               // for the scores
     uint32_t c0 = 0;                               // the CTA's tiles before this row
     while (w.next(a, sh)) {
         const int hk = w.u / groups, g0 = (w.u - hk * groups) * GT;    // in the group of G
-        for (int i = tid; i < GT * D; i += 32 * W) {
+        for (int i = tid; i < GT * D; i += 32 * CW) {
             const int g = i / D;
             s_q[i] = g0 + g < G ? static_cast<const float*>(a.q)[((int64_t)w.n * a.Hq + hk * G + g0) *
                                                                      D + i] * qscale
                                 : 0.f;
         }
-        float m[HG], l[HG], o[GT][4];
+        float m[HG], l[HG], o[GH][4];
 #pragma unroll
         for (int g = 0; g < HG; ++g) {
             m[g] = -CUDART_INF_F;
             l[g] = 0.f;
         }
 #pragma unroll
-        for (int g = 0; g < GT; ++g)
+        for (int g = 0; g < GH; ++g)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[g][i] = 0.f;
-        named_sync(1, 32 * W);
+        named_sync(1, 32 * CW);
         // tile c of the CTA is in slot c % W, which is the warp's own: a warp that shared
         // slots could mistake an earlier filling's phase for its own
-        for (int t = w.tile0 + (int)((warp + W - c0 % W) % W); t < w.tile1; t += W) {
+        for (int t = w.tile0 + (int)((mine + W - c0 % W) % W); t < w.tile1; t += W) {
             const uint32_t c = c0 + (t - w.tile0);
             const int valid = min(kTile, w.L - (t << kTileShift));
-            wait(&bar.full[warp], (c / W) & 1);
+            wait(&bar.full[mine], (c / W) & 1);
             // tokens tl, tl + TL, ...: their rows have the same place in the swizzle
-            const unsigned char* kt = sm + warp * C::SLOT + tl * 128;
-            const float* vt = reinterpret_cast<const float*>(sm + warp * C::SLOT + C::TILE);
+            const unsigned char* kt = sm + mine * C::SLOT + tl * 128;
+            const float* vt = reinterpret_cast<const float*>(sm + mine * C::SLOT + C::TILE);
             float2 s[TT][HG];
 #pragma unroll
             for (int i = 0; i < TT; ++i)
@@ -184,7 +187,7 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
                                                             (((j & 7) ^ (tl & 7)) << 4));
 #pragma unroll
                 for (int g = 0; g < HG; ++g) {
-                    const float4 q = *reinterpret_cast<const float4*>(s_q + (head + g) * D + 4 * j);
+                    const float4 q = *reinterpret_cast<const float4*>(s_q + (first + head + g) * D + 4 * j);
 #pragma unroll
                     for (int i = 0; i < TT; ++i) {
                         s[i][g] = fma2(make_float2(q.x, q.y), make_float2(k[i].x, k[i].y), s[i][g]);
@@ -224,7 +227,7 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
                     l[g] *= keep[g];
                 }
 #pragma unroll
-                for (int g = 0; g < GT; ++g) {
+                for (int g = 0; g < GH; ++g) {
                     const float k = __shfl_sync(0xffffffffu, keep[g % HG], g / HG * TL);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[g][i] *= k;
@@ -253,7 +256,7 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
                     if (row < valid) v[i] = *reinterpret_cast<const float4*>(vt + row * D + chan);
                 }
 #pragma unroll
-                for (int g = 0; g < GT; ++g) {
+                for (int g = 0; g < GH; ++g) {
                     const float4 p = *reinterpret_cast<const float4*>(my_p + g * kTile + r + 4 * sub);
                     const float pi[4] = {p.x, p.y, p.z, p.w};
                     float2 lo = make_float2(o[g][0], o[g][1]), hi = make_float2(o[g][2], o[g][3]);
@@ -269,7 +272,7 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.empty[warp]);
+            if (lane == 0) mbar_arrive(&bar.empty[mine]);
         }
         // merge: the row's maximum of each head over the warps, then outputs to it; in the
         // order of the row's tiles, whatever the CTA did before
@@ -279,33 +282,36 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
         for (int g = 0; g < HG; ++g) {
 #pragma unroll
             for (int k = TL / 2; k > 0; k >>= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], k);
-            if (tl == 0) s_ml[warp * GT + head + g] = make_float2(m[g], l[g]);
+            if (tl == 0) s_ml[mine * GT + first + head + g] = make_float2(m[g], l[g]);
         }
-        named_sync(1, 32 * W);
+        named_sync(1, 32 * CW);
         const bool whole = w.tile0 == 0 && w.tile1 == w.tiles;
         const int64_t r0 = whole ? (int64_t)w.n * a.Hq + hk * G + g0
                                  : (2 * (int64_t)blockIdx.x + (w.tile0 == 0)) * GT;
 #pragma unroll
         for (int gb = 0; gb < GT; gb += kMerge) {
+            // the warps that have these heads
+            if (first == gb / GH * GH) {
 #pragma unroll
-            for (int g = gb; g < gb + kMerge && g < GT; ++g) {
-                float top = -CUDART_INF_F;
+                for (int g = gb; g < gb + kMerge && g < GT; ++g) {
+                    float top = -CUDART_INF_F;
 #pragma unroll
-                for (int k = 0; k < W; ++k) top = fmaxf(top, s_ml[k * GT + g].x);
-                const float keep = top == -CUDART_INF_F ? 0.f : exp2f(s_ml[warp * GT + g].x - top);
+                    for (int k = 0; k < W; ++k) top = fmaxf(top, s_ml[k * GT + g].x);
+                    const float keep = top == -CUDART_INF_F ? 0.f : exp2f(s_ml[mine * GT + g].x - top);
+                    float (&x)[4] = o[g % GH];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    o[g][i] *= keep;
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] *= keep;
 #pragma unroll
-                    for (int k = LPR; k < 32; k <<= 1)
-                        o[g][i] += __shfl_xor_sync(0xffffffffu, o[g][i], k);
+                        for (int k = LPR; k < 32; k <<= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], k);
+                    }
+                    if (sub == 0)
+                        *reinterpret_cast<float4*>(s_o + (mine * kMerge + g - gb) * D + chan) =
+                            make_float4(x[0], x[1], x[2], x[3]);
                 }
-                if (sub == 0)
-                    *reinterpret_cast<float4*>(s_o + (warp * kMerge + g - gb) * D + chan) =
-                        make_float4(o[g][0], o[g][1], o[g][2], o[g][3]);
             }
-            named_sync(1, 32 * W);
-            for (int i = tid; i < kMerge * D; i += 32 * W) {
+            named_sync(1, 32 * CW);
+            for (int i = tid; i < kMerge * D; i += 32 * CW) {
                 const int g = gb + i / D, ch = i % D;
                 if (g >= GT || g0 + g >= G) continue;
                 float top = -CUDART_INF_F, sum = 0.f, x = 0.f;
@@ -331,7 +337,7 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
                     if (ch == 0) ws_ml[r] = make_float2(top, sum);
                 }
             }
-            named_sync(1, 32 * W);
+            named_sync(1, 32 * CW);
         }
     }
 }
