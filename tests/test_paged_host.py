@@ -237,3 +237,23 @@ def test_rope_inv_freq_refuses(lib, args):
     buf, m = (ctypes.c_float * 64)(), ctypes.c_float()
     assert lib.kda_rope_inv_freq(*args, ctypes.addressof(buf), ctypes.addressof(m)) == INVALID
     assert lib.kda_rope_inv_freq(64, 1e4, 0, 1., 1., 32., 1., None, ctypes.addressof(m)) == INVALID
+
+
+def test_marshalling_module_refuses_what_it_cannot_read(lib):
+    m = binding._load_marshal()
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    with pytest.raises(TypeError, match="arguments"):
+        m.page_plan(1, 2)
+    with pytest.raises(TypeError, match="cached_lens must be a torch.Tensor"):
+        kda.kda_page_plan([1, 2], i32(3), i32(2, 4), i32(5), 16, 0)
+    with pytest.raises(TypeError, match="num_tokens must be an integer"):
+        kda.kda_page_plan(i32(2), i32(3), i32(2, 4), i32(5), 16, 1.5)
+    x = torch.zeros(3, 2, 64)
+    with pytest.raises(ValueError, match="q must have shape"):
+        kda.kda_qk_norm_rope(x[0], x, i32(3), None)
+    with pytest.raises(ValueError, match="k must have shape"):
+        kda.kda_qk_norm_rope(x, x[0], i32(3), None)
+    with pytest.raises(KeyError):
+        m.bind({})
+    binding._fast = None                       # bound again by the next call
+    assert binding._load_marshal() is m
