@@ -503,7 +503,7 @@ kda_status kda_rope_inv_freq(int32_t rot_dim, double theta, int32_t scaling, dou
  *
  *   q [T, Hq, D], k [T, Hk, D]  x_dtype; token t's heads start at t * q_stride
  *               (k_stride) elements, so both can lie in one fused projection:
- *               stride >= heads * D, and a multiple of 16 bytes
+ *               stride >= heads * D, a multiple of 16 bytes, below 2^31 elements
  *   positions [T] int32;  inv_freq [rot_dim / 2] F32 (NULL when rot_dim = 0)
  *   q_weight, k_weight [D] F32, or NULL for ones (unread when qk_norm = 0)
  *   q_out [T, Hq, D], k_out [T, Hk, D]  out_dtype, dense; may be q (k) where

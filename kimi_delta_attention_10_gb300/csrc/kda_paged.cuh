@@ -68,9 +68,9 @@ struct RopeArgs {
     const void* q;
     const void* k;
     const void* v;           // append only
-    int64_t q_stride;        // elements between tokens
-    int64_t k_stride;
-    int64_t v_stride;
+    int32_t q_stride;        // elements between tokens
+    int32_t k_stride;
+    int32_t v_stride;
     bool x_bf16;
     const int32_t* positions;
     const float* inv_freq;

@@ -40,6 +40,7 @@ kda_status check_rope(const void* q, int64_t q_stride, const void* k, int64_t k_
     if (T > INT32_MAX || !valid_head(D)) return KDA_ERR_UNSUPPORTED;
     if (rot_dim % 16 != 0 || rot_dim > D) return KDA_ERR_UNSUPPORTED;
     if (q_stride < (int64_t)Hq * D || k_stride < (int64_t)Hk * D) return KDA_ERR_INVALID_ARG;
+    if (q_stride > INT32_MAX || k_stride > INT32_MAX) return KDA_ERR_UNSUPPORTED;
     const int64_t es = dtype_size(x_dtype);
     if (q_stride * es % 16 != 0 || k_stride * es % 16 != 0) return KDA_ERR_ALIGNMENT;
     if (T > 0 && (!q || !k || !positions)) return KDA_ERR_INVALID_ARG;
@@ -48,7 +49,8 @@ kda_status check_rope(const void* q, int64_t q_stride, const void* k, int64_t k_
                       static_cast<const void*>(q_weight), static_cast<const void*>(k_weight)}))
         return KDA_ERR_ALIGNMENT;
     *r = {};
-    r->q = q; r->k = k; r->q_stride = q_stride; r->k_stride = k_stride;
+    r->q = q; r->k = k; r->q_stride = (int32_t)q_stride;
+    r->k_stride = (int32_t)k_stride;
     r->x_bf16 = x_dtype == KDA_BF16; r->positions = positions; r->inv_freq = inv_freq;
     r->rot = rot_dim; r->interleaved = interleaved; r->rope_scale = rope_scale;
     r->q_weight = q_weight; r->k_weight = k_weight; r->eps = eps; r->norm = qk_norm;
@@ -182,6 +184,7 @@ kda_status kda_qk_norm_rope_append(const void* q, int64_t q_stride, const void* 
     if (st != KDA_OK) return st;
     if (num_pages < 0 || page_size < 1) return KDA_ERR_INVALID_ARG;
     if (v_stride < (int64_t)Hk * D) return KDA_ERR_INVALID_ARG;
+    if (v_stride > INT32_MAX) return KDA_ERR_UNSUPPORTED;
     if (v_stride * dtype_size(x_dtype) % 16 != 0) return KDA_ERR_ALIGNMENT;
     if (T > 0 && (!v || !slots || !q_out)) return KDA_ERR_INVALID_ARG;
     if (T > 0 && num_pages > 0 && (!k_cache || !v_cache)) return KDA_ERR_INVALID_ARG;
@@ -202,7 +205,7 @@ kda_status kda_qk_norm_rope_append(const void* q, int64_t q_stride, const void* 
             if (outs[j] == outs[i]) return KDA_ERR_INVALID_ARG;
         if (i > 0 && outs[i] == q) return KDA_ERR_INVALID_ARG;
     }
-    a.v = v; a.v_stride = v_stride; a.slots = slots; a.q_out = q_out; a.k_out = k_cache;
+    a.v = v; a.v_stride = (int32_t)v_stride; a.slots = slots; a.q_out = q_out; a.k_out = k_cache;
     a.v_out = v_cache; a.page = page_size; a.num_slots = (int64_t)num_pages * page_size;
     a.status = status_dev;
     return result(kda::launch_qk_rope(a, true, reinterpret_cast<cudaStream_t>(stream)));

@@ -75,6 +75,9 @@ template <int N> __device__ __forceinline__ void store2(__nv_bfloat16* p, const 
         *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y));
 }
 
+// One instruction, where a product of two 64-bit factors is half a dozen.
+__device__ __forceinline__ int64_t wide(int a, int b) { return (int64_t)a * b; }
+
 template <int LPR> __device__ __forceinline__ float row_sum(float x)
 {
 #pragma unroll
@@ -134,16 +137,6 @@ __device__ __forceinline__ uint64_t turns_of(float inv_freq)
     return bits >> 31 ? 0 - t : t;
 }
 
-// The lane's two frequencies (pairs lane and lane + 32).
-__device__ __forceinline__ void lane_turns(const RopeArgs& a, int lane, uint64_t (&f)[2])
-{
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int p = lane + 32 * i;
-        f[i] = p < a.rot / 2 ? turns_of(a.inv_freq[p]) : 0;
-    }
-}
-
 // Cosines and sines of the warp's token into its table.
 __device__ __forceinline__ void warp_angles(const RopeArgs& a, const uint64_t (&f)[2],
                                             float2* table, int32_t pos, int lane)
@@ -164,18 +157,57 @@ __device__ __forceinline__ void warp_angles(const RopeArgs& a, const uint64_t (&
     __syncwarp();
 }
 
-// Channel ch's cosine and signed sine (1 and 0 where it is not rotated), and the
-// other channel of its pair.
-__device__ __forceinline__ float2 channel_turn(const RopeArgs& a, const float2* table, bool inter,
-                                               int ch, int* other)
+// Cosines and signed sines of the lane's VEC channels (1 and 0 where they are not
+// rotated), in pairs of channels, and the first of the other channels of their pairs.
+// rot_dim is a multiple of 16, so that a lane's channels are all rotated or none, and in
+// the half layout all first or all second ones: their pairs lie side by side in the table.
+template <int VEC, bool kInter>
+__device__ __forceinline__ int lane_turn(const RopeArgs& a, const float2* table, int chan,
+                                         float2 (&c)[VEC / 2], float2 (&s)[VEC / 2])
 {
-    *other = ch;
-    if (ch >= a.rot) return make_float2(1.f, 0.f);
-    const int h = a.rot >> 1;
-    const bool second = inter ? (ch & 1) : ch >= h;
-    *other = inter ? ch ^ 1 : second ? ch - h : ch + h;
-    const float2 t = table[inter ? ch >> 1 : second ? ch - h : ch];
-    return make_float2(t.x, second ? t.y : -t.y);
+    if (chan >= a.rot) {
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+            c[j] = make_float2(1.f, 1.f);
+            s[j] = make_float2(0.f, 0.f);
+        }
+        return chan;
+    }
+    if constexpr (kInter) {
+        // (cos, sin) of pair chan / 2 + j
+#pragma unroll
+        for (int j = 0; j < VEC / 2; j += 2) {
+            const float4 t = *reinterpret_cast<const float4*>(table + chan / 2 + j);
+            c[j] = make_float2(t.x, t.x);
+            s[j] = make_float2(-t.y, t.y);
+            c[j + 1] = make_float2(t.z, t.z);
+            s[j + 1] = make_float2(-t.w, t.w);
+        }
+        return chan;
+    } else {
+        const int h = a.rot >> 1;
+        const bool second = chan >= h;
+        const float sign = second ? 1.f : -1.f;
+        const float2* at = table + (second ? chan - h : chan);
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+            const float4 t = *reinterpret_cast<const float4*>(at + 2 * j);
+            c[j] = make_float2(t.x, t.z);
+            s[j] = make_float2(t.y * sign, t.w * sign);
+        }
+        return second ? chan - h : chan + h;
+    }
+}
+
+// N pairs of consecutive weights.
+template <int N> __device__ __forceinline__ void weight_pairs(const float* w, float2 (&f)[N])
+{
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+        const float4 t = *reinterpret_cast<const float4*>(w + 2 * j);
+        f[j] = make_float2(t.x, t.y);
+        f[j + 1] = make_float2(t.z, t.w);
+    }
 }
 
 // The lane that holds the other channels of this lane's pairs (half layout).
@@ -186,15 +218,30 @@ __device__ __forceinline__ int partner_lane(const RopeArgs& a, int lane, int cha
     return chan < a.rot / 2 ? lane + d : lane - d;
 }
 
-// The weights of both kinds in shared memory (ones where there are none).
-template <int D> __device__ __forceinline__ void block_weights(const RopeArgs& a, float (*w)[D])
-{
-    for (int i = threadIdx.x; i < 2 * D; i += NT) {
-        const float* p = i < D ? a.q_weight : a.k_weight;
-        w[i / D][i % D] = a.norm && p != nullptr ? p[i % D] : 1.f;
+// What all tokens share, in shared memory: the weights of both kinds (ones where there are
+// none) and the frequencies.
+template <int D> struct Common {
+    float weights[2][D];
+    uint64_t turns[kMaxPairs];
+
+    __device__ __forceinline__ void load(const RopeArgs& a)
+    {
+        for (int i = threadIdx.x; i < 2 * D; i += NT) {
+            const float* p = i < D ? a.q_weight : a.k_weight;
+            weights[i / D][i % D] = a.norm && p != nullptr ? p[i % D] : 1.f;
+        }
+        // the last warps: the first ones may have most of the weights
+        const int i = NT - 1 - (int)threadIdx.x;
+        if (i < a.rot / 2) turns[i] = turns_of(a.inv_freq[i]);
+        __syncthreads();
     }
-    __syncthreads();
-}
+    // The lane's two frequencies: pairs lane and lane + 32.
+    __device__ __forceinline__ void lane_turns(const RopeArgs& a, int lane, uint64_t (&f)[2]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) f[i] = lane + 32 * i < a.rot / 2 ? turns[lane + 32 * i] : 0;
+    }
+};
 
 // ---------------------------------------------------------------- forward
 constexpr int kRing = 4;
@@ -202,34 +249,35 @@ constexpr int kRing = 4;
 // items = T * slices; warp-item i: token i / slices, rows of slice i % slices of
 // the q heads, then of the k heads, then (append) of the v heads.
 template <typename TIn, typename TOut, int D, bool kAppend, bool kInter>
-__global__ void __launch_bounds__(NT, 4) qk_rope_kernel(RopeArgs a, int slices)
+__global__ void __launch_bounds__(NT, 4) qk_rope_kernel(RopeArgs a, int log_slices)
 {
     using L = Layout<TIn, D>;
     constexpr int NP = L::VEC / 2;                         // pairs of values per lane
     constexpr int kKinds = kAppend ? 3 : 2;
-    __shared__ float2 table[NW][kMaxPairs];
-    __shared__ float weights[2][D];
+    __shared__ __align__(16) float2 table[NW][kMaxPairs];
+    __shared__ __align__(16) Common<D> common;
     __shared__ __align__(16) unsigned char ring[NW][kRing][512];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane / L::LPR, chan = (lane % L::LPR) * L::VEC;
     const int partner = partner_lane(a, lane, chan, L::VEC);
-    const int64_t items = (int64_t)a.T * slices, nwarps = (int64_t)gridDim.x * NW;
-    const int step = slices * L::RPW;
+    const int64_t items = (int64_t)a.T << log_slices;
+    const int nwarps = gridDim.x * NW;
+    const int step = L::RPW << log_slices;
     wait_for_previous();
     uint64_t f[2];
     bool ready = false;
     for (int64_t i = (int64_t)blockIdx.x * NW + warp;; i += nwarps) {
         // every warp of the block passes here once before its first item
         const bool any = i < items;
-        const int64_t t = any ? (int64_t)((uint32_t)i / (uint32_t)slices) : 0;
-        const int top = (int)(i - t * slices) * L::RPW;    // uniform in the warp
+        const int t = any ? (int)(i >> log_slices) : 0;
+        const int top = ((int)i & ((1 << log_slices) - 1)) * L::RPW;    // uniform in the warp
         const int32_t pos = any ? a.positions[t] : 0;
         int64_t slot = 0;
         if (kAppend && any) slot = a.slots[t];
-        const int64_t lane_off = (int64_t)(top + sub) * D + chan;
-        const TIn* src[3] = {static_cast<const TIn*>(a.q) + t * a.q_stride + lane_off,
-                             static_cast<const TIn*>(a.k) + t * a.k_stride + lane_off,
-                             kAppend ? static_cast<const TIn*>(a.v) + t * a.v_stride + lane_off : nullptr};
+        const int lane_off = (top + sub) * D + chan;
+        const TIn* src[3] = {static_cast<const TIn*>(a.q) + wide(t, a.q_stride) + lane_off,
+                             static_cast<const TIn*>(a.k) + wide(t, a.k_stride) + lane_off,
+                             kAppend ? static_cast<const TIn*>(a.v) + wide(t, a.v_stride) + lane_off : nullptr};
         // the next copy: rows row .. of kind `want`
         int want = 0, row = top;
         const TIn* p = src[0];
@@ -251,7 +299,7 @@ __global__ void __launch_bounds__(NT, 4) qk_rope_kernel(RopeArgs a, int slices)
             if (want < 3) {
                 const bool valid = row + sub < (want == 0 ? a.Hq : a.Hk);
                 tc::cp_async16(&ring[warp][put][lane * 16], valid ? p : static_cast<const TIn*>(a.q), valid);
-                p += (int64_t)step * D;
+                p += step * D;
                 row += step;
                 settle();
             }
@@ -264,8 +312,8 @@ __global__ void __launch_bounds__(NT, 4) qk_rope_kernel(RopeArgs a, int slices)
             for (int k = 0; k < kRing - 1; ++k) request();
         }
         if (!ready) {
-            lane_turns(a, lane, f);
-            block_weights<D>(a, weights);
+            common.load(a);
+            common.lane_turns(a, lane, f);
             ready = true;
         }
         if (!any) break;
@@ -274,7 +322,7 @@ __global__ void __launch_bounds__(NT, 4) qk_rope_kernel(RopeArgs a, int slices)
         if (kAppend && slot >= a.num_slots && lane == 0) report_status(a.status, KDA_ERR_DEVICE_ARG);
         int64_t paged = 0;                                 // the slot's row of head 0
         if (kAppend && stored) {
-            const int64_t page = slot / a.page;
+            const int64_t page = slot >> 32 ? slot / a.page : (uint32_t)slot / (uint32_t)a.page;
             paged = (page * a.Hk * a.page + (slot - page * a.page)) * D;
         }
         int get = 0;
@@ -283,21 +331,25 @@ __global__ void __launch_bounds__(NT, 4) qk_rope_kernel(RopeArgs a, int slices)
             const int H = kind == 0 ? a.Hq : a.Hk;
             if (top >= H) continue;
             const int64_t hstep = kAppend && kind > 0 ? (int64_t)a.page * D : D;
-            TOut* y = (kind == 0   ? static_cast<TOut*>(a.q_out) + t * a.Hq * D
-                       : !kAppend  ? static_cast<TOut*>(a.k_out) + t * a.Hk * D
+            TOut* y = (kind == 0   ? static_cast<TOut*>(a.q_out) + wide(t, a.Hq * D)
+                       : !kAppend  ? static_cast<TOut*>(a.k_out) + wide(t, a.Hk * D)
                        : kind == 1 ? static_cast<TOut*>(a.k_out) + paged
                                    : static_cast<TOut*>(a.v_out) + paged) +
                       (top + sub) * hstep + chan;
             const int64_t jump = step * hstep;
             float2 c[NP], s[NP];
             if (kind < 2) {
+                const int o = lane_turn<L::VEC, kInter>(a, table[warp], chan, c, s);
+                if (a.norm) {
+                    float2 w[NP], v[NP];
+                    weight_pairs<NP>(&common.weights[kind][chan], w);
+                    weight_pairs<NP>(&common.weights[kind][o], v);
 #pragma unroll
-                for (int j = 0; j < L::VEC; ++j) {
-                    int o;
-                    const float2 cs = channel_turn(a, table[warp], kInter, chan + j, &o);
-                    const float x = cs.x * weights[kind][chan + j], z = cs.y * weights[kind][o];
-                    if (j & 1) { c[j / 2].y = x; s[j / 2].y = z; }
-                    else { c[j / 2].x = x; s[j / 2].x = z; }
+                    for (int j = 0; j < NP; ++j) {
+                        c[j] = mul2(c[j], w[j]);
+                        // neighbours' weights trade places with them
+                        s[j] = mul2(s[j], kInter ? make_float2(v[j].y, v[j].x) : v[j]);
+                    }
                 }
             }
             for (int h = top; h < H; h += step, y += jump) {
@@ -366,20 +418,21 @@ template <typename TIn, typename TDy, int D> struct BwdRing {
 };
 
 template <typename TIn, typename TDy, typename TOut, int D, bool kInter>
-__global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int slices)
+__global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int log_slices)
 {
     using L = Layout<TIn, D>;
     using R = BwdRing<TIn, TDy, D>;
     constexpr int NP = L::VEC / 2, DYB = R::DYB, S = R::SLOTS;
-    __shared__ float2 table[NW][kMaxPairs];
-    __shared__ float weights[2][D];
+    __shared__ __align__(16) float2 table[NW][kMaxPairs];
+    __shared__ __align__(16) Common<D> common;
     __shared__ __align__(16) unsigned char ring[NW][S][R::BYTES];
     static_assert(sizeof(ring) >= NW * D * sizeof(float), "the sums of dw reuse the ring");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane / L::LPR, chan = (lane % L::LPR) * L::VEC;
     const int partner = partner_lane(a, lane, chan, L::VEC);
-    const int64_t items = (int64_t)a.T * slices, nwarps = (int64_t)gridDim.x * NW;
-    const int step = slices * L::RPW;
+    const int64_t items = (int64_t)a.T << log_slices;
+    const int nwarps = gridDim.x * NW;
+    const int step = L::RPW << log_slices;
     wait_for_previous();
     uint64_t f[2];
     bool ready = false;
@@ -388,14 +441,14 @@ __global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int slic
     for (int j = 0; j < NP; ++j) dwq[j] = dwk[j] = make_float2(0.f, 0.f);
     for (int64_t i = (int64_t)blockIdx.x * NW + warp;; i += nwarps) {
         const bool any = i < items;
-        const int64_t t = any ? (int64_t)((uint32_t)i / (uint32_t)slices) : 0;
-        const int top = (int)(i - t * slices) * L::RPW;
+        const int t = any ? (int)(i >> log_slices) : 0;
+        const int top = ((int)i & ((1 << log_slices) - 1)) * L::RPW;
         const int32_t pos = any ? a.positions[t] : 0;
-        const int64_t lane_off = (int64_t)(top + sub) * D + chan;
-        const TIn* xq = static_cast<const TIn*>(a.q) + t * a.q_stride + lane_off;
-        const TIn* xk = static_cast<const TIn*>(a.k) + t * a.k_stride + lane_off;
-        const TDy* yq = static_cast<const TDy*>(a.dq) + t * a.Hq * D + lane_off;
-        const TDy* yk = static_cast<const TDy*>(a.dk) + t * a.Hk * D + lane_off;
+        const int lane_off = (top + sub) * D + chan;
+        const TIn* xq = static_cast<const TIn*>(a.q) + wide(t, a.q_stride) + lane_off;
+        const TIn* xk = static_cast<const TIn*>(a.k) + wide(t, a.k_stride) + lane_off;
+        const TDy* yq = static_cast<const TDy*>(a.dq) + wide(t, a.Hq * D) + lane_off;
+        const TDy* yk = static_cast<const TDy*>(a.dk) + wide(t, a.Hk * D) + lane_off;
         int want = 0, row = top;
         const TIn* px = xq;
         const TDy* py = yq;
@@ -423,8 +476,8 @@ __global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int slic
                         tc::cp_async16(at + 512 + lane * DYB + 16 * k, from + k * (16 / (int)sizeof(TDy)),
                                        valid);
                 }
-                px += (int64_t)step * D;
-                py += (int64_t)step * D;
+                px += step * D;
+                py += step * D;
                 row += step;
                 settle();
             }
@@ -437,31 +490,25 @@ __global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int slic
             for (int k = 0; k < S - 1; ++k) request();
         }
         if (!ready) {
-            lane_turns(a, lane, f);
-            block_weights<D>(a, weights);
+            common.load(a);
+            common.lane_turns(a, lane, f);
             ready = true;
         }
         if (!any) break;
         warp_angles(a, f, table[warp], pos, lane);
         float2 c[NP], s[NP];                               // of the transposed rotation
+        lane_turn<L::VEC, kInter>(a, table[warp], chan, c, s);
 #pragma unroll
-        for (int j = 0; j < L::VEC; ++j) {
-            int o;
-            const float2 cs = channel_turn(a, table[warp], kInter, chan + j, &o);
-            if (j & 1) { c[j / 2].y = cs.x; s[j / 2].y = -cs.y; }
-            else { c[j / 2].x = cs.x; s[j / 2].x = -cs.y; }
-        }
+        for (int j = 0; j < NP; ++j) s[j] = make_float2(-s[j].x, -s[j].y);
         int get = 0;
 #pragma unroll
         for (int kind = 0; kind < 2; ++kind) {
             const int H = kind == 0 ? a.Hq : a.Hk;
             if (top >= H) continue;
-            TOut* dx = static_cast<TOut*>(kind == 0 ? a.q_out : a.k_out) + t * H * D + lane_off;
+            TOut* dx = static_cast<TOut*>(kind == 0 ? a.q_out : a.k_out) + wide(t, H * D) + lane_off;
             float2 w[NP];
-#pragma unroll
-            for (int j = 0; j < NP; ++j)
-                w[j] = make_float2(weights[kind][chan + 2 * j], weights[kind][chan + 2 * j + 1]);
-            for (int h = top; h < H; h += step, dx += (int64_t)step * D) {
+            weight_pairs<NP>(&common.weights[kind][chan], w);
+            for (int h = top; h < H; h += step, dx += step * D) {
                 copies_wait<S - 2>();
                 __syncwarp();
                 const unsigned char* at = ring[warp][get];
@@ -559,7 +606,7 @@ __global__ void __launch_bounds__(1024) dw_sum_kernel(const float* partials, int
 constexpr int kFwdCtasPerSm = 4, kBwdCtasPerSm = 2;    // resident, by registers
 int64_t bwd_ctas_bound() { return (int64_t)sm_count() * kBwdCtasPerSm; }
 
-// Warps per token.  A warp-item of s slices costs its share of the token's row steps
+// log2 of the warps per token (a power of two: a shift tells an item's token).  A warp-item of s slices costs its share of the token's row steps
 // and a start (the angles, C and S), measured at about three steps where the arithmetic
 // is near the issue limit (BF16) and one where it hides behind memory (FP32).  Items run
 // `warps` at a time: the whole takes T s / warps items' time (but no less than 0.45 of
@@ -569,16 +616,16 @@ int64_t bwd_ctas_bound() { return (int64_t)sm_count() * kBwdCtasPerSm; }
 // 191, 181, 178 for 1, 2, 4.
 int slices_for(int64_t T, int q_steps, int k_steps, int k_kinds, float start, int64_t warps)
 {
-    int best = 1;
     float least = 0.f;
     const int most = q_steps > k_steps ? q_steps : k_steps;
-    for (int s = 1; s <= most && s <= 64 && T * s <= INT32_MAX; ++s) {
-        const int steps = (q_steps + s - 1) / s + k_kinds * ((k_steps + s - 1) / s);
+    int best = 0;
+    for (int log = 0; log <= 6 && (1 << log) < 2 * most && (T << log) <= INT32_MAX; ++log) {
+        const int s = 1 << log, steps = (q_steps + s - 1) / s + k_kinds * ((k_steps + s - 1) / s);
         const float fill = (float)(T * s) / (float)warps;
         const float cost = ((fill > 0.45f ? fill : 0.45f) + 0.25f) * (steps + start);
-        if (s == 1 || cost < least) {
+        if (log == 0 || cost < least) {
             least = cost;
-            best = s;
+            best = log;
         }
     }
     return best;
@@ -591,14 +638,14 @@ cudaError_t launch_fwd(const RopeArgs& a, bool append, cudaStream_t stream)
 {
     const int64_t resident = (int64_t)sm_count() * kFwdCtasPerSm;
     constexpr int rpw = Layout<TIn, D>::RPW;
-    const int slices = slices_for(a.T, row_steps(a.Hq, rpw), row_steps(a.Hk, rpw), append ? 2 : 1,
+    const int log_slices = slices_for(a.T, row_steps(a.Hq, rpw), row_steps(a.Hk, rpw), append ? 2 : 1,
                                   start_steps<TIn>(), resident * NW);
-    int64_t blocks = ((int64_t)a.T * slices + NW - 1) / NW;
+    int64_t blocks = (((int64_t)a.T << log_slices) + NW - 1) / NW;
     // beyond eight rounds of CTAs each warp takes more tokens instead
     if (blocks > 8 * resident) blocks = 8 * resident;
     return launch_after(append ? qk_rope_kernel<TIn, TOut, D, true, kInter>
                                : qk_rope_kernel<TIn, TOut, D, false, kInter>,
-                        launch_config(blocks, NT), stream, a, slices);
+                        launch_config(blocks, NT), stream, a, log_slices);
 }
 
 template <typename TIn, typename TOut>
@@ -617,14 +664,14 @@ cudaError_t launch_bwd(const RopeArgs& a, cudaStream_t stream)
     // every CTA leaves a partial sum, so there are no more than are resident
     const int64_t resident = bwd_ctas_bound();
     constexpr int rpw = Layout<TIn, D>::RPW;
-    const int slices = slices_for(a.T, row_steps(a.Hq, rpw), row_steps(a.Hk, rpw), 1,
+    const int log_slices = slices_for(a.T, row_steps(a.Hq, rpw), row_steps(a.Hk, rpw), 1,
                                   sizeof(TIn) == 2 ? 3.f : 2.5f,
                                   resident * NW);
-    int64_t blocks = ((int64_t)a.T * slices + NW - 1) / NW;
+    int64_t blocks = (((int64_t)a.T << log_slices) + NW - 1) / NW;
     if (blocks > resident) blocks = resident;
     cudaError_t e = launch_after(a.interleaved ? qk_rope_bwd_kernel<TIn, TDy, TOut, D, true>
                                                : qk_rope_bwd_kernel<TIn, TDy, TOut, D, false>,
-                                 launch_config(blocks, NT), stream, a, slices);
+                                 launch_config(blocks, NT), stream, a, log_slices);
     if (e == cudaSuccess && a.norm && (a.q_wgrad != nullptr || a.k_wgrad != nullptr)) {
         e = launch_after(dw_sum_kernel, launch_config(2 * D / 32, 1024), stream, a.partials, (int)blocks,
                          D, a.q_wgrad, a.k_wgrad);
