@@ -245,29 +245,46 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
             const uint64_t dQ = desc_kmajor(smem_u32(sm + C::OFF_Q), C::QR, 0);
             const uint64_t dP = desc_kmajor(smem_u32(sm + C::OFF_P), C::NPV, 0);
             uint32_t i = 0, item = 0;
-            bool begins = false;                           // tile i - 1 is its row's first here
-            auto product_with_v = [&](uint32_t t, int tokens) {
-                const uint32_t slot = (2 * t + 1) % NS, b = t & 1;
+            // the product with V that tile i - 1 still needs: its tokens, and whether it is
+            // its row's first here
+            int tokens = 0;
+            bool begins = false;
+            auto product_with_v = [&] {
+                const uint32_t t = i - 1, slot = (2 * t + 1) % NS, b = t & 1;
                 wait(&bar.full[slot], ((2 * t + 1) / NS) & 1);
                 wait(&bar.pfull[b], (t >> 1) & 1);
-                if (wait.dead) return;
-                fence_after_sync();
-#pragma unroll
-                for (int s = 0; s < kTile / 16; ++s)
-                    if (16 * s < tokens)
+                if (!wait.dead) {
+                    fence_after_sync();
+                    auto step = [&](int s) {
                         mma_bf16(tmem + C::TM_O, desc_advance(dV, slot * C::SLOT + mnmajor_off(s)),
                                  desc_advance(dP, b * C::PBUF + kmajor_off(C::NPV, s)), id_o,
                                  s > 0 || !begins);
-                commit(&bar.empty[slot]);
-                commit(&bar.ofull[b]);
+                    };
+                    if (tokens >= kTile) {
+#pragma unroll
+                        for (int s = 0; s < kTile / 16; ++s) step(s);
+                    } else {
+                        for (int s = 0; 16 * s < tokens; ++s) step(s);
+                    }
+                    commit(&bar.empty[slot]);
+                    commit(&bar.ofull[b]);
+                }
+                tokens = 0;
             };
             while (w.next(a, sh)) {
-                const uint32_t qb = item % C::NQ;
-                wait(&bar.qfull[qb], (item / C::NQ) & 1);
-                for (int t = w.tile0; t < w.tile1; ++t, ++i) {
+                const uint32_t qb = item % C::NQ, q_phase = (item / C::NQ) & 1;
+                for (int t = w.tile0; t < w.tile1; ++t) {
                     const uint32_t slot = (2 * i) % NS, b = i & 1;
-                    wait(&bar.full[slot], ((2 * i) / NS) & 1);
-                    wait(&bar.sempty[b], ((i >> 1) & 1) ^ 1);
+                    const uint32_t k_phase = ((2 * i) / NS) & 1, s_phase = ((i >> 1) & 1) ^ 1;
+                    // Between rows: the new row's scores go first where they can at once, and
+                    // run beside the old row's softmax; else the old row is not kept waiting.
+                    if (t == w.tile0 && tokens &&
+                        !(mbar_test(&bar.qfull[qb], q_phase) && mbar_test(&bar.full[slot], k_phase) &&
+                          mbar_test(&bar.sempty[b], s_phase)))
+                        product_with_v();
+                    if (t == w.tile0) wait(&bar.qfull[qb], q_phase);
+                    wait(&bar.full[slot], k_phase);
+                    wait(&bar.sempty[b], s_phase);
                     if (!wait.dead) {
                         fence_after_sync();
 #pragma unroll
@@ -280,13 +297,14 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                         if (t + 1 == w.tile1) commit(&bar.qempty[qb]);
                         commit(&bar.sfull[b]);
                     }
-                    if (t > w.tile0) product_with_v(i - 1, kTile);
+                    if (tokens) product_with_v();
                     begins = t == w.tile0;
+                    tokens = w.L - (t << kTileShift);      // more than a tile's: a whole one
+                    ++i;
                 }
-                // the row's last product before the next row's keys are waited for
-                product_with_v(i - 1, w.L - ((w.tile1 - 1) << kTileShift));
                 ++item;
             }
+            if (tokens) product_with_v();
             commit(&bar.drain);                            // no MMA outlives the loop
             mbar_wait(&bar.drain, 0);
         }

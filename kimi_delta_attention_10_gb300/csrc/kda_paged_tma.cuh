@@ -62,6 +62,19 @@ struct DecodeWalk {
     }
 };
 
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* m, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(m)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // A wait that gives up marks the CTA: its producer then stops, the other roles run
 // their loops to the end without waiting or multiplying, so that all barriers meet.
 struct BoundedWait {
