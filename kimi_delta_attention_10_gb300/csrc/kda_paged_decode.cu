@@ -105,35 +105,30 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
     const DecodeRange rg = decode_range<C::NT>(a, sh, lens, ws);
 
     BoundedWait wait(&bar.abort, a.status);
-    DecodeWalk w(rg);
+    DecodeWalk w(rg, a, sh, groups);
     if (warp >= CW) {
         // ------------------------------------------------------------ producers
         const bool keys = warp == CW;
         const void* map = keys ? &maps.k : &maps.v;
         const int shift = a.page_shift < kTileShift ? a.page_shift : kTileShift;
         const int rows = 1 << shift;                               // tokens per box
-        const int j = keys ? lane / BLOCKS : lane, col = keys ? lane % BLOCKS : 0;
-        const uint32_t box = keys ? col * (kTile * 128) + (j << shift) * 128
-                                  : C::TILE + (j << shift) * (D * 4);
+        const int token = (keys ? lane / BLOCKS : lane) << shift, col = keys ? lane % BLOCKS : 0;
+        const uint32_t box = keys ? col * (kTile * 128) + token * 128 : C::TILE + token * (D * 4);
         uint32_t c = 0;
-        while (!wait.dead && w.next(a, sh)) {
-            const int hk = w.u / groups;
-            const int32_t* table = a.table + (int64_t)w.n * a.max_pages;
-            for (int t = w.tile0; t < w.tile1; ++t, ++c) {
-                const int tok = t << kTileShift, valid = min(kTile, w.L - tok);
-                const int pages = (valid + rows - 1) >> shift;
-                int y = 0;
-                if (j < pages) y = page_row(a, table, hk, tok + (j << shift));
-                const uint32_t slot = c % W;
-                wait(&bar.empty[slot], ((c / W) & 1) ^ 1);
-                wait.dead = __any_sync(0xffffffffu, wait.dead);
-                if (wait.dead) break;
-                if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], pages * rows * D * 4);
-                __syncwarp();
-                if (j < pages)
-                    tma_load_2d(smem_u32(sm + slot * C::SLOT) + box, map, 32 * col, y,
-                                &bar.full[slot]);
-            }
+        int t = 0;
+        DecodeTile tile, next;
+        bool more = tile.next(w, t, a, sh, kTile, shift, token);
+        for (; more; tile = next, ++c) {
+            more = next.next(w, t, a, sh, kTile, shift, token);
+            const uint32_t slot = c % W;
+            wait(&bar.empty[slot], ((c / W) & 1) ^ 1);
+            wait.dead = __any_sync(0xffffffffu, wait.dead);
+            if (wait.dead) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], tile.boxes * rows * D * 4);
+            __syncwarp();
+            if (token < tile.boxes << shift)
+                tma_load_2d(smem_u32(sm + slot * C::SLOT) + box, map, 32 * col,
+                            page_row(a, tile.entry, tile.hk, tile.at), &bar.full[slot]);
         }
         // every copy has landed before the CTA ends
         if (lane == 0)
@@ -151,7 +146,7 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
     const int head = lane / TL * HG, tl = lane % TL;               // for the scores
     uint32_t c0 = 0;                               // the CTA's tiles before this row
     while (w.next(a, sh)) {
-        const int hk = w.u / groups, g0 = (w.u - hk * groups) * GT;    // in the group of G
+        const int hk = w.hk, g0 = w.part * GT;                         // in the group of G
         for (int i = tid; i < GT * D; i += 32 * CW) {
             const int g = i / D;
             s_q[i] = g0 + g < G ? static_cast<const float*>(a.q)[((int64_t)w.n * a.Hq + hk * G + g0) *

@@ -190,7 +190,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
     const uint32_t tmem = bar.tmem;
 
     BoundedWait wait(&bar.abort, a.status);
-    DecodeWalk w(rg);
+    DecodeWalk w(rg, a, sh, groups);
     if (warp == C::WARP_K || warp == C::WARP_V) {
         // ------------------------------------------------------------ producers
         const bool keys = warp == C::WARP_K;
@@ -198,10 +198,13 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
         const int row_shift = a.page_shift < kTileShift ? a.page_shift : kTileShift;
         const int rows = 1 << row_shift;                           // tokens per box
         uint32_t i = 0, item = 0;                                  // tiles and rows so far
-        const int j = lane / HALVES, half = lane % HALVES;
-        while (!wait.dead && w.next(a, sh)) {
-            const int hk = w.u / groups, g0 = (w.u - hk * groups) * HP;
-            if (keys) {
+        const int half = lane % HALVES, token = lane / HALVES << row_shift;
+        int t = 0;
+        DecodeTile tile, next;
+        bool more = tile.next(w, t, a, sh, kTile, row_shift, token);
+        for (; more; tile = next, ++i) {
+            more = next.next(w, t, a, sh, kTile, row_shift, token);
+            if (keys && tile.opens) {
                 const uint32_t qb = item % C::NQ;
                 wait(&bar.qempty[qb], ((item / C::NQ) & 1) ^ 1);
                 wait.dead = __any_sync(0xffffffffu, wait.dead);
@@ -210,26 +213,19 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                 __syncwarp();
                 if (lane < HALVES)
                     tma_load_2d(smem_u32(sm + C::OFF_Q + qb * C::QBUF + lane * C::QR * 128),
-                                &maps.q, 64 * lane, w.n * a.Hq + hk * G + g0, &bar.qfull[qb]);
+                                &maps.q, 64 * lane, tile.n * a.Hq + tile.hk * G + tile.part * HP,
+                                &bar.qfull[qb]);
                 ++item;
             }
-            const int32_t* table = a.table + (int64_t)w.n * a.max_pages;
-            for (int t = w.tile0; t < w.tile1; ++t, ++i) {
-                const int tok = t << kTileShift, valid = min(kTile, w.L - tok);
-                const int boxes = ((valid + rows - 1) >> row_shift) * HALVES;
-                int y = 0;
-                if (lane < boxes) y = page_row(a, table, hk, tok + (j << row_shift));
-                const uint32_t c = 2 * i + (keys ? 0 : 1), slot = c % NS;
-                wait(&bar.empty[slot], ((c / NS) & 1) ^ 1);
-                wait.dead = __any_sync(0xffffffffu, wait.dead);
-                if (wait.dead) break;
-                if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], boxes * rows * 128);
-                __syncwarp();
-                if (lane < boxes)
-                    tma_load_2d(smem_u32(sm + slot * C::SLOT + half * (kTile * 128) +
-                                         ((j << row_shift) * 128)),
-                                map, 64 * half, y, &bar.full[slot]);
-            }
+            const uint32_t c = 2 * i + (keys ? 0 : 1), slot = c % NS;
+            wait(&bar.empty[slot], ((c / NS) & 1) ^ 1);
+            wait.dead = __any_sync(0xffffffffu, wait.dead);
+            if (wait.dead) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], tile.boxes * HALVES * rows * 128);
+            __syncwarp();
+            if (lane < tile.boxes * HALVES)
+                tma_load_2d(smem_u32(sm + slot * C::SLOT + half * (kTile * 128) + token * 128), map,
+                            64 * half, page_row(a, tile.entry, tile.hk, tile.at), &bar.full[slot]);
         }
         // every copy has landed before the CTA ends (all were waited for, unless a wait gave up)
         if (lane == 0) {
@@ -463,7 +459,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
             constexpr int EACH = 32 / HW;
             if (lane % EACH == 0) s_sum[quad * HP + wg * HW + lane / EACH] = l[0];
             named_sync(bar_id, 128);
-            const int hk = w.u / groups, g0 = (w.u - hk * groups) * HP + wg * HW;
+            const int hk = w.hk, g0 = w.part * HP + wg * HW;
             const bool whole = w.tile0 == 0 && w.tile1 == w.tiles;
             const int64_t r0 = whole ? (int64_t)w.n * a.Hq + hk * G + g0
                                      : (2 * (int64_t)blockIdx.x + (w.tile0 == 0)) * HP + wg * HW;

@@ -29,33 +29,52 @@ __device__ __forceinline__ float warp_max(float x)
     return r;
 }
 
-// The rows (request, head unit) of a CTA's tiles, in order; every role walks its own.
+// The rows (request, head unit) of a CTA's tiles, in order; every role walks its own.  A
+// role is one warp or thread, whose time per row is its instructions' latency: one
+// division at the start, none after it, and the next request's length loaded ahead.
 struct DecodeWalk {
-    int64_t pos, end, at;
-    int32_t n, u, tile0, tile1, tiles, L;
-    int32_t known;        // the request that L is of
-    __device__ __forceinline__ explicit DecodeWalk(const DecodeRange& r)
-        : pos(r.begin), end(r.end), at(r.at), n(r.n), u(0), tile0(0), tile1(0), tiles(0), L(r.L), known(r.n) {}
+    int64_t left;         // places still to come
+    int32_t skip;         // places of the next row that are an earlier CTA's
+    int32_t n, L, tiles;  // the request, its length and tiles
+    int32_t ahead;        // length of request n + 1, as given
+    int32_t hk, part;     // head unit: key-value head, part of its group of query heads
+    int32_t tile0, tile1;
+    int32_t parts;        // units per key-value head
+    __device__ __forceinline__ DecodeWalk(const DecodeRange& r, const DecodeArgs& a, const DecodeShape& sh,
+                                          int32_t units_per_head)
+        : left(r.end - r.begin), skip(0), n(r.n), L(r.L), tiles(tiles_of(r.L, sh.tile_shift)), ahead(0),
+          hk(0), part(-1), tile0(0), tile1(0), parts(units_per_head)
+    {
+        if (left <= 0) return;
+        const int32_t places = tiles + sh.start;
+        const int32_t u = (int32_t)quotient(r.begin - r.at, places);
+        skip = (int32_t)(r.begin - r.at - (int64_t)u * places);
+        hk = u / parts;
+        part = u - hk * parts - 1;
+        if (n + 1 < a.N) ahead = a.seq_lens[n + 1];
+    }
     // The next row with tiles tile0 .. tile1 - 1 (at least one) of this CTA.
     __device__ __forceinline__ bool next(const DecodeArgs& a, const DecodeShape& sh)
     {
-        while (pos < end) {
-            for (;; ++n) {
-                if (n != known) {
-                    L = decode_len(a, n);
-                    known = n;
+        while (left > 0) {
+            if (++part == parts) {
+                part = 0;
+                if (++hk == a.Hk) {
+                    hk = 0;
+                    do {
+                        if (++n >= a.N) return false;      // lengths that changed meanwhile
+                        L = valid_len(a, ahead);
+                        tiles = tiles_of(L, sh.tile_shift);
+                        if (n + 1 < a.N) ahead = a.seq_lens[n + 1];
+                    } while (tiles == 0);
                 }
-                tiles = tiles_of(L, sh.tile_shift);
-                const int64_t all = tiles ? (int64_t)(tiles + sh.start) * sh.units : 0;
-                if (pos < at + all) break;
-                at += all;
             }
-            const int32_t places = tiles + sh.start;
-            u = (int32_t)quotient(pos - at, places);
-            const int64_t row = at + (int64_t)u * places;      // the row's first place
-            tile0 = max((int32_t)(pos - row) - sh.start, 0);
-            pos = min(end, row + places);
-            tile1 = (int32_t)(pos - row) - sh.start;
+            const int32_t places = tiles + sh.start - skip;
+            const int32_t take = left < places ? (int32_t)left : places;
+            tile0 = max(skip - sh.start, 0);
+            tile1 = skip + take - sh.start;
+            left -= take;
+            skip = 0;
             if (tile1 > tile0) return true;
         }
         return false;
@@ -101,17 +120,45 @@ struct BoundedWait {
     }
 };
 
-// The cache row (of num_pages * Hk * page_size) of a request's token `at` and head hk.
-// An entry outside the cache is reported and read as page 0.
-__device__ __forceinline__ int32_t page_row(const DecodeArgs& a, const int32_t* table, int hk, int at)
+// The cache row (of num_pages * Hk * page_size) of head hk's token `at`, with the block
+// table's entry for it.  An entry outside the cache is reported and read as page 0.
+__device__ __forceinline__ int32_t page_row(const DecodeArgs& a, int32_t page, int hk, int at)
 {
-    int32_t page = table[at >> a.page_shift];
     if ((uint32_t)page >= (uint32_t)a.num_pages) {
         report_status(a.status, KDA_ERR_DEVICE_ARG);
         page = 0;
     }
     return ((page * a.Hk + hk) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
 }
+
+// A producer's tiles in order.  It moves to the next one before it waits for the slot
+// of the one at hand, so that the table's entries are there when that slot is free.
+struct DecodeTile {
+    int32_t boxes;        // boxes of the tile; this lane has one if its `token` is within
+    int32_t entry;        // the block table's, for the lane's box
+    int32_t hk, at;       // head, and the token at which the lane's box begins
+    int32_t n, part;      // the row, for its queries
+    bool opens;           // the row's first tile here
+    // lane_token: where in a tile the lane's box begins; a box holds 1 << shift tokens
+    __device__ __forceinline__ bool next(DecodeWalk& w, int& t, const DecodeArgs& a, const DecodeShape& sh,
+                                         int tile, int shift, int lane_token)
+    {
+        opens = ++t >= w.tile1;
+        if (opens) {
+            if (!w.next(a, sh)) return false;
+            t = w.tile0;
+        }
+        const int tok = t * tile;
+        boxes = (min(tile, w.L - tok) + (1 << shift) - 1) >> shift;
+        at = tok + lane_token;
+        hk = w.hk;
+        n = w.n;
+        part = w.part;
+        entry = 0;
+        if (lane_token < boxes << shift) entry = a.table[(int64_t)n * a.max_pages + (at >> a.page_shift)];
+        return true;
+    }
+};
 
 // ---------------------------------------------------------------- host
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
