@@ -24,12 +24,12 @@
 //             reduction, four values through shared memory) and a rescaling of O.
 // The CTA's tiles run through all its rows without draining the ring.
 //
-// Measured (us, and the share of the rate of a plain copy): 64 requests of 0 to 16384 tokens, 8
-// key-value heads of 128 channels with 8 query heads each, 296 (100%); two requests of 131072
-// to 262144 253 (100%); 64 of 4096 166 (95%), the tensor pipe 4% busy.  Where the softmax
-// has as much to do as the memory it bounds the kernel: groups of 64 heads 72%, groups of 32
-// heads of 64 channels 57%.  Short rows cost about 2 us each (128 requests of 1 to 600
-// tokens 49, 45%), one request of 129 tokens 8.3 with the join.
+// Measured (us, and the share of the rate of a plain copy): 64 requests of 0 to 16384
+// tokens, 8 key-value heads of 128 channels with 8 query heads each, 302 (98%); two requests
+// of 131072 to 262144 256 (98%); 64 of 4096 169 (94%), the tensor pipe 4% busy.  Where the
+// softmax has as much to do as the memory it bounds the kernel: groups of 64 heads 72%,
+// groups of 32 heads of 64 channels 57%.  A short row costs about 2 us beside its bytes (128
+// requests of 1 to 600 tokens 45, 49%), one request of 129 tokens 8.6 with the join.
 //
 // Tokens past the request's end: their scores are replaced by -infinity, their
 // value rows by zeros in shared memory (0 * NaN would not be 0), and pages past the
