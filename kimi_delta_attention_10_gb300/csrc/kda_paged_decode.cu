@@ -116,10 +116,9 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
         const uint32_t box = keys ? col * (kTile * 128) + token * 128 : C::TILE + token * (D * 4);
         uint32_t c = 0;
         int t = 0;
-        DecodeTile tile, next;
+        DecodeTile tile;
         bool more = tile.next(w, t, a, sh, kTile, shift, token);
-        for (; more; tile = next, ++c) {
-            more = next.next(w, t, a, sh, kTile, shift, token);
+        for (; more; ++c, more = tile.next(w, t, a, sh, kTile, shift, token)) {
             const uint32_t slot = c % W;
             wait(&bar.empty[slot], ((c / W) & 1) ^ 1);
             wait.dead = __any_sync(0xffffffffu, wait.dead);

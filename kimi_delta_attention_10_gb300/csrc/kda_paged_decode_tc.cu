@@ -200,10 +200,9 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
         uint32_t i = 0, item = 0;                                  // tiles and rows so far
         const int half = lane % HALVES, token = lane / HALVES << row_shift;
         int t = 0;
-        DecodeTile tile, next;
+        DecodeTile tile;
         bool more = tile.next(w, t, a, sh, kTile, row_shift, token);
-        for (; more; tile = next, ++i) {
-            more = next.next(w, t, a, sh, kTile, row_shift, token);
+        for (; more; ++i, more = tile.next(w, t, a, sh, kTile, row_shift, token)) {
             if (keys && tile.opens) {
                 const uint32_t qb = item % C::NQ;
                 wait(&bar.qempty[qb], ((item / C::NQ) & 1) ^ 1);

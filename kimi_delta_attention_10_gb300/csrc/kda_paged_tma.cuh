@@ -131,8 +131,8 @@ __device__ __forceinline__ int32_t page_row(const DecodeArgs& a, int32_t page, i
     return ((page * a.Hk + hk) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
 }
 
-// A producer's tiles in order.  It moves to the next one before it waits for the slot
-// of the one at hand, so that the table's entries are there when that slot is free.
+// A producer's tiles in order.  The table's entries are asked for before the wait for the
+// tile's slot, and looked at after it.
 struct DecodeTile {
     int32_t boxes;        // boxes of the tile; this lane has one if its `token` is within
     int32_t entry;        // the block table's, for the lane's box
