@@ -175,11 +175,13 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
         bar.abort = 0;
         fence_mbar_init();
     }
+    // Tensor memory after the wait: a kernel that lets this one start early may still have
+    // its own to allocate, and would never end if this one held it.
+    wait_for_previous();
     if (warp == C::WARP_MMA) {
         tmem_alloc(&bar.tmem, C::TM_COLS);
         tmem_relinquish();
     }
-    wait_for_previous();
     DecodeLens lens;
     lens.load(a);
     fence_before_sync();

@@ -500,3 +500,25 @@ def test_decode_repeats_bit_for_bit_and_in_a_graph(dtype):
     g.replay()
     b, _ = kda.kda_paged_decode(q, kc, vc, table, lens)
     assert torch.equal(out, b)
+
+
+# ---------------------------------------------------------------- beside other kernels
+def test_decode_behind_the_chunk_scan():
+    """The scan lets the next kernel start early and takes tensor memory of its own: the two in
+    turn, without a wait between them, give what each gives alone."""
+    T, H = 2048, 8
+    q, k, v, g = (randn(T, H, 128, seed=s) for s in range(4))
+    g, beta, cu = -0.05 * g.abs(), torch.rand(T, H, device="cuda"), ints([0, T])
+    ws = torch.empty(kda.chunk_workspace_size(1, T, H), dtype=torch.uint8, device="cuda")
+    chunk = lambda: kda.kda_chunk_fwd(q.bfloat16(), k.bfloat16(), v.bfloat16(), g, beta, cu,
+                                      cu_seqlens_host=[0, T], workspace=ws)[0]
+    for D, G in ((128, 8), (64, 4)):
+        case = decode_case([700, 3, 2000], 2 * G, 2, D, 64, BF16, 60)
+        o, (y, _) = chunk(), check_decode(case)
+        st = status_word()
+        seen = []
+        for _ in range(20):
+            seen.append((chunk(), kda.kda_paged_decode(*case, status=st)[0]))
+        torch.cuda.synchronize()
+        assert int(st[0]) == 0
+        assert all(torch.equal(a, o) and torch.equal(b, y) for a, b in seen)

@@ -2,6 +2,7 @@
 launched): refusals of bad arguments, and the frequencies of a rotation."""
 import ctypes
 import math
+import os
 
 import numpy as np
 import pytest
@@ -257,3 +258,12 @@ def test_marshalling_module_refuses_what_it_cannot_read(lib):
         m.bind({})
     binding._fast = None                       # bound again by the next call
     assert binding._load_marshal() is m
+
+
+# ---------------------------------------------------------------- kernels, by their source
+def test_decode_allocates_tensor_memory_after_its_wait():
+    """A CTA that may start while the kernel before it runs holds no tensor memory while it
+    waits: that kernel may signal first and allocate its own afterwards."""
+    src = open(os.path.join(_build.CSRC, "kda_paged_decode_tc.cu")).read()
+    body = src[src.index("paged_decode_tc_kernel(DecodeArgs"):]
+    assert 0 < body.index("wait_for_previous();") < body.index("tmem_alloc(") < body.index("__syncthreads();")
