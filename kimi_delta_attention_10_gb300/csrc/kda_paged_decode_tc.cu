@@ -16,7 +16,7 @@
 //             the lanes;
 //   MMA       one thread: S of tile i + 1 is issued before the product with V of
 //             tile i, so that it runs while the softmax of tile i does; O adds up in
-//             tensor memory over a row's tiles;
+//             tensor memory over runs of a row's tiles;
 //   softmax   four warps per 16 heads, one token a lane.  The reference maximum m
 //             moves only when some score of the tile exceeds it by more than 2^8 (p stays
 //             within FP32 and BF16 range, the ratios are exact either way): one barrier
@@ -54,6 +54,11 @@ using namespace tc;
 constexpr int kTile = 128;             // tokens per tile
 constexpr int kTileShift = 7;
 constexpr float kGrowth = 8.f;         // log2 of the growth that moves the reference maximum
+// Tiles that O adds up in tensor memory before it joins a total that is rounded: the tensor
+// core truncates its sums, so that a row of 262144 tokens in one sum lost up to 5e-4 of itself.
+// Two rows of 131072 to 262144 tokens with FP32 output: 2.5e-5 off in one sum, 5e-6 in runs
+// of 32 tiles, at the same speed (with groups of 64 heads 1 to 4% slower).
+constexpr int kRun = 32;
 
 template <int D_, int HP_> struct Cfg {
     static constexpr int D = D_, HP = HP_;             // HP: query heads per unit, padded
@@ -67,7 +72,7 @@ template <int D_, int HP_> struct Cfg {
     static constexpr uint32_t SLOT = kTile * D * 2;
     static constexpr uint32_t PBUF = NPV * 256, QBUF = QR * D * 2;
     static constexpr int NQ = HP > 32 ? 1 : 2;         // query buffers
-    static constexpr uint32_t MISC = HP <= 8 ? 1024 : HP <= 32 ? 2048 : 4096;   // barriers, maxima, sums
+    static constexpr uint32_t MISC = HP <= 8 ? 1024 : HP <= 16 ? 2048 : 80 * HP;   // barriers, maxima, sums
     // shared memory of an SM 228 KB, 1 KB of it kept per CTA; 1 KB for alignment
     // and 1 KB for the static part
     static constexpr uint32_t ROOM = (CTAS == 2 ? 113 * 1024 : 227 * 1024) - 2048;
@@ -80,7 +85,7 @@ template <int D_, int HP_> struct Cfg {
     static constexpr uint32_t OFF_P = NS * SLOT, OFF_Q = OFF_P + 2 * PBUF,
                               OFF_MISC = OFF_Q + NQ * QBUF, SMEM = OFF_MISC + MISC + 1024;
     static constexpr uint32_t TM_O = 2 * QR;           // after two S buffers
-    static constexpr uint32_t TM_USED = TM_O + NPV;
+    static constexpr uint32_t TM_TOTAL = TM_O + NPV, TM_USED = TM_TOTAL + HP;
     static constexpr uint32_t TM_COLS = TM_USED <= 64 ? 64 : TM_USED <= 128 ? 128
                                         : TM_USED <= 256 ? 256 : 512;
     static_assert(TM_COLS * CTAS <= 512, "tensor memory of an SM");
@@ -154,7 +159,8 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
     float* s_max = reinterpret_cast<float*>(sm + C::OFF_MISC + 256);     // [2][NWG][4][HW]
     float* s_sum = s_max + 2 * 4 * HP;                                   // [4][HP]
     float* s_inv = s_sum + 4 * HP;                                       // [HP]
-    static_assert(sizeof(Bars) <= 256 && 256 + 13 * HP * 4 <= C::MISC, "misc region");
+    float* s_ref = s_inv + HP;                                           // [4][HP]
+    static_assert(sizeof(Bars) <= 256 && 256 + 17 * HP * 4 <= C::MISC, "misc region");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.Hq / a.Hk, groups = sh.units / a.Hk;
 
@@ -301,7 +307,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                         commit(&bar.sfull[b]);
                     }
                     if (tokens) product_with_v();
-                    begins = t == w.tile0;
+                    begins = ((t - w.tile0) & (kRun - 1)) == 0;
                     tokens = w.L - (t << kTileShift);      // more than a tile's: a whole one
                     ++i;
                 }
@@ -323,6 +329,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
         const uint32_t p_chunk = (row >> 3) & 7;
         float2* ws_ml = reinterpret_cast<float2*>(ws + decode_ml_offset(sh));
         float* ws_o = reinterpret_cast<float*>(ws + decode_o_offset(sh));
+        float* my_ref = s_ref + quad * HP + wg * HW;       // the warp's copy
         uint32_t i = 0;
         while (w.next(a, sh)) {
             float ref[HW], l[HW];
@@ -332,122 +339,158 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                 l[g] = 0.f;
             }
             bool open = true;                              // some reference is still -infinity
-            for (int t = w.tile0; t < w.tile1; ++t, ++i) {
-                const uint32_t b = i & 1;
-                const int valid = w.L - (t << kTileShift);
-                float s[HW];
-                wait(&bar.sfull[b], (i >> 1) & 1);
+            // O's heads g0 .. g0 + 7 in x; the total's added to it, from its references to these
+            auto sum8 = [&](int g0, float (&x)[8]) {
+                float y[8];
+                tmem_ld8(tlane + C::TM_O + wg * HW + g0, x);
+                tmem_ld8(tlane + C::TM_O + HP + wg * HW + g0, y);
+#pragma unroll
+                for (int g = 0; g < 8; ++g) x[g] += y[g];
+            };
+            auto add_total = [&](int g0, float (&x)[8]) {
+                float y[8];
+                tmem_ld8(tlane + C::TM_TOTAL + wg * HW + g0, y);
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    const float m = ref[g0 + g], old = my_ref[g0 + g];
+                    x[g] = fmaf(y[g], old == m ? 1.f : exp2f(old - m), x[g]);
+                }
+            };
+            for (int t0 = w.tile0;;) {
+                const int t1 = min(t0 + kRun, w.tile1);
+                for (int t = t0; t < t1; ++t, ++i) {
+                    const uint32_t b = i & 1;
+                    const int valid = w.L - (t << kTileShift);
+                    float s[HW];
+                    wait(&bar.sfull[b], (i >> 1) & 1);
+                    __syncwarp();
+                    fence_after_sync();
+                    tmem_ld(tlane + b * C::QR + wg * HW, s);
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.sempty[b]);
+                    if (valid < kTile) {
+#pragma unroll
+                        for (int g = 0; g < HW; ++g) s[g] = row < valid ? s[g] * c : -CUDART_INF_F;
+                    } else {
+#pragma unroll
+                        for (int g = 0; g < HW; ++g) s[g] *= c;
+                    }
+                    bool grown = open;                     // uniform over the warpgroup
+                    if (!grown) {
+                        float over = -CUDART_INF_F;
+#pragma unroll
+                        for (int g = 0; g < HW; ++g) over = fmaxf(over, s[g] - ref[g]);
+                        grown = named_sync_or(bar_id, 128, over > kGrowth);
+                    }
+                    if (grown) {
+                        float* maxima = s_max + (b * C::NWG + wg) * 4 * HW;
+                        float mine = 0.f;
+#pragma unroll
+                        for (int g = 0; g < HW; ++g) {
+                            const float m = warp_max(s[g]);
+                            if (lane == g) mine = m;
+                        }
+                        if (lane < HW) maxima[quad * HW + lane] = mine;
+                        if (t > t0) wait(&bar.ofull[b ^ 1], ((i - 1) >> 1) & 1);
+                        named_sync(bar_id, 128);
+                        open = false;
+#pragma unroll
+                        for (int g0 = 0; g0 < HW; g0 += 8) {
+                            float keep[8];
+                            bool moved = false;
+#pragma unroll
+                            for (int g = 0; g < 8; ++g) {
+                                const float* x = maxima + g0 + g;
+                                const float top = fmaxf(fmaxf(x[0], x[HW]), fmaxf(x[2 * HW], x[3 * HW]));
+                                keep[g] = 1.f;
+                                if (top > ref[g0 + g] + kGrowth) {
+                                    keep[g] = exp2f(ref[g0 + g] - top);
+                                    ref[g0 + g] = top;
+                                    l[g0 + g] *= keep[g];
+                                    moved = true;
+                                }
+                                open |= ref[g0 + g] == -CUDART_INF_F;
+                            }
+                            if (t > t0 && moved) {
+                                fence_after_sync();
+#pragma unroll
+                                for (int part = 0; part < 2; ++part) {
+                                    const uint32_t o = tlane + C::TM_O + part * HP + wg * HW + g0;
+                                    float x[8];
+                                    tmem_ld8(o, x);
+#pragma unroll
+                                    for (int g = 0; g < 8; ++g) x[g] *= keep[g];
+                                    tmem_st8(o, x);
+                                }
+                                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                            }
+                        }
+                    }
+                    // the P buffer's last reader
+                    if (i >= 2) wait(&bar.ofull[b], ((i - 2) >> 1) & 1);
+                    const uint32_t p = p_base + b * C::PBUF;
+#pragma unroll
+                    for (int g = 0; g < HW; g += 2) {
+                        float e[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            // all scores so far -infinity: nothing to subtract
+                            const float m = ref[g + k] == -CUDART_INF_F ? 0.f : ref[g + k];
+                            e[k] = ex2_approx(s[g + k] - m);
+                            l[g + k] += e[k];
+                        }
+                        const uint32_t hi = pack_bf16(e[0], e[1]);
+                        const uint32_t lo = pack_bf16(e[0] - __uint_as_float(hi << 16),
+                                                      e[1] - __uint_as_float(hi & 0xffff0000u));
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            // row g + k of the warpgroup's (HW and HP are multiples of 8)
+                            const uint32_t at = p + ((g + k) >> 3) * 1024 + ((g + k) & 7) * 128 +
+                                                ((p_chunk ^ ((g + k) & 7)) << 4);
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at),
+                                         "h"((uint16_t)(k ? hi >> 16 : hi & 0xffffu)) : "memory");
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + HP * 128),
+                                         "h"((uint16_t)(k ? lo >> 16 : lo & 0xffffu)) : "memory");
+                        }
+                    }
+                    if (valid < kTile && wg == 0) {
+                        // value rows past the end, once they have landed
+                        const uint32_t slot = (2 * i + 1) % NS;
+                        wait(&bar.full[slot], ((2 * i + 1) / NS) & 1);
+                        // as far as the product reads: its steps are 16 tokens
+                        const int rows = ((valid + 15) & ~15) - valid;
+                        for (int e = row; e < rows * 8 * HALVES; e += 128)
+                            *reinterpret_cast<uint4*>(sm + slot * C::SLOT + ((e >> 3) % HALVES) * (kTile * 128) +
+                                                      (valid + (e >> 3) / HALVES) * 128 + (e & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.pfull[b]);
+                }
+                // the run's last product; the next one overwrites O after the next pfull
+                wait(&bar.ofull[(i - 1) & 1], ((i - 1) >> 1) & 1);
                 __syncwarp();
                 fence_after_sync();
-                tmem_ld(tlane + b * C::QR + wg * HW, s);
-                fence_before_sync();
+                if (__builtin_expect(t1 == w.tile1, 1)) break;
+#pragma unroll
+                for (int g0 = 0; g0 < HW; g0 += 8) {
+                    float x[8];
+                    sum8(g0, x);
+                    if (t0 > w.tile0) add_total(g0, x);
+                    tmem_st8(tlane + C::TM_TOTAL + wg * HW + g0, x);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.sempty[b]);
-                if (valid < kTile) {
+                if (lane == 0) {
 #pragma unroll
-                    for (int g = 0; g < HW; ++g) s[g] = row < valid ? s[g] * c : -CUDART_INF_F;
-                } else {
-#pragma unroll
-                    for (int g = 0; g < HW; ++g) s[g] *= c;
+                    for (int g = 0; g < HW; ++g) my_ref[g] = ref[g];
                 }
-                bool grown = open;                         // uniform over the warpgroup
-                if (!grown) {
-                    float over = -CUDART_INF_F;
-#pragma unroll
-                    for (int g = 0; g < HW; ++g) over = fmaxf(over, s[g] - ref[g]);
-                    grown = named_sync_or(bar_id, 128, over > kGrowth);
-                }
-                if (grown) {
-                    float* maxima = s_max + (b * C::NWG + wg) * 4 * HW;
-                    float mine = 0.f;
-#pragma unroll
-                    for (int g = 0; g < HW; ++g) {
-                        const float m = warp_max(s[g]);
-                        if (lane == g) mine = m;
-                    }
-                    if (lane < HW) maxima[quad * HW + lane] = mine;
-                    if (t > w.tile0) wait(&bar.ofull[b ^ 1], ((i - 1) >> 1) & 1);
-                    named_sync(bar_id, 128);
-                    open = false;
-#pragma unroll
-                    for (int g0 = 0; g0 < HW; g0 += 8) {
-                        float keep[8];
-                        bool moved = false;
-#pragma unroll
-                        for (int g = 0; g < 8; ++g) {
-                            const float* x = maxima + g0 + g;
-                            const float top = fmaxf(fmaxf(x[0], x[HW]), fmaxf(x[2 * HW], x[3 * HW]));
-                            keep[g] = 1.f;
-                            if (top > ref[g0 + g] + kGrowth) {
-                                keep[g] = exp2f(ref[g0 + g] - top);
-                                ref[g0 + g] = top;
-                                l[g0 + g] *= keep[g];
-                                moved = true;
-                            }
-                            open |= ref[g0 + g] == -CUDART_INF_F;
-                        }
-                        if (t > w.tile0 && moved) {
-                            fence_after_sync();
-#pragma unroll
-                            for (int part = 0; part < 2; ++part) {
-                                const uint32_t o = tlane + C::TM_O + part * HP + wg * HW + g0;
-                                float x[8];
-                                tmem_ld8(o, x);
-#pragma unroll
-                                for (int g = 0; g < 8; ++g) x[g] *= keep[g];
-                                tmem_st8(o, x);
-                            }
-                            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                        }
-                    }
-                }
-                // the P buffer's last reader
-                if (i >= 2) wait(&bar.ofull[b], ((i - 2) >> 1) & 1);
-                const uint32_t p = p_base + b * C::PBUF;
-#pragma unroll
-                for (int g = 0; g < HW; g += 2) {
-                    float e[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        // all scores so far -infinity: nothing to subtract
-                        const float m = ref[g + k] == -CUDART_INF_F ? 0.f : ref[g + k];
-                        e[k] = ex2_approx(s[g + k] - m);
-                        l[g + k] += e[k];
-                    }
-                    const uint32_t hi = pack_bf16(e[0], e[1]);
-                    const uint32_t lo = pack_bf16(e[0] - __uint_as_float(hi << 16),
-                                                  e[1] - __uint_as_float(hi & 0xffff0000u));
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        // row g + k of the warpgroup's (HW and HP are multiples of 8)
-                        const uint32_t at = p + ((g + k) >> 3) * 1024 + ((g + k) & 7) * 128 +
-                                            ((p_chunk ^ ((g + k) & 7)) << 4);
-                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at),
-                                     "h"((uint16_t)(k ? hi >> 16 : hi & 0xffffu)) : "memory");
-                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + HP * 128),
-                                     "h"((uint16_t)(k ? lo >> 16 : lo & 0xffffu)) : "memory");
-                    }
-                }
-                if (valid < kTile && wg == 0) {
-                    // value rows past the end, once they have landed
-                    const uint32_t slot = (2 * i + 1) % NS;
-                    wait(&bar.full[slot], ((2 * i + 1) / NS) & 1);
-                    // as far as the product reads: its steps are 16 tokens
-                    const int rows = ((valid + 15) & ~15) - valid;
-                    for (int e = row; e < rows * 8 * HALVES; e += 128)
-                        *reinterpret_cast<uint4*>(sm + slot * C::SLOT + ((e >> 3) % HALVES) * (kTile * 128) +
-                                                  (valid + (e >> 3) / HALVES) * 128 + (e & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                }
-                fence_async_smem();
-                fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.pfull[b]);
+                t0 = t1;
             }
-            // the row's last product; the next one overwrites O after the next pfull
-            wait(&bar.ofull[(i - 1) & 1], ((i - 1) >> 1) & 1);
-            __syncwarp();
-            fence_after_sync();
             float acc[HW];
             tmem_ld(tlane + C::TM_O + wg * HW, acc);
             {
@@ -455,6 +498,17 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                 tmem_ld(tlane + C::TM_O + HP + wg * HW, x);
 #pragma unroll
                 for (int g = 0; g < HW; ++g) acc[g] += x[g];
+            }
+            if (__builtin_expect(w.tile1 - w.tile0 > kRun, 0)) {
+#pragma unroll
+                for (int g0 = 0; g0 < HW; g0 += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) x[g] = acc[g0 + g];
+                    add_total(g0, x);
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) acc[g0 + g] = x[g];
+                }
             }
             warp_sums<HW>(l, lane);
             constexpr int EACH = 32 / HW;

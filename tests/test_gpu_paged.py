@@ -522,3 +522,28 @@ def test_decode_behind_the_chunk_scan():
         torch.cuda.synchronize()
         assert int(st[0]) == 0
         assert all(torch.equal(a, o) and torch.equal(b, y) for a, b in seen)
+
+
+# ---------------------------------------------------------------- long sums
+@pytest.mark.parametrize("D", [128, 64])
+def test_decode_long_rows_lose_nothing(D):
+    """Rows of 262144 tokens, each whole in a block: a few pages over and over, so that the
+    output is that of the pages once.  Values about one, which truncated sums would shrink.
+    The tolerance in u = 2^-24 of |out|: a sum of 128 products' results in the tensor core, each
+    truncated by up to 2 u of a partial sum that grows evenly, 128 u; 128 totals and the two parts
+    added, 64 u + 2 u; a lane's sum of 2048 weights, 1024 u; a score's 12 u of reach twice, a
+    weight's 2^-15 as above."""
+    P, pages, L = 64, 16, 262144
+    N = torch.cuda.get_device_properties(0).multi_processor_count * (2 if D == 64 else 1)
+    kc = randn(pages, 1, P, D, seed=1, dtype=BF16)
+    vc = (1 + 0.25 * randn(pages, 1, P, D, seed=2)).to(BF16)
+    q = randn(N, 1, D, seed=3, dtype=BF16)
+    table = ints([list(range(pages)) * (L // P // pages)]).expand(N, -1).contiguous()
+    out, lse = kda.kda_paged_decode(q, kc, vc, table, ints([L] * N), out_dtype=F32, want_lse=True)
+    once = np.arange(pages)[None].repeat(N, 0)
+    ref, ref_lse, _, reach = paged.paged_decode(f64(q), f64(kc), f64(vc), once, [pages * P] * N, D ** -0.5)
+    tol = (1218 * U + 24 * U * reach[..., None] + 2.0 ** -15) * np.abs(ref)
+    err = np.abs(f64(out) - ref)
+    assert (err <= tol).all(), float((err / tol).max())
+    many = ref_lse + np.log(L / (pages * P))
+    assert (np.abs(f64(lse) - many) <= 1024 * U + 12 * U * reach + 8 * U * np.abs(many)).all()
