@@ -127,7 +127,7 @@ kda_status kda_rope_inv_freq(int32_t rot_dim, double theta, int32_t scaling, dou
     double lo = 0.0, hi = 0.0;
     if (scaling == KDA_ROPE_YARN) {
         lo = fmax(floor(pair_of(beta_fast)), 0.0);
-        hi = fmin(ceil(pair_of(beta_slow)), pairs - 1.0);
+        hi = fmin(ceil(pair_of(beta_slow)), rot_dim - 1.0);
     }
     for (int i = 0; i < pairs; ++i) {
         double f = pow(base, -(double)i / pairs);

@@ -260,6 +260,26 @@ def test_marshalling_module_refuses_what_it_cannot_read(lib):
     assert binding._load_marshal() is m
 
 
+@pytest.mark.parametrize("original_len", [4096, 65536, 131072, 1 << 22])
+def test_rope_inv_freq_yarn_ramp_written_out(original_len):
+    """Every channel of the ramp, also where its slow end lies past the last pair: a pair that
+    still turns more than beta_slow times is never interpolated whole."""
+    pairs, theta, factor, fast, slow = 64, 1e4, 4.0, 32.0, 1.0
+    # the (fractional) index of the pair that turns b times in original_len tokens
+    index = lambda b: pairs * math.log(original_len / (2 * math.pi * b)) / math.log(theta)
+    lo, hi = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), 2 * pairs - 1)
+    want = []
+    for i in range(pairs):
+        f = theta ** (-i / pairs)
+        share = min(max((i - lo) / (hi - lo), 0.0), 1.0) if hi > lo else float(i > lo)
+        want.append(f * (1 - share) + f / factor * share)
+    a, _ = kda.rope_inv_freq(2 * pairs, theta, "yarn", factor, original_len, fast, slow)
+    assert near(a, want)
+    turns = original_len * theta ** (-np.arange(pairs) / pairs) / (2 * math.pi)
+    kept = a.double().numpy() > theta ** (-np.arange(pairs) / pairs) / factor * (1 + 1e-6)
+    assert kept[turns > slow * 1.0001].all() and not kept[turns < slow / 1.2].any()
+
+
 # ---------------------------------------------------------------- kernels, by their source
 def test_decode_allocates_tensor_memory_after_its_wait():
     """A CTA that may start while the kernel before it runs holds no tensor memory while it
