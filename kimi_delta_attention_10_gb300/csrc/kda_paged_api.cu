@@ -133,8 +133,8 @@ kda_status kda_rope_inv_freq(int32_t rot_dim, double theta, int32_t scaling, dou
         double f = pow(base, -(double)i / pairs);
         if (scaling == KDA_ROPE_LINEAR) f /= factor;
         if (scaling == KDA_ROPE_YARN) {
-            double slow = hi > lo ? (i - lo) / (hi - lo) : i > lo ? 1.0 : 0.0;
-            slow = fmin(fmax(slow, 0.0), 1.0);             // 1: interpolated, 0: kept
+            // 1: interpolated, 0: kept
+            const double slow = i >= hi ? 1.0 : i <= lo ? 0.0 : (i - lo) / (hi - lo);
             f = f * (1.0 - slow) + f / factor * slow;
         }
         inv_freq_host[i] = (float)f;

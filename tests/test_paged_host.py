@@ -280,6 +280,13 @@ def test_rope_inv_freq_yarn_ramp_written_out(original_len):
     assert kept[turns > slow * 1.0001].all() and not kept[turns < slow / 1.2].any()
 
 
+@pytest.mark.parametrize("original_len", [0.5, 4.0, 6.0])
+def test_rope_inv_freq_yarn_shorter_than_a_turn(original_len):
+    """No pair turns once in the trained length: all take f / factor."""
+    f = 1e4 ** (-np.arange(32) / 32)
+    assert near(kda.rope_inv_freq(64, 1e4, "yarn", 4.0, original_len)[0], f / 4)
+
+
 # ---------------------------------------------------------------- kernels, by their source
 def test_decode_allocates_tensor_memory_after_its_wait():
     """A CTA that may start while the kernel before it runs holds no tensor memory while it
