@@ -563,7 +563,9 @@ __global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int log_
                         hw[j] = mul2(d[j], w[j]);
                         hx = fma2(hw[j], x[j], hx);
                     }
-                    const float rstd = rsqrtf(row_sum<L::LPR>(ss.x + ss.y) * (1.f / D) + a.eps);
+                    // rows past the heads are zeros, which an infinite factor would make NaN in dw
+                    const float ms = row_sum<L::LPR>(ss.x + ss.y) * (1.f / D) + a.eps;
+                    const float rstd = h + sub < H ? rsqrtf(ms) : 0.f;
                     // n mean(h n) = x rstd^2 mean(h x)
                     const float m = row_sum<L::LPR>(hx.x + hx.y) * (1.f / D) * rstd * rstd;
 #pragma unroll

@@ -313,6 +313,26 @@ def test_rope_bwd_against_differences():
     assert abs((4 * d1 - d2) / 3 - got) <= 1024 * (h ** 4 + 4 * U / h) + 0.01 * abs(d1 - d2)
 
 
+@pytest.mark.parametrize("dt,D,Hq,Hk", [(BF16, 128, 4, 1), (BF16, 128, 3, 5), (BF16, 64, 3, 1),
+                                        (BF16, 64, 6, 7), (F32, 64, 3, 1), (F32, 128, 2, 1)])
+def test_rope_bwd_without_epsilon(dt, D, Hq, Hk):
+    """eps = 0 with head counts that leave rows of a warp without a head: nothing of those
+    reaches the weights' gradients.  Tolerances as in test_rope_bwd_matches_oracle."""
+    T = 11
+    q, k, _, pos, f, w, scale = rope_case(T, Hq, Hk, D, 32, dt, D + Hk)
+    dy = [randn(T, H, D, seed=H + 50, dtype=dt) for H in (Hq, Hk)]
+    out = kda.kda_qk_norm_rope_bwd(q, k, *dy, pos, f, *w, eps=0.0, rope_scale=scale)
+    for i, (x, d, wi) in enumerate(zip((q, k), dy, w)):
+        dx, dw = paged.norm_rope_grad(f64(x), f64(d), f64(pos), f64(f), f64(wi), 0.0, True, False, scale)
+        xs, big = f64(x), 2 * np.abs(f64(d)).max(-1, keepdims=True) * scale
+        rstd = 1 / np.sqrt((xs * xs).mean(-1, keepdims=True))
+        n = np.abs(xs * rstd)
+        assert (np.abs(f64(out[i]) - dx) <= 64 * U * rstd * big * f64(wi).max() * (1 + n)
+                + U * np.abs(dx)).all(), "qk"[i]
+        tol = (40 + T * x.shape[1]) * U * (big * n).sum((0, 1))
+        assert (np.abs(f64(out[2 + i]) - dw) <= tol).all(), "qk"[i]
+
+
 # ---------------------------------------------------------------- decode
 def decode_case(lens, Hq, Hk, D, page, dtype, seed, spare=2, extra=1):
     """Pages dealt from a shuffled pool; everything no request reaches is NaN, and so is
