@@ -129,6 +129,13 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&r)[8])
                  : "memory");
 }
 
+// O of the weights' two parts.  An infinite value makes the first infinite (or NaN, as it
+// should); times the rest of a weight, which may be zero or negative, it would make NaN.
+__device__ __forceinline__ float both_parts(float hi, float lo)
+{
+    return fabsf(hi) < CUDART_INF_F ? hi + lo : hi;
+}
+
 // Sums of N values over the warp's lanes: each step halves the values a lane sums, so that
 // l[0] of lane 32 / N * g is the sum of the lanes' l[g].
 template <int N, int O = 16, int M>
@@ -345,7 +352,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                 tmem_ld8(tlane + C::TM_O + wg * HW + g0, x);
                 tmem_ld8(tlane + C::TM_O + HP + wg * HW + g0, y);
 #pragma unroll
-                for (int g = 0; g < 8; ++g) x[g] += y[g];
+                for (int g = 0; g < 8; ++g) x[g] = both_parts(x[g], y[g]);
             };
             auto add_total = [&](int g0, float (&x)[8]) {
                 float y[8];
@@ -497,7 +504,7 @@ paged_decode_tc_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Map
                 float x[HW];
                 tmem_ld(tlane + C::TM_O + HP + wg * HW, x);
 #pragma unroll
-                for (int g = 0; g < HW; ++g) acc[g] += x[g];
+                for (int g = 0; g < HW; ++g) acc[g] = both_parts(acc[g], x[g]);
             }
             if (__builtin_expect(w.tile1 - w.tile0 > kRun, 0)) {
 #pragma unroll

@@ -522,6 +522,29 @@ def test_decode_repeats_bit_for_bit_and_in_a_graph(dtype):
     assert torch.equal(out, b)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("L,Hq", [(1, 4), (3, 20), (130, 8), (7000, 4)])
+def test_decode_infinite_values(dtype, D, L, Hq):
+    """An infinite value makes its channel infinite whatever its weight, both signs make it NaN,
+    and no other channel notices."""
+    q, kc, vc, table, lens = decode_case([L, 60], Hq, 1, D, 64, dtype, L + D)
+    fine, lse = check_decode((q, kc, vc, table, lens))
+    at = lambda t: (int(table[0, t // 64]), 0, t % 64)
+    for t in {0, L // 2, L - 1}:
+        vc[at(t)][3] = float("inf")
+        vc[at(t)][D - 1] = -float("inf")
+    vc[at(0)][10], vc[at(L - 1)][10] = float("inf"), float("inf") if L == 1 else -float("inf")
+    vc[at(L // 2)][20] = float("nan")
+    out, lse2 = kda.kda_paged_decode(q, kc, vc, table, lens, want_lse=True)
+    assert torch.equal(lse2, lse) and torch.equal(out[1], fine[1])
+    assert bool((out[0, :, 3] == float("inf")).all()) and bool((out[0, :, D - 1] == -float("inf")).all())
+    assert bool((out[0, :, 10] == float("inf")).all() if L == 1 else out[0, :, 10].isnan().all())
+    assert bool(out[0, :, 20].isnan().all())
+    rest = [c for c in range(D) if c not in (3, 10, 20, D - 1)]
+    assert torch.equal(out[0][:, rest], fine[0][:, rest])
+
+
 # ---------------------------------------------------------------- beside other kernels
 def test_decode_behind_the_chunk_scan():
     """The scan lets the next kernel start early and takes tensor memory of its own: the two in
