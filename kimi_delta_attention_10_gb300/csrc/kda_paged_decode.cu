@@ -320,7 +320,8 @@ paged_decode_kernel(DecodeArgs a, DecodeShape sh, const __grid_constant__ Maps m
                 for (int j = 0; j < W; ++j) {
                     const int k = turn + j < W ? turn + j : turn + j - W;
                     const float2 ml = s_ml[k * GT + g];
-                    if (top != -CUDART_INF_F) sum += ml.y * exp2f(ml.x - top);
+                    // without a maximum the sums are zero, or NaN where scores are
+                    sum += top == -CUDART_INF_F ? ml.y : ml.y * exp2f(ml.x - top);
                     x += s_o[(k * kMerge + g - gb) * D + ch];
                 }
                 const int64_t r = r0 + g;
@@ -394,7 +395,12 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(DecodeArgs a, Decode
             float m = top;
 #pragma unroll
             for (int j = 0; j < kMany; ++j) m = fmaxf(m, ml[j].x);
-            if (m == -CUDART_INF_F) return;
+            if (m == -CUDART_INF_F) {
+                // no score but -infinity and NaN so far: sums of zero, or NaN
+#pragma unroll
+                for (int j = 0; j < kMany; ++j) l += ml[j].y;
+                return;
+            }
             const float old = exp2f(top - m);
             top = m;
             l *= old;

@@ -545,6 +545,24 @@ def test_decode_infinite_values(dtype, D, L, Hq):
     assert torch.equal(out[0][:, rest], fine[0][:, rest])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D,Hq", [(64, 4), (128, 20)])
+@pytest.mark.parametrize("lens", [[3, 60], [5000, 700, 1]])
+def test_decode_scores_that_are_no_numbers(dtype, D, Hq, lens):
+    """A query that holds NaN makes its head's output and log-sum-exp NaN, one whose scores are
+    all -infinity sums nothing (lse -infinity, output 0 / 0); the other heads notice neither."""
+    q, kc, vc, table, seq = decode_case(lens, Hq, 1, D, 64, dtype, 70 + D)
+    kc[..., 5] = torch.where(kc[..., 5].isnan(), kc[..., 5], torch.ones_like(kc[..., 5]))
+    fine, lse = check_decode((q, kc, vc, table, seq))
+    q[:, 1, 0] = float("nan")
+    q[:, 2, 5] = -float("inf")
+    out, lse2 = kda.kda_paged_decode(q, kc, vc, table, seq, want_lse=True)
+    assert bool(out[:, 1:3].isnan().all()) and bool(lse2[:, 1].isnan().all())
+    assert bool((lse2[:, 2] == -float("inf")).all())
+    rest = [h for h in range(Hq) if h not in (1, 2)]
+    assert torch.equal(out[:, rest], fine[:, rest]) and torch.equal(lse2[:, rest], lse[:, rest])
+
+
 # ---------------------------------------------------------------- beside other kernels
 def test_decode_behind_the_chunk_scan():
     """The scan lets the next kernel start early and takes tensor memory of its own: the two in
