@@ -174,7 +174,7 @@ __device__ __forceinline__ int lane_turn(const RopeArgs& a, const float2* table,
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
             c[j] = make_float2(1.f, 1.f);
-            s[j] = make_float2(0.f, 0.f);
+            s[j] = make_float2(-0.f, -0.f);               // a zero keeps its sign too
         }
         return chan;
     }
@@ -202,6 +202,16 @@ __device__ __forceinline__ int lane_turn(const RopeArgs& a, const float2* table,
         }
         return second ? chan - h : chan + h;
     }
+}
+
+// x c + o s.  A channel that is not rotated takes nothing of another, which may be infinite:
+// in the half layout its o is zero.
+template <bool kInter>
+__device__ __forceinline__ float2 turn(float2 x, float2 o, float2 c, float2 s, bool turned)
+{
+    float2 y = mul2(x, c);
+    if (!kInter || turned) y = fma2(o, s, y);
+    return y;
 }
 
 // N pairs of consecutive weights.
@@ -261,10 +271,14 @@ __global__ void __launch_bounds__(NT, 4) qk_rope_kernel(RopeArgs a, int log_slic
     constexpr int kKinds = kAppend ? 3 : 2;
     __shared__ __align__(16) float2 table[NW][kMaxPairs];
     __shared__ __align__(16) Common<D> common;
-    __shared__ __align__(16) unsigned char ring[NW][kRing][512];
+    __shared__ __align__(16) unsigned char ring[NW][kRing][kInter ? 512 : 528];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane / L::LPR, chan = (lane % L::LPR) * L::VEC;
-    const int partner = partner_lane(a, lane, chan, L::VEC);
+    const bool turned = chan < a.rot;
+    // where in a slot of the ring the other channels of the lane's pairs lie; zeros for none
+    const int partner = turned ? partner_lane(a, lane, chan, L::VEC) * 16 : 512;
+    if (!kInter && lane < kRing)
+        *reinterpret_cast<uint4*>(&ring[warp][lane][512]) = make_uint4(0, 0, 0, 0);
     const int64_t items = (int64_t)a.T << log_slices;
     const int nwarps = gridDim.x * NW;
     const int step = L::RPW << log_slices;
@@ -365,7 +379,7 @@ __global__ void __launch_bounds__(NT, 4) qk_rope_kernel(RopeArgs a, int log_slic
                 unpack2<NP>(lds16(at + lane * 16), x);
                 if (kind < 2) {
                     float2 o[NP];
-                    partners<kInter, NP>(x, at + partner * 16, o);
+                    partners<kInter, NP>(x, at + partner, o);
                     request();
                     float inv = 1.f;
                     if (a.norm) {
@@ -376,7 +390,7 @@ __global__ void __launch_bounds__(NT, 4) qk_rope_kernel(RopeArgs a, int log_slic
                     }
 #pragma unroll
                     for (int j = 0; j < NP; ++j)
-                        x[j] = mul2(fma2(o[j], s[j], mul2(x[j], c[j])), both(inv));
+                        x[j] = mul2(turn<kInter>(x[j], o[j], c[j], s[j], turned), both(inv));
                 } else {
                     request();
                 }
@@ -415,18 +429,19 @@ __device__ __forceinline__ void block_dw(const float2 (&dw)[NP], float (*red)[D]
     }
 }
 
-// A warp's ring of x and dy rows; DYB: bytes of dy a lane takes (8, 16 or 32).
-template <typename TIn, typename TDy, int D> struct BwdRing {
+// A warp's ring of x and dy rows, in the half layout with zeros at each slot's end; DYB: bytes
+// of dy a lane takes (8, 16 or 32).
+template <typename TIn, typename TDy, int D, bool kInter> struct BwdRing {
     static constexpr int DYB = Layout<TIn, D>::VEC * (int)sizeof(TDy);
     static constexpr int SLOTS = DYB == 32 ? 3 : 4;
-    static constexpr int BYTES = 512 + 32 * DYB;
+    static constexpr int ZEROS = 512 + 32 * DYB, BYTES = ZEROS + (kInter ? 0 : DYB == 32 ? 32 : 16);
 };
 
 template <typename TIn, typename TDy, typename TOut, int D, bool kInter>
 __global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int log_slices)
 {
     using L = Layout<TIn, D>;
-    using R = BwdRing<TIn, TDy, D>;
+    using R = BwdRing<TIn, TDy, D, kInter>;
     constexpr int NP = L::VEC / 2, DYB = R::DYB, S = R::SLOTS;
     __shared__ __align__(16) float2 table[NW][kMaxPairs];
     __shared__ __align__(16) Common<D> common;
@@ -434,7 +449,11 @@ __global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int log_
     static_assert(sizeof(ring) >= NW * D * sizeof(float), "the sums of dw reuse the ring");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane / L::LPR, chan = (lane % L::LPR) * L::VEC;
-    const int partner = partner_lane(a, lane, chan, L::VEC);
+    const bool turned = chan < a.rot;
+    const int partner = turned ? 512 + partner_lane(a, lane, chan, L::VEC) * DYB : R::ZEROS;
+    if (!kInter && lane < S)
+        for (int i = R::ZEROS; i < R::BYTES; i += 16)
+            *reinterpret_cast<uint4*>(&ring[warp][lane][i]) = make_uint4(0, 0, 0, 0);
     const int64_t items = (int64_t)a.T << log_slices;
     const int nwarps = gridDim.x * NW;
     const int step = L::RPW << log_slices;
@@ -504,7 +523,8 @@ __global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int log_
         float2 c[NP], s[NP];                               // of the transposed rotation
         lane_turn<L::VEC, kInter>(a, table[warp], chan, c, s);
 #pragma unroll
-        for (int j = 0; j < NP; ++j) s[j] = make_float2(-s[j].x, -s[j].y);
+        for (int j = 0; j < NP; ++j)
+            if (turned) s[j] = make_float2(-s[j].x, -s[j].y);
         int get = 0;
 #pragma unroll
         for (int kind = 0; kind < 2; ++kind) {
@@ -530,7 +550,7 @@ __global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int log_
                         o[0] = make_float2(d[0].y, d[0].x);
                         o[1] = make_float2(d[1].y, d[1].x);
                     } else {
-                        const uint2 z = *reinterpret_cast<const uint2*>(at + 512 + partner * 8);
+                        const uint2 z = *reinterpret_cast<const uint2*>(at + partner);
                         unpack2<4>(make_uint4(z.x, z.y, 0, 0), v);
                         o[0] = v[0];
                         o[1] = v[1];
@@ -541,7 +561,7 @@ __global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int log_
                     for (int k = 0; k < DYB / 16; ++k) {
                         float2 v[PV], z[PV];
                         unpack2<PV>(lds16(at + 512 + lane * DYB + 16 * k), v);
-                        partners<kInter, PV>(v, at + 512 + partner * DYB + 16 * k, z);
+                        partners<kInter, PV>(v, at + partner + 16 * k, z);
 #pragma unroll
                         for (int j = 0; j < PV; ++j) {
                             d[k * PV + j] = v[j];
@@ -552,7 +572,7 @@ __global__ void __launch_bounds__(NT, 2) qk_rope_bwd_kernel(RopeArgs a, int log_
                 request();
                 get = (get + 1) % S;
 #pragma unroll
-                for (int j = 0; j < NP; ++j) d[j] = fma2(o[j], s[j], mul2(d[j], c[j]));
+                for (int j = 0; j < NP; ++j) d[j] = turn<kInter>(d[j], o[j], c[j], s[j], turned);
                 if (a.norm) {
                     float2 ss = mul2(x[0], x[0]), hx = make_float2(0.f, 0.f);
 #pragma unroll

@@ -333,6 +333,34 @@ def test_rope_bwd_without_epsilon(dt, D, Hq, Hk):
         assert (np.abs(f64(out[2 + i]) - dw) <= tol).all(), "qk"[i]
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("D,rot", [(64, 0), (64, 32), (128, 96)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_leaves_other_channels_alone(dt, D, rot, inter):
+    """Channels that are not rotated, without the norm: the very values, infinities and NaN
+    among them, and nothing of theirs in their neighbours; forward, append and backward."""
+    q, k, v, pos, f, _, _ = rope_case(6, 3, 2, D, rot, dt, D + rot, start=1)
+    fine = kda.kda_qk_norm_rope(q, k, pos, f, qk_norm=False, interleaved=inter)
+    for x in (q, k):
+        x[0, 0, rot + 3], x[1, 1, D - 1], x[2, 0, rot + 8] = float("inf"), -float("inf"), float("nan")
+    y = kda.kda_qk_norm_rope(q, k, pos, f, qk_norm=False, interleaved=inter)
+    g = kda.kda_qk_norm_rope_bwd(q, k, q.contiguous(), k.contiguous(), pos, f, qk_norm=False,
+                                 interleaved=inter, grad_dtype=dt)
+    kc, vc = torch.zeros(2, 1, 2, 8, D, dtype=dt, device="cuda").unbind(0)
+    a = kda.kda_qk_norm_rope_append(q, k, v, pos, ints(range(6), torch.int64), kc, vc, f,
+                                    qk_norm=False, interleaved=inter)
+    bits = lambda t: t.contiguous().view(torch.int16 if dt == BF16 else torch.int32)
+    for x, out, grad, ref in ((q, y[0], g[0], fine[0]), (k, y[1], g[1], fine[1])):
+        want = x[..., rot:].clone()
+        nan = want.isnan()
+        for got in (out, grad):
+            assert torch.equal(got[..., rot:].isnan(), nan)
+            assert torch.equal(bits(got[..., rot:])[~nan], bits(want)[~nan])
+        assert torch.equal(out[..., :rot], ref[..., :rot])
+    assert torch.equal(bits(a), bits(y[0]))
+    assert torch.equal(bits(kc[0, :, :6].transpose(0, 1)), bits(y[1]))
+
+
 # ---------------------------------------------------------------- decode
 def decode_case(lens, Hq, Hk, D, page, dtype, seed, spare=2, extra=1):
     """Pages dealt from a shuffled pool; everything no request reaches is NaN, and so is
