@@ -8,7 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
-#include <c10/cuda/CUDAGraphsC10Utils.h>
+#include <c10/cuda/CUDAException.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -202,6 +202,14 @@ ScalarType dtype_or(PyObject* o, ScalarType otherwise)
     return reinterpret_cast<THPDtype*>(o)->scalar_type;
 }
 
+// Whether the call's stream, which need not be the current one, is being captured.
+bool captures(const Stream& stream)
+{
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    C10_CUDA_CHECK(cudaStreamIsCapturing(stream.s.stream(), &st));
+    return st != cudaStreamCaptureStatusNone;
+}
+
 // The workspace of a call that was given none: one buffer per stream, kept and grown,
 // since calls on one stream are ordered.  A captured call gets one of its graph's own.
 struct Workspace {
@@ -219,17 +227,16 @@ Workspace workspace(PyObject* given, int64_t bytes, const Tensor& t, const Strea
     }
     w.bytes = bytes;
     const auto bytes_like = like(t, ScalarType::Byte);
-    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
+    // On the stream that uses it: memory that is given up waits for that stream's calls, and a
+    // captured stream's belongs to its graph.
+    const c10::cuda::CUDAStreamGuard guard(stream.s);
+    if (captures(stream)) {
         w.keep = at::empty({bytes}, bytes_like);
     } else {
         // never destroyed: the allocator may be gone first when the process ends
         static auto* kept = new std::map<std::pair<int, cudaStream_t>, Tensor>;
         Tensor& mine = (*kept)[{t.device().index(), stream.s.stream()}];
-        if (!mine.defined() || mine.numel() < bytes) {
-            // on the stream that uses it, so that a smaller one's memory waits for its calls
-            const c10::cuda::CUDAStreamGuard guard(stream.s);
-            mine = at::empty({bytes}, bytes_like);
-        }
+        if (!mine.defined() || mine.numel() < bytes) mine = at::empty({bytes}, bytes_like);
         w.keep = mine;
     }
     w.p = w.keep.data_ptr();

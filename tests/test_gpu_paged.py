@@ -636,3 +636,55 @@ def test_decode_long_rows_lose_nothing(D):
     assert (err <= tol).all(), float((err / tol).max())
     many = ref_lse + np.log(L / (pages * P))
     assert (np.abs(f64(lse) - many) <= 1024 * U + 12 * U * reach + 8 * U * np.abs(many)).all()
+
+
+# ---------------------------------------------------------------- streams
+def test_a_capture_on_the_given_stream_has_its_own_workspace():
+    """The current stream is not the one that is captured: the graph must not hold the buffer
+    that is kept for eager calls on that stream, which a larger call replaces."""
+    case, big = decode_case([3000, 17, 900], 8, 2, 128, 64, BF16, 80), decode_case([4000], 64, 1, 128, 64, BF16, 81)
+    want, lse = kda.kda_paged_decode(*case, want_lse=True)
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    out, lse2 = torch.zeros_like(want), torch.zeros_like(lse)
+    kda.kda_paged_decode(*case, out=out, lse=lse2, stream=side)          # a buffer is kept
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        g.capture_begin()
+    kda.kda_paged_decode(*case, out=out, lse=lse2, stream=side)
+    with torch.cuda.stream(side):
+        g.capture_end()
+    kda.kda_paged_decode(*big, stream=side)                               # and replaced
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        taken = [torch.full((kda.paged_decode_workspace_size(3, 8, 2),), 255, dtype=torch.uint8, device="cuda")
+                 for _ in range(4)]
+    out.zero_()
+    lse2.zero_()
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse2, lse)
+    assert all(bool((t == 255).all()) for t in taken)
+
+
+def test_a_forked_stream_of_a_capture_has_its_workspace_there():
+    """The current stream is captured, the call goes to a stream forked from it: its workspace
+    belongs to that stream, not to the one whose next tensor would get the memory at once."""
+    case = decode_case([3000, 17, 900], 8, 2, 128, 64, BF16, 80)
+    want, lse = kda.kda_paged_decode(*case, want_lse=True)
+    out, lse2, side = torch.zeros_like(want), torch.zeros_like(lse), torch.cuda.Stream()
+    bytes_ = kda.paged_decode_workspace_size(3, 8, 2)
+    mine = lambda: sum(s["total_size"] for s in torch.cuda.memory_snapshot()
+                       if s["stream"] == side.cuda_stream)
+    torch.cuda.synchronize()
+    g, before = torch.cuda.CUDAGraph(), mine()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        kda.kda_paged_decode(*case, out=out, lse=lse2, stream=side)
+        other = torch.full((bytes_,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.current_stream().wait_stream(side)
+    assert mine() >= before + bytes_
+    for _ in range(5):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want) and torch.equal(lse2, lse) and bool((other == 255).all())
