@@ -170,22 +170,31 @@ int32_t flag(PyObject* o)
     return x;
 }
 
-// The stream of a call: the current one of the tensors' device, or the one given.
-struct Stream {
-    c10::cuda::CUDAStream s;
+// The stream of a call: the current one of the tensors' device, or the one given, which is
+// the current one while this lives.  So what the call allocates belongs to the stream that
+// writes it: the memory waits for that stream's calls, and a captured stream's is its graph's.
+class Stream {
+    static c10::cuda::CUDAStream find(PyObject* o, const Tensor& t)
+    {
+        const c10::DeviceIndex dev = t.device().index();
+        if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev);
+        PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+        if (!h) throw Raised();
+        void* p = PyLong_AsVoidPtr(h);
+        Py_DECREF(h);
+        if (!p && PyErr_Occurred()) throw Raised();
+        return c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), dev);
+    }
+    c10::cuda::OptionalCUDAStreamGuard guard;
+
+public:
+    const c10::cuda::CUDAStream s;
+    Stream(PyObject* o, const Tensor& t) : s(find(o, t))
+    {
+        if (o != Py_None) guard.reset_stream(s);
+    }
     kda_stream_t handle() const { return reinterpret_cast<kda_stream_t>(s.stream()); }
 };
-Stream stream_of(PyObject* o, const Tensor& t)
-{
-    const c10::DeviceIndex dev = t.device().index();
-    if (o == Py_None) return {c10::cuda::getCurrentCUDAStream(dev)};
-    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-    if (!h) throw Raised();
-    void* p = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-    if (!p && PyErr_Occurred()) throw Raised();
-    return {c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), dev)};
-}
 
 at::TensorOptions like(const Tensor& t, ScalarType dtype)
 {
@@ -227,9 +236,6 @@ Workspace workspace(PyObject* given, int64_t bytes, const Tensor& t, const Strea
     }
     w.bytes = bytes;
     const auto bytes_like = like(t, ScalarType::Byte);
-    // On the stream that uses it: memory that is given up waits for that stream's calls, and a
-    // captured stream's belongs to its graph.
-    const c10::cuda::CUDAStreamGuard guard(stream.s);
     if (captures(stream)) {
         w.keep = at::empty({bytes}, bytes_like);
     } else {
@@ -308,6 +314,7 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n)
             raise(PyExc_ValueError, "block_table must have shape [%lld, max_pages]", (long long)N);
         const auto i32 = ScalarType::Int;
         const int32_t* c = pointer<int32_t>(cached, "cached_lens", i32);
+        const Stream s(a[12], cached);
         const Tensor lens = output(a[7], "seq_lens", {N}, cached, i32),
                      pos = output(a[8], "positions", {T}, cached, i32),
                      slots = output(a[9], "slots", {T}, cached, ScalarType::Long),
@@ -321,7 +328,7 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n)
             pointer<int32_t>(lens, "seq_lens", i32, N), pointer<int32_t>(pos, "positions", i32, T),
             pointer<int64_t>(slots, "slots", ScalarType::Long, T),
             pointer<int32_t>(end, "free_end", i32, 1), any_pointer<int32_t>(a[11], "status"),
-            stream_of(a[12], cached).handle());
+            s.handle());
         if (st != KDA_OK) return status(st);
         return tuple({wrap(lens), wrap(pos), wrap(slots), wrap(end)});
     });
@@ -375,13 +382,14 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n)
         const Heads h(q, k);
         const Rows qr = rows(q, "q", dt, h.T, h.Hq, h.D), kr = rows(k, "k", dt, h.T, h.Hk, h.D);
         const Rope r(a + 2, h.T, h.D);
+        const Stream s(a[13], q);
         const Tensor qo = output(a[10], "q_out", {h.T, h.Hq, h.D}, q, dtype_or(a[12], dt));
         const auto odt = qo.scalar_type();
         const Tensor ko = output(a[11], "k_out", {h.T, h.Hk, h.D}, q, odt);
         const kda_status st = lib.rope(
             qr.p, qr.stride, kr.p, kr.stride, code(dt), r.positions, r.inv_freq, r.rot, r.inter, r.scale,
             r.qw, r.kw, r.eps, r.norm, h.T, h.Hq, h.Hk, h.D, dense(qo, "q_out", odt, h.T, h.Hq, h.D),
-            dense(ko, "k_out", odt, h.T, h.Hk, h.D), code(odt), stream_of(a[13], q).handle());
+            dense(ko, "k_out", odt, h.T, h.Hk, h.D), code(odt), s.handle());
         if (st != KDA_OK) return status(st);
         return tuple({wrap(qo), wrap(ko)});
     });
@@ -408,6 +416,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n)
         const Rows qr = rows(q, "q", dt, h.T, h.Hq, h.D), kr = rows(k, "k", dt, h.T, h.Hk, h.D),
                    vr = rows(v, "v", dt, h.T, h.Hk, h.D);
         const Rope r(a + 6, h.T, h.D);
+        const Stream s(a[16], q);
         const Tensor qo = output(a[14], "q_out", {h.T, h.Hq, h.D}, q, cdt);
         const kda_status st = lib.append(
             qr.p, qr.stride, kr.p, kr.stride, vr.p, vr.stride, code(dt), r.positions,
@@ -416,7 +425,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n)
             dense(qo, "q_out", cdt, h.T, h.Hq, h.D), pointer(kc, "k_cache", cdt),
             pointer(vc, "v_cache", cdt), code(cdt), as_i32(kc.size(0), "the number of pages"),
             as_i32(kc.size(2), "page_size"), any_pointer<int32_t>(a[15], "status"),
-            stream_of(a[16], q).handle());
+            s.handle());
         if (st != KDA_OK) return status(st);
         return wrap(qo);
     });
@@ -431,13 +440,13 @@ PyObject* norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n)
         const Heads h(q, k);
         const Rows qr = rows(q, "q", dt, h.T, h.Hq, h.D), kr = rows(k, "k", dt, h.T, h.Hk, h.D);
         const Rope r(a + 4, h.T, h.D);
+        const Stream s(a[16], q);
         const Tensor qg = output(a[12], "q_grad", {h.T, h.Hq, h.D}, q, dtype_or(a[14], ScalarType::Float));
         const auto gdt = qg.scalar_type();
         const Tensor kg = output(a[13], "k_grad", {h.T, h.Hk, h.D}, q, gdt);
         Tensor wq, wk;
         if (r.norm && r.qw) wq = at::empty({h.D}, like(q, ScalarType::Float));
         if (r.norm && r.kw) wk = at::empty({h.D}, like(q, ScalarType::Float));
-        const Stream s = stream_of(a[16], q);
         Workspace w;
         if (wq.defined() || wk.defined() || a[15] != Py_None) {
             static auto* known = new std::map<std::array<int64_t, 4>, int64_t>;
@@ -472,13 +481,13 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n)
             raise(PyExc_ValueError, "block_table must have shape [%lld, max_pages]", (long long)N);
         const auto dt = kc.scalar_type(), f32 = ScalarType::Float;
         const void* qp = pointer(q, "q", dt);
+        const Stream s(a[12], q);
         const float scale = a[5] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : number(a[5], "scale");
         const Tensor out = output(a[6], "out", {N, Hq, D}, q, dtype_or(a[7], dt));
         const auto odt = out.scalar_type();
         Tensor lse;
         if (a[8] != Py_None) lse = tensor(a[8], "lse");
         else if (flag(a[9])) lse = at::empty({N, Hq}, like(q, f32));
-        const Stream s = stream_of(a[12], q);
         static auto* known = new std::map<std::array<int64_t, 4>, int64_t>;
         const int64_t bytes = a[11] != Py_None ? 0 : size_of(
             [&](int64_t* b) { return lib.decode_size(as_i32(N, "the number of requests"), Hq, Hk, D, b); },

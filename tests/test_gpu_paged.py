@@ -688,3 +688,31 @@ def test_a_forked_stream_of_a_capture_has_its_workspace_there():
         out.zero_()
         g.replay()
         assert torch.equal(out, want) and torch.equal(lse2, lse) and bool((other == 255).all())
+
+
+def test_outputs_belong_to_the_call_s_stream():
+    """What a call allocates is memory of the stream that writes it: neither a block whose
+    kernels on the current stream are still to come, nor given to that stream's next tensor."""
+    q, k, v, pos, f, w, _ = rope_case(40, 8, 2, 128, 64, BF16, 90)
+    q, k = q.contiguous(), k.contiguous()
+    kc, vc = torch.zeros(2, 8, 2, 16, 128, dtype=BF16, device="cuda").unbind(0)
+    table, lens = ints([list(range(3))]), ints([40])
+    none, cu, planned, free = ints([0]), ints([0, 40]), ints([[-1] * 3]), ints([2, 1, 0])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def calls(**kw):
+        plan = kda.kda_page_plan(none, cu, planned, free, 16, 40, **kw)
+        return [*plan, *kda.kda_qk_norm_rope(q, k, pos, f, *w, **kw),
+                kda.kda_qk_norm_rope_append(q, k, v, pos, plan[2], kc, vc, f, *w, **kw),
+                *kda.kda_qk_norm_rope_bwd(q, k, q, k, pos, f, *w, **kw),
+                *kda.kda_paged_decode(q[:1], kc, vc, table, lens, want_lse=True, **kw)]
+
+    want = calls()
+    torch.cuda.synchronize()
+    got = calls(stream=side)
+    torch.cuda.synchronize()
+    assert len(got) == 13 and all(torch.equal(a, b) for a, b in zip(got, want))
+    at = {b["address"]: seg["stream"] for seg in torch.cuda.memory_snapshot() for b in seg["blocks"]}
+    assert [at[t.data_ptr()] for t in got] == [side.cuda_stream] * 13
+    assert torch.cuda.current_stream() != side
