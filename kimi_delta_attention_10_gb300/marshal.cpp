@@ -170,8 +170,9 @@ int32_t flag(PyObject* o)
     return x;
 }
 
-// The stream of a call: the current one of the tensors' device, or the one given, which is
-// the current one while this lives.  So what the call allocates belongs to the stream that
+// The stream of a call: the current one of the tensors' device, or the one given.  While this
+// lives the device and the stream are the current ones: the library asks the device its
+// sizes and launches there, and what the call allocates belongs to the stream that
 // writes it: the memory waits for that stream's calls, and a captured stream's is its graph's.
 class Stream {
     static c10::cuda::CUDAStream find(PyObject* o, const Tensor& t)
@@ -185,13 +186,15 @@ class Stream {
         if (!p && PyErr_Occurred()) throw Raised();
         return c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), dev);
     }
-    c10::cuda::OptionalCUDAStreamGuard guard;
+    c10::cuda::OptionalCUDAGuard device;
+    c10::cuda::OptionalCUDAStreamGuard current;
 
 public:
     const c10::cuda::CUDAStream s;
     Stream(PyObject* o, const Tensor& t) : s(find(o, t))
     {
-        if (o != Py_None) guard.reset_stream(s);
+        if (c10::cuda::current_device() != t.device().index()) device.set_device(t.device());
+        if (o != Py_None) current.reset_stream(s);
     }
     kda_stream_t handle() const { return reinterpret_cast<kda_stream_t>(s.stream()); }
 };
@@ -285,9 +288,24 @@ template <size_t N> PyObject* tuple(PyObject* const (&items)[N])
     return t;
 }
 
+// A call's CUDA tensors are on one device, which Stream makes the current one.
+void need_one_device(PyObject* const* a, Py_ssize_t n)
+{
+    int first = -1;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        if (!THPVariable_Check(a[i])) continue;
+        const at::Device d = THPVariable_Unpack(a[i]).device();
+        if (!d.is_cuda()) continue;            // refused by name, with what it should be
+        if (first < 0) first = d.index();
+        if (d.index() != first)
+            raise(PyExc_ValueError, "all tensors of a call must be on one device, not cuda:%d and cuda:%d",
+                  first, (int)d.index());
+    }
+}
+
 // What every entry does: its arguments counted, Python errors and C++ exceptions caught.
 // A refusal by the library comes back as its status, an int.
-template <typename F> PyObject* entry(Py_ssize_t got, Py_ssize_t want, F body)
+template <typename F> PyObject* entry(PyObject* const* a, Py_ssize_t got, Py_ssize_t want, F body)
 {
     HANDLE_TH_ERRORS
     if (got != want) return PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, got);
@@ -296,6 +314,7 @@ template <typename F> PyObject* entry(Py_ssize_t got, Py_ssize_t want, F body)
         return nullptr;
     }
     try {
+        need_one_device(a, got);
         return body();
     } catch (const Raised&) {
         return nullptr;
@@ -306,7 +325,7 @@ PyObject* status(kda_status st) { return PyLong_FromLong(st); }
 
 PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return entry(n, 13, [&]() -> PyObject* {
+    return entry(a, n, 13, [&]() -> PyObject* {
         const Tensor &cached = tensor(a[0], "cached_lens"), &cu = tensor(a[1], "cu_seqlens"),
                      &table = tensor(a[2], "block_table"), &free = tensor(a[3], "free_pages");
         const int64_t N = cached.numel(), T = integer(a[5], "num_tokens");
@@ -376,7 +395,7 @@ struct Heads {
 
 PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return entry(n, 14, [&]() -> PyObject* {
+    return entry(a, n, 14, [&]() -> PyObject* {
         const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
         const auto dt = q.scalar_type();
         const Heads h(q, k);
@@ -407,7 +426,7 @@ void need_caches(const Tensor& kc, const Tensor& vc, int64_t Hk, int64_t D)
 
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return entry(n, 17, [&]() -> PyObject* {
+    return entry(a, n, 17, [&]() -> PyObject* {
         const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"),
                      &kc = tensor(a[4], "k_cache"), &vc = tensor(a[5], "v_cache");
         const auto dt = q.scalar_type(), cdt = kc.scalar_type();
@@ -433,7 +452,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n)
 
 PyObject* norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return entry(n, 17, [&]() -> PyObject* {
+    return entry(a, n, 17, [&]() -> PyObject* {
         const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &dq = tensor(a[2], "dq_out"),
                      &dk = tensor(a[3], "dk_out");
         const auto dt = q.scalar_type(), ydt = dq.scalar_type();
@@ -469,7 +488,7 @@ PyObject* norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n)
 
 PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return entry(n, 13, [&]() -> PyObject* {
+    return entry(a, n, 13, [&]() -> PyObject* {
         const Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache"),
                      &table = tensor(a[3], "block_table"), &lens = tensor(a[4], "seq_lens");
         if (q.dim() != 3) raise(PyExc_ValueError, "q must have shape [N, Hq, D]");

@@ -198,6 +198,26 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
                              workspace=torch.zeros(16))
 
 
+def test_binding_refuses_tensors_of_two_devices(lib):
+    """Before anything is allocated or launched; the tensors have a device and no memory."""
+    fake = pytest.importorskip("torch._subclasses.fake_tensor")
+    with fake.FakeTensorMode():
+        on = lambda d, *s, dtype=torch.float32: torch.empty(*s, dtype=dtype, device=f"cuda:{d}")
+        i32 = lambda d, *s: on(d, *s, dtype=torch.int32)
+        x, c = on(1, 3, 2, 64), on(1, 2, 2, 16, 64)
+        two = pytest.raises(ValueError, match="one device, not cuda:1 and cuda:0")
+        with two:
+            kda.kda_page_plan(i32(1, 2), i32(1, 3), i32(0, 2, 4), i32(1, 5), 16, 0)
+        with two:
+            kda.kda_qk_norm_rope(x, x, i32(1, 3), None, q_weight=on(0, 64))
+        with two:
+            kda.kda_qk_norm_rope_append(x, x, x, i32(1, 3), on(1, 3, dtype=torch.int64), c, on(0, 2, 2, 16, 64), None)
+        with two:
+            kda.kda_qk_norm_rope_bwd(x, x, x, on(0, 3, 2, 64), i32(1, 3), None)
+        with two:
+            kda.kda_paged_decode(x, c, c, i32(1, 3, 1), i32(1, 3), workspace=on(0, 1 << 20))
+
+
 # ---------------------------------------------------------------- frequencies
 HALF = 2.0 ** -24      # one rounding to FP32; the FP64 work before it adds far less
 
