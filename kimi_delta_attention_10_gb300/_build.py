@@ -1,5 +1,5 @@
 """Builds libkda_gb300.so in-tree with nvcc for sm_103a (one -gencode), and the CPython
-module _marshal.so (g++, against the headers of the installed PyTorch)."""
+module _marshal (g++, against the headers of the installed PyTorch)."""
 from __future__ import annotations
 
 import glob
@@ -7,6 +7,7 @@ import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
@@ -18,7 +19,6 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libkda_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 MARSHAL_SRC = os.path.join(PKG, "marshal.cpp")
-MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -44,10 +44,17 @@ def _deps():
             glob.glob(os.path.join(INCLUDE, "*.h")) + [MARSHAL_SRC, os.path.abspath(__file__)])
 
 
+def marshal_path() -> str:
+    """The _marshal module's file.  It uses interfaces of the interpreter and of PyTorch that
+    change between versions, so its name says which it was compiled for."""
+    import torch
+    return os.path.join(PKG, f"_marshal.{sys.implementation.cache_tag}-torch-{torch.__version__}.so")
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(MARSHAL_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(marshal_path()):
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(MARSHAL_PATH))
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(marshal_path()))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -76,11 +83,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     inc = ["-I", INCLUDE, "-I", CSRC]
 
     def compile_marshal(_):
-        tmp = MARSHAL_PATH + f".tmp{os.getpid()}"
+        tmp = marshal_path() + f".tmp{os.getpid()}"
         r = subprocess.run(marshal_command(tmp), capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stdout}{r.stderr}")
-        os.replace(tmp, MARSHAL_PATH)
+        os.replace(tmp, marshal_path())
 
     def compile_one(src):
         obj = os.path.join(obj_dir, os.path.basename(src) + ".o")

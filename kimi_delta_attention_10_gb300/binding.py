@@ -8,7 +8,9 @@ missing, or a tensor is not on a CUDA device, the call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
+import sys
 import threading
 from typing import Optional, Sequence, Tuple
 
@@ -479,11 +481,19 @@ _fast = None
 
 
 def _load_marshal():
-    """The _marshal module, bound to the loaded library's functions."""
+    """The _marshal module of this interpreter and PyTorch, bound to the loaded library's
+    functions."""
     global _fast
     lib = load_library()
     if _fast is None:
-        from . import _marshal
+        path, name = _build.marshal_path(), __package__ + "._marshal"
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with {_build.__name__}.build()")
+        if name not in sys.modules:
+            spec = importlib.util.spec_from_file_location(name, path)
+            sys.modules[name] = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(sys.modules[name])
+        _marshal = sys.modules[name]
         _marshal.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
                        for name in EXPORTS})
         _fast = _marshal

@@ -307,6 +307,22 @@ def test_rope_inv_freq_yarn_shorter_than_a_turn(original_len):
     assert near(kda.rope_inv_freq(64, 1e4, "yarn", 4.0, original_len)[0], f / 4)
 
 
+@pytest.mark.parametrize("what", ["torch", "interpreter"])
+def test_marshalling_module_of_another_version_is_not_loaded(lib, monkeypatch, what):
+    """It uses interfaces that change between versions: one that was compiled for others does
+    not count as built, nor is it imported."""
+    binding._load_marshal()
+    assert os.path.exists(_build.marshal_path()) and _build.up_to_date()
+    if what == "torch":
+        monkeypatch.setattr(torch, "__version__", "0.0.0+other")
+    else:
+        monkeypatch.setattr(_build.sys.implementation, "cache_tag", "cpython-000")
+    assert not _build.up_to_date()
+    monkeypatch.setattr(binding, "_fast", None)
+    with pytest.raises(RuntimeError, match="build it with"):
+        kda.kda_page_plan(*[torch.zeros(1)] * 4, 16, 0)
+
+
 # ---------------------------------------------------------------- kernels, by their source
 def test_decode_allocates_tensor_memory_after_its_wait():
     """A CTA that may start while the kernel before it runs holds no tensor memory while it
