@@ -591,6 +591,30 @@ def test_decode_scores_that_are_no_numbers(dtype, D, Hq, lens):
     assert torch.equal(out[:, rest], fine[:, rest]) and torch.equal(lse2[:, rest], lse[:, rest])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("G", [9, 16, 17, 32, 33, 64, 71, 130])
+def test_decode_head_groups_of_64_channels(dtype, G):
+    check_decode(decode_case([300, 1, 130], G, 1, 64, 32, dtype, G))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D,G", [(64, 8), (64, 16), (64, 32), (64, 64), (128, 16), (128, 32), (128, 64)])
+def test_decode_head_groups_of_long_rows(dtype, D, G):
+    """Rows long enough to go round the rings, to be split over blocks and to add up in several
+    runs, with many short ones among them; first of even scores, then of scores that grow along
+    a row, so that what is summed so far is rescaled again and again."""
+    lens = [9000, 1, 0, 700, 20000] + [3, 129, 40, 260] * 20
+    q, kc, vc, table, seq = decode_case(lens, 2 * G, 2, D, 64, dtype, D + G)
+    check_decode((q, kc, vc, table, seq))
+    q.abs_()
+    for n in (0, 3, 4):
+        for j in range(-(-lens[n] // 64)):
+            kc[int(table[n, j])] += j / 8
+    a = check_decode((q, kc, vc, table, seq))
+    b = check_decode((q, kc, vc, table, seq))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 # ---------------------------------------------------------------- beside other kernels
 def test_decode_behind_the_chunk_scan():
     """The scan lets the next kernel start early and takes tensor memory of its own: the two in
