@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "kda_internal.cuh"
+#include "kda_tc.cuh"
 
 namespace kda {
 
@@ -33,7 +34,7 @@ cudaError_t launch_after(void (*kern)(P...), cudaLaunchConfig_t cfg, cudaStream_
 }
 __device__ __forceinline__ void wait_for_previous()
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    tc::grid_dependency_wait();
 }
 inline cudaLaunchConfig_t launch_config(int64_t blocks, unsigned threads, size_t smem = 0)
 {
@@ -157,56 +158,10 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// ---------------------------------------------------------------- vectors
-// 16 bytes of a row as FP32 values.
-template <typename T> struct Vec16;
-template <> struct Vec16<float> {
-    static constexpr int N = 4;
-    static __device__ __forceinline__ void unpack(uint4 u, float (&f)[4])
-    {
-        f[0] = __uint_as_float(u.x);
-        f[1] = __uint_as_float(u.y);
-        f[2] = __uint_as_float(u.z);
-        f[3] = __uint_as_float(u.w);
-    }
-};
-template <> struct Vec16<__nv_bfloat16> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void unpack(uint4 u, float (&f)[8])
-    {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-};
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&p);
-}
-
-// Stores N consecutive values (N * sizeof(TOut) a multiple of 8 bytes, aligned).
-template <int N>
-__device__ __forceinline__ void store_vec(float* p, const float (&f)[N])
-{
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-        *reinterpret_cast<float4*>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
-}
-template <int N>
-__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&f)[N])
-{
-    if constexpr (N == 8) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
-                                                  pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-    } else {
-        static_assert(N == 4, "four or eight values");
-        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
-    }
 }
 
 }  // namespace kda

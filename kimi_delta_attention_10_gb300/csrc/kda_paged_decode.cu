@@ -473,7 +473,6 @@ DecodeShape fp32_shape(const DecodeArgs& a)
     // 103 requests of 1 to 863 with 8 heads a group 119, 94.5, 93.0, 93.1 us, 32 of 1 to 2000
     // with 4 heads 67, 55.5, 52.6, 52.7, 64 of 1 to 256 with one head 22.3, 21.6, 22.5, 22.3.
     s.start = (s.heads >= 4 ? 256 : 192) >> s.tile_shift;
-    s.least = 1;
     return s;
 }
 

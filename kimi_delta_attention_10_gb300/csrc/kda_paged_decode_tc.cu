@@ -605,7 +605,6 @@ DecodeShape decode_tc_shape(const DecodeArgs& a)
     s.ctas = sm_count() * (a.D == 64 && hp <= 16 ? 2 : 1);
     s.tile_shift = kTileShift;
     s.start = 1;
-    s.least = 1;
     return s;
 }
 

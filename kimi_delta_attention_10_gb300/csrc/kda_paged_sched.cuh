@@ -2,8 +2,8 @@
 // every (request, head unit) row of `tiles` tiles lies on one axis of
 // W = units * sum_n (tiles_n + start) places, ordered by request, unit, tile; each row
 // begins with `start` places without a tile, which stand for the time that starting and
-// ending a row costs.  CTA b of B = min(CTAs, W / least) takes W / B places, the first W %
-// B CTAs one more.  A row whose tiles a CTA covers whole is finished there; of a split row
+// ending a row costs.  CTA b of B = min(CTAs, W) takes W / B places, the first W % B CTAs
+// one more.  A row whose tiles a CTA covers whole is finished there; of a split row
 // each CTA leaves a piece (maximum, sum, unscaled output) in one of its two slots: slot
 // 2 b where the row's tiles began before the CTA's, 2 b + 1 where they begin in them.
 // A CTA has at most one of each.
@@ -21,10 +21,7 @@ struct DecodeShape {
     int32_t ctas;         // CTAs launched
     int32_t tile_shift;   // log2 of the tokens per tile
     int32_t start;        // places without a tile at the beginning of a row
-    int32_t least;        // places worth a CTA
 };
-
-
 
 // The split row that a CTA's tiles begin inside of, for the join: its request and unit,
 // and the CTAs of its first and last tile (last < first: none, or not its first split).
@@ -88,8 +85,7 @@ struct DecodeShares {
 
     __device__ __forceinline__ DecodeShares(int64_t W, const DecodeShape& s)
     {
-        B = (W + s.least - 1) / s.least;
-        if (B > s.ctas) B = s.ctas;
+        B = W < s.ctas ? W : s.ctas;
         share = B ? quotient(W, B) : 0;
         more = W - share * B;
     }
