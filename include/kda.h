@@ -474,7 +474,8 @@ typedef enum {
     KDA_ROPE_NTK = 2,      /* theta * factor^(rot_dim / (rot_dim - 2)) as the base      */
     KDA_ROPE_YARN = 3      /* by parts: channels that turn more than beta_fast times in
                               original_len tokens keep f_i, fewer than beta_slow take
-                              f_i / factor, a linear ramp between (in channel index);
+                              f_i / factor, a linear ramp between (in channel index, its
+                              ends rounded outwards, within 0 .. rot_dim - 1);
                               rotated values are scaled by 0.1 ln(factor) + 1           */
 } kda_rope_scaling;
 
@@ -498,13 +499,15 @@ kda_status kda_rope_inv_freq(int32_t rot_dim, double theta, int32_t scaling, dou
  * with the angle position * inv_freq[i] for pair i, cos and sin multiplied by
  * rope_scale, and channels rot_dim .. D-1 left as normed.
  *   interleaved = 0: pair i is channels (i, i + rot_dim / 2); 1: (2 i, 2 i + 1)
- * FP32 arithmetic, rounded once to out_dtype.  The angle's turns are exact to
- * 2^-53 times the position (64-bit fixed point), so far positions lose nothing.
+ * FP32 arithmetic, rounded once to out_dtype.  The angle's fraction of a turn is
+ * found in 64-bit integers and good to 2^-32 at any position, so far positions lose
+ * nothing.  A channel that is not rotated takes nothing of another one.
  *
  *   q [T, Hq, D], k [T, Hk, D]  x_dtype; token t's heads start at t * q_stride
  *               (k_stride) elements, so both can lie in one fused projection:
  *               stride >= heads * D, a multiple of 16 bytes, below 2^31 elements
- *   positions [T] int32;  inv_freq [rot_dim / 2] F32 (NULL when rot_dim = 0)
+ *   positions [T] int32;  inv_freq [rot_dim / 2] F32 (NULL when rot_dim = 0), finite
+ *               and below 2^64
  *   q_weight, k_weight [D] F32, or NULL for ones (unread when qk_norm = 0)
  *   q_out [T, Hq, D], k_out [T, Hk, D]  out_dtype, dense; may be q (k) where
  *               that is dense and of the same type
@@ -579,14 +582,20 @@ kda_status kda_paged_decode_workspace_size(int32_t N, int32_t Hq, int32_t Hk, in
  * lengths of all requests together split evenly over the GPU and the pieces of
  * a row joined from their (maximum, sum, output) in a second kernel.
  * L = 0 gives a row of zeros and lse -infinity.  What a page holds past the
- * request's last token is never used, whatever it is (NaN included).
+ * request's last token is never used, whatever it is (NaN included).  Infinities
+ * and NaN in q, k and v give what the formula gives, as long as a weight that meets an
+ * infinite value does not underflow.  There is one query a request: the other
+ * tokens of a prompt, which a layer above would need, are not attended for.
  *
  *   q [N, Hq, D] dtype;  k_cache, v_cache [num_pages, Hk, page_size, D] dtype
  *   block_table [N, max_pages] int32, seq_lens [N] int32
  *   out [N, Hq, D] out_dtype;  lse [N, Hq] F32 or NULL (natural logarithm)
  * Scores, statistics and output sums are FP32.  F32: products are IEEE FP32.
  * BF16: products of BF16 values are exact; each weight e^(s_t) is used as two
- * BF16 parts (16 significant bits, relative error 2^-17).
+ * BF16 parts (16 significant bits, relative error 2^-17), and the tensor core's
+ * sums, which it truncates, are added up rounded every 4096 tokens (an F32 output
+ * is about 5e-6 off).  The weights reach 2^8 before they are divided by their sum,
+ * so values need that room below FP32's largest.
  * A length outside [0, max_pages * page_size] counts as 0 and sets
  * KDA_ERR_DEVICE_ARG in status_dev; a page outside [0, num_pages) that a
  * request's length reaches sets it too: nothing outside the cache is read, and

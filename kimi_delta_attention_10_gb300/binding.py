@@ -475,7 +475,8 @@ def kda_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
 
 # ---------------------------------------------------------------- paged attention
 # These calls are short on the GPU, so their tensors are looked at in C++ (marshal.cpp):
-# a call costs the host the launch and little else.
+# a call costs the host the launch and little else.  All tensors of a call are on one device.
+# stream: None (the current one) or the call's; what the call allocates belongs to it.
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
 _fast = None
 

@@ -19,8 +19,10 @@ int sm_count();
 // before it on the stream ends (programmatic dependent launch), and waits for that one,
 // complete and its memory visible, ahead of its first access to global memory: in a chain
 // of short calls the launches overlap (a decode of one request 15.4 -> 10.3 us a call, the
-// append of 64 tokens 8.2 -> 4.9 us).  None signals early: blocks of the next kernel that
-// wait beside it cost more than the signal saves (129 rotated tokens 6.9 instead of 4.8 us).
+// append of 64 tokens 8.2 -> 4.9 us).  None of these signals early: blocks of the next kernel
+// that wait beside it cost more than the signal saves (129 rotated tokens 6.9 instead of 4.8
+// us).  Others do (the chunk scan), so nothing is held during the wait that a kernel may still
+// have to allocate.
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kern)(P...), cudaLaunchConfig_t cfg, cudaStream_t stream, A... args)
 {

@@ -8,7 +8,8 @@
 // (K-major keys, MN-major values), so nothing is transposed and nothing padded but
 // N.  The weights p = e^(s - m) go back to shared memory as two BF16 rows, the
 // rounded value and the rounded rest: N is nearly free here (the MMA's time is the
-// 128-row operand's read), and the weights then carry 16 bits instead of 8.
+// 128-row operand's read), and the weights then carry 16 bits instead of 8.  The two rows'
+// sums stay apart until they are read: an infinite value is right in the first alone.
 //
 // HBM-bound: 2 D values a token and key-value head, once.  Warp roles:
 //   producers one warp for K, one for V: a TMA box per page and 64 channels into a
@@ -26,10 +27,13 @@
 //
 // Measured (us, and the share of the rate of a plain copy): 64 requests of 0 to 16384
 // tokens, 8 key-value heads of 128 channels with 8 query heads each, 302 (98%); two requests
-// of 131072 to 262144 256 (98%); 64 of 4096 169 (94%), the tensor pipe 4% busy.  Where the
-// softmax has as much to do as the memory it bounds the kernel: groups of 64 heads 72%,
-// groups of 32 heads of 64 channels 57%.  A short row costs about 2 us beside its bytes (128
-// requests of 1 to 600 tokens 45, 49%), one request of 129 tokens 8.6 with the join.
+// of 131072 to 262144 256 (98%); 64 of 4096 169 (94%), the tensor pipe 4% busy.  With many
+// heads the chain of one tile (scores, vote, weights, product) is longer than its loads and
+// nothing runs beside it: 64 requests of 4096 tokens and 4 key-value heads take 95 with groups
+// of 16 heads of 128 channels (84%), 98 with 32 (81%), 117 with 64 (69%; 42% of the issue slots,
+// the tensor pipe 15%), of 64 channels 57 (69%), 82 (49%) and 103 (39%).  A short row costs about
+// 2 us beside its bytes (128 requests of 1 to 600 tokens 46, 48%), one request of 129 tokens 8.6
+// with the join.
 //
 // Tokens past the request's end: their scores are replaced by -infinity, their
 // value rows by zeros in shared memory (0 * NaN would not be 0), and pages past the
@@ -55,9 +59,10 @@ constexpr int kTile = 128;             // tokens per tile
 constexpr int kTileShift = 7;
 constexpr float kGrowth = 8.f;         // log2 of the growth that moves the reference maximum
 // Tiles that O adds up in tensor memory before it joins a total that is rounded: the tensor
-// core truncates its sums, so that a row of 262144 tokens in one sum lost up to 5e-4 of itself.
+// core truncates its sums, so that 262144 values about one lost 1.6e-3 of their mean in one sum.
 // Two rows of 131072 to 262144 tokens with FP32 output: 2.5e-5 off in one sum, 5e-6 in runs
-// of 32 tiles, at the same speed (with groups of 64 heads 1 to 4% slower).
+// of 32 tiles, in the same time (64 requests of 4096 tokens, groups of 64 heads: 113 -> 117 us
+// with runs of 32 tiles, 119 with 16).
 constexpr int kRun = 32;
 
 template <int D_, int HP_> struct Cfg {

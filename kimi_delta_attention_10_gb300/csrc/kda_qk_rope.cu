@@ -22,9 +22,10 @@
 // angles: that costs less than leaving SMs idle.
 //
 // Measured (us, and the share of the rate of a plain copy): append of 30392 BF16 tokens of
-// 64 + 8 heads of 128 channels 195 (94%; 83% of the issue slots), forward of 2048 FP32 tokens of
-// 64 + 64 heads 43.5 (90%), backward of 16384 BF16 tokens of 64 + 8 heads 144 (93%), 64 or
-// 129 tokens 4.5.  Few heads and many tokens are issue-bound by the angles (5 + 1 heads: 40%).
+// 64 + 8 heads of 128 channels 196.5 (93%; 83% of the issue slots), forward of 2048 FP32 tokens
+// of 64 + 64 heads 43.8 (90%), backward of 16384 BF16 tokens of 64 + 8 heads 146 (91%), 64 or
+// 129 tokens 4.5.  Few heads and many tokens spend their issue slots on the angles: 16384 BF16
+// tokens of 5 + 1 heads 25.8 (29%; 61% of the issue slots).
 //
 // Angles: position * inv_freq can be 10^6 radians, where FP32 has lost 0.06.
 // The frequency is turned into turns per position as a 64-bit binary fraction
