@@ -25,7 +25,8 @@
  *   - Every device pointer must be 16-byte aligned (KDA_ERR_ALIGNMENT), except
  *     kda_page_plan's.
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = the legacy
- *     default stream).  The library never synchronises.
+ *     default stream) of the current device, which holds every array.  The
+ *     library never synchronises.
  *   - Argument errors are detected on the host before anything is launched:
  *     the call returns a non-zero kda_status and launches nothing.  A CUDA
  *     launch failure returns KDA_ERR_CUDA.  Errors that only the device can
@@ -583,9 +584,11 @@ kda_status kda_paged_decode_workspace_size(int32_t N, int32_t Hq, int32_t Hk, in
  * a row joined from their (maximum, sum, output) in a second kernel.
  * L = 0 gives a row of zeros and lse -infinity.  What a page holds past the
  * request's last token is never used, whatever it is (NaN included).  Infinities
- * and NaN in q, k and v give what the formula gives, as long as a weight that meets an
- * infinite value does not underflow.  There is one query a request: the other
- * tokens of a prompt, which a layer above would need, are not attended for.
+ * and NaN in v give what the formula gives, as long as a weight that meets an
+ * infinite value does not underflow; a score of NaN or +infinity makes its row's
+ * output and lse NaN, scores of -infinity alone lse -infinity and 0 / 0 in the
+ * output.  There is one query a request: the other tokens of a prompt, which a
+ * layer above would need, are not attended for.
  *
  *   q [N, Hq, D] dtype;  k_cache, v_cache [num_pages, Hk, page_size, D] dtype
  *   block_table [N, max_pages] int32, seq_lens [N] int32
