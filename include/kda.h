@@ -23,7 +23,7 @@
  *     test switch of kda_test_set_fault; calls of every other entry point on
  *     different streams are independent.
  *   - Every device pointer must be 16-byte aligned (KDA_ERR_ALIGNMENT), except
- *     kda_page_plan's.
+ *     kda_page_plan's and the integer arrays of attention for several tokens.
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = the legacy
  *     default stream) of the current device, which holds every array.  The
  *     library never synchronises.
@@ -587,8 +587,7 @@ kda_status kda_paged_decode_workspace_size(int32_t N, int32_t Hq, int32_t Hk, in
  * and NaN in v give what the formula gives, as long as a weight that meets an
  * infinite value does not underflow; a score of NaN or +infinity makes its row's
  * output and lse NaN, scores of -infinity alone lse -infinity and 0 / 0 in the
- * output.  There is one query a request: the other tokens of a prompt, which a
- * layer above would need, are not attended for.
+ * output.  There is one query a request; kda_paged_prompt attends for several.
  *
  *   q [N, Hq, D] dtype;  k_cache, v_cache [num_pages, Hk, page_size, D] dtype
  *   block_table [N, max_pages] int32, seq_lens [N] int32
@@ -615,6 +614,128 @@ kda_status kda_paged_decode(const void* q, const void* k_cache, const void* v_ca
                             int32_t page_size, int32_t max_pages, float scale, void* out,
                             int32_t out_dtype, float* lse, void* workspace,
                             int64_t workspace_bytes, int32_t* status_dev, kda_stream_t stream);
+
+/* ================================================ attention for several tokens
+ *
+ * The full attention of a hybrid stack over prompts and for training, and decode for
+ * requests that share a prefix.  For query head h, reading key-value head
+ * h / (Hq / Hk), and the keys j that token i sees,
+ *   s_ij = scale * q_i . k_j,   lse_i = log sum_j e^(s_ij),   o_i = sum_j e^(s_ij - lse_i) v_j
+ * in one pass over the keys with a running maximum and sum.
+ *
+ * Common to these entry points: dtype is that of q, k, v (or the cache) and of every
+ * output but lse (F32, natural logarithm, [T, Hq], or NULL).  F32: products are IEEE
+ * FP32.  BF16: products of BF16 values are exact and summed in FP32; the weights and, in
+ * the backward, the scores' gradients are rounded to BF16 (2^-8) before the products with
+ * them, statistics and sums are FP32, and outputs are rounded once.  Few rows over many
+ * keys are taken in pieces of the keys' axis, which a second kernel joins.  Every sum's
+ * order is set by the sizes alone: the same call gives the same bits.
+ *
+ * A token that sees no key gets an output of zeros and lse -infinity, and so does one all
+ * of whose scores are -infinity.  A score of NaN or +infinity makes its row's output and
+ * lse NaN.  Nothing of another sequence, of rows that belong to none, of pages past a
+ * request's last token, or of tokens after all those that a tile's queries see reaches a
+ * result, whatever it is (NaN included).  An infinity or NaN in k or v of a token may reach
+ * queries up to 255 tokens before it in its own sequence (a tile's, which the products take
+ * together with weights of zero), and in the backward one in q or dout the gradients of keys
+ * up to 255 tokens behind it.
+ *
+ * Offsets: 0 = cu_seqlens[0] <= cu_seqlens[1] <= ... <= cu_seqlens[N] <= T.  Rows behind
+ * cu_seqlens[N] belong to no sequence, and their outputs are left as they were.  Bad
+ * offsets set KDA_ERR_DEVICE_ARG in status_dev, and no output is written.  All lengths
+ * are read on the device, so that a captured call follows them.
+ *
+ * D = 64 or 128, Hq a multiple of Hk, T * Hq < 2^31 (else KDA_ERR_UNSUPPORTED).  Packed
+ * rows may be slices of one projection: token t's heads start at t * q_stride (k_stride,
+ * v_stride) elements, dense among themselves, strides whole 16 bytes.  Integer arrays need
+ * 4-byte alignment only (a row of a table or a slice will do).  No output may be an
+ * input or another output.  workspace: 16-byte aligned, at least the size its entry point
+ * names, contents on entry irrelevant; calls that share one must be ordered on one stream.
+ */
+
+/* Bytes of workspace kda_attention_fwd needs, whatever the lengths. */
+kda_status kda_attention_workspace_size(int32_t N, int64_t T, int32_t Hq, int32_t Hk, int32_t D,
+                                        int64_t* bytes_host);
+
+/*
+ * kda_attention_fwd -- causal attention of N packed sequences: token i of a sequence
+ * sees its tokens 0 .. i.
+ *   q [T, Hq, D], k, v [T, Hk, D] (strided tokens), cu_seqlens [N+1] int32
+ *   out [T, Hq, D] dense
+ */
+kda_status kda_attention_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, int32_t dtype,
+                             const int32_t* cu_seqlens, int32_t N, int64_t T, int32_t Hq,
+                             int32_t Hk, int32_t D, float scale, void* out, float* lse,
+                             void* workspace, int64_t workspace_bytes, int32_t* status_dev,
+                             kda_stream_t stream);
+
+/* Bytes of workspace kda_attention_bwd needs, whatever the lengths. */
+kda_status kda_attention_bwd_workspace_size(int32_t N, int64_t T, int32_t Hq, int32_t Hk, int32_t D,
+                                            int64_t* bytes_host);
+
+/*
+ * kda_attention_bwd -- the vector-Jacobian product of kda_attention_fwd: from out and
+ * lse as the forward left them and dout [T, Hq, D] (dense) the gradients q_grad
+ * [T, Hq, D], k_grad, v_grad [T, Hk, D] (dense).  With p_ij = e^(s_ij - lse_i),
+ * delta_i = dout_i . out_i and ds_ij = p_ij (dout_i . v_j - delta_i),
+ *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i,
+ * the last two over all heads of the group.  Scores are formed again, never stored.
+ */
+kda_status kda_attention_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, int32_t dtype, const void* out,
+                             const float* lse, const void* dout, const int32_t* cu_seqlens,
+                             int32_t N, int64_t T, int32_t Hq, int32_t Hk, int32_t D, float scale,
+                             void* q_grad, void* k_grad, void* v_grad, void* workspace,
+                             int64_t workspace_bytes, int32_t* status_dev, kda_stream_t stream);
+
+/* Bytes of workspace kda_paged_prompt needs, whatever the lengths. */
+kda_status kda_paged_prompt_workspace_size(int32_t N, int64_t T, int32_t Hq, int32_t Hk, int32_t D,
+                                           int64_t* bytes_host);
+
+/*
+ * kda_paged_prompt -- attention of several new tokens a request over its pages
+ * (prompts, pieces of prompts behind a cached part, drafted tokens): request n's
+ * tokens cu_seqlens[n] .. cu_seqlens[n+1]-1, m of them, are the last m of its
+ * seq_lens[n], all appended already (kda_page_plan, kda_qk_norm_rope_append), and each sees
+ * the tokens up to itself.  With one token a request it computes what kda_paged_decode does.
+ *   q [T, Hq, D] (strided tokens), k_cache, v_cache [num_pages, Hk, page_size, D]
+ *   block_table [N, max_pages], seq_lens [N], cu_seqlens [N+1] int32;  out [T, Hq, D]
+ * A request with seq_lens[n] < m has tokens before its first key: they see none.
+ * Lengths, pages and cache sizes as in kda_paged_decode.
+ */
+kda_status kda_paged_prompt(const void* q, int64_t q_stride, const void* k_cache,
+                            const void* v_cache, int32_t dtype, const int32_t* block_table,
+                            const int32_t* seq_lens, const int32_t* cu_seqlens, int32_t N,
+                            int64_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t num_pages,
+                            int32_t page_size, int32_t max_pages, float scale, void* out,
+                            float* lse, void* workspace, int64_t workspace_bytes,
+                            int32_t* status_dev, kda_stream_t stream);
+
+/* Bytes of workspace kda_paged_decode_shared needs, whatever the lengths. */
+kda_status kda_paged_decode_shared_workspace_size(int32_t N, int32_t groups, int32_t Hq, int32_t Hk,
+                                                  int32_t D, int64_t* bytes_host);
+
+/*
+ * kda_paged_decode_shared -- kda_paged_decode for requests that share prefixes: requests
+ * cu_groups[g] .. cu_groups[g+1]-1 attend to the prefix_lens[g] tokens in the pages of
+ * row g of prefix_table, read once for all of them, and then each to the seq_lens[n]
+ * tokens of its own row of block_table (the new token's among them).
+ *   q [N, Hq, D];  prefix_table [groups, max_prefix_pages], prefix_lens [groups],
+ *   cu_groups [groups+1], block_table [N, max_pages], seq_lens [N] int32
+ *   out [N, Hq, D], lse [N, Hq]
+ * cu_groups are offsets as above with T = N: requests behind the last group keep their
+ * outputs.  Either length may be 0.  Lengths, pages and cache sizes as in kda_paged_decode.
+ */
+kda_status kda_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache,
+                                   int32_t dtype, const int32_t* prefix_table,
+                                   const int32_t* prefix_lens, const int32_t* cu_groups,
+                                   int32_t groups, int32_t max_prefix_pages,
+                                   const int32_t* block_table, const int32_t* seq_lens, int32_t N,
+                                   int32_t Hq, int32_t Hk, int32_t D, int32_t num_pages,
+                                   int32_t page_size, int32_t max_pages, float scale, void* out,
+                                   float* lse, void* workspace, int64_t workspace_bytes,
+                                   int32_t* status_dev, kda_stream_t stream);
 
 /*
  * kda_test_set_fault -- TEST HOOK, not for production use (no page
@@ -649,7 +770,8 @@ const char* kda_status_string(int32_t status);
  * change no existing signature keep the number: kda_chunk_fwd_static,
  * kda_gated_rmsnorm, kda_chunk_bwd_workspace_size, kda_chunk_bwd,
  * KDA_ERR_RANGE, kda_test_set_fault, kda_chunk_fwd_gated_norm, the paged
- * attention entry points and KDA_ERR_NO_PAGES). */
+ * attention entry points and KDA_ERR_NO_PAGES, the entry points of attention for
+ * several tokens). */
 int32_t kda_abi_version(void);
 
 #ifdef __cplusplus

@@ -50,7 +50,11 @@ EXPORTS = ("kda_gate", "kda_chunk_workspace_size", "kda_chunk_fwd", "kda_chunk_f
            "kda_chunk_bwd_workspace_size", "kda_chunk_bwd", "kda_page_plan",
            "kda_rope_inv_freq", "kda_qk_norm_rope", "kda_qk_norm_rope_append",
            "kda_qk_norm_rope_bwd_workspace_size", "kda_qk_norm_rope_bwd",
-           "kda_paged_decode_workspace_size", "kda_paged_decode", "kda_test_set_fault",
+           "kda_paged_decode_workspace_size", "kda_paged_decode",
+           "kda_attention_workspace_size", "kda_attention_fwd",
+           "kda_attention_bwd_workspace_size", "kda_attention_bwd",
+           "kda_paged_prompt_workspace_size", "kda_paged_prompt",
+           "kda_paged_decode_shared_workspace_size", "kda_paged_decode_shared", "kda_test_set_fault",
            "kda_status_string", "kda_abi_version")
 
 _lock = threading.Lock()
@@ -136,6 +140,30 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.kda_paged_decode.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
                                          i32, f32, vp, i32, vp, vp, i64, vp, vp]
         lib.kda_paged_decode.restype = i32
+        size = [i32, i64, i32, i32, i32, ctypes.POINTER(i64)]
+        packed = [vp, i64, vp, i64, vp, i64, i32]
+        cache = [i32, i32, i32, f32, vp, vp, vp, i64, vp, vp]
+        lib.kda_attention_workspace_size.argtypes = size
+        lib.kda_attention_workspace_size.restype = i32
+        lib.kda_attention_fwd.argtypes = [*packed, vp, i32, i64, i32, i32, i32, f32, vp, vp, vp,
+                                          i64, vp, vp]
+        lib.kda_attention_fwd.restype = i32
+        lib.kda_attention_bwd_workspace_size.argtypes = size
+        lib.kda_attention_bwd_workspace_size.restype = i32
+        lib.kda_attention_bwd.argtypes = [*packed, vp, vp, vp, vp, i32, i64, i32, i32, i32, f32,
+                                          vp, vp, vp, vp, i64, vp, vp]
+        lib.kda_attention_bwd.restype = i32
+        lib.kda_paged_prompt_workspace_size.argtypes = size
+        lib.kda_paged_prompt_workspace_size.restype = i32
+        lib.kda_paged_prompt.argtypes = [vp, i64, vp, vp, i32, vp, vp, vp, i32, i64, i32, i32, i32,
+                                         *cache]
+        lib.kda_paged_prompt.restype = i32
+        lib.kda_paged_decode_shared_workspace_size.argtypes = [i32, i32, i32, i32, i32,
+                                                               ctypes.POINTER(i64)]
+        lib.kda_paged_decode_shared_workspace_size.restype = i32
+        lib.kda_paged_decode_shared.argtypes = [vp, vp, vp, i32, vp, vp, vp, i32, i32, vp, vp, i32,
+                                                i32, i32, i32, *cache]
+        lib.kda_paged_decode_shared.restype = i32
         lib.kda_test_set_fault.argtypes = [i32]
         lib.kda_test_set_fault.restype = i32
         lib.kda_status_string.argtypes = [i32]
@@ -473,7 +501,7 @@ def kda_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     return dq, dk, dv, dg, dbeta, dinit
 
 
-# ---------------------------------------------------------------- paged attention
+# ---------------------------------------------------------------- attention
 # These calls are short on the GPU, so their tensors are looked at in C++ (marshal.cpp):
 # a call costs the host the launch and little else.  All tensors of a call are on one device.
 # stream: None (the current one) or the call's; what the call allocates belongs to it.
@@ -629,4 +657,108 @@ def kda_paged_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
                                                 stream)
     if r.__class__ is int:
         raise KDAError(r, "kda_paged_decode")
+    return r
+
+
+def attention_workspace_size(N: int, T: int, Hq: int, Hk: int, D: int = 128) -> int:
+    """Bytes of workspace kda_attention_fwd needs, whatever the lengths."""
+    return _bytes("kda_attention_workspace_size", N, T, Hq, Hk, D)
+
+
+def _bytes(name: str, *sizes: int) -> int:
+    out = ctypes.c_int64(0)
+    st = getattr(load_library(), name)(*sizes, ctypes.byref(out))
+    if st != KDA_OK:
+        raise KDAError(st, name)
+    return out.value
+
+
+def kda_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                      scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None, want_lse: bool = False,
+                      status: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None, workspace=None):
+    """Causal attention of the packed sequences cu_seqlens [N+1]: q [T,Hq,D], k and v
+    [T,Hk,D], which may be slices of one projection.  Returns (out [T,Hq,D], lse [T,Hq] or
+    None); rows behind cu_seqlens[N] are left as they were.  workspace: None (one kept per
+    stream) or a CUDA tensor of at least attention_workspace_size(...) bytes."""
+    r = (_fast or _load_marshal()).attention_fwd(q, k, v, cu_seqlens, scale, out, lse, want_lse,
+                                                 status, stream, workspace)
+    if r.__class__ is int:
+        raise KDAError(r, "kda_attention_fwd")
+    return r
+
+
+def attention_bwd_workspace_size(N: int, T: int, Hq: int, Hk: int, D: int = 128) -> int:
+    """Bytes of workspace kda_attention_bwd needs, whatever the lengths."""
+    return _bytes("kda_attention_bwd_workspace_size", N, T, Hq, Hk, D)
+
+
+def kda_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                      lse: torch.Tensor, dout: torch.Tensor, cu_seqlens: torch.Tensor,
+                      scale: Optional[float] = None, q_grad: Optional[torch.Tensor] = None,
+                      k_grad: Optional[torch.Tensor] = None,
+                      v_grad: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None, workspace=None):
+    """Backward of kda_attention_fwd from its out and lse and dout [T,Hq,D].  Returns
+    (q_grad [T,Hq,D], k_grad, v_grad [T,Hk,D]) in the inputs' dtype.  workspace: None (one
+    kept per stream) or a CUDA tensor of at least attention_bwd_workspace_size(...) bytes."""
+    r = (_fast or _load_marshal()).attention_bwd(q, k, v, out, lse, dout, cu_seqlens, scale, q_grad,
+                                                 k_grad, v_grad, status, stream, workspace)
+    if r.__class__ is int:
+        raise KDAError(r, "kda_attention_bwd")
+    return r
+
+
+def paged_prompt_workspace_size(N: int, T: int, Hq: int, Hk: int, D: int = 128) -> int:
+    """Bytes of workspace kda_paged_prompt needs, whatever the lengths."""
+    return _bytes("kda_paged_prompt_workspace_size", N, T, Hq, Hk, D)
+
+
+def kda_paged_prompt(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     block_table: torch.Tensor, seq_lens: torch.Tensor, cu_seqlens: torch.Tensor,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, want_lse: bool = False,
+                     status: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None, workspace=None):
+    """Attention of several new tokens a request over its pages: q [T,Hq,D] packed by
+    cu_seqlens [N+1], request n's the last of its seq_lens[n] tokens, each seeing those up to
+    itself (kda_paged_decode for more than one token).  Returns (out [T,Hq,D], lse [T,Hq] or
+    None).  workspace: None (one kept per stream) or a CUDA tensor of at least
+    paged_prompt_workspace_size(...) bytes."""
+    r = (_fast or _load_marshal()).paged_prompt(q, k_cache, v_cache, block_table, seq_lens,
+                                                cu_seqlens, scale, out, lse, want_lse, status,
+                                                stream, workspace)
+    if r.__class__ is int:
+        raise KDAError(r, "kda_paged_prompt")
+    return r
+
+
+def paged_decode_shared_workspace_size(N: int, groups: int, Hq: int, Hk: int,
+                                       D: int = 128) -> int:
+    """Bytes of workspace kda_paged_decode_shared needs, whatever the lengths."""
+    return _bytes("kda_paged_decode_shared_workspace_size", N, groups, Hq, Hk, D)
+
+
+def kda_paged_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                            prefix_table: torch.Tensor, prefix_lens: torch.Tensor,
+                            cu_groups: torch.Tensor, block_table: torch.Tensor,
+                            seq_lens: torch.Tensor, scale: Optional[float] = None,
+                            out: Optional[torch.Tensor] = None,
+                            lse: Optional[torch.Tensor] = None, want_lse: bool = False,
+                            status: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None, workspace=None):
+    """kda_paged_decode for groups of requests (cu_groups [groups+1]) that share a prefix:
+    prefix_lens [groups] tokens in the pages of prefix_table, read once a group, then each
+    request's own seq_lens [N] tokens in those of block_table.  Returns (out [N,Hq,D], lse
+    [N,Hq] or None); requests behind the last group are left as they were.  workspace: None
+    (one kept per stream) or a CUDA tensor of at least
+    paged_decode_shared_workspace_size(...) bytes."""
+    r = (_fast or _load_marshal()).paged_decode_shared(q, k_cache, v_cache, prefix_table,
+                                                       prefix_lens, cu_groups, block_table,
+                                                       seq_lens, scale, out, lse, want_lse, status,
+                                                       stream, workspace)
+    if r.__class__ is int:
+        raise KDAError(r, "kda_paged_decode_shared")
     return r

@@ -1,0 +1,197 @@
+// Internal declarations of the attention entry points for several tokens a sequence
+// (kda_attention_fwd, kda_attention_bwd, kda_paged_prompt, kda_paged_decode_shared).
+//
+// Rows.  The query heads of a group (those that share a key-value head) and the tokens
+// are packed into one axis: a tile of R tokens and GP heads is R * GP rows, row r being
+// token r / GP, head r % GP.  The keys that a tile reads then serve the whole group, and a
+// call with one token a sequence still fills its rows.
+//
+// Order.  A tile's work is its number of key tiles; CTAs are numbered so that the tiles
+// with the most come first, whichever sequence they belong to (attn_find), and the last
+// CTAs to start are the shortest.
+#pragma once
+
+#include <stdint.h>
+
+#include "kda_paged.cuh"
+
+namespace kda {
+
+struct AttnArgs {
+    const void* q;           // [T, Hq, D], tokens q_stride elements apart
+    const void* k;           // packed [T, Hk, D] (k_stride), or the cache
+    const void* v;
+    int32_t q_stride, k_stride, v_stride;
+    bool bf16;
+    const int32_t* cu;       // [N + 1]
+    int32_t N, T, Hq, Hk, D;
+    float scale;
+    // the paged forms; table == nullptr: keys and values are packed like the queries
+    const int32_t* table;    // [N, max_pages]
+    const int32_t* kv_lens;  // [N]
+    int32_t num_pages, page_shift, max_pages;
+    bool causal;             // the last query is the last key's token; else all see all keys
+    void* out;               // [T, Hq, D]
+    float* lse;              // [T, Hq] or nullptr
+    // pieces of the keys' axis, joined by launch_attn_join: [pieces][T, Hq] lse, then
+    // [pieces][T, Hq, D] FP32 outputs, behind a header (the number of tokens with a row)
+    int32_t splits, pieces;
+    void* workspace;
+    int32_t* status;
+    // backward
+    const void* dout;        // [T, Hq, D]
+    const float* lse_in;
+    float* delta;            // [T, Hq], in the workspace
+    void* dq;
+    void* dk;
+    void* dv;
+};
+
+// Bytes before the pieces' statistics.
+constexpr int64_t kAttnHeader = 256;
+__host__ __device__ inline int64_t attn_pieces_lse(const AttnArgs& a, int32_t piece)
+{
+    return kAttnHeader + (int64_t)piece * a.T * a.Hq * 4;
+}
+__host__ __device__ inline int64_t attn_pieces_o(const AttnArgs& a, int32_t piece)
+{
+    const int64_t rows = (int64_t)a.T * a.Hq;
+    return kAttnHeader + ((int64_t)a.pieces * rows * 4 + 255) / 256 * 256 + piece * rows * a.D * 4;
+}
+
+// How a call's rows are cut into tiles.
+struct AttnShape {
+    int32_t tokens;          // of a CTA's tile
+    int32_t heads;           // query heads of a tile (of the last part of a group: fewer)
+    int32_t parts;           // tiles of heads per group
+    int32_t units;           // Hk * parts
+};
+
+cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attention_bwd(const AttnArgs& a, cudaStream_t stream);
+int64_t attention_bwd_workspace_bytes(int32_t N, int32_t T, int32_t Hq, int32_t Hk, int32_t D);
+cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t stream);
+// Pieces of the keys' axis for a call whose sequences have at most kv_most keys.
+int32_t attn_splits(bool bf16, int32_t N, int32_t T, int32_t Hq, int32_t Hk, int32_t D, int64_t kv_most);
+
+// ---------------------------------------------------------------- device
+struct AttnTile {
+    int32_t n;               // sequence
+    int32_t index;           // of the tile in it
+    int32_t row0, tokens;    // first packed token, and how many
+    int32_t seq0, seq_tokens;    // the sequence's first packed token, and its tokens
+    int32_t kv_len;          // keys of the sequence
+    int32_t pos0;            // position of the tile's first token (below 0: it sees no key)
+};
+
+// The sequence's keys; a length that the table or the cache cannot hold counts as none.
+__device__ __forceinline__ int32_t attn_kv_len(const AttnArgs& a, int32_t n, int32_t tokens)
+{
+    if (a.table == nullptr) return tokens;
+    const int32_t L = a.kv_lens[n];
+    const int64_t most = (int64_t)a.max_pages << a.page_shift;
+    if (L < 0 || L > most || (L > 0 && a.num_pages == 0)) {
+        report_status(a.status, KDA_ERR_DEVICE_ARG);
+        return 0;
+    }
+    return L;
+}
+
+// Of a sequence of m tokens and L keys, cut into nt tiles of `tokens`: the first tile that
+// has more than d key tiles of 2^key_shift (nt: none has).
+__device__ __forceinline__ int32_t attn_deeper(int32_t m, int32_t L, int32_t nt, bool causal, int32_t tokens,
+                                               int key_shift, int32_t d)
+{
+    if (d < 0) return 0;
+    const int64_t lim = (int64_t)d << key_shift;
+    if (L <= lim) return nt;
+    if (!causal) return 0;
+    const int64_t x = lim - ((int64_t)L - m);          // tokens whose keys end within lim
+    return x <= 0 ? 0 : min(nt, (int32_t)((uint32_t)x / (uint32_t)tokens));
+}
+
+// Tile `item` in the order of falling work; false: there is none, or the offsets are bad
+// (reported; then no tile is found by any CTA).  Called by one whole warp.
+__device__ __forceinline__ bool attn_find(const AttnArgs& a, int32_t item, int32_t tokens, int key_shift,
+                                          AttnTile& t)
+{
+    const int lane = threadIdx.x & 31;
+    bool bad = false;
+    int32_t deepest = 0;
+    for (int32_t n = lane; n < a.N; n += 32) {
+        const int32_t c0 = a.cu[n], c1 = a.cu[n + 1];
+        bad |= c0 < 0 || c1 < c0 || c1 > a.T || (n == 0 && c0 != 0);
+        deepest = max(deepest, attn_kv_len(a, n, c1 - c0));
+    }
+    if (__any_sync(0xffffffffu, bad)) {
+        if (lane == 0) report_status(a.status, KDA_ERR_DEVICE_ARG);
+        return false;
+    }
+    deepest = __reduce_max_sync(0xffffffffu, deepest);
+    auto count = [&](int32_t n, int32_t d) {           // tiles of n with more than d key tiles
+        const int32_t m = a.cu[n + 1] - a.cu[n], nt = (int32_t)(((uint32_t)m + tokens - 1) / (uint32_t)tokens);
+        return nt - attn_deeper(m, attn_kv_len(a, n, m), nt, a.causal, tokens, key_shift, d);
+    };
+    auto total = [&](int32_t d) {
+        int32_t s = 0;
+        for (int32_t n = lane; n < a.N; n += 32) s += count(n, d);
+        return (int32_t)__reduce_add_sync(0xffffffffu, (unsigned)s);
+    };
+    // the least d with at most `item` tiles of more than d key tiles: the item has d itself
+    int32_t lo = 0, hi = (int32_t)(((int64_t)deepest + (1 << key_shift) - 1) >> key_shift);
+    while (lo < hi) {
+        const int32_t mid = (lo + hi) >> 1;
+        if (total(mid) <= item) hi = mid;
+        else lo = mid + 1;
+    }
+    int32_t rank = item - total(lo);
+    for (int32_t base = 0; base < a.N; base += 32) {
+        const int32_t n = base + lane;
+        const int32_t mine = n < a.N ? count(n, lo - 1) - count(n, lo) : 0;
+        int32_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, upto > rank);
+        if (past) {
+            const int at = __ffs(past) - 1;
+            rank -= __shfl_sync(0xffffffffu, upto - mine, at);
+            const int32_t who = base + at, c0 = a.cu[who], m = a.cu[who + 1] - c0;
+            const int32_t L = attn_kv_len(a, who, m);
+            const int32_t nt = (int32_t)(((uint32_t)m + tokens - 1) / (uint32_t)tokens);
+            t.n = who;
+            t.index = attn_deeper(m, L, nt, a.causal, tokens, key_shift, lo - 1) + rank;
+            t.seq0 = c0;
+            t.seq_tokens = m;
+            t.row0 = c0 + t.index * tokens;
+            t.tokens = min(tokens, m - t.index * tokens);
+            t.kv_len = L;
+            t.pos0 = L - m + t.index * tokens;
+            return true;
+        }
+        rank -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;
+}
+
+// Keys that the tile's last token sees.
+__device__ __forceinline__ int32_t attn_keys(const AttnArgs& a, const AttnTile& t)
+{
+    return a.causal ? max(0, t.pos0 + t.tokens) : t.kv_len;
+}
+
+// The cache row (of num_pages * Hk * page_size) of head hk's token `at` of sequence n.  An
+// entry outside the cache is reported and read as page 0.
+__device__ __forceinline__ int64_t attn_page_row(const AttnArgs& a, int32_t n, int32_t hk, int32_t at)
+{
+    int32_t page = a.table[(int64_t)n * a.max_pages + (at >> a.page_shift)];
+    if ((uint32_t)page >= (uint32_t)a.num_pages) {
+        report_status(a.status, KDA_ERR_DEVICE_ARG);
+        page = 0;
+    }
+    return (((int64_t)page * a.Hk + hk) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
+}
+
+}  // namespace kda

@@ -1,0 +1,653 @@
+// Attention for several tokens a sequence on CUDA cores (IEEE FP32 products): forward
+// over packed or paged keys, its backward, and the join of pieces of the keys' axis for
+// either type.
+//
+//     s_ij = scale q_i . k_j,  lse_i = log sum_j e^(s_ij),  o_i = sum_j e^(s_ij - lse_i) v_j
+//     p_ij = e^(s_ij - lse_i), delta_i = do_i . o_i, ds_ij = p_ij (do_i . v_j - delta_i)
+//     dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i
+//
+// Bound by the FMA pipe: 4 D operations a score forward, 14 D backward (the two backward
+// kernels each form the scores and the products with v again, so that dk and dv are summed
+// in one CTA over all heads of the group and dq in another: no atomics, the same bits in
+// every run).  A CTA of 256 threads holds a tile of scores in registers, 8 x 4 or 4 x 4 a
+// thread; operands are read from shared memory four channels at a time, the rows of a
+// tile padded by 16 bytes so that 16 lanes' rows lie in different banks.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "kda_attn.cuh"
+#include "kda_paged_tma.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 256;
+constexpr int kKeys = 64, kKeyShift = 6;       // keys of a tile
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ void load4(float* dst, const float* src, bool valid)
+{
+    cp_async16(dst, src, valid);
+}
+__device__ __forceinline__ void load4(float* dst, const __nv_bfloat16* src, bool valid)
+{
+    uint2 u = make_uint2(0, 0);
+    if (valid) u = *reinterpret_cast<const uint2*>(src);
+    *reinterpret_cast<float4*>(dst) =
+        make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                    __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x)
+{
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+}
+
+// A tile's rows: row r is token r / heads of the tile, head first + r % heads of the group.
+struct RowMap {
+    int32_t heads, rows;     // heads of the tile (a row's divisor), rows in use
+    int32_t row0, head0;     // first packed token, first query head
+    int32_t live;            // heads of the tile that the group has
+    __device__ __forceinline__ RowMap(const AttnArgs& a, const AttnShape& sh, int32_t unit, int32_t token0,
+                                      int32_t tokens)
+    {
+        const int32_t hk = unit / sh.parts, part = unit - hk * sh.parts, G = a.Hq / a.Hk;
+        heads = sh.heads;
+        rows = tokens * sh.heads;
+        row0 = token0;
+        head0 = hk * G + part * sh.heads;
+        live = min(sh.heads, G - part * sh.heads);
+    }
+    // (token, head) of row r; false: the row is not in use
+    __device__ __forceinline__ bool at(int32_t r, int32_t& token, int32_t& head) const
+    {
+        const int32_t i = r / heads, g = r - i * heads;
+        token = row0 + i;
+        head = head0 + g;
+        return r < rows && g < live;
+    }
+};
+
+// ROWS rows of D values to shared memory rows of D + 4, zeros where a row is not in use.
+template <int ROWS, int D, typename T>
+__device__ __forceinline__ void load_rows(float* dst, const T* x, int64_t stride, const RowMap& m)
+{
+    for (int e = threadIdx.x; e < ROWS * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), c = e % (D / 4) * 4;
+        int32_t token, head;
+        const bool ok = m.at(r, token, head);
+        load4(dst + r * (D + 4) + c, ok ? x + token * stride + (int64_t)head * D + c : x, ok);
+    }
+}
+// Keys or values `at` .. at + 63 of head hk, zeros past `end`.
+template <int D, int PITCH, typename T>
+__device__ __forceinline__ void load_keys(float* dst, const AttnArgs& a, const T* x, int64_t stride,
+                                          const AttnTile& t, int32_t hk, int32_t at, int32_t end)
+{
+    for (int e = threadIdx.x; e < kKeys * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), c = e % (D / 4) * 4, j = at + r;
+        const bool ok = j < end;
+        const T* src = x;
+        if (ok)
+            src = a.table != nullptr ? x + attn_page_row(a, t.n, hk, j) * D + c
+                                     : x + (t.seq0 + j) * stride + (int64_t)hk * D + c;
+        load4(dst + r * PITCH + c, src, ok);
+    }
+}
+
+// s[i][c] = sum over channels of A row (ty * R + i) and B row (tx + 16 c).
+template <int R, int D>
+__device__ __forceinline__ void scores(float (&s)[R][4], const float* A, const float* B, int ty, int tx)
+{
+    float2 acc[R][4];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][c] = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+        float4 x[R], y[4];
+#pragma unroll
+        for (int i = 0; i < R; ++i) x[i] = *reinterpret_cast<const float4*>(A + (ty * R + i) * (D + 4) + d);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const float4*>(B + (tx + 16 * c) * (D + 4) + d);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                acc[i][c] = fma2(make_float2(x[i].x, x[i].y), make_float2(y[c].x, y[c].y), acc[i][c]);
+                acc[i][c] = fma2(make_float2(x[i].z, x[i].w), make_float2(y[c].z, y[c].w), acc[i][c]);
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[i][c] = acc[i][c].x + acc[i][c].y;
+}
+
+// o[i][h] (four channels 4 tx + 64 h of row ty * R + i) += sum over `keys` of
+// w[row][key] x[key][channel]; w in rows of `pitch`.
+template <int R, int H, int PITCH>
+__device__ __forceinline__ void accumulate(float2 (&o)[R][2 * H], const float* w, int pitch, const float* x,
+                                           int ty, int tx)
+{
+#pragma unroll 2
+    for (int j = 0; j < kKeys; j += 4) {
+        float4 p[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) p[i] = *reinterpret_cast<const float4*>(w + (ty * R + i) * pitch + j);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const float4 y = *reinterpret_cast<const float4*>(x + (j + k) * PITCH + 4 * tx + 64 * h);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float2 pk = both(k == 0 ? p[i].x : k == 1 ? p[i].y : k == 2 ? p[i].z : p[i].w);
+                    o[i][2 * h] = fma2(pk, make_float2(y.x, y.y), o[i][2 * h]);
+                    o[i][2 * h + 1] = fma2(pk, make_float2(y.z, y.w), o[i][2 * h + 1]);
+                }
+            }
+        }
+    }
+}
+// The same with w transposed: o of key ty * 4 + i += sum over rows of w[row][key] x[row][channel].
+template <int ROWS, int H, int PITCH>
+__device__ __forceinline__ void accumulate_t(float2 (&o)[4][2 * H], const float* w, int pitch, const float* x,
+                                             int ty, int tx)
+{
+#pragma unroll 4
+    for (int r = 0; r < ROWS; ++r) {
+        const float4 p = *reinterpret_cast<const float4*>(w + r * pitch + 4 * ty);
+        const float2 pk[4] = {both(p.x), both(p.y), both(p.z), both(p.w)};
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const float4 y = *reinterpret_cast<const float4*>(x + r * PITCH + 4 * tx + 64 * h);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[i][2 * h] = fma2(pk[i], make_float2(y.x, y.y), o[i][2 * h]);
+                o[i][2 * h + 1] = fma2(pk[i], make_float2(y.z, y.w), o[i][2 * h + 1]);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ float over16(float x, bool sum)
+{
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+        const float y = __shfl_xor_sync(0xffffffffu, x, o);
+        x = sum ? x + y : fmaxf(x, y);
+    }
+    return x;
+}
+
+// ---------------------------------------------------------------- forward
+constexpr int kRows = 128;                     // rows of a forward tile
+
+template <int D> struct Fwd {
+    static constexpr int OFF_K = kRows * (D + 4), OFF_V = OFF_K + kKeys * (D + 4), OFF_P = OFF_V + kKeys * D;
+    static constexpr int PITCH_P = kKeys + 4;
+    static constexpr uint32_t SMEM = (OFF_P + kRows * PITCH_P) * 4;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(AttnArgs a, AttnShape sh)
+{
+    using F = Fwd<D>;
+    constexpr int H = D / 64;
+    extern __shared__ __align__(16) float sm[];
+    __shared__ AttnTile s_tile;
+    __shared__ int s_found;
+    float *sQ = sm, *sK = sm + F::OFF_K, *sV = sm + F::OFF_V, *sP = sm + F::OFF_P;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    wait_for_previous();
+    const int32_t piece = blockIdx.x % a.splits, unit = blockIdx.x / a.splits % sh.units,
+                  item = blockIdx.x / a.splits / sh.units;
+    if (tid < 32) {
+        AttnTile t;
+        const bool found = attn_find(a, item, sh.tokens, kKeyShift, t);
+        if (tid == 0) {
+            s_tile = t;
+            s_found = found;
+            if (blockIdx.x == 0 && a.pieces > 1) *static_cast<int32_t*>(a.workspace) = found ? a.cu[a.N] : 0;
+        }
+    }
+    __syncthreads();
+    if (!s_found) return;
+    const AttnTile t = s_tile;
+    const int32_t hk = unit / sh.parts;
+    const RowMap rows(a, sh, unit, t.row0, t.tokens);
+    const T *q = static_cast<const T*>(a.q), *k = static_cast<const T*>(a.k), *v = static_cast<const T*>(a.v);
+    const int32_t keys = attn_keys(a, t), tiles = (keys + kKeys - 1) / kKeys;
+    const int32_t j0 = (int32_t)((int64_t)tiles * piece / a.splits),
+                  j1 = (int32_t)((int64_t)tiles * (piece + 1) / a.splits);
+    const float c = a.scale * kLog2e;
+
+    int32_t limit[8];                          // keys that each of the thread's rows sees
+    float m[8], l[8];
+    float2 o[8][2 * H];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        limit[i] = a.causal ? t.pos0 + (ty * 8 + i) / sh.heads + 1 : t.kv_len;
+        m[i] = -CUDART_INF_F;
+        l[i] = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2 * H; ++h) o[i][h] = make_float2(0.f, 0.f);
+    }
+    if (j0 < j1) {
+        load_rows<kRows, D>(sQ, q, a.q_stride, rows);
+        load_keys<D, D + 4>(sK, a, k, a.k_stride, t, hk, j0 * kKeys, keys);
+        cp_async_commit();
+        load_keys<D, D>(sV, a, v, a.v_stride, t, hk, j0 * kKeys, keys);
+        cp_async_commit();
+    }
+    for (int32_t j = j0; j < j1; ++j) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+        float s[8][4];
+        scores<8, D>(s, sQ, sK, ty, tx);
+        __syncthreads();
+        if (j + 1 < j1) load_keys<D, D + 4>(sK, a, k, a.k_stride, t, hk, (j + 1) * kKeys, keys);
+        cp_async_commit();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float top = -CUDART_INF_F;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                s[i][n] = j * kKeys + tx + 16 * n < limit[i] ? s[i][n] * c : -CUDART_INF_F;
+                top = fmaxf(top, s[i][n]);
+            }
+            top = fmaxf(m[i], over16(top, false));
+            const float ref = top == -CUDART_INF_F ? 0.f : top, keep = exp2f(m[i] - ref);
+            m[i] = top;
+            l[i] *= keep;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const float e = exp2f(s[i][n] - ref);
+                l[i] += e;
+                sP[(ty * 8 + i) * F::PITCH_P + tx + 16 * n] = e;
+            }
+#pragma unroll
+            for (int h = 0; h < 2 * H; ++h) o[i][h] = mul2(o[i][h], both(keep));
+        }
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+        accumulate<8, H, D>(o, sP, F::PITCH_P, sV, ty, tx);
+        __syncthreads();
+        if (j + 1 < j1) load_keys<D, D>(sV, a, v, a.v_stride, t, hk, (j + 1) * kKeys, keys);
+        cp_async_commit();
+    }
+    char* ws = static_cast<char*>(a.workspace);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float sum = over16(l[i], true), inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float ref = m[i] == -CUDART_INF_F ? 0.f : m[i];
+        int32_t token, head;
+        if (!rows.at(ty * 8 + i, token, head)) continue;
+        const int64_t r = (int64_t)token * a.Hq + head;
+        const float lse = ref * kLn2 + logf(sum);
+        if (a.pieces > 1) {
+            float* y = reinterpret_cast<float*>(ws + attn_pieces_o(a, piece)) + r * D + 4 * tx;
+            if (tx == 0) reinterpret_cast<float*>(ws + attn_pieces_lse(a, piece))[r] = lse;
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+                store4(y + 64 * h, make_float4(o[i][2 * h].x * inv, o[i][2 * h].y * inv, o[i][2 * h + 1].x * inv,
+                                               o[i][2 * h + 1].y * inv));
+        } else {
+            T* y = static_cast<T*>(a.out) + r * D + 4 * tx;
+            if (tx == 0 && a.lse != nullptr) a.lse[r] = lse;
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+                store4(y + 64 * h, make_float4(o[i][2 * h].x * inv, o[i][2 * h].y * inv, o[i][2 * h + 1].x * inv,
+                                               o[i][2 * h + 1].y * inv));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- join
+// out = sum_p e^(lse_p - lse) o_p, lse = log sum_p e^(lse_p): a warp a row, whose lanes have D / 32
+// channels each.  A piece without weight (lse -infinity) is not read.
+template <typename T, int D> __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a)
+{
+    constexpr int C = D / 32;
+    wait_for_previous();
+    const char* ws = static_cast<const char*>(a.workspace);
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= (int64_t)*reinterpret_cast<const int32_t*>(ws) * a.Hq) return;
+    float top = -CUDART_INF_F;
+    bool nan = false;
+    for (int p = lane; p < a.pieces; p += 32) {
+        const float x = reinterpret_cast<const float*>(ws + attn_pieces_lse(a, p))[row];
+        top = fmaxf(top, x);
+        nan |= x != x;
+    }
+    top = warp_max(top);
+    nan = __any_sync(0xffffffffu, nan);
+    float sum = 0.f, o[C] = {};
+    for (int p = 0; p < a.pieces; ++p) {
+        const float x = reinterpret_cast<const float*>(ws + attn_pieces_lse(a, p))[row];
+        if (x == -CUDART_INF_F) continue;
+        const float w = exp2f((x - top) * kLog2e);
+        sum += w;
+        const float* y = reinterpret_cast<const float*>(ws + attn_pieces_o(a, p)) + row * D + C * lane;
+        if constexpr (C == 4) {
+            const float4 z = *reinterpret_cast<const float4*>(y);
+            o[0] = fmaf(w, z.x, o[0]); o[1] = fmaf(w, z.y, o[1]); o[2] = fmaf(w, z.z, o[2]); o[3] = fmaf(w, z.w, o[3]);
+        } else {
+            const float2 z = *reinterpret_cast<const float2*>(y);
+            o[0] = fmaf(w, z.x, o[0]); o[1] = fmaf(w, z.y, o[1]);
+        }
+    }
+    const float inv = nan ? CUDART_NAN_F : sum == 0.f ? 0.f : 1.f / sum;
+    if (lane == 0 && a.lse != nullptr)
+        a.lse[row] = nan ? CUDART_NAN_F : sum == 0.f ? -CUDART_INF_F : top + logf(sum);
+    T* y = static_cast<T*>(a.out) + row * D + C * lane;
+    if constexpr (C == 4) {
+        store4(y, make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv));
+    } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float2*>(y) = make_float2(o[0] * inv, o[1] * inv);
+    } else {
+        *reinterpret_cast<uint32_t*>(y) = pack_bf16(o[0] * inv, o[1] * inv);
+    }
+}
+
+// ---------------------------------------------------------------- backward
+// delta = do . o of every row, a warp a row.
+template <typename T, int D> __global__ void __launch_bounds__(256) attn_delta_kernel(AttnArgs a)
+{
+    constexpr int C = D / 32;
+    wait_for_previous();
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= (int64_t)a.T * a.Hq) return;
+    const T *x = static_cast<const T*>(a.dout) + row * D + C * lane, *y = static_cast<const T*>(a.out) + row * D + C * lane;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) s = fmaf(load_as_float(x + i), load_as_float(y + i), s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) a.delta[row] = s;
+}
+
+constexpr int kBwdRows = 64;                   // rows of a backward tile
+
+template <int D> struct Bwd {
+    static constexpr int TILE = 64 * (D + 4), PITCH_P = kKeys + 4;
+    static constexpr int OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = 3 * TILE, OFF_P = 4 * TILE,
+                         OFF_DS = OFF_P + kBwdRows * PITCH_P, OFF_L = OFF_DS + kBwdRows * PITCH_P;
+    static constexpr uint32_t SMEM = (OFF_L + 2 * kBwdRows) * 4;
+};
+
+// lse * log2 e and delta of a tile's rows; +infinity where a row is not in use or has no
+// weight, which gives it weights of zero.
+__device__ __forceinline__ void load_stats(float* dst, const AttnArgs& a, const RowMap& rows)
+{
+    const int r = threadIdx.x;
+    if (r >= kBwdRows) return;
+    int32_t token, head;
+    const bool ok = rows.at(r, token, head);
+    const int64_t at = (int64_t)token * a.Hq + head;
+    const float lse = ok ? a.lse_in[at] : CUDART_INF_F;
+    dst[r] = lse == -CUDART_INF_F ? CUDART_INF_F : lse * kLog2e;
+    dst[kBwdRows + r] = ok ? a.delta[at] : 0.f;
+}
+
+// P and dS of a tile: rows ty * 4 + i, keys tx + 16 n.
+template <int D>
+__device__ __forceinline__ void weights(float (&p)[4][4], float (&ds)[4][4], const float* sm, const AttnArgs& a,
+                                        int32_t pos0, int32_t heads, int32_t key0, int32_t end, int ty, int tx)
+{
+    using B = Bwd<D>;
+    const float c = a.scale * kLog2e;
+    scores<4, D>(p, sm, sm + B::OFF_K, ty, tx);
+    scores<4, D>(ds, sm + B::OFF_DO, sm + B::OFF_V, ty, tx);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty * 4 + i;
+        const int32_t limit = min(end, pos0 + r / heads + 1);
+        const float lse = sm[B::OFF_L + r], delta = sm[B::OFF_L + kBwdRows + r];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const bool live = key0 + tx + 16 * n < limit;
+            p[i][n] = live ? exp2f(fmaf(p[i][n], c, -lse)) : 0.f;
+            ds[i][n] = live ? p[i][n] * (ds[i][n] - delta) : 0.f;
+        }
+    }
+}
+
+// dk and dv of 64 keys, over all rows that see them.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(AttnArgs a, AttnShape sh)
+{
+    using B = Bwd<D>;
+    constexpr int H = D / 64;
+    extern __shared__ __align__(16) float sm[];
+    __shared__ AttnTile s_tile;
+    __shared__ int s_found;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    wait_for_previous();
+    const int32_t hk = blockIdx.x % a.Hk, item = blockIdx.x / a.Hk;
+    if (tid < 32) {
+        AttnTile t;
+        const bool found = attn_find(a, item, kKeys, kKeyShift, t);
+        if (tid == 0) {
+            s_tile = t;
+            s_found = found;
+        }
+    }
+    __syncthreads();
+    if (!s_found) return;
+    const AttnTile t = s_tile;
+    // the tile found has t.index tiles of queries before it; the one with as many behind it
+    const int32_t nt = (t.seq_tokens + kKeys - 1) / kKeys, key0 = (nt - 1 - t.index) * kKeys;
+    const int32_t end = t.seq_tokens;
+    load_keys<D, D + 4>(sm + B::OFF_K, a, static_cast<const T*>(a.k), a.k_stride, t, hk, key0, end);
+    load_keys<D, D + 4>(sm + B::OFF_V, a, static_cast<const T*>(a.v), a.v_stride, t, hk, key0, end);
+    float2 dk[4][2 * H], dv[4][2 * H];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2 * H; ++h) dk[i][h] = dv[i][h] = make_float2(0.f, 0.f);
+    for (int32_t part = 0; part < sh.parts; ++part) {
+        for (int32_t at = key0; at < t.seq_tokens; at += sh.tokens) {
+            const RowMap rows(a, sh, hk * sh.parts + part, t.seq0 + at, min(sh.tokens, t.seq_tokens - at));
+            __syncthreads();
+            load_rows<kBwdRows, D>(sm, static_cast<const T*>(a.q), a.q_stride, rows);
+            load_rows<kBwdRows, D>(sm + B::OFF_DO, static_cast<const T*>(a.dout), (int64_t)a.Hq * D, rows);
+            load_stats(sm + B::OFF_L, a, rows);
+            cp_async_commit();
+            cp_async_wait_all();
+            __syncthreads();
+            float p[4][4], ds[4][4];
+            weights<D>(p, ds, sm, a, at, sh.heads, key0, end, ty, tx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    sm[B::OFF_P + (ty * 4 + i) * B::PITCH_P + tx + 16 * n] = p[i][n];
+                    sm[B::OFF_DS + (ty * 4 + i) * B::PITCH_P + tx + 16 * n] = ds[i][n];
+                }
+            __syncthreads();
+            accumulate_t<kBwdRows, H, D + 4>(dv, sm + B::OFF_P, B::PITCH_P, sm + B::OFF_DO, ty, tx);
+            accumulate_t<kBwdRows, H, D + 4>(dk, sm + B::OFF_DS, B::PITCH_P, sm, ty, tx);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int32_t j = key0 + ty * 4 + i;
+        if (j >= end) continue;
+        const int64_t r = ((int64_t)(t.seq0 + j) * a.Hk + hk) * D + 4 * tx;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const float2 x = dk[i][2 * h], y = dk[i][2 * h + 1];
+            store4(static_cast<T*>(a.dk) + r + 64 * h,
+                   make_float4(x.x * a.scale, x.y * a.scale, y.x * a.scale, y.y * a.scale));
+            store4(static_cast<T*>(a.dv) + r + 64 * h,
+                   make_float4(dv[i][2 * h].x, dv[i][2 * h].y, dv[i][2 * h + 1].x, dv[i][2 * h + 1].y));
+        }
+    }
+}
+
+// dq of a tile of rows, over the keys they see.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(AttnArgs a, AttnShape sh)
+{
+    using B = Bwd<D>;
+    constexpr int H = D / 64;
+    extern __shared__ __align__(16) float sm[];
+    __shared__ AttnTile s_tile;
+    __shared__ int s_found;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    wait_for_previous();
+    const int32_t unit = blockIdx.x % sh.units, item = blockIdx.x / sh.units;
+    if (tid < 32) {
+        AttnTile t;
+        const bool found = attn_find(a, item, sh.tokens, kKeyShift, t);
+        if (tid == 0) {
+            s_tile = t;
+            s_found = found;
+        }
+    }
+    __syncthreads();
+    if (!s_found) return;
+    const AttnTile t = s_tile;
+    const int32_t hk = unit / sh.parts, end = attn_keys(a, t);
+    const RowMap rows(a, sh, unit, t.row0, t.tokens);
+    load_rows<kBwdRows, D>(sm, static_cast<const T*>(a.q), a.q_stride, rows);
+    load_rows<kBwdRows, D>(sm + B::OFF_DO, static_cast<const T*>(a.dout), (int64_t)a.Hq * D, rows);
+    load_stats(sm + B::OFF_L, a, rows);
+    float2 dq[4][2 * H];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2 * H; ++h) dq[i][h] = make_float2(0.f, 0.f);
+    for (int32_t key0 = 0; key0 < end; key0 += kKeys) {
+        __syncthreads();
+        load_keys<D, D + 4>(sm + B::OFF_K, a, static_cast<const T*>(a.k), a.k_stride, t, hk, key0, end);
+        load_keys<D, D + 4>(sm + B::OFF_V, a, static_cast<const T*>(a.v), a.v_stride, t, hk, key0, end);
+        cp_async_commit();
+        cp_async_wait_all();
+        __syncthreads();
+        float p[4][4], ds[4][4];
+        weights<D>(p, ds, sm, a, t.pos0, sh.heads, key0, end, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) sm[B::OFF_DS + (ty * 4 + i) * B::PITCH_P + tx + 16 * n] = ds[i][n];
+        __syncthreads();
+        accumulate<4, H, D + 4>(dq, sm + B::OFF_DS, B::PITCH_P, sm + B::OFF_K, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int32_t token, head;
+        if (!rows.at(ty * 4 + i, token, head)) continue;
+        T* y = static_cast<T*>(a.dq) + ((int64_t)token * a.Hq + head) * D + 4 * tx;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            store4(y + 64 * h, make_float4(dq[i][2 * h].x * a.scale, dq[i][2 * h].y * a.scale,
+                                           dq[i][2 * h + 1].x * a.scale, dq[i][2 * h + 1].y * a.scale));
+    }
+}
+
+// ---------------------------------------------------------------- launch
+AttnShape shape(int32_t rows, int32_t Hq, int32_t Hk)
+{
+    AttnShape s;
+    const int32_t G = Hq / Hk;
+    s.heads = G < rows ? G : rows;
+    s.parts = (G + s.heads - 1) / s.heads;
+    s.tokens = rows / s.heads;
+    s.units = Hk * s.parts;
+    return s;
+}
+// Tiles of a call: every one has a token, and all but a sequence's last are full.
+int64_t tiles(int32_t N, int32_t T, int32_t tokens)
+{
+    const int64_t n = (int64_t)T / tokens + N;
+    return n < T ? n : T;
+}
+
+template <typename T, int D> cudaError_t forward(const AttnArgs& a, cudaStream_t stream)
+{
+    const AttnShape sh = shape(kRows, a.Hq, a.Hk);
+    const int64_t ctas = tiles(a.N, a.T, sh.tokens) * sh.units * a.splits;
+    if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+    auto kern = attn_fwd_kernel<T, D>;
+    static std::atomic<uint64_t> set{0};
+    const cudaError_t e = allow_smem(kern, Fwd<D>::SMEM, &set);
+    if (e != cudaSuccess) return e;
+    return launch_after(kern, launch_config(ctas, kThreads, Fwd<D>::SMEM), stream, a, sh);
+}
+
+template <typename T, int D> cudaError_t backward(const AttnArgs& a, cudaStream_t stream)
+{
+    const AttnShape sh = shape(kBwdRows, a.Hq, a.Hk);
+    const int64_t rows = (int64_t)a.T * a.Hq;
+    cudaError_t e = launch_after(attn_delta_kernel<T, D>, launch_config((rows + 7) / 8, 256), stream, a);
+    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> set_kv{0}, set_q{0};
+    e = allow_smem(attn_bwd_kv_kernel<T, D>, Bwd<D>::SMEM, &set_kv);
+    if (e == cudaSuccess) e = allow_smem(attn_bwd_q_kernel<T, D>, Bwd<D>::SMEM, &set_q);
+    if (e != cudaSuccess) return e;
+    e = launch_after(attn_bwd_kv_kernel<T, D>,
+                     launch_config(tiles(a.N, a.T, kKeys) * a.Hk, kThreads, Bwd<D>::SMEM), stream, a, sh);
+    if (e != cudaSuccess) return e;
+    return launch_after(attn_bwd_q_kernel<T, D>,
+                        launch_config(tiles(a.N, a.T, sh.tokens) * sh.units, kThreads, Bwd<D>::SMEM), stream, a,
+                        sh);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t stream)
+{
+    const cudaLaunchConfig_t cfg = launch_config(((int64_t)a.T * a.Hq + 7) / 8, 256);
+    if (a.bf16)
+        return a.D == 64 ? launch_after(attn_join_kernel<__nv_bfloat16, 64>, cfg, stream, a)
+                         : launch_after(attn_join_kernel<__nv_bfloat16, 128>, cfg, stream, a);
+    return a.D == 64 ? launch_after(attn_join_kernel<float, 64>, cfg, stream, a)
+                     : launch_after(attn_join_kernel<float, 128>, cfg, stream, a);
+}
+
+int32_t attn_splits(bool bf16, int32_t N, int32_t T, int32_t Hq, int32_t Hk, int32_t D, int64_t kv_most)
+{
+    const AttnShape sh = shape(kRows, Hq, Hk);
+    const int64_t ctas = tiles(N, T, sh.tokens) * sh.units, most = 2 * (int64_t)sm_count();
+    if (ctas * 2 > most) return 1;
+    const int64_t by_keys = kv_most / (4 * kKeys), by_ctas = most / ctas;
+    int64_t s = by_ctas < by_keys ? by_ctas : by_keys;
+    return (int32_t)(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+
+cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream)
+{
+    cudaError_t e;
+    if (a.bf16)
+        e = a.D == 64 ? forward<__nv_bfloat16, 64>(a, stream) : forward<__nv_bfloat16, 128>(a, stream);
+    else
+        e = a.D == 64 ? forward<float, 64>(a, stream) : forward<float, 128>(a, stream);
+    return e;
+}
+
+int64_t attention_bwd_workspace_bytes(int32_t N, int32_t T, int32_t Hq, int32_t Hk, int32_t D)
+{
+    return ((int64_t)T * Hq * 4 + 255) / 256 * 256 + 16;
+}
+
+cudaError_t launch_attention_bwd(const AttnArgs& args, cudaStream_t stream)
+{
+    AttnArgs a = args;
+    a.delta = static_cast<float*>(a.workspace);
+    if (a.bf16) return a.D == 64 ? backward<__nv_bfloat16, 64>(a, stream) : backward<__nv_bfloat16, 128>(a, stream);
+    return a.D == 64 ? backward<float, 64>(a, stream) : backward<float, 128>(a, stream);
+}
+
+}  // namespace kda

@@ -15,6 +15,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <array>
 #include <map>
 #include <string>
 #include <utility>
@@ -35,10 +37,20 @@ struct Library {
     decltype(&kda_qk_norm_rope_bwd_workspace_size) rope_bwd_size;
     decltype(&kda_paged_decode) decode;
     decltype(&kda_paged_decode_workspace_size) decode_size;
+    decltype(&kda_attention_fwd) attention;
+    decltype(&kda_attention_workspace_size) attention_size;
+    decltype(&kda_attention_bwd) attention_bwd;
+    decltype(&kda_attention_bwd_workspace_size) attention_bwd_size;
+    decltype(&kda_paged_prompt) prompt;
+    decltype(&kda_paged_decode_shared) shared;
+    decltype(&kda_paged_decode_shared_workspace_size) shared_size;
 } lib;
 const char* const kNames[] = {"kda_page_plan", "kda_qk_norm_rope", "kda_qk_norm_rope_append",
                               "kda_qk_norm_rope_bwd", "kda_qk_norm_rope_bwd_workspace_size",
-                              "kda_paged_decode", "kda_paged_decode_workspace_size"};
+                              "kda_paged_decode", "kda_paged_decode_workspace_size",
+                              "kda_attention_fwd", "kda_attention_workspace_size", "kda_attention_bwd",
+                              "kda_attention_bwd_workspace_size", "kda_paged_prompt",
+                              "kda_paged_decode_shared", "kda_paged_decode_shared_workspace_size"};
 
 // A Python exception is set; unwinds to the entry point.
 struct Raised {};
@@ -253,9 +265,11 @@ Workspace workspace(PyObject* given, int64_t bytes, const Tensor& t, const Strea
 }
 
 // Sizes depend on the device and the arguments alone; asked once each.
-template <typename F> int64_t size_of(F ask, const int64_t (&key)[4], std::map<std::array<int64_t, 4>, int64_t>& known)
+template <typename F, size_t K>
+int64_t size_of(F ask, const int64_t (&key)[K], std::map<std::array<int64_t, K>, int64_t>& known)
 {
-    const std::array<int64_t, 4> k = {key[0], key[1], key[2], key[3]};
+    std::array<int64_t, K> k;
+    std::copy(key, key + K, k.begin());
     const auto it = known.find(k);
     if (it != known.end()) return it->second;
     int64_t bytes = 0;
@@ -525,6 +539,165 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// q [T, Hq, D] and k, v [T, Hk, D] of packed sequences.
+struct Packed {
+    const Heads h;
+    const ScalarType dt;
+    const Rows q, k, v;
+    const int32_t* cu;
+    int32_t N;
+    Packed(const Tensor& q_, const Tensor& k_, const Tensor& v_, const Tensor& cu_)
+        : h(q_, k_), dt(q_.scalar_type()), q(rows(q_, "q", dt, h.T, h.Hq, h.D)),
+          k(rows(k_, "k", dt, h.T, h.Hk, h.D)), v(rows(v_, "v", dt, h.T, h.Hk, h.D)),
+          cu(pointer<int32_t>(cu_, "cu_seqlens", ScalarType::Int))
+    {
+        if (cu_.numel() < 1) raise(PyExc_ValueError, "cu_seqlens must have at least one element");
+        N = as_i32(cu_.numel() - 1, "the number of sequences");
+    }
+};
+float scale_or_default(PyObject* o, int64_t D)
+{
+    return o == Py_None ? (float)(1.0 / std::sqrt((double)D)) : number(o, "scale");
+}
+// lse given, or a new one of [rows, Hq] where it is wanted.
+Tensor lse_of(PyObject* given, PyObject* wanted, int64_t rows, int64_t Hq, const Tensor& q)
+{
+    if (given != Py_None) return tensor(given, "lse");
+    return flag(wanted) ? at::empty({rows, Hq}, like(q, ScalarType::Float)) : Tensor();
+}
+float* lse_pointer(const Tensor& lse, int64_t n)
+{
+    return lse.defined() ? pointer<float>(lse, "lse", ScalarType::Float, n) : nullptr;
+}
+int64_t two(int32_t a, int32_t b) { return ((int64_t)a << 32) | (uint32_t)b; }
+
+PyObject* attention_fwd(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return entry(a, n, 11, [&]() -> PyObject* {
+        const Tensor& q = tensor(a[0], "q");
+        const Packed p(q, tensor(a[1], "k"), tensor(a[2], "v"), tensor(a[3], "cu_seqlens"));
+        const Heads& h = p.h;
+        const Stream s(a[9], q);
+        const Tensor out = output(a[5], "out", {h.T, h.Hq, h.D}, q, p.dt), lse = lse_of(a[6], a[7], h.T, h.Hq, q);
+        static auto* known = new std::map<std::array<int64_t, 5>, int64_t>;
+        const int64_t bytes = a[10] != Py_None ? 0 : size_of(
+            [&](int64_t* b) { return lib.attention_size(p.N, h.T, h.Hq, h.Hk, h.D, b); },
+            {q.device().index(), two(h.Hq, h.Hk), h.D, p.N, h.T}, *known);
+        const Workspace w = workspace(a[10], bytes, q, s);
+        const kda_status st = lib.attention(
+            p.q.p, p.q.stride, p.k.p, p.k.stride, p.v.p, p.v.stride, code(p.dt), p.cu, p.N, h.T, h.Hq, h.Hk,
+            h.D, scale_or_default(a[4], h.D), dense(out, "out", p.dt, h.T, h.Hq, h.D),
+            lse_pointer(lse, h.T * h.Hq), w.p, w.bytes, any_pointer<int32_t>(a[8], "status"), s.handle());
+        if (st != KDA_OK) return status(st);
+        return tuple({wrap(out), wrap_or_none(lse)});
+    });
+}
+
+PyObject* attention_bwd(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return entry(a, n, 14, [&]() -> PyObject* {
+        const Tensor &q = tensor(a[0], "q"), &out = tensor(a[3], "out"), &lse = tensor(a[4], "lse"),
+                     &dout = tensor(a[5], "dout");
+        const Packed p(q, tensor(a[1], "k"), tensor(a[2], "v"), tensor(a[6], "cu_seqlens"));
+        const Heads& h = p.h;
+        const Stream s(a[12], q);
+        const Tensor qg = output(a[8], "q_grad", {h.T, h.Hq, h.D}, q, p.dt),
+                     kg = output(a[9], "k_grad", {h.T, h.Hk, h.D}, q, p.dt),
+                     vg = output(a[10], "v_grad", {h.T, h.Hk, h.D}, q, p.dt);
+        static auto* known = new std::map<std::array<int64_t, 5>, int64_t>;
+        const int64_t bytes = a[13] != Py_None ? 0 : size_of(
+            [&](int64_t* b) { return lib.attention_bwd_size(p.N, h.T, h.Hq, h.Hk, h.D, b); },
+            {q.device().index(), two(h.Hq, h.Hk), h.D, p.N, h.T}, *known);
+        const Workspace w = workspace(a[13], bytes, q, s);
+        const kda_status st = lib.attention_bwd(
+            p.q.p, p.q.stride, p.k.p, p.k.stride, p.v.p, p.v.stride, code(p.dt),
+            dense(out, "out", p.dt, h.T, h.Hq, h.D), lse_pointer(lse, h.T * h.Hq),
+            dense(dout, "dout", p.dt, h.T, h.Hq, h.D), p.cu, p.N, h.T, h.Hq, h.Hk, h.D,
+            scale_or_default(a[7], h.D), dense(qg, "q_grad", p.dt, h.T, h.Hq, h.D),
+            dense(kg, "k_grad", p.dt, h.T, h.Hk, h.D), dense(vg, "v_grad", p.dt, h.T, h.Hk, h.D), w.p, w.bytes,
+            any_pointer<int32_t>(a[11], "status"), s.handle());
+        if (st != KDA_OK) return status(st);
+        return tuple({wrap(qg), wrap(kg), wrap(vg)});
+    });
+}
+
+// A block table of `rows` rows.
+const int32_t* table_of(const Tensor& t, const char* name, int64_t rows)
+{
+    if (t.dim() != 2 || t.size(0) != rows)
+        raise(PyExc_ValueError, "%s must have shape [%lld, max_pages]", name, (long long)rows);
+    return pointer<int32_t>(t, name, ScalarType::Int);
+}
+
+PyObject* paged_prompt(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return entry(a, n, 13, [&]() -> PyObject* {
+        const Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache"),
+                     &table = tensor(a[3], "block_table"), &lens = tensor(a[4], "seq_lens"),
+                     &cu = tensor(a[5], "cu_seqlens");
+        if (q.dim() != 3) raise(PyExc_ValueError, "q must have shape [T, Hq, D]");
+        const int64_t T = q.size(0), N = lens.numel();
+        const int32_t Hq = as_i32(q.size(1), "the number of heads"), D = as_i32(q.size(2), "the head dimension");
+        need_caches(kc, vc, -1, D);
+        const int32_t Hk = as_i32(kc.size(1), "the number of heads"), N32 = as_i32(N, "the number of requests");
+        const auto dt = kc.scalar_type();
+        const Rows qr = rows(q, "q", dt, T, Hq, D);
+        const int32_t* tp = table_of(table, "block_table", N);
+        const Stream s(a[11], q);
+        const Tensor out = output(a[7], "out", {T, Hq, D}, q, dt), lse = lse_of(a[8], a[9], T, Hq, q);
+        static auto* known = new std::map<std::array<int64_t, 5>, int64_t>;
+        const int64_t bytes = a[12] != Py_None ? 0 : size_of(
+            [&](int64_t* b) { return lib.attention_size(N32, T, Hq, Hk, D, b); },
+            {q.device().index(), two(Hq, Hk), D, N, T}, *known);
+        const Workspace w = workspace(a[12], bytes, q, s);
+        const kda_status st = lib.prompt(
+            qr.p, qr.stride, pointer(kc, "k_cache", dt), pointer(vc, "v_cache", dt), code(dt), tp,
+            pointer<int32_t>(lens, "seq_lens", ScalarType::Int, N),
+            pointer<int32_t>(cu, "cu_seqlens", ScalarType::Int, N + 1), N32, T, Hq, Hk, D,
+            as_i32(kc.size(0), "the number of pages"), as_i32(kc.size(2), "page_size"),
+            as_i32(table.size(1), "max_pages"), scale_or_default(a[6], D), dense(out, "out", dt, T, Hq, D),
+            lse_pointer(lse, T * Hq), w.p, w.bytes, any_pointer<int32_t>(a[10], "status"), s.handle());
+        if (st != KDA_OK) return status(st);
+        return tuple({wrap(out), wrap_or_none(lse)});
+    });
+}
+
+PyObject* paged_decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return entry(a, n, 15, [&]() -> PyObject* {
+        const Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache"),
+                     &ptable = tensor(a[3], "prefix_table"), &plens = tensor(a[4], "prefix_lens"),
+                     &cu = tensor(a[5], "cu_groups"), &table = tensor(a[6], "block_table"),
+                     &lens = tensor(a[7], "seq_lens");
+        if (q.dim() != 3) raise(PyExc_ValueError, "q must have shape [N, Hq, D]");
+        const int64_t N = q.size(0), groups = plens.numel();
+        const int32_t Hq = as_i32(q.size(1), "the number of heads"), D = as_i32(q.size(2), "the head dimension");
+        need_caches(kc, vc, -1, D);
+        const int32_t Hk = as_i32(kc.size(1), "the number of heads"), N32 = as_i32(N, "the number of requests"),
+                      g32 = as_i32(groups, "the number of groups");
+        const auto dt = kc.scalar_type(), i32 = ScalarType::Int;
+        const void* qp = pointer(q, "q", dt);
+        const int32_t *pt = table_of(ptable, "prefix_table", groups), *tp = table_of(table, "block_table", N);
+        const Stream s(a[13], q);
+        const Tensor out = output(a[9], "out", {N, Hq, D}, q, dt), lse = lse_of(a[10], a[11], N, Hq, q);
+        static auto* known = new std::map<std::array<int64_t, 5>, int64_t>;
+        const int64_t bytes = a[14] != Py_None ? 0 : size_of(
+            [&](int64_t* b) { return lib.shared_size(N32, g32, Hq, Hk, D, b); },
+            {q.device().index(), two(Hq, Hk), D, N, groups}, *known);
+        const Workspace w = workspace(a[14], bytes, q, s);
+        const kda_status st = lib.shared(
+            qp, pointer(kc, "k_cache", dt), pointer(vc, "v_cache", dt), code(dt), pt,
+            pointer<int32_t>(plens, "prefix_lens", i32, groups),
+            pointer<int32_t>(cu, "cu_groups", i32, groups + 1), g32, as_i32(ptable.size(1), "max_prefix_pages"),
+            tp, pointer<int32_t>(lens, "seq_lens", i32, N), N32, Hq, Hk, D,
+            as_i32(kc.size(0), "the number of pages"), as_i32(kc.size(2), "page_size"),
+            as_i32(table.size(1), "max_pages"), scale_or_default(a[8], D), dense(out, "out", dt, N, Hq, D),
+            lse_pointer(lse, N * Hq), w.p, w.bytes, any_pointer<int32_t>(a[12], "status"), s.handle());
+        if (st != KDA_OK) return status(st);
+        return tuple({wrap(out), wrap_or_none(lse)});
+    });
+}
+
 // bind(names -> addresses): the loaded library's functions.
 PyObject* bind(PyObject*, PyObject* addresses)
 {
@@ -547,6 +720,10 @@ PyMethodDef kMethods[] = {{"bind", bind, METH_O, nullptr},
                           {"append", fast(append), METH_FASTCALL, nullptr},
                           {"norm_rope_bwd", fast(norm_rope_bwd), METH_FASTCALL, nullptr},
                           {"paged_decode", fast(paged_decode), METH_FASTCALL, nullptr},
+                          {"attention_fwd", fast(attention_fwd), METH_FASTCALL, nullptr},
+                          {"attention_bwd", fast(attention_bwd), METH_FASTCALL, nullptr},
+                          {"paged_prompt", fast(paged_prompt), METH_FASTCALL, nullptr},
+                          {"paged_decode_shared", fast(paged_decode_shared), METH_FASTCALL, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods};
 
