@@ -67,6 +67,7 @@ struct AttnShape {
     int32_t units;           // Hk * parts
 };
 
+cudaError_t launch_attention_tc(const AttnArgs& a, cudaStream_t stream);      // BF16
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attention_bwd(const AttnArgs& a, cudaStream_t stream);
 int64_t attention_bwd_workspace_bytes(int32_t N, int32_t T, int32_t Hq, int32_t Hk, int32_t D);

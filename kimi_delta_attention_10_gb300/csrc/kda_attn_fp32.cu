@@ -19,8 +19,7 @@
 
 #include <atomic>
 
-#include "kda_attn.cuh"
-#include "kda_paged_tma.cuh"
+#include "kda_attn_tc.cuh"
 
 namespace kda {
 namespace {
@@ -558,27 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(AttnArgs a, Att
 }
 
 // ---------------------------------------------------------------- launch
-AttnShape shape(int32_t rows, int32_t Hq, int32_t Hk)
-{
-    AttnShape s;
-    const int32_t G = Hq / Hk;
-    s.heads = G < rows ? G : rows;
-    s.parts = (G + s.heads - 1) / s.heads;
-    s.tokens = rows / s.heads;
-    s.units = Hk * s.parts;
-    return s;
-}
-// Tiles of a call: every one has a token, and all but a sequence's last are full.
-int64_t tiles(int32_t N, int32_t T, int32_t tokens)
-{
-    const int64_t n = (int64_t)T / tokens + N;
-    return n < T ? n : T;
-}
-
 template <typename T, int D> cudaError_t forward(const AttnArgs& a, cudaStream_t stream)
 {
-    const AttnShape sh = shape(kRows, a.Hq, a.Hk);
-    const int64_t ctas = tiles(a.N, a.T, sh.tokens) * sh.units * a.splits;
+    const AttnShape sh = attn_shape(kRows, a.Hq, a.Hk);
+    const int64_t ctas = attn_tiles(a.N, a.T, sh.tokens) * sh.units * a.splits;
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
     auto kern = attn_fwd_kernel<T, D>;
     static std::atomic<uint64_t> set{0};
@@ -589,7 +571,7 @@ template <typename T, int D> cudaError_t forward(const AttnArgs& a, cudaStream_t
 
 template <typename T, int D> cudaError_t backward(const AttnArgs& a, cudaStream_t stream)
 {
-    const AttnShape sh = shape(kBwdRows, a.Hq, a.Hk);
+    const AttnShape sh = attn_shape(kBwdRows, a.Hq, a.Hk);
     const int64_t rows = (int64_t)a.T * a.Hq;
     cudaError_t e = launch_after(attn_delta_kernel<T, D>, launch_config((rows + 7) / 8, 256), stream, a);
     if (e != cudaSuccess) return e;
@@ -598,10 +580,10 @@ template <typename T, int D> cudaError_t backward(const AttnArgs& a, cudaStream_
     if (e == cudaSuccess) e = allow_smem(attn_bwd_q_kernel<T, D>, Bwd<D>::SMEM, &set_q);
     if (e != cudaSuccess) return e;
     e = launch_after(attn_bwd_kv_kernel<T, D>,
-                     launch_config(tiles(a.N, a.T, kKeys) * a.Hk, kThreads, Bwd<D>::SMEM), stream, a, sh);
+                     launch_config(attn_tiles(a.N, a.T, kKeys) * a.Hk, kThreads, Bwd<D>::SMEM), stream, a, sh);
     if (e != cudaSuccess) return e;
     return launch_after(attn_bwd_q_kernel<T, D>,
-                        launch_config(tiles(a.N, a.T, sh.tokens) * sh.units, kThreads, Bwd<D>::SMEM), stream, a,
+                        launch_config(attn_tiles(a.N, a.T, sh.tokens) * sh.units, kThreads, Bwd<D>::SMEM), stream, a,
                         sh);
 }
 
@@ -619,10 +601,10 @@ cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t stream)
 
 int32_t attn_splits(bool bf16, int32_t N, int32_t T, int32_t Hq, int32_t Hk, int32_t D, int64_t kv_most)
 {
-    const AttnShape sh = shape(kRows, Hq, Hk);
-    const int64_t ctas = tiles(N, T, sh.tokens) * sh.units, most = 2 * (int64_t)sm_count();
+    const AttnShape sh = attn_shape(bf16 ? kTcRows : kRows, Hq, Hk);
+    const int64_t ctas = attn_tiles(N, T, bf16 ? 2 * sh.tokens : sh.tokens) * sh.units, most = 2 * (int64_t)sm_count();
     if (ctas * 2 > most) return 1;
-    const int64_t by_keys = kv_most / (4 * kKeys), by_ctas = most / ctas;
+    const int64_t by_keys = kv_most / (4 * (bf16 ? kTcKeys : kKeys)), by_ctas = most / ctas;
     int64_t s = by_ctas < by_keys ? by_ctas : by_keys;
     return (int32_t)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
@@ -631,7 +613,7 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream)
 {
     cudaError_t e;
     if (a.bf16)
-        e = a.D == 64 ? forward<__nv_bfloat16, 64>(a, stream) : forward<__nv_bfloat16, 128>(a, stream);
+        e = launch_attention_tc(a, stream);
     else
         e = a.D == 64 ? forward<float, 64>(a, stream) : forward<float, 128>(a, stream);
     return e;

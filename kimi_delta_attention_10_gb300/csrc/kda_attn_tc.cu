@@ -1,0 +1,430 @@
+// Attention for several tokens a sequence, BF16 on the tensor cores (tcgen05): the forward
+// over packed or paged keys.
+//
+// A CTA has two tiles of 128 rows (tokens times the heads of a group) that share the
+// stream of its key tiles.  Per tile of 128 keys and each of the two
+//     S[128, 128]  = Q[128, D] K[128, D]^T      both operands in shared memory
+//     O[128, D]   += P[128, 128] V[128, D]      P in tensor memory, where S was
+// so that one tile's softmax runs while the tensor core works for the other.  Warp roles:
+//   softmax   four warps a tile, one row a thread: no reduction crosses a thread.  The
+//             reference maximum m moves only when it would grow by more than 2^8 (exact
+//             either way), and then the thread's warp rescales O in tensor memory; the weights
+//             e^(s - m) are rounded to BF16 (2^-8 each; their sum adds them up unrounded);
+//   producer  one warp: Q once, then K and V tiles through a ring of slots by TMA, a box of
+//             64 channels, or of a page's tokens of them, at a time;
+//   MMA       one thread.
+// S of the next key tile is issued behind the product with V that reads P in its place.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "kda_attn_tc.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr float kGrowth = 8.f;                 // log2 of the growth that moves the reference
+
+template <int D> struct Cfg {
+    static constexpr int HALVES = D / 64;
+    static constexpr uint32_t QTILE = kTcRows * D * 2, SLOT = kTcKeys * D * 2;
+    static constexpr int NS = D == 128 ? 5 : 8;                // ring slots: 160, 128 KB
+    static constexpr uint32_t OFF_KV = 2 * QTILE, OFF_BAR = OFF_KV + NS * SLOT, SMEM = OFF_BAR + 512 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
+    static constexpr int NT = 320, WARP_LOAD = 8, WARP_MMA = 9;
+    static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
+};
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+struct Bars {
+    uint64_t full[8], empty[8];        // ring slots
+    uint64_t qfull[2];
+    uint64_t sfull[2];                 // S in tensor memory
+    uint64_t pfull[2];                 // P in its place
+    uint64_t ofull[2];                 // product with V done
+    uint64_t drain;
+    uint32_t tmem;
+    int32_t abort;
+    int32_t found;
+    AttnTile tile;
+};
+
+// Bytes that a tile's thread stores of its row of O, scaled.
+template <int D>
+__device__ __forceinline__ void store_row(uint32_t o_tmem, float inv, bool live, __nv_bfloat16* out, float* piece)
+{
+#pragma unroll
+    for (int c = 0; c < D; c += 32) {
+        float x[32];
+        __syncwarp();
+        tmem_ld32(o_tmem + c, x);
+        if (!live) {
+        } else if (piece != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4*>(piece + c + i) =
+                    make_float4(x[i] * inv, x[i + 1] * inv, x[i + 2] * inv, x[i + 3] * inv);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4*>(out + c + i) = make_uint4(
+                    pack_bf16(x[i] * inv, x[i + 1] * inv), pack_bf16(x[i + 2] * inv, x[i + 3] * inv),
+                    pack_bf16(x[i + 4] * inv, x[i + 5] * inv), pack_bf16(x[i + 6] * inv, x[i + 7] * inv));
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::NT, 1)
+attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
+{
+    using C = Cfg<D>;
+    constexpr int HALVES = C::HALVES, NS = C::NS;
+    extern __shared__ unsigned char raw[];
+    unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    Bars& bar = *reinterpret_cast<Bars*>(sm + C::OFF_BAR);
+    static_assert(sizeof(Bars) <= 512, "barriers");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.qfull[i], 1);
+            mbar_init(&bar.sfull[i], 1);
+            mbar_init(&bar.pfull[i], 4);
+            mbar_init(&bar.ofull[i], 1);
+        }
+        mbar_init(&bar.drain, 1);
+        bar.abort = 0;
+        fence_mbar_init();
+    }
+    wait_for_previous();
+    const int32_t piece = blockIdx.x % a.splits, unit = blockIdx.x / a.splits % sh.units,
+                  item = blockIdx.x / a.splits / sh.units;
+    if (warp == 0) {
+        AttnTile t;
+        const bool found = attn_find(a, item, 2 * sh.tokens, kTcKeyShift, t);
+        if (lane == 0) {
+            bar.tile = t;
+            bar.found = found;
+            if (blockIdx.x == 0 && a.pieces > 1) *static_cast<int32_t*>(a.workspace) = found ? a.cu[a.N] : 0;
+        }
+    } else if (warp == C::WARP_MMA) {
+        tmem_alloc(&bar.tmem, C::TM_COLS);
+        tmem_relinquish();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = bar.tmem;
+    BoundedWait wait(&bar.abort, a.status);
+
+    if (bar.found) {
+        const AttnTile t = bar.tile;
+        const int32_t hk = unit / sh.parts, part = unit - hk * sh.parts, G = a.Hq / a.Hk;
+        const int32_t head0 = hk * G + part * sh.heads;
+        // of each of the two tiles of rows: tokens, keys that its last token sees, key tiles
+        int32_t tokens[2], keys[2], n[2];
+        tokens[0] = min(t.tokens, sh.tokens);
+        tokens[1] = t.tokens - tokens[0];
+        const int32_t all = attn_keys(a, t), tiles = (int32_t)(((int64_t)all + kTcKeys - 1) >> kTcKeyShift);
+        const int32_t j0 = (int32_t)((int64_t)tiles * piece / a.splits),
+                      j1 = (int32_t)((int64_t)tiles * (piece + 1) / a.splits);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            keys[m] = tokens[m] == 0 ? 0
+                      : a.causal     ? max(0, t.pos0 + m * sh.tokens + tokens[m])
+                                     : t.kv_len;
+            n[m] = max(0, min(j1, (int32_t)(((int64_t)keys[m] + kTcKeys - 1) >> kTcKeyShift)) - j0);
+        }
+        const int32_t steps = max(n[0], n[1]);
+
+        if (warp == C::WARP_LOAD) {
+            // -------------------------------------------------------- producer
+            const uint32_t qbytes = (uint32_t)sh.tokens * sh.heads * 128 * HALVES;
+            auto load_q = [&](int m) {
+                if (n[m] == 0) return;
+                if (lane == 0) mbar_arrive_expect_tx(&bar.qfull[m], qbytes);
+                __syncwarp();
+                if (lane < HALVES)
+                    tma_load_3d(sm + m * C::QTILE + lane * (kTcRows * 128), &maps.q, 64 * lane, head0,
+                                t.row0 + m * sh.tokens, &bar.qfull[m]);
+            };
+            // a box: rows of a page, or a whole tile; the lane's part of a tile
+            const int shift = a.table == nullptr || a.page_shift > kTcKeyShift ? kTcKeyShift : a.page_shift;
+            const int half = lane % HALVES, token = lane / HALVES << shift;
+            const bool mine = lane / HALVES < kTcKeys >> shift;
+            int32_t row = 0;
+            auto find_row = [&](int32_t j) {
+                const int32_t at = (j << kTcKeyShift) + token;
+                if (a.table != nullptr && mine && at < all) row = (int32_t)attn_page_row(a, t.n, hk, at);
+            };
+            if (steps > 0) find_row(j0);
+            load_q(0);
+            uint32_t c = 0;
+            for (int32_t i = 0; i < steps; ++i) {
+                const int32_t j = j0 + i, left = all - (j << kTcKeyShift);
+                const int32_t boxes = (min(left, kTcKeys) + (1 << shift) - 1) >> shift;
+                const int32_t here = row;
+                if (i + 1 < steps) find_row(j + 1);
+                for (int kv = 0; kv < 2; ++kv, ++c) {
+                    const uint32_t slot = c % NS;
+                    wait(&bar.empty[slot], ((c / NS) & 1) ^ 1);
+                    wait.dead = __any_sync(0xffffffffu, wait.dead);
+                    if (wait.dead) break;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&bar.full[slot], (uint32_t)(boxes * HALVES) << (shift + 7));
+                    __syncwarp();
+                    if (lane < boxes * HALVES) {
+                        unsigned char* dst = sm + C::OFF_KV + slot * C::SLOT + half * (kTcKeys * 128) + token * 128;
+                        const void* map = kv ? &maps.v : &maps.k;
+                        if (a.table != nullptr)
+                            tma_load_2d(smem_u32(dst), map, 64 * half, here, &bar.full[slot]);
+                        else
+                            tma_load_3d(dst, map, 64 * half, hk, t.seq0 + (j << kTcKeyShift), &bar.full[slot]);
+                    }
+                    if (i == 0 && kv == 0) load_q(1);
+                }
+                if (wait.dead) break;
+            }
+            // every copy has landed before the CTA ends
+            if (lane == 0) {
+                for (int m = 0; m < 2; ++m)
+                    if (n[m] > 0 && (m == 0 || c > 0)) mbar_wait(&bar.qfull[m], 0);
+                for (uint32_t k = c > (uint32_t)NS ? c - NS : 0; k < c; ++k)
+                    mbar_wait(&bar.full[k % NS], (k / NS) & 1);
+            }
+        } else if (warp == C::WARP_MMA) {
+            // -------------------------------------------------------- MMA
+            if (lane == 0) {
+                constexpr uint32_t id_s = idesc(kFmtBF16, kTcRows, kTcKeys);
+                constexpr uint32_t id_o = idesc(kFmtBF16, kTcRows, D, false, true);
+                const uint64_t dQ = desc_kmajor(smem_u32(sm), kTcRows, 0);
+                const uint64_t dK = desc_kmajor(smem_u32(sm + C::OFF_KV), kTcKeys, 0);
+                const uint64_t dV = D == 128 ? desc_mnmajor128(smem_u32(sm + C::OFF_KV), kTcKeys * 128, 0)
+                                             : desc_mnmajor64(smem_u32(sm + C::OFF_KV), 0);
+                auto full = [&](uint32_t c) { wait(&bar.full[c % NS], (c / NS) & 1); };
+                auto scores = [&](int m, int32_t i) {
+                    if (wait.dead) return;
+                    fence_after_sync();
+                    const uint32_t at = (2 * i) % NS * C::SLOT;
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s)
+                        mma_bf16(tmem + C::TM_S + m * kTcKeys,
+                                 desc_advance(dQ, m * C::QTILE + kmajor_off(kTcRows, s)),
+                                 desc_advance(dK, at + kmajor_off(kTcKeys, s)), id_s, s > 0);
+                    commit(&bar.sfull[m]);
+                };
+                auto product = [&](int m, int32_t i) {
+                    if (wait.dead) return;
+                    fence_after_sync();
+                    const uint32_t at = (2 * i + 1) % NS * C::SLOT;
+                    const int32_t left = keys[m] - ((j0 + i) << kTcKeyShift);
+                    auto step = [&](int s) {
+                        mma_bf16_ta(tmem + C::TM_O + m * D, tmem + C::TM_S + m * kTcKeys + 8 * s,
+                                    desc_advance(dV, at + mnmajor_off(s)), id_o, i > 0 || s > 0);
+                    };
+                    if (left >= kTcKeys) {
+#pragma unroll
+                        for (int s = 0; s < kTcKeys / 16; ++s) step(s);
+                    } else {
+                        for (int s = 0; 16 * s < left; ++s) step(s);
+                    }
+                    commit(&bar.ofull[m]);
+                };
+                for (int32_t i = -1; i < steps; ++i) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        if (i >= 0 && i < n[m]) {
+                            full(2 * i + 1);
+                            wait(&bar.pfull[m], i & 1);
+                            product(m, i);
+                        }
+                        if (m == 1 && i >= 0 && !wait.dead) commit(&bar.empty[(2 * i + 1) % NS]);
+                        if (i + 1 < n[m]) {
+                            if (i < 0) wait(&bar.qfull[m], 0);
+                            full(2 * i + 2);
+                            scores(m, i + 1);
+                        }
+                        if (m == 1 && i + 1 < steps && !wait.dead) commit(&bar.empty[(2 * i + 2) % NS]);
+                    }
+                }
+                commit(&bar.drain);                    // no MMA outlives the loop
+                mbar_wait(&bar.drain, 0);
+            }
+        } else {
+            // -------------------------------------------------------- softmax
+            const int m = warp >> 2, quad = warp & 3, r = tid & 127;
+            const uint32_t lane0 = tmem_addr(tmem, 32 * quad, 0);
+            const uint32_t s_tm = lane0 + C::TM_S + m * kTcKeys, o_tm = lane0 + C::TM_O + m * D;
+            const int32_t i_tok = r / sh.heads, g = r - i_tok * sh.heads;
+            const int32_t token = m * sh.tokens + i_tok;          // of the CTA's tokens
+            const int32_t limit = a.causal ? t.pos0 + token + 1 : t.kv_len;
+            const int32_t least = a.causal ? t.pos0 + m * sh.tokens + 1 : t.kv_len;   // any row's
+            // maxima are taken of the products themselves, which a positive factor keeps in order
+            const bool ordered = a.scale > 0.f;
+            const float c = ordered ? a.scale * kAttnLog2e : 1.f;
+            float ref = -CUDART_INF_F, sum = 0.f;
+            const int32_t mine = n[m];
+            for (int32_t i = 0; i < mine; ++i) {
+                const int32_t key0 = (j0 + i) << kTcKeyShift;
+                wait(&bar.sfull[m], i & 1);
+                __syncwarp();
+                fence_after_sync();
+                float s[kTcKeys];
+#pragma unroll
+                for (int k = 0; k < kTcKeys; k += 32) tmem_ld32_start(s_tm + k, s + k);
+                tmem_ld_wait(s);
+                if (!ordered) {
+#pragma unroll
+                    for (int k = 0; k < kTcKeys; ++k) s[k] *= a.scale * kAttnLog2e;
+                }
+                if (key0 + kTcKeys > least) {
+#pragma unroll
+                    for (int k = 0; k < kTcKeys; ++k) s[k] = key0 + k < limit ? s[k] : -CUDART_INF_F;
+                }
+                float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int k = 4; k < kTcKeys; k += 4) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], s[k + x]);
+                }
+                const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+                const bool grown = most > ref + kGrowth;
+                if (__any_sync(0xffffffffu, grown)) {
+                    const float keep = grown ? exp2f(ref - most) : 1.f;
+                    if (grown) ref = most;
+                    sum *= keep;
+                    if (i > 0) {
+                        wait(&bar.ofull[m], (i - 1) & 1);
+                        __syncwarp();
+                        fence_after_sync();
+#pragma unroll
+                        for (int k = 0; k < D; k += 32) {
+                            float x[32];
+                            tmem_ld32(o_tm + k, x);
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) x[y] *= keep;
+                            tmem_st32(o_tm + k, reinterpret_cast<const uint32_t*>(x));
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                // all scores so far -infinity: nothing to subtract
+                const float base = ref == -CUDART_INF_F ? 0.f : -ref;
+                float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int at = 64 * half + 2 * k;
+                        const float2 x = fma2(make_float2(s[at], s[at + 1]), both(c), both(base));
+                        const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                        add[k & 1] = fma2(e, both(1.f), add[k & 1]);
+                        p[k] = pack_bf16(e.x, e.y);
+                    }
+                    tmem_st32(s_tm + 32 * half, p);
+                }
+                sum += add[0].x + add[0].y + add[1].x + add[1].y;
+                if (key0 + kTcKeys > all) {
+                    // value rows past the last key, as far as the product reads (16 at a time)
+                    const uint32_t at = 2 * i + 1;
+                    wait(&bar.full[at % NS], (at / NS) & 1);
+                    const int first = all - key0, rows = ((first + 15) & ~15) - first;
+                    unsigned char* v = sm + C::OFF_KV + at % NS * C::SLOT;
+                    for (int e = r; e < rows * 8 * HALVES; e += 128)
+                        *reinterpret_cast<uint4*>(v + (e >> 3) % HALVES * (kTcKeys * 128) +
+                                                  (first + (e >> 3) / HALVES) * 128 + (e & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                tmem_st_wait();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.pfull[m]);
+            }
+            if (mine > 0) {
+                wait(&bar.ofull[m], (mine - 1) & 1);
+                __syncwarp();
+                fence_after_sync();
+            }
+            const bool live = i_tok < sh.tokens && i_tok < tokens[m] && g < min(sh.heads, G - part * sh.heads);
+            const int64_t row = (int64_t)(t.row0 + token) * a.Hq + head0 + g;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            char* ws = static_cast<char*>(a.workspace);
+            float* py = a.pieces > 1 ? reinterpret_cast<float*>(ws + attn_pieces_o(a, piece)) + row * D : nullptr;
+            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.out) + row * D;
+            if (live) {
+                const float lse = sum == 0.f ? -CUDART_INF_F : (ref + log2f(sum)) * kAttnLn2;
+                if (a.pieces > 1) reinterpret_cast<float*>(ws + attn_pieces_lse(a, piece))[row] = lse;
+                else if (a.lse != nullptr) a.lse[row] = lse;
+            }
+            // a sum of zero: no weight, and O may hold 0 times an infinity
+            if (mine > 0 && __any_sync(0xffffffffu, sum != 0.f)) {
+                store_row<D>(o_tm, inv, live && sum != 0.f, y, py);
+            }
+            if (live && sum == 0.f) {
+                if (py != nullptr) {
+                    for (int k = 0; k < D; k += 4) *reinterpret_cast<float4*>(py + k) = make_float4(0.f, 0.f, 0.f, 0.f);
+                } else {
+                    for (int k = 0; k < D; k += 8) *reinterpret_cast<uint4*>(y + k) = make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == C::WARP_MMA) {
+        fence_after_sync();
+        tmem_dealloc(tmem, C::TM_COLS);
+    }
+}
+
+template <int D> cudaError_t forward(const AttnArgs& a, cudaStream_t stream)
+{
+    using C = Cfg<D>;
+    const AttnShape sh = attn_shape(kTcRows, a.Hq, a.Hk);
+    const int64_t ctas = attn_tiles(a.N, a.T, 2 * sh.tokens) * sh.units * a.splits;
+    if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+    Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    cudaError_t e = encode_heads(&maps.q, a.q, a.T, a.Hq, D, a.q_stride, sh.heads, sh.tokens);
+    if (a.table == nullptr) {
+        if (e == cudaSuccess) e = encode_heads(&maps.k, a.k, a.T, a.Hk, D, a.k_stride, 1, kTcKeys);
+        if (e == cudaSuccess) e = encode_heads(&maps.v, a.v, a.T, a.Hk, D, a.v_stride, 1, kTcKeys);
+    } else {
+        const int page = 1 << a.page_shift, box = page < kTcKeys ? page : kTcKeys;
+        const int64_t rows = (int64_t)a.num_pages * a.Hk * page;
+        // an empty cache has no page to read: the maps only have to be valid
+        const int64_t any = (int64_t)a.T;
+        if (e == cudaSuccess) e = encode_rows(&maps.k, rows ? a.k : a.q, true, rows ? rows : any, D, 64, box, true);
+        if (e == cudaSuccess) e = encode_rows(&maps.v, rows ? a.v : a.q, true, rows ? rows : any, D, 64, box, true);
+    }
+    if (e != cudaSuccess) return e;
+    auto kern = attn_fwd_tc_kernel<D>;
+    static std::atomic<uint64_t> set{0};
+    e = allow_smem(kern, C::SMEM, &set);
+    if (e != cudaSuccess) return e;
+    return launch_after(kern, launch_config(ctas, C::NT, C::SMEM), stream, a, sh, maps);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_tc(const AttnArgs& a, cudaStream_t stream)
+{
+    return a.D == 64 ? forward<64>(a, stream) : forward<128>(a, stream);
+}
+
+}  // namespace kda

@@ -1,0 +1,110 @@
+// What the tensor-core kernels of attention for several tokens share: products with an
+// operand in tensor memory, wide tensor-memory loads and stores, tiles of rows and keys by TMA.
+#pragma once
+
+#include <cuda.h>
+#include <math_constants.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "kda_attn.cuh"
+#include "kda_paged_tma.cuh"
+
+namespace kda {
+
+constexpr float kAttnLog2e = 1.4426950408889634f, kAttnLn2 = 0.6931471805599453f;
+constexpr int kTcRows = 128;                   // rows of an MMA
+constexpr int kTcKeys = 128, kTcKeyShift = 7;  // keys of a tile
+
+// D[128, N] (+)= A[128, 16] B[N, 16]^T with A in tensor memory: row r in lane r, two
+// BF16 values of K a column.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id,
+                                            uint32_t acc)
+{
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(id), "r"(acc));
+}
+
+// As tc::tmem_ld32, without the wait (tmem_ld_wait).
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, float* r)
+{
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]),
+          "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]),
+          "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+          "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]),
+          "=r"(u[31])
+        : "r"(taddr)
+        : "memory");
+}
+// The registers of the loads before it may be read after this; they pass through it, so that
+// no use of them is moved ahead.
+template <int N> __device__ __forceinline__ void tmem_ld_wait(float (&r)[N])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* u)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n" ::"r"(u[0]),
+        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]),
+        "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]),
+        "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]),
+        "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]),
+        "r"(u[30]), "r"(u[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- host
+// [T, H, D] of 16-bit values, tokens `stride` elements apart, read as boxes of 64 channels of
+// `heads` heads of `tokens` tokens in 128-byte swizzled rows (token, head); rows past the end
+// read as zeros.
+inline cudaError_t encode_heads(CUtensorMap* m, const void* base, int64_t T, int H, int D, int64_t stride, int heads,
+                                int tokens)
+{
+    const EncodeTiledFn fn = encode_tiled();
+    if (fn == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Rows of a call cut into tiles of at most `rows`.
+inline AttnShape attn_shape(int32_t rows, int32_t Hq, int32_t Hk)
+{
+    AttnShape s;
+    const int32_t G = Hq / Hk;
+    s.heads = G < rows ? G : rows;
+    s.parts = (G + s.heads - 1) / s.heads;
+    s.tokens = rows / s.heads;
+    s.units = Hk * s.parts;
+    return s;
+}
+// Tiles of a call: every one has a token, and all but a sequence's last are full.
+inline int64_t attn_tiles(int32_t N, int32_t T, int32_t tokens)
+{
+    const int64_t n = (int64_t)T / tokens + N;
+    return n < T ? n : T;
+}
+
+}  // namespace kda
