@@ -62,12 +62,13 @@ __host__ __device__ inline int64_t attn_pieces_o(const AttnArgs& a, int32_t piec
 // How a call's rows are cut into tiles.
 struct AttnShape {
     int32_t tokens;          // of a CTA's tile
-    int32_t heads;           // query heads of a tile (of the last part of a group: fewer)
+    int32_t heads;           // query heads of a tile
     int32_t parts;           // tiles of heads per group
     int32_t units;           // Hk * parts
 };
 
 cudaError_t launch_attention_tc(const AttnArgs& a, cudaStream_t stream);      // BF16
+cudaError_t launch_attention_bwd_tc(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attention_bwd(const AttnArgs& a, cudaStream_t stream);
 int64_t attention_bwd_workspace_bytes(int32_t N, int32_t T, int32_t Hq, int32_t Hk, int32_t D);

@@ -1,0 +1,574 @@
+// Backward of attention for several tokens, BF16 on the tensor cores (tcgen05), in two
+// kernels that each form the scores again:
+//
+//   keys     a CTA has 128 keys of a sequence and one key-value head, and walks over the rows
+//            (tokens times the group's heads) that see them, 128 at a time:
+//                S^T = K Q^T, dP^T = V dO^T          both operands in shared memory
+//                dV += P^T dO, dK += dS^T Q          P^T and dS^T in tensor memory
+//   queries  a CTA has 128 rows and walks over the key tiles they see:
+//                S = Q K^T, dP = dO V^T, dQ += dS K
+//
+// so that every gradient adds up in one CTA's tensor memory, over all heads of the group, in
+// an order that the sizes set: no atomics, the same bits every time.  The price is seven
+// products a tile of scores instead of five.  Transposing the scores in the first kernel lets
+// P and dS stay in tensor memory as operands; the other operand of every product is read from
+// shared memory as TMA left it, as rows or as columns.
+//
+// Eight warps form P and dS, a thread half a row of a tile: P while the tensor core works on
+// the products with the tile before, dS = P (dP - delta) while it forms P^T dO and the next
+// scores.  P and dS are rounded to BF16 (2^-8) as operands.  A warp reads the rows' lse and delta.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "kda_attn_tc.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+template <int D> struct Cfg {
+    static constexpr int HALVES = D / 64;
+    static constexpr uint32_t TILE = 128 * D * 2;              // 128 rows of keys, values, queries or dO
+    static constexpr uint32_t OFF_RING = 2 * TILE;             // two stages of two tiles
+    static constexpr uint32_t OFF_STAT = OFF_RING + 4 * TILE, OFF_BAR = OFF_STAT + 2 * 1024,
+                              SMEM = OFF_BAR + 512 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
+    static constexpr int NT = 352, WARP_LOAD = 8, WARP_MMA = 9, WARP_STAT = 10;
+};
+
+struct KvMaps {
+    CUtensorMap q, dout, k, v;
+};
+
+struct Bars {
+    uint64_t afull[2];                 // the CTA's own two tiles
+    uint64_t full[2][2], empty[2][2];  // the walked tiles: [first or second][stage]
+    uint64_t sfull[2], pfull;          // S (the second kernel: of even and odd tiles), P in its place
+    uint64_t dpfull, dsfull;           // dP, dS in its place
+    uint64_t statfull[2], statempty[2];
+    uint64_t done;
+    uint32_t tmem;
+    int32_t abort;
+    int32_t found;
+    AttnTile tile;
+};
+
+__device__ __forceinline__ void start(Bars& bar, const AttnArgs& a, int32_t item, int32_t tokens)
+{
+    const int tid = threadIdx.x, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.afull[i], 1);
+            mbar_init(&bar.sfull[i], 1);
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(&bar.full[x][i], 1);
+                mbar_init(&bar.empty[x][i], 1);
+            }
+            mbar_init(&bar.statfull[i], 1);
+            mbar_init(&bar.statempty[i], 8);
+        }
+        mbar_init(&bar.pfull, 8);
+        mbar_init(&bar.dpfull, 1);
+        mbar_init(&bar.dsfull, 8);
+        mbar_init(&bar.done, 1);
+        bar.abort = 0;
+        fence_mbar_init();
+    }
+    wait_for_previous();
+    if (warp == 0) {
+        AttnTile t;
+        const bool found = attn_find(a, item, tokens, kTcKeyShift, t);
+        if (tid == 0) {
+            bar.tile = t;
+            bar.found = found;
+        }
+    } else if (warp == 9) {
+        tmem_alloc(&bar.tmem, 512);
+        tmem_relinquish();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+}
+
+// Zeroes rows first .. last - 1 of a tile, by `threads` threads, for the products' reads.
+template <int D>
+__device__ __forceinline__ void zero_rows(unsigned char* tile, int first, int last, int thread, int threads)
+{
+    constexpr int HALVES = D / 64;
+    for (int e = thread; e < (last - first) * 8 * HALVES; e += threads)
+        *reinterpret_cast<uint4*>(tile + (e >> 3) % HALVES * (128 * 128) + (first + (e >> 3) / HALVES) * 128 +
+                                  (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// 64 values of a thread's lane, from column `t` on, as BF16 pairs in 32 columns there.
+__device__ __forceinline__ void store_pairs(uint32_t t, const float (&x)[64])
+{
+    uint32_t u[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) u[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+    tmem_st32(t, u);
+    tmem_st_wait();
+}
+
+// A lane's D values, scaled, to a row of the output.
+template <int D> __device__ __forceinline__ void store_row(uint32_t t, float scale, bool live, __nv_bfloat16* y)
+{
+#pragma unroll
+    for (int c = 0; c < D; c += 32) {
+        float x[32];
+        __syncwarp();
+        tmem_ld32(t + c, x);
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4*>(y + c + i) = make_uint4(
+                    pack_bf16(x[i] * scale, x[i + 1] * scale), pack_bf16(x[i + 2] * scale, x[i + 3] * scale),
+                    pack_bf16(x[i + 4] * scale, x[i + 5] * scale), pack_bf16(x[i + 6] * scale, x[i + 7] * scale));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- dk, dv
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::NT, 1)
+attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps maps)
+{
+    using C = Cfg<D>;
+    constexpr int HALVES = C::HALVES;
+    constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + D;
+    extern __shared__ unsigned char raw[];
+    unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    Bars& bar = *reinterpret_cast<Bars*>(sm + C::OFF_BAR);
+    static_assert(sizeof(Bars) <= 512, "barriers");
+    float* stats = reinterpret_cast<float*>(sm + C::OFF_STAT);     // [stage][-lse log2 e, -delta][128]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t hk = blockIdx.x % a.Hk, item = blockIdx.x / a.Hk, rows = sh.tokens * sh.heads;
+    // Rows of a tile that no copy fills are zeros for good.
+    if (rows < 128) {
+        for (int x = 0; x < 4; ++x) zero_rows<D>(sm + C::OFF_RING + x * C::TILE, rows, 128, tid, C::NT);
+        fence_async_smem();
+    }
+    start(bar, a, item, kTcKeys);
+    const uint32_t tmem = bar.tmem;
+    BoundedWait wait(&bar.abort, a.status);
+    if (bar.found) {
+        const AttnTile t = bar.tile;
+        // the tile found has t.index tiles of queries before it; the one with as many behind it
+        const int32_t nt = (t.seq_tokens + kTcKeys - 1) >> kTcKeyShift, key0 = (nt - 1 - t.index) << kTcKeyShift;
+        const int32_t left = t.seq_tokens - key0;                  // tokens from the first key on
+        const int32_t per = (left + sh.tokens - 1) / sh.tokens, n = per * sh.parts;
+        const int32_t last = left - (per - 1) * sh.tokens;         // tokens of a part's last tile
+        auto ring = [&](int x, int32_t i) { return sm + C::OFF_RING + ((i & 1) * 2 + x) * C::TILE; };
+
+        if (warp == C::WARP_LOAD) {
+            // -------------------------------------------------------- producer
+            if (lane == 0) {
+                for (int x = 0; x < 2; ++x) {
+                    mbar_arrive_expect_tx(&bar.afull[x], C::TILE);
+                    for (int h = 0; h < HALVES; ++h)
+                        tma_load_3d(sm + x * C::TILE + h * (128 * 128), x ? &maps.v : &maps.k, 64 * h, hk,
+                                    t.seq0 + key0, &bar.afull[x]);
+                }
+                int32_t i = 0, part = 0, at = 0;
+                for (; i < n; ++i) {
+                    for (int x = 0; x < 2; ++x) {
+                        wait(&bar.empty[x][i & 1], ((i >> 1) & 1) ^ 1);
+                        if (wait.dead) break;
+                        mbar_arrive_expect_tx(&bar.full[x][i & 1], (uint32_t)rows * 128 * HALVES);
+                        for (int h = 0; h < HALVES; ++h)
+                            tma_load_3d(ring(x, i) + h * (128 * 128), x ? &maps.dout : &maps.q, 64 * h,
+                                        (hk * sh.parts + part) * sh.heads, t.seq0 + key0 + at * sh.tokens,
+                                        &bar.full[x][i & 1]);
+                    }
+                    if (wait.dead) break;
+                    if (++at == per) {
+                        at = 0;
+                        ++part;
+                    }
+                }
+                // every copy has landed before the CTA ends
+                mbar_wait(&bar.afull[0], 0);
+                mbar_wait(&bar.afull[1], 0);
+                for (int32_t k = max(0, i - 2); k < i; ++k)
+                    for (int x = 0; x < 2; ++x) mbar_wait(&bar.full[x][k & 1], (k >> 1) & 1);
+            }
+        } else if (warp == C::WARP_MMA) {
+            // -------------------------------------------------------- MMA
+            if (lane == 0) {
+                constexpr uint32_t id_s = idesc(kFmtBF16, 128, 128), id_d = idesc(kFmtBF16, 128, D, false, true);
+                const uint32_t base = smem_u32(sm);
+                const uint64_t dA = desc_kmajor(base, 128, 0), dB = desc_kmajor(base + C::OFF_RING, 128, 0);
+                const uint64_t dN = D == 128 ? desc_mnmajor128(base + C::OFF_RING, 128 * 128, 0)
+                                             : desc_mnmajor64(base + C::OFF_RING, 0);
+                // tile x of the CTA's own times tile x of the ring
+                auto scores = [&](int x, int32_t i) {
+                    if (wait.dead) return;
+                    fence_after_sync();
+                    const uint32_t at = ((i & 1) * 2 + x) * C::TILE;
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s)
+                        mma_bf16(tmem + (x ? TM_DP : TM_S), desc_advance(dA, x * C::TILE + kmajor_off(128, s)),
+                                 desc_advance(dB, at + kmajor_off(128, s)), id_s, s > 0);
+                    commit(x ? &bar.dpfull : &bar.sfull[0]);
+                };
+                // the weights in tensor memory (rows 0 .. 63 where the first half of the scores
+                // was, the others where the second was) times a tile of the ring
+                auto gradient = [&](int x, int32_t i) {
+                    if (wait.dead) return;
+                    fence_after_sync();
+                    const uint32_t at = ((i & 1) * 2 + (x ^ 1)) * C::TILE;
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        mma_bf16_ta(tmem + (x ? TM_DK : TM_DV),
+                                    tmem + (x ? TM_DP : TM_S) + 8 * (s & 3) + 64 * (s >> 2),
+                                    desc_advance(dN, at + mnmajor_off(s)), id_d, i > 0 || s > 0);
+                    commit(&bar.empty[x ^ 1][i & 1]);
+                };
+                int32_t at = 0;
+                auto first = [&](int32_t i) {                      // S of tile i
+                    wait(&bar.full[0][i & 1], (i >> 1) & 1);
+                    // a part's last tile: once the rows past the end are zeros
+                    if (at + 1 == per && last < sh.tokens) wait(&bar.statfull[i & 1], (i >> 1) & 1);
+                    scores(0, i);
+                    if (++at == per) at = 0;
+                };
+                wait(&bar.afull[0], 0);
+                first(0);
+                wait(&bar.afull[1], 0);
+                for (int32_t i = 0; i < n; ++i) {
+                    wait(&bar.full[1][i & 1], (i >> 1) & 1);
+                    scores(1, i);
+                    wait(&bar.pfull, i & 1);
+                    gradient(0, i);
+                    if (i + 1 < n) first(i + 1);
+                    wait(&bar.dsfull, i & 1);
+                    gradient(1, i);
+                }
+                commit(&bar.done);                     // no MMA outlives the loop
+                mbar_wait(&bar.done, 0);
+            }
+        } else if (warp == C::WARP_STAT) {
+            // -------------------------------------------------------- lse and delta of the rows
+            int32_t part = 0, at = 0;
+            for (int32_t i = 0; i < n; ++i) {
+                const int32_t tokens = at + 1 == per ? last : sh.tokens, b = i & 1;
+                const int64_t row0 = (int64_t)(t.seq0 + key0 + at * sh.tokens) * a.Hq +
+                                     (hk * sh.parts + part) * sh.heads;
+                float l[4], d[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int32_t r = lane + 32 * k, tok = r / sh.heads, g = r - tok * sh.heads;
+                    const bool live = tok < tokens;
+                    const int64_t x = row0 + (int64_t)tok * a.Hq + g;
+                    const float lse = live ? a.lse_in[x] : CUDART_INF_F;
+                    // no weight: none to any key
+                    l[k] = lse == -CUDART_INF_F ? -CUDART_INF_F : -lse * kAttnLog2e;
+                    d[k] = live ? -a.delta[x] : 0.f;
+                }
+                wait(&bar.statempty[b], ((i >> 1) & 1) ^ 1);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    stats[b * 256 + lane + 32 * k] = l[k];
+                    stats[b * 256 + 128 + lane + 32 * k] = d[k];
+                }
+                if (tokens < sh.tokens) {
+                    // rows of the next sequence: zeros, since the gradients add over all rows
+                    for (int x = 0; x < 2; ++x) {
+                        wait(&bar.full[x][b], (i >> 1) & 1);
+                        zero_rows<D>(ring(x, i), tokens * sh.heads, rows, lane, 32);
+                    }
+                    fence_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.statfull[b]);
+                if (++at == per) {
+                    at = 0;
+                    ++part;
+                }
+            }
+        } else {
+            // -------------------------------------------------------- P and dS
+            const int half = warp >> 2, key = tid & 127;           // the thread's rows: 64 half ..
+            const uint32_t lane0 = tmem_addr(tmem, 32 * (warp & 3), 0);
+            const uint32_t s_tm = lane0 + TM_S + 64 * half, dp_tm = lane0 + TM_DP + 64 * half;
+            const float2 c = both(a.scale * kAttnLog2e);
+            int32_t at = 0;
+            for (int32_t i = 0; i < n; ++i) {
+                const int32_t b = i & 1;
+                const float4* nl = reinterpret_cast<const float4*>(stats + b * 256 + 64 * half);
+                const float4* nd = nl + 32;
+                // rows before this one are tokens before the key
+                const int32_t begin = min(128, max(0, key - at * sh.tokens)) * sh.heads - 64 * half;
+                const bool cut = at * sh.tokens < kTcKeys - 1;     // for some key
+                if (++at == per) at = 0;
+                wait(&bar.statfull[b], (i >> 1) & 1);
+                wait(&bar.sfull[0], i & 1);
+                __syncwarp();
+                fence_after_sync();
+                float p[64];
+                tmem_ld32_start(s_tm, p);
+                tmem_ld32_start(s_tm + 32, p + 32);
+                tmem_ld_wait(p);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float4 l = nl[k];
+                    const float2 x = fma2(make_float2(p[4 * k], p[4 * k + 1]), c, make_float2(l.x, l.y));
+                    const float2 y = fma2(make_float2(p[4 * k + 2], p[4 * k + 3]), c, make_float2(l.z, l.w));
+                    p[4 * k] = ex2_approx(x.x);
+                    p[4 * k + 1] = ex2_approx(x.y);
+                    p[4 * k + 2] = ex2_approx(y.x);
+                    p[4 * k + 3] = ex2_approx(y.y);
+                }
+                if (cut) {
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) p[k] = k < begin ? 0.f : p[k];
+                }
+                store_pairs(s_tm, p);
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.pfull);
+                wait(&bar.dpfull, i & 1);
+                __syncwarp();
+                fence_after_sync();
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float d[32];
+                    tmem_ld32(dp_tm + 32 * x, d);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 e = nd[8 * x + k];
+                        float* q = p + 32 * x + 4 * k;
+                        const float2 u = mul2(make_float2(q[0], q[1]),
+                                              fma2(make_float2(d[4 * k], d[4 * k + 1]), both(1.f), make_float2(e.x, e.y)));
+                        const float2 v = mul2(make_float2(q[2], q[3]),
+                                              fma2(make_float2(d[4 * k + 2], d[4 * k + 3]), both(1.f), make_float2(e.z, e.w)));
+                        q[0] = u.x; q[1] = u.y; q[2] = v.x; q[3] = v.y;
+                    }
+                }
+                if (cut) {
+                    // whatever dP is there
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) p[k] = k < begin ? 0.f : p[k];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.statempty[b]);
+                store_pairs(dp_tm, p);
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.dsfull);
+            }
+            wait(&bar.done, 0);
+            __syncwarp();
+            fence_after_sync();
+            const int64_t row = ((int64_t)(t.seq0 + key0 + key) * a.Hk + hk) * D;
+            store_row<D>(lane0 + (half ? TM_DK : TM_DV), half ? a.scale : 1.f, key < left,
+                         static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + row);
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == C::WARP_MMA) {
+        fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- dq
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::NT, 1)
+attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps maps)
+{
+    using C = Cfg<D>;
+    constexpr int HALVES = C::HALVES;
+    constexpr uint32_t TM_S = 0, TM_DP = 256, TM_DQ = 384;         // two buffers of S
+    extern __shared__ unsigned char raw[];
+    unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    Bars& bar = *reinterpret_cast<Bars*>(sm + C::OFF_BAR);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t unit = blockIdx.x % sh.units, item = blockIdx.x / sh.units, rows = sh.tokens * sh.heads;
+    const int32_t hk = unit / sh.parts, head0 = unit * sh.heads;
+    start(bar, a, item, sh.tokens);
+    const uint32_t tmem = bar.tmem;
+    BoundedWait wait(&bar.abort, a.status);
+    if (bar.found) {
+        const AttnTile t = bar.tile;
+        const int32_t all = attn_keys(a, t), n = (all + kTcKeys - 1) >> kTcKeyShift;
+        auto ring = [&](int x, int32_t i) { return sm + C::OFF_RING + ((i & 1) * 2 + x) * C::TILE; };
+
+        if (warp == C::WARP_LOAD) {
+            if (lane == 0) {
+                for (int x = 0; x < 2; ++x) {
+                    mbar_arrive_expect_tx(&bar.afull[x], (uint32_t)rows * 128 * HALVES);
+                    for (int h = 0; h < HALVES; ++h)
+                        tma_load_3d(sm + x * C::TILE + h * (128 * 128), x ? &maps.dout : &maps.q, 64 * h, head0,
+                                    t.row0, &bar.afull[x]);
+                }
+                int32_t i = 0;
+                for (; i < n; ++i) {
+                    for (int x = 0; x < 2; ++x) {
+                        wait(&bar.empty[x][i & 1], ((i >> 1) & 1) ^ 1);
+                        if (wait.dead) break;
+                        mbar_arrive_expect_tx(&bar.full[x][i & 1], C::TILE);
+                        for (int h = 0; h < HALVES; ++h)
+                            tma_load_3d(ring(x, i) + h * (128 * 128), x ? &maps.v : &maps.k, 64 * h, hk,
+                                        t.seq0 + (i << kTcKeyShift), &bar.full[x][i & 1]);
+                    }
+                    if (wait.dead) break;
+                }
+                mbar_wait(&bar.afull[0], 0);
+                mbar_wait(&bar.afull[1], 0);
+                for (int32_t k = max(0, i - 2); k < i; ++k)
+                    for (int x = 0; x < 2; ++x) mbar_wait(&bar.full[x][k & 1], (k >> 1) & 1);
+            }
+        } else if (warp == C::WARP_MMA) {
+            if (lane == 0) {
+                constexpr uint32_t id_s = idesc(kFmtBF16, 128, 128), id_d = idesc(kFmtBF16, 128, D, false, true);
+                const uint32_t base = smem_u32(sm);
+                const uint64_t dA = desc_kmajor(base, 128, 0), dB = desc_kmajor(base + C::OFF_RING, 128, 0);
+                const uint64_t dN = D == 128 ? desc_mnmajor128(base + C::OFF_RING, 128 * 128, 0)
+                                             : desc_mnmajor64(base + C::OFF_RING, 0);
+                auto scores = [&](int x, int32_t i) {
+                    wait(&bar.full[x][i & 1], (i >> 1) & 1);
+                    if (wait.dead) return;
+                    fence_after_sync();
+                    const uint32_t at = ((i & 1) * 2 + x) * C::TILE;
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s)
+                        mma_bf16(tmem + (x ? TM_DP : TM_S + (i & 1) * 128), desc_advance(dA, x * C::TILE + kmajor_off(128, s)),
+                                 desc_advance(dB, at + kmajor_off(128, s)), id_s, s > 0);
+                    if (x) commit(&bar.empty[1][i & 1]);
+                    commit(x ? &bar.dpfull : &bar.sfull[i & 1]);
+                };
+                wait(&bar.afull[0], 0);
+                scores(0, 0);
+                wait(&bar.afull[1], 0);
+                for (int32_t i = 0; i < n; ++i) {
+                    scores(1, i);
+                    if (i + 1 < n) scores(0, i + 1);
+                    wait(&bar.dsfull, i & 1);
+                    if (wait.dead) continue;
+                    fence_after_sync();
+                    const uint32_t at = (i & 1) * 2 * C::TILE;
+                    const int32_t keys = all - (i << kTcKeyShift);
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        if (16 * s < keys)
+                            mma_bf16_ta(tmem + TM_DQ, tmem + TM_DP + 8 * (s & 3) + 64 * (s >> 2),
+                                        desc_advance(dN, at + mnmajor_off(s)), id_d, i > 0 || s > 0);
+                    commit(&bar.empty[0][i & 1]);
+                }
+                commit(&bar.done);
+                mbar_wait(&bar.done, 0);
+            }
+        } else if (warp < 8) {
+            const int half = warp >> 2, r = tid & 127;             // the thread's keys: 64 half ..
+            const uint32_t lane0 = tmem_addr(tmem, 32 * (warp & 3), 0);
+            const uint32_t dp_tm = lane0 + TM_DP + 64 * half;
+            const float2 c = both(a.scale * kAttnLog2e);
+            const int32_t tok = r / sh.heads, g = r - tok * sh.heads;
+            const bool live = tok < t.tokens;
+            const int64_t row = (int64_t)(t.row0 + tok) * a.Hq + head0 + g;
+            const float lse = live ? a.lse_in[row] : CUDART_INF_F;
+            const float2 nl = both(lse == -CUDART_INF_F ? -CUDART_INF_F : -lse * kAttnLog2e);
+            const float2 nd = both(live ? -a.delta[row] : 0.f);
+            for (int32_t i = 0; i < n; ++i) {
+                // keys from this one on are tokens behind the row's
+                const int32_t end = t.pos0 + tok + 1 - (i << kTcKeyShift) - 64 * half;
+                const bool cut = ((i + 1) << kTcKeyShift) > t.pos0 + 1;
+                const uint32_t s_tm = lane0 + TM_S + (i & 1) * 128 + 64 * half;
+                wait(&bar.sfull[i & 1], (i >> 1) & 1);
+                __syncwarp();
+                fence_after_sync();
+                float p[64];
+                tmem_ld32_start(s_tm, p);
+                tmem_ld32_start(s_tm + 32, p + 32);
+                tmem_ld_wait(p);
+#pragma unroll
+                for (int k = 0; k < 64; k += 2) {
+                    const float2 x = fma2(make_float2(p[k], p[k + 1]), c, nl);
+                    p[k] = ex2_approx(x.x);
+                    p[k + 1] = ex2_approx(x.y);
+                }
+                wait(&bar.dpfull, i & 1);
+                __syncwarp();
+                fence_after_sync();
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float d[32];
+                    tmem_ld32(dp_tm + 32 * x, d);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        float* q = p + 32 * x + k;
+                        const float2 u = mul2(make_float2(q[0], q[1]), fma2(make_float2(d[k], d[k + 1]), both(1.f), nd));
+                        q[0] = u.x;
+                        q[1] = u.y;
+                    }
+                }
+                if (cut) {
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) p[k] = k < end ? p[k] : 0.f;
+                }
+                const int32_t keys = all - (i << kTcKeyShift);
+                if (keys < kTcKeys && half == 0) {
+                    // keys past the end, as far as the product reads (16 at a time); the scores
+                    // with them are done
+                    zero_rows<D>(ring(0, i), keys, (keys + 15) & ~15, r, 128);
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                store_pairs(dp_tm, p);
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.dsfull);
+            }
+            wait(&bar.done, 0);
+            __syncwarp();
+            fence_after_sync();
+            // each half of the warps stores half of the channels
+            store_row<D / 2>(lane0 + TM_DQ + D / 2 * half, a.scale, live,
+                             static_cast<__nv_bfloat16*>(a.dq) + row * D + D / 2 * half);
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == C::WARP_MMA) {
+        fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D> cudaError_t backward(const AttnArgs& a, cudaStream_t stream)
+{
+    using C = Cfg<D>;
+    const AttnShape sh = attn_shape(kTcRows, a.Hq, a.Hk);
+    KvMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    cudaError_t e = encode_heads(&maps.q, a.q, a.T, a.Hq, D, a.q_stride, sh.heads, sh.tokens);
+    if (e == cudaSuccess) e = encode_heads(&maps.dout, a.dout, a.T, a.Hq, D, (int64_t)a.Hq * D, sh.heads, sh.tokens);
+    if (e == cudaSuccess) e = encode_heads(&maps.k, a.k, a.T, a.Hk, D, a.k_stride, 1, kTcKeys);
+    if (e == cudaSuccess) e = encode_heads(&maps.v, a.v, a.T, a.Hk, D, a.v_stride, 1, kTcKeys);
+    if (e != cudaSuccess) return e;
+    const int64_t kv = attn_tiles(a.N, a.T, kTcKeys) * a.Hk, q = attn_tiles(a.N, a.T, sh.tokens) * sh.units;
+    if (kv > INT32_MAX || q > INT32_MAX) return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> set_kv{0}, set_q{0};
+    e = allow_smem(attn_bwd_kv_tc_kernel<D>, C::SMEM, &set_kv);
+    if (e == cudaSuccess) e = allow_smem(attn_bwd_q_tc_kernel<D>, C::SMEM, &set_q);
+    if (e != cudaSuccess) return e;
+    e = launch_after(attn_bwd_kv_tc_kernel<D>, launch_config(kv, C::NT, C::SMEM), stream, a, sh, maps);
+    if (e != cudaSuccess) return e;
+    return launch_after(attn_bwd_q_tc_kernel<D>, launch_config(q, C::NT, C::SMEM), stream, a, sh, maps);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_bwd_tc(const AttnArgs& a, cudaStream_t stream)
+{
+    return a.D == 64 ? backward<64>(a, stream) : backward<128>(a, stream);
+}
+
+}  // namespace kda

@@ -30,18 +30,6 @@ constexpr int kThreads = 256;
 constexpr int kKeys = 64, kKeyShift = 6;       // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ void load4(float* dst, const float* src, bool valid)
-{
-    cp_async16(dst, src, valid);
-}
-__device__ __forceinline__ void load4(float* dst, const __nv_bfloat16* src, bool valid)
-{
-    uint2 u = make_uint2(0, 0);
-    if (valid) u = *reinterpret_cast<const uint2*>(src);
-    *reinterpret_cast<float4*>(dst) =
-        make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                    __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x)
 {
@@ -52,51 +40,42 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x)
 struct RowMap {
     int32_t heads, rows;     // heads of the tile (a row's divisor), rows in use
     int32_t row0, head0;     // first packed token, first query head
-    int32_t live;            // heads of the tile that the group has
-    __device__ __forceinline__ RowMap(const AttnArgs& a, const AttnShape& sh, int32_t unit, int32_t token0,
-                                      int32_t tokens)
-    {
-        const int32_t hk = unit / sh.parts, part = unit - hk * sh.parts, G = a.Hq / a.Hk;
-        heads = sh.heads;
-        rows = tokens * sh.heads;
-        row0 = token0;
-        head0 = hk * G + part * sh.heads;
-        live = min(sh.heads, G - part * sh.heads);
-    }
+    __device__ __forceinline__ RowMap(const AttnShape& sh, int32_t unit, int32_t token0, int32_t tokens)
+        : heads(sh.heads), rows(tokens * sh.heads), row0(token0), head0(unit * sh.heads) {}
     // (token, head) of row r; false: the row is not in use
     __device__ __forceinline__ bool at(int32_t r, int32_t& token, int32_t& head) const
     {
         const int32_t i = r / heads, g = r - i * heads;
         token = row0 + i;
         head = head0 + g;
-        return r < rows && g < live;
+        return r < rows;
     }
 };
 
 // ROWS rows of D values to shared memory rows of D + 4, zeros where a row is not in use.
-template <int ROWS, int D, typename T>
-__device__ __forceinline__ void load_rows(float* dst, const T* x, int64_t stride, const RowMap& m)
+template <int ROWS, int D>
+__device__ __forceinline__ void load_rows(float* dst, const float* x, int64_t stride, const RowMap& m)
 {
     for (int e = threadIdx.x; e < ROWS * (D / 4); e += kThreads) {
         const int r = e / (D / 4), c = e % (D / 4) * 4;
         int32_t token, head;
         const bool ok = m.at(r, token, head);
-        load4(dst + r * (D + 4) + c, ok ? x + token * stride + (int64_t)head * D + c : x, ok);
+        cp_async16(dst + r * (D + 4) + c, ok ? x + token * stride + (int64_t)head * D + c : x, ok);
     }
 }
 // Keys or values `at` .. at + 63 of head hk, zeros past `end`.
-template <int D, int PITCH, typename T>
-__device__ __forceinline__ void load_keys(float* dst, const AttnArgs& a, const T* x, int64_t stride,
+template <int D, int PITCH>
+__device__ __forceinline__ void load_keys(float* dst, const AttnArgs& a, const float* x, int64_t stride,
                                           const AttnTile& t, int32_t hk, int32_t at, int32_t end)
 {
     for (int e = threadIdx.x; e < kKeys * (D / 4); e += kThreads) {
         const int r = e / (D / 4), c = e % (D / 4) * 4, j = at + r;
         const bool ok = j < end;
-        const T* src = x;
+        const float* src = x;
         if (ok)
             src = a.table != nullptr ? x + attn_page_row(a, t.n, hk, j) * D + c
                                      : x + (t.seq0 + j) * stride + (int64_t)hk * D + c;
-        load4(dst + r * PITCH + c, src, ok);
+        cp_async16(dst + r * PITCH + c, src, ok);
     }
 }
 
@@ -196,7 +175,7 @@ template <int D> struct Fwd {
     static constexpr uint32_t SMEM = (OFF_P + kRows * PITCH_P) * 4;
 };
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(AttnArgs a, AttnShape sh)
 {
     using F = Fwd<D>;
@@ -222,8 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(AttnArgs a, AttnS
     if (!s_found) return;
     const AttnTile t = s_tile;
     const int32_t hk = unit / sh.parts;
-    const RowMap rows(a, sh, unit, t.row0, t.tokens);
-    const T *q = static_cast<const T*>(a.q), *k = static_cast<const T*>(a.k), *v = static_cast<const T*>(a.v);
+    const RowMap rows(sh, unit, t.row0, t.tokens);
+    const float *q = static_cast<const float*>(a.q), *k = static_cast<const float*>(a.k), *v = static_cast<const float*>(a.v);
     const int32_t keys = attn_keys(a, t), tiles = (keys + kKeys - 1) / kKeys;
     const int32_t j0 = (int32_t)((int64_t)tiles * piece / a.splits),
                   j1 = (int32_t)((int64_t)tiles * (piece + 1) / a.splits);
@@ -300,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(AttnArgs a, AttnS
                 store4(y + 64 * h, make_float4(o[i][2 * h].x * inv, o[i][2 * h].y * inv, o[i][2 * h + 1].x * inv,
                                                o[i][2 * h + 1].y * inv));
         } else {
-            T* y = static_cast<T*>(a.out) + r * D + 4 * tx;
+            float* y = static_cast<float*>(a.out) + r * D + 4 * tx;
             if (tx == 0 && a.lse != nullptr) a.lse[r] = lse;
 #pragma unroll
             for (int h = 0; h < H; ++h)
@@ -423,7 +402,7 @@ __device__ __forceinline__ void weights(float (&p)[4][4], float (&ds)[4][4], con
 }
 
 // dk and dv of 64 keys, over all rows that see them.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(AttnArgs a, AttnShape sh)
 {
     using B = Bwd<D>;
@@ -448,8 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(AttnArgs a, At
     // the tile found has t.index tiles of queries before it; the one with as many behind it
     const int32_t nt = (t.seq_tokens + kKeys - 1) / kKeys, key0 = (nt - 1 - t.index) * kKeys;
     const int32_t end = t.seq_tokens;
-    load_keys<D, D + 4>(sm + B::OFF_K, a, static_cast<const T*>(a.k), a.k_stride, t, hk, key0, end);
-    load_keys<D, D + 4>(sm + B::OFF_V, a, static_cast<const T*>(a.v), a.v_stride, t, hk, key0, end);
+    load_keys<D, D + 4>(sm + B::OFF_K, a, static_cast<const float*>(a.k), a.k_stride, t, hk, key0, end);
+    load_keys<D, D + 4>(sm + B::OFF_V, a, static_cast<const float*>(a.v), a.v_stride, t, hk, key0, end);
     float2 dk[4][2 * H], dv[4][2 * H];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -457,10 +436,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(AttnArgs a, At
         for (int h = 0; h < 2 * H; ++h) dk[i][h] = dv[i][h] = make_float2(0.f, 0.f);
     for (int32_t part = 0; part < sh.parts; ++part) {
         for (int32_t at = key0; at < t.seq_tokens; at += sh.tokens) {
-            const RowMap rows(a, sh, hk * sh.parts + part, t.seq0 + at, min(sh.tokens, t.seq_tokens - at));
+            const RowMap rows(sh, hk * sh.parts + part, t.seq0 + at, min(sh.tokens, t.seq_tokens - at));
             __syncthreads();
-            load_rows<kBwdRows, D>(sm, static_cast<const T*>(a.q), a.q_stride, rows);
-            load_rows<kBwdRows, D>(sm + B::OFF_DO, static_cast<const T*>(a.dout), (int64_t)a.Hq * D, rows);
+            load_rows<kBwdRows, D>(sm, static_cast<const float*>(a.q), a.q_stride, rows);
+            load_rows<kBwdRows, D>(sm + B::OFF_DO, static_cast<const float*>(a.dout), (int64_t)a.Hq * D, rows);
             load_stats(sm + B::OFF_L, a, rows);
             cp_async_commit();
             cp_async_wait_all();
@@ -487,16 +466,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(AttnArgs a, At
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             const float2 x = dk[i][2 * h], y = dk[i][2 * h + 1];
-            store4(static_cast<T*>(a.dk) + r + 64 * h,
+            store4(static_cast<float*>(a.dk) + r + 64 * h,
                    make_float4(x.x * a.scale, x.y * a.scale, y.x * a.scale, y.y * a.scale));
-            store4(static_cast<T*>(a.dv) + r + 64 * h,
+            store4(static_cast<float*>(a.dv) + r + 64 * h,
                    make_float4(dv[i][2 * h].x, dv[i][2 * h].y, dv[i][2 * h + 1].x, dv[i][2 * h + 1].y));
         }
     }
 }
 
 // dq of a tile of rows, over the keys they see.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(AttnArgs a, AttnShape sh)
 {
     using B = Bwd<D>;
@@ -519,9 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(AttnArgs a, Att
     if (!s_found) return;
     const AttnTile t = s_tile;
     const int32_t hk = unit / sh.parts, end = attn_keys(a, t);
-    const RowMap rows(a, sh, unit, t.row0, t.tokens);
-    load_rows<kBwdRows, D>(sm, static_cast<const T*>(a.q), a.q_stride, rows);
-    load_rows<kBwdRows, D>(sm + B::OFF_DO, static_cast<const T*>(a.dout), (int64_t)a.Hq * D, rows);
+    const RowMap rows(sh, unit, t.row0, t.tokens);
+    load_rows<kBwdRows, D>(sm, static_cast<const float*>(a.q), a.q_stride, rows);
+    load_rows<kBwdRows, D>(sm + B::OFF_DO, static_cast<const float*>(a.dout), (int64_t)a.Hq * D, rows);
     load_stats(sm + B::OFF_L, a, rows);
     float2 dq[4][2 * H];
 #pragma unroll
@@ -530,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(AttnArgs a, Att
         for (int h = 0; h < 2 * H; ++h) dq[i][h] = make_float2(0.f, 0.f);
     for (int32_t key0 = 0; key0 < end; key0 += kKeys) {
         __syncthreads();
-        load_keys<D, D + 4>(sm + B::OFF_K, a, static_cast<const T*>(a.k), a.k_stride, t, hk, key0, end);
-        load_keys<D, D + 4>(sm + B::OFF_V, a, static_cast<const T*>(a.v), a.v_stride, t, hk, key0, end);
+        load_keys<D, D + 4>(sm + B::OFF_K, a, static_cast<const float*>(a.k), a.k_stride, t, hk, key0, end);
+        load_keys<D, D + 4>(sm + B::OFF_V, a, static_cast<const float*>(a.v), a.v_stride, t, hk, key0, end);
         cp_async_commit();
         cp_async_wait_all();
         __syncthreads();
@@ -548,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(AttnArgs a, Att
     for (int i = 0; i < 4; ++i) {
         int32_t token, head;
         if (!rows.at(ty * 4 + i, token, head)) continue;
-        T* y = static_cast<T*>(a.dq) + ((int64_t)token * a.Hq + head) * D + 4 * tx;
+        float* y = static_cast<float*>(a.dq) + ((int64_t)token * a.Hq + head) * D + 4 * tx;
 #pragma unroll
         for (int h = 0; h < H; ++h)
             store4(y + 64 * h, make_float4(dq[i][2 * h].x * a.scale, dq[i][2 * h].y * a.scale,
@@ -557,32 +536,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(AttnArgs a, Att
 }
 
 // ---------------------------------------------------------------- launch
-template <typename T, int D> cudaError_t forward(const AttnArgs& a, cudaStream_t stream)
+template <int D> cudaError_t forward(const AttnArgs& a, cudaStream_t stream)
 {
     const AttnShape sh = attn_shape(kRows, a.Hq, a.Hk);
     const int64_t ctas = attn_tiles(a.N, a.T, sh.tokens) * sh.units * a.splits;
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-    auto kern = attn_fwd_kernel<T, D>;
+    auto kern = attn_fwd_kernel<D>;
     static std::atomic<uint64_t> set{0};
     const cudaError_t e = allow_smem(kern, Fwd<D>::SMEM, &set);
     if (e != cudaSuccess) return e;
     return launch_after(kern, launch_config(ctas, kThreads, Fwd<D>::SMEM), stream, a, sh);
 }
 
-template <typename T, int D> cudaError_t backward(const AttnArgs& a, cudaStream_t stream)
+template <int D> cudaError_t backward(const AttnArgs& a, cudaStream_t stream)
 {
     const AttnShape sh = attn_shape(kBwdRows, a.Hq, a.Hk);
-    const int64_t rows = (int64_t)a.T * a.Hq;
-    cudaError_t e = launch_after(attn_delta_kernel<T, D>, launch_config((rows + 7) / 8, 256), stream, a);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     static std::atomic<uint64_t> set_kv{0}, set_q{0};
-    e = allow_smem(attn_bwd_kv_kernel<T, D>, Bwd<D>::SMEM, &set_kv);
-    if (e == cudaSuccess) e = allow_smem(attn_bwd_q_kernel<T, D>, Bwd<D>::SMEM, &set_q);
+    e = allow_smem(attn_bwd_kv_kernel<D>, Bwd<D>::SMEM, &set_kv);
+    if (e == cudaSuccess) e = allow_smem(attn_bwd_q_kernel<D>, Bwd<D>::SMEM, &set_q);
     if (e != cudaSuccess) return e;
-    e = launch_after(attn_bwd_kv_kernel<T, D>,
+    e = launch_after(attn_bwd_kv_kernel<D>,
                      launch_config(attn_tiles(a.N, a.T, kKeys) * a.Hk, kThreads, Bwd<D>::SMEM), stream, a, sh);
     if (e != cudaSuccess) return e;
-    return launch_after(attn_bwd_q_kernel<T, D>,
+    return launch_after(attn_bwd_q_kernel<D>,
                         launch_config(attn_tiles(a.N, a.T, sh.tokens) * sh.units, kThreads, Bwd<D>::SMEM), stream, a,
                         sh);
 }
@@ -611,12 +588,8 @@ int32_t attn_splits(bool bf16, int32_t N, int32_t T, int32_t Hq, int32_t Hk, int
 
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream)
 {
-    cudaError_t e;
-    if (a.bf16)
-        e = launch_attention_tc(a, stream);
-    else
-        e = a.D == 64 ? forward<float, 64>(a, stream) : forward<float, 128>(a, stream);
-    return e;
+    if (a.bf16) return launch_attention_tc(a, stream);
+    return a.D == 64 ? forward<64>(a, stream) : forward<128>(a, stream);
 }
 
 int64_t attention_bwd_workspace_bytes(int32_t N, int32_t T, int32_t Hq, int32_t Hk, int32_t D)
@@ -628,8 +601,15 @@ cudaError_t launch_attention_bwd(const AttnArgs& args, cudaStream_t stream)
 {
     AttnArgs a = args;
     a.delta = static_cast<float*>(a.workspace);
-    if (a.bf16) return a.D == 64 ? backward<__nv_bfloat16, 64>(a, stream) : backward<__nv_bfloat16, 128>(a, stream);
-    return a.D == 64 ? backward<float, 64>(a, stream) : backward<float, 128>(a, stream);
+    const cudaLaunchConfig_t cfg = launch_config(((int64_t)a.T * a.Hq + 7) / 8, 256);
+    const cudaError_t e =
+        a.bf16 ? a.D == 64 ? launch_after(attn_delta_kernel<__nv_bfloat16, 64>, cfg, stream, a)
+                           : launch_after(attn_delta_kernel<__nv_bfloat16, 128>, cfg, stream, a)
+        : a.D == 64 ? launch_after(attn_delta_kernel<float, 64>, cfg, stream, a)
+                    : launch_after(attn_delta_kernel<float, 128>, cfg, stream, a);
+    if (e != cudaSuccess) return e;
+    if (a.bf16) return launch_attention_bwd_tc(a, stream);
+    return a.D == 64 ? backward<64>(a, stream) : backward<128>(a, stream);
 }
 
 }  // namespace kda

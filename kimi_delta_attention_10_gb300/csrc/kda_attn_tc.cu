@@ -131,8 +131,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
 
     if (bar.found) {
         const AttnTile t = bar.tile;
-        const int32_t hk = unit / sh.parts, part = unit - hk * sh.parts, G = a.Hq / a.Hk;
-        const int32_t head0 = hk * G + part * sh.heads;
+        const int32_t hk = unit / sh.parts, head0 = unit * sh.heads;
         // of each of the two tiles of rows: tokens, keys that its last token sees, key tiles
         int32_t tokens[2], keys[2], n[2];
         tokens[0] = min(t.tokens, sh.tokens);
@@ -360,7 +359,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
                 __syncwarp();
                 fence_after_sync();
             }
-            const bool live = i_tok < sh.tokens && i_tok < tokens[m] && g < min(sh.heads, G - part * sh.heads);
+            const bool live = i_tok < sh.tokens && i_tok < tokens[m];
             const int64_t row = (int64_t)(t.row0 + token) * a.Hq + head0 + g;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             char* ws = static_cast<char*>(a.workspace);

@@ -89,13 +89,15 @@ inline cudaError_t encode_heads(CUtensorMap* m, const void* base, int64_t T, int
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Rows of a call cut into tiles of at most `rows`.
+// Rows of a call cut into tiles of at most `rows`: as many heads of the group as fit and
+// divide it, so that no tile has a head of another group.
 inline AttnShape attn_shape(int32_t rows, int32_t Hq, int32_t Hk)
 {
     AttnShape s;
     const int32_t G = Hq / Hk;
     s.heads = G < rows ? G : rows;
-    s.parts = (G + s.heads - 1) / s.heads;
+    while (G % s.heads != 0) --s.heads;
+    s.parts = G / s.heads;
     s.tokens = rows / s.heads;
     s.units = Hk * s.parts;
     return s;
