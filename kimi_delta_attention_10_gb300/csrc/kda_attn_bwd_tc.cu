@@ -199,7 +199,9 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
             }
         } else if (warp == C::WARP_MMA) {
             // -------------------------------------------------------- MMA
-            if (lane == 0) {
+            {
+                const uint32_t lead = elect_one();
+                WarpWait wait(&bar.abort, a.status);
                 constexpr uint32_t id_s = idesc(kFmtBF16, 128, 128), id_d = idesc(kFmtBF16, 128, D, false, true);
                 const uint32_t base = smem_u32(sm);
                 const uint64_t dA = desc_kmajor(base, 128, 0), dB = desc_kmajor(base + C::OFF_RING, 128, 0);
@@ -207,27 +209,27 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
                                              : desc_mnmajor64(base + C::OFF_RING, 0);
                 // tile x of the CTA's own times tile x of the ring
                 auto scores = [&](int x, int32_t i) {
-                    if (wait.dead) return;
+                    if (wait.dead()) return;
                     fence_after_sync();
                     const uint32_t at = ((i & 1) * 2 + x) * C::TILE;
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s)
-                        mma_bf16(tmem + (x ? TM_DP : TM_S), desc_advance(dA, x * C::TILE + kmajor_off(128, s)),
+                        mma_ss(lead, tmem + (x ? TM_DP : TM_S), desc_advance(dA, x * C::TILE + kmajor_off(128, s)),
                                  desc_advance(dB, at + kmajor_off(128, s)), id_s, s > 0);
-                    commit(x ? &bar.dpfull : &bar.sfull[0]);
+                    commit_if(lead, x ? &bar.dpfull : &bar.sfull[0]);
                 };
                 // the weights in tensor memory (rows 0 .. 63 where the first half of the scores
                 // was, the others where the second was) times a tile of the ring
                 auto gradient = [&](int x, int32_t i) {
-                    if (wait.dead) return;
+                    if (wait.dead()) return;
                     fence_after_sync();
                     const uint32_t at = ((i & 1) * 2 + (x ^ 1)) * C::TILE;
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
-                        mma_bf16_ta(tmem + (x ? TM_DK : TM_DV),
+                        mma_ts(lead, tmem + (x ? TM_DK : TM_DV),
                                     tmem + (x ? TM_DP : TM_S) + 8 * (s & 3) + 64 * (s >> 2),
                                     desc_advance(dN, at + mnmajor_off(s)), id_d, i > 0 || s > 0);
-                    commit(&bar.empty[x ^ 1][i & 1]);
+                    commit_if(lead, &bar.empty[x ^ 1][i & 1]);
                 };
                 int32_t at = 0;
                 auto first = [&](int32_t i) {                      // S of tile i
@@ -249,8 +251,9 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
                     wait(&bar.dsfull, i & 1);
                     gradient(1, i);
                 }
-                commit(&bar.done);                     // no MMA outlives the loop
+                commit_if(lead, &bar.done);                     // no MMA outlives the loop
                 mbar_wait(&bar.done, 0);
+                __syncwarp();
             }
         } else if (warp == C::WARP_STAT) {
             // -------------------------------------------------------- lse and delta of the rows
@@ -426,7 +429,9 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps ma
                     for (int x = 0; x < 2; ++x) mbar_wait(&bar.full[x][k & 1], (k >> 1) & 1);
             }
         } else if (warp == C::WARP_MMA) {
-            if (lane == 0) {
+            {
+                const uint32_t lead = elect_one();
+                WarpWait wait(&bar.abort, a.status);
                 constexpr uint32_t id_s = idesc(kFmtBF16, 128, 128), id_d = idesc(kFmtBF16, 128, D, false, true);
                 const uint32_t base = smem_u32(sm);
                 const uint64_t dA = desc_kmajor(base, 128, 0), dB = desc_kmajor(base + C::OFF_RING, 128, 0);
@@ -434,15 +439,15 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps ma
                                              : desc_mnmajor64(base + C::OFF_RING, 0);
                 auto scores = [&](int x, int32_t i) {
                     wait(&bar.full[x][i & 1], (i >> 1) & 1);
-                    if (wait.dead) return;
+                    if (wait.dead()) return;
                     fence_after_sync();
                     const uint32_t at = ((i & 1) * 2 + x) * C::TILE;
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s)
-                        mma_bf16(tmem + (x ? TM_DP : TM_S + (i & 1) * 128), desc_advance(dA, x * C::TILE + kmajor_off(128, s)),
+                        mma_ss(lead, tmem + (x ? TM_DP : TM_S + (i & 1) * 128), desc_advance(dA, x * C::TILE + kmajor_off(128, s)),
                                  desc_advance(dB, at + kmajor_off(128, s)), id_s, s > 0);
-                    if (x) commit(&bar.empty[1][i & 1]);
-                    commit(x ? &bar.dpfull : &bar.sfull[i & 1]);
+                    if (x) commit_if(lead, &bar.empty[1][i & 1]);
+                    commit_if(lead, x ? &bar.dpfull : &bar.sfull[i & 1]);
                 };
                 wait(&bar.afull[0], 0);
                 scores(0, 0);
@@ -451,19 +456,25 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps ma
                     scores(1, i);
                     if (i + 1 < n) scores(0, i + 1);
                     wait(&bar.dsfull, i & 1);
-                    if (wait.dead) continue;
+                    if (wait.dead()) continue;
                     fence_after_sync();
                     const uint32_t at = (i & 1) * 2 * C::TILE;
                     const int32_t keys = all - (i << kTcKeyShift);
+                    auto step = [&](int s) {
+                        mma_ts(lead, tmem + TM_DQ, tmem + TM_DP + 8 * (s & 3) + 64 * (s >> 2),
+                               desc_advance(dN, at + mnmajor_off(s)), id_d, i > 0 || s > 0);
+                    };
+                    if (keys >= kTcKeys) {
 #pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        if (16 * s < keys)
-                            mma_bf16_ta(tmem + TM_DQ, tmem + TM_DP + 8 * (s & 3) + 64 * (s >> 2),
-                                        desc_advance(dN, at + mnmajor_off(s)), id_d, i > 0 || s > 0);
-                    commit(&bar.empty[0][i & 1]);
+                        for (int s = 0; s < 8; ++s) step(s);
+                    } else {
+                        for (int s = 0; 16 * s < keys; ++s) step(s);
+                    }
+                    commit_if(lead, &bar.empty[0][i & 1]);
                 }
-                commit(&bar.done);
+                commit_if(lead, &bar.done);
                 mbar_wait(&bar.done, 0);
+                __syncwarp();
             }
         } else if (warp < 8) {
             const int half = warp >> 2, r = tid & 127;             // the thread's keys: 64 half ..

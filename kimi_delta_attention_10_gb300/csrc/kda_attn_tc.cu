@@ -35,7 +35,10 @@ template <int D> struct Cfg {
     static constexpr int NS = D == 128 ? 5 : 8;                // ring slots: 160, 128 KB
     static constexpr uint32_t OFF_KV = 2 * QTILE, OFF_BAR = OFF_KV + NS * SLOT, SMEM = OFF_BAR + 512 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
-    static constexpr int NT = 320, WARP_LOAD = 8, WARP_MMA = 9;
+    static constexpr int NT = 384, WARP_LOAD = 8, WARP_MMA = 9;
+    // registers of a thread: at launch, then of the softmax's threads, of the others
+    static constexpr int REGS = 168, REGS_SOFTMAX = 216, REGS_OTHER = 72;
+    static_assert(2 * REGS_SOFTMAX + REGS_OTHER <= 3 * REGS, "registers of the block");
     static constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
 };
 
@@ -47,7 +50,7 @@ struct Bars {
     uint64_t full[8], empty[8];        // ring slots
     uint64_t qfull[2];
     uint64_t sfull[2];                 // S in tensor memory
-    uint64_t pfull[2];                 // P in its place
+    uint64_t pfull[2][2];              // its first and second 64 keys' weights in its place
     uint64_t ofull[2];                 // product with V done
     uint64_t drain;
     uint32_t tmem;
@@ -101,7 +104,8 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.qfull[i], 1);
             mbar_init(&bar.sfull[i], 1);
-            mbar_init(&bar.pfull[i], 4);
+            mbar_init(&bar.pfull[i][0], 4);
+            mbar_init(&bar.pfull[i][1], 4);
             mbar_init(&bar.ofull[i], 1);
         }
         mbar_init(&bar.drain, 1);
@@ -128,8 +132,8 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
     fence_after_sync();
     const uint32_t tmem = bar.tmem;
     BoundedWait wait(&bar.abort, a.status);
-
-    if (bar.found) {
+    const bool found = bar.found;
+    {
         const AttnTile t = bar.tile;
         const int32_t hk = unit / sh.parts, head0 = unit * sh.heads;
         // of each of the two tiles of rows: tokens, keys that its last token sees, key tiles
@@ -148,7 +152,10 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
         }
         const int32_t steps = max(n[0], n[1]);
 
-        if (warp == C::WARP_LOAD) {
+        if (warp >= 8) {
+        fewer_registers<C::REGS_OTHER>();
+        if (!found) {
+        } else if (warp == C::WARP_LOAD) {
             // -------------------------------------------------------- producer
             const uint32_t qbytes = (uint32_t)sh.tokens * sh.heads * 128 * HALVES;
             auto load_q = [&](int m) {
@@ -205,7 +212,9 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
             }
         } else if (warp == C::WARP_MMA) {
             // -------------------------------------------------------- MMA
-            if (lane == 0) {
+            {
+                const uint32_t lead = elect_one();
+                WarpWait wait(&bar.abort, a.status);
                 constexpr uint32_t id_s = idesc(kFmtBF16, kTcRows, kTcKeys);
                 constexpr uint32_t id_o = idesc(kFmtBF16, kTcRows, D, false, true);
                 const uint64_t dQ = desc_kmajor(smem_u32(sm), kTcRows, 0);
@@ -214,55 +223,71 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
                                              : desc_mnmajor64(smem_u32(sm + C::OFF_KV), 0);
                 auto full = [&](uint32_t c) { wait(&bar.full[c % NS], (c / NS) & 1); };
                 auto scores = [&](int m, int32_t i) {
-                    if (wait.dead) return;
+                    if (wait.dead()) return;
                     fence_after_sync();
                     const uint32_t at = (2 * i) % NS * C::SLOT;
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s)
-                        mma_bf16(tmem + C::TM_S + m * kTcKeys,
+                        mma_ss(lead, tmem + C::TM_S + m * kTcKeys,
                                  desc_advance(dQ, m * C::QTILE + kmajor_off(kTcRows, s)),
                                  desc_advance(dK, at + kmajor_off(kTcKeys, s)), id_s, s > 0);
-                    commit(&bar.sfull[m]);
+                    commit_if(lead, &bar.sfull[m]);
                 };
-                auto product = [&](int m, int32_t i) {
-                    if (wait.dead) return;
-                    fence_after_sync();
+                // The products of S saturate shared memory's bandwidth, and a look at a barrier
+                // then takes as long as they do (400 cycles): what can be looked at before
+                // them is.
+                auto ready = [&](int m, int32_t i) {
+                    const bool both = mbar_test(&bar.pfull[m][0], i & 1) && mbar_test(&bar.pfull[m][1], i & 1);
+                    return (bool)__all_sync(0xffffffffu, both);
+                };
+                auto product = [&](int m, int32_t i, bool known) {
                     const uint32_t at = (2 * i + 1) % NS * C::SLOT;
                     const int32_t left = keys[m] - ((j0 + i) << kTcKeyShift);
                     auto step = [&](int s) {
-                        mma_bf16_ta(tmem + C::TM_O + m * D, tmem + C::TM_S + m * kTcKeys + 8 * s,
-                                    desc_advance(dV, at + mnmajor_off(s)), id_o, i > 0 || s > 0);
+                        mma_ts(lead, tmem + C::TM_O + m * D, tmem + C::TM_S + m * kTcKeys + 8 * s,
+                               desc_advance(dV, at + mnmajor_off(s)), id_o, i > 0 || s > 0);
                     };
-                    if (left >= kTcKeys) {
 #pragma unroll
-                        for (int s = 0; s < kTcKeys / 16; ++s) step(s);
-                    } else {
-                        for (int s = 0; 16 * s < left; ++s) step(s);
+                    for (int half = 0; half < 2; ++half) {
+                        if (!known) wait(&bar.pfull[m][half], i & 1);
+                        if (wait.dead()) return;
+                        fence_after_sync();
+                        if (left >= kTcKeys) {
+#pragma unroll
+                            for (int s = 4 * half; s < 4 * half + 4; ++s) step(s);
+                        } else {
+                            for (int s = 4 * half; s < 4 * half + 4 && 16 * s < left; ++s) step(s);
+                        }
                     }
-                    commit(&bar.ofull[m]);
+                    commit_if(lead, &bar.ofull[m]);
                 };
-                for (int32_t i = -1; i < steps; ++i) {
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        if (i >= 0 && i < n[m]) {
-                            full(2 * i + 1);
-                            wait(&bar.pfull[m], i & 1);
-                            product(m, i);
-                        }
-                        if (m == 1 && i >= 0 && !wait.dead) commit(&bar.empty[(2 * i + 1) % NS]);
-                        if (i + 1 < n[m]) {
-                            if (i < 0) wait(&bar.qfull[m], 0);
-                            full(2 * i + 2);
-                            scores(m, i + 1);
-                        }
-                        if (m == 1 && i + 1 < steps && !wait.dead) commit(&bar.empty[(2 * i + 2) % NS]);
-                    }
+                for (int m = 0; m < 2; ++m) {
+                    if (n[m] == 0) continue;
+                    wait(&bar.qfull[m], 0);
+                    full(0);
+                    scores(m, 0);
                 }
-                commit(&bar.drain);                    // no MMA outlives the loop
+                if (steps > 0 && !wait.dead()) commit_if(lead, &bar.empty[0]);
+                for (int32_t i = 0; i < steps; ++i) {
+                    full(2 * i + 1);
+                    if (i + 1 < steps) full(2 * i + 2);
+                    if (i < n[0]) product(0, i, false);
+                    const bool known = i < n[1] && ready(1, i);
+                    if (i + 1 < n[0]) scores(0, i + 1);
+                    if (i < n[1]) product(1, i, known);
+                    if (!wait.dead()) commit_if(lead, &bar.empty[(2 * i + 1) % NS]);
+                    if (i + 1 < n[1]) scores(1, i + 1);
+                    if (i + 1 < steps && !wait.dead()) commit_if(lead, &bar.empty[(2 * i + 2) % NS]);
+                }
+                commit_if(lead, &bar.drain);                    // no MMA outlives the loop
                 mbar_wait(&bar.drain, 0);
+                __syncwarp();
             }
+        }
         } else {
             // -------------------------------------------------------- softmax
+            more_registers<C::REGS_SOFTMAX>();
+            if (found) {
             const int m = warp >> 2, quad = warp & 3, r = tid & 127;
             const uint32_t lane0 = tmem_addr(tmem, 32 * quad, 0);
             const uint32_t s_tm = lane0 + C::TM_S + m * kTcKeys, o_tm = lane0 + C::TM_O + m * D;
@@ -294,10 +319,12 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
                 }
                 float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int k = 4; k < kTcKeys; k += 4) {
+                for (int k = 4; k + 8 <= kTcKeys; k += 8) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], s[k + x]);
+                    for (int x = 0; x < 4; ++x) top[x] = max3(top[x], s[k + x], s[k + 4 + x]);
                 }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], s[kTcKeys - 4 + x]);
                 const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
                 const bool grown = most > ref + kGrowth;
                 if (__any_sync(0xffffffffu, grown)) {
@@ -321,21 +348,6 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
                 }
                 // all scores so far -infinity: nothing to subtract
                 const float base = ref == -CUDART_INF_F ? 0.f : -ref;
-                float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int at = 64 * half + 2 * k;
-                        const float2 x = fma2(make_float2(s[at], s[at + 1]), both(c), both(base));
-                        const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                        add[k & 1] = fma2(e, both(1.f), add[k & 1]);
-                        p[k] = pack_bf16(e.x, e.y);
-                    }
-                    tmem_st32(s_tm + 32 * half, p);
-                }
-                sum += add[0].x + add[0].y + add[1].x + add[1].y;
                 if (key0 + kTcKeys > all) {
                     // value rows past the last key, as far as the product reads (16 at a time)
                     const uint32_t at = 2 * i + 1;
@@ -349,10 +361,25 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
                     fence_async_smem();
                     __syncwarp();
                 }
-                tmem_st_wait();
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.pfull[m]);
+                float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int at = 64 * half + 2 * k;
+                        const float2 x = fma2(make_float2(s[at], s[at + 1]), both(c), both(base));
+                        const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                        add[k & 1] = fma2(e, both(1.f), add[k & 1]);
+                        p[k] = pack_bf16(e.x, e.y);
+                    }
+                    tmem_st32(s_tm + 32 * half, p);
+                    tmem_st_wait();
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.pfull[m][half]);
+                }
+                sum += add[0].x + add[0].y + add[1].x + add[1].y;
             }
             if (mine > 0) {
                 wait(&bar.ofull[m], (mine - 1) & 1);
@@ -380,6 +407,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
                 } else {
                     for (int k = 0; k < D; k += 8) *reinterpret_cast<uint4*>(y + k) = make_uint4(0, 0, 0, 0);
                 }
+            }
             }
         }
     }
@@ -414,7 +442,8 @@ template <int D> cudaError_t forward(const AttnArgs& a, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     auto kern = attn_fwd_tc_kernel<D>;
     static std::atomic<uint64_t> set{0};
-    e = allow_smem(kern, C::SMEM, &set);
+    static const cudaError_t registers = check_registers(kern, C::REGS);
+    e = registers == cudaSuccess ? allow_smem(kern, C::SMEM, &set) : registers;
     if (e != cudaSuccess) return e;
     return launch_after(kern, launch_config(ctas, C::NT, C::SMEM), stream, a, sh, maps);
 }

@@ -16,16 +16,52 @@ constexpr float kAttnLog2e = 1.4426950408889634f, kAttnLn2 = 0.6931471805599453f
 constexpr int kTcRows = 128;                   // rows of an MMA
 constexpr int kTcKeys = 128, kTcKeyShift = 7;  // keys of a tile
 
-// D[128, N] (+)= A[128, 16] B[N, 16]^T with A in tensor memory: row r in lane r, two
-// BF16 values of K a column.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id,
-                                            uint32_t acc)
+// The products below are called by a whole converged warp, and `lead` is nonzero in the one
+// lane that issues them.
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t lead;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(lead));
+    return lead;
+}
+// D[128, N] (+)= A[128, 16] B[N, 16]^T, both operands in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
 {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(id), "r"(acc));
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(id), "r"(acc), "r"(lead));
 }
+// The same with A in tensor memory: row r in lane r, two BF16 values of K a column.
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id,
+                                       uint32_t acc)
+{
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(id), "r"(acc), "r"(lead));
+}
+// Arrives on `mbar` when every product that the lane issued before has completed.
+__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t* mbar)
+{
+    asm volatile(
+        "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+            tc::smem_u32(mbar)), "r"(lead)
+        : "memory");
+}
+
+// A bounded wait of a whole warp: it gives up for all lanes or for none.
+struct WarpWait {
+    BoundedWait wait;
+    __device__ __forceinline__ WarpWait(int32_t* abort_flag, int32_t* status) : wait(abort_flag, status) {}
+    __device__ __forceinline__ void operator()(uint64_t* m, uint32_t parity)
+    {
+        wait(m, parity);
+        wait.dead = __any_sync(0xffffffffu, wait.dead);
+    }
+    __device__ __forceinline__ bool dead() const { return wait.dead; }
+};
 
 // As tc::tmem_ld32, without the wait (tmem_ld_wait).
 __device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, float* r)
@@ -70,6 +106,24 @@ __device__ __forceinline__ void tmem_st_wait()
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// Registers of a thread of the warps of this warpgroup from here on (all of whose warps call
+// it), out of those that the block was launched with.
+template <int N> __device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // ---------------------------------------------------------------- host
 // [T, H, D] of 16-bit values, tokens `stride` elements apart, read as boxes of 64 channels of
 // `heads` heads of `tokens` tokens in 128-byte swizzled rows (token, head); rows past the end
@@ -87,6 +141,16 @@ inline cudaError_t encode_heads(CUtensorMap* m, const void* base, int64_t T, int
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Whether a kernel was given exactly the registers a thread that its setmaxnreg counts on:
+// with fewer, the threads that ask for more would wait for good.
+template <typename K> cudaError_t check_registers(K kern, int registers)
+{
+    cudaFuncAttributes f;
+    const cudaError_t e = cudaFuncGetAttributes(&f, kern);
+    if (e != cudaSuccess) return e;
+    return f.numRegs == registers ? cudaSuccess : cudaErrorLaunchOutOfResources;
 }
 
 // Rows of a call cut into tiles of at most `rows`: as many heads of the group as fit and
