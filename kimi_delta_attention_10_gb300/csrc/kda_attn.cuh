@@ -7,8 +7,8 @@
 // call with one token a sequence still fills its rows.
 //
 // Order.  A tile's work is its number of key tiles; CTAs are numbered so that the tiles
-// with the most come first, whichever sequence they belong to (attn_find), and the last
-// CTAs to start are the shortest.
+// with the most come first, whichever sequence they belong to (AttnWalk), and the last
+// to start are the shortest.
 #pragma once
 
 #include <stdint.h>
@@ -112,70 +112,106 @@ __device__ __forceinline__ int32_t attn_deeper(int32_t m, int32_t L, int32_t nt,
     return x <= 0 ? 0 : min(nt, (int32_t)((uint32_t)x / (uint32_t)tokens));
 }
 
-// Tile `item` in the order of falling work; false: there is none, or the offsets are bad
-// (reported; then no tile is found by any CTA).  Called by one whole warp.
+// The tiles of a call in the order of falling work, walked by one whole warp: next(item) for
+// rising items.  Tiles that have the same number of key tiles are a level; a walk keeps its
+// place in one, so that a call with thousands of short sequences looks at each once.
+struct AttnWalk {
+    int32_t tokens, key_shift;
+    bool bad;                // bad offsets (reported): there are no tiles
+    int32_t level;           // tiles of `level` key tiles
+    int32_t first, behind;   // the level's first item, and the next one's
+    int32_t base, passed;    // sequences from `base` on; items of the level before them
+
+    __device__ __forceinline__ int32_t tiles(const AttnArgs& a, int32_t n) const
+    {
+        return (int32_t)(((uint32_t)(a.cu[n + 1] - a.cu[n]) + tokens - 1) / (uint32_t)tokens);
+    }
+    // tiles of sequence n that have more than d key tiles
+    __device__ __forceinline__ int32_t count(const AttnArgs& a, int32_t n, int32_t d) const
+    {
+        const int32_t m = a.cu[n + 1] - a.cu[n], nt = tiles(a, n);
+        return nt - attn_deeper(m, attn_kv_len(a, n, m), nt, a.causal, tokens, key_shift, d);
+    }
+    __device__ __forceinline__ int32_t total(const AttnArgs& a, int32_t d) const
+    {
+        int32_t s = 0;
+        for (int32_t n = threadIdx.x & 31; n < a.N; n += 32) s += count(a, n, d);
+        return (int32_t)__reduce_add_sync(0xffffffffu, (unsigned)s);
+    }
+    __device__ __forceinline__ AttnWalk(const AttnArgs& a, int32_t tile_tokens, int shift)
+        : tokens(tile_tokens), key_shift(shift), bad(false), level(0), first(0), behind(0), base(0), passed(0)
+    {
+        int32_t deepest = 0;
+        for (int32_t n = threadIdx.x & 31; n < a.N; n += 32) {
+            const int32_t c0 = a.cu[n], c1 = a.cu[n + 1];
+            bad |= c0 < 0 || c1 < c0 || c1 > a.T || (n == 0 && c0 != 0);
+            deepest = max(deepest, attn_kv_len(a, n, c1 - c0));
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        if (bad && (threadIdx.x & 31) == 0) report_status(a.status, KDA_ERR_DEVICE_ARG);
+        deepest = __reduce_max_sync(0xffffffffu, deepest);
+        level = (int32_t)(((int64_t)deepest + (1 << key_shift) - 1) >> key_shift) + 1;   // above the first
+    }
+    // false: there is no such tile
+    __device__ __forceinline__ bool next(const AttnArgs& a, int32_t item, AttnTile& t)
+    {
+        const int lane = threadIdx.x & 31;
+        if (bad) return false;
+        if (item >= behind) {
+            // the least d with at most `item` tiles of more than d key tiles: the item has d itself
+            int32_t lo = 0, hi = level - 1;
+            if (hi < 0) return false;
+            while (lo < hi) {
+                const int32_t mid = (lo + hi) >> 1;
+                if (total(a, mid) <= item) hi = mid;
+                else lo = mid + 1;
+            }
+            level = lo;
+            first = total(a, lo);
+            behind = total(a, lo - 1);
+            base = passed = 0;
+            if (item >= behind) return false;
+        }
+        int32_t rank = item - first - passed;
+        for (;; base += 32) {
+            if (base >= a.N) return false;             // lengths that changed meanwhile
+            const int32_t n = base + lane;
+            const int32_t mine = n < a.N ? count(a, n, level - 1) - count(a, n, level) : 0;
+            int32_t upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, upto > rank);
+            if (past) {
+                const int at = __ffs(past) - 1;
+                rank -= __shfl_sync(0xffffffffu, upto - mine, at);
+                const int32_t who = base + at, c0 = a.cu[who], m = a.cu[who + 1] - c0;
+                const int32_t L = attn_kv_len(a, who, m);
+                t.n = who;
+                t.index = attn_deeper(m, L, tiles(a, who), a.causal, tokens, key_shift, level - 1) + rank;
+                t.seq0 = c0;
+                t.seq_tokens = m;
+                t.row0 = c0 + t.index * tokens;
+                t.tokens = min(tokens, m - t.index * tokens);
+                t.kv_len = L;
+                t.pos0 = L - m + t.index * tokens;
+                return true;
+            }
+            const int32_t all = __shfl_sync(0xffffffffu, upto, 31);
+            rank -= all;
+            passed += all;
+        }
+    }
+};
+
+// Tile `item` alone.
 __device__ __forceinline__ bool attn_find(const AttnArgs& a, int32_t item, int32_t tokens, int key_shift,
                                           AttnTile& t)
 {
-    const int lane = threadIdx.x & 31;
-    bool bad = false;
-    int32_t deepest = 0;
-    for (int32_t n = lane; n < a.N; n += 32) {
-        const int32_t c0 = a.cu[n], c1 = a.cu[n + 1];
-        bad |= c0 < 0 || c1 < c0 || c1 > a.T || (n == 0 && c0 != 0);
-        deepest = max(deepest, attn_kv_len(a, n, c1 - c0));
-    }
-    if (__any_sync(0xffffffffu, bad)) {
-        if (lane == 0) report_status(a.status, KDA_ERR_DEVICE_ARG);
-        return false;
-    }
-    deepest = __reduce_max_sync(0xffffffffu, deepest);
-    auto count = [&](int32_t n, int32_t d) {           // tiles of n with more than d key tiles
-        const int32_t m = a.cu[n + 1] - a.cu[n], nt = (int32_t)(((uint32_t)m + tokens - 1) / (uint32_t)tokens);
-        return nt - attn_deeper(m, attn_kv_len(a, n, m), nt, a.causal, tokens, key_shift, d);
-    };
-    auto total = [&](int32_t d) {
-        int32_t s = 0;
-        for (int32_t n = lane; n < a.N; n += 32) s += count(n, d);
-        return (int32_t)__reduce_add_sync(0xffffffffu, (unsigned)s);
-    };
-    // the least d with at most `item` tiles of more than d key tiles: the item has d itself
-    int32_t lo = 0, hi = (int32_t)(((int64_t)deepest + (1 << key_shift) - 1) >> key_shift);
-    while (lo < hi) {
-        const int32_t mid = (lo + hi) >> 1;
-        if (total(mid) <= item) hi = mid;
-        else lo = mid + 1;
-    }
-    int32_t rank = item - total(lo);
-    for (int32_t base = 0; base < a.N; base += 32) {
-        const int32_t n = base + lane;
-        const int32_t mine = n < a.N ? count(n, lo - 1) - count(n, lo) : 0;
-        int32_t upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += x;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, upto > rank);
-        if (past) {
-            const int at = __ffs(past) - 1;
-            rank -= __shfl_sync(0xffffffffu, upto - mine, at);
-            const int32_t who = base + at, c0 = a.cu[who], m = a.cu[who + 1] - c0;
-            const int32_t L = attn_kv_len(a, who, m);
-            const int32_t nt = (int32_t)(((uint32_t)m + tokens - 1) / (uint32_t)tokens);
-            t.n = who;
-            t.index = attn_deeper(m, L, nt, a.causal, tokens, key_shift, lo - 1) + rank;
-            t.seq0 = c0;
-            t.seq_tokens = m;
-            t.row0 = c0 + t.index * tokens;
-            t.tokens = min(tokens, m - t.index * tokens);
-            t.kv_len = L;
-            t.pos0 = L - m + t.index * tokens;
-            return true;
-        }
-        rank -= __shfl_sync(0xffffffffu, upto, 31);
-    }
-    return false;
+    AttnWalk w(a, tokens, key_shift);
+    return w.next(a, item, t);
 }
 
 // Keys that the tile's last token sees.

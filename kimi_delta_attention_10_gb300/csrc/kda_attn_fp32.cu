@@ -579,7 +579,7 @@ cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t stream)
 int32_t attn_splits(bool bf16, int32_t N, int32_t T, int32_t Hq, int32_t Hk, int32_t D, int64_t kv_most)
 {
     const AttnShape sh = attn_shape(bf16 ? kTcRows : kRows, Hq, Hk);
-    const int64_t ctas = attn_tiles(N, T, bf16 ? 2 * sh.tokens : sh.tokens) * sh.units, most = 2 * (int64_t)sm_count();
+    const int64_t ctas = attn_tiles(N, T, bf16 ? 2 * sh.tokens : sh.tokens) * sh.units, most = sm_count();
     if (ctas * 2 > most) return 1;
     const int64_t by_keys = kv_most / (4 * (bf16 ? kTcKeys : kKeys)), by_ctas = most / ctas;
     int64_t s = by_ctas < by_keys ? by_ctas : by_keys;

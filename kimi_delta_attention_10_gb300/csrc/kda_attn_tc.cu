@@ -43,23 +43,57 @@ template <int D> struct Cfg {
 };
 
 struct Maps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, out;
+};
+
+// A CTA's next tile of rows, from the producer to the other roles.
+struct Job {
+    AttnTile t;
+    int32_t unit, piece, found;
 };
 
 struct Bars {
     uint64_t full[8], empty[8];        // ring slots
-    uint64_t qfull[2];
+    uint64_t qfull[2], qempty[2];
     uint64_t sfull[2];                 // S in tensor memory
-    uint64_t pfull[2][2];              // its first and second 64 keys' weights in its place
+    uint64_t pfull[2];                 // P in its place
     uint64_t ofull[2];                 // product with V done
+    uint64_t oempty[2];                // O read
+    uint64_t jfull[2], jempty[2];
     uint64_t drain;
     uint32_t tmem;
     int32_t abort;
-    int32_t found;
-    AttnTile tile;
+    Job job[2];
 };
 
-// Bytes that a tile's thread stores of its row of O, scaled.
+// What a job is for each of its two tiles of rows.
+struct Plan {
+    int32_t tokens[2], keys[2];        // tokens, and keys that its last token sees
+    int32_t n[2], steps;               // key tiles in this piece, and the most of them
+    int32_t all, j0;                   // keys that any row sees, first key tile
+    bool slot[2];                      // the rows leave through a ring slot
+    __device__ __forceinline__ Plan(const AttnArgs& a, const AttnShape& sh, const Job& job)
+    {
+        const AttnTile& t = job.t;
+        tokens[0] = min(t.tokens, sh.tokens);
+        tokens[1] = t.tokens - tokens[0];
+        all = attn_keys(a, t);
+        const int32_t tiles = (int32_t)(((int64_t)all + kTcKeys - 1) >> kTcKeyShift);
+        j0 = (int32_t)((int64_t)tiles * job.piece / a.splits);
+        const int32_t j1 = (int32_t)((int64_t)tiles * (job.piece + 1) / a.splits);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            keys[m] = tokens[m] == 0 ? 0
+                      : a.causal     ? max(0, t.pos0 + m * sh.tokens + tokens[m])
+                                     : t.kv_len;
+            n[m] = max(0, min(j1, (int32_t)(((int64_t)keys[m] + kTcKeys - 1) >> kTcKeyShift)) - j0);
+            slot[m] = n[m] > 0 && tokens[m] == sh.tokens && a.pieces == 1;
+        }
+        steps = max(n[0], n[1]);
+    }
+};
+
+// The D values of a thread's row of O, scaled, to the output or a piece of it.
 template <int D>
 __device__ __forceinline__ void store_row(uint32_t o_tmem, float inv, bool live, __nv_bfloat16* out, float* piece)
 {
@@ -82,11 +116,12 @@ __device__ __forceinline__ void store_row(uint32_t o_tmem, float inv, bool live,
                     pack_bf16(x[i + 4] * inv, x[i + 5] * inv), pack_bf16(x[i + 6] * inv, x[i + 7] * inv));
         }
     }
+    __syncwarp();
 }
 
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::NT, 1)
-attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
+attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant__ Maps maps)
 {
     using C = Cfg<D>;
     constexpr int HALVES = C::HALVES, NS = C::NS;
@@ -103,27 +138,20 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.qfull[i], 1);
+            mbar_init(&bar.qempty[i], 1);
             mbar_init(&bar.sfull[i], 1);
-            mbar_init(&bar.pfull[i][0], 4);
-            mbar_init(&bar.pfull[i][1], 4);
+            mbar_init(&bar.pfull[i], 4);
             mbar_init(&bar.ofull[i], 1);
+            mbar_init(&bar.oempty[i], 4);
+            mbar_init(&bar.jfull[i], 1);
+            mbar_init(&bar.jempty[i], 9);
         }
         mbar_init(&bar.drain, 1);
         bar.abort = 0;
         fence_mbar_init();
     }
     wait_for_previous();
-    const int32_t piece = blockIdx.x % a.splits, unit = blockIdx.x / a.splits % sh.units,
-                  item = blockIdx.x / a.splits / sh.units;
-    if (warp == 0) {
-        AttnTile t;
-        const bool found = attn_find(a, item, 2 * sh.tokens, kTcKeyShift, t);
-        if (lane == 0) {
-            bar.tile = t;
-            bar.found = found;
-            if (blockIdx.x == 0 && a.pieces > 1) *static_cast<int32_t*>(a.workspace) = found ? a.cu[a.N] : 0;
-        }
-    } else if (warp == C::WARP_MMA) {
+    if (warp == C::WARP_MMA) {
         tmem_alloc(&bar.tmem, C::TM_COLS);
         tmem_relinquish();
     }
@@ -131,211 +159,268 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = bar.tmem;
-    BoundedWait wait(&bar.abort, a.status);
-    const bool found = bar.found;
-    {
-        const AttnTile t = bar.tile;
-        const int32_t hk = unit / sh.parts, head0 = unit * sh.heads;
-        // of each of the two tiles of rows: tokens, keys that its last token sees, key tiles
-        int32_t tokens[2], keys[2], n[2];
-        tokens[0] = min(t.tokens, sh.tokens);
-        tokens[1] = t.tokens - tokens[0];
-        const int32_t all = attn_keys(a, t), tiles = (int32_t)(((int64_t)all + kTcKeys - 1) >> kTcKeyShift);
-        const int32_t j0 = (int32_t)((int64_t)tiles * piece / a.splits),
-                      j1 = (int32_t)((int64_t)tiles * (piece + 1) / a.splits);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            keys[m] = tokens[m] == 0 ? 0
-                      : a.causal     ? max(0, t.pos0 + m * sh.tokens + tokens[m])
-                                     : t.kv_len;
-            n[m] = max(0, min(j1, (int32_t)(((int64_t)keys[m] + kTcKeys - 1) >> kTcKeyShift)) - j0);
-        }
-        const int32_t steps = max(n[0], n[1]);
+    WarpWait wait(&bar.abort, a.status);
 
-        if (warp >= 8) {
+    if (warp >= 8) {
         fewer_registers<C::REGS_OTHER>();
-        if (!found) {
-        } else if (warp == C::WARP_LOAD) {
+        if (warp == C::WARP_LOAD) {
             // -------------------------------------------------------- producer
-            const uint32_t qbytes = (uint32_t)sh.tokens * sh.heads * 128 * HALVES;
-            auto load_q = [&](int m) {
-                if (n[m] == 0) return;
-                if (lane == 0) mbar_arrive_expect_tx(&bar.qfull[m], qbytes);
-                __syncwarp();
-                if (lane < HALVES)
-                    tma_load_3d(sm + m * C::QTILE + lane * (kTcRows * 128), &maps.q, 64 * lane, head0,
-                                t.row0 + m * sh.tokens, &bar.qfull[m]);
-            };
+            AttnWalk walk(a, 2 * sh.tokens, kTcKeyShift);
+            if (blockIdx.x == 0 && lane == 0 && a.pieces > 1)
+                *static_cast<int32_t*>(a.workspace) = walk.bad ? 0 : a.cu[a.N];
             // a box: rows of a page, or a whole tile; the lane's part of a tile
             const int shift = a.table == nullptr || a.page_shift > kTcKeyShift ? kTcKeyShift : a.page_shift;
             const int half = lane % HALVES, token = lane / HALVES << shift;
             const bool mine = lane / HALVES < kTcKeys >> shift;
-            int32_t row = 0;
-            auto find_row = [&](int32_t j) {
-                const int32_t at = (j << kTcKeyShift) + token;
-                if (a.table != nullptr && mine && at < all) row = (int32_t)attn_page_row(a, t.n, hk, at);
-            };
-            if (steps > 0) find_row(j0);
-            load_q(0);
-            uint32_t c = 0;
-            for (int32_t i = 0; i < steps; ++i) {
-                const int32_t j = j0 + i, left = all - (j << kTcKeyShift);
-                const int32_t boxes = (min(left, kTcKeys) + (1 << shift) - 1) >> shift;
-                const int32_t here = row;
-                if (i + 1 < steps) find_row(j + 1);
-                for (int kv = 0; kv < 2; ++kv, ++c) {
-                    const uint32_t slot = c % NS;
-                    wait(&bar.empty[slot], ((c / NS) & 1) ^ 1);
-                    wait.dead = __any_sync(0xffffffffu, wait.dead);
-                    if (wait.dead) break;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&bar.full[slot], (uint32_t)(boxes * HALVES) << (shift + 7));
-                    __syncwarp();
-                    if (lane < boxes * HALVES) {
-                        unsigned char* dst = sm + C::OFF_KV + slot * C::SLOT + half * (kTcKeys * 128) + token * 128;
-                        const void* map = kv ? &maps.v : &maps.k;
-                        if (a.table != nullptr)
-                            tma_load_2d(smem_u32(dst), map, 64 * half, here, &bar.full[slot]);
-                        else
-                            tma_load_3d(dst, map, 64 * half, hk, t.seq0 + (j << kTcKeyShift), &bar.full[slot]);
-                    }
-                    if (i == 0 && kv == 0) load_q(1);
+            const uint32_t qbytes = (uint32_t)sh.tokens * sh.heads * 128 * HALVES;
+            uint32_t c = 0, loads[2] = {0, 0};
+            for (int32_t round = 0; !wait.dead(); ++round) {
+                // to and fro over the CTAs, since the work falls
+                const int64_t at = (int64_t)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                Job job;
+                job.found = 0;
+                if (at < jobs) {
+                    const int32_t rest = (int32_t)at / a.splits;
+                    job.piece = (int32_t)at - rest * a.splits;
+                    job.unit = rest % sh.units;
+                    job.found = walk.next(a, rest / sh.units, job.t);
                 }
-                if (wait.dead) break;
+                wait(&bar.jempty[round & 1], ((round >> 1) & 1) ^ 1);
+                if (lane == 0) bar.job[round & 1] = job;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.jfull[round & 1]);
+                if (!job.found) break;
+                const Plan p(a, sh, job);
+                const int32_t hk = job.unit / sh.parts;
+                auto load_q = [&](int m) {
+                    if (p.n[m] == 0) return;
+                    wait(&bar.qempty[m], (loads[m] & 1) ^ 1);
+                    if (wait.dead()) return;
+                    if (lane == 0) mbar_arrive_expect_tx(&bar.qfull[m], qbytes);
+                    __syncwarp();
+                    if (lane < HALVES)
+                        tma_load_3d(sm + m * C::QTILE + lane * (kTcRows * 128), &maps.q, 64 * lane,
+                                    job.unit * sh.heads, job.t.row0 + m * sh.tokens, &bar.qfull[m]);
+                    ++loads[m];
+                };
+                int32_t row = 0;
+                auto find_row = [&](int32_t j) {
+                    const int32_t k = (j << kTcKeyShift) + token;
+                    if (a.table != nullptr && mine && k < p.all) row = (int32_t)attn_page_row(a, job.t.n, hk, k);
+                };
+                if (p.steps > 0) find_row(p.j0);
+                load_q(0);
+                for (int32_t i = 0; i < p.steps && !wait.dead(); ++i) {
+                    const int32_t j = p.j0 + i, left = p.all - (j << kTcKeyShift);
+                    const int32_t boxes = (min(left, kTcKeys) + (1 << shift) - 1) >> shift;
+                    const int32_t here = row;
+                    if (i + 1 < p.steps) find_row(j + 1);
+                    for (int kv = 0; kv < 2; ++kv, ++c) {
+                        const uint32_t slot = c % NS;
+                        wait(&bar.empty[slot], ((c / NS) & 1) ^ 1);
+                        if (wait.dead()) break;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(&bar.full[slot], (uint32_t)(boxes * HALVES) << (shift + 7));
+                        __syncwarp();
+                        if (lane < boxes * HALVES) {
+                            unsigned char* dst = sm + C::OFF_KV + slot * C::SLOT + half * (kTcKeys * 128) + token * 128;
+                            const void* map = kv ? &maps.v : &maps.k;
+                            if (a.table != nullptr)
+                                tma_load_2d(smem_u32(dst), map, 64 * half, here, &bar.full[slot]);
+                            else
+                                tma_load_3d(dst, map, 64 * half, hk, job.t.seq0 + (j << kTcKeyShift), &bar.full[slot]);
+                        }
+                        if (i == 0 && kv == 0) load_q(1);
+                    }
+                }
+                // slots for the outputs
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    if (!p.slot[m] || wait.dead()) continue;
+                    wait(&bar.empty[c % NS], ((c / NS) & 1) ^ 1);
+                    if (wait.dead()) continue;
+                    if (lane == 0) mbar_arrive(&bar.full[c % NS]);
+                    ++c;
+                }
             }
             // every copy has landed before the CTA ends
             if (lane == 0) {
                 for (int m = 0; m < 2; ++m)
-                    if (n[m] > 0 && (m == 0 || c > 0)) mbar_wait(&bar.qfull[m], 0);
+                    if (loads[m] > 0) mbar_wait(&bar.qfull[m], (loads[m] - 1) & 1);
                 for (uint32_t k = c > (uint32_t)NS ? c - NS : 0; k < c; ++k)
                     mbar_wait(&bar.full[k % NS], (k / NS) & 1);
             }
+            __syncwarp();
         } else if (warp == C::WARP_MMA) {
             // -------------------------------------------------------- MMA
-            {
-                const uint32_t lead = elect_one();
-                WarpWait wait(&bar.abort, a.status);
-                constexpr uint32_t id_s = idesc(kFmtBF16, kTcRows, kTcKeys);
-                constexpr uint32_t id_o = idesc(kFmtBF16, kTcRows, D, false, true);
-                const uint64_t dQ = desc_kmajor(smem_u32(sm), kTcRows, 0);
-                const uint64_t dK = desc_kmajor(smem_u32(sm + C::OFF_KV), kTcKeys, 0);
-                const uint64_t dV = D == 128 ? desc_mnmajor128(smem_u32(sm + C::OFF_KV), kTcKeys * 128, 0)
-                                             : desc_mnmajor64(smem_u32(sm + C::OFF_KV), 0);
-                auto full = [&](uint32_t c) { wait(&bar.full[c % NS], (c / NS) & 1); };
+            // a negative scale's sign goes into the products, so that their order is the scores'
+            const uint32_t id_s = idesc(kFmtBF16, kTcRows, kTcKeys) | (a.scale < 0.f ? kNegateA : 0u);
+            constexpr uint32_t id_o = idesc(kFmtBF16, kTcRows, D, false, true);
+            const uint32_t lead = elect_one();
+            const uint64_t dQ = desc_kmajor(smem_u32(sm), kTcRows, 0);
+            const uint64_t dK = desc_kmajor(smem_u32(sm + C::OFF_KV), kTcKeys, 0);
+            const uint64_t dV = D == 128 ? desc_mnmajor128(smem_u32(sm + C::OFF_KV), kTcKeys * 128, 0)
+                                         : desc_mnmajor64(smem_u32(sm + C::OFF_KV), 0);
+            uint32_t c = 0;                            // ring slots of the jobs before
+            uint32_t done[2] = {0, 0};                 // key tiles of the jobs before, of each tile of rows
+            uint32_t held[2] = {0, 0};                 // jobs with any
+            for (int32_t round = 0;; ++round) {
+                wait(&bar.jfull[round & 1], (round >> 1) & 1);
+                if (wait.dead()) break;
+                const Job& job = bar.job[round & 1];
+                if (!job.found) break;
+                const Plan p(a, sh, job);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);
+                auto full = [&](uint32_t i) { wait(&bar.full[(c + i) % NS], ((c + i) / NS) & 1); };
+                auto emptied = [&](uint32_t i) {
+                    if (!wait.dead()) commit_if(lead, &bar.empty[(c + i) % NS]);
+                };
                 auto scores = [&](int m, int32_t i) {
                     if (wait.dead()) return;
                     fence_after_sync();
-                    const uint32_t at = (2 * i) % NS * C::SLOT;
+                    const uint32_t at = (c + 2 * i) % NS * C::SLOT;
+                    const uint64_t q = desc_advance(dQ, m * C::QTILE), k = desc_advance(dK, at);
 #pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        mma_ss(lead, tmem + C::TM_S + m * kTcKeys,
-                                 desc_advance(dQ, m * C::QTILE + kmajor_off(kTcRows, s)),
-                                 desc_advance(dK, at + kmajor_off(kTcKeys, s)), id_s, s > 0);
+                    for (uint32_t s = 0; s < D / 16; ++s)
+                        mma_ss(lead, tmem + C::TM_S + m * kTcKeys, desc_advance(q, kmajor_off(kTcRows, s)),
+                               desc_advance(k, kmajor_off(kTcKeys, s)), id_s, s > 0);
                     commit_if(lead, &bar.sfull[m]);
+                    if (i + 1 == p.n[m]) commit_if(lead, &bar.qempty[m]);
                 };
                 // The products of S saturate shared memory's bandwidth, and a look at a barrier
-                // then takes as long as they do (400 cycles): what can be looked at before
-                // them is.
+                // then takes several hundred cycles: what can be looked at beside the others is.
                 auto ready = [&](int m, int32_t i) {
-                    const bool both = mbar_test(&bar.pfull[m][0], i & 1) && mbar_test(&bar.pfull[m][1], i & 1);
-                    return (bool)__all_sync(0xffffffffu, both);
+                    return (bool)__all_sync(0xffffffffu, mbar_test(&bar.pfull[m], (done[m] + i) & 1));
                 };
                 auto product = [&](int m, int32_t i, bool known) {
-                    const uint32_t at = (2 * i + 1) % NS * C::SLOT;
-                    const int32_t left = keys[m] - ((j0 + i) << kTcKeyShift);
-                    auto step = [&](int s) {
+                    if (i == 0) wait(&bar.oempty[m], (held[m] & 1) ^ 1);
+                    if (!known) wait(&bar.pfull[m], (done[m] + i) & 1);
+                    if (wait.dead()) return;
+                    fence_after_sync();
+                    const uint64_t v = desc_advance(dV, (c + 2 * i + 1) % NS * C::SLOT);
+                    const int32_t left = p.keys[m] - ((p.j0 + i) << kTcKeyShift);
+                    auto step = [&](uint32_t s) {
                         mma_ts(lead, tmem + C::TM_O + m * D, tmem + C::TM_S + m * kTcKeys + 8 * s,
-                               desc_advance(dV, at + mnmajor_off(s)), id_o, i > 0 || s > 0);
+                               desc_advance(v, mnmajor_off(s)), id_o, i > 0 || s > 0);
                     };
+                    if (left >= kTcKeys) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (!known) wait(&bar.pfull[m][half], i & 1);
-                        if (wait.dead()) return;
-                        fence_after_sync();
-                        if (left >= kTcKeys) {
-#pragma unroll
-                            for (int s = 4 * half; s < 4 * half + 4; ++s) step(s);
-                        } else {
-                            for (int s = 4 * half; s < 4 * half + 4 && 16 * s < left; ++s) step(s);
-                        }
+                        for (uint32_t s = 0; s < kTcKeys / 16; ++s) step(s);
+                    } else {
+#pragma unroll 1
+                        for (uint32_t s = 0; 16 * (int32_t)s < left; ++s) step(s);
                     }
                     commit_if(lead, &bar.ofull[m]);
                 };
                 for (int m = 0; m < 2; ++m) {
-                    if (n[m] == 0) continue;
-                    wait(&bar.qfull[m], 0);
+                    if (p.n[m] == 0) continue;
+                    wait(&bar.qfull[m], held[m] & 1);
                     full(0);
                     scores(m, 0);
                 }
-                if (steps > 0 && !wait.dead()) commit_if(lead, &bar.empty[0]);
-                for (int32_t i = 0; i < steps; ++i) {
-                    full(2 * i + 1);
-                    if (i + 1 < steps) full(2 * i + 2);
-                    if (i < n[0]) product(0, i, false);
-                    const bool known = i < n[1] && ready(1, i);
-                    if (i + 1 < n[0]) scores(0, i + 1);
-                    if (i < n[1]) product(1, i, known);
-                    if (!wait.dead()) commit_if(lead, &bar.empty[(2 * i + 1) % NS]);
-                    if (i + 1 < n[1]) scores(1, i + 1);
-                    if (i + 1 < steps && !wait.dead()) commit_if(lead, &bar.empty[(2 * i + 2) % NS]);
+                if (p.steps > 0) {
+                    emptied(0);
+                    full(1);
+                    if (p.steps > 1) full(2);
                 }
-                commit_if(lead, &bar.drain);                    // no MMA outlives the loop
-                mbar_wait(&bar.drain, 0);
-                __syncwarp();
+                for (int32_t i = 0; i < p.steps; ++i) {
+                    if (i < p.n[0]) product(0, i, false);
+                    const bool known = i < p.n[1] && ready(1, i);
+                    if (i + 1 < p.n[0]) scores(0, i + 1);
+                    if (i < p.n[1]) product(1, i, known);
+                    emptied(2 * i + 1);
+                    // the next step's tiles, while these products run
+                    if (i + 1 < p.steps) full(2 * i + 3);
+                    if (i + 2 < p.steps) full(2 * i + 4);
+                    if (i + 1 < p.n[1]) scores(1, i + 1);
+                    if (i + 1 < p.steps) emptied(2 * i + 2);
+                }
+                c += 2 * p.steps + p.slot[0] + p.slot[1];
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    done[m] += p.n[m];
+                    held[m] += p.n[m] > 0;
+                }
             }
+            commit_if(lead, &bar.drain);               // no MMA outlives the loop
+            mbar_wait(&bar.drain, 0);
+            __syncwarp();
         }
-        } else {
-            // -------------------------------------------------------- softmax
-            more_registers<C::REGS_SOFTMAX>();
-            if (found) {
-            const int m = warp >> 2, quad = warp & 3, r = tid & 127;
-            const uint32_t lane0 = tmem_addr(tmem, 32 * quad, 0);
-            const uint32_t s_tm = lane0 + C::TM_S + m * kTcKeys, o_tm = lane0 + C::TM_O + m * D;
-            const int32_t i_tok = r / sh.heads, g = r - i_tok * sh.heads;
-            const int32_t token = m * sh.tokens + i_tok;          // of the CTA's tokens
+    } else {
+        // ------------------------------------------------------------ softmax
+        more_registers<C::REGS_SOFTMAX>();
+        const int m = warp >> 2, quad = warp & 3, r = tid & 127;
+        const uint32_t lane0 = tmem_addr(tmem, 32 * quad, 0);
+        const uint32_t s_tm = lane0 + C::TM_S + m * kTcKeys, o_tm = lane0 + C::TM_O + m * D;
+        const int32_t i_tok = r / sh.heads, g = r - i_tok * sh.heads;
+        const int32_t token = m * sh.tokens + i_tok;                  // of the job's tokens
+        // positive (for a scale of zero as good as zero), so that a masked score stays -infinity
+        const float factor = a.scale == 0.f ? 1.2e-38f : fabsf(a.scale) * kAttnLog2e;
+        uint32_t c = 0, done = 0;                      // ring slots and key tiles of the jobs before
+        for (int32_t round = 0;; ++round) {
+            wait(&bar.jfull[round & 1], (round >> 1) & 1);
+            if (wait.dead()) break;
+            const Job job = bar.job[round & 1];
+            if (!job.found) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);
+            const Plan p(a, sh, job);
+            const AttnTile& t = job.t;
+            const int32_t n = m ? p.n[1] : p.n[0];
             const int32_t limit = a.causal ? t.pos0 + token + 1 : t.kv_len;
             const int32_t least = a.causal ? t.pos0 + m * sh.tokens + 1 : t.kv_len;   // any row's
-            // maxima are taken of the products themselves, which a positive factor keeps in order
-            const bool ordered = a.scale > 0.f;
-            const float c = ordered ? a.scale * kAttnLog2e : 1.f;
             float ref = -CUDART_INF_F, sum = 0.f;
-            const int32_t mine = n[m];
-            for (int32_t i = 0; i < mine; ++i) {
-                const int32_t key0 = (j0 + i) << kTcKeyShift;
-                wait(&bar.sfull[m], i & 1);
-                __syncwarp();
+            for (int32_t i = 0; i < n; ++i) {
+                const int32_t key0 = (p.j0 + i) << kTcKeyShift;
+                const uint32_t phase = (done + i) & 1;
+                wait(&bar.sfull[m], phase);
                 fence_after_sync();
                 float s[kTcKeys];
 #pragma unroll
                 for (int k = 0; k < kTcKeys; k += 32) tmem_ld32_start(s_tm + k, s + k);
                 tmem_ld_wait(s);
-                if (!ordered) {
-#pragma unroll
-                    for (int k = 0; k < kTcKeys; ++k) s[k] *= a.scale * kAttnLog2e;
-                }
                 if (key0 + kTcKeys > least) {
 #pragma unroll
                     for (int k = 0; k < kTcKeys; ++k) s[k] = key0 + k < limit ? s[k] : -CUDART_INF_F;
                 }
-                float top[4] = {s[0], s[1], s[2], s[3]};
+                // The first half's weights from the reference as it is, beside the maximum that may
+                // move it: then once more.
+                uint32_t w[32];
+                float2 add[2];
+                auto weigh = [&](int half) {
+                    // all scores so far -infinity: nothing to subtract
+                    const float base = ref == -CUDART_INF_F ? 0.f : -ref;
 #pragma unroll
-                for (int k = 4; k + 8 <= kTcKeys; k += 8) {
+                    for (int k = 0; k < 32; ++k) {
+                        const int at = 64 * half + 2 * k;
+                        const float2 x = fma2(make_float2(s[at], s[at + 1]), both(factor), both(base));
+                        const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                        add[k & 1] = fma2(e, both(1.f), add[k & 1]);
+                        w[k] = pack_bf16(e.x, e.y);
+                    }
+                };
+                for (;;) {
+                    add[0] = add[1] = make_float2(0.f, 0.f);
+                    weigh(0);
+                    float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) top[x] = max3(top[x], s[k + x], s[k + 4 + x]);
-                }
+                    for (int k = 4; k + 8 <= kTcKeys; k += 8) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], s[kTcKeys - 4 + x]);
-                const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-                const bool grown = most > ref + kGrowth;
-                if (__any_sync(0xffffffffu, grown)) {
+                        for (int x = 0; x < 4; ++x) top[x] = max3(top[x], s[k + x], s[k + 4 + x]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], s[kTcKeys - 4 + x]);
+                    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
+                    const bool grown = most > ref + kGrowth;
+                    if (!__any_sync(0xffffffffu, grown)) break;
                     const float keep = grown ? exp2f(ref - most) : 1.f;
                     if (grown) ref = most;
                     sum *= keep;
                     if (i > 0) {
-                        wait(&bar.ofull[m], (i - 1) & 1);
-                        __syncwarp();
+                        wait(&bar.ofull[m], phase ^ 1);
                         fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < D; k += 32) {
                             float x[32];
                             tmem_ld32(o_tm + k, x);
@@ -343,17 +428,19 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
                             for (int y = 0; y < 32; ++y) x[y] *= keep;
                             tmem_st32(o_tm + k, reinterpret_cast<const uint32_t*>(x));
                         }
-                        tmem_st_wait();
                     }
                 }
-                // all scores so far -infinity: nothing to subtract
-                const float base = ref == -CUDART_INF_F ? 0.f : -ref;
-                if (key0 + kTcKeys > all) {
+                tmem_st32(s_tm, w);
+                weigh(1);
+                tmem_st32(s_tm + 32, w);
+                sum += add[0].x + add[0].y + add[1].x + add[1].y;
+                if (key0 + kTcKeys > p.all) {
                     // value rows past the last key, as far as the product reads (16 at a time)
-                    const uint32_t at = 2 * i + 1;
+                    const uint32_t at = c + 2 * i + 1;
                     wait(&bar.full[at % NS], (at / NS) & 1);
-                    const int first = all - key0, rows = ((first + 15) & ~15) - first;
+                    const int first = p.all - key0, rows = ((first + 15) & ~15) - first;
                     unsigned char* v = sm + C::OFF_KV + at % NS * C::SLOT;
+#pragma unroll 1
                     for (int e = r; e < rows * 8 * HALVES; e += 128)
                         *reinterpret_cast<uint4*>(v + (e >> 3) % HALVES * (kTcKeys * 128) +
                                                   (first + (e >> 3) / HALVES) * 128 + (e & 7) * 16) =
@@ -361,55 +448,77 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ Maps maps)
                     fence_async_smem();
                     __syncwarp();
                 }
-                float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int at = 64 * half + 2 * k;
-                        const float2 x = fma2(make_float2(s[at], s[at + 1]), both(c), both(base));
-                        const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                        add[k & 1] = fma2(e, both(1.f), add[k & 1]);
-                        p[k] = pack_bf16(e.x, e.y);
-                    }
-                    tmem_st32(s_tm + 32 * half, p);
-                    tmem_st_wait();
-                    fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.pfull[m][half]);
-                }
-                sum += add[0].x + add[0].y + add[1].x + add[1].y;
-            }
-            if (mine > 0) {
-                wait(&bar.ofull[m], (mine - 1) & 1);
+                tmem_st_wait();
+                fence_before_sync();
                 __syncwarp();
-                fence_after_sync();
+                if (lane == 0) mbar_arrive(&bar.pfull[m]);
             }
-            const bool live = i_tok < sh.tokens && i_tok < tokens[m];
-            const int64_t row = (int64_t)(t.row0 + token) * a.Hq + head0 + g;
+            const bool live = i_tok < (m ? p.tokens[1] : p.tokens[0]);
+            const int64_t row = (int64_t)(t.row0 + token) * a.Hq + job.unit * sh.heads + g;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             char* ws = static_cast<char*>(a.workspace);
-            float* py = a.pieces > 1 ? reinterpret_cast<float*>(ws + attn_pieces_o(a, piece)) + row * D : nullptr;
+            float* py = a.pieces > 1 ? reinterpret_cast<float*>(ws + attn_pieces_o(a, job.piece)) + row * D : nullptr;
             __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.out) + row * D;
             if (live) {
                 const float lse = sum == 0.f ? -CUDART_INF_F : (ref + log2f(sum)) * kAttnLn2;
-                if (a.pieces > 1) reinterpret_cast<float*>(ws + attn_pieces_lse(a, piece))[row] = lse;
+                if (a.pieces > 1) reinterpret_cast<float*>(ws + attn_pieces_lse(a, job.piece))[row] = lse;
                 else if (a.lse != nullptr) a.lse[row] = lse;
             }
-            // a sum of zero: no weight, and O may hold 0 times an infinity
-            if (mine > 0 && __any_sync(0xffffffffu, sum != 0.f)) {
-                store_row<D>(o_tm, inv, live && sum != 0.f, y, py);
+            const bool slot = m ? p.slot[1] : p.slot[0];
+            if (n > 0) {
+                wait(&bar.ofull[m], (done + n - 1) & 1);
+                fence_after_sync();
+                if (slot) {
+                    // through a ring slot: 32 rows of a warp in 16-byte pieces would take a cycle
+                    // each of the path that the barriers share
+                    const uint32_t at = c + 2 * p.steps + (m ? p.slot[0] : 0);
+                    unsigned char* buf = sm + C::OFF_KV + at % NS * C::SLOT;
+                    wait(&bar.full[at % NS], (at / NS) & 1);
+                    const bool weight = sum != 0.f;        // else zeros, whatever the products gave
+#pragma unroll
+                    for (int k = 0; k < D; k += 32) {
+                        float x[32];
+                        tmem_ld32(o_tm + k, x);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) x[y] = weight ? x[y] * inv : 0.f;
+#pragma unroll
+                        for (int y = 0; y < 32; y += 8)
+                            *reinterpret_cast<uint4*>(buf + sw128_tile(kTcRows, r, 2 * (k + y))) =
+                                make_uint4(pack_bf16(x[y], x[y + 1]), pack_bf16(x[y + 2], x[y + 3]),
+                                           pack_bf16(x[y + 4], x[y + 5]), pack_bf16(x[y + 6], x[y + 7]));
+                    }
+                    fence_async_smem();
+                    fence_before_sync();
+                    named_sync(1 + m, 128);
+                    if (r == 0) {
+                        mbar_arrive_n(&bar.oempty[m], 4);
+                        for (int h = 0; h < HALVES; ++h)
+                            tma_store_3d(&maps.out, buf + h * (kTcRows * 128), 64 * h, job.unit * sh.heads,
+                                         t.row0 + m * sh.tokens);
+                        tma_store_wait<true>();
+                        mbar_arrive(&bar.empty[at % NS]);
+                    }
+                } else {
+                    store_row<D>(o_tm, inv, live && sum != 0.f, y, py);
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.oempty[m]);
+                }
             }
-            if (live && sum == 0.f) {
+            // no weight: zeros, whatever the products gave
+            if (live && sum == 0.f && !slot) {
                 if (py != nullptr) {
                     for (int k = 0; k < D; k += 4) *reinterpret_cast<float4*>(py + k) = make_float4(0.f, 0.f, 0.f, 0.f);
                 } else {
                     for (int k = 0; k < D; k += 8) *reinterpret_cast<uint4*>(y + k) = make_uint4(0, 0, 0, 0);
                 }
             }
-            }
+            __syncwarp();
+            c += 2 * p.steps + p.slot[0] + p.slot[1];
+            done += n;
         }
+        if (r == 0) tma_store_wait<false>();
+        __syncwarp();
     }
     fence_before_sync();
     __syncthreads();
@@ -423,11 +532,13 @@ template <int D> cudaError_t forward(const AttnArgs& a, cudaStream_t stream)
 {
     using C = Cfg<D>;
     const AttnShape sh = attn_shape(kTcRows, a.Hq, a.Hk);
-    const int64_t ctas = attn_tiles(a.N, a.T, 2 * sh.tokens) * sh.units * a.splits;
-    if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+    const int64_t jobs = attn_tiles(a.N, a.T, 2 * sh.tokens) * sh.units * a.splits;
+    if (jobs > INT32_MAX) return cudaErrorInvalidValue;
+    const int64_t ctas = jobs < sm_count() ? jobs : sm_count();
     Maps maps;
     memset(&maps, 0, sizeof(maps));
     cudaError_t e = encode_heads(&maps.q, a.q, a.T, a.Hq, D, a.q_stride, sh.heads, sh.tokens);
+    if (e == cudaSuccess) e = encode_heads(&maps.out, a.out, a.T, a.Hq, D, (int64_t)a.Hq * D, sh.heads, sh.tokens);
     if (a.table == nullptr) {
         if (e == cudaSuccess) e = encode_heads(&maps.k, a.k, a.T, a.Hk, D, a.k_stride, 1, kTcKeys);
         if (e == cudaSuccess) e = encode_heads(&maps.v, a.v, a.T, a.Hk, D, a.v_stride, 1, kTcKeys);
@@ -445,7 +556,8 @@ template <int D> cudaError_t forward(const AttnArgs& a, cudaStream_t stream)
     static const cudaError_t registers = check_registers(kern, C::REGS);
     e = registers == cudaSuccess ? allow_smem(kern, C::SMEM, &set) : registers;
     if (e != cudaSuccess) return e;
-    return launch_after(kern, launch_config(ctas, C::NT, C::SMEM), stream, a, sh, maps);
+    return launch_after(kern, launch_config(ctas, C::NT, C::SMEM), stream, a, sh,
+                        (int32_t)jobs, maps);
 }
 
 }  // namespace

@@ -24,6 +24,8 @@ __device__ __forceinline__ uint32_t elect_one()
     asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(lead));
     return lead;
 }
+// Negates A of a product (an addend of its instruction descriptor).
+constexpr uint32_t kNegateA = 1u << 13;
 // D[128, N] (+)= A[128, 16] B[N, 16]^T, both operands in shared memory.
 __device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
 {
@@ -51,16 +53,39 @@ __device__ __forceinline__ void commit_if(uint32_t lead, uint64_t* mbar)
         : "memory");
 }
 
-// A bounded wait of a whole warp: it gives up for all lanes or for none.
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* m, uint32_t n)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(m)), "r"(n) : "memory");
+}
+
+// A bounded wait of a whole converged warp: it gives up for all lanes or for none, after
+// which the role's waits return at once and it works no more.  Short, since the roles' code
+// competes for the instruction cache.
 struct WarpWait {
-    BoundedWait wait;
-    __device__ __forceinline__ WarpWait(int32_t* abort_flag, int32_t* status) : wait(abort_flag, status) {}
+    volatile int32_t* abort;
+    int32_t* status;
+    bool gave_up;
+    __device__ __forceinline__ WarpWait(int32_t* abort_flag, int32_t* status_word)
+        : abort(abort_flag), status(status_word), gave_up(false) {}
     __device__ __forceinline__ void operator()(uint64_t* m, uint32_t parity)
     {
-        wait(m, parity);
-        wait.dead = __any_sync(0xffffffffu, wait.dead);
+        if (__all_sync(0xffffffffu, mbar_test(m, parity))) return;
+        uint32_t polls = 0;
+        uint64_t since = 0;
+        while (!gave_up && !tc::mbar_try_wait(m, parity)) {
+            if (++polls % tc::kPollsPerCheck == 0) {
+                const uint64_t now = tc::globaltimer_ns();
+                if (since == 0) since = now;
+                if (*abort || now - since > tc::kWaitLimitNs || polls > tc::kPollsPerCheck * tc::kMaxTimerChecks) {
+                    gave_up = true;
+                    *abort = 1;
+                    report_status(status, KDA_ERR_TIMEOUT);
+                }
+            }
+        }
+        gave_up = __any_sync(0xffffffffu, gave_up);
     }
-    __device__ __forceinline__ bool dead() const { return wait.dead; }
+    __device__ __forceinline__ bool dead() const { return gave_up; }
 };
 
 // As tc::tmem_ld32, without the wait (tmem_ld_wait).
@@ -104,6 +129,22 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* u)
 __device__ __forceinline__ void tmem_st_wait()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Stores a box of shared memory (swizzled as tma_load_3d leaves it) to a 3-D tensor map; the
+// thread's stores are waited for together.
+__device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(tmap),
+                 "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(src))
+                 : "memory");
+}
+// The thread's stores so far have read shared memory (kRead), or are complete.
+template <bool kRead> __device__ __forceinline__ void tma_store_wait()
+{
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    if (kRead) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    else asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // Registers of a thread of the warps of this warpgroup from here on (all of whose warps call
@@ -166,11 +207,10 @@ inline AttnShape attn_shape(int32_t rows, int32_t Hq, int32_t Hk)
     s.units = Hk * s.parts;
     return s;
 }
-// Tiles of a call: every one has a token, and all but a sequence's last are full.
+// Tiles of a call, at most: all but one of the sequences end in a tile of one token.
 inline int64_t attn_tiles(int32_t N, int32_t T, int32_t tokens)
 {
-    const int64_t n = (int64_t)T / tokens + N;
-    return n < T ? n : T;
+    return N < T ? (int64_t)(T - N) / tokens + N : T;
 }
 
 }  // namespace kda
