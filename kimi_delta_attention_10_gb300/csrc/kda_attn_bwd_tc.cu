@@ -43,6 +43,9 @@ template <int D> struct Cfg {
 struct KvMaps {
     CUtensorMap q, dout, k, v;
 };
+struct QMaps {
+    CUtensorMap q, dout, k, v, dq;
+};
 
 struct Bars {
     uint64_t afull[2];                 // the CTA's own two tiles
@@ -382,108 +385,233 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
 }
 
 // ---------------------------------------------------------------- dq
+template <int D> struct CfgQ {
+    static constexpr int HALVES = D / 64;
+    static constexpr uint32_t TILE = 128 * D * 2;
+    // slots of keys and of values, each in a ring of its own: a tile's keys are held until the
+    // product with dS, its values only until dP
+    static constexpr int KS = D == 128 ? 3 : 4, VS = D == 128 ? 2 : 4;
+    static constexpr uint32_t OFF_K = 2 * TILE, OFF_V = OFF_K + KS * TILE, OFF_BAR = OFF_V + VS * TILE,
+                              SMEM = OFF_BAR + 512 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
+    static constexpr int NT = 320, WARP_LOAD = 8, WARP_MMA = 9;
+    static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DQ = 384;      // two buffers of dP
+};
+
+struct QBars {
+    uint64_t afull[2], aempty[2];      // the rows' queries and dO
+    uint64_t kfull[4], kempty[4], vfull[4], vempty[4];         // ring slots
+    uint64_t sfull, sempty;
+    uint64_t dpfull[2], dsfull[2];     // dP, dS in its place
+    uint64_t ofull, oempty;            // dq added up, read
+    uint64_t jfull[2], jempty[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int32_t abort;
+    AttnJob job[2];
+};
+
 template <int D>
-__global__ void __launch_bounds__(Cfg<D>::NT, 1)
-attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps maps)
+__global__ void __launch_bounds__(CfgQ<D>::NT, 1)
+attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant__ QMaps maps)
 {
-    using C = Cfg<D>;
-    constexpr int HALVES = C::HALVES;
-    constexpr uint32_t TM_S = 0, TM_DP = 256, TM_DQ = 384;         // two buffers of S
+    using C = CfgQ<D>;
+    constexpr int HALVES = C::HALVES, KS = C::KS, VS = C::VS;
     extern __shared__ unsigned char raw[];
     unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    Bars& bar = *reinterpret_cast<Bars*>(sm + C::OFF_BAR);
+    QBars& bar = *reinterpret_cast<QBars*>(sm + C::OFF_BAR);
+    static_assert(sizeof(QBars) <= 512, "barriers");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int32_t unit = blockIdx.x % sh.units, item = blockIdx.x / sh.units, rows = sh.tokens * sh.heads;
-    const int32_t hk = unit / sh.parts, head0 = unit * sh.heads;
-    start(bar, a, item, sh.tokens);
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bar.kfull[i], 1);
+            mbar_init(&bar.kempty[i], 1);
+            mbar_init(&bar.vfull[i], 1);
+            mbar_init(&bar.vempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.afull[i], 1);
+            mbar_init(&bar.aempty[i], 1);
+            mbar_init(&bar.dpfull[i], 1);
+            mbar_init(&bar.dsfull[i], 8);
+            mbar_init(&bar.jfull[i], 1);
+            mbar_init(&bar.jempty[i], 9);
+        }
+        mbar_init(&bar.sfull, 1);
+        mbar_init(&bar.sempty, 8);
+        mbar_init(&bar.ofull, 1);
+        mbar_init(&bar.oempty, 8);
+        mbar_init(&bar.drain, 1);
+        bar.abort = 0;
+        fence_mbar_init();
+    }
+    wait_for_previous();
+    if (warp == C::WARP_MMA) {
+        tmem_alloc(&bar.tmem, 512);
+        tmem_relinquish();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
     const uint32_t tmem = bar.tmem;
-    BoundedWait wait(&bar.abort, a.status);
-    if (bar.found) {
-        const AttnTile t = bar.tile;
-        const int32_t all = attn_keys(a, t), n = (all + kTcKeys - 1) >> kTcKeyShift;
-        auto ring = [&](int x, int32_t i) { return sm + C::OFF_RING + ((i & 1) * 2 + x) * C::TILE; };
+    WarpWait wait(&bar.abort, a.status);
 
-        if (warp == C::WARP_LOAD) {
-            if (lane == 0) {
-                for (int x = 0; x < 2; ++x) {
-                    mbar_arrive_expect_tx(&bar.afull[x], (uint32_t)rows * 128 * HALVES);
-                    for (int h = 0; h < HALVES; ++h)
-                        tma_load_3d(sm + x * C::TILE + h * (128 * 128), x ? &maps.dout : &maps.q, 64 * h, head0,
-                                    t.row0, &bar.afull[x]);
+    if (warp == C::WARP_LOAD) {
+        // ------------------------------------------------------------ producer
+        AttnWalk walk(a, sh.tokens, kTcKeyShift);
+        uint32_t ck = 0, cv = 0, loads[2] = {0, 0};
+        for (int32_t round = 0; !wait.dead(); ++round) {
+            const AttnJob job = attn_job(walk, a, sh, jobs, round);
+            wait(&bar.jempty[round & 1], ((round >> 1) & 1) ^ 1);
+            if (lane == 0) bar.job[round & 1] = job;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.jfull[round & 1]);
+            if (!job.found) break;
+            const int32_t n = (attn_keys(a, job.t) + kTcKeys - 1) >> kTcKeyShift, hk = job.unit / sh.parts;
+            auto load = [&](unsigned char* dst, const void* map, int y, int z, uint32_t bytes, uint64_t* full) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(full, bytes);
+                    for (int h = 0; h < HALVES; ++h) tma_load_3d(dst + h * (128 * 128), map, 64 * h, y, z, full);
                 }
-                int32_t i = 0;
-                for (; i < n; ++i) {
-                    for (int x = 0; x < 2; ++x) {
-                        wait(&bar.empty[x][i & 1], ((i >> 1) & 1) ^ 1);
-                        if (wait.dead) break;
-                        mbar_arrive_expect_tx(&bar.full[x][i & 1], C::TILE);
-                        for (int h = 0; h < HALVES; ++h)
-                            tma_load_3d(ring(x, i) + h * (128 * 128), x ? &maps.v : &maps.k, 64 * h, hk,
-                                        t.seq0 + (i << kTcKeyShift), &bar.full[x][i & 1]);
-                    }
-                    if (wait.dead) break;
-                }
-                mbar_wait(&bar.afull[0], 0);
-                mbar_wait(&bar.afull[1], 0);
-                for (int32_t k = max(0, i - 2); k < i; ++k)
-                    for (int x = 0; x < 2; ++x) mbar_wait(&bar.full[x][k & 1], (k >> 1) & 1);
-            }
-        } else if (warp == C::WARP_MMA) {
-            {
-                const uint32_t lead = elect_one();
-                WarpWait wait(&bar.abort, a.status);
-                constexpr uint32_t id_s = idesc(kFmtBF16, 128, 128), id_d = idesc(kFmtBF16, 128, D, false, true);
-                const uint32_t base = smem_u32(sm);
-                const uint64_t dA = desc_kmajor(base, 128, 0), dB = desc_kmajor(base + C::OFF_RING, 128, 0);
-                const uint64_t dN = D == 128 ? desc_mnmajor128(base + C::OFF_RING, 128 * 128, 0)
-                                             : desc_mnmajor64(base + C::OFF_RING, 0);
-                auto scores = [&](int x, int32_t i) {
-                    wait(&bar.full[x][i & 1], (i >> 1) & 1);
-                    if (wait.dead()) return;
-                    fence_after_sync();
-                    const uint32_t at = ((i & 1) * 2 + x) * C::TILE;
+                __syncwarp();
+            };
 #pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        mma_ss(lead, tmem + (x ? TM_DP : TM_S + (i & 1) * 128), desc_advance(dA, x * C::TILE + kmajor_off(128, s)),
-                                 desc_advance(dB, at + kmajor_off(128, s)), id_s, s > 0);
-                    if (x) commit_if(lead, &bar.empty[1][i & 1]);
-                    commit_if(lead, x ? &bar.dpfull : &bar.sfull[i & 1]);
-                };
-                wait(&bar.afull[0], 0);
-                scores(0, 0);
-                wait(&bar.afull[1], 0);
-                for (int32_t i = 0; i < n; ++i) {
-                    scores(1, i);
-                    if (i + 1 < n) scores(0, i + 1);
-                    wait(&bar.dsfull, i & 1);
-                    if (wait.dead()) continue;
+            for (int x = 0; x < 2; ++x) {
+                wait(&bar.aempty[x], (loads[x] & 1) ^ 1);
+                if (wait.dead()) continue;
+                load(sm + x * C::TILE, x ? &maps.dout : &maps.q, job.unit * sh.heads, job.t.row0,
+                     (uint32_t)sh.tokens * sh.heads * 128 * HALVES, &bar.afull[x]);
+                ++loads[x];
+            }
+            for (int32_t i = 0; i < n; ++i) {
+                const int32_t key = job.t.seq0 + (i << kTcKeyShift);
+                wait(&bar.kempty[ck % KS], ((ck / KS) & 1) ^ 1);
+                if (wait.dead()) break;
+                load(sm + C::OFF_K + ck % KS * C::TILE, &maps.k, hk, key, C::TILE, &bar.kfull[ck % KS]);
+                ++ck;
+                wait(&bar.vempty[cv % VS], ((cv / VS) & 1) ^ 1);
+                if (wait.dead()) break;
+                load(sm + C::OFF_V + cv % VS * C::TILE, &maps.v, hk, key, C::TILE, &bar.vfull[cv % VS]);
+                ++cv;
+            }
+            if (job.t.tokens == sh.tokens) {           // a slot for the gradients
+                wait(&bar.vempty[cv % VS], ((cv / VS) & 1) ^ 1);
+                if (wait.dead()) break;
+                if (lane == 0) mbar_arrive(&bar.vfull[cv % VS]);
+                ++cv;
+            }
+        }
+        // every copy has landed before the CTA ends
+        if (lane == 0) {
+            for (int x = 0; x < 2; ++x)
+                if (loads[x] > 0) mbar_wait(&bar.afull[x], (loads[x] - 1) & 1);
+            for (uint32_t k = ck > KS ? ck - KS : 0; k < ck; ++k) mbar_wait(&bar.kfull[k % KS], (k / KS) & 1);
+            for (uint32_t k = cv > VS ? cv - VS : 0; k < cv; ++k) mbar_wait(&bar.vfull[k % VS], (k / VS) & 1);
+        }
+        __syncwarp();
+    } else if (warp == C::WARP_MMA) {
+        // ------------------------------------------------------------ MMA
+        constexpr uint32_t id_s = idesc(kFmtBF16, 128, 128), id_d = idesc(kFmtBF16, 128, D, false, true);
+        const uint32_t lead = elect_one(), base = smem_u32(sm);
+        const uint64_t dA = desc_kmajor(base, 128, 0);
+        const uint64_t dK = desc_kmajor(base + C::OFF_K, 128, 0), dV = desc_kmajor(base + C::OFF_V, 128, 0);
+        const uint64_t dN = D == 128 ? desc_mnmajor128(base + C::OFF_K, 128 * 128, 0)
+                                     : desc_mnmajor64(base + C::OFF_K, 0);
+        uint32_t done = 0, cv = 0;                     // key tiles, and slots of values, of the jobs before
+        for (int32_t round = 0;; ++round) {
+            wait(&bar.jfull[round & 1], (round >> 1) & 1);
+            if (wait.dead()) break;
+            const AttnJob& job = bar.job[round & 1];
+            if (!job.found) break;
+            const int32_t all = attn_keys(a, job.t), n = (all + kTcKeys - 1) >> kTcKeyShift;
+            const bool slot = job.t.tokens == sh.tokens;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);
+            auto keys_full = [&](uint32_t i) { wait(&bar.kfull[(done + i) % KS], ((done + i) / KS) & 1); };
+            auto values_full = [&](uint32_t i) { wait(&bar.vfull[(cv + i) % VS], ((cv + i) / VS) & 1); };
+            // S, then dP, of key tile i
+            auto scores = [&](int x, int32_t i) {
+                if (x == 0) wait(&bar.sempty, ((done + i) & 1) ^ 1);
+                if (wait.dead()) return;
+                fence_after_sync();
+                const uint64_t p = desc_advance(dA, x * C::TILE), 
+                               q = x ? desc_advance(dV, (cv + i) % VS * C::TILE) : desc_advance(dK, (done + i) % KS * C::TILE);
+                const uint32_t d = tmem + (x ? C::TM_DP + ((done + i) & 1) * 128 : C::TM_S);
+#pragma unroll
+                for (uint32_t s = 0; s < D / 16; ++s)
+                    mma_ss(lead, d, desc_advance(p, kmajor_off(128, s)), desc_advance(q, kmajor_off(128, s)), id_s, s > 0);
+                commit_if(lead, x ? &bar.dpfull[(done + i) & 1] : &bar.sfull);
+                if (x) commit_if(lead, &bar.vempty[(cv + i) % VS]);
+                if (i + 1 == n) commit_if(lead, &bar.aempty[x]);
+            };
+            wait(&bar.afull[0], round & 1);
+            keys_full(0);
+            scores(0, 0);
+            wait(&bar.afull[1], round & 1);
+            values_full(0);
+            scores(1, 0);
+            if (n > 1) {
+                keys_full(1);
+                values_full(1);
+            }
+            for (int32_t i = 0; i < n; ++i) {
+                if (i + 1 < n) {
+                    scores(0, i + 1);
+                    scores(1, i + 1);
+                }
+                if (i == 0) wait(&bar.oempty, (round & 1) ^ 1);
+                const uint32_t b = (done + i) & 1;
+                wait(&bar.dsfull[b], ((done + i) >> 1) & 1);
+                if (!wait.dead()) {
                     fence_after_sync();
-                    const uint32_t at = (i & 1) * 2 * C::TILE;
+                    const uint64_t q = desc_advance(dN, (done + i) % KS * C::TILE);
                     const int32_t keys = all - (i << kTcKeyShift);
-                    auto step = [&](int s) {
-                        mma_ts(lead, tmem + TM_DQ, tmem + TM_DP + 8 * (s & 3) + 64 * (s >> 2),
-                               desc_advance(dN, at + mnmajor_off(s)), id_d, i > 0 || s > 0);
+                    // dS: keys 0 .. 63 where the first half of dP was, the others where the second was
+                    auto step = [&](uint32_t s) {
+                        mma_ts(lead, tmem + C::TM_DQ, tmem + C::TM_DP + b * 128 + 8 * (s & 3) + 64 * (s >> 2),
+                               desc_advance(q, mnmajor_off(s)), id_d, i > 0 || s > 0);
                     };
                     if (keys >= kTcKeys) {
 #pragma unroll
-                        for (int s = 0; s < 8; ++s) step(s);
+                        for (uint32_t s = 0; s < 8; ++s) step(s);
                     } else {
-                        for (int s = 0; 16 * s < keys; ++s) step(s);
+#pragma unroll 1
+                        for (uint32_t s = 0; 16 * (int32_t)s < keys; ++s) step(s);
                     }
-                    commit_if(lead, &bar.empty[0][i & 1]);
+                    commit_if(lead, &bar.kempty[(done + i) % KS]);
+                    if (i + 1 == n) commit_if(lead, &bar.ofull);
                 }
-                commit_if(lead, &bar.done);
-                mbar_wait(&bar.done, 0);
-                __syncwarp();
+                // the next step's tiles, while this product runs
+                if (i + 2 < n) {
+                    keys_full(i + 2);
+                    values_full(i + 2);
+                }
             }
-        } else if (warp < 8) {
-            const int half = warp >> 2, r = tid & 127;             // the thread's keys: 64 half ..
-            const uint32_t lane0 = tmem_addr(tmem, 32 * (warp & 3), 0);
-            const uint32_t dp_tm = lane0 + TM_DP + 64 * half;
-            const float2 c = both(a.scale * kAttnLog2e);
-            const int32_t tok = r / sh.heads, g = r - tok * sh.heads;
+            cv += n + slot;
+            done += n;
+        }
+        commit_if(lead, &bar.drain);                   // no MMA outlives the loop
+        mbar_wait(&bar.drain, 0);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ P and dS
+        const int half = warp >> 2, r = tid & 127;                 // the thread's keys: 64 half ..
+        const uint32_t lane0 = tmem_addr(tmem, 32 * (warp & 3), 0);
+        const uint32_t s_tm = lane0 + C::TM_S + 64 * half;
+        const float2 factor = both(a.scale * kAttnLog2e);
+        const int32_t tok = r / sh.heads, g = r - tok * sh.heads;
+        uint32_t cv = 0, done = 0;
+        for (int32_t round = 0;; ++round) {
+            wait(&bar.jfull[round & 1], (round >> 1) & 1);
+            if (wait.dead()) break;
+            const AttnJob job = bar.job[round & 1];
+            if (!job.found) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);
+            const AttnTile& t = job.t;
+            const int32_t all = attn_keys(a, t), n = (all + kTcKeys - 1) >> kTcKeyShift;
             const bool live = tok < t.tokens;
-            const int64_t row = (int64_t)(t.row0 + tok) * a.Hq + head0 + g;
+            const int64_t row = (int64_t)(t.row0 + tok) * a.Hq + job.unit * sh.heads + g;
             const float lse = live ? a.lse_in[row] : CUDART_INF_F;
             const float2 nl = both(lse == -CUDART_INF_F ? -CUDART_INF_F : -lse * kAttnLog2e);
             const float2 nd = both(live ? -a.delta[row] : 0.f);
@@ -491,22 +619,23 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps ma
                 // keys from this one on are tokens behind the row's
                 const int32_t end = t.pos0 + tok + 1 - (i << kTcKeyShift) - 64 * half;
                 const bool cut = ((i + 1) << kTcKeyShift) > t.pos0 + 1;
-                const uint32_t s_tm = lane0 + TM_S + (i & 1) * 128 + 64 * half;
-                wait(&bar.sfull[i & 1], (i >> 1) & 1);
-                __syncwarp();
+                const uint32_t at = done + i, b = at & 1, dp_tm = lane0 + C::TM_DP + b * 128 + 64 * half;
+                wait(&bar.sfull, at & 1);
                 fence_after_sync();
                 float p[64];
                 tmem_ld32_start(s_tm, p);
                 tmem_ld32_start(s_tm + 32, p + 32);
                 tmem_ld_wait(p);
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.sempty);
 #pragma unroll
                 for (int k = 0; k < 64; k += 2) {
-                    const float2 x = fma2(make_float2(p[k], p[k + 1]), c, nl);
+                    const float2 x = fma2(make_float2(p[k], p[k + 1]), factor, nl);
                     p[k] = ex2_approx(x.x);
                     p[k + 1] = ex2_approx(x.y);
                 }
-                wait(&bar.dpfull, i & 1);
-                __syncwarp();
+                wait(&bar.dpfull[b], (at >> 1) & 1);
                 fence_after_sync();
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -528,22 +657,56 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps ma
                 if (keys < kTcKeys && half == 0) {
                     // keys past the end, as far as the product reads (16 at a time); the scores
                     // with them are done
-                    zero_rows<D>(ring(0, i), keys, (keys + 15) & ~15, r, 128);
+                    zero_rows<D>(sm + C::OFF_K + at % KS * C::TILE, keys, (keys + 15) & ~15, r, 128);
                     fence_async_smem();
                     __syncwarp();
                 }
                 store_pairs(dp_tm, p);
                 fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.dsfull);
+                if (lane == 0) mbar_arrive(&bar.dsfull[b]);
             }
-            wait(&bar.done, 0);
-            __syncwarp();
+            wait(&bar.ofull, round & 1);
             fence_after_sync();
-            // each half of the warps stores half of the channels
-            store_row<D / 2>(lane0 + TM_DQ + D / 2 * half, a.scale, live,
-                             static_cast<__nv_bfloat16*>(a.dq) + row * D + D / 2 * half);
+            // each half of the warps takes half of the channels
+            const uint32_t o_tm = lane0 + C::TM_DQ + D / 2 * half;
+            if (t.tokens == sh.tokens) {
+                const uint32_t slot = (cv + n) % VS;
+                unsigned char* buf = sm + C::OFF_V + slot * C::TILE;
+                wait(&bar.vfull[slot], ((cv + n) / VS) & 1);
+#pragma unroll
+                for (int k = 0; k < D / 2; k += 32) {
+                    float x[32];
+                    tmem_ld32(o_tm + k, x);
+#pragma unroll
+                    for (int y = 0; y < 32; y += 8)
+                        *reinterpret_cast<uint4*>(buf + sw128_tile(128, r, 2 * (D / 2 * half + k + y))) = make_uint4(
+                            pack_bf16(x[y] * a.scale, x[y + 1] * a.scale), pack_bf16(x[y + 2] * a.scale, x[y + 3] * a.scale),
+                            pack_bf16(x[y + 4] * a.scale, x[y + 5] * a.scale), pack_bf16(x[y + 6] * a.scale, x[y + 7] * a.scale));
+                }
+                fence_async_smem();
+                fence_before_sync();
+                named_sync(1, 256);
+                if (tid == 0) {
+                    mbar_arrive_n(&bar.oempty, 8);
+                    for (int h = 0; h < HALVES; ++h)
+                        tma_store_3d(&maps.dq, buf + h * (128 * 128), 64 * h, job.unit * sh.heads, t.row0);
+                    tma_store_wait<true>();
+                    mbar_arrive(&bar.vempty[slot]);
+                }
+                __syncwarp();
+                ++cv;
+            } else {
+                store_row<D / 2>(o_tm, a.scale, live, static_cast<__nv_bfloat16*>(a.dq) + row * D + D / 2 * half);
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.oempty);
+            }
+            cv += n;
+            done += n;
         }
+        if (tid == 0) tma_store_wait<false>();
+        __syncwarp();
     }
     fence_before_sync();
     __syncthreads();
@@ -564,15 +727,19 @@ template <int D> cudaError_t backward(const AttnArgs& a, cudaStream_t stream)
     if (e == cudaSuccess) e = encode_heads(&maps.k, a.k, a.T, a.Hk, D, a.k_stride, 1, kTcKeys);
     if (e == cudaSuccess) e = encode_heads(&maps.v, a.v, a.T, a.Hk, D, a.v_stride, 1, kTcKeys);
     if (e != cudaSuccess) return e;
+    QMaps qmaps = {maps.q, maps.dout, maps.k, maps.v, maps.q};
+    e = encode_heads(&qmaps.dq, a.dq, a.T, a.Hq, D, (int64_t)a.Hq * D, sh.heads, sh.tokens);
+    if (e != cudaSuccess) return e;
     const int64_t kv = attn_tiles(a.N, a.T, kTcKeys) * a.Hk, q = attn_tiles(a.N, a.T, sh.tokens) * sh.units;
     if (kv > INT32_MAX || q > INT32_MAX) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> set_kv{0}, set_q{0};
     e = allow_smem(attn_bwd_kv_tc_kernel<D>, C::SMEM, &set_kv);
-    if (e == cudaSuccess) e = allow_smem(attn_bwd_q_tc_kernel<D>, C::SMEM, &set_q);
+    if (e == cudaSuccess) e = allow_smem(attn_bwd_q_tc_kernel<D>, CfgQ<D>::SMEM, &set_q);
     if (e != cudaSuccess) return e;
     e = launch_after(attn_bwd_kv_tc_kernel<D>, launch_config(kv, C::NT, C::SMEM), stream, a, sh, maps);
     if (e != cudaSuccess) return e;
-    return launch_after(attn_bwd_q_tc_kernel<D>, launch_config(q, C::NT, C::SMEM), stream, a, sh, maps);
+    return launch_after(attn_bwd_q_tc_kernel<D>, launch_config(q < sm_count() ? q : sm_count(), CfgQ<D>::NT, CfgQ<D>::SMEM),
+                        stream, a, sh, (int32_t)q, qmaps);
 }
 
 }  // namespace

@@ -338,21 +338,51 @@ template <typename T, int D> __global__ void __launch_bounds__(256) attn_join_ke
 }
 
 // ---------------------------------------------------------------- backward
-// delta = do . o of every row, a warp a row.
-template <typename T, int D> __global__ void __launch_bounds__(256) attn_delta_kernel(AttnArgs a)
+__device__ __forceinline__ float dot16(const uint4& x, const uint4& y, float)
 {
-    constexpr int C = D / 32;
-    wait_for_previous();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.T * a.Hq) return;
-    const T *x = static_cast<const T*>(a.dout) + row * D + C * lane, *y = static_cast<const T*>(a.out) + row * D + C * lane;
+    const float4 *a = reinterpret_cast<const float4*>(&x), *b = reinterpret_cast<const float4*>(&y);
+    return fmaf(a->x, b->x, fmaf(a->y, b->y, fmaf(a->z, b->z, a->w * b->w)));
+}
+__device__ __forceinline__ float dot16(const uint4& x, const uint4& y, __nv_bfloat16)
+{
+    const uint32_t *a = &x.x, *b = &y.x;
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < C; ++i) s = fmaf(load_as_float(x + i), load_as_float(y + i), s);
+    for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16), s);
+        s = fmaf(__uint_as_float(a[i] & 0xffff0000u), __uint_as_float(b[i] & 0xffff0000u), s);
+    }
+    return s;
+}
+// delta = do . o of every row: 16 bytes a lane, kDeltaRows times as many rows as a warp's lanes
+// cover in flight (HBM-bound).
+constexpr int kDeltaRows = 4;
+template <typename T, int D> struct Delta {
+    static constexpr int LANES = D * sizeof(T) / 16, PER_WARP = 32 / LANES * kDeltaRows;
+    static constexpr int PER_BLOCK = 8 * PER_WARP;
+};
+template <typename T, int D> __global__ void __launch_bounds__(256) attn_delta_kernel(AttnArgs a)
+{
+    using C = Delta<T, D>;
+    wait_for_previous();
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = (int64_t)a.T * a.Hq;
+    const int64_t row0 = (int64_t)blockIdx.x * C::PER_BLOCK + (threadIdx.x >> 5) * C::PER_WARP + lane / C::LANES;
+    uint4 x[kDeltaRows], y[kDeltaRows];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) a.delta[row] = s;
+    for (int k = 0; k < kDeltaRows; ++k) {
+        const int64_t r = min(row0 + k * (32 / C::LANES), rows - 1) * C::LANES + lane % C::LANES;
+        x[k] = static_cast<const uint4*>(a.dout)[r];
+        y[k] = static_cast<const uint4*>(a.out)[r];
+    }
+#pragma unroll
+    for (int k = 0; k < kDeltaRows; ++k) {
+        float s = dot16(x[k], y[k], T());
+#pragma unroll
+        for (int o = C::LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        const int64_t r = row0 + k * (32 / C::LANES);
+        if (lane % C::LANES == 0 && r < rows) a.delta[r] = s;
+    }
 }
 
 constexpr int kBwdRows = 64;                   // rows of a backward tile
@@ -548,6 +578,12 @@ template <int D> cudaError_t forward(const AttnArgs& a, cudaStream_t stream)
     return launch_after(kern, launch_config(ctas, kThreads, Fwd<D>::SMEM), stream, a, sh);
 }
 
+template <typename T, int D> cudaError_t delta(const AttnArgs& a, cudaStream_t stream)
+{
+    const int64_t rows = (int64_t)a.T * a.Hq, per = Delta<T, D>::PER_BLOCK;
+    return launch_after(attn_delta_kernel<T, D>, launch_config((rows + per - 1) / per, 256), stream, a);
+}
+
 template <int D> cudaError_t backward(const AttnArgs& a, cudaStream_t stream)
 {
     const AttnShape sh = attn_shape(kBwdRows, a.Hq, a.Hk);
@@ -601,12 +637,9 @@ cudaError_t launch_attention_bwd(const AttnArgs& args, cudaStream_t stream)
 {
     AttnArgs a = args;
     a.delta = static_cast<float*>(a.workspace);
-    const cudaLaunchConfig_t cfg = launch_config(((int64_t)a.T * a.Hq + 7) / 8, 256);
     const cudaError_t e =
-        a.bf16 ? a.D == 64 ? launch_after(attn_delta_kernel<__nv_bfloat16, 64>, cfg, stream, a)
-                           : launch_after(attn_delta_kernel<__nv_bfloat16, 128>, cfg, stream, a)
-        : a.D == 64 ? launch_after(attn_delta_kernel<float, 64>, cfg, stream, a)
-                    : launch_after(attn_delta_kernel<float, 128>, cfg, stream, a);
+        a.bf16 ? a.D == 64 ? delta<__nv_bfloat16, 64>(a, stream) : delta<__nv_bfloat16, 128>(a, stream)
+        : a.D == 64 ? delta<float, 64>(a, stream) : delta<float, 128>(a, stream);
     if (e != cudaSuccess) return e;
     if (a.bf16) return launch_attention_bwd_tc(a, stream);
     return a.D == 64 ? backward<64>(a, stream) : backward<128>(a, stream);

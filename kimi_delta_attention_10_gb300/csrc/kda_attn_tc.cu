@@ -46,12 +46,6 @@ struct Maps {
     CUtensorMap q, k, v, out;
 };
 
-// A CTA's next tile of rows, from the producer to the other roles.
-struct Job {
-    AttnTile t;
-    int32_t unit, piece, found;
-};
-
 struct Bars {
     uint64_t full[8], empty[8];        // ring slots
     uint64_t qfull[2], qempty[2];
@@ -63,7 +57,7 @@ struct Bars {
     uint64_t drain;
     uint32_t tmem;
     int32_t abort;
-    Job job[2];
+    AttnJob job[2];
 };
 
 // What a job is for each of its two tiles of rows.
@@ -72,7 +66,7 @@ struct Plan {
     int32_t n[2], steps;               // key tiles in this piece, and the most of them
     int32_t all, j0;                   // keys that any row sees, first key tile
     bool slot[2];                      // the rows leave through a ring slot
-    __device__ __forceinline__ Plan(const AttnArgs& a, const AttnShape& sh, const Job& job)
+    __device__ __forceinline__ Plan(const AttnArgs& a, const AttnShape& sh, const AttnJob& job)
     {
         const AttnTile& t = job.t;
         tokens[0] = min(t.tokens, sh.tokens);
@@ -175,16 +169,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
             const uint32_t qbytes = (uint32_t)sh.tokens * sh.heads * 128 * HALVES;
             uint32_t c = 0, loads[2] = {0, 0};
             for (int32_t round = 0; !wait.dead(); ++round) {
-                // to and fro over the CTAs, since the work falls
-                const int64_t at = (int64_t)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-                Job job;
-                job.found = 0;
-                if (at < jobs) {
-                    const int32_t rest = (int32_t)at / a.splits;
-                    job.piece = (int32_t)at - rest * a.splits;
-                    job.unit = rest % sh.units;
-                    job.found = walk.next(a, rest / sh.units, job.t);
-                }
+                const AttnJob job = attn_job(walk, a, sh, jobs, round);
                 wait(&bar.jempty[round & 1], ((round >> 1) & 1) ^ 1);
                 if (lane == 0) bar.job[round & 1] = job;
                 __syncwarp();
@@ -267,7 +252,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
             for (int32_t round = 0;; ++round) {
                 wait(&bar.jfull[round & 1], (round >> 1) & 1);
                 if (wait.dead()) break;
-                const Job& job = bar.job[round & 1];
+                const AttnJob& job = bar.job[round & 1];
                 if (!job.found) break;
                 const Plan p(a, sh, job);
                 __syncwarp();
@@ -361,7 +346,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
         for (int32_t round = 0;; ++round) {
             wait(&bar.jfull[round & 1], (round >> 1) & 1);
             if (wait.dead()) break;
-            const Job job = bar.job[round & 1];
+            const AttnJob job = bar.job[round & 1];
             if (!job.found) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);

@@ -184,6 +184,28 @@ inline cudaError_t encode_heads(CUtensorMap* m, const void* base, int64_t T, int
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// A CTA's next tile of rows, from the warp that walks over them to the other roles.
+struct AttnJob {
+    AttnTile t;
+    int32_t unit, piece, found;
+};
+// The CTA's round-th job of `jobs`, by a whole warp: to and fro over the CTAs, since the work
+// falls from job to job.
+__device__ __forceinline__ AttnJob attn_job(AttnWalk& walk, const AttnArgs& a, const AttnShape& sh, int32_t jobs,
+                                            int32_t round)
+{
+    const int64_t at = (int64_t)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    AttnJob job;
+    job.found = 0;
+    if (at < jobs) {
+        const int32_t rest = (int32_t)at / a.splits;
+        job.piece = (int32_t)at - rest * a.splits;
+        job.unit = rest % sh.units;
+        job.found = walk.next(a, rest / sh.units, job.t);
+    }
+    return job;
+}
+
 // Whether a kernel was given exactly the registers a thread that its setmaxnreg counts on:
 // with fewer, the threads that ask for more would wait for good.
 template <typename K> cudaError_t check_registers(K kern, int registers)
