@@ -114,70 +114,103 @@ __device__ __forceinline__ int32_t attn_deeper(int32_t m, int32_t L, int32_t nt,
 
 // The tiles of a call in the order of falling work, walked by one whole warp: next(item) for
 // rising items.  Tiles that have the same number of key tiles are a level; a walk keeps its
-// place in one, so that a call with thousands of short sequences looks at each once.
+// place in one, so that a call with thousands of short sequences looks at each once.  The
+// first 32 sequences stay in the lanes' registers: a look at memory takes several hundred
+// cycles beside the products.
 struct AttnWalk {
     int32_t tokens, key_shift;
     bool bad;                // bad offsets (reported): there are no tiles
     int32_t level;           // tiles of `level` key tiles
     int32_t first, behind;   // the level's first item, and the next one's
     int32_t base, passed;    // sequences from `base` on; items of the level before them
+    struct Sequence {
+        int32_t c0, m, L, nt;        // first packed token, tokens, keys, tiles
+    } mine;                  // of sequence `lane`
 
-    __device__ __forceinline__ int32_t tiles(const AttnArgs& a, int32_t n) const
+    __device__ __forceinline__ Sequence look(const AttnArgs& a, int32_t n) const
     {
-        return (int32_t)(((uint32_t)(a.cu[n + 1] - a.cu[n]) + tokens - 1) / (uint32_t)tokens);
+        Sequence s;
+        s.c0 = a.cu[n];
+        s.m = a.cu[n + 1] - s.c0;
+        s.L = attn_kv_len(a, n, s.m);
+        s.nt = (int32_t)(((uint32_t)s.m + tokens - 1) / (uint32_t)tokens);
+        return s;
     }
-    // tiles of sequence n that have more than d key tiles
-    __device__ __forceinline__ int32_t count(const AttnArgs& a, int32_t n, int32_t d) const
+    // the sequence base + lane; none: without tiles
+    __device__ __forceinline__ Sequence at(const AttnArgs& a, int32_t base_) const
     {
-        const int32_t m = a.cu[n + 1] - a.cu[n], nt = tiles(a, n);
-        return nt - attn_deeper(m, attn_kv_len(a, n, m), nt, a.causal, tokens, key_shift, d);
+        const int32_t n = base_ + (threadIdx.x & 31);
+        return base_ == 0 ? mine : n < a.N ? look(a, n) : Sequence{0, 0, 0, 0};
+    }
+    // its tiles that have more than d key tiles
+    __device__ __forceinline__ int32_t count(const AttnArgs& a, const Sequence& s, int32_t d) const
+    {
+        return s.nt - attn_deeper(s.m, s.L, s.nt, a.causal, tokens, key_shift, d);
     }
     __device__ __forceinline__ int32_t total(const AttnArgs& a, int32_t d) const
     {
-        int32_t s = 0;
-        for (int32_t n = threadIdx.x & 31; n < a.N; n += 32) s += count(a, n, d);
-        return (int32_t)__reduce_add_sync(0xffffffffu, (unsigned)s);
+        int32_t x = count(a, mine, d);
+        for (int32_t b = 32; b < a.N; b += 32) x += count(a, at(a, b), d);
+        return (int32_t)__reduce_add_sync(0xffffffffu, (unsigned)x);
     }
     __device__ __forceinline__ AttnWalk(const AttnArgs& a, int32_t tile_tokens, int shift)
-        : tokens(tile_tokens), key_shift(shift), bad(false), level(0), first(0), behind(0), base(0), passed(0)
+        : tokens(tile_tokens), key_shift(shift), bad(false), level(0), first(0), behind(0), base(0), passed(0),
+          mine{0, 0, 0, 0}
     {
+        const int lane = threadIdx.x & 31;
         int32_t deepest = 0;
-        for (int32_t n = threadIdx.x & 31; n < a.N; n += 32) {
-            const int32_t c0 = a.cu[n], c1 = a.cu[n + 1];
-            bad |= c0 < 0 || c1 < c0 || c1 > a.T || (n == 0 && c0 != 0);
-            deepest = max(deepest, attn_kv_len(a, n, c1 - c0));
+        for (int32_t n = lane; n < a.N; n += 32) {
+            const int32_t c1 = a.cu[n + 1];
+            const Sequence s = look(a, n);
+            bad |= s.c0 < 0 || s.m < 0 || c1 > a.T || (n == 0 && s.c0 != 0);
+            deepest = max(deepest, s.L);
+            if (n == lane) mine = s;
         }
         bad = __any_sync(0xffffffffu, bad);
-        if (bad && (threadIdx.x & 31) == 0) report_status(a.status, KDA_ERR_DEVICE_ARG);
+        if (bad && lane == 0) report_status(a.status, KDA_ERR_DEVICE_ARG);
         deepest = __reduce_max_sync(0xffffffffu, deepest);
         level = (int32_t)(((int64_t)deepest + (1 << key_shift) - 1) >> key_shift) + 1;   // above the first
     }
     // false: there is no such tile
     __device__ __forceinline__ bool next(const AttnArgs& a, int32_t item, AttnTile& t)
     {
-        const int lane = threadIdx.x & 31;
         if (bad) return false;
         if (item >= behind) {
-            // the least d with at most `item` tiles of more than d key tiles: the item has d itself
-            int32_t lo = 0, hi = level - 1;
+            // The item has the least d with at most `item` tiles of more than d key tiles; level - 1
+            // is one.  Down from there in growing steps, then by halves.
+            int32_t hi = level - 1, hi_total = behind, lo = hi - 1, step = 1;
             if (hi < 0) return false;
-            while (lo < hi) {
-                const int32_t mid = (lo + hi) >> 1;
-                if (total(a, mid) <= item) hi = mid;
-                else lo = mid + 1;
+            int32_t lo_total = total(a, lo);
+            while (lo_total <= item) {
+                if (lo < 0) return false;
+                hi = lo;
+                hi_total = lo_total;
+                step *= 2;
+                lo = max(hi - step, -1);
+                lo_total = total(a, lo);
             }
-            level = lo;
-            first = total(a, lo);
-            behind = total(a, lo - 1);
+            while (hi - lo > 1) {
+                const int32_t mid = (lo + hi) >> 1, x = total(a, mid);
+                if (x <= item) {
+                    hi = mid;
+                    hi_total = x;
+                } else {
+                    lo = mid;
+                    lo_total = x;
+                }
+            }
+            level = hi;
+            first = hi_total;
+            behind = lo_total;
             base = passed = 0;
-            if (item >= behind) return false;
         }
         int32_t rank = item - first - passed;
+        const int lane = threadIdx.x & 31;
         for (;; base += 32) {
             if (base >= a.N) return false;             // lengths that changed meanwhile
-            const int32_t n = base + lane;
-            const int32_t mine = n < a.N ? count(a, n, level - 1) - count(a, n, level) : 0;
-            int32_t upto = mine;
+            const Sequence s = at(a, base);
+            const int32_t tiles = count(a, s, level - 1) - count(a, s, level);
+            int32_t upto = tiles;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
@@ -185,18 +218,18 @@ struct AttnWalk {
             }
             const unsigned past = __ballot_sync(0xffffffffu, upto > rank);
             if (past) {
-                const int at = __ffs(past) - 1;
-                rank -= __shfl_sync(0xffffffffu, upto - mine, at);
-                const int32_t who = base + at, c0 = a.cu[who], m = a.cu[who + 1] - c0;
-                const int32_t L = attn_kv_len(a, who, m);
-                t.n = who;
-                t.index = attn_deeper(m, L, tiles(a, who), a.causal, tokens, key_shift, level - 1) + rank;
-                t.seq0 = c0;
+                const int who = __ffs(past) - 1;
+                auto of = [&](int32_t x) { return __shfl_sync(0xffffffffu, x, who); };
+                rank -= of(upto - tiles);
+                const int32_t begin = of(s.nt - count(a, s, level - 1)), m = of(s.m);
+                t.n = base + who;
+                t.index = begin + rank;
+                t.seq0 = of(s.c0);
                 t.seq_tokens = m;
-                t.row0 = c0 + t.index * tokens;
+                t.row0 = t.seq0 + t.index * tokens;
                 t.tokens = min(tokens, m - t.index * tokens);
-                t.kv_len = L;
-                t.pos0 = L - m + t.index * tokens;
+                t.kv_len = of(s.L);
+                t.pos0 = t.kv_len - m + t.index * tokens;
                 return true;
             }
             const int32_t all = __shfl_sync(0xffffffffu, upto, 31);

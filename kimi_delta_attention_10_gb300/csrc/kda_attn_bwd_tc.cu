@@ -394,7 +394,7 @@ template <int D> struct CfgQ {
     static constexpr uint32_t OFF_K = 2 * TILE, OFF_V = OFF_K + KS * TILE, OFF_BAR = OFF_V + VS * TILE,
                               SMEM = OFF_BAR + 512 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
-    static constexpr int NT = 320, WARP_LOAD = 8, WARP_MMA = 9;
+    static constexpr int NT = 352, WARP_LOAD = 8, WARP_MMA = 9, WARP_STORE = 10;
     static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DQ = 384;      // two buffers of dP
 };
 
@@ -403,7 +403,7 @@ struct QBars {
     uint64_t kfull[4], kempty[4], vfull[4], vempty[4];         // ring slots
     uint64_t sfull, sempty;
     uint64_t dpfull[2], dsfull[2];     // dP, dS in its place
-    uint64_t ofull, oempty;            // dq added up, read
+    uint64_t ofull, oempty, staged;    // dq added up, read, in its ring slot
     uint64_t jfull[2], jempty[2];
     uint64_t drain;
     uint32_t tmem;
@@ -435,15 +435,20 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
             mbar_init(&bar.dpfull[i], 1);
             mbar_init(&bar.dsfull[i], 8);
             mbar_init(&bar.jfull[i], 1);
-            mbar_init(&bar.jempty[i], 9);
+            mbar_init(&bar.jempty[i], 10);
         }
         mbar_init(&bar.sfull, 1);
         mbar_init(&bar.sempty, 8);
         mbar_init(&bar.ofull, 1);
         mbar_init(&bar.oempty, 8);
+        mbar_init(&bar.staged, 8);
         mbar_init(&bar.drain, 1);
         bar.abort = 0;
         fence_mbar_init();
+        prefetch_map(&maps.q);
+        prefetch_map(&maps.dout);
+        prefetch_map(&maps.k);
+        prefetch_map(&maps.v);
     }
     wait_for_previous();
     if (warp == C::WARP_MMA) {
@@ -529,39 +534,48 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
             if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);
             auto keys_full = [&](uint32_t i) { wait(&bar.kfull[(done + i) % KS], ((done + i) / KS) & 1); };
             auto values_full = [&](uint32_t i) { wait(&bar.vfull[(cv + i) % VS], ((cv + i) / VS) & 1); };
-            // S, then dP, of key tile i
-            auto scores = [&](int x, int32_t i) {
+            // S, then dP, of key tile i.  The looks at barriers are issued among the products
+            // before those that need them: one takes 200 cycles beside them.
+            bool weights = false;
+            auto scores = [&](int x, int32_t i, int32_t look) {
                 if (x == 0) wait(&bar.sempty, ((done + i) & 1) ^ 1);
                 if (wait.dead()) return;
                 fence_after_sync();
-                const uint64_t p = desc_advance(dA, x * C::TILE), 
+                const uint64_t p = desc_advance(dA, x * C::TILE),
                                q = x ? desc_advance(dV, (cv + i) % VS * C::TILE) : desc_advance(dK, (done + i) % KS * C::TILE);
                 const uint32_t d = tmem + (x ? C::TM_DP + ((done + i) & 1) * 128 : C::TM_S);
 #pragma unroll
-                for (uint32_t s = 0; s < D / 16; ++s)
+                for (uint32_t s = 0; s < D / 16; ++s) {
+                    if (s == D / 32 && look >= 0) weights = mbar_test(&bar.dsfull[(done + look) & 1], ((done + look) >> 1) & 1);
                     mma_ss(lead, d, desc_advance(p, kmajor_off(128, s)), desc_advance(q, kmajor_off(128, s)), id_s, s > 0);
+                }
                 commit_if(lead, x ? &bar.dpfull[(done + i) & 1] : &bar.sfull);
                 if (x) commit_if(lead, &bar.vempty[(cv + i) % VS]);
                 if (i + 1 == n) commit_if(lead, &bar.aempty[x]);
             };
             wait(&bar.afull[0], round & 1);
             keys_full(0);
-            scores(0, 0);
+            scores(0, 0, -1);
             wait(&bar.afull[1], round & 1);
             values_full(0);
-            scores(1, 0);
+            scores(1, 0, -1);
             if (n > 1) {
                 keys_full(1);
                 values_full(1);
             }
             for (int32_t i = 0; i < n; ++i) {
+                weights = false;
                 if (i + 1 < n) {
-                    scores(0, i + 1);
-                    scores(1, i + 1);
+                    scores(0, i + 1, -1);
+                    scores(1, i + 1, i);
                 }
                 if (i == 0) wait(&bar.oempty, (round & 1) ^ 1);
                 const uint32_t b = (done + i) & 1;
-                wait(&bar.dsfull[b], ((done + i) >> 1) & 1);
+                wait(weights, &bar.dsfull[b], ((done + i) >> 1) & 1);
+                // the next step's tiles, while this product runs
+                const bool more = i + 2 < n;
+                const bool k_there = !more || mbar_test(&bar.kfull[(done + i + 2) % KS], ((done + i + 2) / KS) & 1);
+                const bool v_there = !more || mbar_test(&bar.vfull[(cv + i + 2) % VS], ((cv + i + 2) / VS) & 1);
                 if (!wait.dead()) {
                     fence_after_sync();
                     const uint64_t q = desc_advance(dN, (done + i) % KS * C::TILE);
@@ -581,10 +595,9 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
                     commit_if(lead, &bar.kempty[(done + i) % KS]);
                     if (i + 1 == n) commit_if(lead, &bar.ofull);
                 }
-                // the next step's tiles, while this product runs
-                if (i + 2 < n) {
-                    keys_full(i + 2);
-                    values_full(i + 2);
+                if (more) {
+                    wait(k_there, &bar.kfull[(done + i + 2) % KS], ((done + i + 2) / KS) & 1);
+                    wait(v_there, &bar.vfull[(cv + i + 2) % VS], ((cv + i + 2) / VS) & 1);
                 }
             }
             cv += n + slot;
@@ -592,6 +605,32 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
         }
         commit_if(lead, &bar.drain);                   // no MMA outlives the loop
         mbar_wait(&bar.drain, 0);
+        __syncwarp();
+    } else if (warp == C::WARP_STORE) {
+        // ------------------------------------------------------------ gradients from their ring slots
+        uint32_t cv = 0, count = 0;
+        for (int32_t round = 0;; ++round) {
+            wait(&bar.jfull[round & 1], (round >> 1) & 1);
+            if (wait.dead()) break;
+            const AttnJob job = bar.job[round & 1];
+            if (!job.found) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);
+            cv += (attn_keys(a, job.t) + kTcKeys - 1) >> kTcKeyShift;
+            if (job.t.tokens != sh.tokens) continue;
+            wait(&bar.staged, count++ & 1);
+            if (wait.dead()) break;
+            if (lane == 0) {
+                for (int h = 0; h < HALVES; ++h)
+                    tma_store_3d(&maps.dq, sm + C::OFF_V + cv % VS * C::TILE + h * (128 * 128), 64 * h,
+                                 job.unit * sh.heads, job.t.row0);
+                tma_store_wait<true>();
+                mbar_arrive(&bar.vempty[cv % VS]);
+            }
+            __syncwarp();
+            ++cv;
+        }
+        if (lane == 0) tma_store_wait<false>();
         __syncwarp();
     } else {
         // ------------------------------------------------------------ P and dS
@@ -685,28 +724,19 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
                             pack_bf16(x[y + 4] * a.scale, x[y + 5] * a.scale), pack_bf16(x[y + 6] * a.scale, x[y + 7] * a.scale));
                 }
                 fence_async_smem();
-                fence_before_sync();
-                named_sync(1, 256);
-                if (tid == 0) {
-                    mbar_arrive_n(&bar.oempty, 8);
-                    for (int h = 0; h < HALVES; ++h)
-                        tma_store_3d(&maps.dq, buf + h * (128 * 128), 64 * h, job.unit * sh.heads, t.row0);
-                    tma_store_wait<true>();
-                    mbar_arrive(&bar.vempty[slot]);
-                }
-                __syncwarp();
                 ++cv;
             } else {
                 store_row<D / 2>(o_tm, a.scale, live, static_cast<__nv_bfloat16*>(a.dq) + row * D + D / 2 * half);
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.oempty);
+            }
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bar.oempty);
+                if (t.tokens == sh.tokens) mbar_arrive(&bar.staged);
             }
             cv += n;
             done += n;
         }
-        if (tid == 0) tma_store_wait<false>();
-        __syncwarp();
     }
     fence_before_sync();
     __syncthreads();

@@ -35,7 +35,7 @@ template <int D> struct Cfg {
     static constexpr int NS = D == 128 ? 5 : 8;                // ring slots: 160, 128 KB
     static constexpr uint32_t OFF_KV = 2 * QTILE, OFF_BAR = OFF_KV + NS * SLOT, SMEM = OFF_BAR + 512 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
-    static constexpr int NT = 384, WARP_LOAD = 8, WARP_MMA = 9;
+    static constexpr int NT = 384, WARP_LOAD = 8, WARP_MMA = 9, WARP_STORE = 10;   // and 11
     // registers of a thread: at launch, then of the softmax's threads, of the others
     static constexpr int REGS = 168, REGS_SOFTMAX = 216, REGS_OTHER = 72;
     static_assert(2 * REGS_SOFTMAX + REGS_OTHER <= 3 * REGS, "registers of the block");
@@ -53,6 +53,7 @@ struct Bars {
     uint64_t pfull[2];                 // P in its place
     uint64_t ofull[2];                 // product with V done
     uint64_t oempty[2];                // O read
+    uint64_t staged[2];                // and in its ring slot
     uint64_t jfull[2], jempty[2];
     uint64_t drain;
     uint32_t tmem;
@@ -137,12 +138,17 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
             mbar_init(&bar.pfull[i], 4);
             mbar_init(&bar.ofull[i], 1);
             mbar_init(&bar.oempty[i], 4);
+            mbar_init(&bar.staged[i], 4);
             mbar_init(&bar.jfull[i], 1);
-            mbar_init(&bar.jempty[i], 9);
+            mbar_init(&bar.jempty[i], 11);
         }
         mbar_init(&bar.drain, 1);
         bar.abort = 0;
         fence_mbar_init();
+        prefetch_map(&maps.q);
+        prefetch_map(&maps.k);
+        prefetch_map(&maps.v);
+        prefetch_map(&maps.out);
     }
     wait_for_previous();
     if (warp == C::WARP_MMA) {
@@ -261,26 +267,34 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                 auto emptied = [&](uint32_t i) {
                     if (!wait.dead()) commit_if(lead, &bar.empty[(c + i) % NS]);
                 };
-                auto scores = [&](int m, int32_t i) {
-                    if (wait.dead()) return;
+                // The products fill shared memory's bandwidth, and a look at a barrier takes 200
+                // cycles beside them: the looks are issued among the products before those that
+                // need them, and only what was too early is waited for.
+                auto weights_there = [&](int m, int32_t i) {
+                    return mbar_test(&bar.pfull[m], (done[m] + i) & 1);
+                };
+                auto tile_there = [&](int32_t i) {
+                    return i >= 2 * p.steps || mbar_test(&bar.full[(c + i) % NS], ((c + i) / NS) & 1);
+                };
+                // S of key tile i; halfway, a look at the weights of the other tile of rows
+                auto scores = [&](int m, int32_t i, int32_t other) {
+                    bool seen = false;
+                    if (wait.dead()) return seen;
                     fence_after_sync();
-                    const uint32_t at = (c + 2 * i) % NS * C::SLOT;
-                    const uint64_t q = desc_advance(dQ, m * C::QTILE), k = desc_advance(dK, at);
+                    const uint64_t q = desc_advance(dQ, m * C::QTILE), k = desc_advance(dK, (c + 2 * i) % NS * C::SLOT);
 #pragma unroll
-                    for (uint32_t s = 0; s < D / 16; ++s)
+                    for (uint32_t s = 0; s < D / 16; ++s) {
+                        if (s == D / 32 && other >= 0) seen = weights_there(m ^ 1, other);
                         mma_ss(lead, tmem + C::TM_S + m * kTcKeys, desc_advance(q, kmajor_off(kTcRows, s)),
                                desc_advance(k, kmajor_off(kTcKeys, s)), id_s, s > 0);
+                    }
                     commit_if(lead, &bar.sfull[m]);
                     if (i + 1 == p.n[m]) commit_if(lead, &bar.qempty[m]);
+                    return seen;
                 };
-                // The products of S saturate shared memory's bandwidth, and a look at a barrier
-                // then takes several hundred cycles: what can be looked at beside the others is.
-                auto ready = [&](int m, int32_t i) {
-                    return (bool)__all_sync(0xffffffffu, mbar_test(&bar.pfull[m], (done[m] + i) & 1));
-                };
-                auto product = [&](int m, int32_t i, bool known) {
+                auto product = [&](int m, int32_t i, bool seen) {
                     if (i == 0) wait(&bar.oempty[m], (held[m] & 1) ^ 1);
-                    if (!known) wait(&bar.pfull[m], (done[m] + i) & 1);
+                    wait(seen, &bar.pfull[m], (done[m] + i) & 1);
                     if (wait.dead()) return;
                     fence_after_sync();
                     const uint64_t v = desc_advance(dV, (c + 2 * i + 1) % NS * C::SLOT);
@@ -302,23 +316,26 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                     if (p.n[m] == 0) continue;
                     wait(&bar.qfull[m], held[m] & 1);
                     full(0);
-                    scores(m, 0);
+                    scores(m, 0, -1);
                 }
                 if (p.steps > 0) {
                     emptied(0);
                     full(1);
                     if (p.steps > 1) full(2);
                 }
+                bool seen = false;
                 for (int32_t i = 0; i < p.steps; ++i) {
-                    if (i < p.n[0]) product(0, i, false);
-                    const bool known = i < p.n[1] && ready(1, i);
-                    if (i + 1 < p.n[0]) scores(0, i + 1);
-                    if (i < p.n[1]) product(1, i, known);
+                    // tiles of the next step: values, and the keys behind them
+                    const bool values = tile_there(2 * i + 3), keys = tile_there(2 * i + 4);
+                    if (i < p.n[0]) product(0, i, seen);
+                    seen = false;
+                    if (i + 1 < p.n[0]) seen = scores(0, i + 1, i < p.n[1] ? i : -1);
+                    if (i < p.n[1]) product(1, i, seen);
                     emptied(2 * i + 1);
-                    // the next step's tiles, while these products run
-                    if (i + 1 < p.steps) full(2 * i + 3);
-                    if (i + 2 < p.steps) full(2 * i + 4);
-                    if (i + 1 < p.n[1]) scores(1, i + 1);
+                    if (i + 1 < p.steps) wait(values, &bar.full[(c + 2 * i + 3) % NS], ((c + 2 * i + 3) / NS) & 1);
+                    if (i + 2 < p.steps) wait(keys, &bar.full[(c + 2 * i + 4) % NS], ((c + 2 * i + 4) / NS) & 1);
+                    seen = false;
+                    if (i + 1 < p.n[1]) seen = scores(1, i + 1, i + 1 < p.n[0] ? i + 1 : -1);
                     if (i + 1 < p.steps) emptied(2 * i + 2);
                 }
                 c += 2 * p.steps + p.slot[0] + p.slot[1];
@@ -330,6 +347,35 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
             }
             commit_if(lead, &bar.drain);               // no MMA outlives the loop
             mbar_wait(&bar.drain, 0);
+            __syncwarp();
+        } else {
+            // -------------------------------------------------------- outputs from their ring slots
+            const int m = warp - C::WARP_STORE;
+            uint32_t c = 0, count = 0;
+            for (int32_t round = 0;; ++round) {
+                wait(&bar.jfull[round & 1], (round >> 1) & 1);
+                if (wait.dead()) break;
+                const AttnJob job = bar.job[round & 1];
+                if (!job.found) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);
+                const Plan p(a, sh, job);
+                if (p.slot[m]) {
+                    const uint32_t at = (c + 2 * p.steps + (m ? p.slot[0] : 0)) % NS;
+                    wait(&bar.staged[m], count++ & 1);
+                    if (wait.dead()) break;
+                    if (lane == 0) {
+                        for (int h = 0; h < HALVES; ++h)
+                            tma_store_3d(&maps.out, sm + C::OFF_KV + at * C::SLOT + h * (kTcRows * 128), 64 * h,
+                                         job.unit * sh.heads, job.t.row0 + m * sh.tokens);
+                        tma_store_wait<true>();
+                        mbar_arrive(&bar.empty[at]);
+                    }
+                    __syncwarp();
+                }
+                c += 2 * p.steps + p.slot[0] + p.slot[1];
+            }
+            if (lane == 0) tma_store_wait<false>();
             __syncwarp();
         }
     } else {
@@ -473,21 +519,14 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                                            pack_bf16(x[y + 4], x[y + 5]), pack_bf16(x[y + 6], x[y + 7]));
                     }
                     fence_async_smem();
-                    fence_before_sync();
-                    named_sync(1 + m, 128);
-                    if (r == 0) {
-                        mbar_arrive_n(&bar.oempty[m], 4);
-                        for (int h = 0; h < HALVES; ++h)
-                            tma_store_3d(&maps.out, buf + h * (kTcRows * 128), 64 * h, job.unit * sh.heads,
-                                         t.row0 + m * sh.tokens);
-                        tma_store_wait<true>();
-                        mbar_arrive(&bar.empty[at % NS]);
-                    }
                 } else {
                     store_row<D>(o_tm, inv, live && sum != 0.f, y, py);
-                    fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.oempty[m]);
+                }
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bar.oempty[m]);
+                    if (slot) mbar_arrive(&bar.staged[m]);
                 }
             }
             // no weight: zeros, whatever the products gave
@@ -502,8 +541,6 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
             c += 2 * p.steps + p.slot[0] + p.slot[1];
             done += n;
         }
-        if (r == 0) tma_store_wait<false>();
-        __syncwarp();
     }
     fence_before_sync();
     __syncthreads();

@@ -53,11 +53,6 @@ __device__ __forceinline__ void commit_if(uint32_t lead, uint64_t* mbar)
         : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* m, uint32_t n)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(m)), "r"(n) : "memory");
-}
-
 // A bounded wait of a whole converged warp: it gives up for all lanes or for none, after
 // which the role's waits return at once and it works no more.  Short, since the roles' code
 // competes for the instruction cache.
@@ -84,6 +79,11 @@ struct WarpWait {
             }
         }
         gave_up = __any_sync(0xffffffffu, gave_up);
+    }
+    // with the outcome of an earlier look (mbar_test): waits where it was too early
+    __device__ __forceinline__ void operator()(bool seen, uint64_t* m, uint32_t parity)
+    {
+        if (!__all_sync(0xffffffffu, seen)) (*this)(m, parity);
     }
     __device__ __forceinline__ bool dead() const { return gave_up; }
 };
@@ -145,6 +145,12 @@ template <bool kRead> __device__ __forceinline__ void tma_store_wait()
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     if (kRead) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     else asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// Brings a tensor map to where the copies look for it.
+__device__ __forceinline__ void prefetch_map(const void* tmap)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
 }
 
 // Registers of a thread of the warps of this warpgroup from here on (all of whose warps call
