@@ -157,14 +157,14 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
         fence_async_smem();
     }
     start(bar, a, item, kTcKeys);
-    const uint32_t tmem = bar.tmem;
+    const uint32_t tmem = uniform(bar.tmem);
     BoundedWait wait(&bar.abort, a.status);
-    if (bar.found) {
+    if (uniform(bar.found)) {
         const AttnTile t = bar.tile;
         // the tile found has t.index tiles of queries before it; the one with as many behind it
         const int32_t nt = (t.seq_tokens + kTcKeys - 1) >> kTcKeyShift, key0 = (nt - 1 - t.index) << kTcKeyShift;
-        const int32_t left = t.seq_tokens - key0;                  // tokens from the first key on
-        const int32_t per = (left + sh.tokens - 1) / sh.tokens, n = per * sh.parts;
+        const int32_t left = uniform(t.seq_tokens - key0);         // tokens from the first key on
+        const int32_t per = uniform((left + sh.tokens - 1) / sh.tokens), n = per * sh.parts;
         const int32_t last = left - (per - 1) * sh.tokens;         // tokens of a part's last tile
         auto ring = [&](int x, int32_t i) { return sm + C::OFF_RING + ((i & 1) * 2 + x) * C::TILE; };
 
@@ -458,7 +458,7 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    const uint32_t tmem = bar.tmem;
+    const uint32_t tmem = uniform(bar.tmem);
     WarpWait wait(&bar.abort, a.status);
 
     if (warp == C::WARP_LOAD) {
@@ -527,9 +527,9 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
             wait(&bar.jfull[round & 1], (round >> 1) & 1);
             if (wait.dead()) break;
             const AttnJob& job = bar.job[round & 1];
-            if (!job.found) break;
-            const int32_t all = attn_keys(a, job.t), n = (all + kTcKeys - 1) >> kTcKeyShift;
-            const bool slot = job.t.tokens == sh.tokens;
+            if (!uniform(job.found)) break;
+            const int32_t all = uniform(attn_keys(a, job.t)), n = (all + kTcKeys - 1) >> kTcKeyShift;
+            const int32_t slot = uniform((int32_t)(job.t.tokens == sh.tokens));
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);
             auto keys_full = [&](uint32_t i) { wait(&bar.kfull[(done + i) % KS], ((done + i) / KS) & 1); };

@@ -158,7 +158,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    const uint32_t tmem = bar.tmem;
+    const uint32_t tmem = uniform(bar.tmem);
     WarpWait wait(&bar.abort, a.status);
 
     if (warp >= 8) {
@@ -252,98 +252,91 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
             const uint64_t dK = desc_kmajor(smem_u32(sm + C::OFF_KV), kTcKeys, 0);
             const uint64_t dV = D == 128 ? desc_mnmajor128(smem_u32(sm + C::OFF_KV), kTcKeys * 128, 0)
                                          : desc_mnmajor64(smem_u32(sm + C::OFF_KV), 0);
-            uint32_t c = 0;                            // ring slots of the jobs before
-            uint32_t done[2] = {0, 0};                 // key tiles of the jobs before, of each tile of rows
-            uint32_t held[2] = {0, 0};                 // jobs with any
+            Ring<NS> ring;
+            uint32_t done0 = 0, done1 = 0;             // key tiles of the jobs before, of each tile of rows
+            uint32_t held0 = 0, held1 = 0;             // jobs with any
             for (int32_t round = 0;; ++round) {
                 wait(&bar.jfull[round & 1], (round >> 1) & 1);
                 if (wait.dead()) break;
                 const AttnJob& job = bar.job[round & 1];
-                if (!job.found) break;
+                if (!uniform(job.found)) break;
                 const Plan p(a, sh, job);
+                const int32_t steps = uniform(p.steps), n0 = uniform(p.n[0]), n1 = uniform(p.n[1]);
+                const int32_t keys0 = uniform(p.keys[0] - (p.j0 << kTcKeyShift)),
+                              keys1 = uniform(p.keys[1] - (p.j0 << kTcKeyShift));
+                const int32_t slots = uniform((int32_t)p.slot[0] + p.slot[1]);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);
-                auto full = [&](uint32_t i) { wait(&bar.full[(c + i) % NS], ((c + i) / NS) & 1); };
-                auto emptied = [&](uint32_t i) {
-                    if (!wait.dead()) commit_if(lead, &bar.empty[(c + i) % NS]);
-                };
-                // The products fill shared memory's bandwidth, and a look at a barrier takes 200
-                // cycles beside them: the looks are issued among the products before those that
-                // need them, and only what was too early is waited for.
-                auto weights_there = [&](int m, int32_t i) {
-                    return mbar_test(&bar.pfull[m], (done[m] + i) & 1);
-                };
-                auto tile_there = [&](int32_t i) {
-                    return i >= 2 * p.steps || mbar_test(&bar.full[(c + i) % NS], ((c + i) / NS) & 1);
-                };
-                // S of key tile i; halfway, a look at the weights of the other tile of rows
-                auto scores = [&](int m, int32_t i, int32_t other) {
-                    bool seen = false;
-                    if (wait.dead()) return seen;
-                    fence_after_sync();
-                    const uint64_t q = desc_advance(dQ, m * C::QTILE), k = desc_advance(dK, (c + 2 * i) % NS * C::SLOT);
-#pragma unroll
-                    for (uint32_t s = 0; s < D / 16; ++s) {
-                        if (s == D / 32 && other >= 0) seen = weights_there(m ^ 1, other);
-                        mma_ss(lead, tmem + C::TM_S + m * kTcKeys, desc_advance(q, kmajor_off(kTcRows, s)),
-                               desc_advance(k, kmajor_off(kTcKeys, s)), id_s, s > 0);
-                    }
-                    commit_if(lead, &bar.sfull[m]);
-                    if (i + 1 == p.n[m]) commit_if(lead, &bar.qempty[m]);
-                    return seen;
-                };
-                auto product = [&](int m, int32_t i, bool seen) {
-                    if (i == 0) wait(&bar.oempty[m], (held[m] & 1) ^ 1);
-                    wait(seen, &bar.pfull[m], (done[m] + i) & 1);
-                    if (wait.dead()) return;
-                    fence_after_sync();
-                    const uint64_t v = desc_advance(dV, (c + 2 * i + 1) % NS * C::SLOT);
-                    const int32_t left = p.keys[m] - ((p.j0 + i) << kTcKeyShift);
-                    auto step = [&](uint32_t s) {
-                        mma_ts(lead, tmem + C::TM_O + m * D, tmem + C::TM_S + m * kTcKeys + 8 * s,
-                               desc_advance(v, mnmajor_off(s)), id_o, i > 0 || s > 0);
-                    };
-                    if (left >= kTcKeys) {
-#pragma unroll
-                        for (uint32_t s = 0; s < kTcKeys / 16; ++s) step(s);
-                    } else {
-#pragma unroll 1
-                        for (uint32_t s = 0; 16 * (int32_t)s < left; ++s) step(s);
-                    }
-                    commit_if(lead, &bar.ofull[m]);
-                };
-                for (int m = 0; m < 2; ++m) {
-                    if (p.n[m] == 0) continue;
-                    wait(&bar.qfull[m], held[m] & 1);
-                    full(0);
-                    scores(m, 0, -1);
-                }
-                if (p.steps > 0) {
-                    emptied(0);
-                    full(1);
-                    if (p.steps > 1) full(2);
-                }
+                // The products fill shared memory's bandwidth, and a look at a barrier takes 100 to
+                // 200 cycles beside them: the looks at weights are issued among the products before
+                // those that need them.  One copy of this code serves both tiles of rows, since the
+                // roles compete for the instruction cache.
                 bool seen = false;
-                for (int32_t i = 0; i < p.steps; ++i) {
-                    // tiles of the next step: values, and the keys behind them
-                    const bool values = tile_there(2 * i + 3), keys = tile_there(2 * i + 4);
-                    if (i < p.n[0]) product(0, i, seen);
-                    seen = false;
-                    if (i + 1 < p.n[0]) seen = scores(0, i + 1, i < p.n[1] ? i : -1);
-                    if (i < p.n[1]) product(1, i, seen);
-                    emptied(2 * i + 1);
-                    if (i + 1 < p.steps) wait(values, &bar.full[(c + 2 * i + 3) % NS], ((c + 2 * i + 3) / NS) & 1);
-                    if (i + 2 < p.steps) wait(keys, &bar.full[(c + 2 * i + 4) % NS], ((c + 2 * i + 4) / NS) & 1);
-                    seen = false;
-                    if (i + 1 < p.n[1]) seen = scores(1, i + 1, i + 1 < p.n[0] ? i + 1 : -1);
-                    if (i + 1 < p.steps) emptied(2 * i + 2);
-                }
-                c += 2 * p.steps + p.slot[0] + p.slot[1];
+                uint32_t v = 0;                        // the slot of the step's values
+                if (steps > 0) wait(&bar.full[ring.slot], ring.phase);
+#pragma unroll 1
+                for (int32_t i = -1; i < steps; ++i) {
+#pragma unroll 1
+                    for (int32_t m = 0; m < 2; ++m) {
+                        const int32_t n = m ? n1 : n0;
+                        const uint32_t s_tm = tmem + C::TM_S + m * kTcKeys, mine = (m ? done1 : done0) + i;
+                        if (i >= 0 && i < n) {
+                            if (i == 0) wait(&bar.oempty[m], ((m ? held1 : held0) & 1) ^ 1);
+                            wait(seen, &bar.pfull[m], mine & 1);
+                            if (!wait.dead()) {
+                                fence_after_sync();
+                                const uint64_t d = desc_advance(dV, v * C::SLOT);
+                                const int32_t left = (m ? keys1 : keys0) - (i << kTcKeyShift);
+                                auto step = [&](uint32_t s) {
+                                    mma_ts(lead, tmem + C::TM_O + m * D, s_tm + 8 * s, desc_advance(d, mnmajor_off(s)),
+                                           id_o, i > 0 || s > 0);
+                                };
+                                if (left >= kTcKeys) {
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    done[m] += p.n[m];
-                    held[m] += p.n[m] > 0;
+                                    for (uint32_t s = 0; s < kTcKeys / 16; ++s) step(s);
+                                } else {
+#pragma unroll 1
+                                    for (uint32_t s = 0; 16 * (int32_t)s < left; ++s) step(s);
+                                }
+                                commit_if(lead, &bar.ofull[m]);
+                            }
+                        }
+                        if (m && i >= 0 && !wait.dead()) commit_if(lead, &bar.empty[v]);
+                        seen = false;
+                        if (i + 1 < n) {
+                            if (i < 0) wait(&bar.qfull[m], (m ? held1 : held0) & 1);
+                            // halfway, a look at the weights of the other tile of rows
+                            const int32_t other = m ? i + 1 : i;
+                            const bool look = other >= 0 && other < (m ? n0 : n1);
+                            if (!wait.dead()) {
+                                fence_after_sync();
+                                const uint64_t q = desc_advance(dQ, m * C::QTILE), k = desc_advance(dK, ring.slot * C::SLOT);
+#pragma unroll
+                                for (uint32_t s = 0; s < D / 16; ++s) {
+                                    if (s == D / 32 && look) seen = mbar_test(&bar.pfull[m ^ 1], ((m ? done0 : done1) + other) & 1);
+                                    mma_ss(lead, s_tm, desc_advance(q, kmajor_off(kTcRows, s)),
+                                           desc_advance(k, kmajor_off(kTcKeys, s)), id_s, s > 0);
+                                }
+                                commit_if(lead, &bar.sfull[m]);
+                                if (i + 2 == n) commit_if(lead, &bar.qempty[m]);
+                            }
+                        }
+                    }
+                    // the step's keys, then the next one's tiles, while these products run
+                    if (i + 1 < steps) {
+                        if (!wait.dead()) commit_if(lead, &bar.empty[ring.slot]);
+                        ring.next();
+                        wait(&bar.full[ring.slot], ring.phase);
+                        v = ring.slot;
+                        ring.next();
+                        if (i + 2 < steps) wait(&bar.full[ring.slot], ring.phase);
+                    }
                 }
+                for (int32_t i = 0; i < slots; ++i) ring.next();
+                done0 += n0;
+                done1 += n1;
+                held0 += n0 > 0;
+                held1 += n1 > 0;
             }
             commit_if(lead, &bar.drain);               // no MMA outlives the loop
             mbar_wait(&bar.drain, 0);

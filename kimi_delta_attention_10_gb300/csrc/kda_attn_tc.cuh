@@ -26,6 +26,12 @@ __device__ __forceinline__ uint32_t elect_one()
 }
 // Negates A of a product (an addend of its instruction descriptor).
 constexpr uint32_t kNegateA = 1u << 13;
+// A value that all lanes have, as one the compiler knows to be uniform: the products' operands
+// then stay in uniform registers (else each product waits for moves there, 100 cycles instead
+// of the 64 that a 128 x 128 x 16 one takes).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // D[128, N] (+)= A[128, 16] B[N, 16]^T, both operands in shared memory.
 __device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
 {
@@ -86,6 +92,18 @@ struct WarpWait {
         if (!__all_sync(0xffffffffu, seen)) (*this)(m, parity);
     }
     __device__ __forceinline__ bool dead() const { return gave_up; }
+};
+
+// A role's place in a ring of N slots.
+template <int N> struct Ring {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
 };
 
 // As tc::tmem_ld32, without the wait (tmem_ld_wait).
