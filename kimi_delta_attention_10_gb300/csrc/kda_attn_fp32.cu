@@ -98,10 +98,13 @@ __device__ __forceinline__ void scores(float (&s)[R][4], const float* A, const f
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 4; ++c)
                 acc[i][c] = fma2(make_float2(x[i].x, x[i].y), make_float2(y[c].x, y[c].y), acc[i][c]);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
                 acc[i][c] = fma2(make_float2(x[i].z, x[i].w), make_float2(y[c].z, y[c].w), acc[i][c]);
-            }
     }
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -167,18 +170,20 @@ __device__ __forceinline__ float over16(float x, bool sum)
 }
 
 // ---------------------------------------------------------------- forward
-constexpr int kRows = 128;                     // rows of a forward tile
-
-template <int D> struct Fwd {
-    static constexpr int OFF_K = kRows * (D + 4), OFF_V = OFF_K + kKeys * (D + 4), OFF_P = OFF_V + kKeys * D;
+// A tile of 16 R rows: the fewer rows a call has, the smaller, down to one row a thread.
+template <int D, int R> struct Fwd {
+    static constexpr int ROWS = 16 * R;
+    static constexpr int OFF_K = ROWS * (D + 4), OFF_V = OFF_K + kKeys * (D + 4), OFF_P = OFF_V + kKeys * D;
     static constexpr int PITCH_P = kKeys + 4;
-    static constexpr uint32_t SMEM = (OFF_P + kRows * PITCH_P) * 4;
+    static constexpr uint32_t SMEM = (OFF_P + ROWS * PITCH_P) * 4;
+    static constexpr int CTAS = R <= 2 || (R == 4 && D == 64) ? 2 : 1;         // per SM
+    static_assert(CTAS * (SMEM + 1024 + 64) <= 228 * 1024, "shared memory of an SM");
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(AttnArgs a, AttnShape sh)
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads, (Fwd<D, R>::CTAS)) attn_fwd_kernel(AttnArgs a, AttnShape sh)
 {
-    using F = Fwd<D>;
+    using F = Fwd<D, R>;
     constexpr int H = D / 64;
     extern __shared__ __align__(16) float sm[];
     __shared__ AttnTile s_tile;
@@ -208,19 +213,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(AttnArgs a, AttnS
                   j1 = (int32_t)((int64_t)tiles * (piece + 1) / a.splits);
     const float c = a.scale * kLog2e;
 
-    int32_t limit[8];                          // keys that each of the thread's rows sees
-    float m[8], l[8];
-    float2 o[8][2 * H];
+    int32_t limit[R];                          // keys that each of the thread's rows sees
+    float m[R], l[R];
+    float2 o[R][2 * H];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        limit[i] = a.causal ? t.pos0 + (ty * 8 + i) / sh.heads + 1 : t.kv_len;
+    for (int i = 0; i < R; ++i) {
+        limit[i] = a.causal ? t.pos0 + (ty * R + i) / sh.heads + 1 : t.kv_len;
         m[i] = -CUDART_INF_F;
         l[i] = 0.f;
 #pragma unroll
         for (int h = 0; h < 2 * H; ++h) o[i][h] = make_float2(0.f, 0.f);
     }
     if (j0 < j1) {
-        load_rows<kRows, D>(sQ, q, a.q_stride, rows);
+        load_rows<F::ROWS, D>(sQ, q, a.q_stride, rows);
         load_keys<D, D + 4>(sK, a, k, a.k_stride, t, hk, j0 * kKeys, keys);
         cp_async_commit();
         load_keys<D, D>(sV, a, v, a.v_stride, t, hk, j0 * kKeys, keys);
@@ -229,13 +234,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(AttnArgs a, AttnS
     for (int32_t j = j0; j < j1; ++j) {
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
-        float s[8][4];
-        scores<8, D>(s, sQ, sK, ty, tx);
+        float s[R][4];
+        scores<R, D>(s, sQ, sK, ty, tx);
         __syncthreads();
         if (j + 1 < j1) load_keys<D, D + 4>(sK, a, k, a.k_stride, t, hk, (j + 1) * kKeys, keys);
         cp_async_commit();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < R; ++i) {
             float top = -CUDART_INF_F;
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
@@ -250,25 +255,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(AttnArgs a, AttnS
             for (int n = 0; n < 4; ++n) {
                 const float e = exp2f(s[i][n] - ref);
                 l[i] += e;
-                sP[(ty * 8 + i) * F::PITCH_P + tx + 16 * n] = e;
+                sP[(ty * R + i) * F::PITCH_P + tx + 16 * n] = e;
             }
 #pragma unroll
             for (int h = 0; h < 2 * H; ++h) o[i][h] = mul2(o[i][h], both(keep));
         }
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
-        accumulate<8, H, D>(o, sP, F::PITCH_P, sV, ty, tx);
+        accumulate<R, H, D>(o, sP, F::PITCH_P, sV, ty, tx);
         __syncthreads();
         if (j + 1 < j1) load_keys<D, D>(sV, a, v, a.v_stride, t, hk, (j + 1) * kKeys, keys);
         cp_async_commit();
     }
     char* ws = static_cast<char*>(a.workspace);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < R; ++i) {
         const float sum = over16(l[i], true), inv = sum == 0.f ? 0.f : 1.f / sum;
         const float ref = m[i] == -CUDART_INF_F ? 0.f : m[i];
         int32_t token, head;
-        if (!rows.at(ty * 8 + i, token, head)) continue;
+        if (!rows.at(ty * R + i, token, head)) continue;
         const int64_t r = (int64_t)token * a.Hq + head;
         const float lse = ref * kLn2 + logf(sum);
         if (a.pieces > 1) {
@@ -387,41 +392,48 @@ template <typename T, int D> __global__ void __launch_bounds__(256) attn_delta_k
 
 constexpr int kBwdRows = 64;                   // rows of a backward tile
 
+// The two tiles that a CTA keeps (keys and values, or queries and dO), and one or, where
+// shared memory has room, two stages of the two that it walks over.
 template <int D> struct Bwd {
-    static constexpr int TILE = 64 * (D + 4), PITCH_P = kKeys + 4;
-    static constexpr int OFF_DO = TILE, OFF_K = 2 * TILE, OFF_V = 3 * TILE, OFF_P = 4 * TILE,
+    static constexpr int STAGES = D == 64 ? 2 : 1;
+    static constexpr int TILE = 64 * (D + 4), PITCH_P = kKeys + 4, STATS = 2 * kBwdRows;
+    static constexpr int OFF_WALK = 2 * TILE, OFF_P = OFF_WALK + STAGES * 2 * TILE,
                          OFF_DS = OFF_P + kBwdRows * PITCH_P, OFF_L = OFF_DS + kBwdRows * PITCH_P;
-    static constexpr uint32_t SMEM = (OFF_L + 2 * kBwdRows) * 4;
+    static constexpr uint32_t SMEM = (OFF_L + STAGES * STATS) * 4;
 };
 
-// lse * log2 e and delta of a tile's rows; +infinity where a row is not in use or has no
-// weight, which gives it weights of zero.
+// lse and delta of a tile's rows, copied beside the tile; +infinity where a row is not in use.
 __device__ __forceinline__ void load_stats(float* dst, const AttnArgs& a, const RowMap& rows)
 {
     const int r = threadIdx.x;
     if (r >= kBwdRows) return;
     int32_t token, head;
-    const bool ok = rows.at(r, token, head);
-    const int64_t at = (int64_t)token * a.Hq + head;
-    const float lse = ok ? a.lse_in[at] : CUDART_INF_F;
-    dst[r] = lse == -CUDART_INF_F ? CUDART_INF_F : lse * kLog2e;
-    dst[kBwdRows + r] = ok ? a.delta[at] : 0.f;
+    if (rows.at(r, token, head)) {
+        const int64_t at = (int64_t)token * a.Hq + head;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst + r)), "l"(a.lse_in + at) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst + kBwdRows + r)), "l"(a.delta + at)
+                     : "memory");
+    } else {
+        dst[r] = CUDART_INF_F;
+        dst[kBwdRows + r] = 0.f;
+    }
 }
 
 // P and dS of a tile: rows ty * 4 + i, keys tx + 16 n.
 template <int D>
-__device__ __forceinline__ void weights(float (&p)[4][4], float (&ds)[4][4], const float* sm, const AttnArgs& a,
+__device__ __forceinline__ void weights(float (&p)[4][4], float (&ds)[4][4], const float* q, const float* dout,
+                                        const float* k, const float* v, const float* stats, const AttnArgs& a,
                                         int32_t pos0, int32_t heads, int32_t key0, int32_t end, int ty, int tx)
 {
-    using B = Bwd<D>;
     const float c = a.scale * kLog2e;
-    scores<4, D>(p, sm, sm + B::OFF_K, ty, tx);
-    scores<4, D>(ds, sm + B::OFF_DO, sm + B::OFF_V, ty, tx);
+    scores<4, D>(p, q, k, ty, tx);
+    scores<4, D>(ds, dout, v, ty, tx);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = ty * 4 + i;
         const int32_t limit = min(end, pos0 + r / heads + 1);
-        const float lse = sm[B::OFF_L + r], delta = sm[B::OFF_L + kBwdRows + r];
+        // a row without weight (lse -infinity) gives none, like one that is not in use
+        const float lse = stats[r] == -CUDART_INF_F ? CUDART_INF_F : stats[r] * kLog2e, delta = stats[kBwdRows + r];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const bool live = key0 + tx + 16 * n < limit;
@@ -429,6 +441,14 @@ __device__ __forceinline__ void weights(float (&p)[4][4], float (&ds)[4][4], con
             ds[i][n] = live ? p[i][n] * (ds[i][n] - delta) : 0.f;
         }
     }
+}
+
+// Waits for the copies of a tile, those of the next one (if any) still under way.
+template <int STAGES> __device__ __forceinline__ void landed()
+{
+    if (STAGES == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else cp_async_wait_all();
+    __syncthreads();
 }
 
 // dk and dv of 64 keys, over all rows that see them.
@@ -457,36 +477,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(AttnArgs a, At
     // the tile found has t.index tiles of queries before it; the one with as many behind it
     const int32_t nt = (t.seq_tokens + kKeys - 1) / kKeys, key0 = (nt - 1 - t.index) * kKeys;
     const int32_t end = t.seq_tokens;
-    load_keys<D, D + 4>(sm + B::OFF_K, a, static_cast<const float*>(a.k), a.k_stride, t, hk, key0, end);
-    load_keys<D, D + 4>(sm + B::OFF_V, a, static_cast<const float*>(a.v), a.v_stride, t, hk, key0, end);
+    const int32_t left = end - key0, per = (left + sh.tokens - 1) / sh.tokens, n = per * sh.parts;
+    load_keys<D, D + 4>(sm, a, static_cast<const float*>(a.k), a.k_stride, t, hk, key0, end);
+    load_keys<D, D + 4>(sm + B::TILE, a, static_cast<const float*>(a.v), a.v_stride, t, hk, key0, end);
+    auto walked = [&](int32_t i) { return sm + B::OFF_WALK + i % B::STAGES * 2 * B::TILE; };
+    auto stats = [&](int32_t i) { return sm + B::OFF_L + i % B::STAGES * B::STATS; };
+    auto load = [&](int32_t i) {
+        if (i < n) {
+            const int32_t part = i / per, at = key0 + (i - part * per) * sh.tokens;
+            const RowMap rows(sh, hk * sh.parts + part, t.seq0 + at, min(sh.tokens, end - at));
+            load_rows<kBwdRows, D>(walked(i), static_cast<const float*>(a.q), a.q_stride, rows);
+            load_rows<kBwdRows, D>(walked(i) + B::TILE, static_cast<const float*>(a.dout), (int64_t)a.Hq * D, rows);
+            load_stats(stats(i), a, rows);
+        }
+        cp_async_commit();
+    };
     float2 dk[4][2 * H], dv[4][2 * H];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int h = 0; h < 2 * H; ++h) dk[i][h] = dv[i][h] = make_float2(0.f, 0.f);
-    for (int32_t part = 0; part < sh.parts; ++part) {
-        for (int32_t at = key0; at < t.seq_tokens; at += sh.tokens) {
-            const RowMap rows(sh, hk * sh.parts + part, t.seq0 + at, min(sh.tokens, t.seq_tokens - at));
-            __syncthreads();
-            load_rows<kBwdRows, D>(sm, static_cast<const float*>(a.q), a.q_stride, rows);
-            load_rows<kBwdRows, D>(sm + B::OFF_DO, static_cast<const float*>(a.dout), (int64_t)a.Hq * D, rows);
-            load_stats(sm + B::OFF_L, a, rows);
-            cp_async_commit();
-            cp_async_wait_all();
-            __syncthreads();
-            float p[4][4], ds[4][4];
-            weights<D>(p, ds, sm, a, at, sh.heads, key0, end, ty, tx);
+    if (B::STAGES == 2) load(0);
+    for (int32_t i = 0; i < n; ++i) {
+        load(i + B::STAGES - 1);
+        landed<B::STAGES>();
+        const float *q = walked(i), *dout = q + B::TILE;
+        float p[4][4], ds[4][4];
+        weights<D>(p, ds, q, dout, sm, sm + B::TILE, stats(i), a, key0 + i % per * sh.tokens, sh.heads, key0, end, ty,
+                   tx);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    sm[B::OFF_P + (ty * 4 + i) * B::PITCH_P + tx + 16 * n] = p[i][n];
-                    sm[B::OFF_DS + (ty * 4 + i) * B::PITCH_P + tx + 16 * n] = ds[i][n];
-                }
-            __syncthreads();
-            accumulate_t<kBwdRows, H, D + 4>(dv, sm + B::OFF_P, B::PITCH_P, sm + B::OFF_DO, ty, tx);
-            accumulate_t<kBwdRows, H, D + 4>(dk, sm + B::OFF_DS, B::PITCH_P, sm, ty, tx);
-        }
+            for (int c = 0; c < 4; ++c) {
+                sm[B::OFF_P + (ty * 4 + r) * B::PITCH_P + tx + 16 * c] = p[r][c];
+                sm[B::OFF_DS + (ty * 4 + r) * B::PITCH_P + tx + 16 * c] = ds[r][c];
+            }
+        __syncthreads();
+        accumulate_t<kBwdRows, H, D + 4>(dv, sm + B::OFF_P, B::PITCH_P, dout, ty, tx);
+        accumulate_t<kBwdRows, H, D + 4>(dk, sm + B::OFF_DS, B::PITCH_P, q, ty, tx);
+        __syncthreads();
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -527,31 +556,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(AttnArgs a, Att
     __syncthreads();
     if (!s_found) return;
     const AttnTile t = s_tile;
-    const int32_t hk = unit / sh.parts, end = attn_keys(a, t);
+    const int32_t hk = unit / sh.parts, end = attn_keys(a, t), n = (end + kKeys - 1) >> kKeyShift;
     const RowMap rows(sh, unit, t.row0, t.tokens);
     load_rows<kBwdRows, D>(sm, static_cast<const float*>(a.q), a.q_stride, rows);
-    load_rows<kBwdRows, D>(sm + B::OFF_DO, static_cast<const float*>(a.dout), (int64_t)a.Hq * D, rows);
+    load_rows<kBwdRows, D>(sm + B::TILE, static_cast<const float*>(a.dout), (int64_t)a.Hq * D, rows);
     load_stats(sm + B::OFF_L, a, rows);
+    auto walked = [&](int32_t i) { return sm + B::OFF_WALK + i % B::STAGES * 2 * B::TILE; };
+    auto load = [&](int32_t i) {
+        if (i < n) {
+            load_keys<D, D + 4>(walked(i), a, static_cast<const float*>(a.k), a.k_stride, t, hk, i * kKeys, end);
+            load_keys<D, D + 4>(walked(i) + B::TILE, a, static_cast<const float*>(a.v), a.v_stride, t, hk, i * kKeys,
+                                end);
+        }
+        cp_async_commit();
+    };
     float2 dq[4][2 * H];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int h = 0; h < 2 * H; ++h) dq[i][h] = make_float2(0.f, 0.f);
-    for (int32_t key0 = 0; key0 < end; key0 += kKeys) {
-        __syncthreads();
-        load_keys<D, D + 4>(sm + B::OFF_K, a, static_cast<const float*>(a.k), a.k_stride, t, hk, key0, end);
-        load_keys<D, D + 4>(sm + B::OFF_V, a, static_cast<const float*>(a.v), a.v_stride, t, hk, key0, end);
-        cp_async_commit();
-        cp_async_wait_all();
-        __syncthreads();
+    if (B::STAGES == 2) load(0);
+    for (int32_t i = 0; i < n; ++i) {
+        load(i + B::STAGES - 1);
+        landed<B::STAGES>();
         float p[4][4], ds[4][4];
-        weights<D>(p, ds, sm, a, t.pos0, sh.heads, key0, end, ty, tx);
+        weights<D>(p, ds, sm, sm + B::TILE, walked(i), walked(i) + B::TILE, sm + B::OFF_L, a, t.pos0, sh.heads,
+                   i * kKeys, end, ty, tx);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int n = 0; n < 4; ++n) sm[B::OFF_DS + (ty * 4 + i) * B::PITCH_P + tx + 16 * n] = ds[i][n];
+            for (int c = 0; c < 4; ++c) sm[B::OFF_DS + (ty * 4 + r) * B::PITCH_P + tx + 16 * c] = ds[r][c];
         __syncthreads();
-        accumulate<4, H, D + 4>(dq, sm + B::OFF_DS, B::PITCH_P, sm + B::OFF_K, ty, tx);
+        accumulate<4, H, D + 4>(dq, sm + B::OFF_DS, B::PITCH_P, walked(i), ty, tx);
+        __syncthreads();
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -566,16 +603,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(AttnArgs a, Att
 }
 
 // ---------------------------------------------------------------- launch
-template <int D> cudaError_t forward(const AttnArgs& a, cudaStream_t stream)
+template <int D, int R> cudaError_t forward_rows(const AttnArgs& a, cudaStream_t stream)
 {
-    const AttnShape sh = attn_shape(kRows, a.Hq, a.Hk);
+    const AttnShape sh = attn_shape(16 * R, a.Hq, a.Hk);
     const int64_t ctas = attn_tiles(a.N, a.T, sh.tokens) * sh.units * a.splits;
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-    auto kern = attn_fwd_kernel<D>;
+    auto kern = attn_fwd_kernel<D, R>;
     static std::atomic<uint64_t> set{0};
-    const cudaError_t e = allow_smem(kern, Fwd<D>::SMEM, &set);
+    const cudaError_t e = allow_smem(kern, Fwd<D, R>::SMEM, &set);
     if (e != cudaSuccess) return e;
-    return launch_after(kern, launch_config(ctas, kThreads, Fwd<D>::SMEM), stream, a, sh);
+    return launch_after(kern, launch_config(ctas, kThreads, Fwd<D, R>::SMEM), stream, a, sh);
+}
+// Rows a thread, by the rows that a group has in a sequence of average length.
+int rows_per_thread(int32_t N, int32_t T, int32_t Hq, int32_t Hk)
+{
+    const int64_t rows = ((int64_t)T + N - 1) / N * (Hq / Hk);
+    return rows > 64 ? 8 : rows > 32 ? 4 : rows > 16 ? 2 : 1;
+}
+
+template <int D> cudaError_t forward(const AttnArgs& a, cudaStream_t stream)
+{
+    switch (rows_per_thread(a.N, a.T, a.Hq, a.Hk)) {
+        case 1: return forward_rows<D, 1>(a, stream);
+        case 2: return forward_rows<D, 2>(a, stream);
+        case 4: return forward_rows<D, 4>(a, stream);
+        default: return forward_rows<D, 8>(a, stream);
+    }
 }
 
 template <typename T, int D> cudaError_t delta(const AttnArgs& a, cudaStream_t stream)
@@ -612,13 +665,16 @@ cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t stream)
                      : launch_after(attn_join_kernel<float, 128>, cfg, stream, a);
 }
 
+// Pieces of two key tiles at least: as many as fill the GPU once on the tensor cores; twice in
+// FP32, where a tile takes long enough that the longest of a causal call would be waited for
+// (1024 tokens, 16 heads of 64 channels: 139 us in one piece, 89 and 8 for the join in two).
 int32_t attn_splits(bool bf16, int32_t N, int32_t T, int32_t Hq, int32_t Hk, int32_t D, int64_t kv_most)
 {
-    const AttnShape sh = attn_shape(bf16 ? kTcRows : kRows, Hq, Hk);
-    const int64_t ctas = attn_tiles(N, T, bf16 ? 2 * sh.tokens : sh.tokens) * sh.units, most = sm_count();
-    if (ctas * 2 > most) return 1;
-    const int64_t by_keys = kv_most / (4 * (bf16 ? kTcKeys : kKeys)), by_ctas = most / ctas;
-    int64_t s = by_ctas < by_keys ? by_ctas : by_keys;
+    const AttnShape sh = attn_shape(bf16 ? kTcRows : 16 * rows_per_thread(N, T, Hq, Hk), Hq, Hk);
+    const int64_t ctas = attn_tiles(N, T, bf16 ? 2 * sh.tokens : sh.tokens) * sh.units;
+    const int64_t by_keys = kv_most / (2 * (bf16 ? kTcKeys : kKeys));
+    const int64_t by_ctas = (int64_t)sm_count() * (bf16 ? 1 : 2) / ctas;
+    const int64_t s = by_ctas < by_keys ? by_ctas : by_keys;
     return (int32_t)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
