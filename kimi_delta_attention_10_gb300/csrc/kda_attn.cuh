@@ -171,10 +171,29 @@ struct AttnWalk {
         deepest = __reduce_max_sync(0xffffffffu, deepest);
         level = (int32_t)(((int64_t)deepest + (1 << key_shift) - 1) >> key_shift) + 1;   // above the first
     }
+    __device__ __forceinline__ void set(AttnTile& t, const Sequence& s, int32_t index) const
+    {
+        t.index = index;
+        t.seq0 = s.c0;
+        t.seq_tokens = s.m;
+        t.row0 = s.c0 + index * tokens;
+        t.tokens = min(tokens, s.m - index * tokens);
+        t.kv_len = s.L;
+        t.pos0 = s.L - s.m + index * tokens;
+    }
     // false: there is no such tile
     __device__ __forceinline__ bool next(const AttnArgs& a, int32_t item, AttnTile& t)
     {
         if (bad) return false;
+        if (a.N == 1) {
+            // one sequence: the tiles from its end (a search costs a short call a microsecond)
+            const Sequence s = {__shfl_sync(0xffffffffu, mine.c0, 0), __shfl_sync(0xffffffffu, mine.m, 0),
+                                __shfl_sync(0xffffffffu, mine.L, 0), __shfl_sync(0xffffffffu, mine.nt, 0)};
+            if (item >= s.nt) return false;
+            t.n = 0;
+            set(t, s, s.nt - 1 - item);
+            return true;
+        }
         if (item >= behind) {
             // The item has the least d with at most `item` tiles of more than d key tiles; level - 1
             // is one.  Down from there in growing steps, then by halves.
@@ -223,13 +242,7 @@ struct AttnWalk {
                 rank -= of(upto - tiles);
                 const int32_t begin = of(s.nt - count(a, s, level - 1)), m = of(s.m);
                 t.n = base + who;
-                t.index = begin + rank;
-                t.seq0 = of(s.c0);
-                t.seq_tokens = m;
-                t.row0 = t.seq0 + t.index * tokens;
-                t.tokens = min(tokens, m - t.index * tokens);
-                t.kv_len = of(s.L);
-                t.pos0 = t.kv_len - m + t.index * tokens;
+                set(t, Sequence{of(s.c0), m, of(s.L), 0}, begin + rank);
                 return true;
             }
             const int32_t all = __shfl_sync(0xffffffffu, upto, 31);

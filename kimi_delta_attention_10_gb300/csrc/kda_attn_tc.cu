@@ -74,8 +74,12 @@ struct Plan {
         tokens[1] = t.tokens - tokens[0];
         all = attn_keys(a, t);
         const int32_t tiles = (int32_t)(((int64_t)all + kTcKeys - 1) >> kTcKeyShift);
-        j0 = (int32_t)((int64_t)tiles * job.piece / a.splits);
-        const int32_t j1 = (int32_t)((int64_t)tiles * (job.piece + 1) / a.splits);
+        int32_t j1 = tiles;
+        j0 = 0;
+        if (a.splits > 1) {                // the quotients are a microsecond of a short call
+            j0 = (int32_t)((int64_t)tiles * job.piece / a.splits);
+            j1 = (int32_t)((int64_t)tiles * (job.piece + 1) / a.splits);
+        }
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             keys[m] = tokens[m] == 0 ? 0
@@ -424,9 +428,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                         w[k] = pack_bf16(e.x, e.y);
                     }
                 };
-                for (;;) {
-                    add[0] = add[1] = make_float2(0.f, 0.f);
-                    weigh(0);
+                auto largest = [&] {
                     float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
                     for (int k = 4; k + 8 <= kTcKeys; k += 8) {
@@ -435,7 +437,13 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                     }
 #pragma unroll
                     for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], s[kTcKeys - 4 + x]);
-                    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
+                    return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
+                };
+                if (i == 0) ref = fmaxf(ref, largest());           // none to begin with (NaN: still none)
+                for (;;) {
+                    add[0] = add[1] = make_float2(0.f, 0.f);
+                    weigh(0);
+                    const float most = largest();
                     const bool grown = most > ref + kGrowth;
                     if (!__any_sync(0xffffffffu, grown)) break;
                     const float keep = grown ? exp2f(ref - most) : 1.f;

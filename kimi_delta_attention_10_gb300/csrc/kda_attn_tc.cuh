@@ -222,7 +222,7 @@ __device__ __forceinline__ AttnJob attn_job(AttnWalk& walk, const AttnArgs& a, c
     AttnJob job;
     job.found = 0;
     if (at < jobs) {
-        const int32_t rest = (int32_t)at / a.splits;
+        const int32_t rest = a.splits > 1 ? (int32_t)at / a.splits : (int32_t)at;
         job.piece = (int32_t)at - rest * a.splits;
         job.unit = rest % sh.units;
         job.found = walk.next(a, rest / sh.units, job.t);
