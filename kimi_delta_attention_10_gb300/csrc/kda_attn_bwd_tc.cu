@@ -22,6 +22,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kda_attn_tc.cuh"
 
@@ -210,49 +211,74 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
                 const uint64_t dA = desc_kmajor(base, 128, 0), dB = desc_kmajor(base + C::OFF_RING, 128, 0);
                 const uint64_t dN = D == 128 ? desc_mnmajor128(base + C::OFF_RING, 128 * 128, 0)
                                              : desc_mnmajor64(base + C::OFF_RING, 0);
-                // tile x of the CTA's own times tile x of the ring
-                auto scores = [&](int x, int32_t i) {
-                    if (wait.dead()) return;
+                // Products come back to back: a look at a barrier waits behind the three products in
+                // the queue (200 cycles), so each is issued among the products before the one that
+                // needs it, and only what was too early is waited for.
+                // tile x of the CTA's own times tile x of the ring, with a look
+                auto scores = [&](int x, int32_t i, auto look) {
                     fence_after_sync();
-                    const uint32_t at = ((i & 1) * 2 + x) * C::TILE;
+                    const uint64_t p = desc_advance(dA, x * C::TILE), q = desc_advance(dB, ((i & 1) * 2 + x) * C::TILE);
 #pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        mma_ss(lead, tmem + (x ? TM_DP : TM_S), desc_advance(dA, x * C::TILE + kmajor_off(128, s)),
-                                 desc_advance(dB, at + kmajor_off(128, s)), id_s, s > 0);
+                    for (uint32_t s = 0; s < D / 16; ++s) {
+                        if (s == D / 32) look();
+                        mma_ss(lead, tmem + (x ? TM_DP : TM_S), desc_advance(p, kmajor_off(128, s)),
+                               desc_advance(q, kmajor_off(128, s)), id_s, s > 0);
+                    }
                     commit_if(lead, x ? &bar.dpfull : &bar.sfull[0]);
                 };
                 // the weights in tensor memory (rows 0 .. 63 where the first half of the scores
                 // was, the others where the second was) times a tile of the ring
-                auto gradient = [&](int x, int32_t i) {
-                    if (wait.dead()) return;
+                auto gradient = [&](int x, int32_t i, bool more, auto look) {
                     fence_after_sync();
-                    const uint32_t at = ((i & 1) * 2 + (x ^ 1)) * C::TILE;
+                    const uint64_t q = desc_advance(dN, ((i & 1) * 2 + (x ^ 1)) * C::TILE);
 #pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        mma_ts(lead, tmem + (x ? TM_DK : TM_DV),
-                                    tmem + (x ? TM_DP : TM_S) + 8 * (s & 3) + 64 * (s >> 2),
-                                    desc_advance(dN, at + mnmajor_off(s)), id_d, i > 0 || s > 0);
+                    for (uint32_t s = 0; s < 8; ++s) {
+                        if (s == 4) look();
+                        mma_ts(lead, tmem + (x ? TM_DK : TM_DV), tmem + (x ? TM_DP : TM_S) + 8 * (s & 3) + 64 * (s >> 2),
+                               desc_advance(q, mnmajor_off(s)), id_d, more || s > 0);
+                    }
                     commit_if(lead, &bar.empty[x ^ 1][i & 1]);
                 };
-                int32_t at = 0;
-                auto first = [&](int32_t i) {                      // S of tile i
-                    wait(&bar.full[0][i & 1], (i >> 1) & 1);
-                    // a part's last tile: once the rows past the end are zeros
+                bool seen = false;
+                auto none = [] {};
+                // S of tile i, unless it was the last; a part's last tile: once the rows past its
+                // end are zeros
+                auto zeroed = [&](int32_t i, int32_t at) {
                     if (at + 1 == per && last < sh.tokens) wait(&bar.statfull[i & 1], (i >> 1) & 1);
-                    scores(0, i);
-                    if (++at == per) at = 0;
+                };
+                // dP and dV of tile i, S of the next, dK of tile i; `middle`: there are tiles
+                // before it, and the next one is no part's last
+                auto turn = [&](auto middle, int32_t i, int32_t next_at) {
+                    constexpr bool kMiddle = decltype(middle)::value;
+                    const uint32_t b = i & 1, ph = (i >> 1) & 1, nb = b ^ 1, nph = ((i + 1) >> 1) & 1;
+                    const bool next = kMiddle || i + 1 < n, more = kMiddle || i > 0;
+                    wait(seen, &bar.full[1][b], ph);
+                    if (wait.dead()) return;
+                    scores(1, i, [&] { seen = mbar_test(&bar.pfull, b); });
+                    wait(seen, &bar.pfull, b);
+                    if (wait.dead()) return;
+                    seen = false;
+                    gradient(0, i, more, [&] { if (next) seen = mbar_test(&bar.full[0][nb], nph); });
+                    if (next) {
+                        wait(seen, &bar.full[0][nb], nph);
+                        if (!kMiddle) zeroed(i + 1, next_at);
+                        if (wait.dead()) return;
+                        scores(0, i + 1, [&] { seen = mbar_test(&bar.dsfull, b); });
+                    }
+                    wait(seen, &bar.dsfull, b);
+                    if (wait.dead()) return;
+                    gradient(1, i, more, [&] { if (next) seen = mbar_test(&bar.full[1][nb], nph); });
                 };
                 wait(&bar.afull[0], 0);
-                first(0);
+                wait(&bar.full[0][0], 0);
+                zeroed(0, 0);
+                if (!wait.dead()) scores(0, 0, none);
                 wait(&bar.afull[1], 0);
+                int32_t at = per == 1 ? 0 : 1;                     // of the next tile in its part
                 for (int32_t i = 0; i < n; ++i) {
-                    wait(&bar.full[1][i & 1], (i >> 1) & 1);
-                    scores(1, i);
-                    wait(&bar.pfull, i & 1);
-                    gradient(0, i);
-                    if (i + 1 < n) first(i + 1);
-                    wait(&bar.dsfull, i & 1);
-                    gradient(1, i);
+                    if (i > 0 && i + 1 < n && at + 1 < per) turn(std::true_type(), i, at);
+                    else turn(std::false_type(), i, at);
+                    if (++at == per) at = 0;
                 }
                 commit_if(lead, &bar.done);                     // no MMA outlives the loop
                 mbar_wait(&bar.done, 0);
@@ -522,7 +548,9 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
         const uint64_t dK = desc_kmajor(base + C::OFF_K, 128, 0), dV = desc_kmajor(base + C::OFF_V, 128, 0);
         const uint64_t dN = D == 128 ? desc_mnmajor128(base + C::OFF_K, 128 * 128, 0)
                                      : desc_mnmajor64(base + C::OFF_K, 0);
-        uint32_t done = 0, cv = 0;                     // key tiles, and slots of values, of the jobs before
+        uint32_t done = 0;                             // key tiles of the jobs before
+        Ring<KS> kr;
+        Ring<VS> vr;
         for (int32_t round = 0;; ++round) {
             wait(&bar.jfull[round & 1], (round >> 1) & 1);
             if (wait.dead()) break;
@@ -532,75 +560,87 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
             const int32_t slot = uniform((int32_t)(job.t.tokens == sh.tokens));
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);
-            auto keys_full = [&](uint32_t i) { wait(&bar.kfull[(done + i) % KS], ((done + i) / KS) & 1); };
-            auto values_full = [&](uint32_t i) { wait(&bar.vfull[(cv + i) % VS], ((cv + i) / VS) & 1); };
-            // S, then dP, of key tile i.  The looks at barriers are issued among the products
-            // before those that need them: one takes 200 cycles beside them.
-            bool weights = false;
-            auto scores = [&](int x, int32_t i, int32_t look) {
-                if (x == 0) wait(&bar.sempty, ((done + i) & 1) ^ 1);
-                if (wait.dead()) return;
+            // Looks at barriers as in the first kernel.  S, then dP, of key tile i:
+            auto scores = [&](int x, int32_t i, uint32_t slot, auto look) {
                 fence_after_sync();
-                const uint64_t p = desc_advance(dA, x * C::TILE),
-                               q = x ? desc_advance(dV, (cv + i) % VS * C::TILE) : desc_advance(dK, (done + i) % KS * C::TILE);
-                const uint32_t d = tmem + (x ? C::TM_DP + ((done + i) & 1) * 128 : C::TM_S);
+                const uint32_t b = (done + i) & 1;
+                const uint64_t p = desc_advance(dA, x * C::TILE), q = desc_advance(x ? dV : dK, slot * C::TILE);
 #pragma unroll
                 for (uint32_t s = 0; s < D / 16; ++s) {
-                    if (s == D / 32 && look >= 0) weights = mbar_test(&bar.dsfull[(done + look) & 1], ((done + look) >> 1) & 1);
-                    mma_ss(lead, d, desc_advance(p, kmajor_off(128, s)), desc_advance(q, kmajor_off(128, s)), id_s, s > 0);
+                    if (s == D / 32) look();
+                    mma_ss(lead, tmem + (x ? C::TM_DP + b * 128 : C::TM_S), desc_advance(p, kmajor_off(128, s)),
+                           desc_advance(q, kmajor_off(128, s)), id_s, s > 0);
                 }
-                commit_if(lead, x ? &bar.dpfull[(done + i) & 1] : &bar.sfull);
-                if (x) commit_if(lead, &bar.vempty[(cv + i) % VS]);
+                commit_if(lead, x ? &bar.dpfull[b] : &bar.sfull);
+                if (x) commit_if(lead, &bar.vempty[slot]);
                 if (i + 1 == n) commit_if(lead, &bar.aempty[x]);
             };
-            wait(&bar.afull[0], round & 1);
-            keys_full(0);
-            scores(0, 0, -1);
-            wait(&bar.afull[1], round & 1);
-            values_full(0);
-            scores(1, 0, -1);
-            if (n > 1) {
-                keys_full(1);
-                values_full(1);
-            }
-            for (int32_t i = 0; i < n; ++i) {
-                weights = false;
-                if (i + 1 < n) {
-                    scores(0, i + 1, -1);
-                    scores(1, i + 1, i);
-                }
-                if (i == 0) wait(&bar.oempty, (round & 1) ^ 1);
-                const uint32_t b = (done + i) & 1;
-                wait(weights, &bar.dsfull[b], ((done + i) >> 1) & 1);
-                // the next step's tiles, while this product runs
-                const bool more = i + 2 < n;
-                const bool k_there = !more || mbar_test(&bar.kfull[(done + i + 2) % KS], ((done + i + 2) / KS) & 1);
-                const bool v_there = !more || mbar_test(&bar.vfull[(cv + i + 2) % VS], ((cv + i + 2) / VS) & 1);
-                if (!wait.dead()) {
-                    fence_after_sync();
-                    const uint64_t q = desc_advance(dN, (done + i) % KS * C::TILE);
-                    const int32_t keys = all - (i << kTcKeyShift);
-                    // dS: keys 0 .. 63 where the first half of dP was, the others where the second was
-                    auto step = [&](uint32_t s) {
-                        mma_ts(lead, tmem + C::TM_DQ, tmem + C::TM_DP + b * 128 + 8 * (s & 3) + 64 * (s >> 2),
-                               desc_advance(q, mnmajor_off(s)), id_d, i > 0 || s > 0);
-                    };
-                    if (keys >= kTcKeys) {
-#pragma unroll
-                        for (uint32_t s = 0; s < 8; ++s) step(s);
-                    } else {
-#pragma unroll 1
-                        for (uint32_t s = 0; 16 * (int32_t)s < keys; ++s) step(s);
+            bool seen = false;
+            // S and dP of tile i + 1, dq of tile i; `middle`: tiles before it and two whole ones behind
+            auto turn = [&](auto middle, int32_t i) {
+                constexpr bool kMiddle = decltype(middle)::value;
+                const uint32_t at = done + i, b = at & 1, k = kr.slot;
+                const bool next = kMiddle || i + 1 < n;
+                const bool known = seen;
+                seen = false;
+                if (next) {
+                    Ring<KS> kn = kr;
+                    kn.next();
+                    if (!__all_sync(0xffffffffu, known)) {
+                        wait(&bar.kfull[kn.slot], kn.phase);
+                        wait(&bar.vfull[vr.slot], vr.phase);
+                        wait(&bar.sempty, (at + 1) & 1 ^ 1);
                     }
-                    commit_if(lead, &bar.kempty[(done + i) % KS]);
-                    if (i + 1 == n) commit_if(lead, &bar.ofull);
+                    if (wait.dead()) return;
+                    scores(0, i + 1, kn.slot, [] {});
+                    scores(1, i + 1, vr.slot, [&] { seen = mbar_test(&bar.dsfull[b], (at >> 1) & 1); });
+                    vr.next();
+                    kr = kn;
                 }
-                if (more) {
-                    wait(k_there, &bar.kfull[(done + i + 2) % KS], ((done + i + 2) / KS) & 1);
-                    wait(v_there, &bar.vfull[(cv + i + 2) % VS], ((cv + i + 2) / VS) & 1);
+                if (!kMiddle && i == 0) wait(&bar.oempty, (round & 1) ^ 1);
+                wait(seen, &bar.dsfull[b], (at >> 1) & 1);
+                if (wait.dead()) return;
+                fence_after_sync();
+                const uint64_t q = desc_advance(dN, k * C::TILE);
+                const int32_t keys = all - (i << kTcKeyShift);
+                // dS: keys 0 .. 63 where the first half of dP was, the others where the second was
+                auto step = [&](uint32_t s) {
+                    mma_ts(lead, tmem + C::TM_DQ, tmem + C::TM_DP + b * 128 + 8 * (s & 3) + 64 * (s >> 2),
+                           desc_advance(q, mnmajor_off(s)), id_d, kMiddle || i > 0 || s > 0);
+                };
+                seen = false;
+                if (kMiddle || keys >= kTcKeys) {
+#pragma unroll
+                    for (uint32_t s = 0; s < 8; ++s) {
+                        if (s == 4 && kMiddle) {
+                            Ring<KS> kn = kr;
+                            kn.next();
+                            seen = mbar_test(&bar.kfull[kn.slot], kn.phase) & mbar_test(&bar.vfull[vr.slot], vr.phase) &
+                                   mbar_test(&bar.sempty, at & 1 ^ 1);
+                        }
+                        step(s);
+                    }
+                } else {
+#pragma unroll 1
+                    for (uint32_t s = 0; 16 * (int32_t)s < keys; ++s) step(s);
                 }
+                commit_if(lead, &bar.kempty[k]);
+                if (!kMiddle && i + 1 == n) commit_if(lead, &bar.ofull);
+            };
+            wait(&bar.afull[0], round & 1);
+            wait(&bar.kfull[kr.slot], kr.phase);
+            wait(&bar.sempty, (done & 1) ^ 1);
+            if (!wait.dead()) scores(0, 0, kr.slot, [] {});
+            wait(&bar.afull[1], round & 1);
+            wait(&bar.vfull[vr.slot], vr.phase);
+            if (!wait.dead()) scores(1, 0, vr.slot, [] {});
+            vr.next();
+            for (int32_t i = 0; i < n; ++i) {
+                if (i > 0 && i + 2 < n) turn(std::true_type(), i);
+                else turn(std::false_type(), i);
             }
-            cv += n + slot;
+            kr.next();
+            if (slot) vr.next();
             done += n;
         }
         commit_if(lead, &bar.drain);                   // no MMA outlives the loop
