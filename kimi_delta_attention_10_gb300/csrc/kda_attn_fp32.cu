@@ -138,20 +138,22 @@ __device__ __forceinline__ void accumulate(float2 (&o)[R][2 * H], const float* w
         }
     }
 }
-// The same with w transposed: o of key ty * 4 + i += sum over rows of w[row][key] x[row][channel].
+// The same with w transposed, of eight keys a thread: o of key 8 ty + i += sum over rows of
+// w[row][key] x[row][channel]; w single, in rows of `pitch`.
 template <int ROWS, int H, int PITCH>
-__device__ __forceinline__ void accumulate_t(float2 (&o)[4][2 * H], const float* w, int pitch, const float* x,
+__device__ __forceinline__ void accumulate_t(float2 (&o)[8][2 * H], const float* w, int pitch, const float* x,
                                              int ty, int tx)
 {
 #pragma unroll 4
     for (int r = 0; r < ROWS; ++r) {
-        const float4 p = *reinterpret_cast<const float4*>(w + r * pitch + 4 * ty);
-        const float2 pk[4] = {both(p.x), both(p.y), both(p.z), both(p.w)};
+        const float4 p = *reinterpret_cast<const float4*>(w + r * pitch + 8 * ty),
+                     q = *reinterpret_cast<const float4*>(w + r * pitch + 8 * ty + 4);
+        const float2 pk[8] = {both(p.x), both(p.y), both(p.z), both(p.w), both(q.x), both(q.y), both(q.z), both(q.w)};
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             const float4 y = *reinterpret_cast<const float4*>(x + r * PITCH + 4 * tx + 64 * h);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 o[i][2 * h] = fma2(pk[i], make_float2(y.x, y.y), o[i][2 * h]);
                 o[i][2 * h + 1] = fma2(pk[i], make_float2(y.z, y.w), o[i][2 * h + 1]);
             }
@@ -314,19 +316,25 @@ template <typename T, int D> __global__ void __launch_bounds__(256) attn_join_ke
     }
     top = warp_max(top);
     nan = __any_sync(0xffffffffu, nan);
+    // the pieces' outputs are asked for four at a time, and one without weight is not used
     float sum = 0.f, o[C] = {};
-    for (int p = 0; p < a.pieces; ++p) {
-        const float x = reinterpret_cast<const float*>(ws + attn_pieces_lse(a, p))[row];
-        if (x == -CUDART_INF_F) continue;
-        const float w = exp2f((x - top) * kLog2e);
-        sum += w;
-        const float* y = reinterpret_cast<const float*>(ws + attn_pieces_o(a, p)) + row * D + C * lane;
-        if constexpr (C == 4) {
-            const float4 z = *reinterpret_cast<const float4*>(y);
-            o[0] = fmaf(w, z.x, o[0]); o[1] = fmaf(w, z.y, o[1]); o[2] = fmaf(w, z.z, o[2]); o[3] = fmaf(w, z.w, o[3]);
-        } else {
-            const float2 z = *reinterpret_cast<const float2*>(y);
-            o[0] = fmaf(w, z.x, o[0]); o[1] = fmaf(w, z.y, o[1]);
+    for (int p0 = 0; p0 < a.pieces; p0 += 4) {
+        float w[4], z[4][C];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int p = min(p0 + k, a.pieces - 1);
+            w[k] = reinterpret_cast<const float*>(ws + attn_pieces_lse(a, p))[row];
+            const float* y = reinterpret_cast<const float*>(ws + attn_pieces_o(a, p)) + row * D + C * lane;
+            if constexpr (C == 4) *reinterpret_cast<float4*>(z[k]) = *reinterpret_cast<const float4*>(y);
+            else *reinterpret_cast<float2*>(z[k]) = *reinterpret_cast<const float2*>(y);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (p0 + k >= a.pieces || w[k] == -CUDART_INF_F) continue;
+            const float x = exp2f((w[k] - top) * kLog2e);
+            sum += x;
+#pragma unroll
+            for (int i = 0; i < C; ++i) o[i] = fmaf(x, z[k][i], o[i]);
         }
     }
     const float inv = nan ? CUDART_NAN_F : sum == 0.f ? 0.f : 1.f / sum;
@@ -492,11 +500,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(AttnArgs a, At
         }
         cp_async_commit();
     };
-    float2 dk[4][2 * H], dv[4][2 * H];
+    // half of the threads add up dv, the others dk: eight keys and 4 H channels each
+    const bool keys = tid >= kThreads / 2;
+    const int gy = (tid & (kThreads / 2 - 1)) >> 4;
+    float2 g[8][2 * H];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int h = 0; h < 2 * H; ++h) dk[i][h] = dv[i][h] = make_float2(0.f, 0.f);
+        for (int h = 0; h < 2 * H; ++h) g[i][h] = make_float2(0.f, 0.f);
     if (B::STAGES == 2) load(0);
     for (int32_t i = 0; i < n; ++i) {
         load(i + B::STAGES - 1);
@@ -513,23 +524,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(AttnArgs a, At
                 sm[B::OFF_DS + (ty * 4 + r) * B::PITCH_P + tx + 16 * c] = ds[r][c];
             }
         __syncthreads();
-        accumulate_t<kBwdRows, H, D + 4>(dv, sm + B::OFF_P, B::PITCH_P, dout, ty, tx);
-        accumulate_t<kBwdRows, H, D + 4>(dk, sm + B::OFF_DS, B::PITCH_P, q, ty, tx);
+        accumulate_t<kBwdRows, H, D + 4>(g, sm + (keys ? B::OFF_DS : B::OFF_P), B::PITCH_P, keys ? q : dout, gy, tx);
         __syncthreads();
     }
+    const float scale = keys ? a.scale : 1.f;
+    float* out = static_cast<float*>(keys ? a.dk : a.dv);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int32_t j = key0 + ty * 4 + i;
+    for (int i = 0; i < 8; ++i) {
+        const int32_t j = key0 + gy * 8 + i;
         if (j >= end) continue;
-        const int64_t r = ((int64_t)(t.seq0 + j) * a.Hk + hk) * D + 4 * tx;
+        float* y = out + ((int64_t)(t.seq0 + j) * a.Hk + hk) * D + 4 * tx;
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-            const float2 x = dk[i][2 * h], y = dk[i][2 * h + 1];
-            store4(static_cast<float*>(a.dk) + r + 64 * h,
-                   make_float4(x.x * a.scale, x.y * a.scale, y.x * a.scale, y.y * a.scale));
-            store4(static_cast<float*>(a.dv) + r + 64 * h,
-                   make_float4(dv[i][2 * h].x, dv[i][2 * h].y, dv[i][2 * h + 1].x, dv[i][2 * h + 1].y));
-        }
+        for (int h = 0; h < H; ++h)
+            store4(y + 64 * h, make_float4(g[i][2 * h].x * scale, g[i][2 * h].y * scale, g[i][2 * h + 1].x * scale,
+                                           g[i][2 * h + 1].y * scale));
     }
 }
 
@@ -614,11 +622,18 @@ template <int D, int R> cudaError_t forward_rows(const AttnArgs& a, cudaStream_t
     if (e != cudaSuccess) return e;
     return launch_after(kern, launch_config(ctas, kThreads, Fwd<D, R>::SMEM), stream, a, sh);
 }
-// Rows a thread, by the rows that a group has in a sequence of average length.
+// Rows a thread, by the rows that a group has in a sequence of average length; the largest
+// tiles, which read the keys least often, where they fill the GPU or nearly so (1024 tokens of 16
+// heads: 95 us, 108 with tiles of 64 rows; 4 prompts of 1 to 300 tokens over up to 1000 cached:
+// 41 us, 34 with tiles of 64 rows).
 int rows_per_thread(int32_t N, int32_t T, int32_t Hq, int32_t Hk)
 {
     const int64_t rows = ((int64_t)T + N - 1) / N * (Hq / Hk);
-    return rows > 64 ? 8 : rows > 32 ? 4 : rows > 16 ? 2 : 1;
+    if (rows > 64) {
+        const AttnShape sh = attn_shape(128, Hq, Hk);
+        return attn_tiles(N, T, sh.tokens) * sh.units * 8 >= (int64_t)sm_count() * 7 ? 8 : 4;
+    }
+    return rows > 32 ? 4 : rows > 16 ? 2 : 1;
 }
 
 template <int D> cudaError_t forward(const AttnArgs& a, cudaStream_t stream)
