@@ -16,7 +16,11 @@
 //
 // Eight warps form P and dS, a thread half a row of a tile: P while the tensor core works on
 // the products with the tile before, dS = P (dP - delta) while it forms P^T dO and the next
-// scores.  P and dS are rounded to BF16 (2^-8) as operands.  A warp reads the rows' lse and delta.
+// scores.  P and dS are rounded to BF16 (2^-8) as operands.  Rows whose keys lie in one tile, up to
+// 128 of them, have the largest dS and lose most to the rounding of `out` in delta: their dS
+// goes in as two BF16 parts, the second in columns of dP that the first leaves free (sequences
+// of 1 to 700 tokens: dq and dk 2.5e-3 off in one part; the rounding of the result is 1.7e-3).
+// A warp reads the rows' lse and delta.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -119,6 +123,22 @@ __device__ __forceinline__ void store_pairs(uint32_t t, const float (&x)[64])
     tmem_st_wait();
 }
 
+// What the BF16 pairs of store_pairs leave of the values, as BF16 pairs in the 32 columns
+// behind theirs.
+__device__ __forceinline__ void store_rests(uint32_t t, const float (&x)[64])
+{
+    uint32_t u[32];
+    auto rest = [](float v, uint32_t bits) {
+        return fabsf(v) < CUDART_INF_F ? v - __uint_as_float(bits) : 0.f;
+    };
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const uint32_t p = pack_bf16(x[2 * i], x[2 * i + 1]);
+        u[i] = pack_bf16(rest(x[2 * i], p << 16), rest(x[2 * i + 1], p & 0xffff0000u));
+    }
+    tmem_st32(t + 32, u);
+}
+
 // A lane's D values, scaled, to a row of the output.
 template <int D> __device__ __forceinline__ void store_row(uint32_t t, float scale, bool live, __nv_bfloat16* y)
 {
@@ -168,6 +188,8 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
         const int32_t per = uniform((left + sh.tokens - 1) / sh.tokens), n = per * sh.parts;
         const int32_t last = left - (per - 1) * sh.tokens;         // tokens of a part's last tile
         auto ring = [&](int x, int32_t i) { return sm + C::OFF_RING + ((i & 1) * 2 + x) * C::TILE; };
+        // whether tile `at` of a part takes dS in two parts
+        auto in_two = [&](int32_t at) { return key0 == 0 && (at + 1) * sh.tokens <= kTcKeys; };
 
         if (warp == C::WARP_LOAD) {
             // -------------------------------------------------------- producer
@@ -228,7 +250,7 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
                 };
                 // the weights in tensor memory (rows 0 .. 63 where the first half of the scores
                 // was, the others where the second was) times a tile of the ring
-                auto gradient = [&](int x, int32_t i, bool more, auto look) {
+                auto gradient = [&](int x, int32_t i, bool more, bool two, auto look) {
                     fence_after_sync();
                     const uint64_t q = desc_advance(dN, ((i & 1) * 2 + (x ^ 1)) * C::TILE);
 #pragma unroll
@@ -236,6 +258,12 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
                         if (s == 4) look();
                         mma_ts(lead, tmem + (x ? TM_DK : TM_DV), tmem + (x ? TM_DP : TM_S) + 8 * (s & 3) + 64 * (s >> 2),
                                desc_advance(q, mnmajor_off(s)), id_d, more || s > 0);
+                    }
+                    if (two) {
+#pragma unroll 1
+                        for (uint32_t s = 0; s < 8; ++s)
+                            mma_ts(lead, tmem + TM_DK, tmem + TM_DP + 32 + 8 * (s & 3) + 64 * (s >> 2),
+                                   desc_advance(q, mnmajor_off(s)), id_d, 1);
                     }
                     commit_if(lead, &bar.empty[x ^ 1][i & 1]);
                 };
@@ -247,37 +275,39 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
                     if (at + 1 == per && last < sh.tokens) wait(&bar.statfull[i & 1], (i >> 1) & 1);
                 };
                 // dP and dV of tile i, S of the next, dK of tile i; `middle`: there are tiles
-                // before it, and the next one is no part's last
-                auto turn = [&](auto middle, int32_t i, int32_t next_at) {
+                // before it, the next one is no part's last, and dS is in one part
+                auto turn = [&](auto middle, int32_t i, int32_t next_at, bool two) {
                     constexpr bool kMiddle = decltype(middle)::value;
                     const uint32_t b = i & 1, ph = (i >> 1) & 1, nb = b ^ 1, nph = ((i + 1) >> 1) & 1;
                     const bool next = kMiddle || i + 1 < n, more = kMiddle || i > 0;
-                    wait(seen, &bar.full[1][b], ph);
+                    wait.after(seen, &bar.full[1][b], ph);
                     if (wait.dead()) return;
                     scores(1, i, [&] { seen = mbar_test(&bar.pfull, b); });
-                    wait(seen, &bar.pfull, b);
+                    wait.after(seen, &bar.pfull, b);
                     if (wait.dead()) return;
                     seen = false;
-                    gradient(0, i, more, [&] { if (next) seen = mbar_test(&bar.full[0][nb], nph); });
+                    gradient(0, i, more, false, [&] { if (next) seen = mbar_test(&bar.full[0][nb], nph); });
                     if (next) {
-                        wait(seen, &bar.full[0][nb], nph);
+                        wait.after(seen, &bar.full[0][nb], nph);
                         if (!kMiddle) zeroed(i + 1, next_at);
                         if (wait.dead()) return;
                         scores(0, i + 1, [&] { seen = mbar_test(&bar.dsfull, b); });
                     }
-                    wait(seen, &bar.dsfull, b);
+                    wait.after(seen, &bar.dsfull, b);
                     if (wait.dead()) return;
-                    gradient(1, i, more, [&] { if (next) seen = mbar_test(&bar.full[1][nb], nph); });
+                    gradient(1, i, more, !kMiddle && two, [&] { if (next) seen = mbar_test(&bar.full[1][nb], nph); });
                 };
                 wait(&bar.afull[0], 0);
                 wait(&bar.full[0][0], 0);
                 zeroed(0, 0);
                 if (!wait.dead()) scores(0, 0, none);
                 wait(&bar.afull[1], 0);
-                int32_t at = per == 1 ? 0 : 1;                     // of the next tile in its part
+                int32_t own = 0, at = per == 1 ? 0 : 1;            // places in their parts: the tile, the next
                 for (int32_t i = 0; i < n; ++i) {
-                    if (i > 0 && i + 1 < n && at + 1 < per) turn(std::true_type(), i, at);
-                    else turn(std::false_type(), i, at);
+                    const bool two = in_two(own);
+                    if (i > 0 && i + 1 < n && at + 1 < per && !two) turn(std::true_type(), i, at, two);
+                    else turn(std::false_type(), i, at, two);
+                    own = at;
                     if (++at == per) at = 0;
                 }
                 commit_if(lead, &bar.done);                     // no MMA outlives the loop
@@ -337,6 +367,7 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
                 // rows before this one are tokens before the key
                 const int32_t begin = min(128, max(0, key - at * sh.tokens)) * sh.heads - 64 * half;
                 const bool cut = at * sh.tokens < kTcKeys - 1;     // for some key
+                const bool two = in_two(at);
                 if (++at == per) at = 0;
                 wait(&bar.statfull[b], (i >> 1) & 1);
                 wait(&bar.sfull[0], i & 1);
@@ -389,6 +420,7 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.statempty[b]);
+                if (two) store_rests(dp_tm, p);
                 store_pairs(dp_tm, p);
                 fence_before_sync();
                 __syncwarp();
@@ -493,7 +525,7 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
         uint32_t ck = 0, cv = 0, loads[2] = {0, 0};
         for (int32_t round = 0; !wait.dead(); ++round) {
             const AttnJob job = attn_job(walk, a, sh, jobs, round);
-            wait(&bar.jempty[round & 1], ((round >> 1) & 1) ^ 1);
+            wait.for_job(&bar.jempty[round & 1], ((round >> 1) & 1) ^ 1);
             if (lane == 0) bar.job[round & 1] = job;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.jfull[round & 1]);
@@ -552,7 +584,7 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
         Ring<KS> kr;
         Ring<VS> vr;
         for (int32_t round = 0;; ++round) {
-            wait(&bar.jfull[round & 1], (round >> 1) & 1);
+            wait.for_job(&bar.jfull[round & 1], (round >> 1) & 1);
             if (wait.dead()) break;
             const AttnJob& job = bar.job[round & 1];
             if (!uniform(job.found)) break;
@@ -598,7 +630,7 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
                     kr = kn;
                 }
                 if (!kMiddle && i == 0) wait(&bar.oempty, (round & 1) ^ 1);
-                wait(seen, &bar.dsfull[b], (at >> 1) & 1);
+                wait.after(seen, &bar.dsfull[b], (at >> 1) & 1);
                 if (wait.dead()) return;
                 fence_after_sync();
                 const uint64_t q = desc_advance(dN, k * C::TILE);
@@ -623,6 +655,12 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
                 } else {
 #pragma unroll 1
                     for (uint32_t s = 0; 16 * (int32_t)s < keys; ++s) step(s);
+                }
+                if (!kMiddle && n == 1) {              // the second parts
+#pragma unroll 1
+                    for (uint32_t s = 0; 16 * (int32_t)s < keys && s < 8; ++s)
+                        mma_ts(lead, tmem + C::TM_DQ, tmem + C::TM_DP + b * 128 + 32 + 8 * (s & 3) + 64 * (s >> 2),
+                               desc_advance(q, mnmajor_off(s)), id_d, 1);
                 }
                 commit_if(lead, &bar.kempty[k]);
                 if (!kMiddle && i + 1 == n) commit_if(lead, &bar.ofull);
@@ -650,7 +688,7 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
         // ------------------------------------------------------------ gradients from their ring slots
         uint32_t cv = 0, count = 0;
         for (int32_t round = 0;; ++round) {
-            wait(&bar.jfull[round & 1], (round >> 1) & 1);
+            wait.for_job(&bar.jfull[round & 1], (round >> 1) & 1);
             if (wait.dead()) break;
             const AttnJob job = bar.job[round & 1];
             if (!job.found) break;
@@ -658,7 +696,7 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
             if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);
             cv += (attn_keys(a, job.t) + kTcKeys - 1) >> kTcKeyShift;
             if (job.t.tokens != sh.tokens) continue;
-            wait(&bar.staged, count++ & 1);
+            wait.for_job(&bar.staged, count++ & 1);
             if (wait.dead()) break;
             if (lane == 0) {
                 for (int h = 0; h < HALVES; ++h)
@@ -681,7 +719,7 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
         const int32_t tok = r / sh.heads, g = r - tok * sh.heads;
         uint32_t cv = 0, done = 0;
         for (int32_t round = 0;; ++round) {
-            wait(&bar.jfull[round & 1], (round >> 1) & 1);
+            wait.for_job(&bar.jfull[round & 1], (round >> 1) & 1);
             if (wait.dead()) break;
             const AttnJob job = bar.job[round & 1];
             if (!job.found) break;
@@ -740,6 +778,7 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
                     fence_async_smem();
                     __syncwarp();
                 }
+                if (n == 1) store_rests(dp_tm, p);
                 store_pairs(dp_tm, p);
                 fence_before_sync();
                 __syncwarp();

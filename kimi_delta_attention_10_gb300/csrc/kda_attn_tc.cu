@@ -180,7 +180,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
             uint32_t c = 0, loads[2] = {0, 0};
             for (int32_t round = 0; !wait.dead(); ++round) {
                 const AttnJob job = attn_job(walk, a, sh, jobs, round);
-                wait(&bar.jempty[round & 1], ((round >> 1) & 1) ^ 1);
+                wait.for_job(&bar.jempty[round & 1], ((round >> 1) & 1) ^ 1);
                 if (lane == 0) bar.job[round & 1] = job;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.jfull[round & 1]);
@@ -204,7 +204,6 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                     if (a.table != nullptr && mine && k < p.all) row = (int32_t)attn_page_row(a, job.t.n, hk, k);
                 };
                 if (p.steps > 0) find_row(p.j0);
-                load_q(0);
                 for (int32_t i = 0; i < p.steps && !wait.dead(); ++i) {
                     const int32_t j = p.j0 + i, left = p.all - (j << kTcKeyShift);
                     const int32_t boxes = (min(left, kTcKeys) + (1 << shift) - 1) >> shift;
@@ -225,7 +224,10 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                             else
                                 tma_load_3d(dst, map, 64 * half, hk, job.t.seq0 + (j << kTcKeyShift), &bar.full[slot]);
                         }
-                        if (i == 0 && kv == 0) load_q(1);
+                    }
+                    if (i == 0) {              // their places may still be the last job's
+                        load_q(0);
+                        load_q(1);
                     }
                 }
                 // slots for the outputs
@@ -260,7 +262,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
             uint32_t done0 = 0, done1 = 0;             // key tiles of the jobs before, of each tile of rows
             uint32_t held0 = 0, held1 = 0;             // jobs with any
             for (int32_t round = 0;; ++round) {
-                wait(&bar.jfull[round & 1], (round >> 1) & 1);
+                wait.for_job(&bar.jfull[round & 1], (round >> 1) & 1);
                 if (wait.dead()) break;
                 const AttnJob& job = bar.job[round & 1];
                 if (!uniform(job.found)) break;
@@ -312,7 +314,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                                desc_advance(k, kmajor_off(kTcKeys, s)), id_s, s > 0);
                     }
                     commit_if(lead, &bar.sfull[0]);
-                    wait(seen, &bar.pfull[1], ph1);
+                    wait.after(seen, &bar.pfull[1], ph1);
                     fence_after_sync();
                     pv(1, d);
                     commit_if(lead, &bar.ofull[1]);
@@ -342,7 +344,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                         v = ring.slot;
                         ring.next();
                         wait(&bar.full[ring.slot], ring.phase);
-                        wait(seen, &bar.pfull[0], (done0 + i) & 1);
+                        wait.after(seen, &bar.pfull[0], (done0 + i) & 1);
                         seen = true;
                     }
 #pragma unroll 1
@@ -351,7 +353,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                         const uint32_t s_tm = tmem + C::TM_S + m * kTcKeys, mine = (m ? done1 : done0) + i;
                         if (i >= 0 && i < n) {
                             if (i == 0) wait(&bar.oempty[m], ((m ? held1 : held0) & 1) ^ 1);
-                            wait(seen, &bar.pfull[m], mine & 1);
+                            wait.after(seen, &bar.pfull[m], mine & 1);
                             if (!wait.dead()) {
                                 fence_after_sync();
                                 const uint64_t d = desc_advance(dV, v * C::SLOT);
@@ -416,7 +418,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
             const int m = warp - C::WARP_STORE;
             uint32_t c = 0, count = 0;
             for (int32_t round = 0;; ++round) {
-                wait(&bar.jfull[round & 1], (round >> 1) & 1);
+                wait.for_job(&bar.jfull[round & 1], (round >> 1) & 1);
                 if (wait.dead()) break;
                 const AttnJob job = bar.job[round & 1];
                 if (!job.found) break;
@@ -425,7 +427,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                 const Plan p(a, sh, job);
                 if (p.slot[m]) {
                     const uint32_t at = (c + 2 * p.steps + (m ? p.slot[0] : 0)) % NS;
-                    wait(&bar.staged[m], count++ & 1);
+                    wait.for_job(&bar.staged[m], count++ & 1);
                     if (wait.dead()) break;
                     if (lane == 0) {
                         for (int h = 0; h < HALVES; ++h)
@@ -453,7 +455,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
         const float factor = a.scale == 0.f ? 1.2e-38f : fabsf(a.scale) * kAttnLog2e;
         uint32_t c = 0, done = 0;                      // ring slots and key tiles of the jobs before
         for (int32_t round = 0;; ++round) {
-            wait(&bar.jfull[round & 1], (round >> 1) & 1);
+            wait.for_job(&bar.jfull[round & 1], (round >> 1) & 1);
             if (wait.dead()) break;
             const AttnJob job = bar.job[round & 1];
             if (!job.found) break;

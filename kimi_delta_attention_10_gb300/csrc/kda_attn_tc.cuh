@@ -68,16 +68,17 @@ struct WarpWait {
     bool gave_up;
     __device__ __forceinline__ WarpWait(int32_t* abort_flag, int32_t* status_word)
         : abort(abort_flag), status(status_word), gave_up(false) {}
-    __device__ __forceinline__ void operator()(uint64_t* m, uint32_t parity)
+    // times: of the limit of one wait, for one that others' whole tiles of rows pass in
+    __device__ __forceinline__ void operator()(uint64_t* m, uint32_t parity, uint32_t times = 1)
     {
         if (__all_sync(0xffffffffu, mbar_test(m, parity))) return;
-        uint32_t polls = 0;
+        uint32_t polls = 0, checks = 0;
         uint64_t since = 0;
         while (!gave_up && !tc::mbar_try_wait(m, parity)) {
             if (++polls % tc::kPollsPerCheck == 0) {
                 const uint64_t now = tc::globaltimer_ns();
                 if (since == 0) since = now;
-                if (*abort || now - since > tc::kWaitLimitNs || polls > tc::kPollsPerCheck * tc::kMaxTimerChecks) {
+                if (*abort || now - since > times * tc::kWaitLimitNs || ++checks > times * tc::kMaxTimerChecks) {
                     gave_up = true;
                     *abort = 1;
                     report_status(status, KDA_ERR_TIMEOUT);
@@ -86,8 +87,10 @@ struct WarpWait {
         }
         gave_up = __any_sync(0xffffffffu, gave_up);
     }
+    // A tile of rows takes a second at 10^8 keys.
+    __device__ __forceinline__ void for_job(uint64_t* m, uint32_t parity) { (*this)(m, parity, 100); }
     // with the outcome of an earlier look (mbar_test): waits where it was too early
-    __device__ __forceinline__ void operator()(bool seen, uint64_t* m, uint32_t parity)
+    __device__ __forceinline__ void after(bool seen, uint64_t* m, uint32_t parity)
     {
         if (!__all_sync(0xffffffffu, seen)) (*this)(m, parity);
     }

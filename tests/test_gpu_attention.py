@@ -92,7 +92,11 @@ CASES = [
     ([127, 128, 129], 4, 4, 128), ([300, 1, 17], 6, 2, 128), ([257], 16, 1, 128),
     ([255, 256], 1, 1, 64), ([70, 3, 130], 130, 1, 64), ([33] * 5, 5, 1, 128), ([600], 2, 1, 64),
     ([40] * 41, 1, 1, 64), ([129], 64, 8, 128), ([513], 2, 2, 128), ([9, 1, 30], 300, 2, 128),
-    ([385, 2], 48, 1, 128)]
+    ([385, 2], 48, 1, 128),
+    # few rows a sequence: the FP32 form's smaller tiles
+    ([20], 1, 1, 64), ([9, 10], 6, 2, 128), ([20, 30], 2, 1, 128), ([50], 1, 1, 64),
+    # many key tiles in a row for the tensor cores
+    ([1300], 1, 1, 64), ([1030, 9], 9, 3, 128)]
 
 
 def run_fwd(q, k, v, cu, **kw):
@@ -136,14 +140,6 @@ def test_forward_where_the_maximum_moves(dtype, falling):
     k[..., 0] = ramp[:, None].to(dtype)
     out, lse = run_fwd(q, k, v, [0, T], scale=1.0)
     check_rows(out, lse, attention.packed(f64(q), f64(k), f64(v), [0, T], 1.0), [(0, T)], dtype)
-
-
-@pytest.mark.parametrize("scale", [0.0, -0.3])
-def test_forward_other_scales(scale):
-    for dtype in (F32, BF16):
-        q, k, v = projected(150, 2, 1, 64, dtype, 4)
-        out, lse = run_fwd(q, k, v, [0, 150], scale=scale)
-        check_rows(out, lse, attention.packed(f64(q), f64(k), f64(v), [0, 150], scale), [(0, 150)], dtype)
 
 
 def grad_tols(r, dout, dtype, out_t):
@@ -198,6 +194,53 @@ def test_backward_matches_oracle(case, dtype):
     grads = kda.kda_attention_bwd(q, k, v, out, lse, dout, ints(cu), 0.11, status=st)
     assert int(st[0]) == 0 and all(g.dtype == dtype for g in grads)
     check_grads(q, k, v, dout, cu, 0.11, grads, dtype)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+def test_other_scales(scale):
+    for dtype in (F32, BF16):
+        q, k, v = projected(150, 2, 1, 64, dtype, 4)
+        out, lse = run_fwd(q, k, v, [0, 150], scale=scale)
+        check_rows(out, lse, attention.packed(f64(q), f64(k), f64(v), [0, 150], scale), [(0, 150)], dtype)
+        dout = randn(150, 2, 64, seed=5, dtype=dtype)
+        grads = kda.kda_attention_bwd(q, k, v, out, lse, dout, ints([0, 150]), scale)
+        check_grads(q, k, v, dout, [0, 150], scale, grads, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_thousands_of_short_sequences(dtype):
+    """More sequences than a warp looks at at once, empty ones among them; forward, backward and
+    the same tokens over pages, against one plain computation over padded rows in 64 bits."""
+    lens = np.random.default_rng(3).integers(0, 6, 2500)
+    cu = offsets(lens)
+    T, Hq, Hk, D = cu[-1], 4, 2, 64
+    q, k, v = (x.contiguous() for x in projected(T, Hq, Hk, D, dtype, 7))
+    dout = randn(T, Hq, D, seed=8, dtype=dtype)
+    out, lse = run_fwd(q, k, v, cu)
+    grads = kda.kda_attention_bwd(q, k, v, out, lse, dout, ints(cu))
+    q64, k64, v64 = (x.double().requires_grad_() for x in (q, k, v))
+    c = torch.tensor(cu[:-1], device="cuda")[:, None] + torch.arange(5, device="cuda")
+    held = torch.arange(5, device="cuda") < torch.tensor(lens, device="cuda")[:, None]
+    c = c.clamp(max=T - 1)
+    rep = lambda x: x[c].repeat_interleave(Hq // Hk, 2)
+    s = torch.einsum("nihd,njhd->nhij", q64[c], rep(k64)) * D ** -0.5
+    see = torch.ones(5, 5, device="cuda").tril().bool() & held[:, None, None, :]
+    p = torch.softmax(s.masked_fill(~see, -math.inf), -1).nan_to_num(0.0)
+    o = torch.einsum("nhij,njhd->nihd", p, rep(v64))[held]
+    want = torch.autograd.grad(o, (q64, k64, v64), dout.double())
+    # five terms of a few units at most: 8 roundings to BF16 (60 of FP32) of values below 16
+    tol = 8 * 2.0 ** -8 * 16 if dtype == BF16 else 600 * U * 16
+    for a, b in zip((out, *grads), (o.detach(), *want)):
+        assert (a.double() - b).abs().max() <= tol
+    page = 8
+    slots = torch.randperm(2500, generator=torch.Generator().manual_seed(1)).int().cuda()
+    kc, vc = (torch.full((2500, Hk, page, D), NAN, dtype=dtype, device="cuda") for _ in range(2))
+    n, i = held.nonzero(as_tuple=True)
+    for cache, x in ((kc, k), (vc, v)):
+        cache[slots[n].long(), :, i] = x
+    paged, pl = kda.kda_paged_prompt(q, kc, vc, slots[:, None].contiguous(), ints(lens.tolist()), ints(cu),
+                                     want_lse=True)
+    assert (paged.double() - o.detach()).abs().max() <= tol and (pl - lse).abs().max() <= 600 * U * 16
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
