@@ -16,7 +16,7 @@
 //             P in its place.  It has the tensor pipe's time to itself, so what lies between
 //             its products is what the kernel loses: operands that the compiler does not know
 //             to be uniform, looks at barriers, conditions (5.6 ms at first for 16384 tokens);
-//   store     one warp: outputs leave through ring slots by TMA.
+//   store     two warps: outputs leave through ring slots by TMA.
 //
 // Bound by the tensor pipe in long sequences, and there by power: 16384 tokens, 64 / 8 heads of 128
 // channels, 2.71 ms, 1620 TFLOP/s, 86% of what a library product reaches in a burst and 97% of what
@@ -39,11 +39,13 @@ using namespace tc;
 
 constexpr float kGrowth = 8.f;                 // log2 of the growth that moves the reference
 
+constexpr uint32_t kMisc = 640;                // bytes for barriers and jobs
+
 template <int D> struct Cfg {
     static constexpr int HALVES = D / 64;
     static constexpr uint32_t QTILE = kTcRows * D * 2, SLOT = kTcKeys * D * 2;
     static constexpr int NS = D == 128 ? 5 : 8;                // ring slots: 160, 128 KB
-    static constexpr uint32_t OFF_KV = 2 * QTILE, OFF_BAR = OFF_KV + NS * SLOT, SMEM = OFF_BAR + 512 + 1024;
+    static constexpr uint32_t OFF_KV = 2 * QTILE, OFF_BAR = OFF_KV + NS * SLOT, SMEM = OFF_BAR + kMisc + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
     static constexpr int NT = 384, WARP_LOAD = 8, WARP_MMA = 9, WARP_STORE = 10;   // and 11
     // registers of a thread: at launch, then of the softmax's threads, of the others
@@ -56,28 +58,13 @@ struct Maps {
     CUtensorMap q, k, v, out;
 };
 
-struct Bars {
-    uint64_t full[8], empty[8];        // ring slots
-    uint64_t qfull[2], qempty[2];
-    uint64_t sfull[2];                 // S in tensor memory
-    uint64_t pfull[2];                 // P in its place
-    uint64_t ofull[2];                 // product with V done
-    uint64_t oempty[2];                // O read
-    uint64_t staged[2];                // and in its ring slot
-    uint64_t jfull[2], jempty[2];
-    uint64_t drain;
-    uint32_t tmem;
-    int32_t abort;
-    AttnJob job[2];
-};
-
-// What a job is for each of its two tiles of rows.
+// What a job is for each of its two tiles of rows; worked out once, by the warp that finds it.
 struct Plan {
     int32_t tokens[2], keys[2];        // tokens, and keys that its last token sees
     int32_t n[2], steps;               // key tiles in this piece, and the most of them
     int32_t all, j0;                   // keys that any row sees, first key tile
-    bool slot[2];                      // the rows leave through a ring slot
-    __device__ __forceinline__ Plan(const AttnArgs& a, const AttnShape& sh, const AttnJob& job)
+    int32_t slot[2];                   // 1: the rows leave through a ring slot
+    __device__ __forceinline__ void set(const AttnArgs& a, const AttnShape& sh, const AttnJob& job)
     {
         const AttnTile& t = job.t;
         tokens[0] = min(t.tokens, sh.tokens);
@@ -100,6 +87,24 @@ struct Plan {
         }
         steps = max(n[0], n[1]);
     }
+};
+struct Job : AttnJob {
+    Plan p;
+};
+
+struct Bars {
+    uint64_t full[8], empty[8];        // ring slots
+    uint64_t qfull[2], qempty[2];
+    uint64_t sfull[2];                 // S in tensor memory
+    uint64_t pfull[2];                 // P in its place
+    uint64_t ofull[2];                 // product with V done
+    uint64_t oempty[2];                // O read
+    uint64_t staged[2];                // and in its ring slot
+    uint64_t jfull[2], jempty[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int32_t abort;
+    Job job[2];
 };
 
 // The D values of a thread's row of O, scaled, to the output or a piece of it.
@@ -137,7 +142,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
     extern __shared__ unsigned char raw[];
     unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     Bars& bar = *reinterpret_cast<Bars*>(sm + C::OFF_BAR);
-    static_assert(sizeof(Bars) <= 512, "barriers");
+    static_assert(sizeof(Bars) <= kMisc, "barriers");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if (tid == 0) {
@@ -189,13 +194,15 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
             const uint32_t qbytes = (uint32_t)sh.tokens * sh.heads * 128 * HALVES;
             uint32_t c = 0, loads[2] = {0, 0};
             for (int32_t round = 0; !wait.dead(); ++round) {
-                const AttnJob job = attn_job(walk, a, sh, jobs, round);
+                Job job;
+                static_cast<AttnJob&>(job) = attn_job(walk, a, sh, jobs, round);
+                if (job.found) job.p.set(a, sh, job);
+                const Plan& p = job.p;
                 wait.for_job(&bar.jempty[round & 1], ((round >> 1) & 1) ^ 1);
                 if (lane == 0) bar.job[round & 1] = job;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.jfull[round & 1]);
                 if (!job.found) break;
-                const Plan p(a, sh, job);
                 const int32_t hk = job.unit / sh.parts;
                 auto load_q = [&](int m) {
                     if (p.n[m] == 0) return;
@@ -274,13 +281,13 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
             for (int32_t round = 0;; ++round) {
                 wait.for_job(&bar.jfull[round & 1], (round >> 1) & 1);
                 if (wait.dead()) break;
-                const AttnJob& job = bar.job[round & 1];
+                const Job& job = bar.job[round & 1];
                 if (!uniform(job.found)) break;
-                const Plan p(a, sh, job);
+                const Plan& p = job.p;
                 const int32_t steps = uniform(p.steps), n0 = uniform(p.n[0]), n1 = uniform(p.n[1]);
                 const int32_t keys0 = uniform(p.keys[0] - (p.j0 << kTcKeyShift)),
                               keys1 = uniform(p.keys[1] - (p.j0 << kTcKeyShift));
-                const int32_t slots = uniform((int32_t)p.slot[0] + p.slot[1]);
+                const int32_t slots = uniform(p.slot[0] + p.slot[1]);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);
                 // The products fill shared memory's bandwidth, and a look at a barrier takes 100 to
@@ -349,7 +356,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                         seen = false;
 #pragma unroll 1
                         for (; i < middle && !wait.dead(); ++i) steady(i);
-                        // back to the general form: step i's values and keys
+                        // back to the general form: step i's values and the keys behind them
                         wait(&bar.full[ring.slot], ring.phase);
                         v = ring.slot;
                         ring.next();
@@ -430,11 +437,11 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
             for (int32_t round = 0;; ++round) {
                 wait.for_job(&bar.jfull[round & 1], (round >> 1) & 1);
                 if (wait.dead()) break;
-                const AttnJob job = bar.job[round & 1];
+                const Job job = bar.job[round & 1];
                 if (!job.found) break;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);
-                const Plan p(a, sh, job);
+                const Plan& p = job.p;
                 if (p.slot[m]) {
                     const uint32_t at = (c + 2 * p.steps + (m ? p.slot[0] : 0)) % NS;
                     wait.for_job(&bar.staged[m], count++ & 1);
@@ -467,11 +474,11 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
         for (int32_t round = 0;; ++round) {
             wait.for_job(&bar.jfull[round & 1], (round >> 1) & 1);
             if (wait.dead()) break;
-            const AttnJob job = bar.job[round & 1];
+            const Job job = bar.job[round & 1];
             if (!job.found) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.jempty[round & 1]);
-            const Plan p(a, sh, job);
+            const Plan& p = job.p;
             const AttnTile& t = job.t;
             const int32_t n = m ? p.n[1] : p.n[0];
             const int32_t limit = a.causal ? t.pos0 + token + 1 : t.kv_len;
