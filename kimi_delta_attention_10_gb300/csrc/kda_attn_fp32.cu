@@ -690,6 +690,7 @@ cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t stream)
 // (1024 tokens, 16 heads of 64 channels: 139 us in one piece, 89 and 8 for the join in two).
 int32_t attn_splits(bool bf16, int32_t N, int32_t T, int32_t Hq, int32_t Hk, int32_t D, int64_t kv_most)
 {
+    if (N == 0 || T == 0) return 1;
     const AttnShape sh = attn_shape(bf16 ? kTcRows : 16 * rows_per_thread(N, T, Hq, Hk), Hq, Hk);
     const int64_t ctas = attn_tiles(N, T, bf16 ? 2 * sh.tokens : sh.tokens) * sh.units;
     const int64_t by_keys = kv_most / (2 * (bf16 ? kTcKeys : kKeys));

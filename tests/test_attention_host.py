@@ -138,6 +138,16 @@ def test_workspace_sizes(lib):
         kda.attention_workspace_size(1, 10, 3, 2)
 
 
+@pytest.mark.parametrize("name", ["kda_attention", "kda_attention_bwd", "kda_paged_prompt",
+                                  "kda_paged_decode_shared"])
+@pytest.mark.parametrize("first,second", [(0, 0), (0, 5), (3, 0)])
+def test_workspace_sizes_of_nothing(lib, name, first, second):
+    """No sequences, or no tokens: a size all the same."""
+    n = ctypes.c_int64()
+    assert getattr(lib, name + "_workspace_size")(first, second, 4, 2, 64, ctypes.byref(n)) == 0
+    assert n.value >= 16
+
+
 def test_binding_refuses_by_name(lib):
     z = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype)
     cu = z(2, dtype=torch.int32)
