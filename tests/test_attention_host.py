@@ -148,6 +148,19 @@ def test_workspace_sizes_of_nothing(lib, name, first, second):
     assert n.value >= 16
 
 
+MANY = (1 << 22) + 1
+
+
+@pytest.mark.parametrize("fn,args,kw", [
+    ("kda_attention_fwd", FWD, dict(N=MANY)), ("kda_attention_bwd", BWD, dict(N=MANY)),
+    ("kda_paged_prompt", PROMPT, dict(N=MANY)), ("kda_paged_decode_shared", SHARED, dict(groups=MANY)),
+    # rows of 2^31 elements
+    ("kda_paged_prompt", PROMPT, dict(T=1, Hq=1 << 24, q_stride=(1 << 31) - 8)),
+    ("kda_paged_decode_shared", SHARED, dict(N=1, Hq=1 << 24))])
+def test_sizes_beyond_the_indices(lib, fn, args, kw):
+    assert call(getattr(lib, fn), args, **kw) == UNSUPPORTED
+
+
 def test_binding_refuses_by_name(lib):
     z = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype)
     cu = z(2, dtype=torch.int32)
