@@ -17,9 +17,11 @@
 // Eight warps form P and dS, a thread half a row of a tile: P while the tensor core works on
 // the products with the tile before, dS = P (dP - delta) while it forms P^T dO and the next
 // scores.  P and dS are rounded to BF16 (2^-8) as operands.  Rows whose keys lie in one tile, up to
-// 128 of them, have the largest dS and lose most to the rounding of `out` in delta: their dS
-// goes in as two BF16 parts, the second in columns of dP that the first leaves free (sequences
-// of 1 to 700 tokens: dq and dk 2.5e-3 off in one part; the rounding of the result is 1.7e-3).
+// 128 of them, have the largest dS and lose most to the rounding of `out` in delta: their delta
+// is the sum of P dP in FP32, which the second kernel forms (it runs first) and leaves to the other,
+// and their dS goes in as two BF16 parts, the second in columns of dP that the first leaves free
+// (sequences of 1 to 700 tokens: dq and dk 2.5e-3 off without both; of 2 to 4 tokens 3.1e-3 off with
+// the rounded out; the rounding of the result is 1.7e-3).
 // A warp reads the rows' lse and delta.
 //
 // Bound by the tensor pipe in long sequences: one of 8192 tokens, 64 / 8 heads of 128 channels,
@@ -457,7 +459,7 @@ template <int D> struct CfgQ {
     // product with dS, its values only until dP
     static constexpr int KS = D == 128 ? 3 : 4, VS = D == 128 ? 2 : 4;
     static constexpr uint32_t OFF_K = 2 * TILE, OFF_V = OFF_K + KS * TILE, OFF_BAR = OFF_V + VS * TILE,
-                              SMEM = OFF_BAR + 512 + 1024;
+                              OFF_SUM = OFF_BAR + 512, SMEM = OFF_SUM + 1024 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
     static constexpr int NT = 352, WARP_LOAD = 8, WARP_MMA = 9, WARP_STORE = 10;
     static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DQ = 384;      // two buffers of dP
@@ -468,6 +470,7 @@ struct QBars {
     uint64_t kfull[4], kempty[4], vfull[4], vempty[4];         // ring slots
     uint64_t sfull, sempty;
     uint64_t dpfull[2], dsfull[2];     // dP, dS in its place
+    uint64_t summed;                   // delta of both halves of the rows' keys
     uint64_t ofull, oempty, staged;    // dq added up, read, in its ring slot
     uint64_t jfull[2], jempty[2];
     uint64_t drain;
@@ -504,6 +507,7 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
         }
         mbar_init(&bar.sfull, 1);
         mbar_init(&bar.sempty, 8);
+        mbar_init(&bar.summed, 8);
         mbar_init(&bar.ofull, 1);
         mbar_init(&bar.oempty, 8);
         mbar_init(&bar.staged, 8);
@@ -724,7 +728,8 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
         const uint32_t s_tm = lane0 + C::TM_S + 64 * half;
         const float2 factor = both(a.scale * kAttnLog2e);
         const int32_t tok = r / sh.heads, g = r - tok * sh.heads;
-        uint32_t cv = 0, done = 0;
+        float* sums = reinterpret_cast<float*>(sm + C::OFF_SUM);   // [half][row]
+        uint32_t cv = 0, done = 0, exact = 0;
         for (int32_t round = 0;; ++round) {
             wait.for_job(&bar.jfull[round & 1], (round >> 1) & 1);
             if (wait.dead()) break;
@@ -738,7 +743,7 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
             const int64_t row = (int64_t)(t.row0 + tok) * a.Hq + job.unit * sh.heads + g;
             const float lse = live ? a.lse_in[row] : CUDART_INF_F;
             const float2 nl = both(lse == -CUDART_INF_F ? -CUDART_INF_F : -lse * kAttnLog2e);
-            const float2 nd = both(live ? -a.delta[row] : 0.f);
+            float2 nd = both(live && n > 1 ? -a.delta[row] : 0.f);
             for (int32_t i = 0; i < n; ++i) {
                 // keys from this one on are tokens behind the row's
                 const int32_t end = t.pos0 + tok + 1 - (i << kTcKeyShift) - 64 * half;
@@ -761,6 +766,24 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
                 }
                 wait(&bar.dpfull[b], (at >> 1) & 1);
                 fence_after_sync();
+                if (n == 1) {
+                    // delta from the row's own weights, for the other kernel too
+                    float sum = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float d[32];
+                        tmem_ld32(dp_tm + 32 * x, d);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) sum += 32 * x + k < end ? p[32 * x + k] * d[k] : 0.f;
+                    }
+                    sums[128 * half + r] = sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.summed);
+                    wait(&bar.summed, exact++ & 1);
+                    sum += sums[128 * (half ^ 1) + r];
+                    if (half == 0 && live) a.delta[row] = sum;
+                    nd = both(-sum);
+                }
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     float d[32];
@@ -852,10 +875,11 @@ template <int D> cudaError_t backward(const AttnArgs& a, cudaStream_t stream)
     e = allow_smem(attn_bwd_kv_tc_kernel<D>, C::SMEM, &set_kv);
     if (e == cudaSuccess) e = allow_smem(attn_bwd_q_tc_kernel<D>, CfgQ<D>::SMEM, &set_q);
     if (e != cudaSuccess) return e;
-    e = launch_after(attn_bwd_kv_tc_kernel<D>, launch_config(kv, C::NT, C::SMEM), stream, a, sh, maps);
+    // the first writes delta of some rows for the second
+    e = launch_after(attn_bwd_q_tc_kernel<D>, launch_config(q < sm_count() ? q : sm_count(), CfgQ<D>::NT, CfgQ<D>::SMEM),
+                     stream, a, sh, (int32_t)q, qmaps);
     if (e != cudaSuccess) return e;
-    return launch_after(attn_bwd_q_tc_kernel<D>, launch_config(q < sm_count() ? q : sm_count(), CfgQ<D>::NT, CfgQ<D>::SMEM),
-                        stream, a, sh, (int32_t)q, qmaps);
+    return launch_after(attn_bwd_kv_tc_kernel<D>, launch_config(kv, C::NT, C::SMEM), stream, a, sh, maps);
 }
 
 }  // namespace
