@@ -645,12 +645,12 @@ kda_status kda_paged_decode(const void* q, const void* k_cache, const void* v_ca
  * offsets set KDA_ERR_DEVICE_ARG in status_dev, and no output is written.  All lengths
  * are read on the device, so that a captured call follows them.
  *
- * D = 64 or 128, Hq a multiple of Hk, T * Hq and Hq * D < 2^31, N (or groups) <= 2^22
- * (else KDA_ERR_UNSUPPORTED).  Packed rows may be slices of one projection: token t's
- * heads start at t * q_stride (k_stride, v_stride) elements, dense among themselves,
- * strides whole 16 bytes.  Integer arrays need 4-byte alignment only (a row of a table or
- * a slice will do).  No output may be an
- * input or another output.  workspace: 16-byte aligned, at least the size its entry point
+ * D = 64 or 128, Hq a multiple of Hk, N (or groups) <= 2^16, (T + N) * Hq (of a decode:
+ * requests and groups) and Hq * D < 2^31 (else KDA_ERR_UNSUPPORTED).  Packed rows may be
+ * slices of one projection: token t's heads start at t * q_stride (k_stride, v_stride)
+ * elements, dense among themselves, strides whole 16 bytes.  Integer arrays need 4-byte
+ * alignment only (a row of a table or a slice will do).  No output may be an input or
+ * another output.  workspace: 16-byte aligned, at least the size its entry point
  * names, contents on entry irrelevant; calls that share one must be ordered on one stream.
  */
 

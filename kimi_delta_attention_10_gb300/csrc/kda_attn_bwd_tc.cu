@@ -96,9 +96,10 @@ __device__ __forceinline__ void start(Bars& bar, const AttnArgs& a, int32_t item
         fence_mbar_init();
     }
     wait_for_previous();
+    const bool bad = a.N > kAttnOrdered && attn_bad(a);
     if (warp == 0) {
         AttnTile t;
-        const bool found = attn_find(a, item, tokens, kTcKeyShift, t);
+        const bool found = attn_find(a, bad, item, tokens, kTcKeyShift, t);
         if (tid == 0) {
             bar.tile = t;
             bar.found = found;
@@ -869,7 +870,7 @@ template <int D> cudaError_t backward(const AttnArgs& a, cudaStream_t stream)
     QMaps qmaps = {maps.q, maps.dout, maps.k, maps.v, maps.q};
     e = encode_heads(&qmaps.dq, a.dq, a.T, a.Hq, D, (int64_t)a.Hq * D, sh.heads, sh.tokens);
     if (e != cudaSuccess) return e;
-    const int64_t kv = attn_tiles(a.N, a.T, kTcKeys) * a.Hk, q = attn_tiles(a.N, a.T, sh.tokens) * sh.units;
+    const int64_t kv = attn_items(a.N, a.T, kTcKeys) * a.Hk, q = attn_tiles(a.N, a.T, sh.tokens) * sh.units;
     if (kv > INT32_MAX || q > INT32_MAX) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> set_kv{0}, set_q{0};
     e = allow_smem(attn_bwd_kv_tc_kernel<D>, C::SMEM, &set_kv);

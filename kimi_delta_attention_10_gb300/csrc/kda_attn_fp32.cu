@@ -200,13 +200,15 @@ __global__ void __launch_bounds__(kThreads, (Fwd<D, R>::CTAS)) attn_fwd_kernel(A
     wait_for_previous();
     const int32_t piece = blockIdx.x % a.splits, unit = blockIdx.x / a.splits % sh.units,
                   item = blockIdx.x / a.splits / sh.units;
+    const bool bad = a.N > kAttnOrdered && attn_bad(a);
     if (tid < 32) {
         AttnTile t;
-        const bool found = attn_find(a, item, sh.tokens, kKeyShift, t);
+        const bool found = attn_find(a, bad, item, sh.tokens, kKeyShift, t);
         if (tid == 0) {
             s_tile = t;
             s_found = found;
-            if (blockIdx.x == 0 && a.pieces > 1) *static_cast<int32_t*>(a.workspace) = found ? a.cu[a.N] : 0;
+            if (blockIdx.x == 0 && a.pieces > 1)
+                *static_cast<int32_t*>(a.workspace) = (a.N > kAttnOrdered ? !bad : found) ? a.cu[a.N] : 0;
         }
     }
     __syncthreads();
@@ -476,9 +478,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(AttnArgs a, At
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     wait_for_previous();
     const int32_t hk = blockIdx.x % a.Hk, item = blockIdx.x / a.Hk;
+    const bool bad = a.N > kAttnOrdered && attn_bad(a);
     if (tid < 32) {
         AttnTile t;
-        const bool found = attn_find(a, item, kKeys, kKeyShift, t);
+        const bool found = attn_find(a, bad, item, kKeys, kKeyShift, t);
         if (tid == 0) {
             s_tile = t;
             s_found = found;
@@ -558,9 +561,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(AttnArgs a, Att
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     wait_for_previous();
     const int32_t unit = blockIdx.x % sh.units, item = blockIdx.x / sh.units;
+    const bool bad = a.N > kAttnOrdered && attn_bad(a);
     if (tid < 32) {
         AttnTile t;
-        const bool found = attn_find(a, item, sh.tokens, kKeyShift, t);
+        const bool found = attn_find(a, bad, item, sh.tokens, kKeyShift, t);
         if (tid == 0) {
             s_tile = t;
             s_found = found;
@@ -619,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(AttnArgs a, Att
 template <int D, int R> cudaError_t forward_rows(const AttnArgs& a, cudaStream_t stream)
 {
     const AttnShape sh = attn_shape(16 * R, a.Hq, a.Hk);
-    const int64_t ctas = attn_tiles(a.N, a.T, sh.tokens) * sh.units * a.splits;
+    const int64_t ctas = attn_items(a.N, a.T, sh.tokens) * sh.units * a.splits;
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
     auto kern = attn_fwd_kernel<D, R>;
     static std::atomic<uint64_t> set{0};
@@ -666,10 +670,10 @@ template <int D> cudaError_t backward(const AttnArgs& a, cudaStream_t stream)
     if (e == cudaSuccess) e = allow_smem(attn_bwd_q_kernel<D>, Bwd<D>::SMEM, &set_q);
     if (e != cudaSuccess) return e;
     e = launch_after(attn_bwd_kv_kernel<D>,
-                     launch_config(attn_tiles(a.N, a.T, kKeys) * a.Hk, kThreads, Bwd<D>::SMEM), stream, a, sh);
+                     launch_config(attn_items(a.N, a.T, kKeys) * a.Hk, kThreads, Bwd<D>::SMEM), stream, a, sh);
     if (e != cudaSuccess) return e;
     return launch_after(attn_bwd_q_kernel<D>,
-                        launch_config(attn_tiles(a.N, a.T, sh.tokens) * sh.units, kThreads, Bwd<D>::SMEM), stream, a,
+                        launch_config(attn_items(a.N, a.T, sh.tokens) * sh.units, kThreads, Bwd<D>::SMEM), stream, a,
                         sh);
 }
 

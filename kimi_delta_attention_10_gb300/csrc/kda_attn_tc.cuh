@@ -261,5 +261,10 @@ inline int64_t attn_tiles(int32_t N, int32_t T, int32_t tokens)
 {
     return N < T ? (int64_t)(T - N) / tokens + N : T;
 }
+// Items of a kernel that starts a CTA a tile (attn_find).
+inline int64_t attn_items(int32_t N, int32_t T, int32_t tokens)
+{
+    return N > kAttnOrdered ? (int64_t)T / tokens + N : attn_tiles(N, T, tokens);
+}
 
 }  // namespace kda

@@ -148,7 +148,7 @@ def test_workspace_sizes_of_nothing(lib, name, first, second):
     assert n.value >= 16
 
 
-MANY = (1 << 22) + 1
+MANY = (1 << 16) + 1
 
 
 @pytest.mark.parametrize("fn,args,kw", [

@@ -243,6 +243,31 @@ def test_thousands_of_short_sequences(dtype):
     assert (paged.double() - o.detach()).abs().max() <= tol and (pl - lse).abs().max() <= 600 * U * 16
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_hundreds_of_sequences_of_all_sizes(dtype):
+    """Empty ones first, in the middle and last, long ones among short ones."""
+    lens = [0] * 40 + [3, 500, 1] + [0] * 100 + [130, 0, 64] + [1, 0, 2] * 50 + [257] + [0] * 30
+    assert len(lens) > 256
+    cu = offsets(lens)
+    q, k, v = projected(cu[-1], 4, 2, 64, dtype, 17)
+    dout = randn(cu[-1], 4, 64, seed=18, dtype=dtype)
+    out, lse = run_fwd(q, k, v, cu)
+    check_rows(out, lse, attention.packed(f64(q), f64(k), f64(v), cu, 0.125), attention.spans(cu), dtype)
+    grads = kda.kda_attention_bwd(q, k, v, out, lse, dout, ints(cu))
+    check_grads(q, k, v, dout, cu, 0.125, grads, dtype)
+    # bad offsets far from a tile's own
+    for n, to in ((200, cu[199] - 1), (7, -1), (len(lens), cu[-1] + 1)):
+        bad, st = list(cu), status_word()
+        bad[n] = to
+        g = [torch.full((cu[-1], h, 64), 7.0, dtype=dtype, device="cuda") for h in (4, 2, 2)]
+        keep = g[0].clone()
+        kda.kda_attention_bwd(q, k, v, out, lse, dout, ints(bad), q_grad=g[0], k_grad=g[1], v_grad=g[2], status=st)
+        assert int(st[0]) == KDA_ERR_DEVICE_ARG and all((x == 7).all() for x in g)
+        st.zero_()
+        kda.kda_attention_fwd(q, k, v, ints(bad), out=keep, status=st)
+        assert int(st[0]) == KDA_ERR_DEVICE_ARG and (keep == 7).all()
+
+
 def test_gradients_of_a_few_tokens():
     """The rounding of out and of the weights must not grow in sequences of 2 to 12 tokens: the
     gradients are what their own rounding leaves, 2^-9 a value on average at most, and a part more."""
@@ -445,6 +470,24 @@ def test_prompt_in_pieces_and_as_decode(dtype):
     for (n, h), r in ref.items():
         within(f64(out[n, h]), f64(d[n, h]), 2 * out_tol(r, dtype)[0], n)
         within(f64(lse[n, h]), f64(dl[n, h]), 2 * lse_tol(r)[0], n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_prompt_of_few_among_hundreds_of_requests(dtype):
+    """Most have no new token, the first neither; the others' keys are cut into pieces."""
+    new, lens = [0] * 300, [1] * 300
+    for n, m, L in ((30, 1, 2500), (150, 2, 900), (299, 1, 1)):
+        new[n], lens[n] = m, L
+    cu = offsets(new)
+    kc, vc, table = paged_case(lens, 1, 64, 32, dtype, 6)
+    q, st = randn(4, 2, 64, seed=6, dtype=dtype), status_word()
+    out, lse = kda.kda_paged_prompt(q, kc, vc, ints(table.tolist()), ints(lens), ints(cu), want_lse=True, status=st)
+    assert int(st[0]) == 0
+    ref = attention.paged_prompt(f64(q), f64(kc), f64(vc), table, lens, cu, 0.125)
+    check_rows(out, lse, ref, attention.spans(cu), dtype)
+    lens[3] = -1                               # of a request without tokens
+    kda.kda_paged_prompt(q, kc, vc, ints(table.tolist()), ints(lens), ints(cu), status=st)
+    assert int(st[0]) == KDA_ERR_DEVICE_ARG
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
