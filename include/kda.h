@@ -681,7 +681,9 @@ kda_status kda_attention_bwd_workspace_size(int32_t N, int64_t T, int32_t Hq, in
  * [T, Hq, D], k_grad, v_grad [T, Hk, D] (dense).  With p_ij = e^(s_ij - lse_i),
  * delta_i = dout_i . out_i and ds_ij = p_ij (dout_i . v_j - delta_i),
  *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i,
- * the last two over all heads of the group.  Scores are formed again, never stored.
+ * the last two over all heads of the group.  Scores are formed again, never stored.  BF16:
+ * delta of a row with up to 128 keys is sum_j p_ij (dout_i . v_j), which does not lose to
+ * the rounding of out.
  */
 kda_status kda_attention_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                              const void* v, int64_t v_stride, int32_t dtype, const void* out,

@@ -689,16 +689,18 @@ cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t stream)
                      : launch_after(attn_join_kernel<float, 128>, cfg, stream, a);
 }
 
-// Pieces of two key tiles at least: as many as fill the GPU once on the tensor cores; twice in
-// FP32, where a tile takes long enough that the longest of a causal call would be waited for
-// (1024 tokens, 16 heads of 64 channels: 139 us in one piece, 89 and 8 for the join in two).
+// Pieces of two key tiles at least: as many as fill the GPU once on the tensor cores (64 requests
+// behind 16384 tokens: 94 us, 110 if twice); three times in FP32, where a tile takes long enough that
+// the longest of a causal call would be waited for (1024 tokens, 16 heads of 64 channels: 139 us in
+// one piece, 89 and 8 for the join in two; 4 prompts of 1 to 300 tokens over up to 1000: 35.0 us if
+// twice, 32.8; 2048 tokens 244, 250 if four times).
 int32_t attn_splits(bool bf16, int32_t N, int32_t T, int32_t Hq, int32_t Hk, int32_t D, int64_t kv_most)
 {
     if (N == 0 || T == 0) return 1;
     const AttnShape sh = attn_shape(bf16 ? kTcRows : 16 * rows_per_thread(N, T, Hq, Hk), Hq, Hk);
     const int64_t ctas = attn_tiles(N, T, bf16 ? 2 * sh.tokens : sh.tokens) * sh.units;
     const int64_t by_keys = kv_most / (2 * (bf16 ? kTcKeys : kKeys));
-    const int64_t by_ctas = (int64_t)sm_count() * (bf16 ? 1 : 2) / ctas;
+    const int64_t by_ctas = (int64_t)sm_count() * (bf16 ? 1 : 3) / ctas;
     const int64_t s = by_ctas < by_keys ? by_ctas : by_keys;
     return (int32_t)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
