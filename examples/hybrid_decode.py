@@ -10,7 +10,8 @@ Nothing of a step comes back to the host, so the step is one CUDA graph.
     python examples/hybrid_decode.py [--requests 8] [--steps 32]
 
 The attention layer is the last one here: of a prompt it attends for the last token only,
-which is what kda_paged_decode does.  A layer above it would need all of them.
+which is what kda_paged_decode does.  A layer above it would need all of them, which
+kda_paged_prompt gives.
 
 Weights and inputs are random: the program shows the calls, and checks that going token
 by token gives what one long prompt gives.
