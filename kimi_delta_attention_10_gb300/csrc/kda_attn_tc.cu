@@ -19,11 +19,11 @@
 //   store     two warps: outputs leave through ring slots by TMA.
 //
 // Bound by the tensor pipe in long sequences, and there by power: 16384 tokens, 64 / 8 heads of 128
-// channels, 2.71 ms, 1620 TFLOP/s, 86% of what a library product reaches in a burst and 97% of what
-// it holds.  Pieces of prompts (16 requests, up to 512 tokens over up to 16384) 0.78 ms, 1440
+// channels, 2.77 ms, 1590 TFLOP/s, 84% of what a library product reaches in a burst and 95% of what
+// it holds.  Pieces of prompts (16 requests, up to 512 tokens over up to 16384) 0.79 ms, 1410
 // TFLOP/s.  With few rows by HBM: 64 requests of 4 drafted tokens over up to 16384, 322 us, 93% of
 // the rate of a plain copy.  Short sequences by a job's start and end, about 3 us: 8
-// sequences of 1 to 2048 tokens 189 us, 850 TFLOP/s; 129 tokens 9.0 us.
+// sequences of 1 to 2048 tokens 185 us, 870 TFLOP/s; 129 tokens 8.7 us.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -300,7 +300,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                 if (steps > 0) wait(&bar.full[ring.slot], ring.phase);
                 // Steps in the middle, of whole tiles for both tiles of rows: without a question but
                 // whether what they need is there.  The few instructions between the products
-                // were a fifth of the time (16384 tokens: 3.21 -> 2.78 ms).
+                // were a fifth of the time (16384 tokens: 3.21 -> 2.77 ms).
                 auto steady = [&](int32_t i) {
                     const uint32_t ph0 = (done0 + i) & 1, ph1 = (done1 + i) & 1;
                     auto pv = [&](uint32_t m, uint64_t d) {
