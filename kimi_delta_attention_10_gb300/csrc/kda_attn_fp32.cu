@@ -14,9 +14,9 @@
 // tile padded by 16 bytes so that 16 lanes' rows lie in different banks.
 //
 // Measured: 2048 tokens, 16 heads of 64 channels, 244 us (35 TFLOP/s, 47% of the FMA pipe's
-// peak; it is busy 55% of the cycles: two warps a scheduler wait for their own instructions, and twice
-// as many with smaller tiles read more); forward and backward of 1024 tokens 340 us, of which dk and dv 138 and dq 111, bound
-// by the longest CTA's walk.
+// peak; it is busy 55% of the cycles: two warps a scheduler wait for their own instructions,
+// and twice as many with smaller tiles read more); forward and backward of 1024 tokens 340 us,
+// of which dk and dv 138 and dq 111, bound by the longest CTA's walk.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>
