@@ -131,7 +131,7 @@ struct AttnWalk {
     {
         Sequence s;
         s.c0 = a.cu[n];
-        s.m = a.cu[n + 1] - s.c0;
+        s.m = (int32_t)((uint32_t)a.cu[n + 1] - (uint32_t)s.c0);
         s.L = attn_kv_len(a, n, s.m);
         s.nt = (int32_t)(((uint32_t)s.m + tokens - 1) / (uint32_t)tokens);
         return s;
@@ -162,7 +162,8 @@ struct AttnWalk {
         for (int32_t n = lane; n < a.N; n += 32) {
             const int32_t c1 = a.cu[n + 1];
             const Sequence s = look(a, n);
-            bad |= s.c0 < 0 || s.m < 0 || c1 > a.T || (n == 0 && s.c0 != 0);
+            // the offsets themselves: a difference of bad ones may wrap to a length
+            bad |= s.c0 < 0 || c1 < s.c0 || c1 > a.T || (n == 0 && s.c0 != 0);
             deepest = max(deepest, s.L);
             if (n == lane) mine = s;
         }
