@@ -39,8 +39,8 @@ kda_status check_sizes(int32_t N, int64_t T, int32_t Hq, int32_t Hk, int32_t D)
 {
     if (N < 0 || T < 0 || Hq < 1 || Hk < 1 || D < 1) return KDA_ERR_INVALID_ARG;
     if ((D != 64 && D != 128) || Hq % Hk != 0) return KDA_ERR_UNSUPPORTED;
-    // N: every CTA looks at all offsets
-    if (T + N > INT32_MAX / Hq || Hq > INT32_MAX / D || N > (1 << 16)) return KDA_ERR_UNSUPPORTED;
+    // N: every CTA looks at all offsets; T by itself first, since T + N could wrap
+    if (N > (1 << 16) || T > INT32_MAX || T + N > INT32_MAX / Hq || Hq > INT32_MAX / D) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 kda_status check_cache(int32_t Hk, int32_t num_pages, int32_t page_size, int32_t max_pages)
