@@ -13,7 +13,7 @@ namespace {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool valid_dtype(int32_t d) { return d == KDA_F32 || d == KDA_BF16; }
 
-// kda_test_set_fault's setting, read by every chunk-forward launch.
+// kda_test_set_fault's setting, read by every launch of the kernels that it can name.
 std::atomic<int32_t> g_test_fault{KDA_TEST_FAULT_NONE};
 
 }  // namespace
@@ -403,7 +403,8 @@ kda_status kda_chunk_bwd(const void* q, const void* k, const void* v, int32_t qk
 
 kda_status kda_test_set_fault(int32_t where)
 {
-    if (where < KDA_TEST_FAULT_NONE || where > KDA_TEST_FAULT_SINGLE_PASS)
+    if ((where < KDA_TEST_FAULT_NONE || where > KDA_TEST_FAULT_SINGLE_PASS) &&
+        where != KDA_TEST_FAULT_ATTENTION_BWD_KV)
         return KDA_ERR_INVALID_ARG;
     g_test_fault.store(where, std::memory_order_relaxed);
     return KDA_OK;

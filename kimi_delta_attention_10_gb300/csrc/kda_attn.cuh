@@ -45,6 +45,8 @@ struct AttnArgs {
     void* dq;
     void* dk;
     void* dv;
+    // test hook (kda_test_set_fault): the kernel that it names withholds an arrival in CTA 0
+    int32_t fault;
 };
 
 // Bytes before the pieces' statistics.

@@ -65,6 +65,7 @@ kda::AttnArgs common(int32_t dtype, int32_t N, int64_t T, int32_t Hq, int32_t Hk
     a.N = N; a.T = (int32_t)T; a.Hq = Hq; a.Hk = Hk; a.D = D; a.scale = scale;
     a.causal = true;
     a.splits = a.pieces = 1;
+    a.fault = kda::test_fault();
     return a;
 }
 

@@ -210,11 +210,13 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
                         tma_load_3d(sm + x * C::TILE + h * (128 * 128), x ? &maps.v : &maps.k, 64 * h, hk,
                                     t.seq0 + key0, &bar.afull[x]);
                 }
-                int32_t i = 0, part = 0, at = 0;
-                for (; i < n; ++i) {
+                int32_t part = 0, at = 0, loads[2] = {0, 0};       // copies of each ring
+                for (int32_t i = 0; i < n; ++i) {
+#pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         wait(&bar.empty[x][i & 1], ((i >> 1) & 1) ^ 1);
                         if (wait.dead) break;
+                        ++loads[x];
                         mbar_arrive_expect_tx(&bar.full[x][i & 1], (uint32_t)rows * 128 * HALVES);
                         for (int h = 0; h < HALVES; ++h)
                             tma_load_3d(ring(x, i) + h * (128 * 128), x ? &maps.dout : &maps.q, 64 * h,
@@ -230,13 +232,16 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
                 // every copy has landed before the CTA ends
                 mbar_wait(&bar.afull[0], 0);
                 mbar_wait(&bar.afull[1], 0);
-                for (int32_t k = max(0, i - 2); k < i; ++k)
-                    for (int x = 0; x < 2; ++x) mbar_wait(&bar.full[x][k & 1], (k >> 1) & 1);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    for (int32_t k = max(0, loads[x] - 2); k < loads[x]; ++k)
+                        mbar_wait(&bar.full[x][k & 1], (k >> 1) & 1);
             }
         } else if (warp == C::WARP_MMA) {
             // -------------------------------------------------------- MMA
             {
                 const uint32_t lead = elect_one();
+                const bool withhold = a.fault == KDA_TEST_FAULT_ATTENTION_BWD_KV && blockIdx.x == 0;
                 WarpWait wait(&bar.abort, a.status);
                 constexpr uint32_t id_s = idesc(kFmtBF16, 128, 128), id_d = idesc(kFmtBF16, 128, D, false, true);
                 const uint32_t base = smem_u32(sm);
@@ -275,7 +280,8 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
                             mma_ts(lead, tmem + TM_DK, tmem + TM_DP + 32 + 8 * (s & 3) + 64 * (s >> 2),
                                    desc_advance(q, mnmajor_off(s)), id_d, 1);
                     }
-                    commit_if(lead, &bar.empty[x ^ 1][i & 1]);
+                    // `withhold`: the first tile's dO never leaves its slot (a test hook)
+                    commit_if(!more && !x && withhold ? 0u : lead, &bar.empty[x ^ 1][i & 1]);
                 };
                 bool seen = false;
                 auto none = [] {};
