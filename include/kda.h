@@ -755,9 +755,12 @@ kda_status kda_paged_decode_shared(const void* q, const void* k_cache, const voi
  *                                           path (its first MMA group and the
  *                                           commit that signals it are withheld)
  *           KDA_TEST_FAULT_SINGLE_PASS (3)  the single-pass kernel (likewise)
+ *           KDA_TEST_FAULT_ATTENTION (8)    attention for several tokens forward, BF16
+ *                                           (the first queries' place is never given back)
+ *           KDA_TEST_FAULT_ATTENTION_BWD_Q (9)
+ *                                           dq of its backward (the first keys' slot)
  *           KDA_TEST_FAULT_ATTENTION_BWD_KV (10)
- *                                           dk and dv of kda_attention_bwd, BF16 (the
- *                                           first dO tile's slot is never given back)
+ *                                           dk and dv (the first dO tile's slot)
  * The setting is process-wide and read at each launch; other values return
  * KDA_ERR_INVALID_ARG.
  */
@@ -765,6 +768,8 @@ kda_status kda_paged_decode_shared(const void* q, const void* k_cache, const voi
 #define KDA_TEST_FAULT_SCAN 1
 #define KDA_TEST_FAULT_PREP 2
 #define KDA_TEST_FAULT_SINGLE_PASS 3
+#define KDA_TEST_FAULT_ATTENTION 8
+#define KDA_TEST_FAULT_ATTENTION_BWD_Q 9
 #define KDA_TEST_FAULT_ATTENTION_BWD_KV 10
 kda_status kda_test_set_fault(int32_t where);
 

@@ -34,6 +34,8 @@ KDA_TEST_FAULT_NONE = 0
 KDA_TEST_FAULT_SCAN = 1
 KDA_TEST_FAULT_PREP = 2
 KDA_TEST_FAULT_SINGLE_PASS = 3
+KDA_TEST_FAULT_ATTENTION = 8
+KDA_TEST_FAULT_ATTENTION_BWD_Q = 9
 KDA_TEST_FAULT_ATTENTION_BWD_KV = 10
 
 KDA_F32 = 0

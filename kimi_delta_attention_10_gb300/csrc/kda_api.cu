@@ -404,7 +404,7 @@ kda_status kda_chunk_bwd(const void* q, const void* k, const void* v, int32_t qk
 kda_status kda_test_set_fault(int32_t where)
 {
     if ((where < KDA_TEST_FAULT_NONE || where > KDA_TEST_FAULT_SINGLE_PASS) &&
-        where != KDA_TEST_FAULT_ATTENTION_BWD_KV)
+        (where < KDA_TEST_FAULT_ATTENTION || where > KDA_TEST_FAULT_ATTENTION_BWD_KV))
         return KDA_ERR_INVALID_ARG;
     g_test_fault.store(where, std::memory_order_relaxed);
     return KDA_OK;

@@ -544,6 +544,7 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
         for (int32_t round = 0; !wait.dead(); ++round) {
             const AttnJob job = attn_job(walk, a, sh, jobs, round);
             wait.for_job(&bar.jempty[round & 1], ((round >> 1) & 1) ^ 1);
+            if (wait.dead()) break;            // a role may still read the job that has the place
             if (lane == 0) bar.job[round & 1] = job;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.jfull[round & 1]);
@@ -598,6 +599,7 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
         const uint64_t dK = desc_kmajor(base + C::OFF_K, 128, 0), dV = desc_kmajor(base + C::OFF_V, 128, 0);
         const uint64_t dN = D == 128 ? desc_mnmajor128(base + C::OFF_K, 128 * 128, 0)
                                      : desc_mnmajor64(base + C::OFF_K, 0);
+        const bool withhold = a.fault == KDA_TEST_FAULT_ATTENTION_BWD_Q && blockIdx.x == 0;
         uint32_t done = 0;                             // key tiles of the jobs before
         Ring<KS> kr;
         Ring<VS> vr;
@@ -680,7 +682,8 @@ attn_bwd_q_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_consta
                         mma_ts(lead, tmem + C::TM_DQ, tmem + C::TM_DP + b * 128 + 32 + 8 * (s & 3) + 64 * (s >> 2),
                                desc_advance(q, mnmajor_off(s)), id_d, 1);
                 }
-                commit_if(lead, &bar.kempty[k]);
+                // `withhold`: the first keys never leave their slot (a test hook)
+                commit_if(!kMiddle && withhold && i == 0 && round == 0 ? 0u : lead, &bar.kempty[k]);
                 if (!kMiddle && i + 1 == n) commit_if(lead, &bar.ofull);
             };
             wait(&bar.afull[0], round & 1);

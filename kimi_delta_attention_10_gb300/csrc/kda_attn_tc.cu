@@ -193,12 +193,15 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
             const bool mine = lane / HALVES < kTcKeys >> shift;
             const uint32_t qbytes = (uint32_t)sh.tokens * sh.heads * 128 * HALVES;
             uint32_t c = 0, loads[2] = {0, 0};
+            // the first queries wait as if their place were never given back (a test hook)
+            const uint32_t lost = a.fault == KDA_TEST_FAULT_ATTENTION && blockIdx.x == 0;
             for (int32_t round = 0; !wait.dead(); ++round) {
                 Job job;
                 static_cast<AttnJob&>(job) = attn_job(walk, a, sh, jobs, round);
                 if (job.found) job.p.set(a, sh, job);
                 const Plan& p = job.p;
                 wait.for_job(&bar.jempty[round & 1], ((round >> 1) & 1) ^ 1);
+                if (wait.dead()) break;        // a role may still read the job that has the place
                 if (lane == 0) bar.job[round & 1] = job;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.jfull[round & 1]);
@@ -206,7 +209,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                 const int32_t hk = job.unit / sh.parts;
                 auto load_q = [&](int m) {
                     if (p.n[m] == 0) return;
-                    wait(&bar.qempty[m], (loads[m] & 1) ^ 1);
+                    wait(&bar.qempty[m], (loads[m] & 1) ^ 1 ^ lost);
                     if (wait.dead()) return;
                     if (lane == 0) mbar_arrive_expect_tx(&bar.qfull[m], qbytes);
                     __syncwarp();
@@ -389,7 +392,8 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                                 commit_if(lead, &bar.ofull[m]);
                             }
                         }
-                        if (m && i >= 0 && !wait.dead()) commit_if(lead, &bar.empty[v]);
+                        if (m && i >= 0 && !wait.dead())
+                            commit_if(lead, &bar.empty[v]);
                         seen = false;
                         if (i + 1 < n) {
                             if (i < 0) wait(&bar.qfull[m], (m ? held1 : held0) & 1);

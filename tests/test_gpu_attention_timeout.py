@@ -1,6 +1,6 @@
 """Bounded waits of attention's tensor-core kernels that run out, on purpose, through the
-test hook: CTA 0 of one kernel never gives a ring slot back, the copy that would take it is
-waited for about a second, and the kernel reports KDA_ERR_TIMEOUT, lets its copies and products in
+test hook: CTA 0 of one kernel never gives a place of its copies back, the copy that would take
+it is waited for about a second, and the kernel reports KDA_ERR_TIMEOUT, lets its copies and products in
 flight finish and returns without a CUDA error.  The next call gives exactly the bits of a call
 before.  Nothing here traps or faults the GPU: the lost arrival is a flag that nothing sets, and
 every wait on it is bounded."""
@@ -15,11 +15,12 @@ from test_gpu_attention import BF16, ints, offsets, projected, randn, status_wor
 pytestmark = pytest.mark.gpu
 
 
-# the first CTA has ten tiles of rows and more, so that it needs the lost slot again; a second
-# sequence gives other CTAs (and its own CTA, after the lost one) work of their own
-@pytest.mark.parametrize("lens,Hq,Hk,D", [([1300, 40], 2, 1, 64), ([1300, 40], 8, 2, 128)])
-@pytest.mark.parametrize("where", [binding.KDA_TEST_FAULT_ATTENTION_BWD_KV])
-def test_lost_slot_times_out_and_the_next_call_is_clean(where, lens, Hq, Hk, D):
+# the first CTA has thirty tiles of keys or rows, so that it needs the lost place again; a
+# second sequence gives other CTAs work
+@pytest.mark.parametrize("lens,Hq,Hk,D", [([4000, 40], 8, 4, 64), ([4000, 40], 16, 8, 128)])
+@pytest.mark.parametrize("where", [binding.KDA_TEST_FAULT_ATTENTION, binding.KDA_TEST_FAULT_ATTENTION_BWD_Q,
+                                   binding.KDA_TEST_FAULT_ATTENTION_BWD_KV])
+def test_lost_place_times_out_and_the_next_call_is_clean(where, lens, Hq, Hk, D):
     cu = ints(offsets(lens))
     T = sum(lens)
     q, k, v = projected(T, Hq, Hk, D, BF16, 3)
