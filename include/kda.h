@@ -728,7 +728,7 @@ kda_status kda_paged_decode_shared_workspace_size(int32_t N, int32_t groups, int
  *   cu_groups [groups+1], block_table [N, max_pages], seq_lens [N] int32
  *   out [N, Hq, D], lse [N, Hq]
  * cu_groups are offsets as above with T = N: requests behind the last group keep their
- * outputs.  Either length may be 0.  Lengths, pages and cache sizes as in kda_paged_decode.
+ * outputs, and their lengths and table rows are not looked at.  Either length may be 0.  Lengths, pages and cache sizes as in kda_paged_decode.
  */
 kda_status kda_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache,
                                    int32_t dtype, const int32_t* prefix_table,

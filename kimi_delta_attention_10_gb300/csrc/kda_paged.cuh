@@ -117,6 +117,7 @@ struct DecodeArgs {
     const int32_t* table;
     const int32_t* seq_lens;
     int32_t N;
+    const int32_t* live;     // requests from *live on have no row, whatever their lengths (nullptr: all have)
     int32_t Hq;
     int32_t Hk;
     int32_t D;

@@ -50,6 +50,11 @@ __device__ __forceinline__ int32_t valid_len(const DecodeArgs& a, int32_t L)
     const int64_t most = (int64_t)a.max_pages << a.page_shift;
     return L < 0 || L > most ? 0 : L;
 }
+// Requests with a row.
+__device__ __forceinline__ int32_t decode_requests(const DecodeArgs& a)
+{
+    return a.live == nullptr ? a.N : min(max(*a.live, 0), a.N);
+}
 __device__ __forceinline__ int32_t decode_len(const DecodeArgs& a, int32_t n)
 {
     return valid_len(a, a.seq_lens[n]);
@@ -122,6 +127,10 @@ struct DecodeLens {
         const int n0 = (threadIdx.x & 31) * kLaneRequests;
 #pragma unroll
         for (int i = 0; i < kLaneRequests; ++i) L[i] = n0 + i < a.N ? a.seq_lens[n0 + i] : 0;
+        if (a.live == nullptr) return;
+        const int32_t N = decode_requests(a);
+#pragma unroll
+        for (int i = 0; i < kLaneRequests; ++i) L[i] = n0 + i < N ? L[i] : 0;
     }
 };
 
@@ -184,8 +193,8 @@ __device__ __forceinline__ DecodeRange decode_range(const DecodeArgs& a, const D
         if (b == 0 && warp == 0 && bad) report_status(a.status, KDA_ERR_DEVICE_ARG);
         return r;
     }
-    const int32_t per = (a.N + NT - 1) / NT;         // consecutive requests per thread
-    const int32_t n0 = min(tid * per, a.N), n1 = min(n0 + per, a.N);
+    const int32_t N = decode_requests(a), per = (N + NT - 1) / NT;      // consecutive requests per thread
+    const int32_t n0 = min(tid * per, N), n1 = min(n0 + per, N);
     int64_t mine = 0;
     for (int32_t n = n0; n < n1; ++n) mine += decode_places(s, decode_len(a, n));
     int64_t upto = warp_scan(mine, lane);

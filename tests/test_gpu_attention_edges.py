@@ -2,6 +2,7 @@
 value, rows of padded batches, gradients through rows without weight, long sequences.
 Tolerances and helpers are those of test_gpu_attention."""
 import numpy as np
+import numpy as np
 import pytest
 import torch
 
@@ -43,3 +44,43 @@ def test_offsets_of_any_value_are_reported(cu, dtype):
     kda.kda_paged_decode_shared(q.contiguous(), kc, vc, ints(table.tolist()), ints([9] * N), ints(cu), own,
                                 ints([9] * 10), out=out, lse=lse, status=st)
     assert int(st[0]) == KDA_ERR_DEVICE_ARG and (out == 7).all() and (lse == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("live,tail", [(3, 1), (3, 40), (3, 200), (140, 3), (0, 5)])
+def test_shared_does_not_look_at_requests_behind_the_groups(live, tail, dtype):
+    """A batch padded to a captured size: whatever the lengths and tables behind the last
+    group hold, no status, the outputs there as they were, the others' bits the same."""
+    Hq, Hk, D, P = 4, 2, 128, 16
+    own = [7 * n % 50 for n in range(live)]
+    kc, vc, table = paged_case([70] + own, Hk, D, P, dtype, 3)
+    table = np.concatenate([table, np.full((tail, table.shape[1]), -1)])
+    cu = [0, live // 2, live]
+    q = randn(live + tail, Hq, D, seed=2, dtype=dtype)
+    q[live:] = float("nan")
+    results = []
+    for behind in (0, 5, table.shape[1] * P, HIGHEST, LOWEST, -1):
+        for entry in (-1, HIGHEST):
+            t = table.copy()
+            t[1 + live:] = entry
+            st = status_word()
+            out = torch.full((live + tail, Hq, D), 7.0, dtype=dtype, device="cuda")
+            lse = torch.full((live + tail, Hq), 7.0, device="cuda")
+            kda.kda_paged_decode_shared(q, kc, vc, ints(t[[0, 0]].tolist()), ints([70, 13]), ints(cu),
+                                        ints(t[1:].tolist()), ints(own + [behind] * tail), out=out, lse=lse, status=st)
+            assert int(st[0]) == 0 and (out[live:] == 7).all() and (lse[live:] == 7).all()
+            results.append((out, lse))
+    for out, lse in results[1:]:
+        assert torch.equal(out, results[0][0]) and torch.equal(lse, results[0][1])
+    if live:
+        alone, al = kda.kda_paged_decode_shared(
+            q[:live].contiguous(), kc, vc, ints(table[[0, 0]].tolist()), ints([70, 13]), ints(cu),
+            ints(table[1:1 + live].tolist()), ints(own), want_lse=True)
+        # fewer requests may be split otherwise: the same values to their rounding
+        torch.testing.assert_close(alone.float(), results[0][0][:live].float(), rtol=2.0 ** -7, atol=2.0 ** -7)
+        torch.testing.assert_close(al, results[0][1][:live], rtol=1e-5, atol=1e-5)
+        # and a bad length of a request that has a group is reported
+        st = status_word()
+        kda.kda_paged_decode_shared(q, kc, vc, ints(table[[0, 0]].tolist()), ints([70, 13]), ints(cu),
+                                    ints(table[1:].tolist()), ints(own[:-1] + [-1] + [0] * tail), status=st)
+        assert int(st[0]) == KDA_ERR_DEVICE_ARG
