@@ -682,8 +682,9 @@ kda_status kda_attention_bwd_workspace_size(int32_t N, int64_t T, int32_t Hq, in
  * delta_i = dout_i . out_i and ds_ij = p_ij (dout_i . v_j - delta_i),
  *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i,
  * the last two over all heads of the group.  Scores are formed again, never stored.  BF16:
- * delta of a row with up to 128 keys is sum_j p_ij (dout_i . v_j), which does not lose to
- * the rounding of out.
+ * the tokens are taken in tiles of floor(128 / h), h the largest divisor of Hq / Hk up to 128.
+ * In a tile whose last token has up to 128 keys delta is sum_j p_ij (dout_i . v_j), which
+ * does not lose to the rounding of out, and ds_ij goes into the products as two BF16 parts.
  */
 kda_status kda_attention_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                              const void* v, int64_t v_stride, int32_t dtype, const void* out,

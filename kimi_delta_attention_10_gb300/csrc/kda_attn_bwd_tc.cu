@@ -16,10 +16,11 @@
 //
 // Eight warps form P and dS, a thread half a row of a tile: P while the tensor core works on
 // the products with the tile before, dS = P (dP - delta) while it forms P^T dO and the next
-// scores.  P and dS are rounded to BF16 (2^-8) as operands.  Rows whose keys lie in one tile, up to
-// 128 of them, have the largest dS and lose most to the rounding of `out` in delta: their delta
-// is the sum of P dP in FP32, which the second kernel forms (it runs first) and leaves to the other,
-// and their dS goes in as two BF16 parts, the second in columns of dP that the first leaves free
+// scores.  P and dS are rounded to BF16 (2^-8) as operands.  Rows with few keys
+// have the largest dS and lose most to the rounding of `out` in delta: in a tile of rows that
+// sees one tile of keys (up to 128 for its last row) delta is the sum of P dP in FP32, which the
+// second kernel forms (it runs first) and leaves to the other, and both take dS as two BF16
+// parts, the second in columns of dP that the first leaves free
 // (sequences of 1 to 700 tokens: dq and dk 2.5e-3 off without both; of 2 to 4 tokens 3.1e-3 off with
 // the rounded out; the rounding of the result is 1.7e-3).
 // A warp reads the rows' lse and delta.
@@ -198,8 +199,9 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
         const int32_t per = uniform((left + sh.tokens - 1) / sh.tokens), n = per * sh.parts;
         const int32_t last = left - (per - 1) * sh.tokens;         // tokens of a part's last tile
         auto ring = [&](int x, int32_t i) { return sm + C::OFF_RING + ((i & 1) * 2 + x) * C::TILE; };
-        // whether tile `at` of a part takes dS in two parts
-        auto in_two = [&](int32_t at) { return key0 == 0 && (at + 1) * sh.tokens <= kTcKeys; };
+        // whether tile `at` of a part takes dS in two parts: where the other kernel's tile has one
+        // tile of keys
+        auto in_two = [&](int32_t at) { return key0 == 0 && min((at + 1) * sh.tokens, left) <= kTcKeys; };
 
         if (warp == C::WARP_LOAD) {
             // -------------------------------------------------------- producer

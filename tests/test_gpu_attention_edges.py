@@ -9,7 +9,10 @@ import torch
 import kimi_delta_attention_10_gb300 as kda
 from kimi_delta_attention_10_gb300.binding import KDA_ERR_DEVICE_ARG
 
-from test_gpu_attention import BF16, F32, ints, paged_case, projected, randn, status_word
+from oracle import attention
+
+from test_gpu_attention import (BF16, F32, ROUND, U, f64, ints, offsets, paged_case, projected, randn, run_fwd,
+                                status_word, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +87,43 @@ def test_shared_does_not_look_at_requests_behind_the_groups(live, tail, dtype):
         kda.kda_paged_decode_shared(q, kc, vc, ints(table[[0, 0]].tolist()), ints([70, 13]), ints(cu),
                                     ints(table[1:].tolist()), ints(own[:-1] + [-1] + [0] * tail), status=st)
         assert int(st[0]) == KDA_ERR_DEVICE_ARG
+
+
+def fine_tols(r, dout):
+    """(ds, dq, dk) and tolerances of one head's rows whose dS goes in as two BF16 parts (2^-16 of
+    it left) and whose delta is the sum of P dP: FP32 otherwise, roundings as in grad_tols."""
+    n = len(r.k) + len(r.q)
+    d, v = np.abs(dout), np.abs(r.v)
+    lse = np.abs(np.where(np.isfinite(r.lse), r.lse, 0.0))[:, None]
+    ep = 140 * U * r.reach.max(1, initial=0.0)[:, None] + (20 + n) * U + 4 * U * lse
+    dp, dp_e = dout @ r.v.T, 70 * U * (d @ v.T)
+    delta_e = (r.p * (np.abs(dp) * (ep + n * U) + dp_e)).sum(1, keepdims=True)
+    dq, dk, _, ds = r.grads(dout)
+    delta = (r.p * dp).sum(1, keepdims=True)
+    ds_e = r.p * (ep * (np.abs(dp) + np.abs(delta)) + dp_e + delta_e) + (2.0 ** -16 + (4 + n) * U) * np.abs(ds)
+    s = abs(r.scale)
+    return (dq, s * (ds_e @ np.abs(r.k))), (dk, s * (ds_e.T @ np.abs(r.q)))
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 5, 6, 7, 16, 43])
+@pytest.mark.parametrize("L", [1, 2, 43, 126, 127, 128])
+def test_gradients_of_up_to_128_keys_lose_nothing_to_the_rounding_of_ds(L, G):
+    """Heads with opposite queries and the same dout: dk is the small difference of their sums, so
+    that one rounding of dS to BF16 would be a few per cent of it."""
+    D, cu = 128, [0, L]
+    _, k, v = projected(L, 1, 1, D, BF16, 5)
+    x = randn(L, 1, D, seed=6, dtype=BF16) * 0.125
+    q = torch.cat([x if h % 2 == 0 else -x for h in range(G)], 1).contiguous()
+    dout = randn(L, 1, D, seed=7, dtype=BF16).expand(L, G, D).contiguous()
+    out, lse = run_fwd(q, k, v, cu)
+    st = status_word()
+    gq, gk, _ = (f64(g) for g in kda.kda_attention_bwd(q, k, v, out, lse, dout, ints(cu), status=st))
+    assert int(st[0]) == 0
+    dk_sum, tol_sum = 0.0, 0.0
+    for (_, h), r in attention.packed(f64(q), f64(k), f64(v), cu, D ** -0.5).items():
+        (dq, tq), (dk, tk) = fine_tols(r, f64(dout[:, h]))
+        # 1.01: terms of second order
+        within(gq[:, h], dq, 1.01 * tq + ROUND[BF16] * np.abs(dq), ("dq", h))
+        # the heads share the sums
+        dk_sum, tol_sum = dk_sum + dk, tol_sum + tk + G * U * np.abs(dk)
+    within(gk[:, 0], dk_sum, 1.01 * tol_sum + ROUND[BF16] * np.abs(dk_sum), "dk")
