@@ -685,6 +685,7 @@ kda_status kda_attention_bwd_workspace_size(int32_t N, int64_t T, int32_t Hq, in
  * the tokens are taken in tiles of floor(128 / h), h the largest divisor of Hq / Hk up to 128.
  * In a tile whose last token has up to 128 keys delta is sum_j p_ij (dout_i . v_j), which
  * does not lose to the rounding of out, and ds_ij goes into the products as two BF16 parts.
+ * A row without weight (lse -infinity) adds nothing to any key's gradients.
  */
 kda_status kda_attention_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                              const void* v, int64_t v_stride, int32_t dtype, const void* out,

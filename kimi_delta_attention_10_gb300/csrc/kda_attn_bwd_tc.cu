@@ -386,6 +386,7 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
                 const int32_t begin = min(128, max(0, key - at * sh.tokens)) * sh.heads - 64 * half;
                 const bool cut = at * sh.tokens < kTcKeys - 1;     // for some key
                 const bool two = in_two(at);
+                const int32_t used = (at + 1 == per ? last : sh.tokens) * sh.heads - 64 * half;
                 if (++at == per) at = 0;
                 wait(&bar.statfull[b], (i >> 1) & 1);
                 wait(&bar.sfull, i & 1);
@@ -395,6 +396,11 @@ attn_bwd_kv_tc_kernel(AttnArgs a, AttnShape sh, const __grid_constant__ KvMaps m
                 tmem_ld32_start(s_tm, p);
                 tmem_ld32_start(s_tm + 32, p + 32);
                 tmem_ld_wait(p);
+                // rows of zeros behind those in use have scores of 0, but NaN with a key that has an infinity
+                if (used < 64 && __any_sync(0xffffffffu, p[63] != p[63])) {
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) p[k] = k < used ? p[k] : 0.f;
+                }
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     const float4 l = nl[k];

@@ -411,19 +411,24 @@ constexpr int kBwdRows = 64;                   // rows of a backward tile
 // shared memory has room, two stages of the two that it walks over.
 template <int D> struct Bwd {
     static constexpr int STAGES = D == 64 ? 2 : 1;
-    static constexpr int TILE = 64 * (D + 4), PITCH_P = kKeys + 4, STATS = 2 * kBwdRows;
+    static constexpr int TILE = 64 * (D + 4), PITCH_P = kKeys + 4, STATS = 3 * kBwdRows;
     static constexpr int OFF_WALK = 2 * TILE, OFF_P = OFF_WALK + STAGES * 2 * TILE,
                          OFF_DS = OFF_P + kBwdRows * PITCH_P, OFF_L = OFF_DS + kBwdRows * PITCH_P;
     static constexpr uint32_t SMEM = (OFF_L + STAGES * STATS) * 4;
 };
 
-// lse and delta of a tile's rows, copied beside the tile; +infinity where a row is not in use.
-__device__ __forceinline__ void load_stats(float* dst, const AttnArgs& a, const RowMap& rows)
+// lse and delta of a tile's rows, copied beside the tile, and how many keys each sees: of `end`,
+// the first token's pos0 + 1 on.  A row that is not in use sees none: its zeros times a key with an
+// infinity are NaN.
+__device__ __forceinline__ void load_stats(float* dst, const AttnArgs& a, const RowMap& rows, int32_t pos0,
+                                           int32_t end)
 {
     const int r = threadIdx.x;
     if (r >= kBwdRows) return;
     int32_t token, head;
-    if (rows.at(r, token, head)) {
+    const bool used = rows.at(r, token, head);
+    reinterpret_cast<int32_t*>(dst)[2 * kBwdRows + r] = used ? min(end, pos0 + token - rows.row0 + 1) : 0;
+    if (used) {
         const int64_t at = (int64_t)token * a.Hq + head;
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst + r)), "l"(a.lse_in + at) : "memory");
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst + kBwdRows + r)), "l"(a.delta + at)
@@ -438,7 +443,7 @@ __device__ __forceinline__ void load_stats(float* dst, const AttnArgs& a, const 
 template <int D>
 __device__ __forceinline__ void weights(float (&p)[4][4], float (&ds)[4][4], const float* q, const float* dout,
                                         const float* k, const float* v, const float* stats, const AttnArgs& a,
-                                        int32_t pos0, int32_t heads, int32_t key0, int32_t end, int ty, int tx)
+                                        int32_t key0, int ty, int tx)
 {
     const float c = a.scale * kLog2e;
     scores<4, D>(p, q, k, ty, tx);
@@ -446,8 +451,8 @@ __device__ __forceinline__ void weights(float (&p)[4][4], float (&ds)[4][4], con
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = ty * 4 + i;
-        const int32_t limit = min(end, pos0 + r / heads + 1);
-        // a row without weight (lse -infinity) gives none, like one that is not in use
+        const int32_t limit = reinterpret_cast<const int32_t*>(stats)[2 * kBwdRows + r];
+        // a row without weight (lse -infinity) gives none
         const float lse = stats[r] == -CUDART_INF_F ? CUDART_INF_F : stats[r] * kLog2e, delta = stats[kBwdRows + r];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -504,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(AttnArgs a, At
             const RowMap rows(sh, hk * sh.parts + part, t.seq0 + at, min(sh.tokens, end - at));
             load_rows<kBwdRows, D>(walked(i), static_cast<const float*>(a.q), a.q_stride, rows);
             load_rows<kBwdRows, D>(walked(i) + B::TILE, static_cast<const float*>(a.dout), (int64_t)a.Hq * D, rows);
-            load_stats(stats(i), a, rows);
+            load_stats(stats(i), a, rows, at, end);
         }
         cp_async_commit();
     };
@@ -522,8 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kv_kernel(AttnArgs a, At
         landed<B::STAGES>();
         const float *q = walked(i), *dout = q + B::TILE;
         float p[4][4], ds[4][4];
-        weights<D>(p, ds, q, dout, sm, sm + B::TILE, stats(i), a, key0 + i % per * sh.tokens, sh.heads, key0, end, ty,
-                   tx);
+        weights<D>(p, ds, q, dout, sm, sm + B::TILE, stats(i), a, key0, ty, tx);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -577,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(AttnArgs a, Att
     const RowMap rows(sh, unit, t.row0, t.tokens);
     load_rows<kBwdRows, D>(sm, static_cast<const float*>(a.q), a.q_stride, rows);
     load_rows<kBwdRows, D>(sm + B::TILE, static_cast<const float*>(a.dout), (int64_t)a.Hq * D, rows);
-    load_stats(sm + B::OFF_L, a, rows);
+    load_stats(sm + B::OFF_L, a, rows, t.pos0, end);
     auto walked = [&](int32_t i) { return sm + B::OFF_WALK + i % B::STAGES * 2 * B::TILE; };
     auto load = [&](int32_t i) {
         if (i < n) {
@@ -597,8 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_q_kernel(AttnArgs a, Att
         load(i + B::STAGES - 1);
         landed<B::STAGES>();
         float p[4][4], ds[4][4];
-        weights<D>(p, ds, sm, sm + B::TILE, walked(i), walked(i) + B::TILE, sm + B::OFF_L, a, t.pos0, sh.heads,
-                   i * kKeys, end, ty, tx);
+        weights<D>(p, ds, sm, sm + B::TILE, walked(i), walked(i) + B::TILE, sm + B::OFF_L, a, i * kKeys, ty, tx);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll

@@ -11,8 +11,8 @@ from kimi_delta_attention_10_gb300.binding import KDA_ERR_DEVICE_ARG
 
 from oracle import attention
 
-from test_gpu_attention import (BF16, F32, ROUND, U, f64, ints, offsets, paged_case, projected, randn, run_fwd,
-                                status_word, within)
+from test_gpu_attention import (BF16, F32, ROUND, U, f64, grad_tols, ints, out_tol, paged_case, projected, randn,
+                                run_fwd, status_word, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +127,75 @@ def test_gradients_of_up_to_128_keys_lose_nothing_to_the_rounding_of_ds(L, G):
         # the heads share the sums
         dk_sum, tol_sum = dk_sum + dk, tol_sum + tk + G * U * np.abs(dk)
     within(gk[:, 0], dk_sum, 1.01 * tol_sum + ROUND[BF16] * np.abs(dk_sum), "dk")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [0.125, -0.125])
+@pytest.mark.parametrize("D", [64, 128])
+def test_gradients_through_rows_without_weight(D, scale, dtype):
+    """The first keys' scores are -infinity for every row, so that the first rows have no weight at
+    all: they add nothing to dk and dv, and the other rows' gradients are those without these keys.
+    The channel that holds the infinities is left out of dq (zero times infinity, in the formula too)."""
+    T, H, bad = 300, 2, 5
+    q, k, v = (x.contiguous() for x in projected(T, H, 1, D, dtype, 12))
+    q[..., 0] = 1.0
+    k[:bad, :, 0] = -np.inf if scale > 0 else np.inf
+    dout = randn(T, H, D, seed=1, dtype=dtype)
+    out, lse = run_fwd(q, k, v, [0, T], scale=scale)
+    assert (out[:bad] == 0).all() and (lse[:bad] == -np.inf).all()
+    gq, gk, gv = (f64(g) for g in kda.kda_attention_bwd(q, k, v, out, lse, dout, ints([0, T]), scale))
+    assert (gq[:bad, :, 1:] == 0).all() and (gk[:bad] == 0).all() and (gv[:bad] == 0).all()
+    d = f64(dout)[bad:]
+    sums = [0.0] * 4
+    for h in range(H):
+        r = attention.Rows(f64(q[bad:, h]), f64(k[bad:, 0]), f64(v[bad:, 0]), np.arange(T - bad) + 1, scale)
+        dq, dk, dv, _ = r.grads(d[:, h])
+        tq, tk, tv = grad_tols(r, d[:, h], dtype, out_tol(r, dtype))
+        # 1.01: terms of second order
+        within(gq[bad:, h, 1:], dq[:, 1:], (1.01 * tq + ROUND[dtype] * np.abs(dq))[:, 1:], ("dq", h))
+        sums = [a + b for a, b in zip(sums, (dk, tk, dv, tv))]
+    dk, tk, dv, tv = sums
+    more = H * U * (np.abs(dk).max() + np.abs(dv).max())
+    within(gk[bad:, 0], dk, 1.01 * tk + more + ROUND[dtype] * np.abs(dk), "dk")
+    within(gv[bad:, 0], dv, 1.01 * tv + more + ROUND[dtype] * np.abs(dv), "dv")
+
+
+REACH = 255
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,at,Hq,Hk,D", [(900, 600, 4, 1, 64), (900, 513, 2, 2, 128), (700, 383, 3, 1, 64),
+                                          (600, 300, 1, 1, 128)])
+@pytest.mark.parametrize("what", ["q", "k", "v", "dout"])
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_how_far_one_token_reaches(what, bad, T, at, Hq, Hk, D, dtype):
+    """NaN or an infinity in one token.  Everything that neither sees it nor is seen by it, and
+    lies past the documented 255 tokens, keeps its bits; what the formula makes of it is no number."""
+    q, k, v = (x.contiguous() for x in projected(T, Hq, Hk, D, dtype, 9))
+    dout, cu = randn(T, Hq, D, seed=10, dtype=dtype), ints([0, T])
+    x = dict(q=q, k=k, v=v, dout=dout)
+
+    def step(out=None, lse=None):
+        if out is None:
+            out, lse = run_fwd(x["q"], x["k"], x["v"], [0, T])
+        return [out, lse, *kda.kda_attention_bwd(x["q"], x["k"], x["v"], out, lse, x["dout"], cu)]
+
+    clean = step()
+    x[what] = x[what].clone()
+    x[what][at] = bad
+    dirty = step()
+    # rows that see the token, or share its tile, may differ; queries up to 255 before it
+    rows = slice(0, at - REACH) if what in "kv" else slice(0, at)
+    for a, b in zip(clean[:3], dirty[:3]):
+        assert torch.equal(a[rows], b[rows])
+    if what in ("q", "dout"):
+        for a, b in zip(clean[:3], dirty[:3]):
+            assert torch.equal(a[at + 1:], b[at + 1:])
+        # keys that the token does not see, past the reach
+        for a, b in zip(clean[3:], dirty[3:]):
+            assert torch.equal(a[at + REACH + 1:], b[at + REACH + 1:])
+        assert not dirty[2][at].isfinite().any()
+    elif np.isnan(bad):
+        out, lse, dq = dirty[:3]
+        assert out[at:].isnan().all() and dq[at:].isnan().all()
+        assert lse[at:].isnan().all() if what == "k" else torch.equal(lse, clean[1])
