@@ -635,15 +635,17 @@ template <int D, int R> cudaError_t forward_rows(const AttnArgs& a, cudaStream_t
     return launch_after(kern, launch_config(ctas, kThreads, Fwd<D, R>::SMEM), stream, a, sh);
 }
 // Rows a thread, by the rows that a group has in a sequence of average length; the largest
-// tiles, which read the keys least often, where they fill the GPU or nearly so (1024 tokens of 16
-// heads: 95 us, 108 with tiles of 64 rows; 4 prompts of 1 to 300 tokens over up to 1000 cached:
-// 41 us, 34 with tiles of 64 rows).
+// tiles, which read the keys least often, where there are tiles for three quarters of the SMs:
+// pieces (attn_splits) then fill the GPU.  With 128 tiles for 152 SMs, tiles of 128 and of 64 rows:
+// 1024 tokens, 16 heads of 64 channels 95 and 105 us, in groups of 4 87 and 105; 2048 tokens, 8
+// heads of 128 channels 240 and 269; but 512 tokens, 32 heads of 128 channels in groups of 4 92 and
+// 79.  With fewer tiles: 4 prompts of 1 to 300 tokens over up to 1000 cached 40 and 33.
 int rows_per_thread(int32_t N, int32_t T, int32_t Hq, int32_t Hk)
 {
     const int64_t rows = ((int64_t)T + N - 1) / N * (Hq / Hk);
     if (rows > 64) {
         const AttnShape sh = attn_shape(128, Hq, Hk);
-        return attn_tiles(N, T, sh.tokens) * sh.units * 8 >= (int64_t)sm_count() * 7 ? 8 : 4;
+        return attn_tiles(N, T, sh.tokens) * sh.units * 4 >= (int64_t)sm_count() * 3 ? 8 : 4;
     }
     return rows > 32 ? 4 : rows > 16 ? 2 : 1;
 }
@@ -694,9 +696,10 @@ cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t stream)
 
 // Pieces of two key tiles at least: as many as fill the GPU once on the tensor cores (64 requests
 // behind 16384 tokens: 94 us, 110 if twice); three times in FP32, where a tile takes long enough that
-// the longest of a causal call would be waited for (1024 tokens, 16 heads of 64 channels: 139 us in
-// one piece, 89 and 8 for the join in two; 4 prompts of 1 to 300 tokens over up to 1000: 35.0 us if
-// twice, 32.8; 2048 tokens 244, 250 if four times).
+// the longest of a causal call would be waited for.  16 heads of 64 channels, twice, three and four times:
+// 768 tokens 76, 60 and 58 us, 1024 83, 95 and 93, 1280 160, 119 and 125, 1536 191, 164 and 163, 2048
+// 245, 245 and 251; 3000 tokens, 8 heads of 128 channels 613, 482 and 464; 4 prompts of 1 to 300 tokens
+// over up to 1000 35.0, 32.7 and 33.8.
 int32_t attn_splits(bool bf16, int32_t N, int32_t T, int32_t Hq, int32_t Hk, int32_t D, int64_t kv_most)
 {
     if (N == 0 || T == 0) return 1;
