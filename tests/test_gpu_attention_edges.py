@@ -11,8 +11,8 @@ from kimi_delta_attention_10_gb300.binding import KDA_ERR_DEVICE_ARG
 
 from oracle import attention
 
-from test_gpu_attention import (BF16, F32, ROUND, U, f64, grad_tols, ints, out_tol, paged_case, projected, randn,
-                                run_fwd, status_word, within)
+from test_gpu_attention import (BF16, F32, ROUND, U, f64, grad_tols, ints, lse_tol, out_tol, paged_case, projected,
+                                randn, run_fwd, status_word, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -199,3 +199,51 @@ def test_how_far_one_token_reaches(what, bad, T, at, Hq, Hk, D, dtype):
         out, lse, dq = dirty[:3]
         assert out[at:].isnan().all() and dq[at:].isnan().all()
         assert lse[at:].isnan().all() if what == "k" else torch.equal(lse, clean[1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("prefix,page", [([40, 300], 16), ([2000, 9], 64)])
+def test_keys_without_weight_over_pages(prefix, page, dtype):
+    """Scores of -infinity over a prefix, over a request's own tokens, over both: as if those keys
+    were not there, zeros and lse -infinity where none is left.  A NaN reaches its group alone."""
+    Hq, Hk, D, own, cu = 6, 2, 128, [9, 0, 130, 1], [0, 2, 4]
+    scale = D ** -0.5
+    kc, vc, table = paged_case(prefix + own, Hk, D, page, dtype, 4)
+    q = randn(4, Hq, D, seed=5, dtype=dtype)
+    q[..., 0] = 1.0
+    pt, ot = ints(table[:2].tolist()), ints(table[2:].tolist())
+
+    def pages_of(rows):
+        ids = table[rows]
+        return torch.tensor(ids[ids >= 0], device="cuda", dtype=torch.long)
+
+    def shared(k):
+        st = status_word()
+        out, lse = kda.kda_paged_decode_shared(q, k, vc, pt, ints(prefix), ints(cu), ot, ints(own), want_lse=True,
+                                               status=st)
+        assert int(st[0]) == 0
+        return out, lse
+
+    def prompt(k, rows, lens):
+        return kda.kda_paged_prompt(q, k, vc, ints(table[rows].tolist()), ints(lens), ints([0, 1, 2, 3, 4]),
+                                    want_lse=True)
+
+    clean = shared(kc)
+    for rows, prefixes, owns in (([0], [0, prefix[1]], own), ([2, 3, 4, 5], prefix, [0] * 4),
+                                 (list(range(6)), [0, 0], [0] * 4)):
+        k = kc.clone()
+        k[pages_of(rows), :, :, 0] = -np.inf
+        out, lse = shared(k)
+        ref = attention.decode_shared(f64(q), f64(kc), f64(vc), table[:2], prefixes, cu, table[2:], owns, scale)
+        for (n, h), r in ref.items():
+            within(f64(out[n, h]), r.out[0], out_tol(r, dtype)[0], (n, h))
+            assert lse[n, h] == -np.inf if len(r.k) == 0 else abs(float(lse[n, h]) - r.lse[0]) <= lse_tol(r)[0]
+        if owns == [0] * 4:
+            # the same keys for prompts of one token
+            po, pl = prompt(k, [2, 3, 4, 5], own)
+            assert (po == 0).all() and (pl == -np.inf).all()
+    k = kc.clone()
+    k[int(table[0, 0]), :, 3] = np.nan
+    out, lse = shared(k)
+    assert out[:2].isnan().all() and lse[:2].isnan().all()
+    assert torch.equal(out[2:], clean[0][2:]) and torch.equal(lse[2:], clean[1][2:])
