@@ -627,7 +627,10 @@ kda_status kda_paged_decode(const void* q, const void* k_cache, const void* v_ca
  * output but lse (F32, natural logarithm, [T, Hq], or NULL).  F32: products are IEEE
  * FP32.  BF16: products of BF16 values are exact and summed in FP32; the weights and, in
  * the backward, the scores' gradients are rounded to BF16 (2^-8) before the products with
- * them, statistics and sums are FP32, and outputs are rounded once.  Few rows over many
+ * them, statistics are FP32, and outputs are rounded once.  The tensor core truncates its
+ * sums: one of n terms of one sign loses up to 6e-9 n of itself (1.3e-3 for the 262144
+ * rows that dv of a sequence's first key adds up).  The weights reach 2^8 before they are
+ * divided by their sum, so values need that room below FP32's largest.  Few rows over many
  * keys are taken in pieces of the keys' axis, which a second kernel joins.  Every sum's
  * order is set by the sizes alone: the same call gives the same bits.
  *
@@ -703,7 +706,9 @@ kda_status kda_paged_prompt_workspace_size(int32_t N, int64_t T, int32_t Hq, int
  * (prompts, pieces of prompts behind a cached part, drafted tokens): request n's
  * tokens cu_seqlens[n] .. cu_seqlens[n+1]-1, m of them, are the last m of its
  * seq_lens[n], all appended already (kda_page_plan, kda_qk_norm_rope_append), and each sees
- * the tokens up to itself.  With one token a request it computes what kda_paged_decode does.
+ * the tokens up to itself.  With one token a request it is the attention of kda_paged_decode,
+ * in BF16 with fewer bits: that call takes each weight in two BF16 parts and adds the tensor
+ * core's sums up rounded (about 1.7e-3 off in a BF16 output, 2.3e-3 here).
  *   q [T, Hq, D] (strided tokens), k_cache, v_cache [num_pages, Hk, page_size, D]
  *   block_table [N, max_pages], seq_lens [N], cu_seqlens [N+1] int32;  out [T, Hq, D]
  * A request with seq_lens[n] < m has tokens before its first key: they see none.
@@ -730,7 +735,9 @@ kda_status kda_paged_decode_shared_workspace_size(int32_t N, int32_t groups, int
  *   cu_groups [groups+1], block_table [N, max_pages], seq_lens [N] int32
  *   out [N, Hq, D], lse [N, Hq]
  * cu_groups are offsets as above with T = N: requests behind the last group keep their
- * outputs, and their lengths and table rows are not looked at.  Either length may be 0.  Lengths, pages and cache sizes as in kda_paged_decode.
+ * outputs, and their lengths and table rows are not looked at.  BF16: weights of the prefix
+ * are rounded as in kda_paged_prompt, those of the own tokens taken as in kda_paged_decode.
+ * Either length may be 0.  Lengths, pages and cache sizes as in kda_paged_decode.
  */
 kda_status kda_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache,
                                    int32_t dtype, const int32_t* prefix_table,

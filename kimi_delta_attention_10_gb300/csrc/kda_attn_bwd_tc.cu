@@ -26,9 +26,9 @@
 // A warp reads the rows' lse and delta.
 //
 // Bound by the tensor pipe in long sequences: one of 8192 tokens, 64 / 8 heads of 128 channels,
-// takes 1.24 ms for dk and dv and 0.90 for dq (1770 and 1830 TFLOP/s of the 1898 that a library
+// takes 1.28 ms for dk and dv and 0.91 for dq (1720 and 1820 TFLOP/s of the 1898 that a library
 // product reaches, counting the products made), delta 0.04.  Short ones are bound by a tile's start
-// and end: 8 sequences of 1 to 2048 tokens 243, 213 and 36 us.  What lies between the
+// and end: 8 sequences of 1 to 2048 tokens 257, 222 and 36 us.  What lies between the
 // products on the issuing warp counts: the same loops with conditions between them took 1.32 and
 // 1.05 ms, dq with one buffer of dP and a CTA a tile 1.25.
 #include <cuda_runtime.h>

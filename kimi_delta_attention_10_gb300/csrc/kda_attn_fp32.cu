@@ -15,8 +15,10 @@
 //
 // Measured: 2048 tokens, 16 heads of 64 channels, 244 us (35 TFLOP/s, 47% of the FMA pipe's
 // peak; it is busy 55% of the cycles: two warps a scheduler wait for their own instructions,
-// and twice as many with smaller tiles read more); forward and backward of 1024 tokens 340 us,
-// of which dk and dv 138 and dq 111, bound by the longest CTA's walk.
+// and twice as many with smaller tiles read more); forward and backward of 1024 tokens 327 us:
+// 92 in three pieces and 9 for their join, delta 4, dk and dv 137, dq 111.  The last two walk over 16
+// tiles at most, 14.3 on the mean SM, in 8.6 and 6.9 us a step whose products would take 4.3
+// and 3.2 at the pipe's peak: eight warps go through scores, weights and sums together.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>

@@ -19,11 +19,12 @@
 //   store     two warps: outputs leave through ring slots by TMA.
 //
 // Bound by the tensor pipe in long sequences, and there by power: 16384 tokens, 64 / 8 heads of 128
-// channels, 2.77 ms, 1590 TFLOP/s, 84% of what a library product reaches in a burst and 95% of what
+// channels, 2.8 ms, 1570 TFLOP/s, 83% of what a library product reaches in a burst and 94% of what
 // it holds.  Pieces of prompts (16 requests, up to 512 tokens over up to 16384) 0.79 ms, 1410
 // TFLOP/s.  With few rows by HBM: 64 requests of 4 drafted tokens over up to 16384, 322 us, 93% of
-// the rate of a plain copy.  Short sequences by a job's start and end, about 3 us: 8
-// sequences of 1 to 2048 tokens 185 us, 870 TFLOP/s; 129 tokens 8.7 us.
+// the rate of a plain copy.  Short sequences by a job's start and end: a job of one tile of rows and
+// one of keys takes 7.4 us (64 channels) or 8.9 (128), of two and two 12 or 14.6, a further tile of
+// keys about one; 8 sequences of 1 to 2048 tokens 187 us, 860 TFLOP/s; 129 tokens 8.7 us.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
