@@ -366,8 +366,8 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(DecodeArgs a, Decode
             *reinterpret_cast<float4*>(static_cast<float*>(a.out) + r * D + ch) = y;
     };
     wait_for_previous();
-    const int32_t N = decode_requests(a);
-    for (int64_t n = blockIdx.x + (int64_t)gridDim.x * blockIdx.y; n < N; n += (int64_t)gridDim.x * gridDim.y) {
+    for (int64_t n = blockIdx.x + (int64_t)gridDim.x * blockIdx.y; n < a.N;
+         n += (int64_t)gridDim.x * gridDim.y) {
         if (decode_len(a, n) != 0) continue;
         for (int h = part; h < a.Hq; h += P) {
             store(n * a.Hq + h, make_float4(0.f, 0.f, 0.f, 0.f));

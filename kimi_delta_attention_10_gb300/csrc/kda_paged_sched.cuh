@@ -122,15 +122,13 @@ __device__ __forceinline__ void leave_split(const DecodeShape& s, const DecodeSh
 constexpr int kLaneRequests = 4;
 struct DecodeLens {
     int32_t L[kLaneRequests];          // of requests 4 lane .. 4 lane + 3, as given
+    int32_t N;                         // requests with a row
     __device__ __forceinline__ void load(const DecodeArgs& a)
     {
         const int n0 = (threadIdx.x & 31) * kLaneRequests;
 #pragma unroll
         for (int i = 0; i < kLaneRequests; ++i) L[i] = n0 + i < a.N ? a.seq_lens[n0 + i] : 0;
-        if (a.live == nullptr) return;
-        const int32_t N = decode_requests(a);
-#pragma unroll
-        for (int i = 0; i < kLaneRequests; ++i) L[i] = n0 + i < N ? L[i] : 0;
+        N = decode_requests(a);
     }
 };
 
@@ -159,8 +157,9 @@ __device__ __forceinline__ DecodeRange decode_range(const DecodeArgs& a, const D
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < kLaneRequests; ++i) {
-            L[i] = valid_len(a, lens.L[i]);
-            bad |= L[i] != lens.L[i];
+            const int32_t given = lane * kLaneRequests + i < lens.N ? lens.L[i] : 0;
+            L[i] = valid_len(a, given);
+            bad |= L[i] != given;
             mine += decode_places(s, L[i]);
         }
         const int64_t upto = warp_scan(mine, lane);
