@@ -262,7 +262,8 @@ kda_status kda_paged_decode_shared(const void* q, const void* k_cache, const voi
     char* ws = static_cast<char*>(workspace);
     kda::DecodeArgs d = {};
     d.q = q; d.k = k_cache; d.v = v_cache; d.bf16 = a.bf16; d.table = block_table; d.seq_lens = seq_lens;
-    d.N = N; d.live = cu_groups + groups; d.Hq = Hq; d.Hk = Hk; d.D = D; d.num_pages = num_pages; d.page_shift = a.page_shift;
+    d.N = N; d.live = cu_groups + groups;
+    d.Hq = Hq; d.Hk = Hk; d.D = D; d.num_pages = num_pages; d.page_shift = a.page_shift;
     d.max_pages = max_pages; d.scale = scale;
     d.out = ws + kda::attn_pieces_o(a, a.splits);
     d.lse = reinterpret_cast<float*>(ws + kda::attn_pieces_lse(a, a.splits));

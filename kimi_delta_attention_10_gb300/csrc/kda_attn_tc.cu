@@ -393,8 +393,7 @@ attn_fwd_tc_kernel(AttnArgs a, AttnShape sh, int32_t jobs, const __grid_constant
                                 commit_if(lead, &bar.ofull[m]);
                             }
                         }
-                        if (m && i >= 0 && !wait.dead())
-                            commit_if(lead, &bar.empty[v]);
+                        if (m && i >= 0 && !wait.dead()) commit_if(lead, &bar.empty[v]);
                         seen = false;
                         if (i + 1 < n) {
                             if (i < 0) wait(&bar.qfull[m], (m ? held1 : held0) & 1);
